@@ -24,7 +24,8 @@ LAYER_SWA, LAYER_FULL, LAYER_REINDEX, LAYER_REUSE = 0, 1, 2, 3
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED",
           3: "CSA2_ERR_WORKSPACE", 4: "CSA2_ERR_CUDA", 5: "CSA2_ERR_DEVICE_TIMEOUT",
-          6: "CSA2_ERR_INDEX_RANGE"}
+          6: "CSA2_ERR_INDEX_RANGE", 7: "CSA2_ERR_NO_PAGES"}
+OUT_F32, OUT_BF16 = 0, 1
 
 
 class Csa2Error(RuntimeError):
@@ -66,6 +67,18 @@ def window(row_pos, lo) -> Window:
     return win
 
 
+class Pages(ctypes.Structure):
+    """csa2_pages: page table [B][max_pages] (int32, device), its row length, pages of the planes."""
+    _fields_ = [("table", ctypes.c_void_p), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+def pages(table, n_pages: int, max_pages: int | None = None) -> Pages:
+    """A csa2_pages over a device int32 array [B, max_pages]; keeps a reference to it."""
+    p = Pages(_ptr(table), int(table.shape[-1] if max_pages is None else max_pages), int(n_pages))
+    p._refs = (table,)
+    return p
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -86,6 +99,7 @@ def lib() -> ctypes.CDLL:
         pl = ctypes.POINTER(KVPlanes)
         nr = ctypes.POINTER(NormRope)
         wn = ctypes.POINTER(Window)
+        pg = ctypes.POINTER(Pages)
         sig = {
             "csa2_quantize_entries": ([vp, vp, i64, pl, i64, vp], ctypes.c_int),
             "csa2_cache_write": ([vp, i64, i32, vp, vp, vp, i32, pl, i32, i64, nr, i64, vp, sz, vp],
@@ -112,6 +126,15 @@ def lib() -> ctypes.CDLL:
             "csa2_dense_attn_decode": ([pl, i32, vp, i64, vp, i32, vp, f32, nr, vp, vp, wn, vp, vp, vp, sz, vp],
                                        ctypes.c_int),
             "csa2_dense_attn_workspace_size": ([i32, i64, i32], sz),
+            "csa2_page_tables": ([i32, vp, vp, i32, i32, vp, vp, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp,
+                                  vp, sz, vp], ctypes.c_int),
+            "csa2_page_tables_workspace_size": ([i32], sz),
+            "csa2_paged_attn_decode": ([pl, pg, i32, vp, i64, vp, i32, vp, f32, nr, vp, vp, wn, vp, i32, vp, vp, sz,
+                                        vp], ctypes.c_int),
+            "csa2_paged_attn_workspace_size": ([i32, i64, i32], sz),
+            "csa2_prefix_attn_decode": ([pl, pg, i32, vp, i32, vp, vp, i64, i64, vp, i32, vp, f32, nr, vp, vp, wn, vp,
+                                         i32, vp, vp, sz, vp], ctypes.c_int),
+            "csa2_prefix_attn_workspace_size": ([i32, i32, i64, i64, i32], sz),
             "csa2_compress_overlap": ([vp, i64, i32, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_compress_hca": ([vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_compress_workspace_size": ([i64, i32], sz),
@@ -366,6 +389,68 @@ def dense_attn_decode(planes: Planes, B: int, n_entries, n_max: int, swa, n_swa:
                                      _ptr(sink), ctypes.byref(win) if win is not None else None, _ptr(out),
                                      _ptr(lse_out), _ptr(ws), _nbytes(ws), _stream(stream)),
         "csa2_dense_attn_decode")
+
+
+def page_tables_workspace_size(B: int) -> int:
+    return lib().csa2_page_tables_workspace_size(B)
+
+
+def page_tables(B: int, n_have, n_new, page_entries: int, table, max_pages: int, n_pages: int, free_pages, n_free,
+                n_free_out, n_entries, ws, n_rows: int = 0, query=None, slot=None, entry=None, pos=None,
+                row_start=None, m: int = 1, n_kept=None, stream=None) -> None:
+    """Extends (n_new >= 0) or shortens (n_new < 0) every request's pages and fills the map of the new
+    entries: query, slot (page), entry (index in the page) and pos per map row, as cache_append takes
+    them, -1 behind the last; n_free_out may be n_free and n_entries n_have (csa2_page_tables)."""
+    _ok(lib().csa2_page_tables(B, _ptr(n_have), _ptr(n_new), page_entries, m, _ptr(n_kept), _ptr(table), max_pages,
+                               n_pages, _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(n_entries), n_rows,
+                               _ptr(query), _ptr(slot), _ptr(entry), _ptr(pos), _ptr(row_start), _ptr(ws),
+                               _nbytes(ws), _stream(stream)), "csa2_page_tables")
+
+
+def _out_type(out, out_type: int | None) -> int:
+    """OUT_F32 / OUT_BF16 of a tensor (a raw pointer's type has to be given)."""
+    if out_type is not None:
+        return out_type
+    name = str(getattr(out, "dtype", "torch.float32"))
+    if name not in ("torch.float32", "torch.bfloat16"):
+        raise Csa2Error(1, f"attention output of type {name}")
+    return OUT_BF16 if name == "torch.bfloat16" else OUT_F32
+
+
+def paged_attn_workspace_size(B: int, n_max: int, n_swa: int) -> int:
+    return lib().csa2_paged_attn_workspace_size(B, n_max, n_swa)
+
+
+def paged_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, n_max: int, swa, n_swa: int, q,
+                      softmax_scale: float, out, ws, lse_out=None, stream=None, q_nr: NormRope | None = None,
+                      q_pos=None, sink=None, win: Window | None = None, out_type: int | None = None) -> None:
+    """Dense attention through a page table: entries [0, n_entries[b]) of row b's pages plus the window
+    rows; out fp32 or bf16 (csa2_paged_attn_decode)."""
+    _ok(lib().csa2_paged_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), B, _ptr(n_entries), n_max,
+                                     _ptr(swa), n_swa, _ptr(q), softmax_scale,
+                                     ctypes.byref(q_nr) if q_nr is not None else None, _ptr(q_pos), _ptr(sink),
+                                     ctypes.byref(win) if win is not None else None, _ptr(out),
+                                     _out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
+                                     _stream(stream)), "csa2_paged_attn_decode")
+
+
+def prefix_attn_workspace_size(B: int, G: int, n_shared_max: int, n_own_max: int, n_swa: int) -> int:
+    return lib().csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa)
+
+
+def prefix_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, G: int, group_start, n_shared,
+                       n_shared_max: int, n_own_max: int, swa, n_swa: int, q, softmax_scale: float, out, ws,
+                       lse_out=None, stream=None, q_nr: NormRope | None = None, q_pos=None, sink=None,
+                       win: Window | None = None, out_type: int | None = None) -> None:
+    """paged_attn_decode for queries that share prefixes: the queries [group_start[g], group_start[g + 1])
+    agree on their first n_shared[g] entries, which are read once for the group
+    (csa2_prefix_attn_decode)."""
+    _ok(lib().csa2_prefix_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), B, _ptr(n_entries), G,
+                                      _ptr(group_start), _ptr(n_shared), n_shared_max, n_own_max, _ptr(swa), n_swa,
+                                      _ptr(q), softmax_scale, ctypes.byref(q_nr) if q_nr is not None else None,
+                                      _ptr(q_pos), _ptr(sink), ctypes.byref(win) if win is not None else None,
+                                      _ptr(out), _out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
+                                      _stream(stream)), "csa2_prefix_attn_decode")
 
 
 def compress_workspace_size(T: int, d_model: int) -> int:

@@ -24,7 +24,7 @@
 // its chunks, so no partial result leaves the SM.  When the batch is too small
 // to fill the GPU a query's chunks are split over a few CTAs, which write
 // (max, l, O) partials that a merge kernel combines by log-sum-exp.
-#include "codec.cuh"
+#include "attn.cuh"
 #include "ptx.cuh"
 #include "timing.cuh"
 
@@ -41,33 +41,17 @@ constexpr int kGatherWarps = 8;
 constexpr int kCtlWarp = 12;
 constexpr int kOWarp = 14;
 constexpr int kAT = 16 * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-// the softmax reference (log2 units) moves only when a chunk exceeds it by
-// more than 8 nats, so probabilities stay below e^8 (inside f16)
-constexpr float kTau2 = 8.0f * kLog2e;
-// the reference of a head with no row yet: finite, so that 2^(S c2 - kNoRef) of a
-// missing (-inf) row stays 0, and far below any logit, so that a row exceeds it
-constexpr float kNoRef = -1.0e30f;
-// q' plane stride: 64 heads x 16 bytes, unpadded, so that every core matrix the
-// S MMAs read sits on a 128-byte line
-constexpr int kQPlane = kHAtt * 8;       // in f16 elements (1024 bytes)
 constexpr int kXPlane = kRows * 8;       // f16 elements per 8-channel plane of a slot (1024 bytes)
 constexpr uint32_t kAttnTmemCols = 512;  // O^T 256 columns; per S half, two slots of 64
 constexpr uint32_t kTmemS = 256;         // first column of S half 0, slot 0 (half h, slot s: + 128 h + 64 s)
 constexpr long long kAttnWaitBudget = 1LL << 32;
 
-// In-layer extras ("DeepSeek-V4: ...", CSA, other details), each off when null /
-// zero: RMSNorm weight of the query heads, RoPE of the query at qpos[b] with the
-// output turned back by -qpos[b], per-head sink logits.
-struct AttnExtras {
-  const float* qnorm_w;
-  float eps;
-  int rope;
-  const int64_t* qpos;
-  const float* sink;
-  const int64_t* win_pos;  // [B][n_swa] position of each window row (< 0: empty), or null: all visible
-  const int64_t* win_lo;   // [B] lowest visible window position
-  RopeTheta th;
+// Page table of a paged cache: entry j of query b is plane row table[b][j / P] * P + j % P
+// (P = seq_stride entries per page).
+struct PageMap {
+  const int32_t* table;
+  int64_t max_pages;
+  int32_t n_pages;
 };
 
 struct __align__(1024) AttnSmem {
@@ -94,152 +78,6 @@ struct __align__(1024) AttnSmem {
 // below 256 KB, which the constant-stepped descriptors rely on)
 static_assert(sizeof(AttnSmem) <= 232448, "attention shared memory");
 
-__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\tmov.b32 {t0, t1, t2, t3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, t0;\n\tcvt.rn.f16x2.e2m1x2 %1, t1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, t2;\n\tcvt.rn.f16x2.e2m1x2 %3, t3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t h;
-  uint16_t v = (uint16_t)two;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
-  return h;
-}
-
-// q' = q_h 2^-s_h in f16 with 2^s_h bringing the head's largest |q| to
-// [2^14, 2^15), clamped so that both 2^s_h and 2^-s_h are normal fp32 values;
-// bf16 q keeps q' exact and inside the f16 range (with RMSNorm or RoPE the
-// fp32 result is rounded to f16 once).  One bulk copy brings the query's bf16
-// rows ([64][512]) into row slot 1; the softmax and MMA warps, idle until the
-// first chunk's rows are written, convert them from there while the row warps
-// dequantize chunk 0 into slot 0.  Warp 8 + w takes heads 8w .. 8w + 7: lane
-// l = 8g + t head 8w + t over the 8-channel planes (t + 4i + g) mod 64, i < 16.
-// The eight lanes of a phase then read eight different banks of the bf16 rows
-// (their planes differ mod 8) and write eight consecutive head slots of the
-// [c/8][head][c%8] image, so neither side conflicts; the values are read again
-// for each pass rather than held (a pass holding all 64 registers spills other
-// warps' state), and the four lanes of a head combine its maximum (and sum of
-// squares) with two shuffles.
-template <bool kEx>
-__device__ __forceinline__ void stage_q(AttnSmem& S, const uint16_t* qs, float scale, int w, int lane,
-                                        const AttnExtras& ex, int b) {
-  const int t = lane & 7, g = lane >> 3, h = 8 * w + t;
-  const uint4* src = reinterpret_cast<const uint4*>(qs + h * kDMain);
-  const bool norm = kEx && ex.qnorm_w != nullptr;
-  const bool rot = kEx && ex.rope;
-  float r = 1.0f;  // 1 / RMS of the head
-  if (norm) {
-    float ss = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const uint4 q4 = src[(t + 4 * i + g) & 63];
-      const uint32_t w4[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v0 = __uint_as_float(w4[j] << 16), v1 = __uint_as_float(w4[j] & 0xFFFF0000u);
-        ss = fmaf(v0, v0, ss);
-        ss = fmaf(v1, v1, ss);
-      }
-    }
-    ss += __shfl_xor_sync(0xffffffffu, ss, 8);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 16);
-    r = 1.0f / sqrtf(ss / (float)kDMain + ex.eps);
-  }
-  // RoPE turns planes 56 .. 63 (pairs 4 (p - 56) + pr); lane l keeps the cosine and
-  // sine of pair l (every head turns by the same angles)
-  float rcos = 1.0f, rsin = 0.0f;
-  if (rot) rope_cos_sin(ex.th.t[lane], (double)ex.qpos[b], rcos, rsin);
-  // the 8 channels of plane p after RMSNorm and RoPE
-  auto plane = [&](int p, float (&v)[8]) {
-    const uint4 q4 = src[p];
-    const uint32_t w4[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w4[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w4[j] & 0xFFFF0000u);
-    }
-    if (norm) {
-      const float4* wv = reinterpret_cast<const float4*>(ex.qnorm_w + 8 * p);
-      const float4 a = __ldg(wv), c = __ldg(wv + 1);
-      const float wq[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = wq[k] * (v[k] * r);
-    }
-    if (rot) {
-#pragma unroll
-      for (int pr = 0; pr < 4; ++pr) {  // every lane shuffles; only planes 56 .. 63 turn
-        const int pair = (4 * (p - 56) + pr) & 31;
-        const float c = __shfl_sync(0xffffffffu, rcos, pair), sn = __shfl_sync(0xffffffffu, rsin, pair);
-        if (p >= 56) rope_pair(v[2 * pr], v[2 * pr + 1], c, sn);
-      }
-    }
-  };
-  float mx = 0.0f;
-  if (kEx) {
-#pragma unroll 2
-    for (int i = 0; i < 16; ++i) {
-      float v[8];
-      plane((t + 4 * i + g) & 63, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[k]));
-    }
-  } else {  // |bf16| orders as its bit pattern: a packed 16-bit maximum over the raw words
-    uint32_t m2 = 0;
-#pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const uint4 q4 = src[(t + 4 * i + g) & 63];
-      const uint32_t w4[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m2) : "r"(w4[j] & 0x7FFF7FFFu));
-    }
-    mx = __uint_as_float(max(m2 & 0xFFFFu, m2 >> 16) << 16);
-  }
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-  const int sig = mx > 0.0f ? min(max(floor_log2_f32(mx) - 14, -126), 126) : 0;
-  const float inv = exp2i_f32(-sig);  // exact power of two: q 2^-sig rounds only in the f16 conversion
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int p = (t + 4 * i + g) & 63;
-    float v[8];
-    plane(p, v);
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h2 = __floats2half2_rn(v[2 * j] * inv, v[2 * j + 1] * inv);
-      o[j] = *reinterpret_cast<const uint32_t*>(&h2);
-    }
-    *reinterpret_cast<uint4*>(&S.q[p][h * 8]) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if (g == 0) S.c2[h] = kLog2e * scale * exp2i_f32(sig);
-}
-
-// Whether some of the four softmax warps (named barrier 2, 128 threads) saw a
-// logit above its head's reference (lane 0 of each warp posts `wover`) and
-// whether one of them gave up waiting (lanes 1-8 post `wbad`): one barrier, the
-// count of posted predicates below 8 for the first, at least 8 for the second.
-// Every softmax warp passes it once per chunk, also after a failed wait, so no
-// warp is left at the barrier.
-__device__ __forceinline__ uint32_t softmax_vote(bool wover, bool wbad, int lane) {
-  const uint32_t pred = lane == 0 ? (wover ? 1u : 0u) : (lane <= 8 && wbad ? 1u : 0u);
-  uint32_t n;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.popc.u32 %0, 2, 128, p;\n\t}"
-      : "=r"(n)
-      : "r"(pred)
-      : "memory");
-  return n;
-}
-// the four softmax warps (named barrier 2): shared-memory writes before it are seen after it
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
 // One thread's share of a chunk row, fetched two chunks ahead of its
 // dequantization.  Gather warp w takes chunk rows 8w .. 8w + 7: lane l row
 // 8w + l % 8 and column block cb = l / 8, so each load instruction reads 64
@@ -255,8 +93,18 @@ struct RowFetch {
 
 // entry of chunk row gr (rows gr >= k are window rows or padding): topk[b][gr],
 // or, dense, entry gr itself while gr < dense_n[b]
+// (paged: the plane row of that entry; a page outside the planes is reported, and its rows are skipped)
+template <bool kPaged>
 __device__ __forceinline__ int64_t fetch_index(const int32_t* __restrict__ topk, const int32_t* __restrict__ dense_n,
-                                               int k, int b, int gr) {
+                                               int k, int b, int gr, const PageMap& pm, int64_t page_entries, int cb,
+                                               void* ws) {
+  if (kPaged) {
+    if (gr >= k) return -1;
+    const int page = __ldg(pm.table + b * pm.max_pages + gr / (int)page_entries);
+    if (page >= 0 && page < pm.n_pages) return page * page_entries + gr % (int)page_entries;
+    if (cb == 0) report_error(ws, CSA2_ERR_INDEX_RANGE, page);
+    return -1;
+  }
   if (gr >= k) return -1;
   if (dense_n) return gr < __ldg(dense_n + b) ? gr : -1;
   return (int64_t)topk[(int64_t)b * k + gr];
@@ -264,14 +112,15 @@ __device__ __forceinline__ int64_t fetch_index(const int32_t* __restrict__ topk,
 
 // Starts this lane's loads of chunk row gr: a selected entry (gr < k, index idx),
 // a window row (k <= gr < k + n_swa, visible) or nothing.
+template <bool kPaged>
 __device__ __forceinline__ void issue_row(RowFetch& f, int64_t idx, const uint8_t* __restrict__ kv_codes,
                                           const uint8_t* __restrict__ kv_scales, int64_t seq_stride,
                                           const uint8_t* __restrict__ swa, int n_swa, int k, int b, int gr,
                                           int cb, void* ws, const int64_t* __restrict__ win_pos, int64_t win_lo) {
   f.kind = 0;
   if (gr < k) {
-    if (idx >= 0 && idx < seq_stride) {
-      const int64_t e = (int64_t)b * seq_stride + idx;
+    if (idx >= 0 && (kPaged || idx < seq_stride)) {
+      const int64_t e = kPaged ? idx : (int64_t)b * seq_stride + idx;
       const uint4* cs = reinterpret_cast<const uint4*>(kv_codes + e * 256);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f.raw[i] = cs[4 * i + cb];
@@ -407,11 +256,14 @@ __device__ __forceinline__ float sum_probs(const uint32_t (&ph)[16]) {
 // kPartial: write the unnormalised O with (m, l) for the merge kernel instead
 // of the normalised output.
 // 16 warps, four per scheduler, whose 16 K registers then allow 128 per thread.
-template <bool kPartial, bool kEx>
+// kPaged: dense over a paged cache.  The rows of query b are its own n_b entries, then the
+// window, so a query of a ragged batch runs only its own chunks, spread evenly over the
+// launch's splits; a split without rows writes an empty partial.
+template <bool kPartial, bool kEx, bool kPaged>
 __global__ void __launch_bounds__(512, 1) k_attn(
     const uint8_t* __restrict__ kv_codes, const uint8_t* __restrict__ kv_scales, int64_t seq_stride,
     const int32_t* __restrict__ topk, const int32_t* __restrict__ dense_n, int k, const uint8_t* __restrict__ swa,
-    int n_swa,
+    int n_swa, PageMap pm,
     const uint16_t* __restrict__ qg, float scale, AttnExtras ex, int nchunks, int cps,
     float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
     float2* __restrict__ part_ml, void* ws) {
@@ -419,8 +271,19 @@ __global__ void __launch_bounds__(512, 1) k_attn(
   AttnSmem& S = *reinterpret_cast<AttnSmem*>(smem_raw);
   volatile int* abort_flag = &S.abort_flag;
   const int b = blockIdx.y, split = blockIdx.x;
-  const int c0 = split * cps, nc = min(nchunks, c0 + cps) - c0;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (kPaged) {
+    ptx::griddep_wait();  // the counts may come from the previous kernel
+    k = min(max(__ldg(dense_n + b), 0), k);
+    nchunks = max((k + n_swa + kRows - 1) / kRows, 1);
+    cps = (nchunks + gridDim.x - 1) / gridDim.x;
+    if (split * cps >= nchunks) {
+      if (tid < kHAtt)
+        part_ml[((int64_t)b * gridDim.x + split) * kHAtt + tid] = make_float2(-INFINITY, 0.0f);
+      return;
+    }
+  }
+  const int c0 = split * cps, nc = min(nchunks, c0 + cps) - c0;
 
   if (warp == kCtlWarp) {
     if (lane == 0) {
@@ -452,8 +315,8 @@ __global__ void __launch_bounds__(512, 1) k_attn(
   int64_t idx0 = -1, idx1 = -1;
   if (warp < kGatherWarps) {
     const int gr0 = c0 * kRows + r, gr1 = gr0 + kRows;
-    idx0 = fetch_index(topk, dense_n, k, b, gr0);
-    idx1 = nc > 1 ? fetch_index(topk, dense_n, k, b, gr1) : -1;
+    idx0 = fetch_index<kPaged>(topk, dense_n, k, b, gr0, pm, seq_stride, cb, ws);
+    idx1 = nc > 1 ? fetch_index<kPaged>(topk, dense_n, k, b, gr1, pm, seq_stride, cb, ws) : -1;
   }
   ptx::tc_fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
@@ -461,7 +324,7 @@ __global__ void __launch_bounds__(512, 1) k_attn(
   const uint32_t tmem = S.tmem_base;
   if (warp >= kGatherWarps) {  // q' and c2 from slot 1, while the row warps dequantize chunk 0
     if (ptx::mbar_wait_warp(&S.q_load, 0, abort_flag, kAttnWaitBudget)) {
-      stage_q<kEx>(S, &S.X[1][0][0], scale, warp - kGatherWarps, lane, ex, b);
+      stage_q<kEx>(S.q, S.c2, &S.X[1][0][0], scale, warp - kGatherWarps, lane, ex, b);
     } else if (lane == 0 && !*abort_flag) {
       *abort_flag = 1;
       report_error(ws, CSA2_ERR_DEVICE_TIMEOUT, 25);
@@ -540,13 +403,13 @@ __global__ void __launch_bounds__(512, 1) k_attn(
     RowFetch rf0, rf1;  // rows of the even / odd chunks
     const int gr0 = c0 * kRows + r;
     rf1.kind = 0;
-    issue_row(rf0, idx0, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0, cb, ws, ex.win_pos, win_lo);
+    issue_row<kPaged>(rf0, idx0, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0, cb, ws, ex.win_pos, win_lo);
     if (nc > 1)
-      issue_row(rf1, idx1, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0 + kRows, cb, ws, ex.win_pos,
+      issue_row<kPaged>(rf1, idx1, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0 + kRows, cb, ws, ex.win_pos,
                 win_lo);
     // this lane's entries in chunks j + 2 (loaded after chunk j) and j + 3 (index read then)
-    int64_t idx2 = nc > 2 ? fetch_index(topk, dense_n, k, b, gr0 + 2 * kRows) : -1;
-    int64_t idx3 = nc > 3 ? fetch_index(topk, dense_n, k, b, gr0 + 3 * kRows) : -1;
+    int64_t idx2 = nc > 2 ? fetch_index<kPaged>(topk, dense_n, k, b, gr0 + 2 * kRows, pm, seq_stride, cb, ws) : -1;
+    int64_t idx3 = nc > 3 ? fetch_index<kPaged>(topk, dense_n, k, b, gr0 + 3 * kRows, pm, seq_stride, cb, ws) : -1;
     bool good = true;
     for (int p = 0; 2 * p < nc && good; ++p) {
       const uint32_t ph = (uint32_t)(p & 1);
@@ -577,10 +440,10 @@ __global__ void __launch_bounds__(512, 1) k_attn(
         }
         if (!good) break;
         if (j + 2 < nc)
-          issue_row(f, idx2, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr + 2 * kRows, cb, ws, ex.win_pos,
+          issue_row<kPaged>(f, idx2, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr + 2 * kRows, cb, ws, ex.win_pos,
                     win_lo);
         idx2 = idx3;
-        idx3 = j + 4 < nc ? fetch_index(topk, dense_n, k, b, gr + 4 * kRows) : -1;
+        idx3 = j + 4 < nc ? fetch_index<kPaged>(topk, dense_n, k, b, gr + 4 * kRows, pm, seq_stride, cb, ws) : -1;
       }
     }
     // ---- epilogue: O^T rows = channels of this lane quarter, 32 heads per warp; for each
@@ -761,8 +624,8 @@ __global__ void __launch_bounds__(512, 1) k_attn(
 
 __global__ void __launch_bounds__(128) k_attn_merge(const float* __restrict__ part_o,
                                                     const float2* __restrict__ part_ml, int nchunks,
-                                                    const float* __restrict__ sink, float* __restrict__ out,
-                                                    float* __restrict__ lse) {
+                                                    const float* __restrict__ sink, void* __restrict__ out,
+                                                    int out_bf16, float* __restrict__ lse) {
   const int bh = blockIdx.x;  // b * 64 + h
   const int b = bh / kHAtt, h = bh % kHAtt;
   ptx::griddep_wait();  // the partials come from the previous kernel
@@ -786,7 +649,13 @@ __global__ void __launch_bounds__(128) k_attn_merge(const float* __restrict__ pa
   }
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
   if (L > 0.0f) r = make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
-  reinterpret_cast<float4*>(out + (int64_t)bh * kDMain)[threadIdx.x] = r;
+  if (out_bf16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(r.x, r.y), hi = __floats2bfloat162_rn(r.z, r.w);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + (int64_t)bh * kDMain)[threadIdx.x] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    reinterpret_cast<float4*>(static_cast<float*>(out) + (int64_t)bh * kDMain)[threadIdx.x] = r;
+  }
   if (lse && threadIdx.x == 0) lse[bh] = L > 0.0f ? ref + logf(L) : -INFINITY;
 }
 
@@ -815,11 +684,11 @@ AttnPlan attn_plan(int32_t B, int32_t k, int32_t n_swa) {
   return p;
 }
 
-AttnWs attn_ws_layout(void* ws, int32_t B, const AttnPlan& plan) {
+AttnWs attn_ws_layout(void* ws, int32_t B, const AttnPlan& plan, bool always_partial = false) {
   AttnWs L{};
   size_t off = kWsHeader;
   char* base = (char*)ws;
-  if (plan.nsplit > 1) {
+  if (plan.nsplit > 1 || always_partial) {
     L.part_o = (float*)(base ? base + off : nullptr);
     off += align_up((size_t)B * plan.nsplit * kHAtt * kDMain * 4, 256);
     L.part_ml = (float2*)(base ? base + off : nullptr);
@@ -839,20 +708,16 @@ extern "C" size_t csa2_sparse_attn_workspace_size(int32_t B, int32_t k, int32_t 
 }
 
 namespace csa2 {
-namespace {
 
-// One attention call over k rows per query named by topk (or, dense_n given,
-// entries 0 .. dense_n[b] - 1) joined with n_swa window rows.
-csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, const int32_t* dense_n, int32_t k,
-                     const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
-                     const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
-                     float* out, float* lse_out, void* ws, size_t ws_bytes, cudaStream_t st) {
+csa2_status attn_extras(const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
+                        int32_t n_swa, float softmax_scale, AttnExtras* e) {
+  AttnExtras& ex = *e;
+  ex = AttnExtras{};
   if (win && (!win->row_pos || !win->lo || !aligned(win->row_pos, 8) || !aligned(win->lo, 8)))
     return CSA2_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.0f) || softmax_scale > 3.0e38f) return CSA2_ERR_INVALID_ARG;  // positive, finite
   if (q_nr && (!norm_rope_ok(q_nr) || (q_nr->rope && !q_pos))) return CSA2_ERR_INVALID_ARG;
   if ((q_pos && !aligned(q_pos, 8)) || (sink && !aligned(sink, 4))) return CSA2_ERR_INVALID_ARG;
-  AttnExtras ex{};
   ex.qnorm_w = q_nr ? q_nr->norm_weight : nullptr;
   ex.eps = q_nr ? q_nr->norm_eps : 0.0f;
   ex.rope = q_nr ? q_nr->rope : 0;
@@ -861,29 +726,47 @@ csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, c
   ex.win_pos = win && n_swa > 0 ? win->row_pos : nullptr;
   ex.win_lo = win && n_swa > 0 ? win->lo : nullptr;
   if (ex.rope) ex.th = make_rope_theta(q_nr->rope_base);
+  return CSA2_OK;
+}
+
+namespace {
+
+// One attention call over k rows per query named by topk (or, dense_n given,
+// entries 0 .. dense_n[b] - 1, through `pages` when given) joined with n_swa window rows.
+csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, const int32_t* dense_n, int32_t k,
+                     const csa2_pages* pages, const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
+                     const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
+                     void* out, int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, cudaStream_t st) {
+  AttnExtras ex;
+  const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
+  if (bad != CSA2_OK) return bad;
   if (!aligned(q_bf16, 16) || !aligned(out, 16) || (swa_e4m3 && !aligned(swa_e4m3, 16)))
     return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
   const AttnPlan plan = attn_plan(B, k, n_swa);
-  AttnWs L = attn_ws_layout(ws, B, plan);
+  AttnWs L = attn_ws_layout(ws, B, plan, pages != nullptr);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const int smem = (int)sizeof(AttnSmem);
-  const bool partial = plan.nsplit > 1;
+  const bool partial = plan.nsplit > 1 || pages;
   const bool extras = ex.qnorm_w || ex.rope || ex.sink;
-  auto kern = partial ? (extras ? k_attn<true, true> : k_attn<true, false>)
-                      : (extras ? k_attn<false, true> : k_attn<false, false>);
+  auto kern = pages     ? (extras ? k_attn<true, true, true> : k_attn<true, false, true>)
+              : partial ? (extras ? k_attn<true, true, false> : k_attn<true, false, false>)
+                        : (extras ? k_attn<false, true, false> : k_attn<false, false, false>);
+  PageMap pm{};
+  if (pages) pm = PageMap{pages->table, pages->max_pages, pages->n_pages};
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return launch_status();
   {
     KernelTimer timer(partial ? "k_attn_part" : "k_attn", st);
     launch_pdl(kern, dim3(plan.nsplit, B), dim3(kAT), (size_t)smem, st, kv->kv_codes, kv->kv_scales, kv->seq_stride,
-               topk, dense_n, k, swa_e4m3, n_swa, (const uint16_t*)q_bf16, softmax_scale, ex, plan.nchunks, plan.cps,
-               out, lse_out, L.part_o, L.part_ml, ws);
+               topk, dense_n, k, swa_e4m3, n_swa, pm, (const uint16_t*)q_bf16, softmax_scale, ex, plan.nchunks, plan.cps,
+               (float*)out, lse_out, L.part_o, L.part_ml, ws);
   }
   if (partial) {
     KernelTimer timer("k_attn_merge", st);
-    launch_pdl(k_attn_merge, dim3(B * kHAtt), dim3(128), 0, st, L.part_o, L.part_ml, plan.nsplit, sink, out, lse_out);
+    launch_pdl(k_attn_merge, dim3(B * kHAtt), dim3(128), 0, st, L.part_o, L.part_ml, plan.nsplit, sink, out,
+               out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
   }
   return launch_status();
 }
@@ -901,8 +784,8 @@ extern "C" csa2_status csa2_sparse_attn_decode(const csa2_kv_planes* kv, int32_t
   if (!planes_ok(kv) || B <= 0 || B > 65535 || k < 0 || k > CSA2_MAX_TOPK || n_swa < 0 || n_swa > CSA2_MAX_SWA)
     return CSA2_ERR_INVALID_ARG;
   if ((k > 0 && !topk) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, topk, nullptr, k, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win, out,
-                  lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, topk, nullptr, k, nullptr, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win,
+                  out, CSA2_OUT_F32, lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
@@ -922,6 +805,36 @@ extern "C" csa2_status csa2_dense_attn_decode(const csa2_kv_planes* kv, int32_t 
     return CSA2_ERR_INVALID_ARG;
   if ((n_max > 0 && !n_entries) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
   if (n_entries && !aligned(n_entries, 4)) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos,
-                  sink, win, out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, nullptr, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
+                  q_pos, sink, win, out, CSA2_OUT_F32, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+namespace csa2 {
+// Page table of a call over B queries: rows long enough for n entries of each.
+bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
+  if (!p || p->max_pages < 0 || p->n_pages < 0 || kv->seq_stride > INT32_MAX) return false;
+  if (n > 0 && (!p->table || !aligned(p->table, 4))) return false;
+  return n <= (int64_t)p->max_pages * kv->seq_stride;
+}
+}  // namespace csa2
+
+extern "C" size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
+  if (B <= 0 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0) return 0;
+  return csa2::attn_ws_layout(nullptr, B, csa2::attn_plan(B, (int32_t)n_max, n_swa), true).bytes;
+}
+
+extern "C" csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                              const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
+                                              int32_t n_swa, const void* q_bf16, float softmax_scale,
+                                              const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink,
+                                              const csa2_window* win, void* out, int32_t out_type, float* lse_out,
+                                              void* ws, size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (!planes_ok(kv) || B <= 0 || B > 65535 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0 ||
+      n_swa > CSA2_MAX_SWA || !pages_ok(pages, kv, n_max))
+    return CSA2_ERR_INVALID_ARG;
+  if (!n_entries || !aligned(n_entries, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
+  if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
+  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, pages, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
+                  q_pos, sink, win, out, out_type, lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }

@@ -21,6 +21,7 @@ extern "C" const char* csa2_status_string(csa2_status s) {
     case CSA2_ERR_CUDA: return "CUDA runtime or launch error";
     case CSA2_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
     case CSA2_ERR_INDEX_RANGE: return "an index outside its sequence slot";
+    case CSA2_ERR_NO_PAGES: return "too few free pages";
   }
   return "unknown status";
 }

@@ -1,0 +1,321 @@
+// Page tables and slot maps of a paged cache, built on the GPU from request lengths.
+//
+// Request b holds have[b] entries in pages(have) = ceil(have / P) pages and gets new[b] more
+// (negative: drops its last -new).  With three exclusive sums over the requests
+//   rows  R_b = sum max(new, 0)              one map row per new entry,
+//   need  N_b = sum pages(have + new) - pages(have)  (new >= 0)   pages taken,
+//   gone  G_b = sum pages(have) - max(pages(have + new), kept)  (new < 0)   pages given back,
+// every output is a closed form: given back page i goes to free[n_free + i], taken page a is the
+// stack's element n_free + G - 1 - a (an element at or above n_free is the given back page itself,
+// so nothing waits for the pushes), and row r finds its request by a search in R.
+//
+// The work is a few kilobytes: launches and dependent loads bound it, not bandwidth.
+#include "common.cuh"
+#include "ptx.cuh"
+#include "timing.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct PageArgs {
+  int32_t B;
+  const int32_t* have;
+  const int32_t* add;
+  const int32_t* kept;  // or null: 0
+  int32_t P, m;
+  int32_t* table;
+  int32_t max_pages, n_pages;
+  int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* n_free_out;
+  int32_t* n_entries;
+  int32_t n_rows;
+  int32_t* query;  // the maps, each or null
+  int32_t* slot;
+  int64_t* entry;
+  int64_t* pos;
+  int32_t* row_start;
+  void* ws;
+};
+
+// What the plan leaves for the fill: the sums, the lengths read before n_entries overwrites them,
+// the totals (total rows 0 and ok 0 after an error).
+struct PlanState {
+  int32_t ok, n_free, total_rows, total_gone;
+};
+struct PlanView {
+  int32_t* have;  // [B]
+  int32_t* rows;  // [B + 1] exclusive sums
+  int32_t* need;  // [B + 1]
+  int32_t* gone;  // [B + 1]
+  PlanState* st;
+};
+
+__device__ __forceinline__ int pages_of(int n, int P) { return (int)(((long long)n + P - 1) / P); }
+
+// largest i in [lo, hi) with sum[i] <= x (sum ascending, sum[lo] <= x)
+__device__ __forceinline__ int find_le(const int32_t* sum, int lo, int hi, int x) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// given back page i
+__device__ __forceinline__ int gone_page(const PageArgs& a, const PlanView& v, int i) {
+  const int b = find_le(v.gone, 0, a.B, i);
+  const int first = pages_of(v.have[b], a.P) - (v.gone[b + 1] - v.gone[b]);
+  return a.table[(int64_t)b * a.max_pages + first + i - v.gone[b]];
+}
+// taken page i: from the top of the stack, the pages given back by this call included
+__device__ __forceinline__ int taken_page(const PageArgs& a, const PlanView& v, int i) {
+  const int at = v.st->n_free + v.st->total_gone - 1 - i;
+  return at >= v.st->n_free ? gone_page(a, v, at - v.st->n_free) : a.free_pages[at];
+}
+
+// The plan, by one CTA of kPlanThreads: sums, checks, n_entries, n_free_out, row_start.
+__device__ void plan_block(const PageArgs& a, const PlanView& v) {
+  __shared__ long long s_warp[3][kPlanThreads / 32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  const long long cap = min((long long)a.max_pages * a.P, (long long)INT32_MAX);
+  long long base[3] = {0, 0, 0};
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long x[3] = {0, 0, 0};
+    if (b < a.B) {
+      const int have = a.have[b], add = a.add[b], kept = a.kept ? a.kept[b] : 0;
+      const long long total = (long long)have + add;
+      v.have[b] = have;
+      if (have < 0 || total < 0 || have > cap || total > cap || kept < 0) {
+        s_bad = 1;
+        report_error(a.ws, CSA2_ERR_INDEX_RANGE, b);
+      } else {
+        const int pc = pages_of(have, a.P), pa = pages_of((int)total, a.P);
+        if (add >= 0) {
+          x[0] = add;
+          x[1] = pa - pc;
+        } else {
+          x[2] = pc - max(pa, min(kept, pc));
+        }
+      }
+    }
+    long long inc[3] = {x[0], x[1], x[2]};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc[q], o);
+        if (lane >= o) inc[q] += y;
+      }
+    if (lane == 31)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) s_warp[q][warp] = inc[q];
+    __syncthreads();
+    long long total[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      long long w = s_warp[q][lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+      total[q] = __shfl_sync(0xffffffffu, w, 31);
+      inc[q] += base[q] + (warp > 0 ? before : 0);
+    }
+    if (b < a.B) {  // sums past 32 bits are refused below; what they leave here is not used
+      v.rows[b + 1] = (int)inc[0];
+      v.need[b + 1] = (int)inc[1];
+      v.gone[b + 1] = (int)inc[2];
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) base[q] += total[q];
+    __syncthreads();  // s_warp is written again by the next strip
+  }
+  const int n_free = *a.n_free;
+  if (tid == 0) {
+    v.rows[0] = v.need[0] = v.gone[0] = 0;
+    const bool maps = a.query || a.slot || a.entry || a.pos;
+    if (base[0] > INT32_MAX || (maps && base[0] > a.n_rows)) {
+      s_bad = 1;
+      report_error(a.ws, CSA2_ERR_INDEX_RANGE, base[0]);
+    }
+    if (n_free < 0 || n_free > a.n_pages || base[2] > a.n_pages - n_free) {
+      s_bad = 1;
+      report_error(a.ws, CSA2_ERR_INDEX_RANGE, n_free);
+    } else if (base[1] > n_free + base[2]) {
+      s_bad = 1;
+      report_error(a.ws, CSA2_ERR_NO_PAGES, base[1] - n_free - base[2]);
+    }
+  }
+  if (tid == 0) *v.st = PlanState{1, n_free, (int)base[0], (int)base[2]};
+  __syncthreads();
+  bool ok = !s_bad;
+  __syncthreads();
+  if (ok) {  // the ids that would move: a bad one refuses the call
+    const int from_stack = (int)min(max(base[1] - base[2], 0LL), (long long)n_free);
+    for (int i = tid; i < from_stack; i += kPlanThreads) {
+      const int id = a.free_pages[n_free - 1 - i];
+      if (id < 0 || id >= a.n_pages) {
+        s_bad = 1;
+        report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
+      }
+    }
+    for (int i = tid; i < (int)base[2]; i += kPlanThreads) {
+      const int id = gone_page(a, v, i);
+      if (id < 0 || id >= a.n_pages) {
+        s_bad = 1;
+        report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
+      }
+    }
+  }
+  __syncthreads();
+  ok = !s_bad;
+  if (tid == 0) {
+    if (!ok) *v.st = PlanState{0, n_free, 0, 0};
+    *a.n_free_out = ok ? (int)(n_free + base[2] - base[1]) : n_free;
+    if (a.row_start) a.row_start[0] = 0;
+  }
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    a.n_entries[b] = ok ? v.have[b] + a.add[b] : v.have[b];
+    if (a.row_start) a.row_start[b + 1] = ok ? v.rows[b + 1] : 0;
+  }
+  __syncthreads();
+}
+
+// Map rows [r0, r1) by the calling threads (tid of n), requests by their warps.
+__device__ void fill_rows(const PageArgs& a, const PlanView& v, int64_t r, int64_t step) {
+  const int total = v.st->total_rows;
+  for (; r < a.n_rows; r += step) {
+    int b = -1, slot = -1;
+    int64_t off = -1, pos = -1;
+    if (r < total) {
+      b = find_le(v.rows, 0, a.B, (int)r);
+      const int have = v.have[b];
+      const int e = have + (int)r - v.rows[b];
+      const int p = e / a.P, pc = pages_of(have, a.P);
+      slot = p < pc ? a.table[(int64_t)b * a.max_pages + p] : taken_page(a, v, v.need[b] + p - pc);
+      off = e - p * a.P;
+      pos = (int64_t)e * a.m;
+    }
+    if (a.query) a.query[r] = b;
+    if (a.slot) a.slot[r] = slot;
+    if (a.entry) a.entry[r] = off;
+    if (a.pos) a.pos[r] = pos;
+  }
+}
+__device__ void fill_requests(const PageArgs& a, const PlanView& v, int warp, int n_warps) {
+  if (!v.st->ok) return;
+  const int lane = threadIdx.x & 31;
+  for (int b = warp; b < a.B; b += n_warps) {
+    const int need = v.need[b + 1] - v.need[b], gone = v.gone[b + 1] - v.gone[b];
+    if (!need && !gone) continue;
+    const int pc = pages_of(v.have[b], a.P);
+    int32_t* row = a.table + (int64_t)b * a.max_pages;
+    for (int i = lane; i < need; i += 32) row[pc + i] = taken_page(a, v, v.need[b] + i);
+    for (int i = lane; i < gone; i += 32) a.free_pages[v.st->n_free + v.gone[b] + i] = row[pc - gone + i];
+  }
+}
+
+// Everything in one CTA, the plan in shared memory.
+__global__ void __launch_bounds__(kPlanThreads) k_page_tables(PageArgs a) {
+  extern __shared__ int32_t smem[];
+  __shared__ PlanState st;
+  const PlanView v{smem, smem + a.B, smem + 2 * a.B + 1, smem + 3 * a.B + 2, &st};
+  ptx::griddep_wait();
+  plan_block(a, v);
+  fill_requests(a, v, threadIdx.x / 32, kPlanThreads / 32);
+  fill_rows(a, v, threadIdx.x, kPlanThreads);
+}
+
+// The plan by one CTA into the workspace, then the fill by many.
+__global__ void __launch_bounds__(kPlanThreads) k_page_plan(PageArgs a, PlanView v) {
+  ptx::griddep_wait();
+  plan_block(a, v);
+}
+constexpr int kFillThreads = 256;
+__global__ void __launch_bounds__(kFillThreads) k_page_fill(PageArgs a, PlanView v) {
+  ptx::griddep_wait();
+  const int64_t t = (int64_t)blockIdx.x * kFillThreads + threadIdx.x, n = (int64_t)gridDim.x * kFillThreads;
+  fill_requests(a, v, (int)(t / 32), (int)(n / 32));
+  fill_rows(a, v, t, n);
+}
+
+// One CTA up to this many map rows and requests.
+constexpr int kOneCtaRows = 8192, kOneCtaRequests = 2048;
+
+PlanView plan_view(void* ws, int32_t B, size_t* bytes) {
+  size_t off = kWsHeader;
+  char* base = (char*)ws;
+  auto take = [&](size_t n) {
+    char* p = base ? base + off : nullptr;
+    off += align_up(n, 256);
+    return (int32_t*)p;
+  };
+  PlanView v;
+  v.st = (PlanState*)take(sizeof(PlanState));
+  v.have = take((size_t)B * 4);
+  v.rows = take(((size_t)B + 1) * 4);
+  v.need = take(((size_t)B + 1) * 4);
+  v.gone = take(((size_t)B + 1) * 4);
+  if (bytes) *bytes = off;
+  return v;
+}
+
+}  // namespace
+}  // namespace csa2
+
+extern "C" size_t csa2_page_tables_workspace_size(int32_t B) {
+  if (B <= 0 || B > 65535) return 0;
+  size_t n;
+  csa2::plan_view(nullptr, B, &n);
+  return n;
+}
+
+extern "C" csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const int32_t* n_new, int32_t page_entries,
+                                        int32_t m, const int32_t* n_kept, int32_t* page_table, int32_t max_pages,
+                                        int32_t n_pages, int32_t* free_pages, const int32_t* n_free,
+                                        int32_t* n_free_out, int32_t* n_entries, int32_t n_rows, int32_t* row_query,
+                                        int32_t* row_slot, int64_t* row_entry, int64_t* row_pos, int32_t* row_start,
+                                        void* ws, size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (B <= 0 || B > 65535 || page_entries <= 0 || m <= 0 || max_pages <= 0 || n_pages <= 0 || n_rows < 0)
+    return CSA2_ERR_INVALID_ARG;
+  if (!n_have || !n_new || !page_table || !free_pages || !n_free || !n_free_out || !n_entries)
+    return CSA2_ERR_INVALID_ARG;
+  const void* p4[] = {n_have, n_new, n_kept, page_table, free_pages, n_free, n_free_out, n_entries, row_query,
+                      row_slot, row_start};
+  for (const void* p : p4)
+    if (!aligned(p, 4)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(row_entry, 8) || !aligned(row_pos, 8)) return CSA2_ERR_INVALID_ARG;
+  if (n_rows > 0 && !row_query && !row_slot && !row_entry && !row_pos) return CSA2_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+  size_t need;
+  const PlanView v = plan_view(ws, B, &need);
+  if (ws_bytes < need) return CSA2_ERR_WORKSPACE;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
+  const PageArgs a{B, n_have, n_new, n_kept, page_entries, m, page_table, max_pages, n_pages, free_pages, n_free,
+                   n_free_out, n_entries, n_rows, row_query, row_slot, row_entry, row_pos, row_start, ws};
+  if (n_rows <= kOneCtaRows && B <= kOneCtaRequests) {
+    KernelTimer timer("k_page_tables", st);
+    launch_pdl(k_page_tables, dim3(1), dim3(kPlanThreads), (4 * (size_t)B + 3) * 4, st, a);
+  } else {
+    {
+      KernelTimer timer("k_page_plan", st);
+      launch_pdl(k_page_plan, dim3(1), dim3(kPlanThreads), 0, st, a, v);
+    }
+    const int64_t threads = n_rows > (int64_t)B * 32 ? n_rows : (int64_t)B * 32;
+    const int blocks = (int)(cdiv(threads, kFillThreads) < 1216 ? cdiv(threads, kFillThreads) : 1216);
+    KernelTimer timer("k_page_fill", st);
+    launch_pdl(k_page_fill, dim3(blocks), dim3(kFillThreads), 0, st, a, v);
+  }
+  return launch_status();
+}

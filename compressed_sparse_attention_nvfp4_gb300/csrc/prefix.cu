@@ -1,0 +1,887 @@
+// Attention for a batch whose queries share prefixes.
+//
+// Two queries of a group make a pair, and their 2 x 64 heads the 128 rows of one MMA, so an entry of
+// the shared prefix is read and widened once for two queries and the tensor cores run at their full
+// rate (64 rows alone run at half of it).  A pair of CTAs (one query each) computes a pair of queries
+// with tcgen05.mma.cta_group::2 in chunks of 128 rows:
+//   S[128 x 128 rows] = q' X^T   each CTA holds 64 of the rows (all channels), K-major;
+//   P = 2^(S c2 - m)             each CTA its own query: thread t head t % 64, rows 64 (t / 64) ..;
+//   O[128 x 512] += P X          each CTA holds 256 of the channels (all rows), N-major.
+// At M = 128 a CTA's tensor memory holds 64 rows of an accumulator in 128 lanes, so O takes 256
+// columns and leaves room for two S buffers; neither operand is exchanged between the CTAs: each
+// widens the 64 x 512 values it holds for S and the 128 x 256 it holds for O from the 288-byte entries
+// itself.  Shared memory is what bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 128 KB
+// of rows and 16 KB of P written, 368 KB = 2,900 cycles at 128 bytes a cycle, against 2,048 cycles of
+// MMA; with one buffer for each operand there is no room for a second chunk, so both are handed over in
+// four pieces (128 channels of S's rows, 32 rows of O's).
+// Behind the shared entries come the two queries' own (their last entries and windows): chunks whose
+// first 64 rows are the first query's and whose last 64 the second's, each query masking the other's.
+// All pairs' chunks form one list that kClusters CTA pairs share evenly, whatever the groups' sizes; a
+// pair cut between them leaves (m, l, O) partials that k_prefix_merge joins by log-sum-exp.
+#include "attn.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of the 152 SMs
+constexpr int kChunk = 128;      // rows of a chunk
+constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
+
+// Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
+// up to vis by each, then each query's own entries ns .. ns + own - 1 and its window.
+struct __align__(16) Pair {
+  int32_t q0, q1;
+  int32_t first;  // the query whose table row holds the shared entries
+  int32_t ns;
+  int32_t vis0, vis1;
+  int32_t own0, own1;
+  int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
+  int32_t nshared; // shared chunks; own chunks follow
+  int32_t pad[2];
+};
+
+struct PrefixArgs {
+  int32_t B, G;
+  const int32_t* n_entries;
+  const int32_t* group_start;  // G == 0: null
+  const int32_t* n_shared;
+  int32_t shared_max, own_max, n_swa;
+  int64_t table_cap;  // entries a table row can hold
+  Pair* pairs;        // [pairs + 1], the last one holds the number of chunks
+  int32_t* gpair;     // [G + 3] first pair of each range of queries
+  int32_t* qpair;     // [B] pair * 2 + place
+  int32_t* cpair;     // [kClusters] pair of each cluster's first chunk
+  int32_t* totals;    // pairs, chunks
+  void* ws;
+};
+
+// exclusive sum over the block of x (all threads call); total = the block's sum
+__device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  __syncthreads();
+  return inc - x + (warp > 0 ? before : 0);
+}
+
+// The pairs of the batch and the chunks of each, by one CTA.  Ranges of queries: those before the
+// first group, the G groups, those behind the last (a range outside the groups shares nothing).
+__global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
+  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x;
+  if (tid == 0) s_bad = 0;
+  ptx::griddep_wait();
+  __syncthreads();
+  for (int g = tid; g < a.G; g += kPlanThreads) {
+    const int lo = a.group_start[g], hi = a.group_start[g + 1];
+    if (lo < 0 || hi < lo || hi > a.B) {
+      s_bad = 1;
+      report_error(a.ws, CSA2_ERR_INDEX_RANGE, g);
+    }
+  }
+  __syncthreads();
+  const int G = s_bad ? 0 : a.G;
+  const int R = G + 2;  // ranges; without groups the first is empty
+  auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
+  auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
+  int base = 0;
+  for (int v0 = 0; v0 < R; v0 += kPlanThreads) {
+    const int v = v0 + tid;
+    const int n = v < R ? (range_hi(v) - range_lo(v) + 1) / 2 : 0;
+    int total;
+    const int at = base + block_scan(n, s_warp, &total);
+    if (v < R) a.gpair[v] = at;
+    base += total;
+  }
+  if (tid == 0) a.gpair[R] = base;
+  const int np = base;
+  __syncthreads();
+  int chunks = 0;
+  for (int p0 = 0; p0 < np; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    Pair x{};
+    int n = 0;
+    if (p < np) {
+      int lo = 0, hi = R;  // the range with gpair[v] <= p < gpair[v + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.gpair[mid] <= p) lo = mid;
+        else hi = mid;
+      }
+      const int first = range_lo(lo), end = range_hi(lo);
+      auto count = [&](int q) { return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap); };
+      x.q0 = first + 2 * (p - a.gpair[lo]);
+      x.q1 = x.q0 + 1 < end ? x.q0 + 1 : -1;
+      x.first = first;
+      // shared entries beyond the first query's own count are read as each query's own
+      if (lo >= 1 && lo <= G) x.ns = min(min(max(a.n_shared[lo - 1], 0), a.shared_max), count(first));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int q = i ? x.q1 : x.q0;
+        if (q < 0) continue;
+        const int c = count(q);
+        int own = max(c - x.ns, 0);
+        if (own > a.own_max) {
+          report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);
+          own = a.own_max;
+        }
+        (i ? x.vis1 : x.vis0) = min(x.ns, c);
+        (i ? x.own1 : x.own0) = own;
+        a.qpair[q] = 2 * p + i;
+      }
+      x.nshared = (max(x.vis0, x.vis1) + kChunk - 1) / kChunk;
+      const int own = max(x.own0, x.own1) + a.n_swa;
+      n = x.nshared + (x.q1 >= 0 ? (own + kOwnChunk - 1) / kOwnChunk : (own + kChunk - 1) / kChunk);
+    }
+    int total;
+    x.chunk0 = chunks + block_scan(n, s_warp, &total);
+    if (p < np) a.pairs[p] = x;
+    chunks += total;
+  }
+  if (tid == 0) {
+    a.pairs[np].chunk0 = chunks;
+    a.totals[0] = np;
+    a.totals[1] = chunks;
+  }
+  __syncthreads();
+  for (int c = tid; c < kClusters; c += kPlanThreads) {  // the pair of chunk floor(chunks * c / clusters)
+    const int t = (int)((long long)chunks * c / kClusters);
+    int lo = 0, hi = np;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.pairs[mid].chunk0 <= t) lo = mid;
+      else hi = mid;
+    }
+    a.cpair[c] = lo;
+  }
+}
+
+// ------------------------------------------------------------------ attention
+
+// warps 0-3: softmax, rescaling of O, epilogue; 4-7: rows of S's operand; 8-11: rows of O's; warp 12:
+// MMA issue (even CTA)
+constexpr int kSWarp = 4, kOWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
+constexpr int kPieces = 4;
+constexpr uint32_t kCols = 512;   // tensor memory: O 2 x 128 columns, S 2 x 64
+constexpr uint32_t kColS = 256;
+constexpr long long kWaitBudget = 1LL << 32;
+
+struct __align__(1024) PrefixSmem {
+  uint16_t q[kDMain / 8][kQPlane];          // q' [c/8][head][c%8]
+  uint16_t xs[kDMain / 8][kOwnChunk * 8];   // this CTA's 64 rows for S [c/8][row][c%8]
+  uint16_t xo[kDMain / 16][kChunk * 8];     // this CTA's 256 channels of all 128 rows [c/8][row][c%8]
+  uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
+  float c2[2][kHAtt];                       // by item: the next one's may be staged before this one's softmax
+  float red[2][kHAtt];
+  uint32_t vmask[2][4];                     // per S buffer: rows that exist
+  uint64_t q_load, q_full, staged[2];
+  uint64_t xs_full[kPieces], xs_free[kPieces];
+  uint64_t xo_full[kPieces], xo_free[kPieces];
+  uint64_t s_full[2], p_full[2], p_free[2], m_full[2];
+  uint64_t o_read;                          // epilogue done with O
+  uint64_t drained;                         // every MMA issued complete
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(PrefixSmem) <= 232448, "prefix attention shared memory");
+
+struct PrefixKernel {
+  const uint8_t *kv_codes, *kv_scales, *swa;
+  const uint16_t* q;
+  const int32_t* table;
+  int64_t max_pages;
+  int32_t n_pages, page_entries, n_swa;
+  float scale;
+  AttnExtras ex;
+  const Pair* pairs;
+  const int32_t *cpair, *totals;
+  float4* part_o;   // [pairs + clusters][2][64][128] float4: element c4 of thread t of the epilogue
+  float2* part_ml;  // [pairs + clusters][2][64]
+  void* ws;
+};
+
+// A row of a chunk: the plane row of an entry, kWindowRow + the index of a window row, or kNoRow.
+constexpr int64_t kNoRow = -1, kWindowRow = 1LL << 62;
+
+// Row i of chunk jc of pair x; a page outside the planes is reported once and skipped.
+__device__ __forceinline__ int64_t row_of(const PrefixKernel& k, const Pair& x, int jc, int i, bool report) {
+  int q, e;
+  if (jc < x.nshared) {
+    q = x.first;
+    e = jc * kChunk + i;
+    if (e >= x.ns) return kNoRow;
+  } else {
+    int idx, h = 0;
+    if (x.q1 < 0) {
+      idx = (jc - x.nshared) * kChunk + i;
+    } else {
+      h = i / kOwnChunk;
+      idx = (jc - x.nshared) * kOwnChunk + i % kOwnChunk;
+    }
+    q = h ? x.q1 : x.q0;
+    const int own = h ? x.own1 : x.own0;
+    if (idx >= own) {
+      idx -= own;
+      if (idx >= k.n_swa) return kNoRow;
+      const int64_t w = (int64_t)q * k.n_swa + idx;
+      if (k.ex.win_pos && __ldg(k.ex.win_pos + w) < max(__ldg(k.ex.win_lo + q), (int64_t)0)) return kNoRow;
+      return kWindowRow + w;
+    }
+    e = x.ns + idx;
+  }
+  const int page = __ldg(k.table + q * k.max_pages + e / k.page_entries);
+  if (page < 0 || page >= k.n_pages) {
+    if (report) report_error(k.ws, CSA2_ERR_INDEX_RANGE, page);
+    return kNoRow;
+  }
+  return (int64_t)page * k.page_entries + e % k.page_entries;
+}
+
+// 32 channels of an entry (16 bytes of codes, two scales) -> four 8-channel vectors of f16
+__device__ __forceinline__ void widen_codes(uint4 cw, uint32_t sc, uint4 (&v)[4]) {
+  const uint32_t s0 = e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u), s1 = e4m3x2_to_f16x2((sc >> 8) * 0x0101u);
+  const uint32_t wq[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h[4];
+    e2m1x8_to_f16(wq[q], h);
+    const uint32_t s = q < 2 ? s0 : s1;
+    v[q] = make_uint4(hmul2_u32(h[0], s), hmul2_u32(h[1], s), hmul2_u32(h[2], s), hmul2_u32(h[3], s));
+  }
+}
+// 16 channels of a window row
+__device__ __forceinline__ void widen_e4m3(uint4 w, uint4& a, uint4& b) {
+  a = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+  b = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
+}
+
+// One thread's fetched codes of 32 channels of a row.
+struct Fetch {
+  uint4 codes;
+  uint32_t scales;
+};
+// Starts the loads of 32-channel block cb of row r (window rows are read when they are written).
+__device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int64_t r, int cb) {
+  if (r >= 0 && r < kWindowRow) {
+    f.codes = __ldg(reinterpret_cast<const uint4*>(k.kv_codes + r * 256) + cb);
+    f.scales = __ldg(reinterpret_cast<const uint16_t*>(k.kv_scales + r * 32) + cb);
+  }
+}
+// Writes 32-channel block cb of the row to dst: vector q of it at dst + q * stride (f16 elements).
+__device__ __forceinline__ void put(const Fetch& f, const PrefixKernel& k, int64_t r, int cb, uint16_t* dst,
+                                    int stride) {
+  uint4 v[4];
+  if (r >= kWindowRow) {
+    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (r - kWindowRow) * kDMain) + 2 * cb;
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    widen_e4m3(a, v[0], v[1]);
+    widen_e4m3(b, v[2], v[3]);
+  } else if (r >= 0) {
+    widen_codes(f.codes, f.scales, v);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + q * stride) = v[q];
+}
+
+// The query of an item into q' and c2, by the eight row warps (w 0-7): its bf16 rows come through the
+// S operand's buffer, which S of the item before has left (n chunks so far).  Returns false when a
+// wait gave up.
+template <bool kEx>
+__device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k, int q, int w, int lane, uint32_t n,
+                                            uint32_t item) {
+  volatile int* abort_flag = &S.abort_flag;
+  bool good = n == 0 || ptx::mbar_wait_warp_cluster(&S.xs_free[kPieces - 1], (n - 1) & 1u, abort_flag, kWaitBudget);
+  if (good && q >= 0) {
+    if (w == 0 && lane == 0) {
+      ptx::mbar_arrive_expect_tx(&S.q_load, kHAtt * kDMain * 2);
+      ptx::bulk_g2s(&S.xs[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_load);
+    }
+    __syncwarp();
+    volatile int keep_waiting = 0;  // the copy writes shared memory: no leaving before it has landed
+    good = ptx::mbar_wait_warp(&S.q_load, item & 1u, &keep_waiting, kWaitBudget);
+    if (good) stage_q<kEx>(S.q, S.c2[item & 1u], &S.xs[0][0], k.scale, w, lane, k.ex, q);
+  } else if (good) {  // no second query: zeros
+    if (w == 0 && lane == 0) ptx::mbar_arrive(&S.q_load);  // keeps its phase
+    for (int i = w * 32 + lane; i < kDMain / 8 * kQPlane / 8; i += 256)
+      reinterpret_cast<uint4*>(&S.q[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (w == 0) S.c2[item & 1u][lane] = S.c2[item & 1u][lane + 32] = 0.0f;
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::mbar_arrive(&S.staged[item & 1u]);
+    ptx::mbar_arrive_cluster(&S.q_full, 0);
+  }
+  return good;
+}
+
+// Chunks [c0, c0 + nc) of pair x by the four row warps of one operand.  kS: this CTA's 64 rows of S's
+// operand, handed over by 128 channels (rows 32 u + rl, block 4 i + cb in piece i); otherwise its 256
+// channels of O's, by 32 rows (row 32 i + rl, blocks 4 u + cb of its eight in piece i).  A warp's eight
+// rows x four 16-byte blocks read 64 contiguous bytes of eight rows, and its stores write eight rows of
+// a plane: no bank conflicts.  The loads of a piece of the next chunk start once this chunk's is written.
+template <bool kEx, bool kS>
+__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, uint32_t rank, int qme,
+                                          int c0, int nc, int warp, int lane, uint32_t n, uint32_t item) {
+  volatile int* abort_flag = &S.abort_flag;
+  constexpr int kN = kS ? 2 : 4;  // rows of this thread in a chunk
+  const int w4 = warp & 3, rl = 8 * w4 + (lane & 7), cb = lane >> 3;
+  int64_t r[kN], rn[kN];
+  Fetch f[kPieces][2];
+  auto rows = [&](int64_t (&d)[kN], int jc) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      d[i] = row_of(k, x, jc, (kS ? kOwnChunk * (int)rank : 0) + 32 * i + rl, !kS && rank == 0 && cb == 0);
+  };
+  auto fetch_piece = [&](const int64_t (&d)[kN], int i) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (kS) fetch(f[i][u], k, d[u], 4 * i + cb);
+      else fetch(f[i][u], k, d[i % kN], 8 * (int)rank + 4 * u + cb);
+  };
+  auto masks = [&](const int64_t (&d)[kN], uint32_t m) {  // rows of chunk number m that exist
+    if (kS) return;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const uint32_t v = __ballot_sync(0xffffffffu, d[i] >= 0) & 0xFFu;
+      if (lane == 0) reinterpret_cast<uint8_t*>(&S.vmask[m & 1][i])[w4] = (uint8_t)v;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.m_full[m & 1]);
+  };
+  rows(r, c0);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) fetch_piece(r, i);
+  bool good = stage_query<kEx>(S, k, qme, warp - kSWarp, lane, n, item);
+  // every row warp has read the query's bf16 rows: the S operand's buffer may be written
+  if (kS && good) good = ptx::mbar_wait_warp(&S.staged[item & 1u], (item >> 1) & 1u, abort_flag, kWaitBudget);
+  if (good) masks(r, n);
+  for (int j = 0; j < nc && good; ++j) {
+    const uint32_t m = n + (uint32_t)j;
+    const bool more = j + 1 < nc;
+    if (more) rows(rn, c0 + j + 1);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (m > 0)
+        good = good && ptx::mbar_wait_warp_cluster(kS ? &S.xs_free[i] : &S.xo_free[i], (m - 1) & 1u, abort_flag,
+                                                   kWaitBudget);
+      if (good) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (kS) put(f[i][u], k, r[u], 4 * i + cb, &S.xs[4 * (4 * i + cb)][(32 * u + rl) * 8], kOwnChunk * 8);
+          else
+            put(f[i][u], k, r[i % kN], 8 * (int)rank + 4 * u + cb, &S.xo[4 * (4 * u + cb)][(32 * i + rl) * 8],
+                kChunk * 8);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(kS ? &S.xs_full[i] : &S.xo_full[i], 0);
+        if (more) fetch_piece(rn, i);
+      }
+    }
+    if (good && more) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) r[i] = rn[i];
+      masks(r, m + 1);
+    }
+  }
+  return good;
+}
+
+// p = 2^(s c2 - m) of 32 rows, packed in pairs as f16 from the fp32 values whose sum goes to `sum`;
+// returns the largest exponent.  Rows that the mask has not are -inf.
+__device__ __forceinline__ float probs32(const uint32_t (&s)[32], uint32_t mask, float c2, float m, uint32_t* ph,
+                                         float& sum) {
+  float top = -INFINITY, s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    float e0 = fmaf(__uint_as_float(s[2 * u]), c2, -m), e1 = fmaf(__uint_as_float(s[2 * u + 1]), c2, -m);
+    if (!((mask >> (2 * u)) & 1u)) e0 = -INFINITY;
+    if (!((mask >> (2 * u + 1)) & 1u)) e1 = -INFINITY;
+    top = fmaxf(top, fmaxf(e0, e1));
+    const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
+    s0 += p0;
+    s1 += p1;
+    const __half2 h2 = __floats2half2_rn(p0, p1);
+    ph[u] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  sum = s0 + s1;
+  return top;
+}
+
+template <bool kEx>
+__global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  PrefixSmem& S = *reinterpret_cast<PrefixSmem*>(smem_raw);
+  volatile int* abort_flag = &S.abort_flag;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int cluster = blockIdx.x / 2;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      ptx::mbar_init(&S.q_load, 1);
+      ptx::mbar_init(&S.drained, 1);
+      ptx::mbar_init(&S.q_full, 16);  // barriers that the MMA warp waits on count both CTAs' warps
+      for (int i = 0; i < kPieces; ++i) {
+        ptx::mbar_init(&S.xs_full[i], 8);
+        ptx::mbar_init(&S.xo_full[i], 8);
+        ptx::mbar_init(&S.xs_free[i], 1);
+        ptx::mbar_init(&S.xo_free[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        ptx::mbar_init(&S.staged[i], 8);
+        ptx::mbar_init(&S.s_full[i], 1);
+        ptx::mbar_init(&S.p_full[i], 8);
+        ptx::mbar_init(&S.p_free[i], 1);
+        ptx::mbar_init(&S.m_full[i], 4);
+      }
+      ptx::mbar_init(&S.o_read, 8);
+      S.abort_flag = 0;
+      ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    ptx::tmem_alloc_pair(&S.tmem_base, kCols);
+  }
+  ptx::griddep_wait();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // both CTAs' barriers initialised
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  const int total = __ldg(k.totals + 1);
+  const int t0 = (int)((long long)total * cluster / kClusters), t1 = (int)((long long)total * (cluster + 1) / kClusters);
+  auto wait = [&](uint64_t* bar, uint32_t n) {
+    return ptx::mbar_wait_warp_cluster(bar, n & 1u, abort_flag, kWaitBudget);
+  };
+  bool good = true;
+  int where = 0;
+
+  // Every role runs the same list of items: pair p, its chunks [c0, c1).  n counts chunks.
+  int p = t0 < t1 ? __ldg(k.cpair + cluster) : 0;
+  uint32_t n = 0, items = 0;
+  for (int t = t0; t < t1 && good; ++p) {
+    const Pair x = k.pairs[p];
+    const int pend = k.pairs[p + 1].chunk0;
+    if (pend <= t) continue;  // a pair without chunks
+    const int c0 = t - x.chunk0, c1 = min(pend, t1) - x.chunk0, nc = c1 - c0;
+    t += nc;
+    const int qme = rank ? x.q1 : x.q0;
+
+    if (warp >= kSWarp && warp < kMmaWarp) {
+      // ---- the rows of S's operand (warps 4-7) and of O's (8-11)
+      good = warp < kOWarp ? rows_role<kEx, true>(S, k, x, rank, qme, c0, nc, warp, lane, n, items)
+                           : rows_role<kEx, false>(S, k, x, rank, qme, c0, nc, warp, lane, n, items);
+      where = warp < kOWarp ? 31 : 32;
+    } else if (warp == kMmaWarp) {
+      // ---- MMA issue (even CTA): S(0), then S(j + 1) before O(j)
+      if (rank == 0) {
+        constexpr uint32_t idesc_s = ptx::idesc_f16(128, kChunk, 0);
+        constexpr uint32_t idesc_o = ptx::idesc_f16(128, 256, 0) | ptx::kIdescBMajorMN;
+        const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
+        const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
+        const uint64_t dp = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
+        const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0], 128, kChunk * 16);
+        good = wait(&S.q_full, items);
+        for (int j = 0; j <= nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j;
+          if (j < nc) {
+            const uint32_t dst = tmem + kColS + 64u * (m & 1u);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              if (good) good = wait(&S.xs_full[i], m);
+              if (!good) break;
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int ks = 8 * i; ks < 8 * i + 8; ++ks)  // q'[2 ks], xs[2 ks]: 2048 bytes on
+                ptx::mma_f16_ss_pair_elect(dst, da + (uint64_t)(ks * 128), db + (uint64_t)(ks * 128), idesc_s,
+                                           ks > 0 ? 1u : 0u);
+              ptx::mma_commit_pair_elect(&S.xs_free[i]);
+            }
+            if (good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
+          }
+          if (j > 0 && good) {
+            const uint32_t o = m - 1;
+            good = wait(&S.p_full[o & 1], o >> 1);
+            if (good && j == 1 && items > 0) good = wait(&S.o_read, items - 1);
+            const uint64_t dpo = dp + (uint64_t)((o & 1u) * (kChunk / 8 * kHAtt * 16 / 16));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              if (good) good = wait(&S.xo_full[i], o);
+              if (!good) break;
+              ptx::tc_fence_after();
+#pragma unroll
+              for (int ks = 2 * i; ks < 2 * i + 2; ++ks)  // p[2 ks]: 2048 bytes on; xo rows 16 ks: 256 bytes on
+#pragma unroll
+                for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[16 h], 32 KB on
+                  ptx::mma_f16_ss_pair_elect(tmem + 128u * (uint32_t)h, dpo + (uint64_t)(ks * 128),
+                                             dx + (uint64_t)(h * 2048 + ks * 16), idesc_o,
+                                             (j > 1 || ks > 0) ? 1u : 0u);
+              ptx::mma_commit_pair_elect(&S.xo_free[i]);
+            }
+            if (good) ptx::mma_commit_pair_elect(&S.p_free[o & 1]);
+          }
+        }
+      }
+      where = 33;
+    } else {
+      // ---- softmax: thread t head t % 64, chunk rows 64 (t / 64) ..
+      const int h = tid & 63, half = tid >> 6;
+      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+      const int vis = rank ? x.vis1 : x.vis0;
+      float m2 = -INFINITY, lsum = 0.0f, c2 = 0.0f;
+      for (int j = 0; j < nc; ++j) {
+        const uint32_t m = n + (uint32_t)j, slot = m & 1u;
+        good = good && wait(&S.s_full[slot], m >> 1) && wait(&S.m_full[slot], m >> 1);
+        if (good && j == 0) good = wait(&S.staged[items & 1u], items >> 1);  // c2
+        if (good && m >= 2) good = wait(&S.p_free[slot], (m >> 1) - 1);
+        const uint32_t ta = tmem + lane_base + kColS + 64u * slot;
+        uint32_t mk[2] = {0u, 0u};
+        uint32_t pp[32];
+        float sum = 0.0f;
+        bool over = false;
+        auto probs = [&](float ref) {
+          float top = -INFINITY;
+          sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[32];
+            float s1;
+            ptx::tmem_ld_32x32b_x32(ta + 32u * (uint32_t)i, a);
+            ptx::tmem_wait_ld();
+            top = fmaxf(top, probs32(a, mk[i], c2, ref, pp + 16 * i, s1));
+            sum += s1;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(&S.p[slot][8 * half + i][h * 8]) =
+                make_uint4(pp[4 * i], pp[4 * i + 1], pp[4 * i + 2], pp[4 * i + 3]);
+          ptx::fence_proxy_async_smem();
+          return top;
+        };
+        if (good) {
+          ptx::tc_fence_after();
+          if (j == 0) c2 = S.c2[items & 1u][h];
+          const int jc = c0 + j;
+          if (jc < x.nshared) {  // entries below this query's own count
+            const int left = vis - jc * kChunk - 64 * half;
+            mk[0] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+            mk[1] = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1u : 0u;
+          } else if (x.q1 < 0 ? rank == 0 : half == (int)rank) {
+            mk[0] = mk[1] = ~0u;
+          }
+          mk[0] &= S.vmask[slot][2 * half];
+          mk[1] &= S.vmask[slot][2 * half + 1];
+          over = probs(m2 == -INFINITY ? kNoRef : m2) > kTau2;
+        }
+        const uint32_t nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
+        if (nv >= 8) {
+          good = false;
+          break;
+        }
+        float alpha = 1.0f;
+        if (nv != 0) {
+          // the chunk's maximum of this head over both threads' rows
+          float cm = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[32];
+            ptx::tmem_ld_32x32b_x32(ta + 32u * (uint32_t)i, a);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) cm = fmaxf(cm, ((mk[i] >> u) & 1u) ? __uint_as_float(a[u]) : -INFINITY);
+          }
+          S.red[half][h] = cm;
+          softmax_sync();
+          cm = fmaxf(S.red[0][h], S.red[1][h]) * c2;
+          if (cm > m2 + kTau2) {
+            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
+            m2 = cm;
+          }
+          (void)probs(m2 == -INFINITY ? kNoRef : m2);
+          if (j > 0) {  // O holds earlier chunks: scale the rows of the heads that moved
+            good = wait(&S.p_free[slot ^ 1u], (m - 1) >> 1);
+            if (good && __any_sync(0xffffffffu, alpha != 1.0f)) {
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 256; c += 32) {
+                uint32_t a[32];
+                ptx::tmem_ld_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) * alpha);
+                ptx::tmem_st_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
+              }
+              ptx::tmem_wait_st();
+            }
+          }
+        }
+        if (good) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(&S.p_full[slot], 0);
+        }
+        lsum = fmaf(alpha, lsum, sum);
+      }
+      // ---- this item's partial: reference, sum, O
+      const uint32_t last = n + (uint32_t)nc - 1;
+      good = good && wait(&S.p_free[last & 1u], last >> 1);
+      // the four warps leave together, or none
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
+      if (good) {
+        ptx::tc_fence_after();
+        const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
+        if (qme >= 0) {
+          float4* po = k.part_o + slot * 64 * 128 + tid;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t a[32];
+            ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              po[(c * 8 + u) * 128] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]),
+                                                  __uint_as_float(a[4 * u + 2]), __uint_as_float(a[4 * u + 3]));
+          }
+        }
+        S.red[half][h] = lsum;
+        softmax_sync();
+        if (half == 0 && qme >= 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, S.red[0][h] + S.red[1][h]);
+        softmax_sync();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(&S.o_read, 0);
+      }
+      where = 34;
+    }
+    n += (uint32_t)nc;
+    ++items;
+  }
+  if (!good && lane == 0 && !*abort_flag) {
+    *abort_flag = 1;
+    report_error(k.ws, CSA2_ERR_DEVICE_TIMEOUT, where);
+  }
+  if (warp == kMmaWarp && rank == 0) {  // every MMA has completed before tensor memory is freed
+    ptx::mma_commit_pair_elect(&S.drained);
+    volatile int keep_waiting = 0;
+    ptx::mbar_wait_warp(&S.drained, 0, &keep_waiting, kWaitBudget);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // no CTA leaves while the other may still arrive on its barriers
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, kCols);
+  }
+}
+
+// Joins the partials of one query: thread t of a CTA has head t % 64 and, of channel half t / 64, the
+// eight float4 of column block blockIdx.y (channels 256 (t / 64) + 32 blockIdx.y ..).
+__global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ qpair,
+                                                      const int32_t* __restrict__ totals,
+                                                      const float4* __restrict__ part_o,
+                                                      const float2* __restrict__ part_ml, AttnExtras ex,
+                                                      void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
+  ptx::griddep_wait();
+  const int b = blockIdx.x, t = threadIdx.x, h = t & 63, half = t >> 6;
+  const int pr = qpair[b], p = pr >> 1, r = pr & 1;
+  const long long total = totals[1];
+  const int s0 = pairs[p].chunk0, s1 = pairs[p + 1].chunk0;
+  // clusters that ran chunks s0 .. s1 - 1: chunk t belongs to cluster ceil((t + 1) clusters / total) - 1
+  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * kClusters + total - 1) / total) - 1 : 0;
+  const int k1 = s1 > s0 ? (int)((s1 * (long long)kClusters + total - 1) / total) : 0;
+  const float z2 = ex.sink ? ex.sink[h] * kLog2e : -INFINITY;
+  float ref = z2;
+  auto ran = [&](int c) {  // with fewer chunks than clusters, some have none
+    return max((long long)s0, total * c / kClusters) < min((long long)s1, total * (c + 1) / kClusters);
+  };
+  for (int c = k0; c < k1; ++c) {
+    if (!ran(c)) continue;
+    const float2 ml = part_ml[((int64_t)(p + c) * 2 + r) * kHAtt + h];
+    if (ml.y > 0.0f) ref = fmaxf(ref, ml.x);
+  }
+  float L = ref > -INFINITY && ex.sink ? ptx::ex2(z2 - ref) : 0.0f;
+  float4 acc[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = k0; c < k1; ++c) {
+    if (!ran(c)) continue;
+    const int64_t slot = (int64_t)(p + c) * 2 + r;
+    const float2 ml = part_ml[slot * kHAtt + h];
+    if (!(ml.y > 0.0f)) continue;
+    const float f = ptx::ex2(ml.x - ref);
+    L = fmaf(f, ml.y, L);
+    const float4* po = part_o + (slot * 64 + blockIdx.y * 8) * 128 + t;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float4 v = po[u * 128];
+      acc[u].x = fmaf(f, v.x, acc[u].x);
+      acc[u].y = fmaf(f, v.y, acc[u].y);
+      acc[u].z = fmaf(f, v.z, acc[u].z);
+      acc[u].w = fmaf(f, v.w, acc[u].w);
+    }
+  }
+  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+  const int c0 = 256 * half + 32 * blockIdx.y;
+  if (ex.rope && c0 >= kRopeFirst) {  // turn back by -q_pos
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float cs, sn;
+      rope_cos_sin(ex.th.t[(c0 - kRopeFirst) / 2 + 2 * u], (double)ex.qpos[b], cs, sn);
+      rope_pair(acc[u].x, acc[u].y, cs, -sn);
+      rope_cos_sin(ex.th.t[(c0 - kRopeFirst) / 2 + 2 * u + 1], (double)ex.qpos[b], cs, sn);
+      rope_pair(acc[u].z, acc[u].w, cs, -sn);
+    }
+  }
+  const int64_t row = ((int64_t)b * kHAtt + h) * kDMain + c0;
+  if (out_bf16) {
+    uint32_t w[16];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[u].x * inv, acc[u].y * inv);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[u].z * inv, acc[u].w * inv);
+      w[2 * u] = *reinterpret_cast<const uint32_t*>(&lo);
+      w[2 * u + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    }
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  } else {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) o[u] = make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
+  }
+  if (lse && blockIdx.y == 0 && half == 0)
+    lse[b * kHAtt + h] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
+}
+
+struct PrefixWs {
+  Pair* pairs;
+  int32_t *gpair, *qpair, *cpair, *totals;
+  float4* part_o;
+  float2* part_ml;
+  size_t bytes;
+};
+int max_pairs(int32_t B, int32_t G) { return (B + G + 2) / 2; }
+
+PrefixWs prefix_ws(void* ws, int32_t B, int32_t G) {
+  PrefixWs L{};
+  size_t off = kWsHeader;
+  char* base = (char*)ws;
+  auto take = [&](size_t n) {
+    char* p = base ? base + off : nullptr;
+    off += align_up(n, 256);
+    return p;
+  };
+  const size_t slots = (size_t)max_pairs(B, G) + kClusters;
+  L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
+  L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
+  L.qpair = (int32_t*)take((size_t)B * 4);
+  L.cpair = (int32_t*)take(kClusters * 4);
+  L.totals = (int32_t*)take(8);
+  L.part_o = (float4*)take(slots * 2 * kHAtt * kDMain * 4);
+  L.part_ml = (float2*)take(slots * 2 * kHAtt * 8);
+  L.bytes = off;
+  return L;
+}
+
+template <typename K>
+cudaError_t launch_pairs(void (*kern)(K), int clusters, size_t smem, cudaStream_t st, const K& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
+}  // namespace
+}  // namespace csa2
+
+extern "C" size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t n_shared_max, int64_t n_own_max,
+                                                  int32_t n_swa) {
+  if (B <= 0 || B > 65535 || G <= 0 || G > B || n_shared_max < 0 || n_own_max < 0 || n_shared_max > CSA2_MAX_DENSE ||
+      n_own_max > CSA2_MAX_DENSE || n_swa < 0)
+    return 0;
+  return csa2::prefix_ws(nullptr, B, G).bytes;
+}
+
+extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                               const int32_t* n_entries, int32_t G, const int32_t* group_start,
+                                               const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
+                                               const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16,
+                                               float softmax_scale, const csa2_norm_rope* q_nr, const int64_t* q_pos,
+                                               const float* sink, const csa2_window* win, void* out, int32_t out_type,
+                                               float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (!planes_ok(kv) || B <= 0 || B > 65535 || G <= 0 || G > B || n_shared_max < 0 || n_own_max < 0 ||
+      n_shared_max > CSA2_MAX_DENSE || n_own_max > CSA2_MAX_DENSE || n_swa < 0 || n_swa > CSA2_MAX_SWA ||
+      !pages_ok(pages, kv, n_shared_max) || !pages_ok(pages, kv, n_own_max))
+    return CSA2_ERR_INVALID_ARG;
+  if (!n_entries || !group_start || !n_shared || !aligned(n_entries, 4) || !aligned(group_start, 4) ||
+      !aligned(n_shared, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out || !aligned(q_bf16, 16) ||
+      !aligned(out, 16) || (swa_e4m3 && !aligned(swa_e4m3, 16)) || (lse_out && !aligned(lse_out, 4)))
+    return CSA2_ERR_INVALID_ARG;
+  if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
+  AttnExtras ex;
+  const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
+  if (bad != CSA2_OK) return bad;
+  if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+  const PrefixWs L = prefix_ws(ws, B, G);
+  if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
+  const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals, ws};
+  {
+    KernelTimer timer("k_prefix_plan", st);
+    launch_pdl(k_prefix_plan, dim3(1), dim3(kPlanThreads), 0, st, a);
+  }
+  auto kern = ex.qnorm_w || ex.rope ? k_prefix_attn<true> : k_prefix_attn<false>;
+  const size_t smem = sizeof(PrefixSmem);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return launch_status();
+  {
+    const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, (const uint16_t*)q_bf16, pages->table,
+                         pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, softmax_scale, ex,
+                         L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
+    KernelTimer timer("k_prefix_attn", st);
+    launch_pairs(kern, kClusters, smem, st, k);
+  }
+  {
+    KernelTimer timer("k_prefix_merge", st);
+    launch_pdl(k_prefix_merge, dim3(B, 8), dim3(128), 0, st, (const Pair*)L.pairs, (const int32_t*)L.qpair,
+               (const int32_t*)L.totals, (const float4*)L.part_o, (const float2*)L.part_ml, ex, out,
+               out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+  }
+  return launch_status();
+}

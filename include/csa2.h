@@ -59,7 +59,8 @@ typedef enum {
   CSA2_ERR_WORKSPACE = 3,     /* workspace missing, misaligned or too small       */
   CSA2_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed             */
   CSA2_ERR_DEVICE_TIMEOUT = 5,/* a bounded device-side wait gave up               */
-  CSA2_ERR_INDEX_RANGE = 6    /* a top-k / pool index outside the sequence slot   */
+  CSA2_ERR_INDEX_RANGE = 6,   /* a top-k / pool index outside the sequence slot   */
+  CSA2_ERR_NO_PAGES = 7       /* a page-table call needs more pages than are free */
 } csa2_status;
 
 typedef void* csa2_stream; /* a cudaStream_t */
@@ -418,6 +419,102 @@ csa2_status csa2_dense_attn_decode(const csa2_kv_planes* kv, int32_t B, const in
                                    float* out, float* lse_out, void* ws, size_t ws_bytes,
                                    csa2_stream stream);
 size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
+
+/* -------------------------------------------------------------- paged cache */
+
+/* The design pages describe no paged cache; these calls exist for serving loops, whose
+ * sequences grow, share prefixes and end at different times.  A page is a slot of a
+ * csa2_kv_planes: page p holds kv->seq_stride entries (the page size P, any size >= 1),
+ * and entry j of a sequence lives in page table[j / P] at index j % P.  So csa2_cache_append
+ * writes into pages as it does into slots: its slot[] and entry[] are the row_slot and
+ * row_entry of csa2_page_tables, n_slots the number of pages. */
+
+/* Page tables and slot maps from request lengths, built on the GPU without reading anything
+ * back.  Request b holds n_have[b] entries and gets n_new[b] more; n_new[b] < 0 drops its
+ * last -n_new[b] (rejected drafts; -n_have[b] when it has ended).
+ *   page_table [B][max_pages]  the pages request b gains are written behind the ceil(n_have[b]
+ *              / page_entries) it has; every other element stays as it is
+ *   free_pages [n_pages], n_free [1]  stack of free page ids, its top at n_free[0] - 1.  First
+ *              the pages that no longer hold an entry are pushed (in order of request and
+ *              page), then the new ones are popped (in the same order), so a page given back
+ *              may be taken by another request in the same call.  Elements below n_free[0]
+ *              stay as they are
+ *   n_kept     [B] or NULL: leading pages of row b that belong to someone else as well (a
+ *              shared prefix) and are never given back
+ *   n_free_out [1], n_entries [B]  the new values (n_have[b] + n_new[b]); each may be the input
+ *              it follows, for a step replayed from a CUDA graph
+ *   row_*      [n_rows], each optional: one row per new entry, in order of request and entry:
+ *              request, page, index in the page, and position (entry index * m, the position of
+ *              csa2_cache_append's and csa2_swa_append's pos for m tokens per entry).  Rows behind
+ *              the last new entry are -1
+ *   row_start  [B + 1] optional: first map row of each request, and their number
+ * All or nothing: when a length is negative or beyond max_pages * page_entries (or 2^31 - 1), the
+ * new entries exceed n_rows (with any row_* given), n_free or a page id that would move lies
+ * outside [0, n_pages] (CSA2_ERR_INDEX_RANGE), or too few pages are free (CSA2_ERR_NO_PAGES,
+ * detail = pages missing), the error word says so, no table or stack element changes, n_entries =
+ * n_have, n_free_out = n_free, row_start = 0 and every row is -1.  A page listed twice is not
+ * noticed.  1 <= B <= 65535, page_entries, m, max_pages, n_pages >= 1; arrays aligned to their
+ * elements; arrays other than the two named pairs must not overlap. */
+csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const int32_t* n_new, int32_t page_entries,
+                             int32_t m, const int32_t* n_kept, int32_t* page_table, int32_t max_pages,
+                             int32_t n_pages, int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out,
+                             int32_t* n_entries, int32_t n_rows, int32_t* row_query, int32_t* row_slot,
+                             int64_t* row_entry, int64_t* row_pos, int32_t* row_start, void* ws, size_t ws_bytes,
+                             csa2_stream stream);
+size_t csa2_page_tables_workspace_size(int32_t B);
+
+/* Page table of an attention call. */
+typedef struct {
+  const int32_t* table; /* [B][max_pages] page ids (device) */
+  int32_t max_pages;    /* row length */
+  int32_t n_pages;      /* pages of the planes: valid ids are [0, n_pages) */
+} csa2_pages;
+
+/* Type of an attention call's output. */
+typedef enum { CSA2_OUT_F32 = 0, CSA2_OUT_BF16 = 1 } csa2_out_type;
+
+/* csa2_dense_attn_decode over a paged cache: query b attends to entries [0, n_entries[b]) of the
+ * sequence whose pages are row b of the table, joined with its window rows.
+ *   n_entries  [B] int32 (device); values above n_max count as n_max, negative ones as 0
+ *   n_max      host bound, 0 <= n_max <= min(CSA2_MAX_DENSE, pages->max_pages * kv->seq_stride)
+ *   out        [B][64][512] of out_type (fp32, or bf16 rounded once), 16-byte aligned
+ * Only table elements below ceil(n_entries[b] / seq_stride) are read, and of the last page only the
+ * entries that exist.  A page id outside [0, n_pages) is reported as CSA2_ERR_INDEX_RANGE and its
+ * entries are skipped.  Probabilities are rounded to f16 for the tensor cores (relative 2^-12), their
+ * sum and the logsumexp are kept in fp32.  Every other argument as in csa2_dense_attn_decode; the
+ * workspace is csa2_paged_attn_workspace_size(B, n_max, n_swa) bytes. */
+csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                   const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3, int32_t n_swa,
+                                   const void* q_bf16, float softmax_scale, const csa2_norm_rope* q_nr,
+                                   const int64_t* q_pos, const float* sink, const csa2_window* win, void* out,
+                                   int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream);
+size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
+
+/* csa2_paged_attn_decode for a batch whose queries share prefixes (one system prompt, one document,
+ * samples drawn in parallel): group g is the queries [group_start[g], group_start[g + 1]), whose
+ * sequences agree on their first n_shared[g] entries.  Those are read once for the group, through the
+ * table row of its first query; entries from n_shared[g] on, and the window, are each query's own,
+ * through its own row.  The result is that of csa2_paged_attn_decode.
+ *   group_start  [G + 1] int32 (device), ascending within [0, B]; queries outside every group share
+ *                nothing.  A group that is not ascending, or leaves [0, B], counts as empty and is
+ *                reported as CSA2_ERR_INDEX_RANGE
+ *   n_shared     [G] int32 (device): negative counts as 0, more than n_shared_max as n_shared_max
+ *                (the rest is read as each query's own).  A query shorter than n_shared sees its
+ *                first n_entries[b] entries only
+ *   n_shared_max, n_own_max  host bounds of the shared and of each query's own entries, each within
+ *                [0, min(CSA2_MAX_DENSE, pages->max_pages * kv->seq_stride)].  Own entries beyond
+ *                n_own_max are left out and reported as CSA2_ERR_INDEX_RANGE (detail n_entries[b]);
+ *                n_entries[b] above pages->max_pages * kv->seq_stride counts as that
+ * 1 <= G <= B.  Every other argument as in csa2_paged_attn_decode; the workspace is
+ * csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa) bytes. */
+csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                    const int32_t* n_entries, int32_t G, const int32_t* group_start,
+                                    const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
+                                    const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
+                                    const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink,
+                                    const csa2_window* win, void* out, int32_t out_type, float* lse_out, void* ws,
+                                    size_t ws_bytes, csa2_stream stream);
+size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t n_shared_max, int64_t n_own_max, int32_t n_swa);
 
 /* ---------------------------------------------------------------- schedule */
 
