@@ -814,6 +814,7 @@ namespace csa2 {
 bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
   if (!p || p->max_pages < 0 || p->n_pages < 0 || kv->seq_stride > INT32_MAX) return false;
   if (n > 0 && (!p->table || !aligned(p->table, 4))) return false;
+  if ((int64_t)p->n_pages * kv->seq_stride > INT32_MAX) return false;  // plane rows are 32-bit
   return n <= (int64_t)p->max_pages * kv->seq_stride;
 }
 }  // namespace csa2

@@ -30,7 +30,7 @@ constexpr int kOwnChunk = 64;    // of which each query of a pair has this many 
 
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
 // up to vis by each, then each query's own entries ns .. ns + own - 1 and its window.
-struct __align__(16) Pair {
+struct Pair {
   int32_t q0, q1;
   int32_t first;  // the query whose table row holds the shared entries
   int32_t ns;
@@ -38,7 +38,6 @@ struct __align__(16) Pair {
   int32_t own0, own1;
   int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
   int32_t nshared; // shared chunks; own chunks follow
-  int32_t pad[2];
 };
 
 struct PrefixArgs {
@@ -160,8 +159,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
     a.totals[1] = chunks;
   }
   __syncthreads();
-  for (int c = tid; c < kClusters; c += kPlanThreads) {  // the pair of chunk floor(chunks * c / clusters)
-    const int t = (int)((long long)chunks * c / kClusters);
+  const int clusters = min(kClusters, chunks);
+  for (int c = tid; c < clusters; c += kPlanThreads) {  // the pair of chunk floor(chunks * c / clusters)
+    const int t = (int)((long long)chunks * c / clusters);
     int lo = 0, hi = np;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -174,10 +174,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
 
 // ------------------------------------------------------------------ attention
 
-// warps 0-3: softmax, rescaling of O, epilogue; 4-7: rows of S's operand; 8-11: rows of O's; warp 12:
-// MMA issue (even CTA)
-constexpr int kSWarp = 4, kOWarp = 8, kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+// warps 0-3: softmax, rescaling of O, epilogue; 4-11: rows of S's operand; 12-19: rows of O's; then one
+// warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), row masks
+constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kMaskWarp = 22;
+constexpr int kThreads = 24 * 32;  // and one that fills the last warpgroup
+// registers of a thread: 80 at launch, then by warpgroup (softmax, four of rows, the last)
+constexpr int kSoftRegs = 128, kRowRegs = 72, kMmaRegs = 64;
+static_assert(kSoftRegs + 4 * kRowRegs + kMmaRegs <= 6 * 80, "registers of the launch");
 constexpr int kPieces = 4;
 constexpr uint32_t kCols = 512;   // tensor memory: O 2 x 128 columns, S 2 x 64
 constexpr uint32_t kColS = 256;
@@ -188,15 +191,17 @@ struct __align__(1024) PrefixSmem {
   uint16_t xs[kDMain / 8][kOwnChunk * 8];   // this CTA's 64 rows for S [c/8][row][c%8]
   uint16_t xo[kDMain / 16][kChunk * 8];     // this CTA's 256 channels of all 128 rows [c/8][row][c%8]
   uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
-  float c2[2][kHAtt];                       // by item: the next one's may be staged before this one's softmax
+  float c2[4][kHAtt];                       // by item: later ones are staged before this one's softmax
   float red[2][kHAtt];
   uint32_t vmask[2][4];                     // per S buffer: rows that exist
-  uint64_t q_load, q_full, staged[2];
-  uint64_t xs_full[kPieces], xs_free[kPieces];
-  uint64_t xo_full[kPieces], xo_free[kPieces];
+  Pair pair[kThreads / 32];                 // each warp's copy of its item's pair: not held in registers
+  // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
+  // of the same role passes on for all of that CTA's
+  uint64_t q_load, q_full, staged[4];
+  uint64_t x_full[2][kPieces], x_free[2][kPieces];  // [0] S's operand, [1] O's
   uint64_t s_full[2], p_full[2], p_free[2], m_full[2];
   uint64_t o_read;                          // epilogue done with O
-  uint64_t drained;                         // every MMA issued complete
+  uint64_t drained;                         // every MMA issued complete (two warps)
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -208,6 +213,7 @@ struct PrefixKernel {
   const int32_t* table;
   int64_t max_pages;
   int32_t n_pages, page_entries, n_swa;
+  uint64_t page_div;  // ceil(2^40 / page_entries): e * page_div >> 40 = e / page_entries for e < 2^18
   float scale;
   AttnExtras ex;
   const Pair* pairs;
@@ -217,16 +223,20 @@ struct PrefixKernel {
   void* ws;
 };
 
-// A row of a chunk: the plane row of an entry, kWindowRow + the index of a window row, or kNoRow.
-constexpr int64_t kNoRow = -1, kWindowRow = 1LL << 62;
+// A row of a chunk: the plane row of an entry (>= 0), kNoRow, or a window row (kNoRow - 1 - its index).
+constexpr int kNoRow = -1;
 
-// Row i of chunk jc of pair x; a page outside the planes is reported once and skipped.
-__device__ __forceinline__ int64_t row_of(const PrefixKernel& k, const Pair& x, int jc, int i, bool report) {
+// Row i of chunk jc of pair x, in two steps so that the page's load is not waited for at once: the page
+// (valid when off >= 0) and the entry's place in it, or kNoRow / a window row as `off`.
+struct RowRef {
+  int page, off;
+};
+__device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x, int jc, int i) {
   int q, e;
   if (jc < x.nshared) {
     q = x.first;
     e = jc * kChunk + i;
-    if (e >= x.ns) return kNoRow;
+    if (e >= x.ns) return RowRef{0, kNoRow};
   } else {
     int idx, h = 0;
     if (x.q1 < 0) {
@@ -239,19 +249,24 @@ __device__ __forceinline__ int64_t row_of(const PrefixKernel& k, const Pair& x, 
     const int own = h ? x.own1 : x.own0;
     if (idx >= own) {
       idx -= own;
-      if (idx >= k.n_swa) return kNoRow;
-      const int64_t w = (int64_t)q * k.n_swa + idx;
-      if (k.ex.win_pos && __ldg(k.ex.win_pos + w) < max(__ldg(k.ex.win_lo + q), (int64_t)0)) return kNoRow;
-      return kWindowRow + w;
+      if (idx >= k.n_swa) return RowRef{0, kNoRow};
+      const int w = q * k.n_swa + idx;
+      if (k.ex.win_pos && __ldg(k.ex.win_pos + w) < max(__ldg(k.ex.win_lo + q), (int64_t)0)) return RowRef{0, kNoRow};
+      return RowRef{0, kNoRow - 1 - w};
     }
     e = x.ns + idx;
   }
-  const int page = __ldg(k.table + q * k.max_pages + e / k.page_entries);
-  if (page < 0 || page >= k.n_pages) {
-    if (report) report_error(k.ws, CSA2_ERR_INDEX_RANGE, page);
+  const int pi = (int)((uint64_t)e * k.page_div >> 40);
+  return RowRef{__ldg(k.table + q * k.max_pages + pi), e - pi * k.page_entries};
+}
+// a page outside the planes is skipped, and reported by the warp that is told to
+__device__ __forceinline__ int resolve(const PrefixKernel& k, RowRef r, bool report) {
+  if (r.off < 0) return r.off;
+  if (r.page < 0 || r.page >= k.n_pages) {
+    if (report) report_error(k.ws, CSA2_ERR_INDEX_RANGE, r.page);
     return kNoRow;
   }
-  return (int64_t)page * k.page_entries + e % k.page_entries;
+  return r.page * k.page_entries + r.off;
 }
 
 // 32 channels of an entry (16 bytes of codes, two scales) -> four 8-channel vectors of f16
@@ -278,23 +293,22 @@ struct Fetch {
   uint32_t scales;
 };
 // Starts the loads of 32-channel block cb of row r (window rows are read when they are written).
-__device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int64_t r, int cb) {
-  if (r >= 0 && r < kWindowRow) {
-    f.codes = __ldg(reinterpret_cast<const uint4*>(k.kv_codes + r * 256) + cb);
-    f.scales = __ldg(reinterpret_cast<const uint16_t*>(k.kv_scales + r * 32) + cb);
+__device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int r, int cb) {
+  if (r >= 0) {
+    f.codes = __ldg(reinterpret_cast<const uint4*>(k.kv_codes + (int64_t)r * 256) + cb);
+    f.scales = __ldg(reinterpret_cast<const uint16_t*>(k.kv_scales + (int64_t)r * 32) + cb);
   }
 }
 // Writes 32-channel block cb of the row to dst: vector q of it at dst + q * stride (f16 elements).
-__device__ __forceinline__ void put(const Fetch& f, const PrefixKernel& k, int64_t r, int cb, uint16_t* dst,
-                                    int stride) {
+__device__ __forceinline__ void put(const Fetch& f, const PrefixKernel& k, int r, int cb, uint16_t* dst, int stride) {
   uint4 v[4];
-  if (r >= kWindowRow) {
-    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (r - kWindowRow) * kDMain) + 2 * cb;
+  if (r >= 0) {
+    widen_codes(f.codes, f.scales, v);
+  } else if (r < kNoRow) {
+    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (int64_t)(kNoRow - 1 - r) * kDMain) + 2 * cb;
     const uint4 a = __ldg(src), b = __ldg(src + 1);
     widen_e4m3(a, v[0], v[1]);
     widen_e4m3(b, v[2], v[3]);
-  } else if (r >= 0) {
-    widen_codes(f.codes, f.scales, v);
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -303,120 +317,21 @@ __device__ __forceinline__ void put(const Fetch& f, const PrefixKernel& k, int64
   for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + q * stride) = v[q];
 }
 
-// The query of an item into q' and c2, by the eight row warps (w 0-7): its bf16 rows come through the
-// S operand's buffer, which S of the item before has left (n chunks so far).  Returns false when a
-// wait gave up.
-template <bool kEx>
-__device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k, int q, int w, int lane, uint32_t n,
-                                            uint32_t item) {
-  volatile int* abort_flag = &S.abort_flag;
-  bool good = n == 0 || ptx::mbar_wait_warp_cluster(&S.xs_free[kPieces - 1], (n - 1) & 1u, abort_flag, kWaitBudget);
-  if (good && q >= 0) {
-    if (w == 0 && lane == 0) {
-      ptx::mbar_arrive_expect_tx(&S.q_load, kHAtt * kDMain * 2);
-      ptx::bulk_g2s(&S.xs[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_load);
-    }
-    __syncwarp();
-    volatile int keep_waiting = 0;  // the copy writes shared memory: no leaving before it has landed
-    good = ptx::mbar_wait_warp(&S.q_load, item & 1u, &keep_waiting, kWaitBudget);
-    if (good) stage_q<kEx>(S.q, S.c2[item & 1u], &S.xs[0][0], k.scale, w, lane, k.ex, q);
-  } else if (good) {  // no second query: zeros
-    if (w == 0 && lane == 0) ptx::mbar_arrive(&S.q_load);  // keeps its phase
-    for (int i = w * 32 + lane; i < kDMain / 8 * kQPlane / 8; i += 256)
-      reinterpret_cast<uint4*>(&S.q[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (w == 0) S.c2[item & 1u][lane] = S.c2[item & 1u][lane + 32] = 0.0f;
-  }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::mbar_arrive(&S.staged[item & 1u]);
-    ptx::mbar_arrive_cluster(&S.q_full, 0);
-  }
-  return good;
-}
-
-// Chunks [c0, c0 + nc) of pair x by the four row warps of one operand.  kS: this CTA's 64 rows of S's
-// operand, handed over by 128 channels (rows 32 u + rl, block 4 i + cb in piece i); otherwise its 256
-// channels of O's, by 32 rows (row 32 i + rl, blocks 4 u + cb of its eight in piece i).  A warp's eight
-// rows x four 16-byte blocks read 64 contiguous bytes of eight rows, and its stores write eight rows of
-// a plane: no bank conflicts.  The loads of a piece of the next chunk start once this chunk's is written.
-template <bool kEx, bool kS>
-__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, uint32_t rank, int qme,
-                                          int c0, int nc, int warp, int lane, uint32_t n, uint32_t item) {
-  volatile int* abort_flag = &S.abort_flag;
-  constexpr int kN = kS ? 2 : 4;  // rows of this thread in a chunk
-  const int w4 = warp & 3, rl = 8 * w4 + (lane & 7), cb = lane >> 3;
-  int64_t r[kN], rn[kN];
-  Fetch f[kPieces][2];
-  auto rows = [&](int64_t (&d)[kN], int jc) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      d[i] = row_of(k, x, jc, (kS ? kOwnChunk * (int)rank : 0) + 32 * i + rl, !kS && rank == 0 && cb == 0);
-  };
-  auto fetch_piece = [&](const int64_t (&d)[kN], int i) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (kS) fetch(f[i][u], k, d[u], 4 * i + cb);
-      else fetch(f[i][u], k, d[i % kN], 8 * (int)rank + 4 * u + cb);
-  };
-  auto masks = [&](const int64_t (&d)[kN], uint32_t m) {  // rows of chunk number m that exist
-    if (kS) return;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const uint32_t v = __ballot_sync(0xffffffffu, d[i] >= 0) & 0xFFu;
-      if (lane == 0) reinterpret_cast<uint8_t*>(&S.vmask[m & 1][i])[w4] = (uint8_t)v;
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.m_full[m & 1]);
-  };
-  rows(r, c0);
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) fetch_piece(r, i);
-  bool good = stage_query<kEx>(S, k, qme, warp - kSWarp, lane, n, item);
-  // every row warp has read the query's bf16 rows: the S operand's buffer may be written
-  if (kS && good) good = ptx::mbar_wait_warp(&S.staged[item & 1u], (item >> 1) & 1u, abort_flag, kWaitBudget);
-  if (good) masks(r, n);
-  for (int j = 0; j < nc && good; ++j) {
-    const uint32_t m = n + (uint32_t)j;
-    const bool more = j + 1 < nc;
-    if (more) rows(rn, c0 + j + 1);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if (m > 0)
-        good = good && ptx::mbar_wait_warp_cluster(kS ? &S.xs_free[i] : &S.xo_free[i], (m - 1) & 1u, abort_flag,
-                                                   kWaitBudget);
-      if (good) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (kS) put(f[i][u], k, r[u], 4 * i + cb, &S.xs[4 * (4 * i + cb)][(32 * u + rl) * 8], kOwnChunk * 8);
-          else
-            put(f[i][u], k, r[i % kN], 8 * (int)rank + 4 * u + cb, &S.xo[4 * (4 * u + cb)][(32 * i + rl) * 8],
-                kChunk * 8);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(kS ? &S.xs_full[i] : &S.xo_full[i], 0);
-        if (more) fetch_piece(rn, i);
-      }
-    }
-    if (good && more) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) r[i] = rn[i];
-      masks(r, m + 1);
-    }
-  }
-  return good;
-}
-
 // p = 2^(s c2 - m) of 32 rows, packed in pairs as f16 from the fp32 values whose sum goes to `sum`;
 // returns the largest exponent.  Rows that the mask has not are -inf.
-__device__ __forceinline__ float probs32(const uint32_t (&s)[32], uint32_t mask, float c2, float m, uint32_t* ph,
+__device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float c2, float m, uint32_t (&ph)[16],
                                          float& sum) {
+#pragma unroll
+  for (int u = 0; u < 32; ++u) s[u] = __float_as_uint(fmaf(__uint_as_float(s[u]), c2, -m));
+  if (mask != ~0u) {
+#pragma unroll
+    for (int u = 0; u < 32; ++u)
+      if (!((mask >> u) & 1u)) s[u] = __float_as_uint(-INFINITY);
+  }
   float top = -INFINITY, s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
-    float e0 = fmaf(__uint_as_float(s[2 * u]), c2, -m), e1 = fmaf(__uint_as_float(s[2 * u + 1]), c2, -m);
-    if (!((mask >> (2 * u)) & 1u)) e0 = -INFINITY;
-    if (!((mask >> (2 * u + 1)) & 1u)) e1 = -INFINITY;
+    const float e0 = __uint_as_float(s[2 * u]), e1 = __uint_as_float(s[2 * u + 1]);
     top = fmaxf(top, fmaxf(e0, e1));
     const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
     s0 += p0;
@@ -428,34 +343,139 @@ __device__ __forceinline__ float probs32(const uint32_t (&s)[32], uint32_t mask,
   return top;
 }
 
+// The query of an item into q' and c2, by S's eight row warps (w 0-7): its bf16 rows come through the
+// S operand's buffer, which S of the item before has left (n chunks so far).  Returns false when a
+// wait gave up.
+template <bool kEx>
+__device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k, int q, int w, int lane, uint32_t n,
+                                            uint32_t item) {
+  volatile int* abort_flag = &S.abort_flag;
+  bool good = n == 0 || ptx::mbar_wait_warp(&S.x_free[0][kPieces - 1], (n - 1) & 1u, abort_flag, kWaitBudget);
+  if (good && q >= 0) {
+    if (w == 0 && lane == 0) {
+      ptx::mbar_arrive_expect_tx(&S.q_load, kHAtt * kDMain * 2);
+      ptx::bulk_g2s(&S.xs[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_load);
+    }
+    __syncwarp();
+    volatile int keep_waiting = 0;  // the copy writes shared memory: no leaving before it has landed
+    good = ptx::mbar_wait_warp(&S.q_load, item & 1u, &keep_waiting, kWaitBudget);
+    if (good) stage_q<kEx>(S.q, S.c2[item & 3u], &S.xs[0][0], k.scale, w, lane, k.ex, q);
+  } else if (good) {  // no second query: zeros
+    if (w == 0 && lane == 0) ptx::mbar_arrive(&S.q_load);  // keeps its phase
+    for (int i = w * 32 + lane; i < kDMain / 8 * kQPlane / 8; i += 256)
+      reinterpret_cast<uint4*>(&S.q[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (w == 0) S.c2[item & 3u][lane] = S.c2[item & 3u][lane + 32] = 1.0f;
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::mbar_arrive(&S.staged[item & 3u]);
+    ptx::mbar_arrive(&S.q_full);
+  }
+  // every row warp has read the query's bf16 rows: the buffer may be written
+  return good && ptx::mbar_wait_warp(&S.staged[item & 3u], (item >> 2) & 1u, abort_flag, kWaitBudget);
+}
+
+// Chunks [c0, c0 + nc) of pair x by the 16 row warps.  Operand 0 (S's, warps 0-7): this CTA's 64 rows,
+// handed over by 128 channels: row 8 w + l % 8, block (of 32 channels) 4 i + l / 8 in piece i.  Operand 1
+// (O's): its 256 channels of all rows, by 32 rows: row 32 i + 8 (w % 4) + l % 8, block 4 (w / 4 % 2) + l / 8
+// of its eight in piece i.  Either way a load reads 64 contiguous bytes of eight rows, and a store writes
+// eight rows of a plane: no bank conflicts.  A step writes one piece; a row's codes are fetched two
+// steps ahead, its page four.  Both operands run the same code: the kernel's loops have to fit the
+// instruction cache (unrolled by piece and operand they waited more for instructions than for data).
+template <bool kEx>
+__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, int rank, int c0,
+                                          int nc, int w, int lane, uint32_t n, uint32_t item) {
+  const int op = w >> 3, cb = lane >> 3;
+  const int rl = 8 * (op ? w & 3 : w) + (lane & 7);
+  const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0;
+  const int blk0 = op ? 8 * rank + 4 * ((w >> 2) & 1) + cb : cb, blk_step = op ? 0 : 4;
+  const int plane = (op ? kChunk : kOwnChunk) * 8;  // f16 elements
+  uint16_t* const dst = (op ? &S.xo[4 * (4 * ((w >> 2) & 1) + cb)][0] : &S.xs[4 * cb][0]) + rl * 8;
+  const int dst_step = op ? 32 * 8 : 16 * kOwnChunk * 8;
+  const int steps = nc * kPieces;
+  int ra, rb;
+  Fetch fa, fb;
+  RowRef na = find_row(k, x, c0, row0), nb = find_row(k, x, c0, row0 + row_step);
+  auto load = [&](Fetch& f, int& r, RowRef& nx, int st) {  // fetch step st, find step st + 2
+    r = resolve(k, nx, false);
+    fetch(f, k, r, blk0 + blk_step * (st & 3));
+    st += 2;
+    if (st < steps) nx = find_row(k, x, c0 + (st >> 2), row0 + row_step * (st & 3));
+  };
+  load(fa, ra, na, 0);
+  load(fb, rb, nb, 1);
+  bool good = op || stage_query<kEx>(S, k, rank ? x.q1 : x.q0, w, lane, n, item);
+  auto step = [&](Fetch& f, int& r, RowRef& nx, int st) {
+    const uint32_t m = n + (uint32_t)(st >> 2);
+    const int i = st & 3;
+    if (m > 0) good = good && ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) return;
+    put(f, k, r, blk0 + blk_step * i, dst + i * dst_step, plane);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
+    if (st + 2 < steps) load(f, r, nx, st + 2);
+  };
+#pragma unroll 1
+  for (int st = 0; st < steps && good; st += 2) {
+    step(fa, ra, na, st);
+    step(fb, rb, nb, st + 1);
+  }
+  return good;
+}
+
+// Which rows of each chunk exist, by one warp (lane l rows l, 32 + l, ..), into the S buffers' masks: a
+// buffer's mask may be written once the softmax of its last chunk has handed P over.  Pages outside the
+// planes are reported here.
+__device__ __forceinline__ bool mask_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, bool report, int c0,
+                                          int nc, int lane, uint32_t n) {
+  bool good = true;
+#pragma unroll 1
+  for (int j = 0; j < nc && good; ++j) {
+    const uint32_t m = n + (uint32_t)j;
+    RowRef r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = find_row(k, x, c0 + j, 32 * i + lane);
+    if (m >= 2) good = ptx::mbar_wait_warp(&S.p_full[m & 1], ((m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __ballot_sync(0xffffffffu, resolve(k, r[i], report) != kNoRow);
+      if (good && lane == i) S.vmask[m & 1][i] = v;
+    }
+    __syncwarp();
+    if (good && lane == 0) ptx::mbar_arrive(&S.m_full[m & 1]);
+  }
+  return good;
+}
+
 template <bool kEx>
 __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrefixSmem& S = *reinterpret_cast<PrefixSmem*>(smem_raw);
   volatile int* abort_flag = &S.abort_flag;
-  const uint32_t rank = ptx::cluster_ctarank();
+  const int rank = (int)ptx::cluster_ctarank();
   const int cluster = blockIdx.x / 2;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
-  if (warp == kMmaWarp) {
+  if (warp == kSMma) {
     if (lane == 0) {
+      const uint32_t peer = rank == 0 ? 1 : 0;
       ptx::mbar_init(&S.q_load, 1);
-      ptx::mbar_init(&S.drained, 1);
-      ptx::mbar_init(&S.q_full, 16);  // barriers that the MMA warp waits on count both CTAs' warps
-      for (int i = 0; i < kPieces; ++i) {
-        ptx::mbar_init(&S.xs_full[i], 8);
-        ptx::mbar_init(&S.xo_full[i], 8);
-        ptx::mbar_init(&S.xs_free[i], 1);
-        ptx::mbar_init(&S.xo_free[i], 1);
+      ptx::mbar_init(&S.q_full, 8 + peer);
+      for (int i = 0; i < 2 * kPieces; ++i) {
+        ptx::mbar_init(&S.x_full[0][0] + i, 8 + peer);
+        ptx::mbar_init(&S.x_free[0][0] + i, 1);
       }
+      for (int i = 0; i < 4; ++i) ptx::mbar_init(&S.staged[i], 8);
       for (int i = 0; i < 2; ++i) {
-        ptx::mbar_init(&S.staged[i], 8);
         ptx::mbar_init(&S.s_full[i], 1);
-        ptx::mbar_init(&S.p_full[i], 8);
+        ptx::mbar_init(&S.p_full[i], 4 + peer);
         ptx::mbar_init(&S.p_free[i], 1);
-        ptx::mbar_init(&S.m_full[i], 4);
+        ptx::mbar_init(&S.m_full[i], 1);
       }
-      ptx::mbar_init(&S.o_read, 8);
+      ptx::mbar_init(&S.o_read, 4 + peer);
+      ptx::mbar_init(&S.drained, 2);
       S.abort_flag = 0;
       ptx::fence_mbar_init();
     }
@@ -469,177 +489,218 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  const int total = __ldg(k.totals + 1);
-  const int t0 = (int)((long long)total * cluster / kClusters), t1 = (int)((long long)total * (cluster + 1) / kClusters);
-  auto wait = [&](uint64_t* bar, uint32_t n) {
+  const int total = __ldg(k.totals + 1), clusters = min(kClusters, total);
+  const bool idle = cluster >= clusters;
+  const int t0 = idle ? 0 : (int)((long long)total * cluster / clusters);
+  const int t1 = idle ? 0 : (int)((long long)total * (cluster + 1) / clusters);
+  auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
+  // an arrival from the other CTA is among those waited for
+  auto ready = [&](uint64_t* bar, uint32_t n) {
     return ptx::mbar_wait_warp_cluster(bar, n & 1u, abort_flag, kWaitBudget);
   };
   bool good = true;
   int where = 0;
+  // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1;
+  // n counts the chunks before them, items the items.
+  auto for_items = [&](auto body) {
+    int p = t0 < t1 ? __ldg(k.cpair + cluster) : 0;
+    uint32_t n = 0, items = 0;
+    for (int t = t0; t < t1 && good; ++p) {
+      const int pend = k.pairs[p + 1].chunk0;
+      __syncwarp();
+      if (lane < (int)(sizeof(Pair) / 4))
+        reinterpret_cast<int32_t*>(&S.pair[warp])[lane] = reinterpret_cast<const int32_t*>(k.pairs + p)[lane];
+      __syncwarp();
+      const Pair& x = S.pair[warp];
+      const int c0 = t - x.chunk0, nc = min(pend, t1) - t;
+      if (nc <= 0) continue;  // a pair without chunks
+      t += nc;
+      body(x, p, c0, nc, n, items);
+      n += (uint32_t)nc;
+      ++items;
+    }
+  };
 
-  // Every role runs the same list of items: pair p, its chunks [c0, c1).  n counts chunks.
-  int p = t0 < t1 ? __ldg(k.cpair + cluster) : 0;
-  uint32_t n = 0, items = 0;
-  for (int t = t0; t < t1 && good; ++p) {
-    const Pair x = k.pairs[p];
-    const int pend = k.pairs[p + 1].chunk0;
-    if (pend <= t) continue;  // a pair without chunks
-    const int c0 = t - x.chunk0, c1 = min(pend, t1) - x.chunk0, nc = c1 - c0;
-    t += nc;
-    const int qme = rank ? x.q1 : x.q0;
-
-    if (warp >= kSWarp && warp < kMmaWarp) {
-      // ---- the rows of S's operand (warps 4-7) and of O's (8-11)
-      good = warp < kOWarp ? rows_role<kEx, true>(S, k, x, rank, qme, c0, nc, warp, lane, n, items)
-                           : rows_role<kEx, false>(S, k, x, rank, qme, c0, nc, warp, lane, n, items);
-      where = warp < kOWarp ? 31 : 32;
-    } else if (warp == kMmaWarp) {
-      // ---- MMA issue (even CTA): S(0), then S(j + 1) before O(j)
-      if (rank == 0) {
-        constexpr uint32_t idesc_s = ptx::idesc_f16(128, kChunk, 0);
-        constexpr uint32_t idesc_o = ptx::idesc_f16(128, 256, 0) | ptx::kIdescBMajorMN;
-        const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
-        const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
-        const uint64_t dp = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
-        const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0], 128, kChunk * 16);
-        good = wait(&S.q_full, items);
-        for (int j = 0; j <= nc && good; ++j) {
+  if (warp >= kRowWarp && warp < kSMma) {
+    ptx::setmaxnreg_dec<kRowRegs>();
+    for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
+      good = rows_role<kEx>(S, k, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
+    });
+    where = 31;
+  } else if (warp >= kSMma) {
+    ptx::setmaxnreg_dec<kMmaRegs>();
+    // the odd CTA's MMA warps pass their CTA's arrivals on, in the order the even CTA's wait for them
+    auto pass = [&](uint64_t* bar, uint32_t ph) {
+      if (good) good = wait(bar, ph);
+      if (good && lane == 0) ptx::mbar_arrive_cluster(bar, 0);
+    };
+    if (warp == kMaskWarp) {
+      for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
+        good = mask_role(S, k, x, rank == 0, c0, nc, lane, n);
+      });
+      where = 32;
+    } else if (warp == kSMma) {
+      // ---- S = q' X^T: 32 K steps of 16 channels, four pieces of eight
+      constexpr uint32_t idesc_s = ptx::idesc_f16(128, kChunk, 0);
+      const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
+      const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
+      for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
+        if (rank) pass(&S.q_full, items);
+        else good = ready(&S.q_full, items);
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j;
-          if (j < nc) {
-            const uint32_t dst = tmem + kColS + 64u * (m & 1u);
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              if (good) good = wait(&S.xs_full[i], m);
-              if (!good) break;
-              ptx::tc_fence_after();
-#pragma unroll
-              for (int ks = 8 * i; ks < 8 * i + 8; ++ks)  // q'[2 ks], xs[2 ks]: 2048 bytes on
-                ptx::mma_f16_ss_pair_elect(dst, da + (uint64_t)(ks * 128), db + (uint64_t)(ks * 128), idesc_s,
-                                           ks > 0 ? 1u : 0u);
-              ptx::mma_commit_pair_elect(&S.xs_free[i]);
+          // the softmax of both CTAs has left this S buffer
+          if (rank == 0 && m >= 2) good = ready(&S.p_full[m & 1], (m >> 1) - 1);
+          const uint32_t dst = tmem + kColS + 64u * (m & 1u);
+#pragma unroll 1
+          for (int i = 0; i < kPieces && good; ++i) {
+            if (rank) {
+              pass(&S.x_full[0][i], m);
+              continue;
             }
-            if (good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
+            good = ready(&S.x_full[0][i], m);
+            if (!good) break;
+            ptx::tc_fence_after();
+            const uint64_t at = (uint64_t)(i * 1024);  // q'[16 i], xs[16 i]: 16 KB on; a K step 2 KB
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              ptx::mma_f16_ss_pair_elect(dst, da + at + (uint64_t)(ks * 128), db + at + (uint64_t)(ks * 128), idesc_s,
+                                         (i | ks) > 0 ? 1u : 0u);
+            ptx::mma_commit_pair_elect(&S.x_free[0][i]);
           }
-          if (j > 0 && good) {
-            const uint32_t o = m - 1;
-            good = wait(&S.p_full[o & 1], o >> 1);
-            if (good && j == 1 && items > 0) good = wait(&S.o_read, items - 1);
-            const uint64_t dpo = dp + (uint64_t)((o & 1u) * (kChunk / 8 * kHAtt * 16 / 16));
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              if (good) good = wait(&S.xo_full[i], o);
-              if (!good) break;
-              ptx::tc_fence_after();
-#pragma unroll
-              for (int ks = 2 * i; ks < 2 * i + 2; ++ks)  // p[2 ks]: 2048 bytes on; xo rows 16 ks: 256 bytes on
-#pragma unroll
-                for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[16 h], 32 KB on
-                  ptx::mma_f16_ss_pair_elect(tmem + 128u * (uint32_t)h, dpo + (uint64_t)(ks * 128),
-                                             dx + (uint64_t)(h * 2048 + ks * 16), idesc_o,
-                                             (j > 1 || ks > 0) ? 1u : 0u);
-              ptx::mma_commit_pair_elect(&S.xo_free[i]);
-            }
-            if (good) ptx::mma_commit_pair_elect(&S.p_free[o & 1]);
-          }
+          if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
         }
-      }
+      });
       where = 33;
-    } else {
-      // ---- softmax: thread t head t % 64, chunk rows 64 (t / 64) ..
-      const int h = tid & 63, half = tid >> 6;
-      const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-      const int vis = rank ? x.vis1 : x.vis0;
-      float m2 = -INFINITY, lsum = 0.0f, c2 = 0.0f;
+    } else if (warp == kOMma) {
+      // ---- O += P X: eight K steps of 16 rows, four pieces of two; two accumulators of 128 channels a CTA
+      constexpr uint32_t idesc_o = ptx::idesc_f16(128, 256, 0) | ptx::kIdescBMajorMN;
+      const uint64_t dp = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
+      const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0], 128, kChunk * 16);
+      for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j;
+          if (rank) {
+            pass(&S.p_full[m & 1], m >> 1);
+            if (j == 0 && items > 0) pass(&S.o_read, items - 1);
+          } else {
+            good = ready(&S.p_full[m & 1], m >> 1);
+            if (good && j == 0 && items > 0) good = ready(&S.o_read, items - 1);
+          }
+          const uint64_t dpo = dp + (uint64_t)((m & 1u) * (kChunk / 8 * kHAtt * 16 / 16));
+#pragma unroll 1
+          for (int i = 0; i < kPieces && good; ++i) {
+            if (rank) {
+              pass(&S.x_full[1][i], m);
+              continue;
+            }
+            good = ready(&S.x_full[1][i], m);
+            if (!good) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)  // p[4 i + 2 ks]: 2 KB a step; xo rows 32 i + 16 ks: 256 bytes a step
+#pragma unroll
+              for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[16 h], 32 KB on
+                ptx::mma_f16_ss_pair_elect(tmem + 128u * (uint32_t)h, dpo + (uint64_t)((2 * i + ks) * 128),
+                                           dx + (uint64_t)(h * 2048 + (2 * i + ks) * 16), idesc_o,
+                                           (j | i | ks) > 0 ? 1u : 0u);
+            ptx::mma_commit_pair_elect(&S.x_free[1][i]);
+          }
+          if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.p_free[m & 1]);
+        }
+      });
+      where = 34;
+    }
+  } else {
+    // ---- softmax: thread t head t % 64, chunk rows 64 (t / 64) ..
+    ptx::setmaxnreg_inc<kSoftRegs>();
+    const int h = tid & 63, half = tid >> 6;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t items) {
+      const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
+      float m2 = -INFINITY, lsum = 0.0f;
+      good = wait(&S.staged[items & 3u], items >> 2);
+      const float c2 = S.c2[items & 3u][h];
+#pragma unroll 1
       for (int j = 0; j < nc; ++j) {
         const uint32_t m = n + (uint32_t)j, slot = m & 1u;
-        good = good && wait(&S.s_full[slot], m >> 1) && wait(&S.m_full[slot], m >> 1);
-        if (good && j == 0) good = wait(&S.staged[items & 1u], items >> 1);  // c2
+        good = good && wait(&S.m_full[slot], m >> 1) && wait(&S.s_full[slot], m >> 1);
         if (good && m >= 2) good = wait(&S.p_free[slot], (m >> 1) - 1);
-        const uint32_t ta = tmem + lane_base + kColS + 64u * slot;
-        uint32_t mk[2] = {0u, 0u};
-        uint32_t pp[32];
-        float sum = 0.0f;
-        bool over = false;
-        auto probs = [&](float ref) {
+        ptx::tc_fence_after();
+        uint32_t mk0 = 0u, mk1 = 0u;
+        if (c0 + j < x.nshared) {  // entries below this query's own count
+          const int left = vis - (c0 + j) * kChunk - 64 * half;
+          mk0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+          mk1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1u : 0u;
+        } else if (x.q1 < 0 ? rank == 0 : half == rank) {
+          mk0 = mk1 = ~0u;
+        }
+        mk0 &= S.vmask[slot][2 * half];
+        mk1 &= S.vmask[slot][2 * half + 1];
+        // P with the reference so far (0 before the first row); it stands unless some head's logits
+        // exceed it by too much, then once more with that head's new reference
+        float alpha = 1.0f, sum, ref = m2 == -INFINITY ? 0.0f : m2;
+        uint32_t nv;
+#pragma unroll 1
+        for (int round = 0;; ++round) {
           float top = -INFINITY;
           sum = 0.0f;
+          if (good) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a[32], ph[16];
+              float s1;
+              ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + 64u * slot + 32u * (uint32_t)i, a);
+              ptx::tmem_wait_ld();
+              top = fmaxf(top, probs32(a, i ? mk1 : mk0, c2, ref, ph, s1));
+              sum += s1;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t a[32];
-            float s1;
-            ptx::tmem_ld_32x32b_x32(ta + 32u * (uint32_t)i, a);
-            ptx::tmem_wait_ld();
-            top = fmaxf(top, probs32(a, mk[i], c2, ref, pp + 16 * i, s1));
-            sum += s1;
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(&S.p[slot][8 * half + 4 * i + u][h * 8]) =
+                    make_uint4(ph[4 * u], ph[4 * u + 1], ph[4 * u + 2], ph[4 * u + 3]);
+            }
+            ptx::fence_proxy_async_smem();
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(&S.p[slot][8 * half + i][h * 8]) =
-                make_uint4(pp[4 * i], pp[4 * i + 1], pp[4 * i + 2], pp[4 * i + 3]);
-          ptx::fence_proxy_async_smem();
-          return top;
-        };
-        if (good) {
-          ptx::tc_fence_after();
-          if (j == 0) c2 = S.c2[items & 1u][h];
-          const int jc = c0 + j;
-          if (jc < x.nshared) {  // entries below this query's own count
-            const int left = vis - jc * kChunk - 64 * half;
-            mk[0] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
-            mk[1] = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1u : 0u;
-          } else if (x.q1 < 0 ? rank == 0 : half == (int)rank) {
-            mk[0] = mk[1] = ~0u;
+          if (round) break;
+          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kTau2;
+          nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
+          if (nv == 0 || nv >= 8) break;
+          S.red[half][h] = top;
+          softmax_sync();
+          const float cm = fmaxf(S.red[0][h], S.red[1][h]) + ref;  // over both threads' rows
+          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kTau2) {
+            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
+            m2 = cm;
           }
-          mk[0] &= S.vmask[slot][2 * half];
-          mk[1] &= S.vmask[slot][2 * half + 1];
-          over = probs(m2 == -INFINITY ? kNoRef : m2) > kTau2;
+          ref = m2 == -INFINITY ? 0.0f : m2;
         }
-        const uint32_t nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
         if (nv >= 8) {
           good = false;
           break;
         }
-        float alpha = 1.0f;
-        if (nv != 0) {
-          // the chunk's maximum of this head over both threads' rows
-          float cm = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t a[32];
-            ptx::tmem_ld_32x32b_x32(ta + 32u * (uint32_t)i, a);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) cm = fmaxf(cm, ((mk[i] >> u) & 1u) ? __uint_as_float(a[u]) : -INFINITY);
-          }
-          S.red[half][h] = cm;
-          softmax_sync();
-          cm = fmaxf(S.red[0][h], S.red[1][h]) * c2;
-          if (cm > m2 + kTau2) {
-            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
-            m2 = cm;
-          }
-          (void)probs(m2 == -INFINITY ? kNoRef : m2);
-          if (j > 0) {  // O holds earlier chunks: scale the rows of the heads that moved
-            good = wait(&S.p_free[slot ^ 1u], (m - 1) >> 1);
-            if (good && __any_sync(0xffffffffu, alpha != 1.0f)) {
-              ptx::tc_fence_after();
+        if (nv != 0 && j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+          // O holds earlier chunks: scale the rows of the heads that moved
+          good = wait(&S.p_free[slot ^ 1u], (m - 1) >> 1);
+          if (good) {
+            ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 256; c += 32) {
-                uint32_t a[32];
-                ptx::tmem_ld_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
-                ptx::tmem_wait_ld();
+            for (int c = 0; c < 256; c += 32) {
+              uint32_t a[32];
+              ptx::tmem_ld_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
+              ptx::tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 32; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) * alpha);
-                ptx::tmem_st_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
-              }
-              ptx::tmem_wait_st();
+              for (int u = 0; u < 32; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) * alpha);
+              ptx::tmem_st_32x32b_x32(tmem + lane_base + (uint32_t)c, a);
             }
+            ptx::tmem_wait_st();
           }
         }
         if (good) {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(&S.p_full[slot], 0);
+          if (lane == 0) ptx::mbar_arrive(&S.p_full[slot]);
         }
         lsum = fmaf(alpha, lsum, sum);
       }
@@ -648,40 +709,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       good = good && wait(&S.p_free[last & 1u], last >> 1);
       // the four warps leave together, or none
       good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
-      if (good) {
-        ptx::tc_fence_after();
-        const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
-        if (qme >= 0) {
-          float4* po = k.part_o + slot * 64 * 128 + tid;
+      if (!good) return;
+      ptx::tc_fence_after();
+      const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
+      if (qme >= 0) {
+        float4* po = k.part_o + slot * 64 * 128 + tid;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t a[32];
-            ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
-            ptx::tmem_wait_ld();
+        for (int c = 0; c < 8; ++c) {
+          uint32_t a[32];
+          ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              po[(c * 8 + u) * 128] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]),
-                                                  __uint_as_float(a[4 * u + 2]), __uint_as_float(a[4 * u + 3]));
-          }
+          for (int u = 0; u < 8; ++u)
+            po[(c * 8 + u) * 128] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]),
+                                                __uint_as_float(a[4 * u + 2]), __uint_as_float(a[4 * u + 3]));
         }
-        S.red[half][h] = lsum;
-        softmax_sync();
-        if (half == 0 && qme >= 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, S.red[0][h] + S.red[1][h]);
-        softmax_sync();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(&S.o_read, 0);
       }
-      where = 34;
-    }
-    n += (uint32_t)nc;
-    ++items;
+      S.red[half][h] = lsum;
+      softmax_sync();
+      if (half == 0 && qme >= 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, S.red[0][h] + S.red[1][h]);
+      softmax_sync();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+    });
+    where = 35;
   }
   if (!good && lane == 0 && !*abort_flag) {
     *abort_flag = 1;
     report_error(k.ws, CSA2_ERR_DEVICE_TIMEOUT, where);
   }
-  if (warp == kMmaWarp && rank == 0) {  // every MMA has completed before tensor memory is freed
+  if (rank == 0 && (warp == kSMma || warp == kOMma)) {  // every MMA has completed before tensor memory is freed
     ptx::mma_commit_pair_elect(&S.drained);
     volatile int keep_waiting = 0;
     ptx::mbar_wait_warp(&S.drained, 0, &keep_waiting, kWaitBudget);
@@ -689,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();  // no CTA leaves while the other may still arrive on its barriers
-  if (warp == kMmaWarp) {
+  if (warp == kSMma) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, kCols);
   }
@@ -708,15 +766,12 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
   const long long total = totals[1];
   const int s0 = pairs[p].chunk0, s1 = pairs[p + 1].chunk0;
   // clusters that ran chunks s0 .. s1 - 1: chunk t belongs to cluster ceil((t + 1) clusters / total) - 1
-  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * kClusters + total - 1) / total) - 1 : 0;
-  const int k1 = s1 > s0 ? (int)((s1 * (long long)kClusters + total - 1) / total) : 0;
+  const int clusters = (int)min((long long)kClusters, total);
+  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * clusters + total - 1) / total) - 1 : 0;
+  const int k1 = s1 > s0 ? (int)((s1 * (long long)clusters + total - 1) / total) : 0;
   const float z2 = ex.sink ? ex.sink[h] * kLog2e : -INFINITY;
   float ref = z2;
-  auto ran = [&](int c) {  // with fewer chunks than clusters, some have none
-    return max((long long)s0, total * c / kClusters) < min((long long)s1, total * (c + 1) / kClusters);
-  };
   for (int c = k0; c < k1; ++c) {
-    if (!ran(c)) continue;
     const float2 ml = part_ml[((int64_t)(p + c) * 2 + r) * kHAtt + h];
     if (ml.y > 0.0f) ref = fmaxf(ref, ml.x);
   }
@@ -725,7 +780,6 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
 #pragma unroll
   for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = k0; c < k1; ++c) {
-    if (!ran(c)) continue;
     const int64_t slot = (int64_t)(p + c) * 2 + r;
     const float2 ml = part_ml[slot * kHAtt + h];
     if (!(ml.y > 0.0f)) continue;
@@ -872,7 +926,8 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
     return launch_status();
   {
     const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, (const uint16_t*)q_bf16, pages->table,
-                         pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, softmax_scale, ex,
+                         pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa,
+                         ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, softmax_scale, ex,
                          L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
     KernelTimer timer("k_prefix_attn", st);
     launch_pairs(kern, kClusters, smem, st, k);

@@ -331,6 +331,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
                : "memory");
 }
 
+// Registers of this warpgroup's threads from here on; every warp of it calls it.  The increase waits for
+// what other warpgroups of the CTA have given back, so the shares must not exceed the launch's total.
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ------------------------------------------------------- CTA pairs (clusters)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

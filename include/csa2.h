@@ -467,7 +467,7 @@ size_t csa2_page_tables_workspace_size(int32_t B);
 typedef struct {
   const int32_t* table; /* [B][max_pages] page ids (device) */
   int32_t max_pages;    /* row length */
-  int32_t n_pages;      /* pages of the planes: valid ids are [0, n_pages) */
+  int32_t n_pages;      /* pages of the planes: valid ids are [0, n_pages); n_pages * seq_stride < 2^31 */
 } csa2_pages;
 
 /* Type of an attention call's output. */
