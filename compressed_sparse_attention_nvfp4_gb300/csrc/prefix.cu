@@ -19,6 +19,7 @@
 // All pairs' chunks form one list that kClusters CTA pairs share evenly, whatever the groups' sizes; a
 // pair cut between them leaves (m, l, O) partials that k_prefix_merge joins by log-sum-exp.
 #include "attn.cuh"
+#include "index_scan.cuh"
 
 namespace csa2 {
 namespace {
@@ -27,6 +28,8 @@ constexpr int kPlanThreads = 1024;
 constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of the 152 SMs
 constexpr int kChunk = 128;      // rows of a chunk
 constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
+constexpr int kImageQueries = 3;   // a group of at least this many queries has its shared entries widened once
+constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
 
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
 // up to vis by each, then each query's own entries ns .. ns + own - 1 and its window.
@@ -38,6 +41,8 @@ struct Pair {
   int32_t own0, own1;
   int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
   int32_t nshared; // shared chunks; own chunks follow
+  int32_t image;   // the shared entries' first chunk in the image, or -1
+  int32_t pad;
 };
 
 struct PrefixArgs {
@@ -51,7 +56,9 @@ struct PrefixArgs {
   int32_t* gpair;     // [G + 3] first pair of each range of queries
   int32_t* qpair;     // [B] pair * 2 + place
   int32_t* cpair;     // [kClusters] pair of each cluster's first chunk
-  int32_t* totals;    // pairs, chunks
+  int32_t* totals;    // pairs, chunks, image chunks
+  int32_t* gimage;    // [G + 1] first image chunk of each group (those at or beyond the total have none)
+  int64_t image_cap;  // chunks the image has room for
   void* ws;
 };
 
@@ -82,9 +89,9 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
 // first group, the G groups, those behind the last (a range outside the groups shares nothing).
 __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
   __shared__ int s_warp[kPlanThreads / 32];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_images;
   const int tid = threadIdx.x;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = s_images = 0;
   ptx::griddep_wait();
   __syncthreads();
   for (int g = tid; g < a.G; g += kPlanThreads) {
@@ -110,6 +117,23 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
   }
   if (tid == 0) a.gpair[R] = base;
   const int np = base;
+  auto count = [&](int q) { return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap); };
+  // a group's shared entries; those beyond its first query's own count are read as each query's own
+  auto shared_of = [&](int g, int first) { return min(min(max(a.n_shared[g], 0), a.shared_max), count(first)); };
+  int images = 0;
+  for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    int n = 0;
+    if (g < G && a.group_start[g + 1] - a.group_start[g] >= kImageQueries)
+      n = (shared_of(g, a.group_start[g]) + kChunk - 1) / kChunk;
+    int total;
+    const int at = images + block_scan(n, s_warp, &total);
+    // a group that ends beyond the image's room has none, and so do all behind it
+    if (g < G) a.gimage[g] = n > 0 && at + n <= a.image_cap ? at : -1;
+    if (n > 0 && at + n <= a.image_cap) atomicMax(&s_images, at + n);
+    images += total;
+    __syncthreads();
+  }
   __syncthreads();
   int chunks = 0;
   for (int p0 = 0; p0 < np; p0 += kPlanThreads) {
@@ -124,12 +148,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
         else hi = mid;
       }
       const int first = range_lo(lo), end = range_hi(lo);
-      auto count = [&](int q) { return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap); };
       x.q0 = first + 2 * (p - a.gpair[lo]);
       x.q1 = x.q0 + 1 < end ? x.q0 + 1 : -1;
       x.first = first;
-      // shared entries beyond the first query's own count are read as each query's own
-      if (lo >= 1 && lo <= G) x.ns = min(min(max(a.n_shared[lo - 1], 0), a.shared_max), count(first));
+      x.image = -1;
+      if (lo >= 1 && lo <= G) {
+        x.ns = shared_of(lo - 1, first);
+        x.image = a.gimage[lo - 1];
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int q = i ? x.q1 : x.q0;
@@ -157,6 +183,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
     a.pairs[np].chunk0 = chunks;
     a.totals[0] = np;
     a.totals[1] = chunks;
+    a.totals[2] = s_images;
+    a.gimage[G] = -1;
   }
   __syncthreads();
   const int clusters = min(kClusters, chunks);
@@ -178,9 +206,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
 // warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), row masks
 constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kMaskWarp = 22;
 constexpr int kThreads = 24 * 32;  // and one that fills the last warpgroup
-// registers of a thread: 80 at launch, then by warpgroup (softmax, four of rows, the last)
-constexpr int kSoftRegs = 128, kRowRegs = 72, kMmaRegs = 64;
-static_assert(kSoftRegs + 4 * kRowRegs + kMmaRegs <= 6 * 80, "registers of the launch");
+// registers of a thread: 80 at launch, which the row warpgroups keep; the softmax takes what the last
+// warpgroup gives back
+constexpr int kSoftRegs = 96, kMmaRegs = 64;
+static_assert(kSoftRegs + 4 * 80 + kMmaRegs <= 6 * 80, "registers of the launch");
 constexpr int kPieces = 4;
 constexpr uint32_t kCols = 512;   // tensor memory: O 2 x 128 columns, S 2 x 64
 constexpr uint32_t kColS = 256;
@@ -189,7 +218,7 @@ constexpr long long kWaitBudget = 1LL << 32;
 struct __align__(1024) PrefixSmem {
   uint16_t q[kDMain / 8][kQPlane];          // q' [c/8][head][c%8]
   uint16_t xs[kDMain / 8][kOwnChunk * 8];   // this CTA's 64 rows for S [c/8][row][c%8]
-  uint16_t xo[kDMain / 16][kChunk * 8];     // this CTA's 256 channels of all 128 rows [c/8][row][c%8]
+  uint16_t xo[4][kDMain / 16][32 * 8];      // this CTA's 256 channels of all 128 rows [row/32][c/8][row%32][c%8]
   uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
   float c2[4][kHAtt];                       // by item: later ones are staged before this one's softmax
   float red[2][kHAtt];
@@ -221,6 +250,12 @@ struct PrefixKernel {
   float4* part_o;   // [pairs + clusters][2][64][128] float4: element c4 of thread t of the epilogue
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
+};
+
+// The image of the shared entries: f16 [chunk][c/8][128 rows][c%8].  A piece of S's operand is 16 planes x
+// 64 rows of it (1 KB runs), a piece of O's 32 planes x 32 rows (512-byte runs); both 16 KB.
+struct ImageMaps {
+  CUtensorMap s, o;
 };
 
 // A row of a chunk: the plane row of an entry (>= 0), kNoRow, or a window row (kNoRow - 1 - its index).
@@ -384,25 +419,33 @@ __device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k
 // steps ahead, its page four.  Both operands run the same code: the kernel's loops have to fit the
 // instruction cache (unrolled by piece and operand they waited more for instructions than for data).
 template <bool kEx>
-__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, int rank, int c0,
-                                          int nc, int w, int lane, uint32_t n, uint32_t item) {
+__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, const Pair& x,
+                                          int rank, int c0, int nc, int w, int lane, uint32_t n, uint32_t item) {
   const int op = w >> 3, cb = lane >> 3;
   const int rl = 8 * (op ? w & 3 : w) + (lane & 7);
   const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0;
   const int blk0 = op ? 8 * rank + 4 * ((w >> 2) & 1) + cb : cb, blk_step = op ? 0 : 4;
-  const int plane = (op ? kChunk : kOwnChunk) * 8;  // f16 elements
-  uint16_t* const dst = (op ? &S.xo[4 * (4 * ((w >> 2) & 1) + cb)][0] : &S.xs[4 * cb][0]) + rl * 8;
-  const int dst_step = op ? 32 * 8 : 16 * kOwnChunk * 8;
+  const int plane = (op ? 32 : kOwnChunk) * 8;  // f16 elements
+  uint16_t* const dst = (op ? &S.xo[0][4 * (4 * ((w >> 2) & 1) + cb)][0] : &S.xs[4 * cb][0]) + rl * 8;
+  constexpr int dst_step = 16 * 1024 / 2;  // a piece
   const int steps = nc * kPieces;
+  // steps whose chunks are copied from the image, by the first warp of each operand
+  const int image_steps = x.image >= 0 ? min(max(x.nshared - c0, 0) * kPieces, steps) : 0;
   int ra, rb;
   Fetch fa, fb;
-  RowRef na = find_row(k, x, c0, row0), nb = find_row(k, x, c0, row0 + row_step);
-  auto load = [&](Fetch& f, int& r, RowRef& nx, int st) {  // fetch step st, find step st + 2
-    r = resolve(k, nx, false);
-    fetch(f, k, r, blk0 + blk_step * (st & 3));
-    st += 2;
-    if (st < steps) nx = find_row(k, x, c0 + (st >> 2), row0 + row_step * (st & 3));
+  RowRef na, nb;
+  auto find = [&](RowRef& nx, int st) {
+    if (st >= image_steps && st < steps) nx = find_row(k, x, c0 + (st >> 2), row0 + row_step * (st & 3));
   };
+  auto load = [&](Fetch& f, int& r, RowRef& nx, int st) {  // fetch step st, find step st + 2
+    if (st >= image_steps && st < steps) {
+      r = resolve(k, nx, false);
+      fetch(f, k, r, blk0 + blk_step * (st & 3));
+    }
+    find(nx, st + 2);
+  };
+  find(na, 0);
+  find(nb, 1);
   load(fa, ra, na, 0);
   load(fb, rb, nb, 1);
   bool good = op || stage_query<kEx>(S, k, rank ? x.q1 : x.q0, w, lane, n, item);
@@ -411,11 +454,22 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
     const int i = st & 3;
     if (m > 0) good = good && ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
-    put(f, k, r, blk0 + blk_step * i, dst + i * dst_step, plane);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
-    if (st + 2 < steps) load(f, r, nx, st + 2);
+    if (st < image_steps) {
+      if ((w & 7) == 0 && lane == 0) {
+        const int plane0 = (x.image + c0 + (st >> 2)) * (kDMain / 8);
+        ptx::mbar_arrive_n(&S.x_full[op][i], 7);  // for the other warps
+        ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
+        if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
+        else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
+      }
+      __syncwarp();
+    } else {
+      put(f, k, r, blk0 + blk_step * i, dst + i * dst_step, plane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
+    }
+    load(f, r, nx, st + 2);
   };
 #pragma unroll 1
   for (int st = 0; st < steps && good; st += 2) {
@@ -450,7 +504,8 @@ __device__ __forceinline__ bool mask_role(PrefixSmem& S, const PrefixKernel& k, 
 }
 
 template <bool kEx>
-__global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k) {
+__global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k,
+                                                                  const __grid_constant__ ImageMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrefixSmem& S = *reinterpret_cast<PrefixSmem*>(smem_raw);
   volatile int* abort_flag = &S.abort_flag;
@@ -494,10 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   const int t0 = idle ? 0 : (int)((long long)total * cluster / clusters);
   const int t1 = idle ? 0 : (int)((long long)total * (cluster + 1) / clusters);
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
-  // an arrival from the other CTA is among those waited for
-  auto ready = [&](uint64_t* bar, uint32_t n) {
-    return ptx::mbar_wait_warp_cluster(bar, n & 1u, abort_flag, kWaitBudget);
-  };
   bool good = true;
   int where = 0;
   // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1;
@@ -522,9 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   };
 
   if (warp >= kRowWarp && warp < kSMma) {
-    ptx::setmaxnreg_dec<kRowRegs>();
     for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
-      good = rows_role<kEx>(S, k, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
+      good = rows_role<kEx>(S, k, maps, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
     });
     where = 31;
   } else if (warp >= kSMma) {
@@ -532,7 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     // the odd CTA's MMA warps pass their CTA's arrivals on, in the order the even CTA's wait for them
     auto pass = [&](uint64_t* bar, uint32_t ph) {
       if (good) good = wait(bar, ph);
-      if (good && lane == 0) ptx::mbar_arrive_cluster(bar, 0);
+      ptx::tc_fence_after();  // the softmax's tensor-memory stores are among what is passed on
+      ptx::tc_fence_before();
+      if (good && lane == 0) ptx::mbar_arrive_peer(bar, 0);
     };
     if (warp == kMaskWarp) {
       for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
@@ -546,12 +598,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
       for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
         if (rank) pass(&S.q_full, items);
-        else good = ready(&S.q_full, items);
+        else good = wait(&S.q_full, items);
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j;
           // the softmax of both CTAs has left this S buffer
-          if (rank == 0 && m >= 2) good = ready(&S.p_full[m & 1], (m >> 1) - 1);
+          if (rank == 0 && m >= 2) good = wait(&S.p_full[m & 1], (m >> 1) - 1);
           const uint32_t dst = tmem + kColS + 64u * (m & 1u);
 #pragma unroll 1
           for (int i = 0; i < kPieces && good; ++i) {
@@ -559,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
               pass(&S.x_full[0][i], m);
               continue;
             }
-            good = ready(&S.x_full[0][i], m);
+            good = wait(&S.x_full[0][i], m);
             if (!good) break;
             ptx::tc_fence_after();
             const uint64_t at = (uint64_t)(i * 1024);  // q'[16 i], xs[16 i]: 16 KB on; a K step 2 KB
@@ -577,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       // ---- O += P X: eight K steps of 16 rows, four pieces of two; two accumulators of 128 channels a CTA
       constexpr uint32_t idesc_o = ptx::idesc_f16(128, 256, 0) | ptx::kIdescBMajorMN;
       const uint64_t dp = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
-      const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0], 128, kChunk * 16);
+      const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0][0], 128, 512);
       for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
@@ -586,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
             pass(&S.p_full[m & 1], m >> 1);
             if (j == 0 && items > 0) pass(&S.o_read, items - 1);
           } else {
-            good = ready(&S.p_full[m & 1], m >> 1);
-            if (good && j == 0 && items > 0) good = ready(&S.o_read, items - 1);
+            good = wait(&S.p_full[m & 1], m >> 1);
+            if (good && j == 0 && items > 0) good = wait(&S.o_read, items - 1);
           }
           const uint64_t dpo = dp + (uint64_t)((m & 1u) * (kChunk / 8 * kHAtt * 16 / 16));
 #pragma unroll 1
@@ -596,15 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
               pass(&S.x_full[1][i], m);
               continue;
             }
-            good = ready(&S.x_full[1][i], m);
+            good = wait(&S.x_full[1][i], m);
             if (!good) break;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)  // p[4 i + 2 ks]: 2 KB a step; xo rows 32 i + 16 ks: 256 bytes a step
+            for (int ks = 0; ks < 2; ++ks)  // p[4 i + 2 ks]: 2 KB a step; xo[i], rows 16 ks: 256 bytes a step
 #pragma unroll
-              for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[16 h], 32 KB on
+              for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[i][16 h], 8 KB on
                 ptx::mma_f16_ss_pair_elect(tmem + 128u * (uint32_t)h, dpo + (uint64_t)((2 * i + ks) * 128),
-                                           dx + (uint64_t)(h * 2048 + (2 * i + ks) * 16), idesc_o,
+                                           dx + (uint64_t)(i * 1024 + h * 512 + ks * 16), idesc_o,
                                            (j | i | ks) > 0 ? 1u : 0u);
             ptx::mma_commit_pair_elect(&S.x_free[1][i]);
           }
@@ -753,6 +805,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   }
 }
 
+// The image, chunk by chunk: a warp's lane l widens block (of 32 channels) 4 i + l / 8 of row l % 8 of its
+// eight, and stores 16 bytes to each of the block's four planes, 128 contiguous bytes for eight rows.
+// Bytes bound it: 288 read and 1,024 written an entry.
+constexpr int kWidenThreads = 512;
+__global__ void __launch_bounds__(kWidenThreads) k_prefix_widen(PrefixArgs a, PrefixKernel k, uint16_t* image) {
+  __shared__ int s_group;
+  ptx::griddep_wait();
+  const int total = a.totals[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cb = lane >> 3;
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    __syncthreads();
+    // the group whose image holds chunk t: the last one that starts at or before it
+    for (int g = threadIdx.x; g < a.G; g += kWidenThreads) {
+      const int at = a.gimage[g];
+      if (at < 0 || at > t) continue;
+      const int first = a.group_start[g];
+      const int ns = min(min(max(a.n_shared[g], 0), a.shared_max),
+                         (int)min((long long)max(a.n_entries[first], 0), (long long)a.table_cap));
+      if (t < at + (ns + kChunk - 1) / kChunk) s_group = g;
+    }
+    __syncthreads();
+    const int g = s_group, first = a.group_start[g];
+    const int ns = min(min(max(a.n_shared[g], 0), a.shared_max),
+                       (int)min((long long)max(a.n_entries[first], 0), (long long)a.table_cap));
+    const int row = 8 * warp + (lane & 7), e = (t - a.gimage[g]) * kChunk + row;
+    int r = kNoRow;
+    if (e < ns) {
+      const int pi = (int)((uint64_t)e * k.page_div >> 40);
+      r = resolve(k, RowRef{k.table[first * k.max_pages + pi], e - pi * k.page_entries}, cb == 0);
+    }
+    Fetch f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, 4 * i + cb);
+    uint16_t* dst = image + (int64_t)t * kDMain * kChunk + (4 * cb * kChunk + row) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(f[i], k, r, 4 * i + cb, dst + i * 16 * kChunk * 8, kChunk * 8);
+  }
+}
+
 // Joins the partials of one query: thread t of a CTA has head t % 64 and, of channel half t / 64, the
 // eight float4 of column block blockIdx.y (channels 256 (t / 64) + 32 blockIdx.y ..).
 __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ qpair,
@@ -831,14 +922,16 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
 
 struct PrefixWs {
   Pair* pairs;
-  int32_t *gpair, *qpair, *cpair, *totals;
+  int32_t *gpair, *qpair, *cpair, *totals, *gimage;
+  uint16_t* image;
+  int64_t image_cap;
   float4* part_o;
   float2* part_ml;
   size_t bytes;
 };
 int max_pairs(int32_t B, int32_t G) { return (B + G + 2) / 2; }
 
-PrefixWs prefix_ws(void* ws, int32_t B, int32_t G) {
+PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   PrefixWs L{};
   size_t off = kWsHeader;
   char* base = (char*)ws;
@@ -852,15 +945,33 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G) {
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.qpair = (int32_t*)take((size_t)B * 4);
   L.cpair = (int32_t*)take(kClusters * 4);
-  L.totals = (int32_t*)take(8);
+  L.totals = (int32_t*)take(12);
+  L.gimage = (int32_t*)take(((size_t)G + 1) * 4);
   L.part_o = (float4*)take(slots * 2 * kHAtt * kDMain * 4);
   L.part_ml = (float2*)take(slots * 2 * kHAtt * 8);
+  const int64_t groups = B / kImageQueries < G ? B / kImageQueries : G;
+  L.image_cap = groups * cdiv(shared_max, kChunk);
+  if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
+  L.image = (uint16_t*)take((size_t)L.image_cap * kChunk * kDMain * 2);
   L.bytes = off;
   return L;
 }
 
-template <typename K>
-cudaError_t launch_pairs(void (*kern)(K), int clusters, size_t smem, cudaStream_t st, const K& args) {
+// f16 image [chunks * 64 planes][128 rows][8 channels] as 32-bit words, boxes of `rows` rows x `planes`
+bool image_map(CUtensorMap* map, uint16_t* image, int64_t chunks, uint32_t rows, uint32_t planes) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)kChunk * 4, (cuuint64_t)(chunks > 0 ? chunks : 1) * (kDMain / 8)};
+  cuuint64_t strides[1] = {(cuuint64_t)kChunk * 16};
+  cuuint32_t box[2] = {rows * 4, planes};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, image, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... K>
+cudaError_t launch_pairs(void (*kern)(K...), int clusters, size_t smem, cudaStream_t st, const K&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(kThreads);
@@ -875,7 +986,7 @@ cudaError_t launch_pairs(void (*kern)(K), int clusters, size_t smem, cudaStream_
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, args);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace
@@ -886,7 +997,7 @@ extern "C" size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t 
   if (B <= 0 || B > 65535 || G <= 0 || G > B || n_shared_max < 0 || n_own_max < 0 || n_shared_max > CSA2_MAX_DENSE ||
       n_own_max > CSA2_MAX_DENSE || n_swa < 0)
     return 0;
-  return csa2::prefix_ws(nullptr, B, G).bytes;
+  return csa2::prefix_ws(nullptr, B, G, n_shared_max).bytes;
 }
 
 extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
@@ -910,12 +1021,13 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
   const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
   if (bad != CSA2_OK) return bad;
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
-  const PrefixWs L = prefix_ws(ws, B, G);
+  const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals, ws};
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals,
+                     L.gimage, L.image_cap, ws};
   {
     KernelTimer timer("k_prefix_plan", st);
     launch_pdl(k_prefix_plan, dim3(1), dim3(kPlanThreads), 0, st, a);
@@ -924,13 +1036,20 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
   const size_t smem = sizeof(PrefixSmem);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return launch_status();
+  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, (const uint16_t*)q_bf16, pages->table,
+                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa,
+                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, softmax_scale, ex,
+                       L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
+  ImageMaps maps{};
+  if (L.image_cap > 0) {
+    if (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32))
+      return CSA2_ERR_CUDA;
+    KernelTimer timer("k_prefix_widen", st);
+    launch_pdl(k_prefix_widen, dim3(2 * 152), dim3(kWidenThreads), 0, st, a, k, L.image);
+  }
   {
-    const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, (const uint16_t*)q_bf16, pages->table,
-                         pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa,
-                         ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, softmax_scale, ex,
-                         L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
     KernelTimer timer("k_prefix_attn", st);
-    launch_pairs(kern, kClusters, smem, st, k);
+    launch_pairs(kern, kClusters, smem, st, k, maps);
   }
   {
     KernelTimer timer("k_prefix_merge", st);

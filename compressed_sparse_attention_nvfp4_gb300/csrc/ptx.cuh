@@ -27,6 +27,9 @@ __device__ __forceinline__ void fence_mbar_init() {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
                "r"(bytes)
@@ -352,34 +355,17 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on the barrier at the same shared-memory offset of the cluster's CTA `rank`.
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+// Arrives on the barrier at the same shared-memory offset of the cluster's CTA `rank`.  The arrival has CTA
+// scope: it tells the other CTA's MMA warp that operands in THIS CTA's shared and tensor memory are ready,
+// which that warp never reads itself -- the pair's MMA reads them here, after the proxy fence and the
+// CTA-scope release of their writers.  (With .release.cluster each arrival waited about 1,400 cycles for
+// the thread's memory operations everywhere.)
+__device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.release.cta.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
-}
-// mbar_wait_warp with cluster-scope acquire: what the other CTA wrote before its arrival is seen
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                       long long budget) {
-  bool ok = mbar_try_wait_cluster(bar, parity, CSA2_WAIT_SLEEP_NS);
-  if (!ok) {
-    const long long t0 = clock64();
-    while (!(ok = mbar_try_wait_cluster(bar, parity, CSA2_WAIT_SLEEP_NS)))
-      if (*abort || clock64() - t0 > budget) break;
-  }
-  return __all_sync(0xffffffffu, ok);
 }
 // Tensor memory of a CTA pair: one warp of each CTA calls each of these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot_smem, uint32_t cols) {
