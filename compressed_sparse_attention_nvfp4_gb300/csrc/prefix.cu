@@ -24,11 +24,12 @@
 namespace csa2 {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPrepThreads = 512;
 constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of the 152 SMs
 constexpr int kChunk = 128;      // rows of a chunk
 constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
 constexpr int kImageQueries = 3;   // a group of at least this many queries has its shared entries widened once
+constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM
 constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
 
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
@@ -42,7 +43,19 @@ struct Pair {
   int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
   int32_t nshared; // shared chunks; own chunks follow
   int32_t image;   // the shared entries' first chunk in the image, or -1
-  int32_t pad;
+};
+
+// The queries' staging: what it reads, and where it leaves their images.
+struct PrefixQuery {
+  const uint16_t* q;
+  const float* norm_w;
+  float eps, scale;
+  int rope;
+  const int64_t* qpos;
+  RopeTheta th;
+  uint16_t* image;  // [B + 1][c/8][head][c%8] f16
+  float* c2;        // [B + 1][64]
+  float2* turn;     // [B][32]
 };
 
 struct PrefixArgs {
@@ -56,8 +69,8 @@ struct PrefixArgs {
   int32_t* gpair;     // [G + 3] first pair of each range of queries
   int32_t* qpair;     // [B] pair * 2 + place
   int32_t* cpair;     // [kClusters] pair of each cluster's first chunk
-  int32_t* totals;    // pairs, chunks, image chunks
-  int32_t* gimage;    // [G + 1] first image chunk of each group (those at or beyond the total have none)
+  int32_t* totals;    // pairs, chunks
+  int32_t* gimage;    // [G] first image chunk of each group, or -1
   int64_t image_cap;  // chunks the image has room for
   void* ws;
 };
@@ -73,7 +86,7 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  int w = s_warp[lane];
+  int w = lane < kPrepThreads / 32 ? s_warp[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, o);
@@ -87,14 +100,27 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
 
 // The pairs of the batch and the chunks of each, by one CTA.  Ranges of queries: those before the
 // first group, the G groups, those behind the last (a range outside the groups shares nothing).
-__global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
-  __shared__ int s_warp[kPlanThreads / 32];
-  __shared__ int s_bad, s_images;
+__device__ __forceinline__ int visible(const PrefixArgs& a, int q) {
+  return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap);
+}
+// a group's shared entries; those beyond its first query's own count are read as each query's own
+__device__ __forceinline__ int shared_of(const PrefixArgs& a, int g, int first) {
+  return min(min(max(a.n_shared[g], 0), a.shared_max), visible(a, first));
+}
+// chunks that group g's image takes, if there is room
+__device__ __forceinline__ int image_chunks(const PrefixArgs& a, int g) {
+  const int first = a.group_start[g], end = a.group_start[g + 1];
+  if (first < 0 || end > a.B || end - first < kImageQueries) return 0;
+  return (shared_of(a, g, first) + kChunk - 1) / kChunk;
+}
+
+__device__ __forceinline__ void plan_block(const PrefixArgs& a) {
+  __shared__ int s_warp[kPrepThreads / 32];
+  __shared__ int s_bad;
   const int tid = threadIdx.x;
-  if (tid == 0) s_bad = s_images = 0;
-  ptx::griddep_wait();
+  if (tid == 0) s_bad = 0;
   __syncthreads();
-  for (int g = tid; g < a.G; g += kPlanThreads) {
+  for (int g = tid; g < a.G; g += kPrepThreads) {
     const int lo = a.group_start[g], hi = a.group_start[g + 1];
     if (lo < 0 || hi < lo || hi > a.B) {
       s_bad = 1;
@@ -107,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
   int base = 0;
-  for (int v0 = 0; v0 < R; v0 += kPlanThreads) {
+  for (int v0 = 0; v0 < R; v0 += kPrepThreads) {
     const int v = v0 + tid;
     const int n = v < R ? (range_hi(v) - range_lo(v) + 1) / 2 : 0;
     int total;
@@ -117,26 +143,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
   }
   if (tid == 0) a.gpair[R] = base;
   const int np = base;
-  auto count = [&](int q) { return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap); };
-  // a group's shared entries; those beyond its first query's own count are read as each query's own
-  auto shared_of = [&](int g, int first) { return min(min(max(a.n_shared[g], 0), a.shared_max), count(first)); };
+  // a group whose image would end beyond the room has none, and so do all behind it
   int images = 0;
-  for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    int n = 0;
-    if (g < G && a.group_start[g + 1] - a.group_start[g] >= kImageQueries)
-      n = (shared_of(g, a.group_start[g]) + kChunk - 1) / kChunk;
+  for (int g0 = 0; g0 < G; g0 += kPrepThreads) {
+    const int g = g0 + tid, n = g < G ? image_chunks(a, g) : 0;
     int total;
     const int at = images + block_scan(n, s_warp, &total);
-    // a group that ends beyond the image's room has none, and so do all behind it
-    if (g < G) a.gimage[g] = n > 0 && at + n <= a.image_cap ? at : -1;
-    if (n > 0 && at + n <= a.image_cap) atomicMax(&s_images, at + n);
+    if (g < G) a.gimage[g] = n > 0 && at + (int64_t)n <= a.image_cap ? at : -1;
     images += total;
-    __syncthreads();
   }
   __syncthreads();
   int chunks = 0;
-  for (int p0 = 0; p0 < np; p0 += kPlanThreads) {
+  for (int p0 = 0; p0 < np; p0 += kPrepThreads) {
     const int p = p0 + tid;
     Pair x{};
     int n = 0;
@@ -153,14 +171,14 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
       x.first = first;
       x.image = -1;
       if (lo >= 1 && lo <= G) {
-        x.ns = shared_of(lo - 1, first);
+        x.ns = shared_of(a, lo - 1, first);
         x.image = a.gimage[lo - 1];
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int q = i ? x.q1 : x.q0;
         if (q < 0) continue;
-        const int c = count(q);
+        const int c = visible(a, q);
         int own = max(c - x.ns, 0);
         if (own > a.own_max) {
           report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);
@@ -183,12 +201,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_prefix_plan(PrefixArgs a) {
     a.pairs[np].chunk0 = chunks;
     a.totals[0] = np;
     a.totals[1] = chunks;
-    a.totals[2] = s_images;
-    a.gimage[G] = -1;
   }
   __syncthreads();
   const int clusters = min(kClusters, chunks);
-  for (int c = tid; c < clusters; c += kPlanThreads) {  // the pair of chunk floor(chunks * c / clusters)
+  for (int c = tid; c < clusters; c += kPrepThreads) {  // the pair of chunk floor(chunks * c / clusters)
     const int t = (int)((long long)chunks * c / clusters);
     int lo = 0, hi = np;
     while (hi - lo > 1) {
@@ -226,7 +242,7 @@ struct __align__(1024) PrefixSmem {
   Pair pair[kThreads / 32];                 // each warp's copy of its item's pair: not held in registers
   // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
   // of the same role passes on for all of that CTA's
-  uint64_t q_load, q_full, staged[4];
+  uint64_t q_land[4], q_peer;               // q' and c2 copied (by item); the odd CTA's q'
   uint64_t x_full[2][kPieces], x_free[2][kPieces];  // [0] S's operand, [1] O's
   uint64_t s_full[2], p_full[2], p_free[2], m_full[2];
   uint64_t o_read;                          // epilogue done with O
@@ -238,16 +254,16 @@ static_assert(sizeof(PrefixSmem) <= 232448, "prefix attention shared memory");
 
 struct PrefixKernel {
   const uint8_t *kv_codes, *kv_scales, *swa;
-  const uint16_t* q;
+  const uint16_t* q;      // [B + 1][c/8][head][c%8] f16 images of the staged queries, the last one zeros
+  const float* c2;        // [B + 1][64] logit (log2 units) per raw S
   const int32_t* table;
   int64_t max_pages;
-  int32_t n_pages, page_entries, n_swa;
+  int32_t n_pages, page_entries, n_swa, B;
   uint64_t page_div;  // ceil(2^40 / page_entries): e * page_div >> 40 = e / page_entries for e < 2^18
-  float scale;
-  AttnExtras ex;
+  const int64_t *win_pos, *win_lo;
   const Pair* pairs;
   const int32_t *cpair, *totals;
-  float4* part_o;   // [pairs + clusters][2][64][128] float4: element c4 of thread t of the epilogue
+  uint4* part_o;    // [pairs + clusters][2][32][128]: eight f16 channels c8 of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
 };
@@ -286,7 +302,7 @@ __device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x,
       idx -= own;
       if (idx >= k.n_swa) return RowRef{0, kNoRow};
       const int w = q * k.n_swa + idx;
-      if (k.ex.win_pos && __ldg(k.ex.win_pos + w) < max(__ldg(k.ex.win_lo + q), (int64_t)0)) return RowRef{0, kNoRow};
+      if (k.win_pos && __ldg(k.win_pos + w) < max(__ldg(k.win_lo + q), (int64_t)0)) return RowRef{0, kNoRow};
       return RowRef{0, kNoRow - 1 - w};
     }
     e = x.ns + idx;
@@ -324,26 +340,28 @@ __device__ __forceinline__ void widen_e4m3(uint4 w, uint4& a, uint4& b) {
 
 // One thread's fetched codes of 32 channels of a row.
 struct Fetch {
-  uint4 codes;
+  uint4 codes, more;  // 16 bytes of codes, or 32 of a window row
   uint32_t scales;
 };
-// Starts the loads of 32-channel block cb of row r (window rows are read when they are written).
+// Starts the loads of 32-channel block cb of row r.
 __device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int r, int cb) {
   if (r >= 0) {
     f.codes = __ldg(reinterpret_cast<const uint4*>(k.kv_codes + (int64_t)r * 256) + cb);
     f.scales = __ldg(reinterpret_cast<const uint16_t*>(k.kv_scales + (int64_t)r * 32) + cb);
+  } else if (r < kNoRow) {
+    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (int64_t)(kNoRow - 1 - r) * kDMain) + 2 * cb;
+    f.codes = __ldg(src);
+    f.more = __ldg(src + 1);
   }
 }
-// Writes 32-channel block cb of the row to dst: vector q of it at dst + q * stride (f16 elements).
-__device__ __forceinline__ void put(const Fetch& f, const PrefixKernel& k, int r, int cb, uint16_t* dst, int stride) {
+// Writes the fetched block of row r to dst: vector q of it at dst + q * stride (f16 elements).
+__device__ __forceinline__ void put(const Fetch& f, int r, uint16_t* dst, int stride) {
   uint4 v[4];
   if (r >= 0) {
     widen_codes(f.codes, f.scales, v);
   } else if (r < kNoRow) {
-    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (int64_t)(kNoRow - 1 - r) * kDMain) + 2 * cb;
-    const uint4 a = __ldg(src), b = __ldg(src + 1);
-    widen_e4m3(a, v[0], v[1]);
-    widen_e4m3(b, v[2], v[3]);
+    widen_e4m3(f.codes, v[0], v[1]);
+    widen_e4m3(f.more, v[2], v[3]);
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -378,39 +396,6 @@ __device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float
   return top;
 }
 
-// The query of an item into q' and c2, by S's eight row warps (w 0-7): its bf16 rows come through the
-// S operand's buffer, which S of the item before has left (n chunks so far).  Returns false when a
-// wait gave up.
-template <bool kEx>
-__device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k, int q, int w, int lane, uint32_t n,
-                                            uint32_t item) {
-  volatile int* abort_flag = &S.abort_flag;
-  bool good = n == 0 || ptx::mbar_wait_warp(&S.x_free[0][kPieces - 1], (n - 1) & 1u, abort_flag, kWaitBudget);
-  if (good && q >= 0) {
-    if (w == 0 && lane == 0) {
-      ptx::mbar_arrive_expect_tx(&S.q_load, kHAtt * kDMain * 2);
-      ptx::bulk_g2s(&S.xs[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_load);
-    }
-    __syncwarp();
-    volatile int keep_waiting = 0;  // the copy writes shared memory: no leaving before it has landed
-    good = ptx::mbar_wait_warp(&S.q_load, item & 1u, &keep_waiting, kWaitBudget);
-    if (good) stage_q<kEx>(S.q, S.c2[item & 3u], &S.xs[0][0], k.scale, w, lane, k.ex, q);
-  } else if (good) {  // no second query: zeros
-    if (w == 0 && lane == 0) ptx::mbar_arrive(&S.q_load);  // keeps its phase
-    for (int i = w * 32 + lane; i < kDMain / 8 * kQPlane / 8; i += 256)
-      reinterpret_cast<uint4*>(&S.q[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (w == 0) S.c2[item & 3u][lane] = S.c2[item & 3u][lane + 32] = 1.0f;
-  }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::mbar_arrive(&S.staged[item & 3u]);
-    ptx::mbar_arrive(&S.q_full);
-  }
-  // every row warp has read the query's bf16 rows: the buffer may be written
-  return good && ptx::mbar_wait_warp(&S.staged[item & 3u], (item >> 2) & 1u, abort_flag, kWaitBudget);
-}
-
 // Chunks [c0, c0 + nc) of pair x by the 16 row warps.  Operand 0 (S's, warps 0-7): this CTA's 64 rows,
 // handed over by 128 channels: row 8 w + l % 8, block (of 32 channels) 4 i + l / 8 in piece i.  Operand 1
 // (O's): its 256 channels of all rows, by 32 rows: row 32 i + 8 (w % 4) + l % 8, block 4 (w / 4 % 2) + l / 8
@@ -418,7 +403,6 @@ __device__ __forceinline__ bool stage_query(PrefixSmem& S, const PrefixKernel& k
 // eight rows of a plane: no bank conflicts.  A step writes one piece; a row's codes are fetched two
 // steps ahead, its page four.  Both operands run the same code: the kernel's loops have to fit the
 // instruction cache (unrolled by piece and operand they waited more for instructions than for data).
-template <bool kEx>
 __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, const Pair& x,
                                           int rank, int c0, int nc, int w, int lane, uint32_t n, uint32_t item) {
   const int op = w >> 3, cb = lane >> 3;
@@ -434,6 +418,7 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   int ra, rb;
   Fetch fa, fb;
   RowRef na, nb;
+  int issued = -1;  // last step copied from the image
   auto find = [&](RowRef& nx, int st) {
     if (st >= image_steps && st < steps) nx = find_row(k, x, c0 + (st >> 2), row0 + row_step * (st & 3));
   };
@@ -448,23 +433,38 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   find(nb, 1);
   load(fa, ra, na, 0);
   load(fb, rb, nb, 1);
-  bool good = op || stage_query<kEx>(S, k, rank ? x.q1 : x.q0, w, lane, n, item);
+  bool good = true;
+  if (w == 0) {  // the item's query, once S of the item before has left q'
+    good = n == 0 || ptx::mbar_wait_warp(&S.x_free[0][kPieces - 1], (n - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (good && lane == 0) {
+      const int64_t q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
+      uint64_t* bar = &S.q_land[item & 3u];
+      ptx::mbar_arrive_expect_tx(bar, kHAtt * kDMain * 2 + kHAtt * 4);
+      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, bar);
+      ptx::bulk_g2s(&S.c2[item & 3u][0], k.c2 + q * kHAtt, kHAtt * 4, bar);
+    }
+    __syncwarp();
+  }
+  const bool copied = w == 0 && good;
   auto step = [&](Fetch& f, int& r, RowRef& nx, int st) {
     const uint32_t m = n + (uint32_t)(st >> 2);
     const int i = st & 3;
     if (m > 0) good = good && ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     if (st < image_steps) {
-      if ((w & 7) == 0 && lane == 0) {
+      // every warp arrives, also those that copy nothing: none may miss a phase of x_free
+      if ((w & 7) != 0) {
+        if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
+      } else if (lane == 0) {
         const int plane0 = (x.image + c0 + (st >> 2)) * (kDMain / 8);
-        ptx::mbar_arrive_n(&S.x_full[op][i], 7);  // for the other warps
         ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
         if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
         else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
       }
+      issued = st;
       __syncwarp();
     } else {
-      put(f, k, r, blk0 + blk_step * i, dst + i * dst_step, plane);
+      put(f, r, dst + i * dst_step, plane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
@@ -475,6 +475,12 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   for (int st = 0; st < steps && good; st += 2) {
     step(fa, ra, na, st);
     step(fb, rb, nb, st + 1);
+  }
+  if (!good && (w & 7) == 0) {  // copies in flight write shared memory: they land before anyone leaves
+    volatile int keep_waiting = 0;
+    if (copied) ptx::mbar_wait_warp(&S.q_land[item & 3u], (item >> 2) & 1u, &keep_waiting, kWaitBudget);
+    for (int st = issued; st >= 0 && st > issued - kPieces; --st)
+      ptx::mbar_wait_warp(&S.x_full[op][st & 3], (n + (uint32_t)(st >> 2)) & 1u, &keep_waiting, kWaitBudget);
   }
   return good;
 }
@@ -503,7 +509,6 @@ __device__ __forceinline__ bool mask_role(PrefixSmem& S, const PrefixKernel& k, 
   return good;
 }
 
-template <bool kEx>
 __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k,
                                                                   const __grid_constant__ ImageMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -516,13 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   if (warp == kSMma) {
     if (lane == 0) {
       const uint32_t peer = rank == 0 ? 1 : 0;
-      ptx::mbar_init(&S.q_load, 1);
-      ptx::mbar_init(&S.q_full, 8 + peer);
+      ptx::mbar_init(&S.q_peer, 1);
       for (int i = 0; i < 2 * kPieces; ++i) {
         ptx::mbar_init(&S.x_full[0][0] + i, 8 + peer);
         ptx::mbar_init(&S.x_free[0][0] + i, 1);
       }
-      for (int i = 0; i < 4; ++i) ptx::mbar_init(&S.staged[i], 8);
+      for (int i = 0; i < 4; ++i) ptx::mbar_init(&S.q_land[i], 1);
       for (int i = 0; i < 2; ++i) {
         ptx::mbar_init(&S.s_full[i], 1);
         ptx::mbar_init(&S.p_full[i], 4 + peer);
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 
   if (warp >= kRowWarp && warp < kSMma) {
     for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
-      good = rows_role<kEx>(S, k, maps, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
+      good = rows_role(S, k, maps, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
     });
     where = 31;
   } else if (warp >= kSMma) {
@@ -597,8 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
       for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
-        if (rank) pass(&S.q_full, items);
-        else good = wait(&S.q_full, items);
+        good = wait(&S.q_land[items & 3u], items >> 2);
+        if (rank == 0) good = good && wait(&S.q_peer, items);
+        else if (good && lane == 0) ptx::mbar_arrive_peer(&S.q_peer, 0);
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j;
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t items) {
       const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
       float m2 = -INFINITY, lsum = 0.0f;
-      good = wait(&S.staged[items & 3u], items >> 2);
+      good = wait(&S.q_land[items & 3u], items >> 2);
       const float c2 = S.c2[items & 3u][h];
 #pragma unroll 1
       for (int j = 0; j < nc; ++j) {
@@ -764,23 +769,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       if (!good) return;
       ptx::tc_fence_after();
       const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
+      S.red[half][h] = lsum;
+      softmax_sync();
+      const float l = S.red[0][h] + S.red[1][h];
+      softmax_sync();
       if (qme >= 0) {
-        float4* po = k.part_o + slot * 64 * 128 + tid;
+        // O / l in f16: at most the largest |x| (2,688), and a rounding of 2^-11 at most, a quarter of that
+        // of a bf16 output; the partials are most of what a short call moves
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        uint4* po = k.part_o + slot * 32 * 128 + tid;
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t a[32];
           ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
           ptx::tmem_wait_ld();
+          auto pk = [&](int u) {
+            const __half2 v = __floats2half2_rn(__uint_as_float(a[2 * u]) * inv, __uint_as_float(a[2 * u + 1]) * inv);
+            return *reinterpret_cast<const uint32_t*>(&v);
+          };
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            po[(c * 8 + u) * 128] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]),
-                                                __uint_as_float(a[4 * u + 2]), __uint_as_float(a[4 * u + 3]));
+          for (int u = 0; u < 4; ++u)
+            po[(c * 4 + u) * 128] = make_uint4(pk(4 * u), pk(4 * u + 1), pk(4 * u + 2), pk(4 * u + 3));
         }
+        if (half == 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, l);
       }
-      S.red[half][h] = lsum;
-      softmax_sync();
-      if (half == 0 && qme >= 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, S.red[0][h] + S.red[1][h]);
-      softmax_sync();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.o_read);
@@ -805,31 +817,112 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   }
 }
 
-// The image, chunk by chunk: a warp's lane l widens block (of 32 channels) 4 i + l / 8 of row l % 8 of its
-// eight, and stores 16 bytes to each of the block's four planes, 128 contiguous bytes for eight rows.
-// Bytes bound it: 288 read and 1,024 written an entry.
-constexpr int kWidenThreads = 512;
-__global__ void __launch_bounds__(kWidenThreads) k_prefix_widen(PrefixArgs a, PrefixKernel k, uint16_t* image) {
-  __shared__ int s_group;
-  ptx::griddep_wait();
-  const int total = a.totals[2];
+// ------------------------------------------------------ preparation and merge
+
+// A query into its f16 image and c2 (attn.cuh, stage_q: the same steps, from global memory by 16 warps of
+// four heads each, lane l holding channels 16 l ..), and the rotation's cosines and sines.  The image goes
+// through shared memory with padded planes, so that its stores are whole lines.
+constexpr int kQPad = kHAtt * 16 + 16;  // bytes of a plane
+__device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, unsigned char* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint4* const img = reinterpret_cast<uint4*>(a.image + (int64_t)b * kHAtt * kDMain);
+  if (b == B) {  // the missing second query of an odd group
+    for (int i = threadIdx.x; i < kHAtt * kDMain / 8; i += kPrepThreads) img[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x < kHAtt) a.c2[(int64_t)b * kHAtt + threadIdx.x] = 1.0f;
+    return;
+  }
+  float rc = 1.0f, rs = 0.0f;  // lane l: pair l
+  if (a.rope) {
+    rope_cos_sin(a.th.t[lane], (double)a.qpos[b], rc, rs);
+    if (warp == 0) a.turn[(int64_t)b * 32 + lane] = make_float2(rc, rs);
+  }
+#pragma unroll 1
+  for (int i = 0; i < kHAtt / (kPrepThreads / 32); ++i) {
+    const int h = warp * (kHAtt / (kPrepThreads / 32)) + i;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + h) * kDMain) + 2 * lane;
+    const uint4 q0 = src[0], q1 = src[1];
+    const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    if (a.norm_w) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ss = fmaf(v[j], v[j], ss);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = 1.0f / sqrtf(ss / (float)kDMain + a.eps);
+      const float4* wv = reinterpret_cast<const float4*>(a.norm_w) + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 g = __ldg(wv + j);
+        v[4 * j] = g.x * (v[4 * j] * r);
+        v[4 * j + 1] = g.y * (v[4 * j + 1] * r);
+        v[4 * j + 2] = g.z * (v[4 * j + 2] * r);
+        v[4 * j + 3] = g.w * (v[4 * j + 3] * r);
+      }
+    }
+    if (a.rope) {  // lanes 28-31 hold the pairs 8 (l - 28) ..
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int pair = (8 * (lane - 28) + j) & 31;
+        const float c = __shfl_sync(0xffffffffu, rc, pair), sn = __shfl_sync(0xffffffffu, rs, pair);
+        if (lane >= 28) rope_pair(v[2 * j], v[2 * j + 1], c, sn);
+      }
+    }
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) mx = fmaxf(mx, fabsf(v[j]));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const int sig = mx > 0.0f ? min(max(floor_log2_f32(mx) - 14, -126), 126) : 0;
+    const float inv = exp2i_f32(-sig);
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __half2 h2 = __floats2half2_rn(v[2 * j] * inv, v[2 * j + 1] * inv);
+      o[j] = *reinterpret_cast<const uint32_t*>(&h2);
+    }
+    *reinterpret_cast<uint4*>(smem + (2 * lane) * kQPad + h * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(smem + (2 * lane + 1) * kQPad + h * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+    if (lane == 0) a.c2[(int64_t)b * kHAtt + h] = kLog2e * a.scale * exp2i_f32(sig);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kHAtt * kDMain / 8; i += kPrepThreads)
+    img[i] = *reinterpret_cast<const uint4*>(smem + (i / kHAtt) * kQPad + (i % kHAtt) * 16);
+}
+
+// The image's chunks first, first + step, ..: a warp's lane l widens block (of 32 channels) 4 i + l / 8 of
+// row l % 8 of its eight, and stores 16 bytes to each of the block's four planes, 128 contiguous bytes for
+// eight rows.  Bytes bound it: 288 read and 1,024 written an entry.
+__device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
+                                             int step) {
+  __shared__ int s_warp[kPrepThreads / 32];
+  __shared__ int s_group, s_at;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cb = lane >> 3;
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+  for (int64_t t = first_chunk;; t += step) {
+    // the group whose image holds chunk t
+    if (threadIdx.x == 0) s_group = -1;
     __syncthreads();
-    // the group whose image holds chunk t: the last one that starts at or before it
-    for (int g = threadIdx.x; g < a.G; g += kWidenThreads) {
-      const int at = a.gimage[g];
-      if (at < 0 || at > t) continue;
-      const int first = a.group_start[g];
-      const int ns = min(min(max(a.n_shared[g], 0), a.shared_max),
-                         (int)min((long long)max(a.n_entries[first], 0), (long long)a.table_cap));
-      if (t < at + (ns + kChunk - 1) / kChunk) s_group = g;
+    int base = 0;
+    for (int g0 = 0; g0 < a.G && base <= t; g0 += kPrepThreads) {
+      const int g = g0 + threadIdx.x, n = g < a.G ? image_chunks(a, g) : 0;
+      int total;
+      const int at = base + block_scan(n, s_warp, &total);
+      if (n > 0 && at + (int64_t)n <= a.image_cap && t >= at && t < at + n) {
+        s_group = g;
+        s_at = at;
+      }
+      base += total;
     }
     __syncthreads();
-    const int g = s_group, first = a.group_start[g];
-    const int ns = min(min(max(a.n_shared[g], 0), a.shared_max),
-                       (int)min((long long)max(a.n_entries[first], 0), (long long)a.table_cap));
-    const int row = 8 * warp + (lane & 7), e = (t - a.gimage[g]) * kChunk + row;
+    const int g = s_group;
+    if (g < 0) return;
+    const int first = a.group_start[g], ns = shared_of(a, g, first);
+    const int row = 8 * warp + (lane & 7), e = (int)(t - s_at) * kChunk + row;
     int r = kNoRow;
     if (e < ns) {
       const int pi = (int)((uint64_t)e * k.page_div >> 40);
@@ -838,18 +931,33 @@ __global__ void __launch_bounds__(kWidenThreads) k_prefix_widen(PrefixArgs a, Pr
     Fetch f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) fetch(f[i], k, r, 4 * i + cb);
-    uint16_t* dst = image + (int64_t)t * kDMain * kChunk + (4 * cb * kChunk + row) * 8;
+    uint16_t* dst = image + t * kDMain * kChunk + (4 * cb * kChunk + row) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(f[i], k, r, 4 * i + cb, dst + i * 16 * kChunk * 8, kChunk * 8);
+    for (int i = 0; i < 4; ++i) put(f[i], r, dst + i * 16 * kChunk * 8, kChunk * 8);
+    __syncthreads();  // s_group is written again
   }
 }
 
-// Joins the partials of one query: thread t of a CTA has head t % 64 and, of channel half t / 64, the
-// eight float4 of column block blockIdx.y (channels 256 (t / 64) + 32 blockIdx.y ..).
+// Everything the attention needs, by independent CTAs of one launch: the plan, the queries, the image.
+__global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, PrefixQuery q,
+                                                              const __grid_constant__ PrefixKernel k, uint16_t* image) {
+  extern __shared__ __align__(16) unsigned char prep_smem[];
+  ptx::griddep_wait();
+  const int64_t b = (int64_t)blockIdx.x - 1;
+  if (b < 0) plan_block(a);
+  else if (b <= a.B) stage_block(q, a.B, (int)b, prep_smem);
+  else widen_chunks(a, k, image, (int)(b - a.B - 1), (int)(gridDim.x - a.B - 2));
+}
+
+// Joins the partials of one query: thread t of a CTA has head t % 64 and, of channel half t / 64, the 32
+// channels 256 (t / 64) + 32 blockIdx.y ...  Partial i has reference m_i (log2 units), sum l_i and O_i / l_i:
+// out = sum 2^(m_i - m) l_i (O_i / l_i) / L, L = sum 2^(m_i - m) l_i (+ the sink's 2^(z - m)).  Latency bounds
+// it: the references of up to eight partials are read at once, then their channels.
 __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ qpair,
                                                       const int32_t* __restrict__ totals,
-                                                      const float4* __restrict__ part_o,
-                                                      const float2* __restrict__ part_ml, AttnExtras ex,
+                                                      const uint4* __restrict__ part_o,
+                                                      const float2* __restrict__ part_ml,
+                                                      const float* __restrict__ sink, const float2* __restrict__ turn,
                                                       void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
   ptx::griddep_wait();
   const int b = blockIdx.x, t = threadIdx.x, h = t & 63, half = t >> 6;
@@ -860,53 +968,66 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
   const int clusters = (int)min((long long)kClusters, total);
   const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * clusters + total - 1) / total) - 1 : 0;
   const int k1 = s1 > s0 ? (int)((s1 * (long long)clusters + total - 1) / total) : 0;
-  const float z2 = ex.sink ? ex.sink[h] * kLog2e : -INFINITY;
-  float ref = z2;
-  for (int c = k0; c < k1; ++c) {
-    const float2 ml = part_ml[((int64_t)(p + c) * 2 + r) * kHAtt + h];
-    if (ml.y > 0.0f) ref = fmaxf(ref, ml.x);
-  }
-  float L = ref > -INFINITY && ex.sink ? ptx::ex2(z2 - ref) : 0.0f;
-  float4 acc[8];
+  const float z2 = sink ? sink[h] * kLog2e : -INFINITY;
+  constexpr int kN = 8;
+  float ref = z2, L = sink && z2 > -INFINITY ? 1.0f : 0.0f;
+  float acc[32];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = k0; c < k1; ++c) {
-    const int64_t slot = (int64_t)(p + c) * 2 + r;
-    const float2 ml = part_ml[slot * kHAtt + h];
-    if (!(ml.y > 0.0f)) continue;
-    const float f = ptx::ex2(ml.x - ref);
-    L = fmaf(f, ml.y, L);
-    const float4* po = part_o + (slot * 64 + blockIdx.y * 8) * 128 + t;
+  for (int u = 0; u < 32; ++u) acc[u] = 0.0f;
+  for (int c0 = k0; c0 < k1; c0 += kN) {
+    float2 ml[kN];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float4 v = po[u * 128];
-      acc[u].x = fmaf(f, v.x, acc[u].x);
-      acc[u].y = fmaf(f, v.y, acc[u].y);
-      acc[u].z = fmaf(f, v.z, acc[u].z);
-      acc[u].w = fmaf(f, v.w, acc[u].w);
+    for (int i = 0; i < kN; ++i)
+      ml[i] = c0 + i < k1 ? part_ml[((int64_t)(p + c0 + i) * 2 + r) * kHAtt + h] : make_float2(-INFINITY, 0.0f);
+    float top = ref;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (ml[i].y > 0.0f) top = fmaxf(top, ml[i].x);
+    if (top > ref) {
+      const float f = ref > -INFINITY ? ptx::ex2(ref - top) : 0.0f;
+      L *= f;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) acc[u] *= f;
+      ref = top;
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (c0 + i >= k1) break;
+      const uint4* po = part_o + (((int64_t)(p + c0 + i) * 2 + r) * 32 + blockIdx.y * 4) * 128 + t;
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = po[u * 128];
+      if (!(ml[i].y > 0.0f)) continue;
+      const float f = ptx::ex2(ml[i].x - ref) * ml[i].y;
+      L += f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          acc[8 * u + 2 * j] = fmaf(f, x.x, acc[8 * u + 2 * j]);
+          acc[8 * u + 2 * j + 1] = fmaf(f, x.y, acc[8 * u + 2 * j + 1]);
+        }
+      }
     }
   }
   const float inv = L > 0.0f ? 1.0f / L : 0.0f;
   const int c0 = 256 * half + 32 * blockIdx.y;
-  if (ex.rope && c0 >= kRopeFirst) {  // turn back by -q_pos
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      float cs, sn;
-      rope_cos_sin(ex.th.t[(c0 - kRopeFirst) / 2 + 2 * u], (double)ex.qpos[b], cs, sn);
-      rope_pair(acc[u].x, acc[u].y, cs, -sn);
-      rope_cos_sin(ex.th.t[(c0 - kRopeFirst) / 2 + 2 * u + 1], (double)ex.qpos[b], cs, sn);
-      rope_pair(acc[u].z, acc[u].w, cs, -sn);
-    }
+  for (int u = 0; u < 32; ++u) acc[u] *= inv;
+  if (turn && c0 >= kRopeFirst) {  // turn back by -q_pos
+    const float2* cs = turn + (int64_t)b * 32 + (c0 - kRopeFirst) / 2;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) rope_pair(acc[2 * u], acc[2 * u + 1], cs[u].x, -cs[u].y);
   }
   const int64_t row = ((int64_t)b * kHAtt + h) * kDMain + c0;
   if (out_bf16) {
     uint32_t w[16];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[u].x * inv, acc[u].y * inv);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[u].z * inv, acc[u].w * inv);
-      w[2 * u] = *reinterpret_cast<const uint32_t*>(&lo);
-      w[2 * u + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    for (int u = 0; u < 16; ++u) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * u], acc[2 * u + 1]);
+      w[u] = *reinterpret_cast<const uint32_t*>(&v);
     }
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row);
 #pragma unroll
@@ -914,7 +1035,7 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
   } else {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) o[u] = make_float4(acc[u].x * inv, acc[u].y * inv, acc[u].z * inv, acc[u].w * inv);
+    for (int u = 0; u < 8; ++u) o[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
   }
   if (lse && blockIdx.y == 0 && half == 0)
     lse[b * kHAtt + h] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
@@ -923,9 +1044,11 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
 struct PrefixWs {
   Pair* pairs;
   int32_t *gpair, *qpair, *cpair, *totals, *gimage;
-  uint16_t* image;
+  uint16_t *image, *qimage;
+  float* c2;
+  float2* turn;
   int64_t image_cap;
-  float4* part_o;
+  uint4* part_o;
   float2* part_ml;
   size_t bytes;
 };
@@ -945,9 +1068,12 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.qpair = (int32_t*)take((size_t)B * 4);
   L.cpair = (int32_t*)take(kClusters * 4);
-  L.totals = (int32_t*)take(12);
-  L.gimage = (int32_t*)take(((size_t)G + 1) * 4);
-  L.part_o = (float4*)take(slots * 2 * kHAtt * kDMain * 4);
+  L.totals = (int32_t*)take(8);
+  L.gimage = (int32_t*)take((size_t)G * 4);
+  L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
+  L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
+  L.turn = (float2*)take((size_t)B * 32 * 8);
+  L.part_o = (uint4*)take(slots * 2 * kHAtt * kDMain * 2);
   L.part_ml = (float2*)take(slots * 2 * kHAtt * 8);
   const int64_t groups = B / kImageQueries < G ? B / kImageQueries : G;
   L.image_cap = groups * cdiv(shared_max, kChunk);
@@ -1028,34 +1154,36 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals,
                      L.gimage, L.image_cap, ws};
-  {
-    KernelTimer timer("k_prefix_plan", st);
-    launch_pdl(k_prefix_plan, dim3(1), dim3(kPlanThreads), 0, st, a);
-  }
-  auto kern = ex.qnorm_w || ex.rope ? k_prefix_attn<true> : k_prefix_attn<false>;
-  const size_t smem = sizeof(PrefixSmem);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return launch_status();
-  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, (const uint16_t*)q_bf16, pages->table,
-                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa,
-                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, softmax_scale, ex,
+  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
+                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
+                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
                        L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
+  const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
+                       L.qimage, L.c2, L.turn};
   ImageMaps maps{};
-  if (L.image_cap > 0) {
-    if (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32))
-      return CSA2_ERR_CUDA;
-    KernelTimer timer("k_prefix_widen", st);
-    launch_pdl(k_prefix_widen, dim3(2 * 152), dim3(kWidenThreads), 0, st, a, k, L.image);
+  if (L.image_cap > 0 &&
+      (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
+    return CSA2_ERR_CUDA;
+  constexpr int prep_smem = kDMain / 8 * kQPad;
+  const size_t smem = sizeof(PrefixSmem);
+  if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem) != cudaSuccess ||
+      cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return launch_status();
+  {
+    KernelTimer timer("k_prefix_prep", st);
+    const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
+    launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)prep_smem, st, a, pq, k,
+               L.image);
   }
   {
     KernelTimer timer("k_prefix_attn", st);
-    launch_pairs(kern, kClusters, smem, st, k, maps);
+    launch_pairs(k_prefix_attn, kClusters, smem, st, k, maps);
   }
   {
     KernelTimer timer("k_prefix_merge", st);
     launch_pdl(k_prefix_merge, dim3(B, 8), dim3(128), 0, st, (const Pair*)L.pairs, (const int32_t*)L.qpair,
-               (const int32_t*)L.totals, (const float4*)L.part_o, (const float2*)L.part_ml, ex, out,
-               out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+               (const int32_t*)L.totals, (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
+               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
   }
   return launch_status();
 }
