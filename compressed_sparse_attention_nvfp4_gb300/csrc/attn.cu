@@ -818,24 +818,3 @@ bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
   return n <= (int64_t)p->max_pages * kv->seq_stride;
 }
 }  // namespace csa2
-
-extern "C" size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
-  if (B <= 0 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0) return 0;
-  return csa2::attn_ws_layout(nullptr, B, csa2::attn_plan(B, (int32_t)n_max, n_swa), true).bytes;
-}
-
-extern "C" csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
-                                              const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
-                                              int32_t n_swa, const void* q_bf16, float softmax_scale,
-                                              const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink,
-                                              const csa2_window* win, void* out, int32_t out_type, float* lse_out,
-                                              void* ws, size_t ws_bytes, csa2_stream stream) {
-  using namespace csa2;
-  if (!planes_ok(kv) || B <= 0 || B > 65535 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0 ||
-      n_swa > CSA2_MAX_SWA || !pages_ok(pages, kv, n_max))
-    return CSA2_ERR_INVALID_ARG;
-  if (!n_entries || !aligned(n_entries, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
-  if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, pages, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
-                  q_pos, sink, win, out, out_type, lse_out, ws, ws_bytes, (cudaStream_t)stream);
-}

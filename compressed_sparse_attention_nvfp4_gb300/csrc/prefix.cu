@@ -40,6 +40,7 @@ struct Pair {
   int32_t ns;
   int32_t vis0, vis1;
   int32_t own0, own1;
+  int32_t paired;  // own chunks that hold 64 rows of each query; behind them 128 of the longer one's
   int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
   int32_t nshared; // shared chunks; own chunks follow
   int32_t image;   // the shared entries' first chunk in the image, or -1
@@ -181,7 +182,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
         const int c = visible(a, q);
         int own = max(c - x.ns, 0);
         if (own > a.own_max) {
-          report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);
+          if (a.G > 0) report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);  // without groups: n_max
           own = a.own_max;
         }
         (i ? x.vis1 : x.vis0) = min(x.ns, c);
@@ -189,8 +190,9 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
         a.qpair[q] = 2 * p + i;
       }
       x.nshared = (max(x.vis0, x.vis1) + kChunk - 1) / kChunk;
-      const int own = max(x.own0, x.own1) + a.n_swa;
-      n = x.nshared + (x.q1 >= 0 ? (own + kOwnChunk - 1) / kOwnChunk : (own + kChunk - 1) / kChunk);
+      x.paired = x.q1 >= 0 ? (min(x.own0, x.own1) + a.n_swa + kOwnChunk - 1) / kOwnChunk : 0;
+      const int alone = max(x.own0, x.own1) + a.n_swa - x.paired * kOwnChunk;
+      n = x.nshared + x.paired + (max(alone, 0) + kChunk - 1) / kChunk;
     }
     int total;
     x.chunk0 = chunks + block_scan(n, s_warp, &total);
@@ -219,8 +221,8 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
 // ------------------------------------------------------------------ attention
 
 // warps 0-3: softmax, rescaling of O, epilogue; 4-11: rows of S's operand; 12-19: rows of O's; then one
-// warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), row masks
-constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kMaskWarp = 22;
+// warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), where rows come from
+constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kIndexWarp = 22;
 constexpr int kThreads = 24 * 32;  // and one that fills the last warpgroup
 // registers of a thread: 80 at launch, which the row warpgroups keep; the softmax takes what the last
 // warpgroup gives back
@@ -236,15 +238,14 @@ struct __align__(1024) PrefixSmem {
   uint16_t xs[kDMain / 8][kOwnChunk * 8];   // this CTA's 64 rows for S [c/8][row][c%8]
   uint16_t xo[4][kDMain / 16][32 * 8];      // this CTA's 256 channels of all 128 rows [row/32][c/8][row%32][c%8]
   uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
-  float c2[4][kHAtt];                       // by item: later ones are staged before this one's softmax
   float red[2][kHAtt];
-  uint32_t vmask[2][4];                     // per S buffer: rows that exist
-  Pair pair[kThreads / 32];                 // each warp's copy of its item's pair: not held in registers
+  int32_t rows[4][kChunk];                  // where a chunk's rows come from, up to four chunks ahead
   // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
   // of the same role passes on for all of that CTA's
-  uint64_t q_land[4], q_peer;               // q' and c2 copied (by item); the odd CTA's q'
+  uint64_t q_land, q_peer;                  // q' copied; the odd CTA's q'
+  uint64_t r_full[4], r_free[4];            // rows written (one warp); read (16 row and 4 softmax warps)
   uint64_t x_full[2][kPieces], x_free[2][kPieces];  // [0] S's operand, [1] O's
-  uint64_t s_full[2], p_full[2], p_free[2], m_full[2];
+  uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_read;                          // epilogue done with O
   uint64_t drained;                         // every MMA issued complete (two warps)
   uint32_t tmem_base;
@@ -289,12 +290,14 @@ __device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x,
     e = jc * kChunk + i;
     if (e >= x.ns) return RowRef{0, kNoRow};
   } else {
-    int idx, h = 0;
-    if (x.q1 < 0) {
-      idx = (jc - x.nshared) * kChunk + i;
-    } else {
+    const int jo = jc - x.nshared;
+    int idx, h;
+    if (jo < x.paired) {
       h = i / kOwnChunk;
-      idx = (jc - x.nshared) * kOwnChunk + i % kOwnChunk;
+      idx = jo * kOwnChunk + i % kOwnChunk;
+    } else {
+      h = x.own1 > x.own0;
+      idx = x.paired * kOwnChunk + (jo - x.paired) * kChunk + i;
     }
     q = h ? x.q1 : x.q0;
     const int own = h ? x.own1 : x.own0;
@@ -400,11 +403,12 @@ __device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float
 // handed over by 128 channels: row 8 w + l % 8, block (of 32 channels) 4 i + l / 8 in piece i.  Operand 1
 // (O's): its 256 channels of all rows, by 32 rows: row 32 i + 8 (w % 4) + l % 8, block 4 (w / 4 % 2) + l / 8
 // of its eight in piece i.  Either way a load reads 64 contiguous bytes of eight rows, and a store writes
-// eight rows of a plane: no bank conflicts.  A step writes one piece; a row's codes are fetched two
-// steps ahead, its page four.  Both operands run the same code: the kernel's loops have to fit the
-// instruction cache (unrolled by piece and operand they waited more for instructions than for data).
-__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, const Pair& x,
-                                          int rank, int c0, int nc, int w, int lane, uint32_t n, uint32_t item) {
+// eight rows of a plane: no bank conflicts.  A step writes one piece; its codes are fetched two steps ahead.
+// Both operands run the same code: the kernel's loops have to fit the instruction cache (unrolled by piece
+// and operand they waited more for instructions than for data).
+__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int image,
+                                          int nshared, int64_t q, int rank, int c0, int nc, int w, int lane, uint32_t n,
+                                          uint32_t item) {
   const int op = w >> 3, cb = lane >> 3;
   const int rl = 8 * (op ? w & 3 : w) + (lane & 7);
   const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0;
@@ -414,39 +418,38 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   constexpr int dst_step = 16 * 1024 / 2;  // a piece
   const int steps = nc * kPieces;
   // steps whose chunks are copied from the image, by the first warp of each operand
-  const int image_steps = x.image >= 0 ? min(max(x.nshared - c0, 0) * kPieces, steps) : 0;
+  const int image_steps = image >= 0 ? min(max(nshared - c0, 0) * kPieces, steps) : 0;
   int ra, rb;
   Fetch fa, fb;
-  RowRef na, nb;
   int issued = -1;  // last step copied from the image
-  auto find = [&](RowRef& nx, int st) {
-    if (st >= image_steps && st < steps) nx = find_row(k, x, c0 + (st >> 2), row0 + row_step * (st & 3));
-  };
-  auto load = [&](Fetch& f, int& r, RowRef& nx, int st) {  // fetch step st, find step st + 2
-    if (st >= image_steps && st < steps) {
-      r = resolve(k, nx, false);
+  bool good = true;
+  auto load = [&](Fetch& f, int& r, int st) {  // this thread's row and codes of step st
+    if (st >= steps) return;
+    const uint32_t m = n + (uint32_t)(st >> 2), slot = m & 3u;
+    if ((st & 3) == 0)
+      good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) return;
+    if (st >= image_steps) {
+      r = S.rows[slot][row0 + row_step * (st & 3)];
       fetch(f, k, r, blk0 + blk_step * (st & 3));
     }
-    find(nx, st + 2);
+    if ((st & 3) == kPieces - 1) {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
+    }
   };
-  find(na, 0);
-  find(nb, 1);
-  load(fa, ra, na, 0);
-  load(fb, rb, nb, 1);
-  bool good = true;
   if (w == 0) {  // the item's query, once S of the item before has left q'
     good = n == 0 || ptx::mbar_wait_warp(&S.x_free[0][kPieces - 1], (n - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (good && lane == 0) {
-      const int64_t q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
-      uint64_t* bar = &S.q_land[item & 3u];
-      ptx::mbar_arrive_expect_tx(bar, kHAtt * kDMain * 2 + kHAtt * 4);
-      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, bar);
-      ptx::bulk_g2s(&S.c2[item & 3u][0], k.c2 + q * kHAtt, kHAtt * 4, bar);
+      ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
+      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
     }
     __syncwarp();
   }
   const bool copied = w == 0 && good;
-  auto step = [&](Fetch& f, int& r, RowRef& nx, int st) {
+  load(fa, ra, 0);
+  load(fb, rb, 1);
+  auto step = [&](Fetch& f, int& r, int st) {
     const uint32_t m = n + (uint32_t)(st >> 2);
     const int i = st & 3;
     if (m > 0) good = good && ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
@@ -456,7 +459,7 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
       if ((w & 7) != 0) {
         if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
       } else if (lane == 0) {
-        const int plane0 = (x.image + c0 + (st >> 2)) * (kDMain / 8);
+        const int plane0 = (image + c0 + (st >> 2)) * (kDMain / 8);
         ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
         if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
         else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
@@ -469,42 +472,46 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
     }
-    load(f, r, nx, st + 2);
+    load(f, r, st + 2);
   };
 #pragma unroll 1
   for (int st = 0; st < steps && good; st += 2) {
-    step(fa, ra, na, st);
-    step(fb, rb, nb, st + 1);
+    step(fa, ra, st);
+    step(fb, rb, st + 1);
   }
   if (!good && (w & 7) == 0) {  // copies in flight write shared memory: they land before anyone leaves
     volatile int keep_waiting = 0;
-    if (copied) ptx::mbar_wait_warp(&S.q_land[item & 3u], (item >> 2) & 1u, &keep_waiting, kWaitBudget);
+    if (copied) ptx::mbar_wait_warp(&S.q_land, item & 1u, &keep_waiting, kWaitBudget);
     for (int st = issued; st >= 0 && st > issued - kPieces; --st)
       ptx::mbar_wait_warp(&S.x_full[op][st & 3], (n + (uint32_t)(st >> 2)) & 1u, &keep_waiting, kWaitBudget);
   }
   return good;
 }
 
-// Which rows of each chunk exist, by one warp (lane l rows l, 32 + l, ..), into the S buffers' masks: a
-// buffer's mask may be written once the softmax of its last chunk has handed P over.  Pages outside the
-// planes are reported here.
-__device__ __forceinline__ bool mask_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, bool report, int c0,
-                                          int nc, int lane, uint32_t n) {
+// Where each chunk's rows come from, by one warp (lane l rows l, 32 + l, ..) up to four chunks ahead of the
+// row and softmax warps.  Pages outside the planes are reported here.
+__device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, bool report, int c0,
+                                           int nc, int lane, uint32_t n) {
   bool good = true;
-#pragma unroll 1
-  for (int j = 0; j < nc && good; ++j) {
-    const uint32_t m = n + (uint32_t)j;
-    RowRef r[4];
+  RowRef r[4];
+  auto find = [&](int j) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = find_row(k, x, c0 + j, 32 * i + lane);
-    if (m >= 2) good = ptx::mbar_wait_warp(&S.p_full[m & 1], ((m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
+  };
+  find(0);
+#pragma unroll 1
+  for (int j = 0; j < nc && good; ++j) {
+    const uint32_t m = n + (uint32_t)j, slot = m & 3u;
+    int row[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = __ballot_sync(0xffffffffu, resolve(k, r[i], report) != kNoRow);
-      if (good && lane == i) S.vmask[m & 1][i] = v;
-    }
+    for (int i = 0; i < 4; ++i) row[i] = resolve(k, r[i], report);
+    if (j + 1 < nc) find(j + 1);
+    if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) break;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S.rows[slot][32 * i + lane] = row[i];
     __syncwarp();
-    if (good && lane == 0) ptx::mbar_arrive(&S.m_full[m & 1]);
+    if (lane == 0) ptx::mbar_arrive(&S.r_full[slot]);
   }
   return good;
 }
@@ -526,12 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         ptx::mbar_init(&S.x_full[0][0] + i, 8 + peer);
         ptx::mbar_init(&S.x_free[0][0] + i, 1);
       }
-      for (int i = 0; i < 4; ++i) ptx::mbar_init(&S.q_land[i], 1);
+      ptx::mbar_init(&S.q_land, 1);
+      for (int i = 0; i < 4; ++i) {
+        ptx::mbar_init(&S.r_full[i], 1);
+        ptx::mbar_init(&S.r_free[i], 20);
+      }
       for (int i = 0; i < 2; ++i) {
         ptx::mbar_init(&S.s_full[i], 1);
         ptx::mbar_init(&S.p_full[i], 4 + peer);
         ptx::mbar_init(&S.p_free[i], 1);
-        ptx::mbar_init(&S.m_full[i], 1);
       }
       ptx::mbar_init(&S.o_read, 4 + peer);
       ptx::mbar_init(&S.drained, 2);
@@ -562,11 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     uint32_t n = 0, items = 0;
     for (int t = t0; t < t1 && good; ++p) {
       const int pend = k.pairs[p + 1].chunk0;
-      __syncwarp();
-      if (lane < (int)(sizeof(Pair) / 4))
-        reinterpret_cast<int32_t*>(&S.pair[warp])[lane] = reinterpret_cast<const int32_t*>(k.pairs + p)[lane];
-      __syncwarp();
-      const Pair& x = S.pair[warp];
+      const Pair x = k.pairs[p];
       const int c0 = t - x.chunk0, nc = min(pend, t1) - t;
       if (nc <= 0) continue;  // a pair without chunks
       t += nc;
@@ -578,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 
   if (warp >= kRowWarp && warp < kSMma) {
     for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
-      good = rows_role(S, k, maps, x, rank, c0, nc, warp - kRowWarp, lane, n, items);
+      const int q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
+      good = rows_role(S, k, maps, x.image, x.nshared, q, rank, c0, nc, warp - kRowWarp, lane, n, items);
     });
     where = 31;
   } else if (warp >= kSMma) {
@@ -590,9 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       ptx::tc_fence_before();
       if (good && lane == 0) ptx::mbar_arrive_peer(bar, 0);
     };
-    if (warp == kMaskWarp) {
+    if (warp == kIndexWarp) {
       for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
-        good = mask_role(S, k, x, rank == 0, c0, nc, lane, n);
+        good = index_role(S, k, x, rank == 0, c0, nc, lane, n);
       });
       where = 32;
     } else if (warp == kSMma) {
@@ -601,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
       for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
-        good = wait(&S.q_land[items & 3u], items >> 2);
+        good = wait(&S.q_land, items);
         if (rank == 0) good = good && wait(&S.q_peer, items);
         else if (good && lane == 0) ptx::mbar_arrive_peer(&S.q_peer, 0);
 #pragma unroll 1
@@ -678,12 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t items) {
       const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
       float m2 = -INFINITY, lsum = 0.0f;
-      good = wait(&S.q_land[items & 3u], items >> 2);
-      const float c2 = S.c2[items & 3u][h];
+      const float c2 = k.c2[(int64_t)(qme >= 0 ? qme : k.B) * kHAtt + h];
 #pragma unroll 1
       for (int j = 0; j < nc; ++j) {
         const uint32_t m = n + (uint32_t)j, slot = m & 1u;
-        good = good && wait(&S.m_full[slot], m >> 1) && wait(&S.s_full[slot], m >> 1);
+        good = good && wait(&S.r_full[m & 3u], m >> 2) && wait(&S.s_full[slot], m >> 1);
         if (good && m >= 2) good = wait(&S.p_free[slot], (m >> 1) - 1);
         ptx::tc_fence_after();
         uint32_t mk0 = 0u, mk1 = 0u;
@@ -691,11 +697,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
           const int left = vis - (c0 + j) * kChunk - 64 * half;
           mk0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
           mk1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1u : 0u;
-        } else if (x.q1 < 0 ? rank == 0 : half == rank) {
+        } else if (c0 + j - x.nshared < x.paired ? half == rank : (x.own1 > x.own0) == (rank == 1)) {
           mk0 = mk1 = ~0u;
         }
-        mk0 &= S.vmask[slot][2 * half];
-        mk1 &= S.vmask[slot][2 * half + 1];
+        mk0 &= __ballot_sync(0xffffffffu, S.rows[m & 3u][64 * half + lane] != kNoRow);
+        mk1 &= __ballot_sync(0xffffffffu, S.rows[m & 3u][64 * half + 32 + lane] != kNoRow);
+        if (good && lane == 0) ptx::mbar_arrive(&S.r_free[m & 3u]);
         // P with the reference so far (0 before the first row); it stands unless some head's logits
         // exceed it by too much, then once more with that head's new reference
         float alpha = 1.0f, sum, ref = m2 == -INFINITY ? 0.0f : m2;
@@ -1126,20 +1133,16 @@ extern "C" size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t 
   return csa2::prefix_ws(nullptr, B, G, n_shared_max).bytes;
 }
 
-extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
-                                               const int32_t* n_entries, int32_t G, const int32_t* group_start,
-                                               const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
-                                               const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16,
-                                               float softmax_scale, const csa2_norm_rope* q_nr, const int64_t* q_pos,
-                                               const float* sink, const csa2_window* win, void* out, int32_t out_type,
-                                               float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
-  using namespace csa2;
-  if (!planes_ok(kv) || B <= 0 || B > 65535 || G <= 0 || G > B || n_shared_max < 0 || n_own_max < 0 ||
-      n_shared_max > CSA2_MAX_DENSE || n_own_max > CSA2_MAX_DENSE || n_swa < 0 || n_swa > CSA2_MAX_SWA ||
-      !pages_ok(pages, kv, n_shared_max) || !pages_ok(pages, kv, n_own_max))
-    return CSA2_ERR_INVALID_ARG;
-  if (!n_entries || !group_start || !n_shared || !aligned(n_entries, 4) || !aligned(group_start, 4) ||
-      !aligned(n_shared, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out || !aligned(q_bf16, 16) ||
+namespace csa2 {
+namespace {
+
+// Attention of B queries through page tables, G groups of them sharing prefixes (G = 0: none).
+csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B, const int32_t* n_entries, int32_t G,
+                       const int32_t* group_start, const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
+                       const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
+                       const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
+                       void* out, int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
+  if (!n_entries || !aligned(n_entries, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out || !aligned(q_bf16, 16) ||
       !aligned(out, 16) || (swa_e4m3 && !aligned(swa_e4m3, 16)) || (lse_out && !aligned(lse_out, 4)))
     return CSA2_ERR_INVALID_ARG;
   if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
@@ -1186,4 +1189,43 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
                ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
   }
   return launch_status();
+}
+
+}  // namespace
+}  // namespace csa2
+
+extern "C" size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
+  if (B <= 0 || B > 65535 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0) return 0;
+  return csa2::prefix_ws(nullptr, B, 0, 0).bytes;
+}
+
+extern "C" csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                              const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
+                                              int32_t n_swa, const void* q_bf16, float softmax_scale,
+                                              const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink,
+                                              const csa2_window* win, void* out, int32_t out_type, float* lse_out,
+                                              void* ws, size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (!planes_ok(kv) || B <= 0 || B > 65535 || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0 ||
+      n_swa > CSA2_MAX_SWA || !pages_ok(pages, kv, n_max))
+    return CSA2_ERR_INVALID_ARG;
+  return prefix_run(kv, pages, B, n_entries, 0, nullptr, nullptr, 0, n_max, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
+                    q_pos, sink, win, out, out_type, lse_out, ws, ws_bytes, stream);
+}
+
+extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
+                                               const int32_t* n_entries, int32_t G, const int32_t* group_start,
+                                               const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
+                                               const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16,
+                                               float softmax_scale, const csa2_norm_rope* q_nr, const int64_t* q_pos,
+                                               const float* sink, const csa2_window* win, void* out, int32_t out_type,
+                                               float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (!planes_ok(kv) || B <= 0 || B > 65535 || G <= 0 || G > B || n_shared_max < 0 || n_own_max < 0 ||
+      n_shared_max > CSA2_MAX_DENSE || n_own_max > CSA2_MAX_DENSE || n_swa < 0 || n_swa > CSA2_MAX_SWA ||
+      !pages_ok(pages, kv, n_shared_max) || !pages_ok(pages, kv, n_own_max))
+    return CSA2_ERR_INVALID_ARG;
+  if (!group_start || !n_shared || !aligned(group_start, 4) || !aligned(n_shared, 4)) return CSA2_ERR_INVALID_ARG;
+  return prefix_run(kv, pages, B, n_entries, G, group_start, n_shared, n_shared_max, n_own_max, swa_e4m3, n_swa, q_bf16,
+                    softmax_scale, q_nr, q_pos, sink, win, out, out_type, lse_out, ws, ws_bytes, stream);
 }
