@@ -399,41 +399,47 @@ __device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float
   return top;
 }
 
-// Chunks [c0, c0 + nc) of pair x by the 16 row warps.  Operand 0 (S's, warps 0-7): this CTA's 64 rows,
-// handed over by 128 channels: row 8 w + l % 8, block (of 32 channels) 4 i + l / 8 in piece i.  Operand 1
-// (O's): its 256 channels of all rows, by 32 rows: row 32 i + 8 (w % 4) + l % 8, block 4 (w / 4 % 2) + l / 8
-// of its eight in piece i.  Either way a load reads 64 contiguous bytes of eight rows, and a store writes
-// eight rows of a plane: no bank conflicts.  A step writes one piece; its codes are fetched two steps ahead.
-// Both operands run the same code: the kernel's loops have to fit the instruction cache (unrolled by piece
-// and operand they waited more for instructions than for data).
+// Chunks [c0, c0 + nc) of pair x by the 16 row warps: per operand two groups of four, which write every
+// other piece.  Operand 0 (S's, warps 0-7): this CTA's 64 rows, handed over by 128 channels: in piece i a
+// thread has block (of 32 channels) 4 i + l / 8 of rows 8 (w % 4) + l % 8 and 32 more.  Operand 1 (O's): its
+// 256 channels of all rows, by 32 rows: a thread has blocks l / 8 and l / 8 + 4 of its eight of row
+// 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64 contiguous bytes of eight rows, and a store writes
+// eight rows of a plane: no bank conflicts.  A step writes one piece and fetches the codes of the next (half
+// a chunk ahead).  Both operands run the same code: the kernel's loops have to fit the instruction cache
+// (unrolled by piece and operand they waited more for instructions than for data).
 __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int image,
                                           int nshared, int64_t q, int rank, int c0, int nc, int w, int lane, uint32_t n,
                                           uint32_t item) {
-  const int op = w >> 3, cb = lane >> 3;
-  const int rl = 8 * (op ? w & 3 : w) + (lane & 7);
-  const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0;
-  const int blk0 = op ? 8 * rank + 4 * ((w >> 2) & 1) + cb : cb, blk_step = op ? 0 : 4;
+  const int op = w >> 3, group = (w >> 2) & 1, cb = lane >> 3;
+  const int rl = 8 * (w & 3) + (lane & 7);
+  const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0, row_u = op ? 0 : 32;
+  const int blk0 = op ? 8 * rank + cb : cb, blk_step = op ? 0 : 4, blk_u = op ? 4 : 0;
   const int plane = (op ? 32 : kOwnChunk) * 8;  // f16 elements
-  uint16_t* const dst = (op ? &S.xo[0][4 * (4 * ((w >> 2) & 1) + cb)][0] : &S.xs[4 * cb][0]) + rl * 8;
+  uint16_t* const dst = (op ? &S.xo[0][4 * cb][0] : &S.xs[4 * cb][0]) + rl * 8;
   constexpr int dst_step = 16 * 1024 / 2;  // a piece
-  const int steps = nc * kPieces;
-  // steps whose chunks are copied from the image, by the first warp of each operand
-  const int image_steps = image >= 0 ? min(max(nshared - c0, 0) * kPieces, steps) : 0;
-  int ra, rb;
-  Fetch fa, fb;
+  const int dst_u = op ? 16 * 32 * 8 : 32 * 8;
+  const int steps = nc * 2;  // step st: chunk st / 2, piece 2 (st % 2) + group
+  // steps whose chunks are copied from the image, by the first warp of each group
+  const int image_steps = image >= 0 ? min(max(nshared - c0, 0) * 2, steps) : 0;
+  int r[2];
+  Fetch f[2];
   int issued = -1;  // last step copied from the image
   bool good = true;
-  auto load = [&](Fetch& f, int& r, int st) {  // this thread's row and codes of step st
+  auto load = [&](int st) {  // this thread's rows and codes of step st
     if (st >= steps) return;
-    const uint32_t m = n + (uint32_t)(st >> 2), slot = m & 3u;
-    if ((st & 3) == 0)
+    const uint32_t m = n + (uint32_t)(st >> 1), slot = m & 3u;
+    const int i = 2 * (st & 1) + group;
+    if ((st & 1) == 0)
       good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     if (st >= image_steps) {
-      r = S.rows[slot][row0 + row_step * (st & 3)];
-      fetch(f, k, r, blk0 + blk_step * (st & 3));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        r[u] = S.rows[slot][row0 + row_step * i + row_u * u];
+        fetch(f[u], k, r[u], blk0 + blk_step * i + blk_u * u);
+      }
     }
-    if ((st & 3) == kPieces - 1) {
+    if (st & 1) {
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
     }
@@ -447,19 +453,19 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
     __syncwarp();
   }
   const bool copied = w == 0 && good;
-  load(fa, ra, 0);
-  load(fb, rb, 1);
-  auto step = [&](Fetch& f, int& r, int st) {
-    const uint32_t m = n + (uint32_t)(st >> 2);
-    const int i = st & 3;
-    if (m > 0) good = good && ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
-    if (!good) return;
+  load(0);
+#pragma unroll 1
+  for (int st = 0; st < steps && good; ++st) {
+    const uint32_t m = n + (uint32_t)(st >> 1);
+    const int i = 2 * (st & 1) + group;
+    if (m > 0) good = ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) break;
     if (st < image_steps) {
       // every warp arrives, also those that copy nothing: none may miss a phase of x_free
-      if ((w & 7) != 0) {
+      if ((w & 3) != 0) {
         if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
       } else if (lane == 0) {
-        const int plane0 = (image + c0 + (st >> 2)) * (kDMain / 8);
+        const int plane0 = (image + c0 + (st >> 1)) * (kDMain / 8);
         ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
         if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
         else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
@@ -467,23 +473,20 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
       issued = st;
       __syncwarp();
     } else {
-      put(f, r, dst + i * dst_step, plane);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) put(f[u], r[u], dst + i * dst_step + u * dst_u, plane);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
     }
-    load(f, r, st + 2);
-  };
-#pragma unroll 1
-  for (int st = 0; st < steps && good; st += 2) {
-    step(fa, ra, st);
-    step(fb, rb, st + 1);
+    load(st + 1);
   }
-  if (!good && (w & 7) == 0) {  // copies in flight write shared memory: they land before anyone leaves
+  if (!good && (w & 3) == 0) {  // copies in flight write shared memory: they land before anyone leaves
     volatile int keep_waiting = 0;
     if (copied) ptx::mbar_wait_warp(&S.q_land, item & 1u, &keep_waiting, kWaitBudget);
-    for (int st = issued; st >= 0 && st > issued - kPieces; --st)
-      ptx::mbar_wait_warp(&S.x_full[op][st & 3], (n + (uint32_t)(st >> 2)) & 1u, &keep_waiting, kWaitBudget);
+    for (int st = issued; st >= 0 && st > issued - 2; --st)
+      ptx::mbar_wait_warp(&S.x_full[op][2 * (st & 1) + group], (n + (uint32_t)(st >> 1)) & 1u, &keep_waiting,
+                          kWaitBudget);
   }
   return good;
 }
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       const uint32_t peer = rank == 0 ? 1 : 0;
       ptx::mbar_init(&S.q_peer, 1);
       for (int i = 0; i < 2 * kPieces; ++i) {
-        ptx::mbar_init(&S.x_full[0][0] + i, 8 + peer);
+        ptx::mbar_init(&S.x_full[0][0] + i, 4 + peer);
         ptx::mbar_init(&S.x_free[0][0] + i, 1);
       }
       ptx::mbar_init(&S.q_land, 1);
