@@ -69,10 +69,11 @@ struct PrefixArgs {
   Pair* pairs;        // [pairs + 1], the last one holds the number of chunks
   int32_t* gpair;     // [G + 3] first pair of each range of queries
   int32_t* qpair;     // [B] pair * 2 + place
-  int32_t* cpair;     // [kClusters] pair of each cluster's first chunk
+  int32_t* cpair;     // [parts] pair of each part's first chunk
   int32_t* totals;    // pairs, chunks
   int32_t* gimage;    // [G] first image chunk of each group, or -1
   int64_t image_cap;  // chunks the image has room for
+  int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
   void* ws;
 };
 
@@ -115,6 +116,7 @@ __device__ __forceinline__ int image_chunks(const PrefixArgs& a, int g) {
   return (shared_of(a, g, first) + kChunk - 1) / kChunk;
 }
 
+template <bool kAloneQueries>
 __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_bad;
@@ -134,7 +136,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
   int base = 0;
-  for (int v0 = 0; v0 < R; v0 += kPrepThreads) {
+  for (int v0 = 0; !kAloneQueries && v0 < R; v0 += kPrepThreads) {
     const int v = v0 + tid;
     const int n = v < R ? (range_hi(v) - range_lo(v) + 1) / 2 : 0;
     int total;
@@ -143,7 +145,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     base += total;
   }
   if (tid == 0) a.gpair[R] = base;
-  const int np = base;
+  const int np = kAloneQueries ? a.B : base;
   // a group whose image would end beyond the room has none, and so do all behind it
   int images = 0;
   for (int g0 = 0; g0 < G; g0 += kPrepThreads) {
@@ -159,7 +161,12 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     const int p = p0 + tid;
     Pair x{};
     int n = 0;
-    if (p < np) {
+    if (kAloneQueries && p < np) {  // a query by itself, in chunks of kOwnChunk rows
+      x.q0 = p;
+      x.q1 = x.image = -1;
+      x.own0 = min(visible(a, p), a.own_max);
+      n = (x.own0 + a.n_swa + kOwnChunk - 1) / kOwnChunk;
+    } else if (p < np) {
       int lo = 0, hi = R;  // the range with gpair[v] <= p < gpair[v + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -182,7 +189,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
         const int c = visible(a, q);
         int own = max(c - x.ns, 0);
         if (own > a.own_max) {
-          if (a.G > 0) report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);  // without groups: n_max
+          report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[q]);
           own = a.own_max;
         }
         (i ? x.vis1 : x.vis0) = min(x.ns, c);
@@ -205,7 +212,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     a.totals[1] = chunks;
   }
   __syncthreads();
-  const int clusters = min(kClusters, chunks);
+  const int clusters = min(a.parts, chunks);
   for (int c = tid; c < clusters; c += kPrepThreads) {  // the pair of chunk floor(chunks * c / clusters)
     const int t = (int)((long long)chunks * c / clusters);
     int lo = 0, hi = np;
@@ -283,35 +290,34 @@ constexpr int kNoRow = -1;
 struct RowRef {
   int page, off;
 };
-__device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x, int jc, int i) {
-  int q, e;
-  if (jc < x.nshared) {
-    q = x.first;
-    e = jc * kChunk + i;
-    if (e >= x.ns) return RowRef{0, kNoRow};
-  } else {
-    const int jo = jc - x.nshared;
-    int idx, h;
-    if (jo < x.paired) {
-      h = i / kOwnChunk;
-      idx = jo * kOwnChunk + i % kOwnChunk;
-    } else {
-      h = x.own1 > x.own0;
-      idx = x.paired * kOwnChunk + (jo - x.paired) * kChunk + i;
-    }
-    q = h ? x.q1 : x.q0;
-    const int own = h ? x.own1 : x.own0;
-    if (idx >= own) {
-      idx -= own;
-      if (idx >= k.n_swa) return RowRef{0, kNoRow};
-      const int w = q * k.n_swa + idx;
-      if (k.win_pos && __ldg(k.win_pos + w) < max(__ldg(k.win_lo + q), (int64_t)0)) return RowRef{0, kNoRow};
-      return RowRef{0, kNoRow - 1 - w};
-    }
-    e = x.ns + idx;
-  }
+__device__ __forceinline__ RowRef find_entry(const PrefixKernel& k, int q, int e) {
   const int pi = (int)((uint64_t)e * k.page_div >> 40);
   return RowRef{__ldg(k.table + q * k.max_pages + pi), e - pi * k.page_entries};
+}
+// row idx of query q's own: entries e0 .. e0 + own - 1, then its window
+__device__ __forceinline__ RowRef find_own(const PrefixKernel& k, int q, int own, int idx, int e0 = 0) {
+  if (idx < own) return find_entry(k, q, e0 + idx);
+  idx -= own;
+  if (idx >= k.n_swa) return RowRef{0, kNoRow};
+  const int w = q * k.n_swa + idx;
+  if (k.win_pos && __ldg(k.win_pos + w) < max(__ldg(k.win_lo + q), (int64_t)0)) return RowRef{0, kNoRow};
+  return RowRef{0, kNoRow - 1 - w};
+}
+__device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x, int jc, int i) {
+  if (jc < x.nshared) {
+    const int e = jc * kChunk + i;
+    return e < x.ns ? find_entry(k, x.first, e) : RowRef{0, kNoRow};
+  }
+  const int jo = jc - x.nshared;
+  int idx, h;
+  if (jo < x.paired) {
+    h = i / kOwnChunk;
+    idx = jo * kOwnChunk + i % kOwnChunk;
+  } else {
+    h = x.own1 > x.own0;
+    idx = x.paired * kOwnChunk + (jo - x.paired) * kChunk + i;
+  }
+  return find_own(k, h ? x.q1 : x.q0, h ? x.own1 : x.own0, idx, x.ns);
 }
 // a page outside the planes is skipped, and reported by the warp that is told to
 __device__ __forceinline__ int resolve(const PrefixKernel& k, RowRef r, bool report) {
@@ -954,7 +960,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, Pref
   extern __shared__ __align__(16) unsigned char prep_smem[];
   ptx::griddep_wait();
   const int64_t b = (int64_t)blockIdx.x - 1;
-  if (b < 0) plan_block(a);
+  if (b < 0) {
+    if (a.G > 0) plan_block<false>(a);
+    else plan_block<true>(a);
+  }
   else if (b <= a.B) stage_block(q, a.B, (int)b, prep_smem);
   else widen_chunks(a, k, image, (int)(b - a.B - 1), (int)(gridDim.x - a.B - 2));
 }
@@ -1051,6 +1060,470 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ p
     lse[b * kHAtt + h] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
 }
 
+// ------------------------------------------------------------ queries alone
+
+// Queries that share nothing run one to a CTA (a pair of them in one MMA would multiply each one's rows by
+// the other's probabilities): 64 heads, chunks of 64 rows in two slots, every row widened once.
+//   S[64 x 64] = q' X^T    heads as M; two accumulators over the channel halves, which the softmax adds;
+//   O^T[512 x 64] += X^T P^T  four tiles of 128 channels, so that the rows serve both products as they are.
+// Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 64 KB of rows and 8 KB of P
+// written, 296 KB = 2,300 cycles at 128 bytes a cycle; the MMAs alone (S at the half rate of M = 64) take
+// 1,800.  All queries' chunks form one list that kAlone CTAs share evenly, and a query cut between them
+// leaves partials, as above.
+constexpr int kAlone = 152;
+constexpr int kRows = 64;  // rows of a chunk
+constexpr int kRing = 8;   // chunks whose rows are found ahead
+
+struct __align__(1024) AloneSmem {
+  uint16_t x[2][kDMain / 8][kRows * 8];  // rows [c/8][row][c%8]
+  uint16_t q[kDMain / 8][kQPlane];       // q' [c/8][head][c%8]
+  uint16_t p[2][kRows / 8][kHAtt * 8];   // probabilities [row/8][head][row%8]
+  float alpha[kHAtt];                    // factor of O when a head's reference moved; at the end 1 / l
+  int32_t rows[kRing][kRows];
+  uint64_t q_land;
+  uint64_t r_full[kRing], r_free[kRing];
+  uint64_t x_full[2][2], x_free[2][2];   // slot, channel half
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_read, drained;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(AloneSmem) <= 232448, "attention shared memory");
+
+// warps 0-3: softmax and epilogue; 4-19: rows (4-11 channels 0-255, 12-19 the others); then S MMAs of each
+// half, O MMAs, where rows come from
+constexpr int kAloneS = 20, kAloneO = 22, kAloneIndex = 23;
+constexpr int kAloneSoftRegs = 128, kAloneRowRegs = 72, kAloneMmaRegs = 64;
+static_assert(kAloneSoftRegs + 4 * kAloneRowRegs + kAloneMmaRegs <= 6 * 80, "registers of the launch");
+
+// The rows of chunks [c0, c0 + nc) of query x.q0: thread's row 8 (w % 8) + l % 8, blocks (of 32 channels)
+// 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
+__device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, int64_t q, int nc, int w, int lane,
+                                           uint32_t n, uint32_t item) {
+  const int half = w >> 3, rl = 8 * (w & 7) + (lane & 7), blk = 8 * half + (lane >> 3);
+  uint16_t* const dst = &S.x[0][4 * blk][rl * 8];
+  bool good = true;
+  int ra, rb;
+  Fetch fa[2], fb[2];
+  auto load = [&](Fetch (&f)[2], int& r, int j) {
+    if (j >= nc) return;
+    const uint32_t m = n + (uint32_t)j, slot = m % kRing;
+    good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m / kRing) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) return;
+    r = S.rows[slot][rl];
+    fetch(f[0], k, r, blk);
+    fetch(f[1], k, r, blk + 4);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
+  };
+  if (w == 0) {  // the item's query, once S of the item before has left q'
+    good = n == 0 ||
+           ptx::mbar_wait_warp(&S.s_full[(n - 1) & 1u], ((n - 1) >> 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (good && lane == 0) {
+      ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
+      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
+    }
+    __syncwarp();
+  }
+  const bool copied = w == 0 && good;
+  load(fa, ra, 0);
+  load(fb, rb, 1);
+  auto step = [&](Fetch (&f)[2], int& r, int j) {
+    if (j >= nc) return;
+    const uint32_t m = n + (uint32_t)j, slot = m & 1u;
+    if (m >= 2)
+      good = good && ptx::mbar_wait_warp(&S.x_free[slot][half], ((m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) return;
+    uint16_t* d = dst + slot * (kDMain * kRows);
+    put(f[0], r, d, kRows * 8);
+    put(f[1], r, d + 16 * kRows * 8, kRows * 8);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.x_full[slot][half]);
+    load(f, r, j + 2);
+  };
+#pragma unroll 1
+  for (int j = 0; j < nc && good; j += 2) {
+    step(fa, ra, j);
+    step(fb, rb, j + 1);
+  }
+  if (!good && copied) {  // the copy writes shared memory: it lands before anyone leaves
+    volatile int keep_waiting = 0;
+    ptx::mbar_wait_warp(&S.q_land, item & 1u, &keep_waiting, kWaitBudget);
+  }
+  return good;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ PrefixKernel k) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  AloneSmem& S = *reinterpret_cast<AloneSmem*>(smem_raw);
+  volatile int* abort_flag = &S.abort_flag;
+  const int cta = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (warp == kAloneS) {
+    if (lane == 0) {
+      ptx::mbar_init(&S.q_land, 1);
+      for (int i = 0; i < kRing; ++i) {
+        ptx::mbar_init(&S.r_full[i], 1);
+        ptx::mbar_init(&S.r_free[i], 20);
+      }
+      for (int i = 0; i < 2; ++i) {
+        for (int h = 0; h < 2; ++h) {
+          ptx::mbar_init(&S.x_full[i][h], 8);
+          ptx::mbar_init(&S.x_free[i][h], 1);
+        }
+        ptx::mbar_init(&S.s_full[i], 2);
+        ptx::mbar_init(&S.p_full[i], 4);
+      }
+      ptx::mbar_init(&S.o_read, 4);
+      ptx::mbar_init(&S.drained, 3);
+      S.abort_flag = 0;
+      ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    ptx::tmem_alloc(&S.tmem_base, kCols);
+  }
+  ptx::griddep_wait();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const int total = __ldg(k.totals + 1), ctas = min(kAlone, total);
+  const bool idle = cta >= ctas;
+  const int t0 = idle ? 0 : (int)((long long)total * cta / ctas);
+  const int t1 = idle ? 0 : (int)((long long)total * (cta + 1) / ctas);
+  auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
+  bool good = true;
+  int where = 0;
+  auto for_items = [&](auto body) {  // as in k_prefix_attn, over queries
+    int p = t0 < t1 ? __ldg(k.cpair + cta) : 0;
+    uint32_t n = 0, items = 0;
+    for (int t = t0; t < t1 && good; ++p) {
+      const int first = k.pairs[p].chunk0, nc = min(k.pairs[p + 1].chunk0, t1) - t, c0 = t - first;
+      if (nc <= 0) continue;
+      t += nc;
+      body(p, c0, nc, n, items);
+      n += (uint32_t)nc;
+      ++items;
+    }
+  };
+
+  if (warp >= 4 && warp < kAloneS) {
+    ptx::setmaxnreg_dec<kAloneRowRegs>();
+    for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
+      good = alone_rows(S, k, k.pairs[p].q0, nc, warp - 4, lane, n, items);
+    });
+    where = 41;
+  } else if (warp >= kAloneS) {
+    ptx::setmaxnreg_dec<kAloneMmaRegs>();
+    if (warp == kAloneIndex) {
+      for_items([&](int p, int c0, int nc, uint32_t n, uint32_t) {
+        const Pair x = k.pairs[p];
+        RowRef r[2];
+        auto find = [&](int j) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) r[i] = find_own(k, x.q0, x.own0, (c0 + j) * kRows + 32 * i + lane);
+        };
+        find(0);
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j, slot = m % kRing;
+          const int r0 = resolve(k, r[0], true), r1 = resolve(k, r[1], true);
+          if (j + 1 < nc) find(j + 1);
+          if (m >= kRing) good = wait(&S.r_free[slot], m / kRing - 1);
+          if (!good) break;
+          S.rows[slot][lane] = r0;
+          S.rows[slot][32 + lane] = r1;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&S.r_full[slot]);
+        }
+      });
+      where = 42;
+    } else if (warp < kAloneO) {
+      // ---- S of a channel half: 16 K steps
+      const int half = warp - kAloneS;
+      constexpr uint32_t idesc_s = ptx::idesc_f16(64, kRows, 0);
+      const uint64_t da = ptx::smem_desc_noswizzle(&S.q[32 * half][0], kQPlane * 2, 128);
+      const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][32 * half][0], kRows * 16, 128);
+      for_items([&](int, int, int nc, uint32_t n, uint32_t items) {
+        good = wait(&S.q_land, items);
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j, slot = m & 1u;
+          good = wait(&S.x_full[slot][half], m >> 1);  // O(m - 2) is done with the slot, so its softmax with S
+          if (!good) break;
+          ptx::tc_fence_after();
+          const uint32_t dst = tmem + kColS + 128u * (uint32_t)half + 64u * slot;
+          const uint64_t dbs = db + (uint64_t)slot * (kDMain * kRows * 2 / 16);
+#pragma unroll 8
+          for (int ks = 0; ks < 16; ++ks)
+            ptx::mma_f16_ss_elect(dst, da + (uint64_t)(ks * 128), dbs + (uint64_t)(ks * 128), idesc_s, ks > 0 ? 1u : 0u);
+          ptx::mma_commit_elect(&S.s_full[slot]);
+        }
+      });
+      where = 43;
+    } else {
+      // ---- O^T: per channel half two tiles of 128 channels, four K steps of 16 rows each
+      constexpr uint32_t idesc_o = ptx::idesc_f16(128, kHAtt, 0) | (1u << 15);  // A M-major
+      const uint64_t da = ptx::smem_desc_noswizzle(&S.x[0][0][0], 128, kRows * 16);
+      const uint64_t db = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
+      for_items([&](int, int, int nc, uint32_t n, uint32_t items) {
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j, slot = m & 1u;
+          good = wait(&S.p_full[slot], m >> 1);
+          if (good && j == 0 && items > 0) good = wait(&S.o_read, items - 1);
+          if (!good) break;
+          ptx::tc_fence_after();
+          const uint64_t das = da + (uint64_t)slot * (kDMain * kRows * 2 / 16);
+          const uint64_t dbs = db + (uint64_t)slot * (kRows * kHAtt * 2 / 16);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int ks = 0; ks < kRows / 16; ++ks)
+                ptx::mma_f16_ss_elect(tmem + 64u * (uint32_t)(2 * half + mt),
+                                      das + (uint64_t)(half * 2048 + mt * 1024 + ks * 16), dbs + (uint64_t)(ks * 128),
+                                      idesc_o, (j | ks) > 0 ? 1u : 0u);
+            ptx::mma_commit_elect(&S.x_free[slot][half]);
+          }
+        }
+      });
+      where = 44;
+    }
+  } else {
+    // ---- softmax: lane l of warp w head 16 w + l % 16, chunk rows 32 (l / 16) .. (the rows of an M = 64
+    // accumulator lie in lanes 0-15 of each quarter; two lanes share a head's columns)
+    ptx::setmaxnreg_inc<kAloneSoftRegs>();
+    const int rh = lane >> 4, h = 16 * warp + (lane & 15);
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
+      const int q = k.pairs[p].q0;
+      const float c2 = k.c2[(int64_t)q * kHAtt + h];
+      float m2 = -INFINITY, lsum = 0.0f;
+#pragma unroll 1
+      for (int j = 0; j < nc; ++j) {
+        const uint32_t m = n + (uint32_t)j, slot = m & 1u, ring = m % kRing;
+        good = good && wait(&S.r_full[ring], m / kRing) && wait(&S.s_full[slot], m >> 1);
+        ptx::tc_fence_after();
+        const uint32_t k0 = __ballot_sync(0xffffffffu, S.rows[ring][lane] != kNoRow);
+        const uint32_t k1 = __ballot_sync(0xffffffffu, S.rows[ring][32 + lane] != kNoRow);
+        if (good && lane == 0) ptx::mbar_arrive(&S.r_free[ring]);
+        const uint32_t mask = rh ? k1 : k0;
+        float alpha = 1.0f, sum = 0.0f, ref = m2 == -INFINITY ? 0.0f : m2;
+        uint32_t nv;
+#pragma unroll 1
+        for (int round = 0;; ++round) {
+          float top = -INFINITY;
+          if (good) {
+            uint32_t a[32], b[32], ph[16];
+            const uint32_t ta = tmem + lane_base + kColS + 64u * slot;
+            ptx::tmem_ld_16x32bx2_x32<32>(ta, a);
+            ptx::tmem_ld_16x32bx2_x32<32>(ta + 128u, b);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) + __uint_as_float(b[u]));
+            top = probs32(a, mask, c2, ref, ph, sum);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(&S.p[slot][4 * rh + u][h * 8]) =
+                  make_uint4(ph[4 * u], ph[4 * u + 1], ph[4 * u + 2], ph[4 * u + 3]);
+            ptx::fence_proxy_async_smem();
+          }
+          if (round) break;
+          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kTau2;
+          nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
+          if (nv == 0 || nv >= 8) break;
+          const float cm = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) + ref;
+          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kTau2) {
+            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
+            m2 = cm;
+          }
+          ref = m2 == -INFINITY ? 0.0f : m2;
+        }
+        if (nv >= 8) {
+          good = false;
+          break;
+        }
+        if (nv != 0 && j > 0) {  // O^T holds earlier chunks: scale the columns of the heads that moved
+          if (rh == 0) S.alpha[h] = alpha;
+          softmax_sync();
+          good = wait(&S.x_free[slot ^ 1u][0], (m - 1) >> 1) && wait(&S.x_free[slot ^ 1u][1], (m - 1) >> 1);
+          if (good) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {  // tile c / 2, heads 32 (c % 2) ..
+              const float a32 = S.alpha[32 * (c & 1) + lane];
+              if (!__any_sync(0xffffffffu, a32 != 1.0f)) continue;
+              uint32_t a[32];
+              ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                a[u] = __float_as_uint(__uint_as_float(a[u]) * __shfl_sync(0xffffffffu, a32, u));
+              ptx::tmem_st_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
+            }
+            ptx::tmem_wait_st();
+          }
+        }
+        if (good) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&S.p_full[slot]);
+        }
+        lsum = fmaf(alpha, lsum, sum);
+      }
+      // ---- this item's partial: O^T / l in f16, [channel][head]
+      const uint32_t last = n + (uint32_t)nc - 1;
+      good = good && wait(&S.x_free[last & 1u][0], last >> 1) && wait(&S.x_free[last & 1u][1], last >> 1);
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // the four warps leave together, or none
+      if (!good) return;
+      ptx::tc_fence_after();
+      const int64_t slot = p + cta;
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+      if (rh == 0) {
+        S.alpha[h] = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+        k.part_ml[slot * kHAtt + h] = make_float2(m2, lsum);
+      }
+      softmax_sync();
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t a[32];
+        ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
+        ptx::tmem_wait_ld();
+        uint4* po = k.part_o + (slot * kDMain + 128 * (c >> 1) + 32 * warp + lane) * 8 + 4 * (c & 1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float2 i2 = *reinterpret_cast<const float2*>(&S.alpha[32 * (c & 1) + 8 * u + 2 * v]);
+            const __half2 hh = __floats2half2_rn(__uint_as_float(a[8 * u + 2 * v]) * i2.x,
+                                                 __uint_as_float(a[8 * u + 2 * v + 1]) * i2.y);
+            w[v] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          po[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      softmax_sync();  // alpha is written again
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+    });
+    where = 45;
+  }
+  if (!good && lane == 0 && !*abort_flag) {
+    *abort_flag = 1;
+    report_error(k.ws, CSA2_ERR_DEVICE_TIMEOUT, where);
+  }
+  if (warp >= kAloneS && warp <= kAloneO) {  // every MMA has completed before tensor memory is freed
+    ptx::mma_commit_elect(&S.drained);
+    volatile int keep_waiting = 0;
+    ptx::mbar_wait_warp(&S.drained, 0, &keep_waiting, kWaitBudget);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kAloneS) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kCols);
+  }
+}
+
+// Joins the partials of one query: thread t of a CTA has heads 2 (t % 32), + 1 and the eight channels
+// 32 blockIdx.y + 8 (t / 32) .. (a warp reads 128 contiguous bytes of a channel's 64 heads).
+__global__ void __launch_bounds__(128) k_paged_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ totals,
+                                                     const uint32_t* __restrict__ part_o,
+                                                     const float2* __restrict__ part_ml,
+                                                     const float* __restrict__ sink, const float2* __restrict__ turn,
+                                                     void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
+  ptx::griddep_wait();
+  const int b = blockIdx.x, t = threadIdx.x, h2 = t & 31;
+  const int cc = 32 * blockIdx.y + 8 * (t >> 5);
+  const long long total = totals[1];
+  const int s0 = pairs[b].chunk0, s1 = pairs[b + 1].chunk0;
+  const int ctas = (int)min((long long)kAlone, total);
+  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * ctas + total - 1) / total) - 1 : 0;
+  const int k1 = s1 > s0 ? (int)((s1 * (long long)ctas + total - 1) / total) : 0;
+  float ref[2], L[2], acc[2][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ref[i] = sink ? sink[2 * h2 + i] * kLog2e : -INFINITY;
+    L[i] = ref[i] > -INFINITY ? 1.0f : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc[i][u] = 0.0f;
+  }
+  constexpr int kN = 4;
+  for (int c0 = k0; c0 < k1; c0 += kN) {
+    float4 ml[kN];  // reference and sum of both heads
+    uint32_t v[kN][8];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      if (c0 + j < k1) {
+        ml[j] = *reinterpret_cast<const float4*>(part_ml + (int64_t)(b + c0 + j) * kHAtt + 2 * h2);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[j][u] = part_o[((int64_t)(b + c0 + j) * kDMain + cc + u) * 32 + h2];
+      } else {
+        ml[j] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = ref[i];
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if ((i ? ml[j].w : ml[j].y) > 0.0f) top = fmaxf(top, i ? ml[j].z : ml[j].x);
+      if (top > ref[i]) {
+        const float f = ref[i] > -INFINITY ? ptx::ex2(ref[i] - top) : 0.0f;
+        L[i] *= f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) acc[i][u] *= f;
+        ref[i] = top;
+      }
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const float l = i ? ml[j].w : ml[j].y;
+        if (!(l > 0.0f)) continue;
+        const float f = ptx::ex2((i ? ml[j].z : ml[j].x) - ref[i]) * l;
+        L[i] += f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j][u]));
+          acc[i][u] = fmaf(f, i ? x.y : x.x, acc[i][u]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int h = 2 * h2 + i;
+    const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc[i][u] *= inv;
+    if (turn && cc >= kRopeFirst) {  // turn back by -q_pos
+      const float2* cs = turn + (int64_t)b * 32 + (cc - kRopeFirst) / 2;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) rope_pair(acc[i][2 * u], acc[i][2 * u + 1], cs[u].x, -cs[u].y);
+    }
+    const int64_t at = ((int64_t)b * kHAtt + h) * kDMain + cc;
+    if (out_bf16) {
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i][2 * u], acc[i][2 * u + 1]);
+        w[u] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+      o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+    if (lse && cc == 0) lse[b * kHAtt + h] = L[i] > 0.0f ? (ref[i] + log2f(L[i])) / kLog2e : -INFINITY;
+  }
+}
+
 struct PrefixWs {
   Pair* pairs;
   int32_t *gpair, *qpair, *cpair, *totals, *gimage;
@@ -1062,7 +1535,7 @@ struct PrefixWs {
   float2* part_ml;
   size_t bytes;
 };
-int max_pairs(int32_t B, int32_t G) { return (B + G + 2) / 2; }
+int max_pairs(int32_t B, int32_t G) { return G > 0 ? (B + G + 2) / 2 : B; }
 
 PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   PrefixWs L{};
@@ -1073,18 +1546,20 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
     off += align_up(n, 256);
     return p;
   };
-  const size_t slots = (size_t)max_pairs(B, G) + kClusters;
+  // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
+  const size_t parts = G > 0 ? kClusters : kAlone;
+  const size_t slots = ((size_t)max_pairs(B, G) + parts) * (G > 0 ? 2 : 1);
   L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.qpair = (int32_t*)take((size_t)B * 4);
-  L.cpair = (int32_t*)take(kClusters * 4);
+  L.cpair = (int32_t*)take(parts * 4);
   L.totals = (int32_t*)take(8);
   L.gimage = (int32_t*)take((size_t)G * 4);
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
   L.turn = (float2*)take((size_t)B * 32 * 8);
-  L.part_o = (uint4*)take(slots * 2 * kHAtt * kDMain * 2);
-  L.part_ml = (float2*)take(slots * 2 * kHAtt * 8);
+  L.part_o = (uint4*)take(slots * kHAtt * kDMain * 2);
+  L.part_ml = (float2*)take(slots * kHAtt * 8);
   const int64_t groups = B / kImageQueries < G ? B / kImageQueries : G;
   L.image_cap = groups * cdiv(shared_max, kChunk);
   if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
@@ -1159,7 +1634,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals,
-                     L.gimage, L.image_cap, ws};
+                     L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
@@ -1173,13 +1648,26 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   constexpr int prep_smem = kDMain / 8 * kQPad;
   const size_t smem = sizeof(PrefixSmem);
   if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem) != cudaSuccess ||
-      cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      (G > 0 ? cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+             : cudaFuncSetAttribute(k_paged_attn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(AloneSmem))) != cudaSuccess)
     return launch_status();
   {
     KernelTimer timer("k_prefix_prep", st);
     const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
     launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)prep_smem, st, a, pq, k,
                L.image);
+  }
+  if (G == 0) {
+    {
+      KernelTimer timer("k_paged_attn", st);
+      launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
+    }
+    KernelTimer timer("k_paged_merge", st);
+    launch_pdl(k_paged_merge, dim3(B, kDMain / 32), dim3(128), 0, st, (const Pair*)L.pairs, (const int32_t*)L.totals,
+               (const uint32_t*)L.part_o, (const float2*)L.part_ml, sink,
+               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+    return launch_status();
   }
   {
     KernelTimer timer("k_prefix_attn", st);
