@@ -17,7 +17,7 @@
 namespace csa2 {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // at most
 
 struct PageArgs {
   int32_t B;
@@ -77,17 +77,60 @@ __device__ __forceinline__ int taken_page(const PageArgs& a, const PlanView& v, 
   return at >= v.st->n_free ? gone_page(a, v, at - v.st->n_free) : a.free_pages[at];
 }
 
-// The plan, by one CTA of kPlanThreads: sums, checks, n_entries, n_free_out, row_start.
+// Exclusive sums over the block of three values a thread, and their totals.  32-bit steps where no value
+// reaches 2^20 (1,024 of them stay below 2^30), else 64-bit ones.
+template <typename T>
+__device__ __forceinline__ void block_scan3(const T (&x)[3], T (*s_warp)[kPlanThreads / 32], long long (&before)[3],
+                                            long long (&total)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  T inc[3] = {x[0], x[1], x[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const T y = __shfl_up_sync(0xffffffffu, inc[q], o);
+      if (lane >= o) inc[q] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int q = 0; q < 3; ++q) s_warp[q][warp] = inc[q];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    T w = lane < warps ? s_warp[q][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    const T b = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    total[q] = __shfl_sync(0xffffffffu, w, 31);
+    before[q] = (long long)(inc[q] - x[q]) + (warp > 0 ? (long long)b : 0);
+  }
+  __syncthreads();  // s_warp is written again by the next strip
+}
+
+// The plan, by one CTA: sums, checks, n_entries, n_free_out, row_start.  It also clears the error word,
+// which no other CTA of the call writes.
 __device__ void plan_block(const PageArgs& a, const PlanView& v) {
-  __shared__ long long s_warp[3][kPlanThreads / 32];
+  __shared__ union {
+    long long l[3][kPlanThreads / 32];
+    int i[3][kPlanThreads / 32];
+  } s_warp;
   __shared__ int s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  const int tid = threadIdx.x, step = blockDim.x;
+  const int n_free = *a.n_free;
+  if (tid == 0) {
+    s_bad = 0;
+    *reinterpret_cast<ErrWord*>(a.ws) = ErrWord{0, 0, 0};
+    v.rows[0] = v.need[0] = v.gone[0] = 0;
+  }
+  __syncthreads();
   const long long cap = min((long long)a.max_pages * a.P, (long long)INT32_MAX);
   long long base[3] = {0, 0, 0};
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += step) {
     const int b = b0 + tid;
-    long long x[3] = {0, 0, 0};
+    int x[3] = {0, 0, 0};
     if (b < a.B) {
       const int have = a.have[b], add = a.add[b], kept = a.kept ? a.kept[b] : 0;
       const long long total = (long long)have + add;
@@ -105,43 +148,22 @@ __device__ void plan_block(const PageArgs& a, const PlanView& v) {
         }
       }
     }
-    long long inc[3] = {x[0], x[1], x[2]};
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc[q], o);
-        if (lane >= o) inc[q] += y;
-      }
-    if (lane == 31)
-#pragma unroll
-      for (int q = 0; q < 3; ++q) s_warp[q][warp] = inc[q];
-    __syncthreads();
-    long long total[3];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      long long w = s_warp[q][lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-      total[q] = __shfl_sync(0xffffffffu, w, 31);
-      inc[q] += base[q] + (warp > 0 ? before : 0);
+    long long before[3], total[3];
+    if (__syncthreads_or(max(max(x[0], x[1]), x[2]) >= 1 << 20)) {
+      const long long y[3] = {x[0], x[1], x[2]};
+      block_scan3<long long>(y, s_warp.l, before, total);
+    } else {
+      block_scan3<int>(x, s_warp.i, before, total);
     }
     if (b < a.B) {  // sums past 32 bits are refused below; what they leave here is not used
-      v.rows[b + 1] = (int)inc[0];
-      v.need[b + 1] = (int)inc[1];
-      v.gone[b + 1] = (int)inc[2];
+      v.rows[b + 1] = (int)(base[0] + before[0] + x[0]);
+      v.need[b + 1] = (int)(base[1] + before[1] + x[1]);
+      v.gone[b + 1] = (int)(base[2] + before[2] + x[2]);
     }
 #pragma unroll
     for (int q = 0; q < 3; ++q) base[q] += total[q];
-    __syncthreads();  // s_warp is written again by the next strip
   }
-  const int n_free = *a.n_free;
   if (tid == 0) {
-    v.rows[0] = v.need[0] = v.gone[0] = 0;
     const bool maps = a.query || a.slot || a.entry || a.pos;
     if (base[0] > INT32_MAX || (maps && base[0] > a.n_rows)) {
       s_bad = 1;
@@ -154,36 +176,32 @@ __device__ void plan_block(const PageArgs& a, const PlanView& v) {
       s_bad = 1;
       report_error(a.ws, CSA2_ERR_NO_PAGES, base[1] - n_free - base[2]);
     }
+    *v.st = PlanState{1, n_free, (int)base[0], (int)base[2]};
   }
-  if (tid == 0) *v.st = PlanState{1, n_free, (int)base[0], (int)base[2]};
   __syncthreads();
-  bool ok = !s_bad;
-  __syncthreads();
-  if (ok) {  // the ids that would move: a bad one refuses the call
+  if (!s_bad) {  // the ids that would move: a bad one refuses the call
+    bool bad = false;
+    int id = 0;
     const int from_stack = (int)min(max(base[1] - base[2], 0LL), (long long)n_free);
-    for (int i = tid; i < from_stack; i += kPlanThreads) {
-      const int id = a.free_pages[n_free - 1 - i];
-      if (id < 0 || id >= a.n_pages) {
-        s_bad = 1;
-        report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
-      }
+    for (int i = tid; i < from_stack && !bad; i += step) {
+      id = a.free_pages[n_free - 1 - i];
+      bad = id < 0 || id >= a.n_pages;
     }
-    for (int i = tid; i < (int)base[2]; i += kPlanThreads) {
-      const int id = gone_page(a, v, i);
-      if (id < 0 || id >= a.n_pages) {
-        s_bad = 1;
-        report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
-      }
+    for (int i = tid; i < (int)base[2] && !bad; i += step) {
+      id = gone_page(a, v, i);
+      bad = id < 0 || id >= a.n_pages;
     }
+    if (bad) report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
+    if (__syncthreads_or(bad) && tid == 0) s_bad = 1;
   }
   __syncthreads();
-  ok = !s_bad;
+  const bool ok = !s_bad;
   if (tid == 0) {
     if (!ok) *v.st = PlanState{0, n_free, 0, 0};
     *a.n_free_out = ok ? (int)(n_free + base[2] - base[1]) : n_free;
     if (a.row_start) a.row_start[0] = 0;
   }
-  for (int b = tid; b < a.B; b += kPlanThreads) {
+  for (int b = tid; b < a.B; b += step) {
     a.n_entries[b] = ok ? v.have[b] + a.add[b] : v.have[b];
     if (a.row_start) a.row_start[b + 1] = ok ? v.rows[b + 1] : 0;
   }
@@ -231,12 +249,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_tables(PageArgs a) {
   const PlanView v{smem, smem + a.B, smem + 2 * a.B + 1, smem + 3 * a.B + 2, &st};
   ptx::griddep_wait();
   plan_block(a, v);
-  fill_requests(a, v, threadIdx.x / 32, kPlanThreads / 32);
-  fill_rows(a, v, threadIdx.x, kPlanThreads);
+  fill_requests(a, v, threadIdx.x / 32, blockDim.x / 32);
+  fill_rows(a, v, threadIdx.x, blockDim.x);
 }
 
 // The plan by one CTA into the workspace, then the fill by many.
 __global__ void __launch_bounds__(kPlanThreads) k_page_plan(PageArgs a, PlanView v) {
+  ptx::griddep_launch();
   ptx::griddep_wait();
   plan_block(a, v);
 }
@@ -301,12 +320,14 @@ extern "C" csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const 
   const PlanView v = plan_view(ws, B, &need);
   if (ws_bytes < need) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
-  if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const PageArgs a{B, n_have, n_new, n_kept, page_entries, m, page_table, max_pages, n_pages, free_pages, n_free,
                    n_free_out, n_entries, n_rows, row_query, row_slot, row_entry, row_pos, row_start, ws};
   if (n_rows <= kOneCtaRows && B <= kOneCtaRequests) {
     KernelTimer timer("k_page_tables", st);
-    launch_pdl(k_page_tables, dim3(1), dim3(kPlanThreads), (4 * (size_t)B + 3) * 4, st, a);
+    // a thread for each request and each row: fewer warps wait less for one another
+    const int want = B > n_rows ? B : n_rows;
+    const int threads = want > kPlanThreads ? kPlanThreads : want < 128 ? 128 : (want + 31) / 32 * 32;
+    launch_pdl(k_page_tables, dim3(1), dim3(threads), (4 * (size_t)B + 3) * 4, st, a);
   } else {
     {
       KernelTimer timer("k_page_plan", st);

@@ -68,7 +68,7 @@ struct PrefixArgs {
   int64_t table_cap;  // entries a table row can hold
   Pair* pairs;        // [pairs + 1], the last one holds the number of chunks
   int32_t* gpair;     // [G + 3] first pair of each range of queries
-  int32_t* qpair;     // [B] pair * 2 + place
+  int2* qpart;        // [B] first partial (see the merges), partials
   int32_t* cpair;     // [parts] pair of each part's first chunk
   int32_t* totals;    // pairs, chunks
   int32_t* gimage;    // [G] first image chunk of each group, or -1
@@ -121,7 +121,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) {
+    s_bad = 0;
+    *reinterpret_cast<ErrWord*>(a.ws) = ErrWord{0, 0, 0};  // no other CTA of the launch reports
+  }
   __syncthreads();
   for (int g = tid; g < a.G; g += kPrepThreads) {
     const int lo = a.group_start[g], hi = a.group_start[g + 1];
@@ -194,7 +197,6 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
         }
         (i ? x.vis1 : x.vis0) = min(x.ns, c);
         (i ? x.own1 : x.own0) = own;
-        a.qpair[q] = 2 * p + i;
       }
       x.nshared = (max(x.vis0, x.vis1) + kChunk - 1) / kChunk;
       x.paired = x.q1 >= 0 ? (min(x.own0, x.own1) + a.n_swa + kOwnChunk - 1) / kOwnChunk : 0;
@@ -213,6 +215,19 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   }
   __syncthreads();
   const int clusters = min(a.parts, chunks);
+  for (int p = tid; p < np; p += kPrepThreads) {
+    // chunk t belongs to part ceil((t + 1) parts / chunks) - 1; a pair's partial of part c is p + c
+    const int s0 = a.pairs[p].chunk0, s1 = a.pairs[p + 1].chunk0;
+    const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * clusters + chunks - 1) / chunks) - 1 : 0;
+    const int k1 = s1 > s0 ? (int)((s1 * (long long)clusters + chunks - 1) / chunks) : 0;
+    if (kAloneQueries) {
+      a.qpart[p] = make_int2(p + k0, k1 - k0);
+    } else {
+      const int q0 = a.pairs[p].q0, q1 = a.pairs[p].q1;
+      a.qpart[q0] = make_int2(2 * (p + k0), k1 - k0);
+      if (q1 >= 0) a.qpart[q1] = make_int2(2 * (p + k0) + 1, k1 - k0);
+    }
+  }
   for (int c = tid; c < clusters; c += kPrepThreads) {  // the pair of chunk floor(chunks * c / clusters)
     const int t = (int)((long long)chunks * c / clusters);
     int lo = 0, hi = np;
@@ -560,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     __syncwarp();
     ptx::tmem_alloc_pair(&S.tmem_base, kCols);
   }
+  ptx::griddep_launch();
   ptx::griddep_wait();
   ptx::tc_fence_before();
   __syncthreads();
@@ -942,7 +958,7 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
     int r = kNoRow;
     if (e < ns) {
       const int pi = (int)((uint64_t)e * k.page_div >> 40);
-      r = resolve(k, RowRef{k.table[first * k.max_pages + pi], e - pi * k.page_entries}, cb == 0);
+      r = resolve(k, RowRef{k.table[first * k.max_pages + pi], e - pi * k.page_entries}, false);  // the attention reports
     }
     Fetch f[4];
 #pragma unroll
@@ -958,6 +974,7 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
 __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, PrefixQuery q,
                                                               const __grid_constant__ PrefixKernel k, uint16_t* image) {
   extern __shared__ __align__(16) unsigned char prep_smem[];
+  ptx::griddep_launch();
   ptx::griddep_wait();
   const int64_t b = (int64_t)blockIdx.x - 1;
   if (b < 0) {
@@ -968,96 +985,133 @@ __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, Pref
   else widen_chunks(a, k, image, (int)(b - a.B - 1), (int)(gridDim.x - a.B - 2));
 }
 
-// Joins the partials of one query: thread t of a CTA has head t % 64 and, of channel half t / 64, the 32
-// channels 256 (t / 64) + 32 blockIdx.y ...  Partial i has reference m_i (log2 units), sum l_i and O_i / l_i:
-// out = sum 2^(m_i - m) l_i (O_i / l_i) / L, L = sum 2^(m_i - m) l_i (+ the sink's 2^(z - m)).  Latency bounds
-// it: the references of up to eight partials are read at once, then their channels.
-__global__ void __launch_bounds__(128) k_prefix_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ qpair,
-                                                      const int32_t* __restrict__ totals,
-                                                      const uint4* __restrict__ part_o,
-                                                      const float2* __restrict__ part_ml,
-                                                      const float* __restrict__ sink, const float2* __restrict__ turn,
-                                                      void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
-  ptx::griddep_wait();
-  const int b = blockIdx.x, t = threadIdx.x, h = t & 63, half = t >> 6;
-  const int pr = qpair[b], p = pr >> 1, r = pr & 1;
-  const long long total = totals[1];
-  const int s0 = pairs[p].chunk0, s1 = pairs[p + 1].chunk0;
-  // clusters that ran chunks s0 .. s1 - 1: chunk t belongs to cluster ceil((t + 1) clusters / total) - 1
-  const int clusters = (int)min((long long)kClusters, total);
-  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * clusters + total - 1) / total) - 1 : 0;
-  const int k1 = s1 > s0 ? (int)((s1 * (long long)clusters + total - 1) / total) : 0;
-  const float z2 = sink ? sink[h] * kLog2e : -INFINITY;
-  constexpr int kN = 8;
-  float ref = z2, L = sink && z2 > -INFINITY ? 1.0f : 0.0f;
-  float acc[32];
+// kC consecutive output channels at element `at`
+template <int kC>
+__device__ __forceinline__ void store_channels(void* out, int out_bf16, int64_t at, const float (&v)[kC]) {
+  if (out_bf16) {
+    uint32_t w[kC / 2];
 #pragma unroll
-  for (int u = 0; u < 32; ++u) acc[u] = 0.0f;
-  for (int c0 = k0; c0 < k1; c0 += kN) {
-    float2 ml[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      ml[i] = c0 + i < k1 ? part_ml[((int64_t)(p + c0 + i) * 2 + r) * kHAtt + h] : make_float2(-INFINITY, 0.0f);
-    float top = ref;
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (ml[i].y > 0.0f) top = fmaxf(top, ml[i].x);
-    if (top > ref) {
-      const float f = ref > -INFINITY ? ptx::ex2(ref - top) : 0.0f;
-      L *= f;
-#pragma unroll
-      for (int u = 0; u < 32; ++u) acc[u] *= f;
-      ref = top;
+    for (int u = 0; u < kC / 2; ++u) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
+      w[u] = *reinterpret_cast<const uint32_t*>(&x);
     }
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (c0 + i >= k1) break;
-      const uint4* po = part_o + (((int64_t)(p + c0 + i) * 2 + r) * 32 + blockIdx.y * 4) * 128 + t;
-      uint4 v[4];
+    for (int u = 0; u < kC / 8; ++u) o[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  } else {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = po[u * 128];
+    for (int u = 0; u < kC / 4; ++u) o[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+  }
+}
+
+// The join of a query's partials.  Partial i has reference m_i (log2 units), sum l_i and O_i / l_i:
+//   out = sum 2^(m_i - m) l_i (O_i / l_i) / L,  L = sum 2^(m_i - m) l_i  (+ 2^(z - m) of the sink).
+// Latency bounds it: a thread reads up to kJoin partials at once (references and channels in one round trip),
+// and for few queries, which are cut into many partials, four slices of a CTA's threads take every fourth
+// and the first joins the four (one query of 4,096 entries, 66 partials: 27 us with one slice, 12 with four;
+// 128 queries of two or three partials: 12 us with one, 37 with four).
+constexpr int kJoin = 8;
+constexpr int kSliceQueries = 16;  // below this many queries: four slices
+
+// the running join of one head's kC channels
+template <int kC>
+struct Join {
+  float ref, L, acc[kC];
+  __device__ __forceinline__ void start(float z) {  // z: the sink's logit (log2 units) or -inf
+    ref = z;
+    L = z > -INFINITY ? 1.0f : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kC; ++u) acc[u] = 0.0f;
+  }
+  __device__ __forceinline__ void raise(float top) {
+    if (!(top > ref)) return;
+    const float f = ref > -INFINITY ? ptx::ex2(ref - top) : 0.0f;
+    L *= f;
+#pragma unroll
+    for (int u = 0; u < kC; ++u) acc[u] *= f;
+    ref = top;
+  }
+};
+
+// Thread t of a slice: head t % 64 and, of channel half t / 64, the 16 channels 256 (t / 64) + 16 blockIdx.y ..
+template <int kSlices>
+__global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __restrict__ qpart,
+                                                                const uint4* __restrict__ part_o,
+                                                                const float2* __restrict__ part_ml,
+                                                                const float* __restrict__ sink,
+                                                                const float2* __restrict__ turn, void* __restrict__ out,
+                                                                int out_bf16, float* __restrict__ lse) {
+  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][18][128];
+  ptx::griddep_wait();
+  const int b = blockIdx.x, slice = threadIdx.x >> 7, t = threadIdx.x & 127, h = t & 63, half = t >> 6;
+  const int2 part = qpart[b];  // twice the first partial's slot, plus the query's place in its pair; partials
+  Join<16> a;
+  a.start(slice == 0 && sink ? sink[h] * kLog2e : -INFINITY);
+  for (int c0 = slice; c0 < part.y; c0 += kSlices * kJoin) {
+    float2 ml[kJoin];
+    uint4 v[kJoin][2];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      if (c0 + i * kSlices < part.y) {
+        const int64_t slot = part.x + 2 * (int64_t)(c0 + i * kSlices);
+        ml[i] = part_ml[slot * kHAtt + h];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) v[i][u] = part_o[(slot * 32 + blockIdx.y * 2 + u) * 128 + t];
+      }
+    }
+    float top = a.ref;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i)
+      if (ml[i].y > 0.0f) top = fmaxf(top, ml[i].x);
+    a.raise(top);
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
       if (!(ml[i].y > 0.0f)) continue;
-      const float f = ptx::ex2(ml[i].x - ref) * ml[i].y;
-      L += f;
+      const float f = ptx::ex2(ml[i].x - a.ref) * ml[i].y;
+      a.L += f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          acc[8 * u + 2 * j] = fmaf(f, x.x, acc[8 * u + 2 * j]);
-          acc[8 * u + 2 * j + 1] = fmaf(f, x.y, acc[8 * u + 2 * j + 1]);
+          a.acc[8 * u + 2 * j] = fmaf(f, x.x, a.acc[8 * u + 2 * j]);
+          a.acc[8 * u + 2 * j + 1] = fmaf(f, x.y, a.acc[8 * u + 2 * j + 1]);
         }
       }
     }
   }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const int c0 = 256 * half + 32 * blockIdx.y;
+  if (slice > 0) {
+    s_join[slice - 1][0][t] = a.ref;
+    s_join[slice - 1][1][t] = a.L;
 #pragma unroll
-  for (int u = 0; u < 32; ++u) acc[u] *= inv;
+    for (int u = 0; u < 16; ++u) s_join[slice - 1][2 + u][t] = a.acc[u];
+  }
+  if (kSlices > 1) __syncthreads();
+  if (slice > 0) return;
+  for (int i = 0; i < kSlices - 1; ++i) {
+    const float m = s_join[i][0][t], l = s_join[i][1][t];
+    if (!(l > 0.0f)) continue;
+    a.raise(m);
+    const float f = ptx::ex2(m - a.ref);
+    a.L = fmaf(f, l, a.L);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) a.acc[u] = fmaf(f, s_join[i][2 + u][t], a.acc[u]);
+  }
+  const float inv = a.L > 0.0f ? 1.0f / a.L : 0.0f;
+  const int c0 = 256 * half + 16 * blockIdx.y;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) a.acc[u] *= inv;
   if (turn && c0 >= kRopeFirst) {  // turn back by -q_pos
     const float2* cs = turn + (int64_t)b * 32 + (c0 - kRopeFirst) / 2;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) rope_pair(acc[2 * u], acc[2 * u + 1], cs[u].x, -cs[u].y);
+    for (int u = 0; u < 8; ++u) rope_pair(a.acc[2 * u], a.acc[2 * u + 1], cs[u].x, -cs[u].y);
   }
-  const int64_t row = ((int64_t)b * kHAtt + h) * kDMain + c0;
-  if (out_bf16) {
-    uint32_t w[16];
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * u], acc[2 * u + 1]);
-      w[u] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) o[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-  } else {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) o[u] = make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]);
-  }
+  store_channels<16>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + c0, a.acc);
   if (lse && blockIdx.y == 0 && half == 0)
-    lse[b * kHAtt + h] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
+    lse[b * kHAtt + h] = a.L > 0.0f ? (a.ref + log2f(a.L)) / kLog2e : -INFINITY;
 }
 
 // ------------------------------------------------------------ queries alone
@@ -1184,6 +1238,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     __syncwarp();
     ptx::tmem_alloc(&S.tmem_base, kCols);
   }
+  ptx::griddep_launch();
   ptx::griddep_wait();
   ptx::tc_fence_before();
   __syncthreads();
@@ -1431,102 +1486,97 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   }
 }
 
-// Joins the partials of one query: thread t of a CTA has heads 2 (t % 32), + 1 and the eight channels
-// 32 blockIdx.y + 8 (t / 32) .. (a warp reads 128 contiguous bytes of a channel's 64 heads).
-__global__ void __launch_bounds__(128) k_paged_merge(const Pair* __restrict__ pairs, const int32_t* __restrict__ totals,
-                                                     const uint32_t* __restrict__ part_o,
-                                                     const float2* __restrict__ part_ml,
-                                                     const float* __restrict__ sink, const float2* __restrict__ turn,
-                                                     void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
+// The join over partials of [channel][head]: thread t of a slice has heads 2 (t % 32), + 1 and the eight
+// channels 32 blockIdx.y + 8 (t / 32) .. (a warp reads 128 contiguous bytes of a channel's 64 heads).
+template <int kSlices>
+__global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __restrict__ qpart,
+                                                               const uint32_t* __restrict__ part_o,
+                                                               const float2* __restrict__ part_ml,
+                                                               const float* __restrict__ sink,
+                                                               const float2* __restrict__ turn, void* __restrict__ out,
+                                                               int out_bf16, float* __restrict__ lse) {
+  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][20][128];
   ptx::griddep_wait();
-  const int b = blockIdx.x, t = threadIdx.x, h2 = t & 31;
+  const int b = blockIdx.x, slice = threadIdx.x >> 7, t = threadIdx.x & 127, h2 = t & 31;
   const int cc = 32 * blockIdx.y + 8 * (t >> 5);
-  const long long total = totals[1];
-  const int s0 = pairs[b].chunk0, s1 = pairs[b + 1].chunk0;
-  const int ctas = (int)min((long long)kAlone, total);
-  const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * ctas + total - 1) / total) - 1 : 0;
-  const int k1 = s1 > s0 ? (int)((s1 * (long long)ctas + total - 1) / total) : 0;
-  float ref[2], L[2], acc[2][8];
+  const int2 part = qpart[b];  // the first partial's slot, partials
+  Join<8> a[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    ref[i] = sink ? sink[2 * h2 + i] * kLog2e : -INFINITY;
-    L[i] = ref[i] > -INFINITY ? 1.0f : 0.0f;
+  for (int i = 0; i < 2; ++i) a[i].start(slice == 0 && sink ? sink[2 * h2 + i] * kLog2e : -INFINITY);
+  for (int c0 = slice; c0 < part.y; c0 += kSlices * kJoin) {
+    float4 ml[kJoin];  // reference and sum of both heads
+    uint32_t v[kJoin][8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc[i][u] = 0.0f;
-  }
-  constexpr int kN = 4;
-  for (int c0 = k0; c0 < k1; c0 += kN) {
-    float4 ml[kN];  // reference and sum of both heads
-    uint32_t v[kN][8];
+    for (int j = 0; j < kJoin; ++j) {
+      ml[j] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+      if (c0 + j * kSlices < part.y) {
+        const int64_t slot = part.x + (int64_t)(c0 + j * kSlices);
+        ml[j] = *reinterpret_cast<const float4*>(part_ml + slot * kHAtt + 2 * h2);
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      if (c0 + j < k1) {
-        ml[j] = *reinterpret_cast<const float4*>(part_ml + (int64_t)(b + c0 + j) * kHAtt + 2 * h2);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[j][u] = part_o[((int64_t)(b + c0 + j) * kDMain + cc + u) * 32 + h2];
-      } else {
-        ml[j] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        for (int u = 0; u < 8; ++u) v[j][u] = part_o[(slot * kDMain + cc + u) * 32 + h2];
       }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float top = ref[i];
+      float top = a[i].ref;
 #pragma unroll
-      for (int j = 0; j < kN; ++j)
+      for (int j = 0; j < kJoin; ++j)
         if ((i ? ml[j].w : ml[j].y) > 0.0f) top = fmaxf(top, i ? ml[j].z : ml[j].x);
-      if (top > ref[i]) {
-        const float f = ref[i] > -INFINITY ? ptx::ex2(ref[i] - top) : 0.0f;
-        L[i] *= f;
+      a[i].raise(top);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) acc[i][u] *= f;
-        ref[i] = top;
-      }
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
+      for (int j = 0; j < kJoin; ++j) {
         const float l = i ? ml[j].w : ml[j].y;
         if (!(l > 0.0f)) continue;
-        const float f = ptx::ex2((i ? ml[j].z : ml[j].x) - ref[i]) * l;
-        L[i] += f;
+        const float f = ptx::ex2((i ? ml[j].z : ml[j].x) - a[i].ref) * l;
+        a[i].L += f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j][u]));
-          acc[i][u] = fmaf(f, i ? x.y : x.x, acc[i][u]);
+          a[i].acc[u] = fmaf(f, i ? x.y : x.x, a[i].acc[u]);
         }
       }
     }
   }
+  if (slice > 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s_join[slice - 1][10 * i][t] = a[i].ref;
+      s_join[slice - 1][10 * i + 1][t] = a[i].L;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s_join[slice - 1][10 * i + 2 + u][t] = a[i].acc[u];
+    }
+  }
+  if (kSlices > 1) __syncthreads();
+  if (slice > 0) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int h = 2 * h2 + i;
-    const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
+    for (int j = 0; j < kSlices - 1; ++j) {
+      const float m = s_join[j][10 * i][t], l = s_join[j][10 * i + 1][t];
+      if (!(l > 0.0f)) continue;
+      a[i].raise(m);
+      const float f = ptx::ex2(m - a[i].ref);
+      a[i].L = fmaf(f, l, a[i].L);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) acc[i][u] *= inv;
+      for (int u = 0; u < 8; ++u) a[i].acc[u] = fmaf(f, s_join[j][10 * i + 2 + u][t], a[i].acc[u]);
+    }
+    const int h = 2 * h2 + i;
+    const float inv = a[i].L > 0.0f ? 1.0f / a[i].L : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a[i].acc[u] *= inv;
     if (turn && cc >= kRopeFirst) {  // turn back by -q_pos
       const float2* cs = turn + (int64_t)b * 32 + (cc - kRopeFirst) / 2;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) rope_pair(acc[i][2 * u], acc[i][2 * u + 1], cs[u].x, -cs[u].y);
+      for (int u = 0; u < 4; ++u) rope_pair(a[i].acc[2 * u], a[i].acc[2 * u + 1], cs[u].x, -cs[u].y);
     }
-    const int64_t at = ((int64_t)b * kHAtt + h) * kDMain + cc;
-    if (out_bf16) {
-      uint32_t w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[i][2 * u], acc[i][2 * u + 1]);
-        w[u] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-      o[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      o[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-    }
-    if (lse && cc == 0) lse[b * kHAtt + h] = L[i] > 0.0f ? (ref[i] + log2f(L[i])) / kLog2e : -INFINITY;
+    store_channels<8>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + cc, a[i].acc);
+    if (lse && cc == 0) lse[b * kHAtt + h] = a[i].L > 0.0f ? (a[i].ref + log2f(a[i].L)) / kLog2e : -INFINITY;
   }
 }
 
 struct PrefixWs {
   Pair* pairs;
-  int32_t *gpair, *qpair, *cpair, *totals, *gimage;
+  int32_t *gpair, *cpair, *totals, *gimage;
+  int2* qpart;
   uint16_t *image, *qimage;
   float* c2;
   float2* turn;
@@ -1551,7 +1601,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   const size_t slots = ((size_t)max_pairs(B, G) + parts) * (G > 0 ? 2 : 1);
   L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
-  L.qpair = (int32_t*)take((size_t)B * 4);
+  L.qpart = (int2*)take((size_t)B * 8);
   L.cpair = (int32_t*)take(parts * 4);
   L.totals = (int32_t*)take(8);
   L.gimage = (int32_t*)take((size_t)G * 4);
@@ -1631,9 +1681,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
-  if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpair, L.cpair, L.totals,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpart, L.cpair, L.totals,
                      L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
@@ -1658,13 +1707,14 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)prep_smem, st, a, pq, k,
                L.image);
   }
+  const int slices = B < kSliceQueries ? 4 : 1;
   if (G == 0) {
     {
       KernelTimer timer("k_paged_attn", st);
       launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
     }
     KernelTimer timer("k_paged_merge", st);
-    launch_pdl(k_paged_merge, dim3(B, kDMain / 32), dim3(128), 0, st, (const Pair*)L.pairs, (const int32_t*)L.totals,
+    launch_pdl(slices > 1 ? k_paged_merge<4> : k_paged_merge<1>, dim3(B, kDMain / 32), dim3(128 * slices), 0, st, (const int2*)L.qpart,
                (const uint32_t*)L.part_o, (const float2*)L.part_ml, sink,
                ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
     return launch_status();
@@ -1675,8 +1725,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   }
   {
     KernelTimer timer("k_prefix_merge", st);
-    launch_pdl(k_prefix_merge, dim3(B, 8), dim3(128), 0, st, (const Pair*)L.pairs, (const int32_t*)L.qpair,
-               (const int32_t*)L.totals, (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
+    launch_pdl(slices > 1 ? k_prefix_merge<4> : k_prefix_merge<1>, dim3(B, 16), dim3(128 * slices), 0, st, (const int2*)L.qpart,
+               (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
                ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
   }
   return launch_status();

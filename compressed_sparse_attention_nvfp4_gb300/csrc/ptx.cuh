@@ -138,6 +138,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // have completed and their memory is visible; a no-op without such a launch.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the grid that depends on this one (programmatic dependent launch) be scheduled once every CTA has
+// called this or left; what this grid writes is still seen only after its completion (griddep_wait).
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 2^x by the hardware approximation (ex2.approx: relative error about 2^-22;
 // 2^-inf = 0)
 __device__ __forceinline__ float ex2(float x) {
