@@ -68,6 +68,7 @@ struct PrefixArgs {
   int64_t table_cap;  // entries a table row can hold
   Pair* pairs;        // [pairs + 1], the last one holds the number of chunks
   int32_t* gpair;     // [G + 3] first pair of each range of queries
+  int32_t* chunk0;    // [pairs + 1] first chunk of each pair (these two where shared memory is too small)
   int2* qpart;        // [B] first partial (see the merges), partials
   int32_t* cpair;     // [parts] pair of each part's first chunk
   int32_t* totals;    // pairs, chunks
@@ -76,6 +77,9 @@ struct PrefixArgs {
   int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
   void* ws;
 };
+
+// pairs of a batch, at most (G = 0: queries)
+__host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return G > 0 ? (B + G + 2) / 2 : B; }
 
 // exclusive sum over the block of x (all threads call); total = the block's sum
 __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
@@ -117,7 +121,7 @@ __device__ __forceinline__ int image_chunks(const PrefixArgs& a, int g) {
 }
 
 template <bool kAloneQueries>
-__device__ __forceinline__ void plan_block(const PrefixArgs& a) {
+__device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, int smem_ints) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x;
@@ -136,6 +140,9 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   __syncthreads();
   const int G = s_bad ? 0 : a.G;
   const int R = G + 2;  // ranges; without groups the first is empty
+  // the lists that are searched, in shared memory where they fit: a search is a chain of dependent loads
+  int32_t* const gpair = R + 1 <= smem_ints / 2 ? smem : a.gpair;
+  int32_t* const chunk0 = max_pairs(a.B, a.G) + 1 <= smem_ints / 2 ? smem + smem_ints / 2 : a.chunk0;
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
   int base = 0;
@@ -144,10 +151,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     const int n = v < R ? (range_hi(v) - range_lo(v) + 1) / 2 : 0;
     int total;
     const int at = base + block_scan(n, s_warp, &total);
-    if (v < R) a.gpair[v] = at;
+    if (v < R) gpair[v] = at;
     base += total;
   }
-  if (tid == 0) a.gpair[R] = base;
+  if (tid == 0) gpair[R] = base;
   const int np = kAloneQueries ? a.B : base;
   // a group whose image would end beyond the room has none, and so do all behind it
   int images = 0;
@@ -173,11 +180,11 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
       int lo = 0, hi = R;  // the range with gpair[v] <= p < gpair[v + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.gpair[mid] <= p) lo = mid;
+        if (gpair[mid] <= p) lo = mid;
         else hi = mid;
       }
       const int first = range_lo(lo), end = range_hi(lo);
-      x.q0 = first + 2 * (p - a.gpair[lo]);
+      x.q0 = first + 2 * (p - gpair[lo]);
       x.q1 = x.q0 + 1 < end ? x.q0 + 1 : -1;
       x.first = first;
       x.image = -1;
@@ -205,11 +212,14 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     }
     int total;
     x.chunk0 = chunks + block_scan(n, s_warp, &total);
-    if (p < np) a.pairs[p] = x;
+    if (p < np) {
+      a.pairs[p] = x;
+      chunk0[p] = x.chunk0;
+    }
     chunks += total;
   }
   if (tid == 0) {
-    a.pairs[np].chunk0 = chunks;
+    a.pairs[np].chunk0 = chunk0[np] = chunks;
     a.totals[0] = np;
     a.totals[1] = chunks;
   }
@@ -217,7 +227,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
   const int clusters = min(a.parts, chunks);
   for (int p = tid; p < np; p += kPrepThreads) {
     // chunk t belongs to part ceil((t + 1) parts / chunks) - 1; a pair's partial of part c is p + c
-    const int s0 = a.pairs[p].chunk0, s1 = a.pairs[p + 1].chunk0;
+    const int s0 = chunk0[p], s1 = chunk0[p + 1];
     const int k0 = s1 > s0 ? (int)(((s0 + 1LL) * clusters + chunks - 1) / chunks) - 1 : 0;
     const int k1 = s1 > s0 ? (int)((s1 * (long long)clusters + chunks - 1) / chunks) : 0;
     if (kAloneQueries) {
@@ -233,7 +243,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a) {
     int lo = 0, hi = np;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (a.pairs[mid].chunk0 <= t) lo = mid;
+      if (chunk0[mid] <= t) lo = mid;
       else hi = mid;
     }
     a.cpair[c] = lo;
@@ -262,6 +272,7 @@ struct __align__(1024) PrefixSmem {
   uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
   float red[2][kHAtt];
   int32_t rows[4][kChunk];                  // where a chunk's rows come from, up to four chunks ahead
+  int32_t image[4];                         // its chunk of the image, or -1
   // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
   // of the same role passes on for all of that CTA's
   uint64_t q_land, q_peer;                  // q' copied; the odd CTA's q'
@@ -420,17 +431,17 @@ __device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float
   return top;
 }
 
-// Chunks [c0, c0 + nc) of pair x by the 16 row warps: per operand two groups of four, which write every
-// other piece.  Operand 0 (S's, warps 0-7): this CTA's 64 rows, handed over by 128 channels: in piece i a
-// thread has block (of 32 channels) 4 i + l / 8 of rows 8 (w % 4) + l % 8 and 32 more.  Operand 1 (O's): its
-// 256 channels of all rows, by 32 rows: a thread has blocks l / 8 and l / 8 + 4 of its eight of row
-// 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64 contiguous bytes of eight rows, and a store writes
-// eight rows of a plane: no bank conflicts.  A step writes one piece and fetches the codes of the next (half
-// a chunk ahead).  Both operands run the same code: the kernel's loops have to fit the instruction cache
-// (unrolled by piece and operand they waited more for instructions than for data).
-__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int image,
-                                          int nshared, int64_t q, int rank, int c0, int nc, int w, int lane, uint32_t n,
-                                          uint32_t item) {
+// The operands of all `chunks` chunks of this pair of CTAs, whatever items they belong to, by the 16 row
+// warps: per operand two groups of four, which write every other piece.  Operand 0 (S's, warps 0-7): this
+// CTA's 64 rows, handed over by 128 channels: in piece i a thread has block (of 32 channels) 4 i + l / 8 of
+// rows 8 (w % 4) + l % 8 and 32 more.  Operand 1 (O's): its 256 channels of all rows, by 32 rows: a thread
+// has blocks l / 8 and l / 8 + 4 of its eight of row 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64
+// contiguous bytes of eight rows, and a store writes eight rows of a plane: no bank conflicts.  A step writes
+// one piece and fetches the codes of the next (half a chunk ahead); a chunk of the image is copied instead,
+// by the first warp of each group.  Both operands run the same code: the kernel's loops have to fit the
+// instruction cache (unrolled by piece and operand they waited more for instructions than for data).
+__device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int rank,
+                                          int chunks, int w, int lane) {
   const int op = w >> 3, group = (w >> 2) & 1, cb = lane >> 3;
   const int rl = 8 * (w & 3) + (lane & 7);
   const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0, row_u = op ? 0 : 32;
@@ -439,21 +450,21 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   uint16_t* const dst = (op ? &S.xo[0][4 * cb][0] : &S.xs[4 * cb][0]) + rl * 8;
   constexpr int dst_step = 16 * 1024 / 2;  // a piece
   const int dst_u = op ? 16 * 32 * 8 : 32 * 8;
-  const int steps = nc * 2;  // step st: chunk st / 2, piece 2 (st % 2) + group
-  // steps whose chunks are copied from the image, by the first warp of each group
-  const int image_steps = image >= 0 ? min(max(nshared - c0, 0) * 2, steps) : 0;
-  int r[2];
+  const int steps = chunks * 2;  // step st: chunk st / 2, piece 2 (st % 2) + group
+  int r[2], image = -1;
   Fetch f[2];
   int issued = -1;  // last step copied from the image
   bool good = true;
   auto load = [&](int st) {  // this thread's rows and codes of step st
     if (st >= steps) return;
-    const uint32_t m = n + (uint32_t)(st >> 1), slot = m & 3u;
+    const uint32_t m = (uint32_t)(st >> 1), slot = m & 3u;
     const int i = 2 * (st & 1) + group;
-    if ((st & 1) == 0)
+    if ((st & 1) == 0) {
       good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
+      if (good) image = S.image[slot];
+    }
     if (!good) return;
-    if (st >= image_steps) {
+    if (image < 0) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         r[u] = S.rows[slot][row0 + row_step * i + row_u * u];
@@ -465,28 +476,19 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
       if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
     }
   };
-  if (w == 0) {  // the item's query, once S of the item before has left q'
-    good = n == 0 || ptx::mbar_wait_warp(&S.x_free[0][kPieces - 1], (n - 1) & 1u, &S.abort_flag, kWaitBudget);
-    if (good && lane == 0) {
-      ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
-      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
-    }
-    __syncwarp();
-  }
-  const bool copied = w == 0 && good;
   load(0);
 #pragma unroll 1
   for (int st = 0; st < steps && good; ++st) {
-    const uint32_t m = n + (uint32_t)(st >> 1);
+    const uint32_t m = (uint32_t)(st >> 1);
     const int i = 2 * (st & 1) + group;
     if (m > 0) good = ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) break;
-    if (st < image_steps) {
+    if (image >= 0) {
       // every warp arrives, also those that copy nothing: none may miss a phase of x_free
       if ((w & 3) != 0) {
         if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
       } else if (lane == 0) {
-        const int plane0 = (image + c0 + (st >> 1)) * (kDMain / 8);
+        const int plane0 = image * (kDMain / 8);
         ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
         if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
         else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
@@ -504,16 +506,14 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   }
   if (!good && (w & 3) == 0) {  // copies in flight write shared memory: they land before anyone leaves
     volatile int keep_waiting = 0;
-    if (copied) ptx::mbar_wait_warp(&S.q_land, item & 1u, &keep_waiting, kWaitBudget);
     for (int st = issued; st >= 0 && st > issued - 2; --st)
-      ptx::mbar_wait_warp(&S.x_full[op][2 * (st & 1) + group], (n + (uint32_t)(st >> 1)) & 1u, &keep_waiting,
-                          kWaitBudget);
+      ptx::mbar_wait_warp(&S.x_full[op][2 * (st & 1) + group], (uint32_t)(st >> 1) & 1u, &keep_waiting, kWaitBudget);
   }
   return good;
 }
 
-// Where each chunk's rows come from, by one warp (lane l rows l, 32 + l, ..) up to four chunks ahead of the
-// row and softmax warps.  Pages outside the planes are reported here.
+// Where each chunk's rows come from (or its chunk of the image), by one warp (lane l rows l, 32 + l, ..) up to
+// four chunks ahead of the row and softmax warps.  Pages outside the planes are reported here.
 __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, bool report, int c0,
                                            int nc, int lane, uint32_t n) {
   bool good = true;
@@ -534,6 +534,7 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
     if (!good) break;
 #pragma unroll
     for (int i = 0; i < 4; ++i) S.rows[slot][32 * i + lane] = row[i];
+    if (lane == 0) S.image[slot] = x.image >= 0 && c0 + j < x.nshared ? x.image + c0 + j : -1;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.r_full[slot]);
   }
@@ -608,10 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   };
 
   if (warp >= kRowWarp && warp < kSMma) {
-    for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
-      const int q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
-      good = rows_role(S, k, maps, x.image, x.nshared, q, rank, c0, nc, warp - kRowWarp, lane, n, items);
-    });
+    good = rows_role(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
     where = 31;
   } else if (warp >= kSMma) {
     ptx::setmaxnreg_dec<kMmaRegs>();
@@ -632,8 +630,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       constexpr uint32_t idesc_s = ptx::idesc_f16(128, kChunk, 0);
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
-      for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
-        good = wait(&S.q_land, items);
+      for_items([&](const Pair& x, int, int, int nc, uint32_t n, uint32_t items) {
+        // the item's query, once S of the item before has left q'; the copy lands before anyone leaves
+        good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
+        if (!good) return;
+        if (lane == 0) {
+          const int64_t q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
+          ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
+          ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
+        }
+        __syncwarp();
+        volatile int keep_waiting = 0;
+        good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
         if (rank == 0) good = good && wait(&S.q_peer, items);
         else if (good && lane == 0) ptx::mbar_arrive_peer(&S.q_peer, 0);
 #pragma unroll 1
@@ -855,6 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 // four heads each, lane l holding channels 16 l ..), and the rotation's cosines and sines.  The image goes
 // through shared memory with padded planes, so that its stores are whole lines.
 constexpr int kQPad = kHAtt * 16 + 16;  // bytes of a plane
+constexpr int kPrepSmem = kDMain / 8 * kQPad;
 __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, unsigned char* smem) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint4* const img = reinterpret_cast<uint4*>(a.image + (int64_t)b * kHAtt * kDMain);
@@ -978,8 +987,9 @@ __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, Pref
   ptx::griddep_wait();
   const int64_t b = (int64_t)blockIdx.x - 1;
   if (b < 0) {
-    if (a.G > 0) plan_block<false>(a);
-    else plan_block<true>(a);
+    int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
+    if (a.G > 0) plan_block<false>(a, ints, kPrepSmem / 4);
+    else plan_block<true>(a, ints, kPrepSmem / 4);
   }
   else if (b <= a.B) stage_block(q, a.B, (int)b, prep_smem);
   else widen_chunks(a, k, image, (int)(b - a.B - 1), (int)(gridDim.x - a.B - 2));
@@ -1150,19 +1160,18 @@ constexpr int kAloneS = 20, kAloneO = 22, kAloneIndex = 23;
 constexpr int kAloneSoftRegs = 128, kAloneRowRegs = 72, kAloneMmaRegs = 64;
 static_assert(kAloneSoftRegs + 4 * kAloneRowRegs + kAloneMmaRegs <= 6 * 80, "registers of the launch");
 
-// The rows of chunks [c0, c0 + nc) of query x.q0: thread's row 8 (w % 8) + l % 8, blocks (of 32 channels)
-// 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
-__device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, int64_t q, int nc, int w, int lane,
-                                           uint32_t n, uint32_t item) {
+// The rows of all `chunks` chunks of this CTA, whatever queries they belong to: thread's row 8 (w % 8) + l % 8,
+// blocks (of 32 channels) 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
+__device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, int chunks, int w, int lane) {
   const int half = w >> 3, rl = 8 * (w & 7) + (lane & 7), blk = 8 * half + (lane >> 3);
   uint16_t* const dst = &S.x[0][4 * blk][rl * 8];
   bool good = true;
   int ra, rb;
   Fetch fa[2], fb[2];
-  auto load = [&](Fetch (&f)[2], int& r, int j) {
-    if (j >= nc) return;
-    const uint32_t m = n + (uint32_t)j, slot = m % kRing;
-    good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m / kRing) & 1u, &S.abort_flag, kWaitBudget);
+  auto load = [&](Fetch (&f)[2], int& r, int m) {
+    if (m >= chunks) return;
+    const uint32_t slot = (uint32_t)m % kRing;
+    good = good && ptx::mbar_wait_warp(&S.r_full[slot], ((uint32_t)m / kRing) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     r = S.rows[slot][rl];
     fetch(f[0], k, r, blk);
@@ -1170,23 +1179,13 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
   };
-  if (w == 0) {  // the item's query, once S of the item before has left q'
-    good = n == 0 ||
-           ptx::mbar_wait_warp(&S.s_full[(n - 1) & 1u], ((n - 1) >> 1) & 1u, &S.abort_flag, kWaitBudget);
-    if (good && lane == 0) {
-      ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
-      ptx::bulk_g2s(&S.q[0][0], k.q + q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
-    }
-    __syncwarp();
-  }
-  const bool copied = w == 0 && good;
   load(fa, ra, 0);
   load(fb, rb, 1);
-  auto step = [&](Fetch (&f)[2], int& r, int j) {
-    if (j >= nc) return;
-    const uint32_t m = n + (uint32_t)j, slot = m & 1u;
+  auto step = [&](Fetch (&f)[2], int& r, int m) {
+    if (m >= chunks) return;
+    const uint32_t slot = (uint32_t)m & 1u;
     if (m >= 2)
-      good = good && ptx::mbar_wait_warp(&S.x_free[slot][half], ((m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
+      good = good && ptx::mbar_wait_warp(&S.x_free[slot][half], (((uint32_t)m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     uint16_t* d = dst + slot * (kDMain * kRows);
     put(f[0], r, d, kRows * 8);
@@ -1194,16 +1193,12 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.x_full[slot][half]);
-    load(f, r, j + 2);
+    load(f, r, m + 2);
   };
 #pragma unroll 1
-  for (int j = 0; j < nc && good; j += 2) {
-    step(fa, ra, j);
-    step(fb, rb, j + 1);
-  }
-  if (!good && copied) {  // the copy writes shared memory: it lands before anyone leaves
-    volatile int keep_waiting = 0;
-    ptx::mbar_wait_warp(&S.q_land, item & 1u, &keep_waiting, kWaitBudget);
+  for (int m = 0; m < chunks && good; m += 2) {
+    step(fa, ra, m);
+    step(fb, rb, m + 1);
   }
   return good;
 }
@@ -1266,9 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 
   if (warp >= 4 && warp < kAloneS) {
     ptx::setmaxnreg_dec<kAloneRowRegs>();
-    for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
-      good = alone_rows(S, k, k.pairs[p].q0, nc, warp - 4, lane, n, items);
-    });
+    good = alone_rows(S, k, t1 - t0, warp - 4, lane);
     where = 41;
   } else if (warp >= kAloneS) {
     ptx::setmaxnreg_dec<kAloneMmaRegs>();
@@ -1301,8 +1294,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       constexpr uint32_t idesc_s = ptx::idesc_f16(64, kRows, 0);
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[32 * half][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][32 * half][0], kRows * 16, 128);
-      for_items([&](int, int, int nc, uint32_t n, uint32_t items) {
-        good = wait(&S.q_land, items);
+      for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
+        volatile int keep_waiting = 0;
+        if (half == 0) {  // the item's query, once S of the item before has left q'; it lands before anyone leaves
+          good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
+          if (!good) return;
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
+            ptx::bulk_g2s(&S.q[0][0], k.q + (int64_t)k.pairs[p].q0 * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
+          }
+          __syncwarp();
+          good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
+        } else {
+          good = wait(&S.q_land, items);
+        }
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j, slot = m & 1u;
@@ -1575,7 +1580,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
 
 struct PrefixWs {
   Pair* pairs;
-  int32_t *gpair, *cpair, *totals, *gimage;
+  int32_t *gpair, *chunk0, *cpair, *totals, *gimage;
   int2* qpart;
   uint16_t *image, *qimage;
   float* c2;
@@ -1585,7 +1590,6 @@ struct PrefixWs {
   float2* part_ml;
   size_t bytes;
 };
-int max_pairs(int32_t B, int32_t G) { return G > 0 ? (B + G + 2) / 2 : B; }
 
 PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   PrefixWs L{};
@@ -1601,6 +1605,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   const size_t slots = ((size_t)max_pairs(B, G) + parts) * (G > 0 ? 2 : 1);
   L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
+  L.chunk0 = (int32_t*)take(((size_t)max_pairs(B, G) + 1) * 4);
   L.qpart = (int2*)take((size_t)B * 8);
   L.cpair = (int32_t*)take(parts * 4);
   L.totals = (int32_t*)take(8);
@@ -1682,7 +1687,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.qpart, L.cpair, L.totals,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.cpair, L.totals,
                      L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
@@ -1694,9 +1699,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (L.image_cap > 0 &&
       (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
     return CSA2_ERR_CUDA;
-  constexpr int prep_smem = kDMain / 8 * kQPad;
   const size_t smem = sizeof(PrefixSmem);
-  if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem) != cudaSuccess ||
+  if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem) != cudaSuccess ||
       (G > 0 ? cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
              : cudaFuncSetAttribute(k_paged_attn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)sizeof(AloneSmem))) != cudaSuccess)
@@ -1704,7 +1708,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   {
     KernelTimer timer("k_prefix_prep", st);
     const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
-    launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)prep_smem, st, a, pq, k,
+    launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)kPrepSmem, st, a, pq, k,
                L.image);
   }
   const int slices = B < kSliceQueries ? 4 : 1;
