@@ -70,8 +70,7 @@ struct PrefixArgs {
   int32_t* gpair;     // [G + 3] first pair of each range of queries
   int32_t* chunk0;    // [pairs + 1] first chunk of each pair (these two where shared memory is too small)
   int2* qpart;        // [B] first partial (see the merges), partials
-  int32_t* cpair;     // [parts] pair of each part's first chunk
-  int32_t* totals;    // pairs, chunks
+  int4* cpart;        // [parts] of each part: first pair, first chunk, end
   int32_t* gimage;    // [G] first image chunk of each group, or -1
   int64_t image_cap;  // chunks the image has room for
   int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
@@ -218,11 +217,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
     }
     chunks += total;
   }
-  if (tid == 0) {
-    a.pairs[np].chunk0 = chunk0[np] = chunks;
-    a.totals[0] = np;
-    a.totals[1] = chunks;
-  }
+  if (tid == 0) a.pairs[np].chunk0 = chunk0[np] = chunks;
   __syncthreads();
   const int clusters = min(a.parts, chunks);
   for (int p = tid; p < np; p += kPrepThreads) {
@@ -238,15 +233,19 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
       if (q1 >= 0) a.qpart[q1] = make_int2(2 * (p + k0) + 1, k1 - k0);
     }
   }
-  for (int c = tid; c < clusters; c += kPrepThreads) {  // the pair of chunk floor(chunks * c / clusters)
-    const int t = (int)((long long)chunks * c / clusters);
+  for (int c = tid; c < a.parts; c += kPrepThreads) {
+    if (c >= clusters) {
+      a.cpart[c] = make_int4(0, 0, 0, 0);
+      continue;
+    }
+    const int t0 = (int)((long long)chunks * c / clusters), t1 = (int)((long long)chunks * (c + 1) / clusters);
     int lo = 0, hi = np;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (chunk0[mid] <= t) lo = mid;
+      if (chunk0[mid] <= t0) lo = mid;
       else hi = mid;
     }
-    a.cpair[c] = lo;
+    a.cpart[c] = make_int4(lo, t0, t1, 0);
   }
 }
 
@@ -296,7 +295,7 @@ struct PrefixKernel {
   uint64_t page_div;  // ceil(2^40 / page_entries): e * page_div >> 40 = e / page_entries for e < 2^18
   const int64_t *win_pos, *win_lo;
   const Pair* pairs;
-  const int32_t *cpair, *totals;
+  const int4* cpart;
   uint4* part_o;    // [pairs + clusters][2][32][128]: eight f16 channels c8 of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
@@ -584,17 +583,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  const int total = __ldg(k.totals + 1), clusters = min(kClusters, total);
-  const bool idle = cluster >= clusters;
-  const int t0 = idle ? 0 : (int)((long long)total * cluster / clusters);
-  const int t1 = idle ? 0 : (int)((long long)total * (cluster + 1) / clusters);
+  const int4 part = __ldg(k.cpart + cluster);
+  const int t0 = part.y, t1 = part.z;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;
   int where = 0;
   // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1;
   // n counts the chunks before them, items the items.
   auto for_items = [&](auto body) {
-    int p = t0 < t1 ? __ldg(k.cpair + cluster) : 0;
+    int p = part.x;
     uint32_t n = 0, items = 0;
     for (int t = t0; t < t1 && good; ++p) {
       const int pend = k.pairs[p + 1].chunk0;
@@ -1239,15 +1236,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int total = __ldg(k.totals + 1), ctas = min(kAlone, total);
-  const bool idle = cta >= ctas;
-  const int t0 = idle ? 0 : (int)((long long)total * cta / ctas);
-  const int t1 = idle ? 0 : (int)((long long)total * (cta + 1) / ctas);
+  const int4 part = __ldg(k.cpart + cta);
+  const int t0 = part.y, t1 = part.z;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;
   int where = 0;
   auto for_items = [&](auto body) {  // as in k_prefix_attn, over queries
-    int p = t0 < t1 ? __ldg(k.cpair + cta) : 0;
+    int p = part.x;
     uint32_t n = 0, items = 0;
     for (int t = t0; t < t1 && good; ++p) {
       const int first = k.pairs[p].chunk0, nc = min(k.pairs[p + 1].chunk0, t1) - t, c0 = t - first;
@@ -1435,7 +1430,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         }
         lsum = fmaf(alpha, lsum, sum);
       }
-      // ---- this item's partial: O^T / l in f16, [channel][head]
+      // ---- this item's partial: O^T / l in f16; uint4 (c, u) of thread t holds heads 32 (c % 2) + 8 u .. of
+      // channel 128 (c / 2) + t, so that every store is 512 contiguous bytes
       const uint32_t last = n + (uint32_t)nc - 1;
       good = good && wait(&S.x_free[last & 1u][0], last >> 1) && wait(&S.x_free[last & 1u][1], last >> 1);
       good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // the four warps leave together, or none
@@ -1453,7 +1449,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         uint32_t a[32];
         ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
         ptx::tmem_wait_ld();
-        uint4* po = k.part_o + (slot * kDMain + 128 * (c >> 1) + 32 * warp + lane) * 8 + 4 * (c & 1);
+        uint4* po = k.part_o + (slot * 32 + 4 * c) * 128 + tid;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           uint32_t w[4];
@@ -1464,7 +1460,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                                                  __uint_as_float(a[8 * u + 2 * v + 1]) * i2.y);
             w[v] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          po[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          po[u * 128] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       softmax_sync();  // alpha is written again
@@ -1491,96 +1487,112 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   }
 }
 
-// The join over partials of [channel][head]: thread t of a slice has heads 2 (t % 32), + 1 and the eight
-// channels 32 blockIdx.y + 8 (t / 32) .. (a warp reads 128 contiguous bytes of a channel's 64 heads).
+// The join over partials of the epilogue's order: a CTA has eight heads 32 (y / 4 % 2) + 8 (y % 4) .. of the 128
+// channels 128 (y / 8) .. (y = blockIdx.y), thread t of a slice the channel t of them.  The weights
+// 2^(m_i - m) l_i / L are the same for all channels: the CTA forms them once, while the first partials' channels
+// are on their way.
 template <int kSlices>
 __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __restrict__ qpart,
-                                                               const uint32_t* __restrict__ part_o,
+                                                               const uint4* __restrict__ part_o,
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
                                                                int out_bf16, float* __restrict__ lse) {
-  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][20][128];
+  __shared__ float s_m[kAlone][8], s_w[kAlone][8];
+  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][8][128];
   ptx::griddep_wait();
-  const int b = blockIdx.x, slice = threadIdx.x >> 7, t = threadIdx.x & 127, h2 = t & 31;
-  const int cc = 32 * blockIdx.y + 8 * (t >> 5);
-  const int2 part = qpart[b];  // the first partial's slot, partials
-  Join<8> a[2];
+  const int b = blockIdx.x, y = blockIdx.y, slice = threadIdx.x >> 7, t = threadIdx.x & 127;
+  const int h0 = 32 * ((y >> 2) & 1) + 8 * (y & 3), c = 128 * (y >> 3) + t;
+  const int2 part = qpart[b];  // the first partial's slot, partials (at most one a CTA)
+  for (int i = threadIdx.x; i < part.y * 8; i += kSlices * 128) {
+    const float2 ml = part_ml[(int64_t)(part.x + i / 8) * kHAtt + h0 + i % 8];
+    s_m[i / 8][i % 8] = ml.y > 0.0f ? ml.x : -INFINITY;
+    s_w[i / 8][i % 8] = ml.y;
+  }
+  uint4 v[kJoin];
+  auto fetch = [&](int k0) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) a[i].start(slice == 0 && sink ? sink[2 * h2 + i] * kLog2e : -INFINITY);
-  for (int c0 = slice; c0 < part.y; c0 += kSlices * kJoin) {
-    float4 ml[kJoin];  // reference and sum of both heads
-    uint32_t v[kJoin][8];
+    for (int j = 0; j < kJoin; ++j)
+      if (k0 + j * kSlices < part.y) v[j] = part_o[((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * 128 + t];
+  };
+  fetch(slice);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < 8; i += kSlices * 4) {  // a warp per head
+    const float z = sink ? sink[h0 + i] * kLog2e : -INFINITY;
+    float ref = z;
+    for (int j = lane; j < part.y; j += 32) ref = fmaxf(ref, s_m[j][i]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    float L = 0.0f;
+    for (int j = lane; j < part.y; j += 32) {
+      const float w = s_m[j][i] > -INFINITY ? ptx::ex2(s_m[j][i] - ref) * s_w[j][i] : 0.0f;
+      s_w[j][i] = w;
+      L += w;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (z > -INFINITY) L += ptx::ex2(z - ref);
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
+    if (lse && y < 8 && lane == 0) lse[b * kHAtt + h0 + i] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
+  }
+  __syncthreads();
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  for (int k0 = slice; k0 < part.y; k0 += kSlices * kJoin) {
+    if (k0 > slice) fetch(k0);
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      ml[j] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-      if (c0 + j * kSlices < part.y) {
-        const int64_t slot = part.x + (int64_t)(c0 + j * kSlices);
-        ml[j] = *reinterpret_cast<const float4*>(part_ml + slot * kHAtt + 2 * h2);
+      const int k = k0 + j * kSlices;
+      if (k >= part.y) break;
+      const float4 w0 = *reinterpret_cast<const float4*>(&s_w[k][0]), w1 = *reinterpret_cast<const float4*>(&s_w[k][4]);
+      const float f[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[j][u] = part_o[(slot * kDMain + cc + u) * 32 + h2];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float top = a[i].ref;
-#pragma unroll
-      for (int j = 0; j < kJoin; ++j)
-        if ((i ? ml[j].w : ml[j].y) > 0.0f) top = fmaxf(top, i ? ml[j].z : ml[j].x);
-      a[i].raise(top);
-#pragma unroll
-      for (int j = 0; j < kJoin; ++j) {
-        const float l = i ? ml[j].w : ml[j].y;
-        if (!(l > 0.0f)) continue;
-        const float f = ptx::ex2((i ? ml[j].z : ml[j].x) - a[i].ref) * l;
-        a[i].L += f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j][u]));
-          a[i].acc[u] = fmaf(f, i ? x.y : x.x, a[i].acc[u]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        acc[2 * i] = fmaf(f[2 * i], x.x, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(f[2 * i + 1], x.y, acc[2 * i + 1]);
       }
     }
   }
-  if (slice > 0) {
+  if (kSlices > 1) {
+    if (slice > 0)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s_join[slice - 1][10 * i][t] = a[i].ref;
-      s_join[slice - 1][10 * i + 1][t] = a[i].L;
+      for (int i = 0; i < 8; ++i) s_join[slice - 1][i][t] = acc[i];
+    __syncthreads();
+    if (slice > 0) return;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s_join[slice - 1][10 * i + 2 + u][t] = a[i].acc[u];
-    }
+    for (int j = 0; j < kSlices - 1; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += s_join[j][i][t];
   }
-  if (kSlices > 1) __syncthreads();
-  if (slice > 0) return;
+  const bool rotated = turn && (y >> 3) == 3 && t >= 64;  // whole warps: channels 448 ..
+  float cs = 1.0f, sn = 0.0f;
+  if (rotated) {  // turn back by -q_pos: x' = x c + y s, y' = y c - x s, pairs in neighbouring lanes
+    const float2 r = turn[(int64_t)b * 32 + (t - 64) / 2];
+    cs = r.x;
+    sn = t & 1 ? -r.y : r.y;
+  }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    for (int j = 0; j < kSlices - 1; ++j) {
-      const float m = s_join[j][10 * i][t], l = s_join[j][10 * i + 1][t];
-      if (!(l > 0.0f)) continue;
-      a[i].raise(m);
-      const float f = ptx::ex2(m - a[i].ref);
-      a[i].L = fmaf(f, l, a[i].L);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) a[i].acc[u] = fmaf(f, s_join[j][10 * i + 2 + u][t], a[i].acc[u]);
+  for (int i = 0; i < 8; ++i) {
+    float o = acc[i];
+    if (rotated) {
+      const float partner = __shfl_xor_sync(0xffffffffu, o, 1);
+      o = fmaf(o, cs, partner * sn);
     }
-    const int h = 2 * h2 + i;
-    const float inv = a[i].L > 0.0f ? 1.0f / a[i].L : 0.0f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) a[i].acc[u] *= inv;
-    if (turn && cc >= kRopeFirst) {  // turn back by -q_pos
-      const float2* cs = turn + (int64_t)b * 32 + (cc - kRopeFirst) / 2;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) rope_pair(a[i].acc[2 * u], a[i].acc[2 * u + 1], cs[u].x, -cs[u].y);
-    }
-    store_channels<8>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + cc, a[i].acc);
-    if (lse && cc == 0) lse[b * kHAtt + h] = a[i].L > 0.0f ? (a[i].ref + log2f(a[i].L)) / kLog2e : -INFINITY;
+    const int64_t at = ((int64_t)b * kHAtt + h0 + i) * kDMain + c;
+    if (out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
+    else static_cast<float*>(out)[at] = o;
   }
 }
 
 struct PrefixWs {
   Pair* pairs;
-  int32_t *gpair, *chunk0, *cpair, *totals, *gimage;
+  int32_t *gpair, *chunk0, *gimage;
+  int4* cpart;
   int2* qpart;
   uint16_t *image, *qimage;
   float* c2;
@@ -1607,8 +1619,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.chunk0 = (int32_t*)take(((size_t)max_pairs(B, G) + 1) * 4);
   L.qpart = (int2*)take((size_t)B * 8);
-  L.cpair = (int32_t*)take(parts * 4);
-  L.totals = (int32_t*)take(8);
+  L.cpart = (int4*)take(parts * 16);
   L.gimage = (int32_t*)take((size_t)G * 4);
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
@@ -1687,12 +1698,12 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.cpair, L.totals,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.cpart,
                      L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
-                       L.pairs, L.cpair, L.totals, L.part_o, L.part_ml, ws};
+                       L.pairs, L.cpart, L.part_o, L.part_ml, ws};
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
                        L.qimage, L.c2, L.turn};
   ImageMaps maps{};
@@ -1718,8 +1729,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
       launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
     }
     KernelTimer timer("k_paged_merge", st);
-    launch_pdl(slices > 1 ? k_paged_merge<4> : k_paged_merge<1>, dim3(B, kDMain / 32), dim3(128 * slices), 0, st, (const int2*)L.qpart,
-               (const uint32_t*)L.part_o, (const float2*)L.part_ml, sink,
+    launch_pdl(slices > 1 ? k_paged_merge<4> : k_paged_merge<1>, dim3(B, 32), dim3(128 * slices), 0, st, (const int2*)L.qpart,
+               (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
                ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
     return launch_status();
   }
