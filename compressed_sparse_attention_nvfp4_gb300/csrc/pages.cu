@@ -208,7 +208,7 @@ __device__ void plan_block(const PageArgs& a, const PlanView& v) {
   __syncthreads();
 }
 
-// Map rows [r0, r1) by the calling threads (tid of n), requests by their warps.
+// The map's rows, by the calling threads (row r, r + step, ..).
 __device__ void fill_rows(const PageArgs& a, const PlanView& v, int64_t r, int64_t step) {
   const int total = v.st->total_rows;
   for (; r < a.n_rows; r += step) {
@@ -229,17 +229,16 @@ __device__ void fill_rows(const PageArgs& a, const PlanView& v, int64_t r, int64
     if (a.pos) a.pos[r] = pos;
   }
 }
-__device__ void fill_requests(const PageArgs& a, const PlanView& v, int warp, int n_warps) {
+// The pages that move, by the calling threads (tid i of step): taken ones into their rows, given back
+// ones onto the stack.
+__device__ void fill_pages(const PageArgs& a, const PlanView& v, int64_t first, int64_t step) {
   if (!v.st->ok) return;
-  const int lane = threadIdx.x & 31;
-  for (int b = warp; b < a.B; b += n_warps) {
-    const int need = v.need[b + 1] - v.need[b], gone = v.gone[b + 1] - v.gone[b];
-    if (!need && !gone) continue;
-    const int pc = pages_of(v.have[b], a.P);
-    int32_t* row = a.table + (int64_t)b * a.max_pages;
-    for (int i = lane; i < need; i += 32) row[pc + i] = taken_page(a, v, v.need[b] + i);
-    for (int i = lane; i < gone; i += 32) a.free_pages[v.st->n_free + v.gone[b] + i] = row[pc - gone + i];
+  const int taken = v.need[a.B], gone = v.gone[a.B];
+  for (int64_t i = first; i < taken; i += step) {
+    const int b = find_le(v.need, 0, a.B, (int)i);
+    a.table[(int64_t)b * a.max_pages + pages_of(v.have[b], a.P) + i - v.need[b]] = taken_page(a, v, (int)i);
   }
+  for (int64_t i = first; i < gone; i += step) a.free_pages[v.st->n_free + i] = gone_page(a, v, (int)i);
 }
 
 // Everything in one CTA, the plan in shared memory.
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_tables(PageArgs a) {
   const PlanView v{smem, smem + a.B, smem + 2 * a.B + 1, smem + 3 * a.B + 2, &st};
   ptx::griddep_wait();
   plan_block(a, v);
-  fill_requests(a, v, threadIdx.x / 32, blockDim.x / 32);
+  fill_pages(a, v, threadIdx.x, blockDim.x);
   fill_rows(a, v, threadIdx.x, blockDim.x);
 }
 
@@ -263,7 +262,7 @@ constexpr int kFillThreads = 256;
 __global__ void __launch_bounds__(kFillThreads) k_page_fill(PageArgs a, PlanView v) {
   ptx::griddep_wait();
   const int64_t t = (int64_t)blockIdx.x * kFillThreads + threadIdx.x, n = (int64_t)gridDim.x * kFillThreads;
-  fill_requests(a, v, (int)(t / 32), (int)(n / 32));
+  fill_pages(a, v, t, n);
   fill_rows(a, v, t, n);
 }
 
@@ -333,7 +332,7 @@ extern "C" csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const 
       KernelTimer timer("k_page_plan", st);
       launch_pdl(k_page_plan, dim3(1), dim3(kPlanThreads), 0, st, a, v);
     }
-    const int64_t threads = n_rows > (int64_t)B * 32 ? n_rows : (int64_t)B * 32;
+    const int64_t threads = n_rows > 4096 ? n_rows : 4096;
     const int blocks = (int)(cdiv(threads, kFillThreads) < 1216 ? cdiv(threads, kFillThreads) : 1216);
     KernelTimer timer("k_page_fill", st);
     launch_pdl(k_page_fill, dim3(blocks), dim3(kFillThreads), 0, st, a, v);

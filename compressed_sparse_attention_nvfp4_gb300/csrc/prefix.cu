@@ -255,10 +255,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
 // warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), where rows come from
 constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kIndexWarp = 22;
 constexpr int kThreads = 24 * 32;  // and one that fills the last warpgroup
-// registers of a thread: 80 at launch, which the row warpgroups keep; the softmax takes what the last
-// warpgroup gives back
-constexpr int kSoftRegs = 96, kMmaRegs = 64;
-static_assert(kSoftRegs + 4 * 80 + kMmaRegs <= 6 * 80, "registers of the launch");
+// registers of a thread: 80 at launch, which the last warpgroup keeps; the softmax takes what the row
+// warpgroups give back
+constexpr int kSoftRegs = 104, kRowRegs = 72;
+static_assert(kSoftRegs + 4 * kRowRegs + 80 <= 6 * 80, "registers of the launch");
 constexpr int kPieces = 4;
 constexpr uint32_t kCols = 512;   // tensor memory: O 2 x 128 columns, S 2 x 64
 constexpr uint32_t kColS = 256;
@@ -606,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   };
 
   if (warp >= kRowWarp && warp < kSMma) {
+    ptx::setmaxnreg_dec<kRowRegs>();
     good = rows_role(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
     where = 31;
   } else if (warp >= kSMma) {
-    ptx::setmaxnreg_dec<kMmaRegs>();
     // the odd CTA's MMA warps pass their CTA's arrivals on, in the order the even CTA's wait for them
     auto pass = [&](uint64_t* bar, uint32_t ph) {
       if (good) good = wait(bar, ph);
@@ -1154,8 +1154,6 @@ static_assert(sizeof(AloneSmem) <= 232448, "attention shared memory");
 // warps 0-3: softmax and epilogue; 4-19: rows (4-11 channels 0-255, 12-19 the others); then S MMAs of each
 // half, O MMAs, where rows come from
 constexpr int kAloneS = 20, kAloneO = 22, kAloneIndex = 23;
-constexpr int kAloneSoftRegs = 128, kAloneRowRegs = 72, kAloneMmaRegs = 64;
-static_assert(kAloneSoftRegs + 4 * kAloneRowRegs + kAloneMmaRegs <= 6 * 80, "registers of the launch");
 
 // The rows of all `chunks` chunks of this CTA, whatever queries they belong to: thread's row 8 (w % 8) + l % 8,
 // blocks (of 32 channels) 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
@@ -1255,11 +1253,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   };
 
   if (warp >= 4 && warp < kAloneS) {
-    ptx::setmaxnreg_dec<kAloneRowRegs>();
+    ptx::setmaxnreg_dec<kRowRegs>();
     good = alone_rows(S, k, t1 - t0, warp - 4, lane);
     where = 41;
   } else if (warp >= kAloneS) {
-    ptx::setmaxnreg_dec<kAloneMmaRegs>();
     if (warp == kAloneIndex) {
       for_items([&](int p, int c0, int nc, uint32_t n, uint32_t) {
         const Pair x = k.pairs[p];
@@ -1351,7 +1348,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   } else {
     // ---- softmax: lane l of warp w head 16 w + l % 16, chunk rows 32 (l / 16) .. (the rows of an M = 64
     // accumulator lie in lanes 0-15 of each quarter; two lanes share a head's columns)
-    ptx::setmaxnreg_inc<kAloneSoftRegs>();
+    ptx::setmaxnreg_inc<kSoftRegs>();
     const int rh = lane >> 4, h = 16 * warp + (lane & 15);
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
