@@ -869,16 +869,29 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     if (threadIdx.x < kHAtt) a.c2[(int64_t)b * kHAtt + threadIdx.x] = 1.0f;
     return;
   }
+  constexpr int kHeads = kHAtt / (kPrepThreads / 32);
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + warp * kHeads) * kDMain) + 2 * lane;
+  uint4 qv[kHeads][2];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    qv[i][0] = src[i * (kDMain / 8)];
+    qv[i][1] = src[i * (kDMain / 8) + 1];
+  }
+  __shared__ float2 s_turn[32];
   float rc = 1.0f, rs = 0.0f;  // lane l: pair l
   if (a.rope) {
-    rope_cos_sin(a.th.t[lane], (double)a.qpos[b], rc, rs);
-    if (warp == 0) a.turn[(int64_t)b * 32 + lane] = make_float2(rc, rs);
+    if (warp == 0) {  // one warp: the angles are formed in fp64, of which an SM does little
+      rope_cos_sin(a.th.t[lane], (double)a.qpos[b], rc, rs);
+      s_turn[lane] = a.turn[(int64_t)b * 32 + lane] = make_float2(rc, rs);
+    }
+    __syncthreads();
+    rc = s_turn[lane].x;
+    rs = s_turn[lane].y;
   }
-#pragma unroll 1
-  for (int i = 0; i < kHAtt / (kPrepThreads / 32); ++i) {
-    const int h = warp * (kHAtt / (kPrepThreads / 32)) + i;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + h) * kDMain) + 2 * lane;
-    const uint4 q0 = src[0], q1 = src[1];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = warp * kHeads + i;
+    const uint4 q0 = qv[i][0], q1 = qv[i][1];
     const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
     float v[16];
 #pragma unroll
