@@ -46,6 +46,14 @@ struct Pair {
   int32_t image;   // the shared entries' first chunk in the image, or -1
 };
 
+// What one part (a CTA, or a pair of CTAs) of the attention launch runs: chunks [t0, t1) of the order of all
+// pairs' chunks, beginning in `pair`, number p, whose chunks end at `end`.  The first item needs no further
+// load.
+struct __align__(16) Part {
+  int32_t p, t0, t1, end;
+  Pair pair;
+};
+
 // The queries' staging: what it reads, and where it leaves their images.
 struct PrefixQuery {
   const uint16_t* q;
@@ -70,7 +78,7 @@ struct PrefixArgs {
   int32_t* gpair;     // [G + 3] first pair of each range of queries
   int32_t* chunk0;    // [pairs + 1] first chunk of each pair (these two where shared memory is too small)
   int2* qpart;        // [B] first partial (see the merges), partials
-  int4* cpart;        // [parts] of each part: first pair, first chunk, end
+  Part* parts_of;     // [parts]
   int32_t* gimage;    // [G] first image chunk of each group, or -1
   int64_t image_cap;  // chunks the image has room for
   int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
@@ -235,7 +243,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   }
   for (int c = tid; c < a.parts; c += kPrepThreads) {
     if (c >= clusters) {
-      a.cpart[c] = make_int4(0, 0, 0, 0);
+      a.parts_of[c] = Part{};
       continue;
     }
     const int t0 = (int)((long long)chunks * c / clusters), t1 = (int)((long long)chunks * (c + 1) / clusters);
@@ -245,7 +253,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
       if (chunk0[mid] <= t0) lo = mid;
       else hi = mid;
     }
-    a.cpart[c] = make_int4(lo, t0, t1, 0);
+    a.parts_of[c] = Part{lo, t0, t1, chunk0[lo + 1], a.pairs[lo]};
   }
 }
 
@@ -275,7 +283,7 @@ struct __align__(1024) PrefixSmem {
   // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
   // of the same role passes on for all of that CTA's
   uint64_t q_land, q_peer;                  // q' copied; the odd CTA's q'
-  uint64_t r_full[4], r_free[4];            // rows written (one warp); read (16 row and 4 softmax warps)
+  uint64_t i_full[4], r_full[4], r_free[4]; // image, rows written (one warp); read (16 row and 4 softmax warps)
   uint64_t x_full[2][kPieces], x_free[2][kPieces];  // [0] S's operand, [1] O's
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_read;                          // epilogue done with O
@@ -295,7 +303,7 @@ struct PrefixKernel {
   uint64_t page_div;  // ceil(2^40 / page_entries): e * page_div >> 40 = e / page_entries for e < 2^18
   const int64_t *win_pos, *win_lo;
   const Pair* pairs;
-  const int4* cpart;
+  const Part* parts;
   uint4* part_o;    // [pairs + clusters][2][32][128]: eight f16 channels c8 of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
@@ -459,8 +467,10 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
     const uint32_t m = (uint32_t)(st >> 1), slot = m & 3u;
     const int i = 2 * (st & 1) + group;
     if ((st & 1) == 0) {
-      good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
+      good = good && ptx::mbar_wait_warp(&S.i_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
       if (good) image = S.image[slot];
+      // rows found; a chunk of the image needs none
+      if (image < 0) good = good && ptx::mbar_wait_warp(&S.r_full[slot], (m >> 2) & 1u, &S.abort_flag, kWaitBudget);
     }
     if (!good) return;
     if (image < 0) {
@@ -525,15 +535,18 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
 #pragma unroll 1
   for (int j = 0; j < nc && good; ++j) {
     const uint32_t m = n + (uint32_t)j, slot = m & 3u;
+    if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
+    if (!good) break;
+    if (lane == 0) {
+      S.image[slot] = x.image >= 0 && c0 + j < x.nshared ? x.image + c0 + j : -1;
+      ptx::mbar_arrive(&S.i_full[slot]);
+    }
     int row[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] = resolve(k, r[i], report);
     if (j + 1 < nc) find(j + 1);
-    if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
-    if (!good) break;
 #pragma unroll
     for (int i = 0; i < 4; ++i) S.rows[slot][32 * i + lane] = row[i];
-    if (lane == 0) S.image[slot] = x.image >= 0 && c0 + j < x.nshared ? x.image + c0 + j : -1;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.r_full[slot]);
   }
@@ -559,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       }
       ptx::mbar_init(&S.q_land, 1);
       for (int i = 0; i < 4; ++i) {
+        ptx::mbar_init(&S.i_full[i], 1);
         ptx::mbar_init(&S.r_full[i], 1);
         ptx::mbar_init(&S.r_free[i], 20);
       }
@@ -583,25 +597,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  const int4 part = __ldg(k.cpart + cluster);
-  const int t0 = part.y, t1 = part.z;
+  const Part& part = k.parts[cluster];
+  const int t0 = part.t0, t1 = part.t1;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;
   int where = 0;
   // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1;
   // n counts the chunks before them, items the items.
   auto for_items = [&](auto body) {
-    int p = part.x;
+    const Pair* px = &part.pair;
+    int p = part.p, end = part.end;
     uint32_t n = 0, items = 0;
-    for (int t = t0; t < t1 && good; ++p) {
-      const int pend = k.pairs[p + 1].chunk0;
-      const Pair x = k.pairs[p];
-      const int c0 = t - x.chunk0, nc = min(pend, t1) - t;
-      if (nc <= 0) continue;  // a pair without chunks
-      t += nc;
-      body(x, p, c0, nc, n, items);
-      n += (uint32_t)nc;
-      ++items;
+    for (int t = t0; t < t1 && good;) {
+      const Pair x = *px;
+      const int c0 = t - x.chunk0, nc = min(end, t1) - t;
+      if (nc > 0) {  // else a pair without chunks
+        t += nc;
+        body(x, p, c0, nc, n, items);
+        n += (uint32_t)nc;
+        ++items;
+      }
+      px = k.pairs + ++p;
+      if (t < t1) end = k.pairs[p + 1].chunk0;
     }
   };
 
@@ -1247,21 +1264,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
-  const int4 part = __ldg(k.cpart + cta);
-  const int t0 = part.y, t1 = part.z;
+  const Part& part = k.parts[cta];
+  const int t0 = part.t0, t1 = part.t1;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;
   int where = 0;
   auto for_items = [&](auto body) {  // as in k_prefix_attn, over queries
-    int p = part.x;
+    const Pair* px = &part.pair;
+    int p = part.p, end = part.end;
     uint32_t n = 0, items = 0;
-    for (int t = t0; t < t1 && good; ++p) {
-      const int first = k.pairs[p].chunk0, nc = min(k.pairs[p + 1].chunk0, t1) - t, c0 = t - first;
-      if (nc <= 0) continue;
-      t += nc;
-      body(p, c0, nc, n, items);
-      n += (uint32_t)nc;
-      ++items;
+    for (int t = t0; t < t1 && good;) {
+      const int q = px->q0, own = px->own0, c0 = t - px->chunk0, nc = min(end, t1) - t;
+      if (nc > 0) {
+        t += nc;
+        body(q, own, p, c0, nc, n, items);
+        n += (uint32_t)nc;
+        ++items;
+      }
+      px = k.pairs + ++p;
+      if (t < t1) end = k.pairs[p + 1].chunk0;
     }
   };
 
@@ -1271,12 +1292,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     where = 41;
   } else if (warp >= kAloneS) {
     if (warp == kAloneIndex) {
-      for_items([&](int p, int c0, int nc, uint32_t n, uint32_t) {
-        const Pair x = k.pairs[p];
+      for_items([&](int q, int own, int, int c0, int nc, uint32_t n, uint32_t) {
         RowRef r[2];
         auto find = [&](int j) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) r[i] = find_own(k, x.q0, x.own0, (c0 + j) * kRows + 32 * i + lane);
+          for (int i = 0; i < 2; ++i) r[i] = find_own(k, q, own, (c0 + j) * kRows + 32 * i + lane);
         };
         find(0);
 #pragma unroll 1
@@ -1299,14 +1319,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       constexpr uint32_t idesc_s = ptx::idesc_f16(64, kRows, 0);
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[32 * half][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][32 * half][0], kRows * 16, 128);
-      for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](int q, int, int, int, int nc, uint32_t n, uint32_t items) {
         volatile int keep_waiting = 0;
         if (half == 0) {  // the item's query, once S of the item before has left q'; it lands before anyone leaves
           good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
           if (!good) return;
           if (lane == 0) {
             ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
-            ptx::bulk_g2s(&S.q[0][0], k.q + (int64_t)k.pairs[p].q0 * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
+            ptx::bulk_g2s(&S.q[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
           }
           __syncwarp();
           good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
@@ -1333,7 +1353,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       constexpr uint32_t idesc_o = ptx::idesc_f16(128, kHAtt, 0) | (1u << 15);  // A M-major
       const uint64_t da = ptx::smem_desc_noswizzle(&S.x[0][0][0], 128, kRows * 16);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
-      for_items([&](int, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](int, int, int, int, int nc, uint32_t n, uint32_t items) {
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j, slot = m & 1u;
@@ -1364,8 +1384,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     ptx::setmaxnreg_inc<kSoftRegs>();
     const int rh = lane >> 4, h = 16 * warp + (lane & 15);
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    for_items([&](int p, int, int nc, uint32_t n, uint32_t items) {
-      const int q = k.pairs[p].q0;
+    for_items([&](int q, int, int p, int, int nc, uint32_t n, uint32_t) {
       const float c2 = k.c2[(int64_t)q * kHAtt + h];
       float m2 = -INFINITY, lsum = 0.0f;
 #pragma unroll 1
@@ -1602,7 +1621,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
 struct PrefixWs {
   Pair* pairs;
   int32_t *gpair, *chunk0, *gimage;
-  int4* cpart;
+  Part* parts;
   int2* qpart;
   uint16_t *image, *qimage;
   float* c2;
@@ -1629,7 +1648,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.chunk0 = (int32_t*)take(((size_t)max_pairs(B, G) + 1) * 4);
   L.qpart = (int2*)take((size_t)B * 8);
-  L.cpart = (int4*)take(parts * 16);
+  L.parts = (Part*)take(parts * sizeof(Part));
   L.gimage = (int32_t*)take((size_t)G * 4);
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
@@ -1708,12 +1727,12 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.cpart,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
                      L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
-                       L.pairs, L.cpart, L.part_o, L.part_ml, ws};
+                       L.pairs, L.parts, L.part_o, L.part_ml, ws};
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
                        L.qimage, L.c2, L.turn};
   ImageMaps maps{};
