@@ -412,28 +412,58 @@ __device__ __forceinline__ void put(const Fetch& f, int r, uint16_t* dst, int st
   for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + q * stride) = v[q];
 }
 
+// packed fp32 arithmetic on two neighbouring registers
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // p = 2^(s c2 - m) of 32 rows, packed in pairs as f16 from the fp32 values whose sum goes to `sum`;
 // returns the largest exponent.  Rows that the mask has not are -inf.
-__device__ __forceinline__ float probs32(uint32_t (&s)[32], uint32_t mask, float c2, float m, uint32_t (&ph)[16],
+__device__ __forceinline__ float probs32(uint64_t (&s)[16], uint32_t mask, float c2, float m, uint32_t (&ph)[16],
                                          float& sum) {
+  const uint64_t cc = pack2(__float_as_uint(c2), __float_as_uint(c2));
+  const uint64_t mm = pack2(__float_as_uint(-m), __float_as_uint(-m));
 #pragma unroll
-  for (int u = 0; u < 32; ++u) s[u] = __float_as_uint(fmaf(__uint_as_float(s[u]), c2, -m));
+  for (int u = 0; u < 16; ++u) s[u] = fma2(s[u], cc, mm);
   if (mask != ~0u) {
 #pragma unroll
-    for (int u = 0; u < 32; ++u)
-      if (!((mask >> u) & 1u)) s[u] = __float_as_uint(-INFINITY);
+    for (int u = 0; u < 16; ++u) {
+      float e0, e1;
+      unpack2(s[u], e0, e1);
+      if (!((mask >> (2 * u)) & 1u)) e0 = -INFINITY;
+      if (!((mask >> (2 * u + 1)) & 1u)) e1 = -INFINITY;
+      s[u] = pack2(__float_as_uint(e0), __float_as_uint(e1));
+    }
   }
-  float top = -INFINITY, s0 = 0.0f, s1 = 0.0f;
+  float top = -INFINITY;
+  uint64_t acc = 0;
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
-    const float e0 = __uint_as_float(s[2 * u]), e1 = __uint_as_float(s[2 * u + 1]);
+    float e0, e1;
+    unpack2(s[u], e0, e1);
     top = fmaxf(top, fmaxf(e0, e1));
     const float p0 = ptx::ex2(e0), p1 = ptx::ex2(e1);
-    s0 += p0;
-    s1 += p1;
+    acc = add2(acc, pack2(__float_as_uint(p0), __float_as_uint(p1)));
     const __half2 h2 = __floats2half2_rn(p0, p1);
     ph[u] = *reinterpret_cast<const uint32_t*>(&h2);
   }
+  float s0, s1;
+  unpack2(acc, s0, s1);
   sum = s0 + s1;
   return top;
 }
@@ -762,10 +792,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               uint32_t a[32], ph[16];
+              uint64_t e[16];
               float s1;
               ptx::tmem_ld_32x32b_x32(tmem + lane_base + kColS + 64u * slot + 32u * (uint32_t)i, a);
               ptx::tmem_wait_ld();
-              top = fmaxf(top, probs32(a, i ? mk1 : mk0, c2, ref, ph, s1));
+#pragma unroll
+              for (int u = 0; u < 16; ++u) e[u] = pack2(a[2 * u], a[2 * u + 1]);
+              top = fmaxf(top, probs32(e, i ? mk1 : mk0, c2, ref, ph, s1));
               sum += s1;
 #pragma unroll
               for (int u = 0; u < 4; ++u)
@@ -1407,9 +1440,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             ptx::tmem_ld_16x32bx2_x32<32>(ta, a);
             ptx::tmem_ld_16x32bx2_x32<32>(ta + 128u, b);
             ptx::tmem_wait_ld();
+            uint64_t e[16];
 #pragma unroll
-            for (int u = 0; u < 32; ++u) a[u] = __float_as_uint(__uint_as_float(a[u]) + __uint_as_float(b[u]));
-            top = probs32(a, mask, c2, ref, ph, sum);
+            for (int u = 0; u < 16; ++u) e[u] = add2(pack2(a[2 * u], a[2 * u + 1]), pack2(b[2 * u], b[2 * u + 1]));
+            top = probs32(e, mask, c2, ref, ph, sum);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               *reinterpret_cast<uint4*>(&S.p[slot][4 * rh + u][h * 8]) =
