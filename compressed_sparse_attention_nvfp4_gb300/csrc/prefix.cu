@@ -65,6 +65,8 @@ struct PrefixQuery {
   uint16_t* image;  // [B + 1][c/8][head][c%8] f16
   float* c2;        // [B + 1][64]
   float2* turn;     // [B][32]
+  uint16_t* rest;   // [B][head][c] what the rounding to f16 took from q', in q's scale (f16); null: not kept
+  int32_t* count;   // [B] zeroed with it
 };
 
 struct PrefixArgs {
@@ -362,9 +364,18 @@ __device__ __forceinline__ int resolve(const PrefixKernel& k, RowRef r, bool rep
   return r.page * k.page_entries + r.off;
 }
 
+// A NaN (a scale or a window value 0x7F, 0xFF) becomes lim, which every finite E4M3 value is at most; a NaN
+// lim leaves all as it is.
+constexpr uint32_t kAnyValue = 0x7FFF7FFFu, kFinite = 0x5F005F00u;  // 448, E4M3's largest
+__device__ __forceinline__ uint32_t min2_u32(uint32_t x, uint32_t lim) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(lim));
+  return r;
+}
 // 32 channels of an entry (16 bytes of codes, two scales) -> four 8-channel vectors of f16
-__device__ __forceinline__ void widen_codes(uint4 cw, uint32_t sc, uint4 (&v)[4]) {
-  const uint32_t s0 = e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u), s1 = e4m3x2_to_f16x2((sc >> 8) * 0x0101u);
+__device__ __forceinline__ void widen_codes(uint4 cw, uint32_t sc, uint32_t lim, uint4 (&v)[4]) {
+  const uint32_t s0 = min2_u32(e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u), lim);
+  const uint32_t s1 = min2_u32(e4m3x2_to_f16x2((sc >> 8) * 0x0101u), lim);
   const uint32_t wq[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -375,9 +386,10 @@ __device__ __forceinline__ void widen_codes(uint4 cw, uint32_t sc, uint4 (&v)[4]
   }
 }
 // 16 channels of a window row
-__device__ __forceinline__ void widen_e4m3(uint4 w, uint4& a, uint4& b) {
-  a = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
-  b = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
+__device__ __forceinline__ void widen_e4m3(uint4 w, uint32_t lim, uint4& a, uint4& b) {
+  auto two = [&](uint32_t x) { return min2_u32(e4m3x2_to_f16x2(x), lim); };
+  a = make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
+  b = make_uint4(two(w.z), two(w.z >> 16), two(w.w), two(w.w >> 16));
 }
 
 // One thread's fetched codes of 32 channels of a row.
@@ -397,13 +409,13 @@ __device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int r, in
   }
 }
 // Writes the fetched block of row r to dst: vector q of it at dst + q * stride (f16 elements).
-__device__ __forceinline__ void put(const Fetch& f, int r, uint16_t* dst, int stride) {
+__device__ __forceinline__ void put(const Fetch& f, int r, uint16_t* dst, int stride, uint32_t lim = kAnyValue) {
   uint4 v[4];
   if (r >= 0) {
-    widen_codes(f.codes, f.scales, v);
+    widen_codes(f.codes, f.scales, lim, v);
   } else if (r < kNoRow) {
-    widen_e4m3(f.codes, v[0], v[1]);
-    widen_e4m3(f.more, v[2], v[3]);
+    widen_e4m3(f.codes, lim, v[0], v[1]);
+    widen_e4m3(f.more, lim, v[2], v[3]);
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -536,7 +548,7 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
       __syncwarp();
     } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) put(f[u], r[u], dst + i * dst_step + u * dst_u, plane);
+      for (int u = 0; u < 2; ++u) put(f[u], r[u], dst + i * dst_step + u * dst_u, plane, op ? kFinite : kAnyValue);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
@@ -562,13 +574,17 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
     for (int i = 0; i < 4; ++i) r[i] = find_row(k, x, c0 + j, 32 * i + lane);
   };
   find(0);
+  // the image serves both operands: only where both queries see all of a chunk's entries
+  const int seen = x.q1 >= 0 ? min(x.vis0, x.vis1) : x.vis0;
 #pragma unroll 1
   for (int j = 0; j < nc && good; ++j) {
     const uint32_t m = n + (uint32_t)j, slot = m & 3u;
     if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) break;
     if (lane == 0) {
-      S.image[slot] = x.image >= 0 && c0 + j < x.nshared ? x.image + c0 + j : -1;
+      S.image[slot] = x.image >= 0 && c0 + j < x.nshared && min((c0 + j + 1) * kChunk, x.ns) <= seen
+                          ? x.image + c0 + j
+                          : -1;
       ptx::mbar_arrive(&S.i_full[slot]);
     }
     int row[4];
@@ -919,6 +935,7 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     if (threadIdx.x < kHAtt) a.c2[(int64_t)b * kHAtt + threadIdx.x] = 1.0f;
     return;
   }
+  if (a.rest && threadIdx.x == 0) a.count[b] = 0;
   constexpr int kHeads = kHAtt / (kPrepThreads / 32);
   const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + warp * kHeads) * kDMain) + 2 * lane;
   uint4 qv[kHeads][2];
@@ -981,11 +998,19 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const int sig = mx > 0.0f ? min(max(floor_log2_f32(mx) - 14, -126), 126) : 0;
     const float inv = exp2i_f32(-sig);
-    uint32_t o[8];
+    uint32_t o[8], rest[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const __half2 h2 = __floats2half2_rn(v[2 * j] * inv, v[2 * j + 1] * inv);
+      const float v0 = v[2 * j] * inv, v1 = v[2 * j + 1] * inv;
+      const __half2 h2 = __floats2half2_rn(v0, v1);
+      const __half2 r2 = __floats2half2_rn(v0 - __low2float(h2), v1 - __high2float(h2));
       o[j] = *reinterpret_cast<const uint32_t*>(&h2);
+      rest[j] = *reinterpret_cast<const uint32_t*>(&r2);
+    }
+    if (a.rest) {
+      uint4* rp = reinterpret_cast<uint4*>(a.rest + ((int64_t)b * kHAtt + h) * kDMain) + 2 * lane;
+      rp[0] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+      rp[1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
     }
     *reinterpret_cast<uint4*>(smem + (2 * lane) * kQPad + h * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(smem + (2 * lane + 1) * kQPad + h * 16) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -1090,7 +1115,7 @@ struct Join {
   float ref, L, acc[kC];
   __device__ __forceinline__ void start(float z) {  // z: the sink's logit (log2 units) or -inf
     ref = z;
-    L = z > -INFINITY ? 1.0f : 0.0f;
+    L = z == -INFINITY ? 0.0f : 1.0f;
 #pragma unroll
     for (int u = 0; u < kC; ++u) acc[u] = 0.0f;
   }
@@ -1104,6 +1129,38 @@ struct Join {
   }
 };
 
+// The logsumexp of queries that were rounded to f16.  With q = q' + r, r of at most 2^-11 |q|, the joins give
+// lse(q'), and lse(q) = lse(q') + E + (at most w^2 / 8), E = the mean of scale r x under q's own weights and w the
+// width of scale r x over the rows (Hoeffding's lemma): E = scale r o with the output o before it turns back.
+// Without it one row of 512 normal channels is off by 2 10^-4, with it by 10^-8.  A CTA leaves the part of its
+// channels, and the last CTA of a query adds them up, in the order of the CTAs.
+struct LseRest {
+  const uint16_t* rest;  // null: q was not rounded, or no logsumexp is asked for
+  const float* c2;
+  float* dots;  // [B][parts][64]
+  int32_t* count;
+};
+__device__ __forceinline__ float rest_of(const LseRest& f, int64_t at) {
+  return __half2float(__ushort_as_half(f.rest[at]));
+}
+// 128 threads of each of `ctas` CTAs, their dots written: the last CTA's finish the heads of query b.
+__device__ __forceinline__ void finish_lse(const LseRest& f, int b, int t, int ctas, int parts, float* lse) {
+  __shared__ int s_last;
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  if (t == 0) {
+    __threadfence();
+    s_last = atomicAdd(f.count + b, 1) == ctas - 1;
+    __threadfence();
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  if (!s_last || t >= kHAtt) return;
+  float e = 0.0f;
+  for (int i = 0; i < parts; ++i) e += __ldcg(f.dots + ((int64_t)b * parts + i) * kHAtt + t);
+  const float l = __ldcg(lse + b * kHAtt + t);
+  // a query without rows may hold anything
+  if (l > -INFINITY && isfinite(e)) lse[b * kHAtt + t] = fmaf(e, f.c2[(int64_t)b * kHAtt + t] / kLog2e, l);
+}
+
 // Thread t of a slice: head t % 64 and, of channel half t / 64, the 16 channels 256 (t / 64) + 16 blockIdx.y ..
 template <int kSlices>
 __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __restrict__ qpart,
@@ -1111,7 +1168,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
                                                                 const float2* __restrict__ part_ml,
                                                                 const float* __restrict__ sink,
                                                                 const float2* __restrict__ turn, void* __restrict__ out,
-                                                                int out_bf16, float* __restrict__ lse) {
+                                                                int out_bf16, float* lse, LseRest fix) {
   __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][18][128];
   ptx::griddep_wait();
   const int b = blockIdx.x, slice = threadIdx.x >> 7, t = threadIdx.x & 127, h = t & 63, half = t >> 6;
@@ -1134,11 +1191,11 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
     float top = a.ref;
 #pragma unroll
     for (int i = 0; i < kJoin; ++i)
-      if (ml[i].y > 0.0f) top = fmaxf(top, ml[i].x);
+      if (ml[i].y != 0.0f) top = fmaxf(top, ml[i].x);
     a.raise(top);
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {
-      if (!(ml[i].y > 0.0f)) continue;
+      if (ml[i].y == 0.0f) continue;
       const float f = ptx::ex2(ml[i].x - a.ref) * ml[i].y;
       a.L += f;
 #pragma unroll
@@ -1163,7 +1220,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
   if (slice > 0) return;
   for (int i = 0; i < kSlices - 1; ++i) {
     const float m = s_join[i][0][t], l = s_join[i][1][t];
-    if (!(l > 0.0f)) continue;
+    if (l == 0.0f) continue;
     a.raise(m);
     const float f = ptx::ex2(m - a.ref);
     a.L = fmaf(f, l, a.L);
@@ -1174,14 +1231,27 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
   const int c0 = 256 * half + 16 * blockIdx.y;
 #pragma unroll
   for (int u = 0; u < 16; ++u) a.acc[u] *= inv;
+  if (lse && blockIdx.y == 0 && half == 0)
+    lse[b * kHAtt + h] = a.L == 0.0f ? -INFINITY : (a.ref + log2f(a.L)) / kLog2e;
+  if (fix.rest) {
+    const uint4* rp = reinterpret_cast<const uint4*>(fix.rest + ((int64_t)b * kHAtt + h) * kDMain + c0);
+    const uint4 r0 = rp[0], r1 = rp[1];
+    const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+    float e = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[u]));
+      e = fmaf(x.x, a.acc[2 * u], fmaf(x.y, a.acc[2 * u + 1], e));
+    }
+    fix.dots[((int64_t)b * 32 + 2 * blockIdx.y + half) * kHAtt + h] = e;
+  }
   if (turn && c0 >= kRopeFirst) {  // turn back by -q_pos
     const float2* cs = turn + (int64_t)b * 32 + (c0 - kRopeFirst) / 2;
 #pragma unroll
     for (int u = 0; u < 8; ++u) rope_pair(a.acc[2 * u], a.acc[2 * u + 1], cs[u].x, -cs[u].y);
   }
   store_channels<16>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + c0, a.acc);
-  if (lse && blockIdx.y == 0 && half == 0)
-    lse[b * kHAtt + h] = a.L > 0.0f ? (a.ref + log2f(a.L)) / kLog2e : -INFINITY;
+  if (fix.rest) finish_lse(fix, b, t, 16, 32, lse);
 }
 
 // ------------------------------------------------------------ queries alone
@@ -1560,8 +1630,9 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
-                                                               int out_bf16, float* __restrict__ lse) {
-  __shared__ float s_m[kAlone][8], s_w[kAlone][8];
+                                                               int out_bf16, float* lse, LseRest fix) {
+  __shared__ __align__(16) float s_w[kAlone][8];  // read four at a time
+  __shared__ float s_m[kAlone][8], s_dot[4][8];
   __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][8][128];
   ptx::griddep_wait();
   const int b = blockIdx.x, y = blockIdx.y, slice = threadIdx.x >> 7, t = threadIdx.x & 127;
@@ -1569,7 +1640,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
   const int2 part = qpart[b];  // the first partial's slot, partials (at most one a CTA)
   for (int i = threadIdx.x; i < part.y * 8; i += kSlices * 128) {
     const float2 ml = part_ml[(int64_t)(part.x + i / 8) * kHAtt + h0 + i % 8];
-    s_m[i / 8][i % 8] = ml.y > 0.0f ? ml.x : -INFINITY;
+    s_m[i / 8][i % 8] = ml.y == 0.0f ? -INFINITY : ml.x;
     s_w[i / 8][i % 8] = ml.y;
   }
   uint4 v[kJoin];
@@ -1589,16 +1660,16 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
     for (int o = 16; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     float L = 0.0f;
     for (int j = lane; j < part.y; j += 32) {
-      const float w = s_m[j][i] > -INFINITY ? ptx::ex2(s_m[j][i] - ref) * s_w[j][i] : 0.0f;
+      const float w = s_w[j][i] == 0.0f ? 0.0f : ptx::ex2(s_m[j][i] - ref) * s_w[j][i];
       s_w[j][i] = w;
       L += w;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (z > -INFINITY) L += ptx::ex2(z - ref);
+    if (z != -INFINITY) L += ptx::ex2(z - ref);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
-    if (lse && y < 8 && lane == 0) lse[b * kHAtt + h0 + i] = L > 0.0f ? (ref + log2f(L)) / kLog2e : -INFINITY;
+    if (lse && y < 8 && lane == 0) lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
   }
   __syncthreads();
   float acc[8];
@@ -1632,6 +1703,19 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += s_join[j][i][t];
   }
+  if (fix.rest) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float e = rest_of(fix, ((int64_t)b * kHAtt + h0 + i) * kDMain + c) * acc[i];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      if (lane == 0) s_dot[t >> 5][i] = e;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (t < 8)
+      fix.dots[((int64_t)b * 4 + (y >> 3)) * kHAtt + h0 + t] =
+          (s_dot[0][t] + s_dot[1][t]) + (s_dot[2][t] + s_dot[3][t]);
+  }
   const bool rotated = turn && (y >> 3) == 3 && t >= 64;  // whole warps: channels 448 ..
   float cs = 1.0f, sn = 0.0f;
   if (rotated) {  // turn back by -q_pos: x' = x c + y s, y' = y c - x s, pairs in neighbouring lanes
@@ -1650,6 +1734,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
     if (out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
     else static_cast<float*>(out)[at] = o;
   }
+  if (fix.rest) finish_lse(fix, b, t, 32, 4, lse);
 }
 
 struct PrefixWs {
@@ -1657,8 +1742,9 @@ struct PrefixWs {
   int32_t *gpair, *chunk0, *gimage;
   Part* parts;
   int2* qpart;
-  uint16_t *image, *qimage;
-  float* c2;
+  uint16_t *image, *qimage, *rest;
+  float *c2, *dots;
+  int32_t* count;
   float2* turn;
   int64_t image_cap;
   uint4* part_o;
@@ -1686,6 +1772,9 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.gimage = (int32_t*)take((size_t)G * 4);
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
+  L.rest = (uint16_t*)take((size_t)B * kHAtt * kDMain * 2);
+  L.dots = (float*)take((size_t)B * (G > 0 ? 32 : 4) * kHAtt * 4);
+  L.count = (int32_t*)take((size_t)B * 4);
   L.turn = (float2*)take((size_t)B * 32 * 8);
   L.part_o = (uint4*)take(slots * kHAtt * kDMain * 2);
   L.part_ml = (float2*)take(slots * kHAtt * 8);
@@ -1767,8 +1856,11 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
                        L.pairs, L.parts, L.part_o, L.part_ml, ws};
+  // bf16 queries are exact in f16 unless they were normalised or rotated
+  uint16_t* const rest = lse_out && (ex.qnorm_w || ex.rope) ? L.rest : nullptr;
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
-                       L.qimage, L.c2, L.turn};
+                       L.qimage, L.c2, L.turn, rest, L.count};
+  const LseRest fix{rest, L.c2, L.dots, L.count};
   ImageMaps maps{};
   if (L.image_cap > 0 &&
       (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
@@ -1794,7 +1886,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     KernelTimer timer("k_paged_merge", st);
     launch_pdl(slices > 1 ? k_paged_merge<4> : k_paged_merge<1>, dim3(B, 32), dim3(128 * slices), 0, st, (const int2*)L.qpart,
                (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
-               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out,
+               fix);
     return launch_status();
   }
   {
@@ -1805,7 +1898,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     KernelTimer timer("k_prefix_merge", st);
     launch_pdl(slices > 1 ? k_prefix_merge<4> : k_prefix_merge<1>, dim3(B, 16), dim3(128 * slices), 0, st, (const int2*)L.qpart,
                (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
-               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out,
+               fix);
   }
   return launch_status();
 }

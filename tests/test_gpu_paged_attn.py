@@ -24,7 +24,7 @@ class Batch:
     """A paged cache on both sides: B sequences of n[b] entries in pages of P, groups of queries that
     share their first entries.  Every entry that no query may see has a NaN scale."""
 
-    def __init__(self, seed, n, P, groups=(), shared=(), n_swa=0, win=False, extras=False, sink=False, spare=3):
+    def __init__(self, seed, n, P, groups=(), shared=(), n_swa=0, win=False, extras=False, sink=False, spare=3, q=None):
         rng = np.random.default_rng(seed)
         self.B, self.P, self.n, self.n_swa, self.groups, self.shared = len(n), P, list(n), n_swa, groups, list(shared)
         B = self.B
@@ -58,7 +58,7 @@ class Batch:
             seen[self.rows[-1]] = True
         self.scales[~seen] = 0x7F
         self.table = table
-        self.q = bf16(rng.standard_normal((B, H, D)))
+        self.q = bf16(rng.standard_normal((B, H, D))) if q is None else q
         self.swa = F = None
         if n_swa:
             F = torch.from_numpy(rng.standard_normal((B, n_swa, D)).astype(np.float32)).to(torch.float8_e4m3fn)
@@ -72,9 +72,9 @@ class Batch:
         self.q_pos = (1_000_003 + 37 * np.arange(B)).astype(np.int64) if extras else None
         self.sink = (2 * rng.standard_normal(H)).astype(np.float32) if sink else None
 
-    def reference(self, n=None, shared=None):
+    def reference(self, n=None, of=None):
         outs, lses, bounds, lbs = [], [], [], []
-        for b in range(self.B):
+        for b in range(self.B) if of is None else of:
             r = self.rows[b][:self.n[b] if n is None else n[b]]
             x = decode(self.codes[r], self.scales[r])
             if self.n_swa:
@@ -117,14 +117,15 @@ class Batch:
                                out, ws, lse_out=lse, stream=stream, **self.kw)
         return out, lse, ws
 
-    def prefix(self, dtype=torch.float32, start=None, shared=None, shared_max=None, own_max=None, stream=None, keep=None):
+    def prefix(self, dtype=torch.float32, start=None, shared=None, shared_max=None, own_max=None, stream=None, keep=None,
+               ws=None):
         out, lse = self.outputs(dtype)
         start = [a for a, _ in self.groups] + [self.groups[-1][1]] if start is None else start
         shared = self.shared if shared is None else shared
         shared_max = max(max(self.shared), 0) if shared_max is None else shared_max
         own_max = max(self.n) if own_max is None else own_max
         G = len(shared)
-        ws = csa2.workspace(csa2.prefix_attn_workspace_size(self.B, G, shared_max, own_max, self.n_swa))
+        ws = csa2.workspace(csa2.prefix_attn_workspace_size(self.B, G, shared_max, own_max, self.n_swa)) if ws is None else ws
         self.keep = keep or (to_dev(np.array(start, np.int32)), to_dev(np.array(shared, np.int32)))
         csa2.prefix_attn_decode(self.planes, self.pages, self.B, self.dn, G, *self.keep, shared_max, own_max,
                                 self.dswa, self.n_swa, self.dq, SCALE, out, ws, lse_out=lse, stream=stream, **self.kw)
@@ -358,6 +359,215 @@ def test_same_results_call_after_call():
         two = b.prefix(torch.bfloat16)
         assert csa2.check(two[2])[0] == 0
         assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_logsumexp_of_one_rounded_row(prefix):
+    """Every head's query is normalised and rotated, which its f16 form rounds; each query's one row has the
+    signs of what head 0's rounding takes, so that it all adds up: some 2^-9.  The logsumexp is corrected for
+    it: left are the fp32 sums' 2^-16 of scale sum |q x|, with e = 2^-11 of that at most e^2 / 2 (half the
+    square of half the width 2 e) and, of the correction itself, e (2^-11 for its f16 terms + 2^-9 for o)."""
+    b = Batch(21, [1, 1], 16, [(0, 2)], [0], extras=True)
+    lost = []
+    for i in range(2):
+        q = norm_rope_q(b.q[i].float().numpy(), b.weight, 1e-6, b.q_pos[i], 10000.0)[0]
+        r = q - q.astype(np.float16).astype(np.float64)
+        code = np.where(r < 0, 12, 4).astype(np.uint8)  # -2, 2
+        b.codes[b.rows[i][0]], b.scales[b.rows[i][0]] = code[0::2] | code[1::2] << 4, 0x38
+        lost.append(SCALE * 2 * np.abs(r).sum())
+    b.device()
+    out, lse, ws = b.prefix() if prefix else b.paged()
+    assert csa2.check(ws)[0] == 0
+    ref = b.reference()
+    close(out, lse, ref)
+    for i in range(2):
+        q = norm_rope_q(b.q[i].float().numpy(), b.weight, 1e-6, b.q_pos[i], 10000.0)
+        x = decode(b.codes[b.rows[i]], b.scales[b.rows[i]])
+        z = SCALE * (np.abs(q) @ np.abs(x).T)[:, 0]
+        e = z * 2.0 ** -11
+        tol = z * 2.0 ** -16 + e * e / 2 + e * (2.0 ** -11 + 2.0 ** -9) + 2.0 ** -22 * np.abs(ref[1][i])
+        assert lost[i] > 4 * tol[0]
+        assert (np.abs(lse[i].double().cpu().numpy() - ref[1][i]) <= tol).all()
+
+
+@pytest.mark.parametrize("n_swa", [0, 128])
+def test_nan_reaches_only_the_queries_that_see_it(n_swa):
+    n = [300, 100, 300, 150, 90, 700, 95, 99]
+    b = Batch(22, n, 16, [(0, 4), (4, 8)], [280, 80], n_swa=n_swa)
+    bad = {0, 2, 5}
+    b.scales[b.rows[0][200], 3] = 0x7F   # shared, seen by 0 and 2
+    b.scales[b.rows[5][600], 31] = 0xFF  # the own of 5
+    b.scales[b.rows[5][85], 0] = 0x7F    # and among the rows next to those of 4
+    if n_swa:
+        b.swa[7, 100, 511] = 0xFF
+        bad.add(7)
+    b.device()
+    good = [i for i in range(8) if i not in bad]
+    want = b.reference(of=good)
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        close(out[good], lse[good], want)
+        assert torch.isnan(out[sorted(bad)]).all() and torch.isnan(lse[sorted(bad)]).all()
+
+
+def test_padded_queries_may_hold_nan():
+    b = Batch(23, [0, 70, 0], 16, [(1, 2)], [64], extras=True, sink=True)
+    q = b.q.clone()
+    b.q[0], b.q[2] = 0, 0
+    want = b.reference()
+    b.q = q
+    b.q[0], b.q[2, :, 5] = float("nan"), float("inf")
+    b.device()
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        close(out, lse, want)
+
+
+def test_sinks_of_minus_infinity_and_no_rows():
+    b = Batch(24, [0, 40], 16, [(0, 2)], [0], sink=True)
+    b.sink[::2] = -np.inf
+    b.device()
+    with np.errstate(divide="ignore"):
+        want = b.reference(of=[1])
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        close(out[1:], lse[1:], want)
+        l0 = lse[0].cpu().numpy()
+        assert (out[0] == 0).all() and np.isneginf(l0[::2]).all()
+        assert np.abs(l0[1::2] - b.sink[1::2]).max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("P,n_pages", [(20000, 5), (70001, 3), (1 << 22, 1)])
+def test_large_pages(P, n_pages):
+    b = Batch(25, [300, 260], 64, [(0, 2)], [256])
+    want = b.reference()
+    N = n_pages * P
+    b.device()
+    codes = torch.zeros((N, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, 32), 0x7F, dtype=torch.uint8, device="cuda")
+    # one sequence after the other: query 1 has its own page where there is one, else sees query 0's entries
+    t = [n_pages - 1, max(n_pages - 2, 0)]
+    rows = [t[i] * P + np.arange(b.n[i]) for i in range(2)]
+    if n_pages == 1:
+        b.rows[1] = b.rows[0][:260]
+        want = b.reference()
+    for i in range(2):
+        at = torch.from_numpy(rows[i]).cuda()
+        codes[at], scales[at] = to_dev(b.codes[b.rows[i]]), to_dev(b.scales[b.rows[i]])
+    b.planes = csa2.Planes(codes, scales, codes, scales, P)
+    b.pages = csa2.pages(to_dev(np.array(t, np.int32)[:, None]), n_pages)
+    b.max_pages = 1
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        close(out, lse, want)
+
+
+def test_one_long_query_among_many():
+    n = [9000] + [3] * 19
+    b = Batch(26, n, 16, [(0, 20)], [2], n_swa=4).device()
+    want = b.reference()
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        close(out, lse, want)
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_batches_beyond_the_plans_shared_memory(prefix):
+    # 9,000 queries, each a group: most of them empty, the last ones not
+    B = 9000
+    rng = np.random.default_rng(27)
+    n = np.zeros(B, int)
+    live = np.concatenate([rng.choice(B - 40, 60, replace=False), np.arange(B - 5, B)])
+    n[live] = rng.integers(1, 300, live.size)
+    q = torch.randn((64, H, D), generator=torch.Generator().manual_seed(27)).to(torch.bfloat16)
+    b = Batch(27, [int(x) for x in n], 16, [(i, i + 1) for i in range(B)], [int(x) // 2 for x in n],
+              q=q.repeat(-(-B // 64), 1, 1)[:B]).device()
+    out, lse, ws = b.prefix(torch.bfloat16) if prefix else b.paged(torch.bfloat16)
+    assert csa2.check(ws)[0] == 0
+    at = torch.from_numpy(live).cuda()
+    close(out[at], lse[at], b.reference(of=live))
+    dead = torch.from_numpy(np.flatnonzero(n == 0)).cuda()
+    assert (lse[dead] == -np.inf).all() and not out[dead].any()
+
+
+def test_groups_beyond_one_strip_of_the_plan():
+    # 700 groups, of one to four queries, over the pages of one long prompt
+    rng = np.random.default_rng(28)
+    size = rng.integers(1, 5, 700)
+    start = np.concatenate([[0], np.cumsum(size)])
+    B = int(start[-1])
+    group = np.repeat(np.arange(700), size)
+    shared = rng.integers(0, 180, 700)
+    n = shared[group] + rng.integers(0, 20, B)
+    one = Batch(28, [200], 16)
+    q = torch.randn((64, H, D), generator=torch.Generator().manual_seed(28)).to(torch.bfloat16)
+    one.device()
+    one.B, one.n, one.dn, one.q = B, [int(x) for x in n], to_dev(n.astype(np.int32)), q.repeat(-(-B // 64), 1, 1)[:B]
+    one.dq, one.rows = one.q.cuda(), [one.rows[0][:x] for x in n]
+    one.groups, one.shared = [(int(start[g]), int(start[g + 1])) for g in range(700)], [int(x) for x in shared]
+    one.pages = csa2.pages(to_dev(np.repeat(one.table, B, 0)), one.n_pages)
+    out, lse, ws = one.prefix(torch.bfloat16, own_max=20)
+    assert csa2.check(ws)[0] == 0
+    of = np.concatenate([np.arange(30), rng.choice(B, 100), np.arange(B - 30, B)])
+    at = torch.from_numpy(of).cuda()
+    close(out[at], lse[at], one.reference(of=of))
+
+
+def test_more_shared_entries_than_the_workspace_widens():
+    # 18 groups of three queries on 65,536 entries each, the same pages: beyond 2^20 entries, the last
+    # groups' entries are widened where they are read
+    G, ns = 18, 65536
+    one = Batch(29, [ns], 64)
+    q = torch.randn((3 * G, H, D), generator=torch.Generator().manual_seed(29)).to(torch.bfloat16)
+    one.device()
+    B = one.B = 3 * G
+    one.n, one.dn, one.q, one.dq = [ns] * B, to_dev(np.full(B, ns, np.int32)), q, q.cuda()
+    one.groups, one.shared = [(3 * g, 3 * g + 3) for g in range(G)], [ns] * G
+    one.pages = csa2.pages(to_dev(np.repeat(one.table, B, 0)), one.n_pages)
+    x = decode(one.codes[one.rows[0]], one.scales[one.rows[0]])
+    out, lse, ws = one.prefix(own_max=0)
+    assert csa2.check(ws)[0] == 0
+    of = [0, 24, 50, 53]
+    close(out[of], lse[of], tuple(np.stack(z) for z in zip(*(attention(x, q[i].double().numpy(), SCALE) for i in of))))
+
+
+def test_two_graphs_share_a_workspace():
+    b = Batch(30, [300, 310, 320, 64], 16, [(0, 3)], [256], n_swa=16, extras=True, sink=True).device()
+    size = max(csa2.prefix_attn_workspace_size(4, 1, 256, 70, 16), csa2.paged_attn_workspace_size(4, 320, 16))
+    ws = csa2.workspace(size)
+    b.prefix(own_max=70, ws=ws)
+    b.paged(ws=ws)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    with torch.cuda.stream(st):
+        for i, g in enumerate(graphs):
+            with torch.cuda.graph(g, stream=st):
+                outs.append(b.paged(ws=ws) if i else b.prefix(own_max=70, ws=ws, keep=b.keep))
+        for i in (0, 1, 1, 0, 1, 0):
+            graphs[i].replay()
+    st.synchronize()
+    want = b.reference()
+    for out, lse, _ in outs:
+        close(out, lse, want)
+    assert csa2.check(ws)[0] == 0
+
+
+def test_calls_at_once_on_streams_of_their_own():
+    b = Batch(31, [900, 901, 902, 64] * 4, 16, [(0, 3), (3, 4), (4, 7)], [880, 10, 400], n_swa=16).device()
+    want = b.reference()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    b.prefix()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(b.prefix(keep=b.keep) if i % 2 else b.paged())
+    torch.cuda.synchronize()
+    for out, lse, ws in got:
+        assert csa2.check(ws)[0] == 0
+        close(out, lse, want)
 
 
 def test_whole_run_tables_append_window_attention(oracle_mod):
