@@ -66,7 +66,6 @@ struct PrefixQuery {
   float* c2;        // [B + 1][64]
   float2* turn;     // [B][32]
   uint16_t* rest;   // [B][head][c] what the rounding to f16 took from q', in q's scale (f16); null: not kept
-  int32_t* count;   // [B] zeroed with it
 };
 
 struct PrefixArgs {
@@ -935,7 +934,6 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     if (threadIdx.x < kHAtt) a.c2[(int64_t)b * kHAtt + threadIdx.x] = 1.0f;
     return;
   }
-  if (a.rest && threadIdx.x == 0) a.count[b] = 0;
   constexpr int kHeads = kHAtt / (kPrepThreads / 32);
   const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + warp * kHeads) * kDMain) + 2 * lane;
   uint4 qv[kHeads][2];
@@ -1132,52 +1130,48 @@ struct Join {
 // The logsumexp of queries that were rounded to f16.  With q = q' + r, r of at most 2^-11 |q|, the joins give
 // lse(q'), and lse(q) = lse(q') + E + (at most w^2 / 8), E = the mean of scale r x under q's own weights and w the
 // width of scale r x over the rows (Hoeffding's lemma): E = scale r o with the output o before it turns back.
-// Without it one row of 512 normal channels is off by 2 10^-4, with it by 10^-8.  A CTA leaves the part of its
-// channels, and the last CTA of a query adds them up, in the order of the CTAs.
+// Without it one row of 512 normal channels is off by 2 10^-4, with it by 10^-8.  So a CTA has all channels of its
+// heads, or is in a cluster of those that have (a counter in global memory and its fence for the last of a
+// query's CTAs instead: 2 to 3 us more a call).
 struct LseRest {
   const uint16_t* rest;  // null: q was not rounded, or no logsumexp is asked for
   const float* c2;
-  float* dots;  // [B][parts][64]
-  int32_t* count;
 };
-__device__ __forceinline__ float rest_of(const LseRest& f, int64_t at) {
-  return __half2float(__ushort_as_half(f.rest[at]));
-}
-// 128 threads of each of `ctas` CTAs, their dots written: the last CTA's finish the heads of query b.
-__device__ __forceinline__ void finish_lse(const LseRest& f, int b, int t, int ctas, int parts, float* lse) {
-  __shared__ int s_last;
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-  if (t == 0) {
-    __threadfence();
-    s_last = atomicAdd(f.count + b, 1) == ctas - 1;
-    __threadfence();
-  }
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-  if (!s_last || t >= kHAtt) return;
-  float e = 0.0f;
-  for (int i = 0; i < parts; ++i) e += __ldcg(f.dots + ((int64_t)b * parts + i) * kHAtt + t);
-  const float l = __ldcg(lse + b * kHAtt + t);
+__device__ __forceinline__ float corrected(const LseRest& f, int b, int h, float l, float e) {
   // a query without rows may hold anything
-  if (l > -INFINITY && isfinite(e)) lse[b * kHAtt + t] = fmaf(e, f.c2[(int64_t)b * kHAtt + t] / kLog2e, l);
+  return l > -INFINITY && isfinite(e) ? fmaf(e, f.c2[(int64_t)b * kHAtt + h] / kLog2e, l) : l;
 }
 
-// Thread t of a slice: head t % 64 and, of channel half t / 64, the 16 channels 256 (t / 64) + 16 blockIdx.y ..
+// A CTA joins 8 / kSlices heads: thread t of a slice has head t % (8 / kSlices) of them and kVec planes (of eight
+// channels): two, which share a weight, or one where slices make for more threads (one for all: 4 us more for
+// 101 queries).
 template <int kSlices>
-__global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __restrict__ qpart,
+struct PrefixMerge {
+  static constexpr int kVec = kSlices > 1 ? 1 : 2, kHeads = 8 / kSlices, kPer = kHeads * (kDMain / 8) / kVec;
+  static constexpr int kThreads = kPer * kSlices;
+};
+template <int kSlices>
+__global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge(const int2* __restrict__ qpart,
                                                                 const uint4* __restrict__ part_o,
                                                                 const float2* __restrict__ part_ml,
                                                                 const float* __restrict__ sink,
                                                                 const float2* __restrict__ turn, void* __restrict__ out,
-                                                                int out_bf16, float* lse, LseRest fix) {
-  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][18][128];
+                                                                int out_bf16, float* __restrict__ lse, LseRest fix) {
+  constexpr int kVec = PrefixMerge<kSlices>::kVec, kHeads = PrefixMerge<kSlices>::kHeads;
+  constexpr int kPer = PrefixMerge<kSlices>::kPer, kC = 8 * kVec;
+  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][2 + kC][kSlices > 1 ? kPer : 1];
+  __shared__ float s_dot[kPer / 32][kHeads];
   ptx::griddep_wait();
-  const int b = blockIdx.x, slice = threadIdx.x >> 7, t = threadIdx.x & 127, h = t & 63, half = t >> 6;
+  const int b = blockIdx.x, slice = threadIdx.x / kPer, t = threadIdx.x % kPer, plane = t / kHeads * kVec;
+  const int h = blockIdx.y * kHeads + t % kHeads;
   const int2 part = qpart[b];  // twice the first partial's slot, plus the query's place in its pair; partials
-  Join<16> a;
+  Join<kC> a;
   a.start(slice == 0 && sink ? sink[h] * kLog2e : -INFINITY);
+  // the epilogue's thread h + 64 (plane / 32) wrote vector plane % 32
+  const uint4* po = part_o + (plane & 31) * 128 + 64 * (plane >> 5) + h;
   for (int c0 = slice; c0 < part.y; c0 += kSlices * kJoin) {
     float2 ml[kJoin];
-    uint4 v[kJoin][2];
+    uint4 v[kJoin][kVec];
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {
       ml[i] = make_float2(-INFINITY, 0.0f);
@@ -1185,7 +1179,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
         const int64_t slot = part.x + 2 * (int64_t)(c0 + i * kSlices);
         ml[i] = part_ml[slot * kHAtt + h];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) v[i][u] = part_o[(slot * 32 + blockIdx.y * 2 + u) * 128 + t];
+        for (int u = 0; u < kVec; ++u) v[i][u] = po[(slot * 32 + u) * 128];
       }
     }
     float top = a.ref;
@@ -1199,7 +1193,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
       const float f = ptx::ex2(ml[i].x - a.ref) * ml[i].y;
       a.L += f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kVec; ++u) {
         const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1210,48 +1204,57 @@ __global__ void __launch_bounds__(kSlices * 128) k_prefix_merge(const int2* __re
       }
     }
   }
-  if (slice > 0) {
-    s_join[slice - 1][0][t] = a.ref;
-    s_join[slice - 1][1][t] = a.L;
+  if (kSlices > 1) {
+    if (slice > 0) {
+      s_join[slice - 1][0][t] = a.ref;
+      s_join[slice - 1][1][t] = a.L;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) s_join[slice - 1][2 + u][t] = a.acc[u];
-  }
-  if (kSlices > 1) __syncthreads();
-  if (slice > 0) return;
-  for (int i = 0; i < kSlices - 1; ++i) {
-    const float m = s_join[i][0][t], l = s_join[i][1][t];
-    if (l == 0.0f) continue;
-    a.raise(m);
-    const float f = ptx::ex2(m - a.ref);
-    a.L = fmaf(f, l, a.L);
+      for (int u = 0; u < kC; ++u) s_join[slice - 1][2 + u][t] = a.acc[u];
+    }
+    __syncthreads();
+    if (slice > 0) return;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) a.acc[u] = fmaf(f, s_join[i][2 + u][t], a.acc[u]);
+    for (int i = 0; i < kSlices - 1; ++i) {
+      const float m = s_join[i][0][t], l = s_join[i][1][t];
+      if (l == 0.0f) continue;
+      a.raise(m);
+      const float f = ptx::ex2(m - a.ref);
+      a.L = fmaf(f, l, a.L);
+#pragma unroll
+      for (int u = 0; u < kC; ++u) a.acc[u] = fmaf(f, s_join[i][2 + u][t], a.acc[u]);
+    }
   }
   const float inv = a.L > 0.0f ? 1.0f / a.L : 0.0f;
-  const int c0 = 256 * half + 16 * blockIdx.y;
 #pragma unroll
-  for (int u = 0; u < 16; ++u) a.acc[u] *= inv;
-  if (lse && blockIdx.y == 0 && half == 0)
-    lse[b * kHAtt + h] = a.L == 0.0f ? -INFINITY : (a.ref + log2f(a.L)) / kLog2e;
-  if (fix.rest) {
-    const uint4* rp = reinterpret_cast<const uint4*>(fix.rest + ((int64_t)b * kHAtt + h) * kDMain + c0);
-    const uint4 r0 = rp[0], r1 = rp[1];
-    const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+  for (int u = 0; u < kC; ++u) a.acc[u] *= inv;
+  if (lse) {
     float e = 0.0f;
+    if (fix.rest) {
+      const __half2* r = reinterpret_cast<const __half2*>(fix.rest + ((int64_t)b * kHAtt + h) * kDMain + 8 * plane);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[u]));
-      e = fmaf(x.x, a.acc[2 * u], fmaf(x.y, a.acc[2 * u + 1], e));
+      for (int u = 0; u < kC / 2; ++u) {
+        const float2 x = __half22float2(r[u]);
+        e = fmaf(x.x, a.acc[2 * u], fmaf(x.y, a.acc[2 * u + 1], e));
+      }
+#pragma unroll
+      for (int o = 16; o >= kHeads; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      if ((t & 31) < kHeads) s_dot[t >> 5][t & 31] = e;
+      asm volatile("bar.sync 1, %0;" ::"n"(kPer) : "memory");
+      e = 0.0f;
+      if (t < kHeads)
+        for (int i = 0; i < kPer / 32; ++i) e += s_dot[i][t];
     }
-    fix.dots[((int64_t)b * 32 + 2 * blockIdx.y + half) * kHAtt + h] = e;
+    if (t < kHeads) {
+      const float l = a.L == 0.0f ? -INFINITY : (a.ref + log2f(a.L)) / kLog2e;
+      lse[b * kHAtt + h] = fix.rest ? corrected(fix, b, h, l, e) : l;
+    }
   }
-  if (turn && c0 >= kRopeFirst) {  // turn back by -q_pos
-    const float2* cs = turn + (int64_t)b * 32 + (c0 - kRopeFirst) / 2;
+  if (turn && plane >= kRopeFirst / 8) {  // turn back by -q_pos
+    const float2* cs = turn + (int64_t)b * 32 + 4 * (plane - kRopeFirst / 8);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) rope_pair(a.acc[2 * u], a.acc[2 * u + 1], cs[u].x, -cs[u].y);
+    for (int u = 0; u < kC / 2; ++u) rope_pair(a.acc[2 * u], a.acc[2 * u + 1], cs[u].x, -cs[u].y);
   }
-  store_channels<16>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + c0, a.acc);
-  if (fix.rest) finish_lse(fix, b, t, 16, 32, lse);
+  store_channels<kC>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + 8 * plane, a.acc);
 }
 
 // ------------------------------------------------------------ queries alone
@@ -1620,25 +1623,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   }
 }
 
-// The join over partials of the epilogue's order: a CTA has eight heads 32 (y / 4 % 2) + 8 (y % 4) .. of the 128
-// channels 128 (y / 8) .. (y = blockIdx.y), thread t of a slice the channel t of them.  The weights
-// 2^(m_i - m) l_i / L are the same for all channels: the CTA forms them once, while the first partials' channels
-// are on their way.
+// The join over partials of the epilogue's order: a CTA has eight heads 8 g .. and all channels, thread t of it
+// channel t; with four slices the 128 channels of a tile, and four CTAs (a cluster where the logsumexp wants all
+// channels) make the heads.  The weights 2^(m_i - m) l_i / L are the same for all channels: the CTA forms them
+// once, while the first partials' channels are on their way.
+constexpr int kMergeThreads = 512;
 template <int kSlices>
-__global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __restrict__ qpart,
+__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const int2* __restrict__ qpart,
                                                                const uint4* __restrict__ part_o,
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
                                                                int out_bf16, float* lse, LseRest fix) {
+  constexpr int kTiles = 4 / kSlices, kPer = 128 * kTiles;
+  static_assert(kSlices == 1 || kTiles == 1, "all channels, or a tile of them");
   __shared__ __align__(16) float s_w[kAlone][8];  // read four at a time
-  __shared__ float s_m[kAlone][8], s_dot[4][8];
-  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][8][128];
+  __shared__ float s_m[kAlone][8], s_dot[4 * kTiles][8], s_part[4][8];
+  __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][8][kSlices > 1 ? 128 : 1];
+  if (kSlices > 1 && fix.rest) ptx::cluster_sync();  // the first CTA's shared memory is there
   ptx::griddep_wait();
-  const int b = blockIdx.x, y = blockIdx.y, slice = threadIdx.x >> 7, t = threadIdx.x & 127;
-  const int h0 = 32 * ((y >> 2) & 1) + 8 * (y & 3), c = 128 * (y >> 3) + t;
+  const int b = blockIdx.x, slice = threadIdx.x / kPer, t = threadIdx.x % kPer;
+  const int tile = kSlices > 1 ? blockIdx.y & 3 : t >> 7, g = kSlices > 1 ? blockIdx.y >> 2 : blockIdx.y;
+  const int h0 = 8 * g, c = kSlices > 1 ? 128 * tile + t : t;
+  const int y = 8 * tile + g;  // the epilogue's vector, of its thread c % 128
   const int2 part = qpart[b];  // the first partial's slot, partials (at most one a CTA)
-  for (int i = threadIdx.x; i < part.y * 8; i += kSlices * 128) {
+  for (int i = threadIdx.x; i < part.y * 8; i += kMergeThreads) {
     const float2 ml = part_ml[(int64_t)(part.x + i / 8) * kHAtt + h0 + i % 8];
     s_m[i / 8][i % 8] = ml.y == 0.0f ? -INFINITY : ml.x;
     s_w[i / 8][i % 8] = ml.y;
@@ -1647,12 +1656,12 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < kJoin; ++j)
-      if (k0 + j * kSlices < part.y) v[j] = part_o[((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * 128 + t];
+      if (k0 + j * kSlices < part.y) v[j] = part_o[((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * 128 + (t & 127)];
   };
   fetch(slice);
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < 8; i += kSlices * 4) {  // a warp per head
+  for (int i = threadIdx.x >> 5; i < 8; i += kMergeThreads / 32) {  // a warp per head
     const float z = sink ? sink[h0 + i] * kLog2e : -INFINITY;
     float ref = z;
     for (int j = lane; j < part.y; j += 32) ref = fmaxf(ref, s_m[j][i]);
@@ -1669,7 +1678,7 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
     if (z != -INFINITY) L += ptx::ex2(z - ref);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
-    if (lse && y < 8 && lane == 0) lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
+    if (lse && (kSlices == 1 || tile == 0) && lane == 0) lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
   }
   __syncthreads();
   float acc[8];
@@ -1706,20 +1715,23 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
   if (fix.rest) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float e = rest_of(fix, ((int64_t)b * kHAtt + h0 + i) * kDMain + c) * acc[i];
+      float e = __half2float(__ushort_as_half(fix.rest[((int64_t)b * kHAtt + h0 + i) * kDMain + c])) * acc[i];
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
       if (lane == 0) s_dot[t >> 5][i] = e;
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (t < 8)
-      fix.dots[((int64_t)b * 4 + (y >> 3)) * kHAtt + h0 + t] =
-          (s_dot[0][t] + s_dot[1][t]) + (s_dot[2][t] + s_dot[3][t]);
+    asm volatile("bar.sync 1, %0;" ::"n"(kPer) : "memory");
+    if (t < 8) {
+      float e = 0.0f;
+      for (int i = 0; i < 4 * kTiles; ++i) e += s_dot[i][t];
+      if (kSlices > 1) ptx::st_cluster_f32(&s_part[tile][t], 0, e);
+      else lse[b * kHAtt + h0 + t] = corrected(fix, b, h0 + t, lse[b * kHAtt + h0 + t], e);
+    }
   }
-  const bool rotated = turn && (y >> 3) == 3 && t >= 64;  // whole warps: channels 448 ..
+  const bool rotated = turn && c >= kRopeFirst;  // whole warps
   float cs = 1.0f, sn = 0.0f;
   if (rotated) {  // turn back by -q_pos: x' = x c + y s, y' = y c - x s, pairs in neighbouring lanes
-    const float2 r = turn[(int64_t)b * 32 + (t - 64) / 2];
+    const float2 r = turn[(int64_t)b * 32 + (c - kRopeFirst) / 2];
     cs = r.x;
     sn = t & 1 ? -r.y : r.y;
   }
@@ -1734,7 +1746,13 @@ __global__ void __launch_bounds__(kSlices * 128) k_paged_merge(const int2* __res
     if (out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
     else static_cast<float*>(out)[at] = o;
   }
-  if (fix.rest) finish_lse(fix, b, t, 32, 4, lse);
+  if (kSlices > 1 && fix.rest) {
+    __syncwarp();
+    ptx::cluster_sync();
+    if (tile == 0 && t < 8)
+      lse[b * kHAtt + h0 + t] = corrected(fix, b, h0 + t, lse[b * kHAtt + h0 + t],
+                                          (s_part[0][t] + s_part[1][t]) + (s_part[2][t] + s_part[3][t]));
+  }
 }
 
 struct PrefixWs {
@@ -1743,8 +1761,7 @@ struct PrefixWs {
   Part* parts;
   int2* qpart;
   uint16_t *image, *qimage, *rest;
-  float *c2, *dots;
-  int32_t* count;
+  float* c2;
   float2* turn;
   int64_t image_cap;
   uint4* part_o;
@@ -1773,8 +1790,6 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
   L.rest = (uint16_t*)take((size_t)B * kHAtt * kDMain * 2);
-  L.dots = (float*)take((size_t)B * (G > 0 ? 32 : 4) * kHAtt * 4);
-  L.count = (int32_t*)take((size_t)B * 4);
   L.turn = (float2*)take((size_t)B * 32 * 8);
   L.part_o = (uint4*)take(slots * kHAtt * kDMain * 2);
   L.part_ml = (float2*)take(slots * kHAtt * 8);
@@ -1799,17 +1814,19 @@ bool image_map(CUtensorMap* map, uint16_t* image, int64_t chunks, uint32_t rows,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// launch_pdl in clusters of cx x cy CTAs
 template <typename... K>
-cudaError_t launch_pairs(void (*kern)(K...), int clusters, size_t smem, cudaStream_t st, const K&... args) {
+cudaError_t launch_clusters(void (*kern)(K...), dim3 grid, dim3 block, unsigned cx, unsigned cy, size_t smem,
+                            cudaStream_t st, const K&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.x = cx;
+  attr[0].val.clusterDim.y = cy;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -1859,8 +1876,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   // bf16 queries are exact in f16 unless they were normalised or rotated
   uint16_t* const rest = lse_out && (ex.qnorm_w || ex.rope) ? L.rest : nullptr;
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
-                       L.qimage, L.c2, L.turn, rest, L.count};
-  const LseRest fix{rest, L.c2, L.dots, L.count};
+                       L.qimage, L.c2, L.turn, rest};
+  const LseRest fix{rest, L.c2};
   ImageMaps maps{};
   if (L.image_cap > 0 &&
       (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
@@ -1878,29 +1895,29 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
                L.image);
   }
   const int slices = B < kSliceQueries ? 4 : 1;
+  const float2* turn = ex.rope ? L.turn : nullptr;
+  const int out_bf16 = out_type == CSA2_OUT_BF16 ? 1 : 0;
+  auto merge = [&](auto kern, unsigned ctas, unsigned threads, unsigned cluster) {
+    launch_clusters(kern, dim3(B, ctas), dim3(threads), 1, cluster, 0, st, (const int2*)L.qpart,
+                    (const uint4*)L.part_o, (const float2*)L.part_ml, sink, turn, out, out_bf16, lse_out, fix);
+  };
   if (G == 0) {
     {
       KernelTimer timer("k_paged_attn", st);
       launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
     }
     KernelTimer timer("k_paged_merge", st);
-    launch_pdl(slices > 1 ? k_paged_merge<4> : k_paged_merge<1>, dim3(B, 32), dim3(128 * slices), 0, st, (const int2*)L.qpart,
-               (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
-               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out,
-               fix);
+    if (slices > 1) merge(k_paged_merge<4>, 32, kMergeThreads, rest ? 4 : 1);
+    else merge(k_paged_merge<1>, 8, kMergeThreads, 1);
     return launch_status();
   }
   {
     KernelTimer timer("k_prefix_attn", st);
-    launch_pairs(k_prefix_attn, kClusters, smem, st, k, maps);
+    launch_clusters(k_prefix_attn, dim3(2 * kClusters), dim3(kThreads), 2, 1, smem, st, k, maps);
   }
-  {
-    KernelTimer timer("k_prefix_merge", st);
-    launch_pdl(slices > 1 ? k_prefix_merge<4> : k_prefix_merge<1>, dim3(B, 16), dim3(128 * slices), 0, st, (const int2*)L.qpart,
-               (const uint4*)L.part_o, (const float2*)L.part_ml, sink,
-               ex.rope ? (const float2*)L.turn : (const float2*)nullptr, out, out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out,
-               fix);
-  }
+  KernelTimer timer("k_prefix_merge", st);
+  if (slices > 1) merge(k_prefix_merge<4>, 32, PrefixMerge<4>::kThreads, 1);
+  else merge(k_prefix_merge<1>, 8, PrefixMerge<1>::kThreads, 1);
   return launch_status();
 }
 

@@ -352,7 +352,14 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// every thread of every CTA of the cluster; memory before it is seen after it
+// a store to the same place of CTA `rank`'s shared memory (seen after the next cluster_sync)
+__device__ __forceinline__ void st_cluster_f32(const float* p, uint32_t rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(p)),
+      "r"(rank), "f"(v)
+      : "memory");
+}
+// every thread, but those that have left, of every CTA of the cluster; memory before it is seen after it
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
