@@ -46,14 +46,6 @@ constexpr uint32_t kAttnTmemCols = 512;  // O^T 256 columns; per S half, two slo
 constexpr uint32_t kTmemS = 256;         // first column of S half 0, slot 0 (half h, slot s: + 128 h + 64 s)
 constexpr long long kAttnWaitBudget = 1LL << 32;
 
-// Page table of a paged cache: entry j of query b is plane row table[b][j / P] * P + j % P
-// (P = seq_stride entries per page).
-struct PageMap {
-  const int32_t* table;
-  int64_t max_pages;
-  int32_t n_pages;
-};
-
 struct __align__(1024) AttnSmem {
   uint16_t X[2][kDMain / 8][kXPlane];  // per slot: f16 rows [c/8][row][c%8]; planes 0-31 / 32-63 = channel halves
   uint16_t q[kDMain / 8][kQPlane];     // f16 q' [c/8][head][c%8]
@@ -93,18 +85,8 @@ struct RowFetch {
 
 // entry of chunk row gr (rows gr >= k are window rows or padding): topk[b][gr],
 // or, dense, entry gr itself while gr < dense_n[b]
-// (paged: the plane row of that entry; a page outside the planes is reported, and its rows are skipped)
-template <bool kPaged>
 __device__ __forceinline__ int64_t fetch_index(const int32_t* __restrict__ topk, const int32_t* __restrict__ dense_n,
-                                               int k, int b, int gr, const PageMap& pm, int64_t page_entries, int cb,
-                                               void* ws) {
-  if (kPaged) {
-    if (gr >= k) return -1;
-    const int page = __ldg(pm.table + b * pm.max_pages + gr / (int)page_entries);
-    if (page >= 0 && page < pm.n_pages) return page * page_entries + gr % (int)page_entries;
-    if (cb == 0) report_error(ws, CSA2_ERR_INDEX_RANGE, page);
-    return -1;
-  }
+                                               int k, int b, int gr) {
   if (gr >= k) return -1;
   if (dense_n) return gr < __ldg(dense_n + b) ? gr : -1;
   return (int64_t)topk[(int64_t)b * k + gr];
@@ -112,15 +94,14 @@ __device__ __forceinline__ int64_t fetch_index(const int32_t* __restrict__ topk,
 
 // Starts this lane's loads of chunk row gr: a selected entry (gr < k, index idx),
 // a window row (k <= gr < k + n_swa, visible) or nothing.
-template <bool kPaged>
 __device__ __forceinline__ void issue_row(RowFetch& f, int64_t idx, const uint8_t* __restrict__ kv_codes,
                                           const uint8_t* __restrict__ kv_scales, int64_t seq_stride,
                                           const uint8_t* __restrict__ swa, int n_swa, int k, int b, int gr,
                                           int cb, void* ws, const int64_t* __restrict__ win_pos, int64_t win_lo) {
   f.kind = 0;
   if (gr < k) {
-    if (idx >= 0 && (kPaged || idx < seq_stride)) {
-      const int64_t e = kPaged ? idx : (int64_t)b * seq_stride + idx;
+    if (idx >= 0 && idx < seq_stride) {
+      const int64_t e = (int64_t)b * seq_stride + idx;
       const uint4* cs = reinterpret_cast<const uint4*>(kv_codes + e * 256);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f.raw[i] = cs[4 * i + cb];
@@ -256,15 +237,11 @@ __device__ __forceinline__ float sum_probs(const uint32_t (&ph)[16]) {
 // kPartial: write the unnormalised O with (m, l) for the merge kernel instead
 // of the normalised output.
 // 16 warps, four per scheduler, whose 16 K registers then allow 128 per thread.
-// kPaged: dense over a paged cache.  The rows of query b are its own n_b entries, then the
-// window, so a query of a ragged batch runs only its own chunks, spread evenly over the
-// launch's splits; a split without rows writes an empty partial.
-template <bool kPartial, bool kEx, bool kPaged>
+template <bool kPartial, bool kEx>
 __global__ void __launch_bounds__(512, 1) k_attn(
     const uint8_t* __restrict__ kv_codes, const uint8_t* __restrict__ kv_scales, int64_t seq_stride,
     const int32_t* __restrict__ topk, const int32_t* __restrict__ dense_n, int k, const uint8_t* __restrict__ swa,
-    int n_swa, PageMap pm,
-    const uint16_t* __restrict__ qg, float scale, AttnExtras ex, int nchunks, int cps,
+    int n_swa, const uint16_t* __restrict__ qg, float scale, AttnExtras ex, int nchunks, int cps,
     float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
     float2* __restrict__ part_ml, void* ws) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -272,17 +249,6 @@ __global__ void __launch_bounds__(512, 1) k_attn(
   volatile int* abort_flag = &S.abort_flag;
   const int b = blockIdx.y, split = blockIdx.x;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  if (kPaged) {
-    ptx::griddep_wait();  // the counts may come from the previous kernel
-    k = min(max(__ldg(dense_n + b), 0), k);
-    nchunks = max((k + n_swa + kRows - 1) / kRows, 1);
-    cps = (nchunks + gridDim.x - 1) / gridDim.x;
-    if (split * cps >= nchunks) {
-      if (tid < kHAtt)
-        part_ml[((int64_t)b * gridDim.x + split) * kHAtt + tid] = make_float2(-INFINITY, 0.0f);
-      return;
-    }
-  }
   const int c0 = split * cps, nc = min(nchunks, c0 + cps) - c0;
 
   if (warp == kCtlWarp) {
@@ -315,8 +281,8 @@ __global__ void __launch_bounds__(512, 1) k_attn(
   int64_t idx0 = -1, idx1 = -1;
   if (warp < kGatherWarps) {
     const int gr0 = c0 * kRows + r, gr1 = gr0 + kRows;
-    idx0 = fetch_index<kPaged>(topk, dense_n, k, b, gr0, pm, seq_stride, cb, ws);
-    idx1 = nc > 1 ? fetch_index<kPaged>(topk, dense_n, k, b, gr1, pm, seq_stride, cb, ws) : -1;
+    idx0 = fetch_index(topk, dense_n, k, b, gr0);
+    idx1 = nc > 1 ? fetch_index(topk, dense_n, k, b, gr1) : -1;
   }
   ptx::tc_fence_before();
   __syncthreads();  // barriers initialised, tensor memory allocated
@@ -403,13 +369,13 @@ __global__ void __launch_bounds__(512, 1) k_attn(
     RowFetch rf0, rf1;  // rows of the even / odd chunks
     const int gr0 = c0 * kRows + r;
     rf1.kind = 0;
-    issue_row<kPaged>(rf0, idx0, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0, cb, ws, ex.win_pos, win_lo);
+    issue_row(rf0, idx0, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0, cb, ws, ex.win_pos, win_lo);
     if (nc > 1)
-      issue_row<kPaged>(rf1, idx1, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0 + kRows, cb, ws, ex.win_pos,
+      issue_row(rf1, idx1, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr0 + kRows, cb, ws, ex.win_pos,
                 win_lo);
     // this lane's entries in chunks j + 2 (loaded after chunk j) and j + 3 (index read then)
-    int64_t idx2 = nc > 2 ? fetch_index<kPaged>(topk, dense_n, k, b, gr0 + 2 * kRows, pm, seq_stride, cb, ws) : -1;
-    int64_t idx3 = nc > 3 ? fetch_index<kPaged>(topk, dense_n, k, b, gr0 + 3 * kRows, pm, seq_stride, cb, ws) : -1;
+    int64_t idx2 = nc > 2 ? fetch_index(topk, dense_n, k, b, gr0 + 2 * kRows) : -1;
+    int64_t idx3 = nc > 3 ? fetch_index(topk, dense_n, k, b, gr0 + 3 * kRows) : -1;
     bool good = true;
     for (int p = 0; 2 * p < nc && good; ++p) {
       const uint32_t ph = (uint32_t)(p & 1);
@@ -440,10 +406,10 @@ __global__ void __launch_bounds__(512, 1) k_attn(
         }
         if (!good) break;
         if (j + 2 < nc)
-          issue_row<kPaged>(f, idx2, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr + 2 * kRows, cb, ws, ex.win_pos,
+          issue_row(f, idx2, kv_codes, kv_scales, seq_stride, swa, n_swa, k, b, gr + 2 * kRows, cb, ws, ex.win_pos,
                     win_lo);
         idx2 = idx3;
-        idx3 = j + 4 < nc ? fetch_index<kPaged>(topk, dense_n, k, b, gr + 4 * kRows, pm, seq_stride, cb, ws) : -1;
+        idx3 = j + 4 < nc ? fetch_index(topk, dense_n, k, b, gr + 4 * kRows) : -1;
       }
     }
     // ---- epilogue: O^T rows = channels of this lane quarter, 32 heads per warp; for each
@@ -624,8 +590,8 @@ __global__ void __launch_bounds__(512, 1) k_attn(
 
 __global__ void __launch_bounds__(128) k_attn_merge(const float* __restrict__ part_o,
                                                     const float2* __restrict__ part_ml, int nchunks,
-                                                    const float* __restrict__ sink, void* __restrict__ out,
-                                                    int out_bf16, float* __restrict__ lse) {
+                                                    const float* __restrict__ sink, float* __restrict__ out,
+                                                    float* __restrict__ lse) {
   const int bh = blockIdx.x;  // b * 64 + h
   const int b = bh / kHAtt, h = bh % kHAtt;
   ptx::griddep_wait();  // the partials come from the previous kernel
@@ -649,13 +615,7 @@ __global__ void __launch_bounds__(128) k_attn_merge(const float* __restrict__ pa
   }
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
   if (L > 0.0f) r = make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
-  if (out_bf16) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(r.x, r.y), hi = __floats2bfloat162_rn(r.z, r.w);
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + (int64_t)bh * kDMain)[threadIdx.x] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  } else {
-    reinterpret_cast<float4*>(static_cast<float*>(out) + (int64_t)bh * kDMain)[threadIdx.x] = r;
-  }
+  reinterpret_cast<float4*>(out + (int64_t)bh * kDMain)[threadIdx.x] = r;
   if (lse && threadIdx.x == 0) lse[bh] = L > 0.0f ? ref + logf(L) : -INFINITY;
 }
 
@@ -684,11 +644,11 @@ AttnPlan attn_plan(int32_t B, int32_t k, int32_t n_swa) {
   return p;
 }
 
-AttnWs attn_ws_layout(void* ws, int32_t B, const AttnPlan& plan, bool always_partial = false) {
+AttnWs attn_ws_layout(void* ws, int32_t B, const AttnPlan& plan) {
   AttnWs L{};
   size_t off = kWsHeader;
   char* base = (char*)ws;
-  if (plan.nsplit > 1 || always_partial) {
+  if (plan.nsplit > 1) {
     L.part_o = (float*)(base ? base + off : nullptr);
     off += align_up((size_t)B * plan.nsplit * kHAtt * kDMain * 4, 256);
     L.part_ml = (float2*)(base ? base + off : nullptr);
@@ -732,11 +692,11 @@ csa2_status attn_extras(const csa2_norm_rope* q_nr, const int64_t* q_pos, const 
 namespace {
 
 // One attention call over k rows per query named by topk (or, dense_n given,
-// entries 0 .. dense_n[b] - 1, through `pages` when given) joined with n_swa window rows.
+// entries 0 .. dense_n[b] - 1) joined with n_swa window rows.
 csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, const int32_t* dense_n, int32_t k,
-                     const csa2_pages* pages, const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
+                     const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
                      const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
-                     void* out, int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, cudaStream_t st) {
+                     float* out, float* lse_out, void* ws, size_t ws_bytes, cudaStream_t st) {
   AttnExtras ex;
   const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
   if (bad != CSA2_OK) return bad;
@@ -744,29 +704,26 @@ csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, c
     return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
   const AttnPlan plan = attn_plan(B, k, n_swa);
-  AttnWs L = attn_ws_layout(ws, B, plan, pages != nullptr);
+  AttnWs L = attn_ws_layout(ws, B, plan);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   if (reset_error(ws, st) != CSA2_OK) return CSA2_ERR_CUDA;
   const int smem = (int)sizeof(AttnSmem);
-  const bool partial = plan.nsplit > 1 || pages;
+  const bool partial = plan.nsplit > 1;
   const bool extras = ex.qnorm_w || ex.rope || ex.sink;
-  auto kern = pages     ? (extras ? k_attn<true, true, true> : k_attn<true, false, true>)
-              : partial ? (extras ? k_attn<true, true, false> : k_attn<true, false, false>)
-                        : (extras ? k_attn<false, true, false> : k_attn<false, false, false>);
-  PageMap pm{};
-  if (pages) pm = PageMap{pages->table, pages->max_pages, pages->n_pages};
+  auto kern = partial ? (extras ? k_attn<true, true> : k_attn<true, false>)
+                      : (extras ? k_attn<false, true> : k_attn<false, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return launch_status();
   {
     KernelTimer timer(partial ? "k_attn_part" : "k_attn", st);
     launch_pdl(kern, dim3(plan.nsplit, B), dim3(kAT), (size_t)smem, st, kv->kv_codes, kv->kv_scales, kv->seq_stride,
-               topk, dense_n, k, swa_e4m3, n_swa, pm, (const uint16_t*)q_bf16, softmax_scale, ex, plan.nchunks, plan.cps,
-               (float*)out, lse_out, L.part_o, L.part_ml, ws);
+               topk, dense_n, k, swa_e4m3, n_swa, (const uint16_t*)q_bf16, softmax_scale, ex, plan.nchunks, plan.cps,
+               out, lse_out, L.part_o, L.part_ml, ws);
   }
   if (partial) {
     KernelTimer timer("k_attn_merge", st);
     launch_pdl(k_attn_merge, dim3(B * kHAtt), dim3(128), 0, st, L.part_o, L.part_ml, plan.nsplit, sink, out,
-               out_type == CSA2_OUT_BF16 ? 1 : 0, lse_out);
+               lse_out);
   }
   return launch_status();
 }
@@ -784,8 +741,8 @@ extern "C" csa2_status csa2_sparse_attn_decode(const csa2_kv_planes* kv, int32_t
   if (!planes_ok(kv) || B <= 0 || B > 65535 || k < 0 || k > CSA2_MAX_TOPK || n_swa < 0 || n_swa > CSA2_MAX_SWA)
     return CSA2_ERR_INVALID_ARG;
   if ((k > 0 && !topk) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, topk, nullptr, k, nullptr, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win,
-                  out, CSA2_OUT_F32, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, topk, nullptr, k, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win,
+                  out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
@@ -805,16 +762,6 @@ extern "C" csa2_status csa2_dense_attn_decode(const csa2_kv_planes* kv, int32_t 
     return CSA2_ERR_INVALID_ARG;
   if ((n_max > 0 && !n_entries) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
   if (n_entries && !aligned(n_entries, 4)) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, nullptr, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
-                  q_pos, sink, win, out, CSA2_OUT_F32, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
+                  q_pos, sink, win, out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }
-
-namespace csa2 {
-// Page table of a call over B queries: rows long enough for n entries of each.
-bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
-  if (!p || p->max_pages < 0 || p->n_pages < 0 || kv->seq_stride > INT32_MAX) return false;
-  if (n > 0 && (!p->table || !aligned(p->table, 4))) return false;
-  if ((int64_t)p->n_pages * kv->seq_stride > INT32_MAX) return false;  // plane rows are 32-bit
-  return n <= (int64_t)p->max_pages * kv->seq_stride;
-}
-}  // namespace csa2

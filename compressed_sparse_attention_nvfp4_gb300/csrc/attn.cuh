@@ -183,7 +183,4 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, 128;"
 csa2_status attn_extras(const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
                         int32_t n_swa, float softmax_scale, AttnExtras* ex);
 
-// Whether the page table has rows for n entries of each query (attn.cu).
-bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n);
-
 }  // namespace csa2

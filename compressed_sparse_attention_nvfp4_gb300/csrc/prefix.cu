@@ -1849,6 +1849,14 @@ extern "C" size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t 
 namespace csa2 {
 namespace {
 
+// Page table of a call over B queries: rows long enough for n entries of each.
+bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
+  if (!p || p->max_pages < 0 || p->n_pages < 0 || kv->seq_stride > INT32_MAX) return false;
+  if (n > 0 && (!p->table || !aligned(p->table, 4))) return false;
+  if ((int64_t)p->n_pages * kv->seq_stride > INT32_MAX) return false;  // plane rows are 32-bit
+  return n <= (int64_t)p->max_pages * kv->seq_stride;
+}
+
 // Attention of B queries through page tables, G groups of them sharing prefixes (G = 0: none).
 csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B, const int32_t* n_entries, int32_t G,
                        const int32_t* group_start, const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
