@@ -1261,7 +1261,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
 
 // Queries that share nothing run one to a CTA (a pair of them in one MMA would multiply each one's rows by
 // the other's probabilities): 64 heads, chunks of 64 rows in two slots, every row widened once.
-//   S[64 x 64] = q' X^T    heads as M; two accumulators over the channel halves, which the softmax adds;
+//   S[64 x 64] = q' X^T    heads as M;
 //   O^T[512 x 64] += X^T P^T  four tiles of 128 channels, so that the rows serve both products as they are.
 // Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 64 KB of rows and 8 KB of P
 // written, 296 KB = 2,300 cycles at 128 bytes a cycle; the MMAs alone (S at the half rate of M = 64) take
@@ -1287,9 +1287,9 @@ struct __align__(1024) AloneSmem {
 };
 static_assert(sizeof(AloneSmem) <= 232448, "attention shared memory");
 
-// warps 0-3: softmax and epilogue; 4-19: rows (4-11 channels 0-255, 12-19 the others); then S MMAs of each
-// half, O MMAs, where rows come from
-constexpr int kAloneS = 20, kAloneO = 22, kAloneIndex = 23;
+// warps 0-3: softmax and epilogue; 4-19: rows (4-11 channels 0-255, 12-19 the others); then one warp
+// each: S MMAs, O MMAs, where rows come from
+constexpr int kAloneS = 20, kAloneO = 21, kAloneIndex = 22;
 
 // The rows of all `chunks` chunks of this CTA, whatever queries they belong to: thread's row 8 (w % 8) + l % 8,
 // blocks (of 32 channels) 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
@@ -1353,11 +1353,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           ptx::mbar_init(&S.x_full[i][h], 8);
           ptx::mbar_init(&S.x_free[i][h], 1);
         }
-        ptx::mbar_init(&S.s_full[i], 2);
+        ptx::mbar_init(&S.s_full[i], 1);
         ptx::mbar_init(&S.p_full[i], 4);
       }
       ptx::mbar_init(&S.o_read, 4);
-      ptx::mbar_init(&S.drained, 3);
+      ptx::mbar_init(&S.drained, 2);
       S.abort_flag = 0;
       ptx::fence_mbar_init();
     }
@@ -1419,42 +1419,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         }
       });
       where = 42;
-    } else if (warp < kAloneO) {
-      // ---- S of a channel half: 16 K steps
-      const int half = warp - kAloneS;
+    } else if (warp == kAloneS) {
+      // ---- S: 32 K steps, of each channel half as it comes
       constexpr uint32_t idesc_s = ptx::idesc_f16(64, kRows, 0);
-      const uint64_t da = ptx::smem_desc_noswizzle(&S.q[32 * half][0], kQPlane * 2, 128);
-      const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][32 * half][0], kRows * 16, 128);
+      const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
+      const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][0][0], kRows * 16, 128);
       for_items([&](int q, int, int, int, int nc, uint32_t n, uint32_t items) {
-        volatile int keep_waiting = 0;
-        if (half == 0) {  // the item's query, once S of the item before has left q'; it lands before anyone leaves
-          good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
-          if (!good) return;
-          if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
-            ptx::bulk_g2s(&S.q[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
-          }
-          __syncwarp();
-          good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
-        } else {
-          good = wait(&S.q_land, items);
+        // the item's query, once S of the item before has left q'; it lands before anyone leaves
+        good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
+        if (!good) return;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&S.q_land, kHAtt * kDMain * 2);
+          ptx::bulk_g2s(&S.q[0][0], k.q + (int64_t)q * kHAtt * kDMain, kHAtt * kDMain * 2, &S.q_land);
         }
+        __syncwarp();
+        volatile int keep_waiting = 0;
+        good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
-          const uint32_t m = n + (uint32_t)j, slot = m & 1u;
-          good = wait(&S.x_full[slot][half], m >> 1);  // O(m - 2) is done with the slot, so its softmax with S
-          if (!good) break;
-          ptx::tc_fence_after();
-          const uint32_t dst = tmem + kColS + 128u * (uint32_t)half + 64u * slot;
-          const uint64_t dbs = db + (uint64_t)slot * (kDMain * kRows * 2 / 16);
+          const uint32_t m = n + (uint32_t)j, slot = m & 1u, dst = tmem + kColS + 64u * slot;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            good = good && wait(&S.x_full[slot][half], m >> 1);  // O(m - 2) is done with the slot, so its softmax with S
+            if (!good) break;
+            ptx::tc_fence_after();
+            const uint64_t das = da + (uint64_t)(half * 2048);
+            const uint64_t dbs = db + (uint64_t)slot * (kDMain * kRows * 2 / 16) + (uint64_t)(half * 2048);
 #pragma unroll 8
-          for (int ks = 0; ks < 16; ++ks)
-            ptx::mma_f16_ss_elect(dst, da + (uint64_t)(ks * 128), dbs + (uint64_t)(ks * 128), idesc_s, ks > 0 ? 1u : 0u);
-          ptx::mma_commit_elect(&S.s_full[slot]);
+            for (int ks = 0; ks < 16; ++ks)
+              ptx::mma_f16_ss_elect(dst, das + (uint64_t)(ks * 128), dbs + (uint64_t)(ks * 128), idesc_s,
+                                    (half | ks) > 0 ? 1u : 0u);
+          }
+          if (good) ptx::mma_commit_elect(&S.s_full[slot]);
         }
       });
       where = 43;
-    } else {
+    } else if (warp == kAloneO) {
       // ---- O^T: per channel half two tiles of 128 channels, four K steps of 16 rows each
       constexpr uint32_t idesc_o = ptx::idesc_f16(128, kHAtt, 0) | (1u << 15);  // A M-major
       const uint64_t da = ptx::smem_desc_noswizzle(&S.x[0][0][0], 128, kRows * 16);
@@ -1508,14 +1508,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         for (int round = 0;; ++round) {
           float top = -INFINITY;
           if (good) {
-            uint32_t a[32], b[32], ph[16];
-            const uint32_t ta = tmem + lane_base + kColS + 64u * slot;
-            ptx::tmem_ld_16x32bx2_x32<32>(ta, a);
-            ptx::tmem_ld_16x32bx2_x32<32>(ta + 128u, b);
+            uint32_t a[32], ph[16];
+            ptx::tmem_ld_16x32bx2_x32<32>(tmem + lane_base + kColS + 64u * slot, a);
             ptx::tmem_wait_ld();
             uint64_t e[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) e[u] = add2(pack2(a[2 * u], a[2 * u + 1]), pack2(b[2 * u], b[2 * u + 1]));
+            for (int u = 0; u < 16; ++u) e[u] = pack2(a[2 * u], a[2 * u + 1]);
             top = probs32(e, mask, c2, ref, ph, sum);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -1610,7 +1608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     *abort_flag = 1;
     report_error(k.ws, CSA2_ERR_DEVICE_TIMEOUT, where);
   }
-  if (warp >= kAloneS && warp <= kAloneO) {  // every MMA has completed before tensor memory is freed
+  if (warp == kAloneS || warp == kAloneO) {  // every MMA has completed before tensor memory is freed
     ptx::mma_commit_elect(&S.drained);
     volatile int keep_waiting = 0;
     ptx::mbar_wait_warp(&S.drained, 0, &keep_waiting, kWaitBudget);
