@@ -391,6 +391,11 @@ __device__ __forceinline__ void widen_e4m3(uint4 w, uint32_t lim, uint4& a, uint
   b = make_uint4(two(w.z), two(w.z >> 16), two(w.w), two(w.w >> 16));
 }
 
+// The block that lane l (row l % 8 of its eight) begins with, mod 8.  A 128-bit load is served eight lanes at a
+// time: with one block for all they would read eight rows at the same bank, 32 accesses for a warp's load
+// instead of 4, from the memory that also feeds the MMAs (paged ragged 48 x 65536: 253 us, rotated @@).
+__device__ __forceinline__ int rotated(int lane) { return (lane & 7) + (lane >> 3); }
+
 // One thread's fetched codes of 32 channels of a row.
 struct Fetch {
   uint4 codes, more;  // 16 bytes of codes, or 32 of a window row
@@ -481,23 +486,24 @@ __device__ __forceinline__ float probs32(uint64_t (&s)[16], uint32_t mask, float
 
 // The operands of all `chunks` chunks of this pair of CTAs, whatever items they belong to, by the 16 row
 // warps: per operand two groups of four, which write every other piece.  Operand 0 (S's, warps 0-7): this
-// CTA's 64 rows, handed over by 128 channels: in piece i a thread has block (of 32 channels) 4 i + l / 8 of
+// CTA's 64 rows, handed over by 128 channels: in piece i a thread has one of the blocks (of 32 channels) 4 i .. of
 // rows 8 (w % 4) + l % 8 and 32 more.  Operand 1 (O's): its 256 channels of all rows, by 32 rows: a thread
-// has blocks l / 8 and l / 8 + 4 of its eight of row 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64
+// has two of its eight blocks, four apart, of row 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64
 // contiguous bytes of eight rows, and a store writes eight rows of a plane: no bank conflicts.  A step writes
 // one piece and fetches the codes of the next (half a chunk ahead); a chunk of the image is copied instead,
 // by the first warp of each group.  Both operands run the same code: the kernel's loops have to fit the
 // instruction cache (unrolled by piece and operand they waited more for instructions than for data).
 __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int rank,
                                           int chunks, int w, int lane) {
-  const int op = w >> 3, group = (w >> 2) & 1, cb = lane >> 3;
+  const int op = w >> 3, group = (w >> 2) & 1;
   const int rl = 8 * (w & 3) + (lane & 7);
   const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0, row_u = op ? 0 : 32;
-  const int blk0 = op ? 8 * rank + cb : cb, blk_step = op ? 0 : 4, blk_u = op ? 4 : 0;
+  const int b = rotated(lane) & (op ? 7 : 3);
+  const int blk0 = op ? 8 * rank + b : b, blk_step = op ? 0 : 4, blk_u = op ? (b ^ 4) - b : 0;
   const int plane = (op ? 32 : kOwnChunk) * 8;  // f16 elements
-  uint16_t* const dst = (op ? &S.xo[0][4 * cb][0] : &S.xs[4 * cb][0]) + rl * 8;
+  uint16_t* const dst = (op ? &S.xo[0][4 * b][0] : &S.xs[4 * b][0]) + rl * 8;
   constexpr int dst_step = 16 * 1024 / 2;  // a piece
-  const int dst_u = op ? 16 * 32 * 8 : 32 * 8;
+  const int dst_u = op ? blk_u * 4 * 32 * 8 : 32 * 8;
   const int steps = chunks * 2;  // step st: chunk st / 2, piece 2 (st % 2) + group
   int r[2], image = -1;
   Fetch f[2];
@@ -1019,14 +1025,14 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     img[i] = *reinterpret_cast<const uint4*>(smem + (i / kHAtt) * kQPad + (i % kHAtt) * 16);
 }
 
-// The image's chunks first, first + step, ..: a warp's lane l widens block (of 32 channels) 4 i + l / 8 of
+// The image's chunks first, first + step, ..: a warp's lane l widens four blocks (of 32 channels), 4 i + the rotated one, of
 // row l % 8 of its eight, and stores 16 bytes to each of the block's four planes, 128 contiguous bytes for
 // eight rows.  Bytes bound it: 288 read and 1,024 written an entry.
 __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
                                              int step) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_group, s_at;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cb = lane >> 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int64_t t = first_chunk;; t += step) {
     // the group whose image holds chunk t
     if (threadIdx.x == 0) s_group = -1;
@@ -1054,10 +1060,11 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
     }
     Fetch f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, 4 * i + cb);
-    uint16_t* dst = image + t * kDMain * kChunk + (4 * cb * kChunk + row) * 8;
+    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, (4 * i + rotated(lane)) & 15);
+    uint16_t* dst = image + t * kDMain * kChunk + row * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(f[i], r, dst + i * 16 * kChunk * 8, kChunk * 8);
+    for (int i = 0; i < 4; ++i)
+      put(f[i], r, dst + ((4 * i + rotated(lane)) & 15) * 4 * kChunk * 8, kChunk * 8);
     __syncthreads();  // s_group is written again
   }
 }
@@ -1292,10 +1299,12 @@ static_assert(sizeof(AloneSmem) <= 232448, "attention shared memory");
 constexpr int kAloneS = 20, kAloneO = 21, kAloneIndex = 22;
 
 // The rows of all `chunks` chunks of this CTA, whatever queries they belong to: thread's row 8 (w % 8) + l % 8,
-// blocks (of 32 channels) 8 (w / 8) + l / 8 and four more; codes fetched two chunks ahead.
+// of the blocks (of 32 channels) 8 (w / 8) .. the rotated first and the one four on; codes fetched two chunks ahead.
 __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, int chunks, int w, int lane) {
-  const int half = w >> 3, rl = 8 * (w & 7) + (lane & 7), blk = 8 * half + (lane >> 3);
-  uint16_t* const dst = &S.x[0][4 * blk][rl * 8];
+  const int half = w >> 3, rl = 8 * (w & 7) + (lane & 7);
+  const int b0 = 8 * half + (rotated(lane) & 7), b1 = b0 ^ 4;
+  uint16_t* const dst = &S.x[0][4 * b0][rl * 8];
+  const int to_b1 = (b1 - b0) * 4 * kRows * 8;
   bool good = true;
   int ra, rb;
   Fetch fa[2], fb[2];
@@ -1305,8 +1314,8 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     good = good && ptx::mbar_wait_warp(&S.r_full[slot], ((uint32_t)m / kRing) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     r = S.rows[slot][rl];
-    fetch(f[0], k, r, blk);
-    fetch(f[1], k, r, blk + 4);
+    fetch(f[0], k, r, b0);
+    fetch(f[1], k, r, b1);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
   };
@@ -1320,7 +1329,7 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     if (!good) return;
     uint16_t* d = dst + slot * (kDMain * kRows);
     put(f[0], r, d, kRows * 8);
-    put(f[1], r, d + 16 * kRows * 8, kRows * 8);
+    put(f[1], r, d + to_b1, kRows * 8);
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.x_full[slot][half]);
