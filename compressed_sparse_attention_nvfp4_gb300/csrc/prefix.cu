@@ -1025,14 +1025,14 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     img[i] = *reinterpret_cast<const uint4*>(smem + (i / kHAtt) * kQPad + (i % kHAtt) * 16);
 }
 
-// The image's chunks first, first + step, ..: a warp's lane l widens four blocks (of 32 channels), 4 i + the rotated one, of
+// The image's chunks first, first + step, ..: a warp's lane l widens four blocks (of 32 channels), the rotated one xor 4 i, of
 // row l % 8 of its eight, and stores 16 bytes to each of the block's four planes, 128 contiguous bytes for
 // eight rows.  Bytes bound it: 288 read and 1,024 written an entry.
 __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
                                              int step) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_group, s_at;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = rotated(lane) & 7;
   for (int64_t t = first_chunk;; t += step) {
     // the group whose image holds chunk t
     if (threadIdx.x == 0) s_group = -1;
@@ -1060,11 +1060,11 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
     }
     Fetch f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, (4 * i + rotated(lane)) & 15);
+    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, b0 ^ (4 * i));
     uint16_t* dst = image + t * kDMain * kChunk + row * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      put(f[i], r, dst + ((4 * i + rotated(lane)) & 15) * 4 * kChunk * 8, kChunk * 8);
+      put(f[i], r, dst + (b0 ^ (4 * i)) * 4 * kChunk * 8, kChunk * 8);
     __syncthreads();  // s_group is written again
   }
 }
@@ -1402,7 +1402,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   };
 
   if (warp >= 4 && warp < kAloneS) {
-    ptx::setmaxnreg_dec<kRowRegs>();
     good = alone_rows(S, k, t1 - t0, warp - 4, lane);
     where = 41;
   } else if (warp >= kAloneS) {
@@ -1496,7 +1495,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   } else {
     // ---- softmax: lane l of warp w head 16 w + l % 16, chunk rows 32 (l / 16) .. (the rows of an M = 64
     // accumulator lie in lanes 0-15 of each quarter; two lanes share a head's columns)
-    ptx::setmaxnreg_inc<kSoftRegs>();
+    ptx::setmaxnreg_dec<72>();
     const int rh = lane >> 4, h = 16 * warp + (lane & 15);
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     for_items([&](int q, int, int p, int, int nc, uint32_t n, uint32_t) {
