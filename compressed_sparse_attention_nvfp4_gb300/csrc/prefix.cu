@@ -725,10 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
             if (!good) break;
             ptx::tc_fence_after();
             const uint64_t at = (uint64_t)(i * 1024);  // q'[16 i], xs[16 i]: 16 KB on; a K step 2 KB
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              ptx::mma_f16_ss_pair_elect(dst, da + at + (uint64_t)(ks * 128), db + at + (uint64_t)(ks * 128), idesc_s,
-                                         (i | ks) > 0 ? 1u : 0u);
+            ptx::mma_f16_ss_pair_run_elect<8, 128, 128>(dst, da + at, db + at, idesc_s, i > 0 ? 1u : 0u);
             ptx::mma_commit_pair_elect(&S.x_free[0][i]);
           }
           if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
@@ -761,13 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
             good = wait(&S.x_full[1][i], m);
             if (!good) break;
             ptx::tc_fence_after();
+            // p[4 i ..]: 2 KB a K step; xo[i], rows 16 ks: 256 bytes a step
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)  // p[4 i + 2 ks]: 2 KB a step; xo[i], rows 16 ks: 256 bytes a step
-#pragma unroll
-              for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[i][16 h], 8 KB on
-                ptx::mma_f16_ss_pair_elect(tmem + 128u * (uint32_t)h, dpo + (uint64_t)((2 * i + ks) * 128),
-                                           dx + (uint64_t)(i * 1024 + h * 512 + ks * 16), idesc_o,
-                                           (j | i | ks) > 0 ? 1u : 0u);
+            for (int h = 0; h < 2; ++h)  // channels 128 h .. of each CTA: xo[i][16 h], 8 KB on
+              ptx::mma_f16_ss_pair_run_elect<2, 128, 16>(tmem + 128u * (uint32_t)h, dpo + (uint64_t)(2 * i * 128),
+                                                         dx + (uint64_t)(i * 1024 + h * 512), idesc_o,
+                                                         (j | i) > 0 ? 1u : 0u);
             ptx::mma_commit_pair_elect(&S.x_free[1][i]);
           }
           if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.p_free[m & 1]);
@@ -1453,10 +1449,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             ptx::tc_fence_after();
             const uint64_t das = da + (uint64_t)(half * 2048);
             const uint64_t dbs = db + (uint64_t)slot * (kDMain * kRows * 2 / 16) + (uint64_t)(half * 2048);
-#pragma unroll 8
-            for (int ks = 0; ks < 16; ++ks)
-              ptx::mma_f16_ss_elect(dst, das + (uint64_t)(ks * 128), dbs + (uint64_t)(ks * 128), idesc_s,
-                                    (half | ks) > 0 ? 1u : 0u);
+#pragma unroll
+            for (int ks = 0; ks < 16; ks += 8)
+              ptx::mma_f16_ss_run_elect<8, 128, 128>(dst, das + (uint64_t)(ks * 128), dbs + (uint64_t)(ks * 128), idesc_s,
+                                                     (half | ks) > 0 ? 1u : 0u);
           }
           if (good) ptx::mma_commit_elect(&S.s_full[slot]);
         }
@@ -1481,11 +1477,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           for (int half = 0; half < 2; ++half) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-              for (int ks = 0; ks < kRows / 16; ++ks)
-                ptx::mma_f16_ss_elect(tmem + 64u * (uint32_t)(2 * half + mt),
-                                      das + (uint64_t)(half * 2048 + mt * 1024 + ks * 16), dbs + (uint64_t)(ks * 128),
-                                      idesc_o, (j | ks) > 0 ? 1u : 0u);
+              ptx::mma_f16_ss_run_elect<kRows / 16, 16, 128>(tmem + 64u * (uint32_t)(2 * half + mt),
+                                                             das + (uint64_t)(half * 2048 + mt * 1024), dbs, idesc_o,
+                                                             j > 0 ? 1u : 0u);
             ptx::mma_commit_elect(&S.x_free[slot][half]);
           }
         }

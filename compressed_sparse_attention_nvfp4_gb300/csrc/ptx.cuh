@@ -248,6 +248,58 @@ __device__ __forceinline__ void mma_f16_ss_elect(uint32_t d_tmem, uint64_t a_des
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// kN (2, 4 or 8) MMAs of one accumulator, operands kA and kB descriptor units (16 bytes) apart, issued by the
+// lane one elect.sync picks: next to busy warps every instruction of the issuing warp counts (32 S MMAs of
+// M = N = 64, 1,024 cycles by themselves, took 2,300 issued one by one; in runs the paged attention of 48
+// queries of up to 65,536 entries fell from 234 to 221 us).  The low words of the descriptors hold the addresses.
+#define CSA2_MMA_FIRST(G)                                                                         \
+  "{\n\t.reg .pred p, e, t;\n\t.reg .b32 r, a, b;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\t" \
+  "setp.eq.b32 t, 0, 0;\n\telect.sync r|e, 0xffffffff;\n\t"                                       \
+  "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"                                            \
+  "@e tcgen05.mma.cta_group::" G ".kind::f16 [%0], da, db, %5, p;\n\t"
+#define CSA2_MMA_NEXT(G, I)                                                                       \
+  "add.u32 a, %1, " I " * %7;\n\tadd.u32 b, %3, " I " * %8;\n\t"                                    \
+  "mov.b64 da, {a, %2};\n\tmov.b64 db, {b, %4};\n\t"                                              \
+  "@e tcgen05.mma.cta_group::" G ".kind::f16 [%0], da, db, %5, t;\n\t"
+#define CSA2_MMA_RUN(G)                                                                           \
+  do {                                                                                            \
+    const uint32_t al = (uint32_t)a_desc, ah = (uint32_t)(a_desc >> 32);                          \
+    const uint32_t bl = (uint32_t)b_desc, bh = (uint32_t)(b_desc >> 32);                          \
+    if constexpr (kN == 2)                                                                        \
+      asm volatile(CSA2_MMA_FIRST(G) CSA2_MMA_NEXT(G, "1") "}" ::"r"(d_tmem), "r"(al), "r"(ah), "r"(bl), "r"(bh), \
+                   "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB)                                  \
+                   : "memory");                                                                   \
+    else if constexpr (kN == 4)                                                                   \
+      asm volatile(CSA2_MMA_FIRST(G) CSA2_MMA_NEXT(G, "1") CSA2_MMA_NEXT(G, "2") CSA2_MMA_NEXT(G, "3") "}" ::"r"( \
+                       d_tmem),                                                                   \
+                   "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB) \
+                   : "memory");                                                                   \
+    else                                                                                          \
+      asm volatile(CSA2_MMA_FIRST(G) CSA2_MMA_NEXT(G, "1") CSA2_MMA_NEXT(G, "2") CSA2_MMA_NEXT(G, "3") \
+                       CSA2_MMA_NEXT(G, "4") CSA2_MMA_NEXT(G, "5") CSA2_MMA_NEXT(G, "6") CSA2_MMA_NEXT(G, "7") "}" ::"r"( \
+                           d_tmem),                                                               \
+                   "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(accumulate), "n"(kA), "n"(kB) \
+                   : "memory");                                                                   \
+  } while (0)
+template <int kN, int kA, int kB>
+__device__ __forceinline__ void mma_f16_ss_run_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                     uint32_t idesc, uint32_t accumulate) {
+  static_assert(kN == 2 || kN == 4 || kN == 8, "MMAs of a run");
+  CSA2_MMA_RUN("1");
+}
+// The same over a CTA pair, issued by the even CTA: each CTA's shared memory holds half of A's rows and half of
+// B's rows (N) at the same offsets.  At M = 128 each CTA's tensor memory holds 64 rows of D: lanes 0-63 the
+// columns of the even CTA's half of N, lanes 64-127 those of the odd's (checked against a CPU product on the
+// GPU, B K-major and N-major, N = 64 .. 256).
+template <int kN, int kA, int kB>
+__device__ __forceinline__ void mma_f16_ss_pair_run_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                          uint32_t idesc, uint32_t accumulate) {
+  static_assert(kN == 2 || kN == 4 || kN == 8, "MMAs of a run");
+  CSA2_MMA_RUN("2");
+}
+#undef CSA2_MMA_FIRST
+#undef CSA2_MMA_NEXT
+#undef CSA2_MMA_RUN
 // mma_f16_ts issued by the lane elect.sync picks (the warp runs the loop together)
 __device__ __forceinline__ void mma_f16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                                  uint32_t idesc, uint32_t accumulate) {
@@ -384,19 +436,6 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot_smem, uint32_t co
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
-}
-// mma_f16_ss_elect over a CTA pair, issued by the even CTA: each CTA's shared memory holds half of
-// A's rows and half of B's rows (N) at the same offsets.  At M = 128 each CTA's tensor memory holds
-// 64 rows of D: lanes 0-63 the columns of the even CTA's half of N, lanes 64-127 those of the odd's
-// (checked against a CPU product on the GPU, B K-major and N-major, N = 64 .. 256).
-__device__ __forceinline__ void mma_f16_ss_pair_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                      uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync r|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 // Arrive on `bar` of both CTAs of the pair once the MMAs issued above have completed.
 __device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar) {
