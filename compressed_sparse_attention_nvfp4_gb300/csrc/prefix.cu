@@ -289,6 +289,7 @@ struct __align__(1024) PrefixSmem {
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_read;                          // epilogue done with O
   uint64_t drained;                         // every MMA issued complete (two warps)
+  Part part;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -640,15 +641,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     __syncwarp();
     ptx::tmem_alloc_pair(&S.tmem_base, kCols);
   }
+  if (warp == kIndexWarp && lane < 2) ptx::prefetch_tensormap(lane ? &maps.o : &maps.s);
   ptx::griddep_launch();
-  ptx::griddep_wait();
   ptx::tc_fence_before();
-  __syncthreads();
   ptx::cluster_sync();  // both CTAs' barriers initialised
+  ptx::griddep_wait();
+  if (tid < (int)(sizeof(Part) / 4))
+    reinterpret_cast<int32_t*>(&S.part)[tid] = reinterpret_cast<const int32_t*>(k.parts + cluster)[tid];
+  __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  const Part& part = k.parts[cluster];
+  const Part& part = S.part;
   const int t0 = part.t0, t1 = part.t1;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;

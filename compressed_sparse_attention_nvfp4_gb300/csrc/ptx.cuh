@@ -398,6 +398,11 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// fetches a tensor map (a kernel parameter) ahead of its first copy
+__device__ __forceinline__ void prefetch_tensormap(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // ------------------------------------------------------- CTA pairs (clusters)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
