@@ -29,7 +29,8 @@ constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of 
 constexpr int kChunk = 128;      // rows of a chunk
 constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
 constexpr int kImageQueries = 3;   // a group of at least this many queries has its shared entries widened once
-constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM
+constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM,
+constexpr int kWidenFirst = 152;   // of which these come before the queries' staging
 constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
 
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
@@ -394,7 +395,7 @@ __device__ __forceinline__ void widen_e4m3(uint4 w, uint32_t lim, uint4& a, uint
 
 // The block that lane l (row l % 8 of its eight) begins with, mod 8.  A 128-bit load is served eight lanes at a
 // time: with one block for all they would read eight rows at the same bank, 32 accesses for a warp's load
-// instead of 4, from the memory that also feeds the MMAs (paged ragged 48 x 65536: 253 us, rotated @@).
+// instead of 4, from the memory that also feeds the MMAs (paged ragged 48 x 65536: 253 us, with the blocks rotated 234).
 __device__ __forceinline__ int rotated(int lane) { return (lane & 7) + (lane >> 3); }
 
 // One thread's fetched codes of 32 channels of a row.
@@ -927,42 +928,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 
 // ------------------------------------------------------ preparation and merge
 
-// A query into its f16 image and c2 (attn.cuh, stage_q: the same steps, from global memory by 16 warps of
-// four heads each, lane l holding channels 16 l ..), and the rotation's cosines and sines.  The image goes
-// through shared memory with padded planes, so that its stores are whole lines.
-constexpr int kQPad = kHAtt * 16 + 16;  // bytes of a plane
-constexpr int kPrepSmem = kDMain / 8 * kQPad;
-__device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, unsigned char* smem) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint4* const img = reinterpret_cast<uint4*>(a.image + (int64_t)b * kHAtt * kDMain);
+// 16 heads of a query into its f16 image and c2 (attn.cuh, stage_q: the same steps, from global memory, a warp to a
+// head, lane l holding channels 16 l ..), and the rotation's cosines and sines.  The image goes through shared
+// memory with padded planes, so that its stores are runs of 256 bytes.  Instructions bound it: with a CTA
+// for all 64 heads the call on 32 normalised and rotated queries took 63.9 us, with four 58.9.
+constexpr int kStageCtas = 4, kStageHeads = kHAtt / kStageCtas;  // of a query; heads of each
+static_assert(kStageHeads == kPrepThreads / 32, "a head for each warp");
+constexpr int kQPad = kStageHeads * 16 + 16;  // bytes of a plane
+constexpr int kPrepSmem = 64 * 1024;          // this, or the plan's lists
+static_assert(kDMain / 8 * kQPad <= kPrepSmem, "shared memory of the staging");
+__device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, int part, unsigned char* smem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = kStageHeads * part + warp;
+  uint4* const img = reinterpret_cast<uint4*>(a.image + (int64_t)b * kHAtt * kDMain) + kStageHeads * part;
+  auto image_at = [&](int i) -> uint4& { return img[i / kStageHeads * kHAtt + i % kStageHeads]; };
   if (b == B) {  // the missing second query of an odd group
-    for (int i = threadIdx.x; i < kHAtt * kDMain / 8; i += kPrepThreads) img[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (threadIdx.x < kHAtt) a.c2[(int64_t)b * kHAtt + threadIdx.x] = 1.0f;
+    for (int i = threadIdx.x; i < kStageHeads * kDMain / 8; i += kPrepThreads) image_at(i) = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) a.c2[(int64_t)b * kHAtt + h] = 1.0f;
     return;
   }
-  constexpr int kHeads = kHAtt / (kPrepThreads / 32);
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + warp * kHeads) * kDMain) + 2 * lane;
-  uint4 qv[kHeads][2];
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + h) * kDMain) + 2 * lane;
+  const uint4 q0 = src[0], q1 = src[1];
+  float4 g[4];
+  if (a.norm_w)
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    qv[i][0] = src[i * (kDMain / 8)];
-    qv[i][1] = src[i * (kDMain / 8) + 1];
-  }
+    for (int j = 0; j < 4; ++j) g[j] = __ldg(reinterpret_cast<const float4*>(a.norm_w) + 4 * lane + j);
   __shared__ float2 s_turn[32];
-  float rc = 1.0f, rs = 0.0f;  // lane l: pair l
-  if (a.rope) {
-    if (warp == 0) {  // one warp: the angles are formed in fp64, of which an SM does little
-      rope_cos_sin(a.th.t[lane], (double)a.qpos[b], rc, rs);
-      s_turn[lane] = a.turn[(int64_t)b * 32 + lane] = make_float2(rc, rs);
-    }
-    __syncthreads();
-    rc = s_turn[lane].x;
-    rs = s_turn[lane].y;
+  if (a.rope && warp == 0) {  // one warp: the angles are formed in fp64, of which an SM does little
+    float c, s;
+    rope_cos_sin(a.th.t[lane], (double)a.qpos[b], c, s);
+    s_turn[lane] = make_float2(c, s);
+    if (part == 0) a.turn[(int64_t)b * 32 + lane] = make_float2(c, s);
   }
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = warp * kHeads + i;
-    const uint4 q0 = qv[i][0], q1 = qv[i][1];
+  {
     const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
     float v[16];
 #pragma unroll
@@ -977,23 +974,22 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float r = 1.0f / sqrtf(ss / (float)kDMain + a.eps);
-      const float4* wv = reinterpret_cast<const float4*>(a.norm_w) + 4 * lane;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 g = __ldg(wv + j);
-        v[4 * j] = g.x * (v[4 * j] * r);
-        v[4 * j + 1] = g.y * (v[4 * j + 1] * r);
-        v[4 * j + 2] = g.z * (v[4 * j + 2] * r);
-        v[4 * j + 3] = g.w * (v[4 * j + 3] * r);
+        v[4 * j] = g[j].x * (v[4 * j] * r);
+        v[4 * j + 1] = g[j].y * (v[4 * j + 1] * r);
+        v[4 * j + 2] = g[j].z * (v[4 * j + 2] * r);
+        v[4 * j + 3] = g[j].w * (v[4 * j + 3] * r);
       }
     }
-    if (a.rope) {  // lanes 28-31 hold the pairs 8 (l - 28) ..
+    if (a.rope) {
+      __syncthreads();
+      if (lane >= 28)  // these hold the pairs 8 (l - 28) ..
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int pair = (8 * (lane - 28) + j) & 31;
-        const float c = __shfl_sync(0xffffffffu, rc, pair), sn = __shfl_sync(0xffffffffu, rs, pair);
-        if (lane >= 28) rope_pair(v[2 * j], v[2 * j + 1], c, sn);
-      }
+        for (int j = 0; j < 8; ++j) {
+          const float2 t = s_turn[8 * (lane - 28) + j];
+          rope_pair(v[2 * j], v[2 * j + 1], t.x, t.y);
+        }
     }
     float mx = 0.0f;
 #pragma unroll
@@ -1016,13 +1012,13 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
       rp[0] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
       rp[1] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
     }
-    *reinterpret_cast<uint4*>(smem + (2 * lane) * kQPad + h * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(smem + (2 * lane + 1) * kQPad + h * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(smem + (2 * lane) * kQPad + warp * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(smem + (2 * lane + 1) * kQPad + warp * 16) = make_uint4(o[4], o[5], o[6], o[7]);
     if (lane == 0) a.c2[(int64_t)b * kHAtt + h] = kLog2e * a.scale * exp2i_f32(sig);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kHAtt * kDMain / 8; i += kPrepThreads)
-    img[i] = *reinterpret_cast<const uint4*>(smem + (i / kHAtt) * kQPad + (i % kHAtt) * 16);
+  for (int i = threadIdx.x; i < kStageHeads * kDMain / 8; i += kPrepThreads)
+    image_at(i) = *reinterpret_cast<const uint4*>(smem + (i / kStageHeads) * kQPad + (i % kStageHeads) * 16);
 }
 
 // The image's chunks first, first + step, ..: a warp's lane l widens four blocks (of 32 channels), the rotated one xor 4 i, of
@@ -1069,20 +1065,26 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
   }
 }
 
-// Everything the attention needs, by independent CTAs of one launch: the plan, the queries, the image.
+// Everything the attention needs, by independent CTAs of one launch: the plan, the queries, the image, of which
+// half the CTAs come first (all behind the queries: 53.4 and 75.1 us for prefix 32 on 8192 and 101 on 4001
+// instead of 50.9 and 71.2).
 __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, PrefixQuery q,
                                                               const __grid_constant__ PrefixKernel k, uint16_t* image) {
   extern __shared__ __align__(16) unsigned char prep_smem[];
   ptx::griddep_launch();
   ptx::griddep_wait();
-  const int64_t b = (int64_t)blockIdx.x - 1;
+  const int stage = kStageCtas * (a.B + 1), widen = (int)gridDim.x - 1 - stage, widen1 = min(widen, kWidenFirst);
+  int b = (int)blockIdx.x - 1;
   if (b < 0) {
     int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
     if (a.G > 0) plan_block<false>(a, ints, kPrepSmem / 4);
     else plan_block<true>(a, ints, kPrepSmem / 4);
+    return;
   }
-  else if (b <= a.B) stage_block(q, a.B, (int)b, prep_smem);
-  else widen_chunks(a, k, image, (int)(b - a.B - 1), (int)(gridDim.x - a.B - 2));
+  if (b < widen1) return widen_chunks(a, k, image, b, widen);
+  b -= widen1;
+  if (b < stage) return stage_block(q, a.B, b / kStageCtas, b % kStageCtas, prep_smem);
+  widen_chunks(a, k, image, widen1 + b - stage, widen);
 }
 
 // kC consecutive output channels at element `at`
@@ -1903,7 +1905,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   {
     KernelTimer timer("k_prefix_prep", st);
     const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
-    launch_pdl(k_prefix_prep, dim3((unsigned)(B + 2 + widen)), dim3(kPrepThreads), (size_t)kPrepSmem, st, a, pq, k,
+    launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads), (size_t)kPrepSmem, st, a, pq, k,
                L.image);
   }
   const int slices = B < kSliceQueries ? 4 : 1;
