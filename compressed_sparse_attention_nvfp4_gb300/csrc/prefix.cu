@@ -1635,12 +1635,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // once, while the first partials' channels are on their way.
 constexpr int kMergeThreads = 512;
 template <int kSlices>
-__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const int2* __restrict__ qpart,
+__global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_merge(const int2* __restrict__ qpart,
                                                                const uint4* __restrict__ part_o,
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
                                                                int out_bf16, float* lse, LseRest fix) {
+  constexpr int kAhead = kSlices > 1 ? kJoin : 4;  // partials on their way
   constexpr int kTiles = 4 / kSlices, kPer = 128 * kTiles;
   static_assert(kSlices == 1 || kTiles == 1, "all channels, or a tile of them");
   __shared__ __align__(16) float s_w[kAlone][8];  // read four at a time
@@ -1658,10 +1659,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const int2* __res
     s_m[i / 8][i % 8] = ml.y == 0.0f ? -INFINITY : ml.x;
     s_w[i / 8][i % 8] = ml.y;
   }
-  uint4 v[kJoin];
+  uint4 v[kAhead];
   auto fetch = [&](int k0) {
 #pragma unroll
-    for (int j = 0; j < kJoin; ++j)
+    for (int j = 0; j < kAhead; ++j)
       if (k0 + j * kSlices < part.y) v[j] = part_o[((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * 128 + (t & 127)];
   };
   fetch(slice);
@@ -1690,10 +1691,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const int2* __res
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  for (int k0 = slice; k0 < part.y; k0 += kSlices * kJoin) {
+  for (int k0 = slice; k0 < part.y; k0 += kSlices * kAhead) {
     if (k0 > slice) fetch(k0);
 #pragma unroll
-    for (int j = 0; j < kJoin; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       const int k = k0 + j * kSlices;
       if (k >= part.y) break;
       const float4 w0 = *reinterpret_cast<const float4*>(&s_w[k][0]), w1 = *reinterpret_cast<const float4*>(&s_w[k][4]);
