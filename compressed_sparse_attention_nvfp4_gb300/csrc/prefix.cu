@@ -1,23 +1,35 @@
-// Attention for a batch whose queries share prefixes.
+// Attention through page tables: for queries by themselves, and for a batch whose queries share prefixes.
 //
-// Two queries of a group make a pair, and their 2 x 64 heads the 128 rows of one MMA, so an entry of
-// the shared prefix is read and widened once for two queries and the tensor cores run at their full
-// rate (64 rows alone run at half of it).  A pair of CTAs (one query each) computes a pair of queries
-// with tcgen05.mma.cta_group::2 in chunks of 128 rows:
+// out = softmax(scale q X^T) X over the rows X that a query sees: the entries its table row names, then its
+// window.  With z the logits in log2 units, a part of the rows leaves its reference m, l = sum 2^(z - m) and
+// O / l = sum 2^(z - m) x / l; parts join by log-sum-exp.  Each call is three launches:
+//   k_prefix_prep   the plan (which chunks of rows every CTA runs), the queries' f16 images, and the image:
+//                   the shared entries of groups of kImageQueries or more queries, widened to f16 once;
+//   k_paged_attn    one query to a CTA (G = 0), or
+//   k_prefix_attn   two queries of a group to a pair of CTAs;
+//   k_paged_merge / k_prefix_merge   the join, the sink, the turn back, the output's type.
+// All chunks form one list that the CTAs share evenly, whatever the queries' lengths; a query cut between
+// CTAs leaves a partial in each.
+//
+// Pairs.  Two queries of a group make a pair, and their 2 x 64 heads the 128 rows of one MMA, so an entry of
+// the shared prefix serves two queries and the tensor cores run at their full rate (64 rows alone run at half
+// of it).  A pair of CTAs (one query each) computes with tcgen05.mma.cta_group::2 in chunks of 128 rows:
 //   S[128 x 128 rows] = q' X^T   each CTA holds 64 of the rows (all channels), K-major;
 //   P = 2^(S c2 - m)             each CTA its own query: thread t head t % 64, rows 64 (t / 64) ..;
 //   O[128 x 512] += P X          each CTA holds 256 of the channels (all rows), N-major.
 // At M = 128 a CTA's tensor memory holds 64 rows of an accumulator in 128 lanes, so O takes 256
-// columns and leaves room for two S buffers; neither operand is exchanged between the CTAs: each
-// widens the 64 x 512 values it holds for S and the 128 x 256 it holds for O from the 288-byte entries
-// itself.  Shared memory is what bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 128 KB
-// of rows and 16 KB of P written, 368 KB = 2,900 cycles at 128 bytes a cycle, against 2,048 cycles of
-// MMA; with one buffer for each operand there is no room for a second chunk, so both are handed over in
-// four pieces (128 channels of S's rows, 32 rows of O's).
+// columns and leaves room for two S buffers; neither operand is exchanged between the CTAs: each holds the
+// 64 x 512 values of S and the 128 x 256 of O.  Chunks of the image come as they are by tensor copies (widened
+// by every pair for itself 768 us a call on 64 queries of 65,000 shared entries, from the image 451); the rest
+// is widened by the row warps.  Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs,
+// 128 KB of rows and 16 KB of P written, 368 KB = 2,900 cycles at 128 bytes a cycle, against 2,048 cycles of
+// MMA; measured, 3,100 to 3,400.  With one buffer for each operand there is no room for a second chunk, so both
+// are handed over in four pieces (128 channels of S's rows, 32 rows of O's).
 // Behind the shared entries come the two queries' own (their last entries and windows): chunks whose
-// first 64 rows are the first query's and whose last 64 the second's, each query masking the other's.
-// All pairs' chunks form one list that kClusters CTA pairs share evenly, whatever the groups' sizes; a
-// pair cut between them leaves (m, l, O) partials that k_prefix_merge joins by log-sum-exp.
+// first 64 rows are the first query's and whose last 64 the second's, each query masking the other's; behind
+// the shorter's last, 128 rows of the longer.
+// Measured: 64 queries on 65,000 shared entries 386 us, 1.42 PFLOP/s, 75 % of the rate of a library bf16
+// product; 2 queries on 512 17 us, three launches and their dependent loads.
 #include "attn.cuh"
 #include "index_scan.cuh"
 
@@ -1274,8 +1286,8 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
 //   O^T[512 x 64] += X^T P^T  four tiles of 128 channels, so that the rows serve both products as they are.
 // Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 64 KB of rows and 8 KB of P
 // written, 296 KB = 2,300 cycles at 128 bytes a cycle; the MMAs alone (S at the half rate of M = 64) take
-// 1,800.  All queries' chunks form one list that kAlone CTAs share evenly, and a query cut between them
-// leaves partials, as above.
+// 1,800; measured, about 2,800, the wait of a slot for its softmax among them.  48 queries of up to 65,536 entries
+// take 219 us (0.79 PFLOP/s, 1.8 TB/s of entries), one of 4,096 entries 17 us.
 constexpr int kAlone = 152;
 constexpr int kRows = 64;  // rows of a chunk
 constexpr int kRing = 8;   // chunks whose rows are found ahead
@@ -1632,7 +1644,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // The join over partials of the epilogue's order: a CTA has eight heads 8 g .. and all channels, thread t of it
 // channel t; with four slices the 128 channels of a tile, and four CTAs (a cluster where the logsumexp wants all
 // channels) make the heads.  The weights 2^(m_i - m) l_i / L are the same for all channels: the CTA forms them
-// once, while the first partials' channels are on their way.
+// once, while the first partials' channels are on their way.  Without slices a query has few partials: four at
+// once, which leaves room for three CTAs on an SM (eight and two: paged ragged 128 x 2000 49.9 us, now 47.9).
 constexpr int kMergeThreads = 512;
 template <int kSlices>
 __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_merge(const int2* __restrict__ qpart,
