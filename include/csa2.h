@@ -480,9 +480,12 @@ typedef enum { CSA2_OUT_F32 = 0, CSA2_OUT_BF16 = 1 } csa2_out_type;
  *   out        [B][64][512] of out_type (fp32, or bf16 rounded once), 16-byte aligned
  * Only table elements below ceil(n_entries[b] / seq_stride) are read, and of the last page only the
  * entries that exist.  A page id outside [0, n_pages) is reported as CSA2_ERR_INDEX_RANGE and its
- * entries are skipped.  Probabilities are rounded to f16 for the tensor cores (relative 2^-12), their
- * sum and the logsumexp are kept in fp32.  Every other argument as in csa2_dense_attn_decode; the
- * workspace is csa2_paged_attn_workspace_size(B, n_max, n_swa) bytes. */
+ * entries are skipped.  A NaN in an entry or a window row reaches the queries that see it, no others.
+ * Rounded to f16 (by at most 2^-11): probabilities, for the tensor cores, and the outputs of the parts of
+ * a query, which are joined in fp32; a normalised or rotated q, whose effect on the logsumexp is
+ * corrected to the second order.  Sums and the logsumexp are kept in fp32.  The same call gives the same
+ * bits again.  Every other argument as in csa2_dense_attn_decode; the workspace is
+ * csa2_paged_attn_workspace_size(B, n_max, n_swa) bytes (192 KB a query and 10 MB). */
 csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                    const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3, int32_t n_swa,
                                    const void* q_bf16, float softmax_scale, const csa2_norm_rope* q_nr,
@@ -506,7 +509,10 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  *                n_own_max are left out and reported as CSA2_ERR_INDEX_RANGE (detail n_entries[b]);
  *                n_entries[b] above pages->max_pages * kv->seq_stride counts as that
  * 1 <= G <= B.  Every other argument as in csa2_paged_attn_decode; the workspace is
- * csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa) bytes. */
+ * csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa) bytes: besides what
+ * csa2_paged_attn_decode takes, 1 KB for each shared entry of a group, counted as n_shared_max for
+ * min(G, B / 3) groups and 1 GB at most (groups of three queries or more read them from there;
+ * beyond 2^20 entries, and in smaller groups, they are widened where they are read). */
 csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                     const int32_t* n_entries, int32_t G, const int32_t* group_start,
                                     const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,

@@ -58,7 +58,8 @@ def attention(x, q, scale, sink=None, q_rounded=False, pos=None, base=10000.0):
     """(out, lse, bound) of one query over rows x [n, 512]: float64 q [64, 512] already normalised and
     rotated; `bound` [64, 512] is what the kernel's output may be off before its own rounding.
 
-    Roundings: P to f16, at most 2^-11 of each p (a p below f16's smallest normal loses at most 2^-25
+    Roundings: P to f16, at most 2^-11 of each p, and O / l of each part of the rows to f16, at most 2^-11
+    of sum p |x| over its rows, which with the parts' weights adds up to 2^-11 of the whole (a p below f16's smallest normal loses at most 2^-25
     absolutely against a row's maximum of at least e^-8: below 2^-13 relative to it, and n of them
     n 2^-13 2^-11 at most, kept in the term with max |x|); a logit is off by e_z = scale * sum |q x| *
     (2^-16 for at most 512 fp32 sums of 2^-24 and the staging, + 2^-11 where q was rounded to f16 after
@@ -77,15 +78,19 @@ def attention(x, q, scale, sink=None, q_rounded=False, pos=None, base=10000.0):
     lse = top + np.log(den)
     if not n:
         return o, lse, np.zeros((H, D)), np.full(H, 2.0 ** -20)
-    ez = scale * (np.abs(q) @ np.abs(x).T).max(1) * (2.0 ** -16 + (2.0 ** -11 if q_rounded else 0.0)) + 2.0 ** -20
+    zx = scale * (np.abs(q) @ np.abs(x).T).max(1)
+    ez = zx * (2.0 ** -16 + (2.0 ** -11 if q_rounded else 0.0)) + 2.0 ** -20
     mass = (p / den[:, None]) @ np.abs(x)
-    bound = mass * (2.0 ** -11 + 2 * ez[:, None] + 2.0 ** -14) + n * 2.0 ** -24 * np.abs(x).max()
+    bound = mass * (2.0 ** -11 + 2.0 ** -11 + 2 * ez[:, None] + 2.0 ** -14) + n * 2.0 ** -24 * np.abs(x).max()
     if pos is not None:  # the output turns back: pairs mix
         o = np.concatenate([o[:, :448], rotate(o[:, 448:], -pos, base)], -1)
         pair = bound[:, 448:].reshape(H, 32, 2).sum(-1, keepdims=True)
         bound[:, 448:] = np.broadcast_to(pair, (H, 32, 2)).reshape(H, 64) + 2.0 ** -20 * np.abs(x).max()
-    # the lse: the logits' error, and the sum of probabilities rounded one by one (at most 2^-11)
-    return o, lse, bound, ez + 2.0 ** -11 + 2.0 ** -22 * np.abs(lse)
+    # the lse: the logits' error of the fp32 sums, and the fp32 sum of probabilities (2^-14).  The rounding of q
+    # to f16, by which a logit is off by e at most, is corrected in the first order: left are the square of its
+    # width 2 e over 8, and of the correction e 2^-11 for its f16 terms and e 2^-9 for the output in it
+    e = zx * 2.0 ** -11 if q_rounded else 0.0
+    return o, lse, bound, zx * 2.0 ** -16 + e * e / 2 + e * (2.0 ** -11 + 2.0 ** -9) + 2.0 ** -14 + 2.0 ** -22 * np.abs(lse)
 
 
 class PagedState:
