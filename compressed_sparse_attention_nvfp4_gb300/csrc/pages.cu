@@ -51,9 +51,13 @@ struct PlanView {
   int32_t* need;  // [B + 1]
   int32_t* gone;  // [B + 1]
   PlanState* st;
+  int32_t* ids;   // the first id_cap ids that move, given back ones first, as the checks have read them
+  int id_cap;     // 0: they are read again
 };
 
-__device__ __forceinline__ int pages_of(int n, int P) { return (int)(((long long)n + P - 1) / P); }
+__device__ __forceinline__ int pages_of(int n, int P) {  // n >= 0
+  return n > 0 ? (int)((uint32_t)(n - 1) / (uint32_t)P) + 1 : 0;
+}
 
 // largest i in [lo, hi) with sum[i] <= x (sum ascending, sum[lo] <= x)
 __device__ __forceinline__ int find_le(const int32_t* sum, int lo, int hi, int x) {
@@ -66,15 +70,19 @@ __device__ __forceinline__ int find_le(const int32_t* sum, int lo, int hi, int x
 }
 
 // given back page i
-__device__ __forceinline__ int gone_page(const PageArgs& a, const PlanView& v, int i) {
+__device__ __forceinline__ int find_gone(const PageArgs& a, const PlanView& v, int i) {
   const int b = find_le(v.gone, 0, a.B, i);
   const int first = pages_of(v.have[b], a.P) - (v.gone[b + 1] - v.gone[b]);
   return a.table[(int64_t)b * a.max_pages + first + i - v.gone[b]];
 }
-// taken page i: from the top of the stack, the pages given back by this call included
+__device__ __forceinline__ int gone_page(const PageArgs& a, const PlanView& v, int i) {
+  return i < v.id_cap ? v.ids[i] : find_gone(a, v, i);
+}
+// taken page i: from the top of the stack, on which the pages given back by this call lie
 __device__ __forceinline__ int taken_page(const PageArgs& a, const PlanView& v, int i) {
-  const int at = v.st->n_free + v.st->total_gone - 1 - i;
-  return at >= v.st->n_free ? gone_page(a, v, at - v.st->n_free) : a.free_pages[at];
+  const int gone = v.st->total_gone;
+  if (i < gone) return gone_page(a, v, gone - 1 - i);
+  return i < v.id_cap ? v.ids[i] : a.free_pages[v.st->n_free + gone - 1 - i];
 }
 
 // Exclusive sums over the block of three values a thread, and their totals.  32-bit steps where no value
@@ -183,13 +191,11 @@ __device__ void plan_block(const PageArgs& a, const PlanView& v) {
     bool bad = false;
     int id = 0;
     const int from_stack = (int)min(max(base[1] - base[2], 0LL), (long long)n_free);
-    for (int i = tid; i < from_stack && !bad; i += step) {
-      id = a.free_pages[n_free - 1 - i];
+    const int gone = (int)base[2], moved = gone + from_stack;  // ids, at most n_pages
+    for (int i = tid; i < moved && !bad; i += step) {
+      id = i < gone ? find_gone(a, v, i) : a.free_pages[n_free - 1 - (i - gone)];
       bad = id < 0 || id >= a.n_pages;
-    }
-    for (int i = tid; i < (int)base[2] && !bad; i += step) {
-      id = gone_page(a, v, i);
-      bad = id < 0 || id >= a.n_pages;
+      if (i < v.id_cap) v.ids[i] = id;
     }
     if (bad) report_error(a.ws, CSA2_ERR_INDEX_RANGE, id);
     if (__syncthreads_or(bad) && tid == 0) s_bad = 1;
@@ -218,7 +224,7 @@ __device__ void fill_rows(const PageArgs& a, const PlanView& v, int64_t r, int64
       b = find_le(v.rows, 0, a.B, (int)r);
       const int have = v.have[b];
       const int e = have + (int)r - v.rows[b];
-      const int p = e / a.P, pc = pages_of(have, a.P);
+      const int p = (int)((uint32_t)e / (uint32_t)a.P), pc = pages_of(have, a.P);
       slot = p < pc ? a.table[(int64_t)b * a.max_pages + p] : taken_page(a, v, v.need[b] + p - pc);
       off = e - p * a.P;
       pos = (int64_t)e * a.m;
@@ -241,11 +247,13 @@ __device__ void fill_pages(const PageArgs& a, const PlanView& v, int64_t first, 
   for (int64_t i = first; i < gone; i += step) a.free_pages[v.st->n_free + i] = gone_page(a, v, (int)i);
 }
 
-// Everything in one CTA, the plan in shared memory.
+// Everything in one CTA, the plan and the first kIds ids in shared memory.
+constexpr int kIds = 2048;
 __global__ void __launch_bounds__(kPlanThreads) k_page_tables(PageArgs a) {
   extern __shared__ int32_t smem[];
   __shared__ PlanState st;
-  const PlanView v{smem, smem + a.B, smem + 2 * a.B + 1, smem + 3 * a.B + 2, &st};
+  __shared__ int32_t ids[kIds];
+  const PlanView v{smem, smem + a.B, smem + 2 * a.B + 1, smem + 3 * a.B + 2, &st, ids, kIds};
   ptx::griddep_wait();
   plan_block(a, v);
   fill_pages(a, v, threadIdx.x, blockDim.x);
@@ -283,6 +291,8 @@ PlanView plan_view(void* ws, int32_t B, size_t* bytes) {
   v.rows = take(((size_t)B + 1) * 4);
   v.need = take(((size_t)B + 1) * 4);
   v.gone = take(((size_t)B + 1) * 4);
+  v.ids = nullptr;
+  v.id_cap = 0;
   if (bytes) *bytes = off;
   return v;
 }
