@@ -48,20 +48,20 @@ constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
 // up to vis by each, then each query's own entries ns .. ns + own - 1 and its window.
 struct Pair {
-  int32_t q0, q1;
+  int32_t q0, own0;
+  int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
+  int32_t q1, own1;
   int32_t first;  // the query whose table row holds the shared entries
   int32_t ns;
   int32_t vis0, vis1;
-  int32_t own0, own1;
   int32_t paired;  // own chunks that hold 64 rows of each query; behind them 128 of the longer one's
-  int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
   int32_t nshared; // shared chunks; own chunks follow
   int32_t image;   // the shared entries' first chunk in the image, or -1
 };
 
 // What one part (a CTA, or a pair of CTAs) of the attention launch runs: chunks [t0, t1) of the order of all
 // pairs' chunks, beginning in `pair`, number p, whose chunks end at `end`.  The first item needs no further
-// load.
+// load, and a query by itself no more than the first 32 bytes.
 struct __align__(16) Part {
   int32_t p, t0, t1, end;
   Pair pair;
@@ -291,7 +291,7 @@ struct __align__(1024) PrefixSmem {
   uint16_t xs[kDMain / 8][kOwnChunk * 8];   // this CTA's 64 rows for S [c/8][row][c%8]
   uint16_t xo[4][kDMain / 16][32 * 8];      // this CTA's 256 channels of all 128 rows [row/32][c/8][row%32][c%8]
   uint16_t p[2][kChunk / 8][kHAtt * 8];     // probabilities [row/8][head][row%8]
-  float red[2][kHAtt];
+  float red[2][kHAtt];                      // of the two threads of a head; at the end their sums of p
   int32_t rows[4][kChunk];                  // where a chunk's rows come from, up to four chunks ahead
   int32_t image[4];                         // its chunk of the image, or -1
   // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
@@ -302,6 +302,8 @@ struct __align__(1024) PrefixSmem {
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_read;                          // epilogue done with O
   uint64_t drained;                         // every MMA issued complete (two warps)
+  uint64_t last_o;                          // the last item's O complete, its sums in red (four softmax warps)
+  int32_t last_slot;                        // its partial, or -1
   Part part;
   uint32_t tmem_base;
   int abort_flag;
@@ -618,6 +620,27 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
   return good;
 }
 
+// Columns 32 c0 .. 32 c1 of O / l of thread t's accumulator row, in f16: at most the largest |x| (2,688), and a
+// rounding of 2^-11 at most, a quarter of that of a bf16 output; the partials are most of what a short call moves.
+__device__ __forceinline__ void store_pair_o(const PrefixKernel& k, uint32_t tmem, int64_t slot, int t, float l, int c0,
+                                             int c1) {
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint4* po = k.part_o + slot * 32 * 128 + t;
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    uint32_t a[32];
+    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(t & ~31) << 16) + 32u * (uint32_t)c, a);
+    ptx::tmem_wait_ld();
+    auto pk = [&](int u) {
+      const __half2 v = __floats2half2_rn(__uint_as_float(a[2 * u]) * inv, __uint_as_float(a[2 * u + 1]) * inv);
+      return *reinterpret_cast<const uint32_t*>(&v);
+    };
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      po[(c * 4 + u) * 128] = make_uint4(pk(4 * u), pk(4 * u + 1), pk(4 * u + 2), pk(4 * u + 3));
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k,
                                                                   const __grid_constant__ ImageMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -647,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         ptx::mbar_init(&S.p_free[i], 1);
       }
       ptx::mbar_init(&S.o_read, 4 + peer);
+      ptx::mbar_init(&S.last_o, 4);
       ptx::mbar_init(&S.drained, 2);
       S.abort_flag = 0;
       ptx::fence_mbar_init();
@@ -693,6 +717,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   if (warp >= kRowWarp && warp < kSMma) {
     ptx::setmaxnreg_dec<kRowRegs>();
     good = rows_role(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
+    // the last item's partial is theirs, a quarter of the columns each four: nothing else is left to do
+    if (good && t1 > t0) good = wait(&S.last_o, 0);
+    if (good && t1 > t0 && S.last_slot >= 0) {
+      ptx::tc_fence_after();
+      const int quarter = (warp - kRowWarp) / 4, t = 32 * (warp % 4) + lane;
+      store_pair_o(k, tmem, S.last_slot, t, S.red[0][t & 63] + S.red[1][t & 63], 2 * quarter, 2 * quarter + 2);
+      ptx::tc_fence_before();
+    }
     where = 31;
   } else if (warp >= kSMma) {
     // the odd CTA's MMA warps pass their CTA's arrivals on, in the order the even CTA's wait for them
@@ -793,7 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     ptx::setmaxnreg_inc<kSoftRegs>();
     const int h = tid & 63, half = tid >> 6;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t items) {
+    for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t) {
+      const bool ends = (int)n + nc == t1 - t0;  // the last item
       const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
       float m2 = -INFINITY, lsum = 0.0f;
       const float c2 = k.c2[(int64_t)(qme >= 0 ? qme : k.B) * kHAtt + h];
@@ -891,27 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       ptx::tc_fence_after();
       const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
       S.red[half][h] = lsum;
+      if (ends && tid == 0) S.last_slot = qme >= 0 ? (int)slot : -1;
       softmax_sync();
       const float l = S.red[0][h] + S.red[1][h];
-      softmax_sync();
+      if (ends) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.last_o);
+      } else {
+        softmax_sync();
+      }
       if (qme >= 0) {
-        // O / l in f16: at most the largest |x| (2,688), and a rounding of 2^-11 at most, a quarter of that
-        // of a bf16 output; the partials are most of what a short call moves
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        uint4* po = k.part_o + slot * 32 * 128 + tid;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t a[32];
-          ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
-          ptx::tmem_wait_ld();
-          auto pk = [&](int u) {
-            const __half2 v = __floats2half2_rn(__uint_as_float(a[2 * u]) * inv, __uint_as_float(a[2 * u + 1]) * inv);
-            return *reinterpret_cast<const uint32_t*>(&v);
-          };
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            po[(c * 4 + u) * 128] = make_uint4(pk(4 * u), pk(4 * u + 1), pk(4 * u + 2), pk(4 * u + 3));
-        }
+        if (!ends) store_pair_o(k, tmem, slot, tid, l, 0, 8);
         if (half == 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, l);
       }
       ptx::tc_fence_before();
@@ -1297,6 +1321,8 @@ struct __align__(1024) AloneSmem {
   uint16_t q[kDMain / 8][kQPlane];       // q' [c/8][head][c%8]
   uint16_t p[2][kRows / 8][kHAtt * 8];   // probabilities [row/8][head][row%8]
   float alpha[kHAtt];                    // factor of O when a head's reference moved; at the end 1 / l
+  int32_t last_slot;                     // the last item's partial
+  uint64_t last_o;                       // its O complete, 1 / l in alpha (four softmax warps)
   int32_t rows[kRing][kRows];
   uint64_t q_land;
   uint64_t r_full[kRing], r_free[kRing];
@@ -1357,6 +1383,31 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
   return good;
 }
 
+// Tiles' columns 32 c0 .. 32 c1 of O^T / l in f16, thread t's channels; uint4 (c, u) of thread t holds heads
+// 32 (c % 2) + 8 u .. of channel 128 (c / 2) + t, so that every store is 512 contiguous bytes.
+__device__ __forceinline__ void store_alone_o(const AloneSmem& S, const PrefixKernel& k, uint32_t tmem, int64_t slot, int t,
+                                              int c0, int c1) {
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    uint32_t a[32];
+    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(t & ~31) << 16) + 32u * (uint32_t)c, a);
+    ptx::tmem_wait_ld();
+    uint4* po = k.part_o + (slot * 32 + 4 * c) * 128 + t;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t w[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float2 i2 = *reinterpret_cast<const float2*>(&S.alpha[32 * (c & 1) + 8 * u + 2 * v]);
+        const __half2 hh = __floats2half2_rn(__uint_as_float(a[8 * u + 2 * v]) * i2.x,
+                                             __uint_as_float(a[8 * u + 2 * v + 1]) * i2.y);
+        w[v] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      po[u * 128] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ PrefixKernel k) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   AloneSmem& S = *reinterpret_cast<AloneSmem*>(smem_raw);
@@ -1380,6 +1431,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         ptx::mbar_init(&S.p_full[i], 4);
       }
       ptx::mbar_init(&S.o_read, 4);
+      ptx::mbar_init(&S.last_o, 4);
       ptx::mbar_init(&S.drained, 2);
       S.abort_flag = 0;
       ptx::fence_mbar_init();
@@ -1417,6 +1469,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 
   if (warp >= 4 && warp < kAloneS) {
     good = alone_rows(S, k, t1 - t0, warp - 4, lane);
+    if (good && t1 > t0) {  // as in k_prefix_attn
+      good = wait(&S.last_o, 0);
+      if (good) {
+        ptx::tc_fence_after();
+        const int quarter = (warp - 4) / 4;
+        store_alone_o(S, k, tmem, S.last_slot, 32 * (warp % 4) + lane, 2 * quarter, 2 * quarter + 2);
+        ptx::tc_fence_before();
+      }
+    }
     where = 41;
   } else if (warp >= kAloneS) {
     if (warp == kAloneIndex) {
@@ -1584,8 +1645,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         }
         lsum = fmaf(alpha, lsum, sum);
       }
-      // ---- this item's partial: O^T / l in f16; uint4 (c, u) of thread t holds heads 32 (c % 2) + 8 u .. of
-      // channel 128 (c / 2) + t, so that every store is 512 contiguous bytes
+      // ---- this item's partial, the last item's left to the row warps
       const uint32_t last = n + (uint32_t)nc - 1;
       good = good && wait(&S.x_free[last & 1u][0], last >> 1) && wait(&S.x_free[last & 1u][1], last >> 1);
       good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // the four warps leave together, or none
@@ -1597,26 +1657,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         S.alpha[h] = lsum > 0.0f ? 1.0f / lsum : 0.0f;
         k.part_ml[slot * kHAtt + h] = make_float2(m2, lsum);
       }
-      softmax_sync();
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t a[32];
-        ptx::tmem_ld_32x32b_x32(tmem + lane_base + 32u * (uint32_t)c, a);
-        ptx::tmem_wait_ld();
-        uint4* po = k.part_o + (slot * 32 + 4 * c) * 128 + tid;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float2 i2 = *reinterpret_cast<const float2*>(&S.alpha[32 * (c & 1) + 8 * u + 2 * v]);
-            const __half2 hh = __floats2half2_rn(__uint_as_float(a[8 * u + 2 * v]) * i2.x,
-                                                 __uint_as_float(a[8 * u + 2 * v + 1]) * i2.y);
-            w[v] = *reinterpret_cast<const uint32_t*>(&hh);
-          }
-          po[u * 128] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+      if ((int)n + nc == t1 - t0) {  // the last item
+        if (tid == 0) S.last_slot = (int)slot;
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.last_o);
+        return;
       }
+      softmax_sync();
+      store_alone_o(S, k, tmem, slot, tid, 0, 8);
       softmax_sync();  // alpha is written again
       ptx::tc_fence_before();
       __syncwarp();
