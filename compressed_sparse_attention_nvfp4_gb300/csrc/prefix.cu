@@ -948,8 +948,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     *abort_flag = 1;
     report_error(k.ws, CSA2_ERR_DEVICE_TIMEOUT, where);
   }
-  if (rank == 0 && (warp == kSMma || warp == kOMma)) {  // every MMA has completed before tensor memory is freed
-    ptx::mma_commit_pair_elect(&S.drained);
+  if (warp == kSMma || warp == kOMma) {  // every MMA has completed, for both, before tensor memory is freed
+    if (rank == 0) ptx::mma_commit_pair_elect(&S.drained);
     volatile int keep_waiting = 0;
     ptx::mbar_wait_warp(&S.drained, 0, &keep_waiting, kWaitBudget);
   }
