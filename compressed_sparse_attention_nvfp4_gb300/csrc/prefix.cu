@@ -94,6 +94,7 @@ struct PrefixArgs {
   int2* qpart;        // [B] first partial (see the merges), partials
   Part* parts_of;     // [parts]
   int32_t* gimage;    // [G] first image chunk of each group, or -1
+  int2* gshared;      // [G] see shared_of (where shared memory is too small)
   int64_t image_cap;  // chunks the image has room for
   int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
   void* ws;
@@ -130,15 +131,20 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
 __device__ __forceinline__ int visible(const PrefixArgs& a, int q) {
   return (int)min((long long)max(a.n_entries[q], 0), (long long)a.table_cap);
 }
-// a group's shared entries; those beyond its first query's own count are read as each query's own
-__device__ __forceinline__ int shared_of(const PrefixArgs& a, int g, int first) {
-  return min(min(max(a.n_shared[g], 0), a.shared_max), visible(a, first));
+// A group's shared entries: the query whose table row holds them (the first that is long enough, else the
+// longest) and their number.
+__device__ __forceinline__ int2 shared_of(const PrefixArgs& a, int g, int first, int end) {
+  const int want = min(max(a.n_shared[g], 0), a.shared_max);
+  int2 best = make_int2(first, visible(a, first));
+  for (int q = first + 1; q < end && best.y < want; ++q) {
+    const int n = visible(a, q);
+    if (n > best.y) best = make_int2(q, n);
+  }
+  return make_int2(best.x, min(best.y, want));
 }
-// chunks that group g's image takes, if there is room
-__device__ __forceinline__ int image_chunks(const PrefixArgs& a, int g) {
-  const int first = a.group_start[g], end = a.group_start[g + 1];
-  if (first < 0 || end > a.B || end - first < kImageQueries) return 0;
-  return (shared_of(a, g, first) + kChunk - 1) / kChunk;
+// chunks that the image of a group of n queries takes, if there is room
+__device__ __forceinline__ int image_chunks(int n, int ns) {
+  return n < kImageQueries ? 0 : (ns + kChunk - 1) / kChunk;
 }
 
 template <bool kAloneQueries>
@@ -151,18 +157,21 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
     *reinterpret_cast<ErrWord*>(a.ws) = ErrWord{0, 0, 0};  // no other CTA of the launch reports
   }
   __syncthreads();
+  // the lists that are searched, in shared memory where they fit: a search is a chain of dependent loads
+  int2* const gshared = a.G <= smem_ints / 8 ? reinterpret_cast<int2*>(smem + smem_ints / 4) : a.gshared;
   for (int g = tid; g < a.G; g += kPrepThreads) {
     const int lo = a.group_start[g], hi = a.group_start[g + 1];
     if (lo < 0 || hi < lo || hi > a.B) {
       s_bad = 1;
       report_error(a.ws, CSA2_ERR_INDEX_RANGE, g);
+    } else if (lo < hi) {
+      gshared[g] = shared_of(a, g, lo, hi);
     }
   }
   __syncthreads();
   const int G = s_bad ? 0 : a.G;
   const int R = G + 2;  // ranges; without groups the first is empty
-  // the lists that are searched, in shared memory where they fit: a search is a chain of dependent loads
-  int32_t* const gpair = R + 1 <= smem_ints / 2 ? smem : a.gpair;
+  int32_t* const gpair = R + 1 <= smem_ints / 4 ? smem : a.gpair;
   int32_t* const chunk0 = max_pairs(a.B, a.G) + 1 <= smem_ints / 2 ? smem + smem_ints / 2 : a.chunk0;
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
@@ -180,7 +189,8 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   // a group whose image would end beyond the room has none, and so do all behind it
   int images = 0;
   for (int g0 = 0; g0 < G; g0 += kPrepThreads) {
-    const int g = g0 + tid, n = g < G ? image_chunks(a, g) : 0;
+    const int g = g0 + tid, size = g < G ? a.group_start[g + 1] - a.group_start[g] : 0;
+    const int n = size > 0 ? image_chunks(size, gshared[g].y) : 0;
     int total;
     const int at = images + block_scan(n, s_warp, &total);
     if (g < G) a.gimage[g] = n > 0 && at + (int64_t)n <= a.image_cap ? at : -1;
@@ -210,7 +220,8 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
       x.first = first;
       x.image = -1;
       if (lo >= 1 && lo <= G) {
-        x.ns = shared_of(a, lo - 1, first);
+        x.first = gshared[lo - 1].x;
+        x.ns = gshared[lo - 1].y;
         x.image = a.gimage[lo - 1];
       }
 #pragma unroll
@@ -1063,27 +1074,36 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
 __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
                                              int step) {
   __shared__ int s_warp[kPrepThreads / 32];
-  __shared__ int s_group, s_at;
+  __shared__ int2 s_found;  // the row's query (-1: no such group) and the shared entries
+  __shared__ int s_at;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = rotated(lane) & 7;
   for (int64_t t = first_chunk;; t += step) {
     // the group whose image holds chunk t
-    if (threadIdx.x == 0) s_group = -1;
+    if (threadIdx.x == 0) s_found.x = -1;
     __syncthreads();
     int base = 0;
     for (int g0 = 0; g0 < a.G && base <= t; g0 += kPrepThreads) {
-      const int g = g0 + threadIdx.x, n = g < a.G ? image_chunks(a, g) : 0;
+      const int g = g0 + threadIdx.x;
+      int2 sh = make_int2(0, 0);
+      int n = 0;
+      if (g < a.G) {
+        const int lo = a.group_start[g], hi = a.group_start[g + 1];
+        if (lo >= 0 && hi <= a.B && hi - lo >= kImageQueries) {
+          sh = shared_of(a, g, lo, hi);
+          n = image_chunks(hi - lo, sh.y);
+        }
+      }
       int total;
       const int at = base + block_scan(n, s_warp, &total);
       if (n > 0 && at + (int64_t)n <= a.image_cap && t >= at && t < at + n) {
-        s_group = g;
+        s_found = sh;
         s_at = at;
       }
       base += total;
     }
     __syncthreads();
-    const int g = s_group;
-    if (g < 0) return;
-    const int first = a.group_start[g], ns = shared_of(a, g, first);
+    const int first = s_found.x, ns = s_found.y;
+    if (first < 0) return;
     const int row = 8 * warp + (lane & 7), e = (int)(t - s_at) * kChunk + row;
     int r = kNoRow;
     if (e < ns) {
@@ -1097,7 +1117,7 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       put(f[i], r, dst + (b0 ^ (4 * i)) * 4 * kChunk * 8, kChunk * 8);
-    __syncthreads();  // s_group is written again
+    __syncthreads();  // s_found is written again
   }
 }
 
@@ -1311,7 +1331,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
 // Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 64 KB of rows and 8 KB of P
 // written, 296 KB = 2,300 cycles at 128 bytes a cycle; the MMAs alone (S at the half rate of M = 64) take
 // 1,800; measured, about 2,800, the wait of a slot for its softmax among them.  48 queries of up to 65,536 entries
-// take 219 us (0.79 PFLOP/s, 1.8 TB/s of entries), one of 4,096 entries 17 us.
+// take 219 us (0.79 PFLOP/s, 1.8 TB/s of entries), one of 4,096 entries 16 us.
 constexpr int kAlone = 152;
 constexpr int kRows = 64;  // rows of a chunk
 constexpr int kRing = 8;   // chunks whose rows are found ahead
@@ -1828,7 +1848,7 @@ struct PrefixWs {
   Pair* pairs;
   int32_t *gpair, *chunk0, *gimage;
   Part* parts;
-  int2* qpart;
+  int2 *qpart, *gshared;
   uint16_t *image, *qimage, *rest;
   float* c2;
   float2* turn;
@@ -1856,6 +1876,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.qpart = (int2*)take((size_t)B * 8);
   L.parts = (Part*)take(parts * sizeof(Part));
   L.gimage = (int32_t*)take((size_t)G * 4);
+  L.gshared = (int2*)take((size_t)G * 8);
   L.qimage = (uint16_t*)take(((size_t)B + 1) * kHAtt * kDMain * 2);
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
   L.rest = (uint16_t*)take((size_t)B * kHAtt * kDMain * 2);
@@ -1945,7 +1966,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   cudaStream_t st = (cudaStream_t)stream;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.image_cap, G > 0 ? kClusters : kAlone, ws};
+                     L.gimage, L.gshared, L.image_cap, G > 0 ? kClusters : kAlone, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,

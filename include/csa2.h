@@ -496,8 +496,9 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
 /* csa2_paged_attn_decode for a batch whose queries share prefixes (one system prompt, one document,
  * samples drawn in parallel): group g is the queries [group_start[g], group_start[g + 1]), whose
  * sequences agree on their first n_shared[g] entries.  Those are read once for the group, through the
- * table row of its first query; entries from n_shared[g] on, and the window, are each query's own,
- * through its own row.  The result is that of csa2_paged_attn_decode.
+ * table row of its first query that has them all (or of the longest, when none has); entries from
+ * n_shared[g] on, and the window, are each query's own, through its own row.  The result is that of
+ * csa2_paged_attn_decode.
  *   group_start  [G + 1] int32 (device), ascending within [0, B]; queries outside every group share
  *                nothing.  A group that is not ascending, or leaves [0, B], counts as empty and is
  *                reported as CSA2_ERR_INDEX_RANGE

@@ -31,9 +31,10 @@ class Batch:
         self.max_pages = max(1, max(-(-x // P) for x in n))
         first, whole, part = list(range(B)), [0] * B, [0] * B
         for g, (a, z) in enumerate(groups):
+            long = next((b for b in range(a, z) if n[b] >= shared[g]), max(range(a, z), key=lambda b: n[b]))
             for b in range(a, z):
-                first[b] = a
-                agree = min(shared[g], n[a], n[b])
+                first[b] = long
+                agree = min(shared[g], n[long], n[b])
                 whole[b], part[b] = agree // P, agree % P
         count = sum(-(-n[b] // P) - (whole[b] if first[b] != b else 0) for b in range(B)) + spare
         ids = rng.permutation(count).astype(np.int32)
@@ -43,8 +44,8 @@ class Batch:
         # garbage behind the last page of a sequence is not read
         table = np.full((B, self.max_pages), 0x7fffffff, np.int32)
         at = 0
-        self.rows = []
-        for b in range(B):
+        self.rows = [None] * B
+        for b in sorted(range(B), key=lambda b: first[b] != b):
             np_b, skip = -(-n[b] // P), whole[b] if first[b] != b else 0
             table[b, :skip] = table[first[b], :skip]
             table[b, skip:np_b] = ids[at:at + np_b - skip]
@@ -54,8 +55,8 @@ class Batch:
                 self.codes[d:d + part[b]], self.scales[d:d + part[b]] = (self.codes[s:s + part[b]],
                                                                         self.scales[s:s + part[b]])
             j = np.arange(n[b])
-            self.rows.append(table[b, j // P].astype(np.int64) * P + j % P if n[b] else np.zeros(0, np.int64))
-            seen[self.rows[-1]] = True
+            self.rows[b] = table[b, j // P].astype(np.int64) * P + j % P if n[b] else np.zeros(0, np.int64)
+            seen[self.rows[b]] = True
         self.scales[~seen] = 0x7F
         self.table = table
         self.q = bf16(rng.standard_normal((B, H, D))) if q is None else q
@@ -245,6 +246,48 @@ def test_prefix_groups(n, groups, shared, P):
     out, lse, ws = b.prefix()
     assert csa2.check(ws)[0] == 0
     close(out, lse, b.reference())
+
+
+@pytest.mark.parametrize("n,groups,shared,own_max", [
+    ([100, 300, 310, 40], [(0, 4)], [280], 30),   # the first query sees a part only: others' rows hold the rest
+    ([50, 300], [(0, 2)], [280], 20),
+    ([0, 0, 300, 290, 0], [(0, 5)], [280], 20),
+    ([100, 200, 150], [(0, 3)], [280], 0),        # none has them all
+    ([0, 0, 0], [(0, 3)], [280], 0),
+])
+def test_prefix_longer_than_the_first_query(n, groups, shared, own_max):
+    b = Batch(40, n, 16, groups, shared, n_swa=5).device()
+    out, lse, ws = b.prefix(own_max=own_max, shared_max=min(280, 16 * b.max_pages))  # the tables' rows end there
+    assert csa2.check(ws)[0] == 0
+    close(out, lse, b.reference())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_one_head_of_a_query_not_finite(value):
+    b = Batch(41, [300, 310, 320], 16, [(0, 3)], [256], n_swa=16)
+    want = b.reference()
+    b.q[1, 7, 3] = value
+    b.device()
+    for out, lse, ws in (b.prefix(), b.paged()):
+        assert csa2.check(ws)[0] == 0
+        assert torch.isnan(out[1, 7]).all()
+        out[1, 7] = torch.from_numpy(want[0][1, 7]).float().cuda()
+        lse[1, 7] = float(want[1][1, 7])
+        close(out, lse, want)
+
+
+@pytest.mark.parametrize("B", [3, 20])
+def test_without_lse_the_same_output(B):
+    b = Batch(42, [300 + i for i in range(B)], 16, [(0, B)], [290], n_swa=16, extras=True, sink=True).device()
+    ws = csa2.workspace(max(csa2.prefix_attn_workspace_size(B, 1, 290, 300, 16), csa2.paged_attn_workspace_size(B, 400, 16)))
+    keep = to_dev(np.array([0, B], np.int32)), to_dev(np.array([290], np.int32))
+    out = torch.empty((B, H, D), dtype=torch.bfloat16, device="cuda")
+    one = b.prefix(torch.bfloat16)
+    csa2.prefix_attn_decode(b.planes, b.pages, B, b.dn, 1, *keep, 290, 300, b.dswa, 16, b.dq, SCALE, out, ws, **b.kw)
+    assert csa2.check(ws)[0] == 0 and torch.equal(out, one[0])
+    one = b.paged(torch.bfloat16)
+    csa2.paged_attn_decode(b.planes, b.pages, B, b.dn, 299 + B, b.dswa, 16, b.dq, SCALE, out, ws, **b.kw)
+    assert csa2.check(ws)[0] == 0 and torch.equal(out, one[0])
 
 
 @pytest.mark.parametrize("extras,sink", [(False, False), (True, False), (False, True), (True, True)])

@@ -73,6 +73,7 @@ def fresh(rng, B, P, max_pages, spare, have_max):
     (33, 16, 200, 20, 0, 4, True), (1025, 8, 40, 9, 3, 1, True), (2048, 3, 9, 3, 1, 1, True),
     (2049, 5, 9, 3, 4, 1, True),          # beyond one CTA's requests
     (7, 64, 1000, 4000, 9, 128, True),    # beyond one CTA's rows
+    (300, 1, 40, 40, 0, 1, True),         # thousands of pages change hands in one CTA
     (65535, 16, 40, 2, 0, 1, True)])
 def test_tables_match_the_model(B, P, have, new, pad, m, drops):
     rng = np.random.default_rng(B * 131 + P)
@@ -179,10 +180,11 @@ def test_no_pages_detail_and_pages_handed_on():
     assert sorted(s.table[1][1:3] + s.table[2][1:2]) == [4, 5, 6] and s.n_free == 0
 
 
-def test_steps_in_place_from_a_graph_on_another_stream():
+@pytest.mark.parametrize("B", [40, 2100])
+def test_steps_in_place_from_a_graph_on_another_stream(B):
     rng = np.random.default_rng(11)
-    B, P = 40, 16
-    s = fresh(rng, B, P, 20, 200, 100)
+    P = 16
+    s = fresh(rng, B, P, 20, 5 * B, 100)  # 38 entries more need three pages each at most
     d = Device(s, B)
     add, kept = [1] * B, [0] * B
     new = i32(add)
