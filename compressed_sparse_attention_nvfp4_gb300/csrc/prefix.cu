@@ -836,8 +836,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     ptx::setmaxnreg_inc<kSoftRegs>();
     const int h = tid & 63, half = tid >> 6;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    // An item's partial (reference, sum, O) is written when the next one's first P is on its way, so that the
+    // MMAs of both run on meanwhile; the last item's by the row warps.
+    bool open = false;
+    uint32_t open_last = 0;  // its last chunk
+    int open_slot = 0;       // its partial's slot, or -1 - slot without a query
+    float open_m = 0.0f, open_l = 0.0f;
+    auto finish = [&](bool ends) {
+      good = wait(&S.p_free[open_last & 1u], open_last >> 1);
+      // the four warps leave together, or none
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
+      if (!good) return;
+      ptx::tc_fence_after();
+      S.red[half][h] = open_l;
+      if (ends && tid == 0) S.last_slot = open_slot;
+      softmax_sync();
+      const float l = S.red[0][h] + S.red[1][h];
+      if (ends) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.last_o);
+      } else {
+        softmax_sync();
+      }
+      if (open_slot >= 0) {
+        if (!ends) store_pair_o(k, tmem, open_slot, tid, l, 0, 8);
+        if (half == 0) k.part_ml[(int64_t)open_slot * kHAtt + h] = make_float2(open_m, l);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+    };
     for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t) {
-      const bool ends = (int)n + nc == t1 - t0;  // the last item
       const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
       float m2 = -INFINITY, lsum = 0.0f;
       const float c2 = k.c2[(int64_t)(qme >= 0 ? qme : k.B) * kHAtt + h];
@@ -925,34 +955,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
           if (lane == 0) ptx::mbar_arrive(&S.p_full[slot]);
         }
         lsum = fmaf(alpha, lsum, sum);
+        if (j == 0 && open) {
+          finish(false);
+          if (!good) break;
+        }
       }
-      // ---- this item's partial: reference, sum, O
-      const uint32_t last = n + (uint32_t)nc - 1;
-      good = good && wait(&S.p_free[last & 1u], last >> 1);
-      // the four warps leave together, or none
-      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
-      if (!good) return;
-      ptx::tc_fence_after();
-      const int64_t slot = (int64_t)(p + cluster) * 2 + rank;
-      S.red[half][h] = lsum;
-      if (ends && tid == 0) S.last_slot = qme >= 0 ? (int)slot : -1;
-      softmax_sync();
-      const float l = S.red[0][h] + S.red[1][h];
-      if (ends) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&S.last_o);
-      } else {
-        softmax_sync();
-      }
-      if (qme >= 0) {
-        if (!ends) store_pair_o(k, tmem, slot, tid, l, 0, 8);
-        if (half == 0) k.part_ml[slot * kHAtt + h] = make_float2(m2, l);
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // together, or none
+      open = true;
+      open_last = n + (uint32_t)nc - 1;
+      open_slot = (p + cluster) * 2 + rank;
+      if (qme < 0) open_slot = -1 - open_slot;
+      open_m = m2;
+      open_l = lsum;
     });
+    if (open && good) finish(true);
     where = 35;
   }
   if (!good && lane == 0 && !*abort_flag) {
@@ -1588,9 +1604,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   } else {
     // ---- softmax: lane l of warp w head 16 w + l % 16, chunk rows 32 (l / 16) .. (the rows of an M = 64
     // accumulator lie in lanes 0-15 of each quarter; two lanes share a head's columns)
-    ptx::setmaxnreg_dec<72>();
     const int rh = lane >> 4, h = 16 * warp + (lane & 15);
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    bool open = false;  // as in k_prefix_attn
+    uint32_t open_last = 0;
+    int open_slot = 0;
+    float open_m = 0.0f, open_l = 0.0f;
+    auto finish = [&](bool ends) {
+      good = wait(&S.x_free[open_last & 1u][0], open_last >> 1) && wait(&S.x_free[open_last & 1u][1], open_last >> 1);
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
+      if (!good) return;
+      ptx::tc_fence_after();
+      open_l += __shfl_xor_sync(0xffffffffu, open_l, 16);
+      if (rh == 0) {
+        S.alpha[h] = open_l > 0.0f ? 1.0f / open_l : 0.0f;
+        k.part_ml[(int64_t)open_slot * kHAtt + h] = make_float2(open_m, open_l);
+      }
+      if (ends) {
+        if (tid == 0) S.last_slot = open_slot;
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.last_o);
+        return;
+      }
+      softmax_sync();
+      store_alone_o(S, k, tmem, open_slot, tid, 0, 8);
+      softmax_sync();  // alpha is written again
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+    };
     for_items([&](int q, int, int p, int, int nc, uint32_t n, uint32_t) {
       const float c2 = k.c2[(int64_t)q * kHAtt + h];
       float m2 = -INFINITY, lsum = 0.0f;
@@ -1664,33 +1707,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           if (lane == 0) ptx::mbar_arrive(&S.p_full[slot]);
         }
         lsum = fmaf(alpha, lsum, sum);
+        if (j == 0 && open) {
+          finish(false);
+          if (!good) break;
+        }
       }
-      // ---- this item's partial, the last item's left to the row warps
-      const uint32_t last = n + (uint32_t)nc - 1;
-      good = good && wait(&S.x_free[last & 1u][0], last >> 1) && wait(&S.x_free[last & 1u][1], last >> 1);
-      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // the four warps leave together, or none
-      if (!good) return;
-      ptx::tc_fence_after();
-      const int64_t slot = p + cta;
-      lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-      if (rh == 0) {
-        S.alpha[h] = lsum > 0.0f ? 1.0f / lsum : 0.0f;
-        k.part_ml[slot * kHAtt + h] = make_float2(m2, lsum);
-      }
-      if ((int)n + nc == t1 - t0) {  // the last item
-        if (tid == 0) S.last_slot = (int)slot;
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&S.last_o);
-        return;
-      }
-      softmax_sync();
-      store_alone_o(S, k, tmem, slot, tid, 0, 8);
-      softmax_sync();  // alpha is written again
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&S.o_read);
+      good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;
+      open = true;
+      open_last = n + (uint32_t)nc - 1;
+      open_slot = p + cta;
+      open_m = m2;
+      open_l = lsum;
     });
+    if (open && good) finish(true);
     where = 45;
   }
   if (!good && lane == 0 && !*abort_flag) {

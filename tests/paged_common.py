@@ -64,7 +64,8 @@ def attention(x, q, scale, sink=None, q_rounded=False, pos=None, base=10000.0):
     n 2^-13 2^-11 at most, kept in the term with max |x|); a logit is off by e_z = scale * sum |q x| *
     (2^-16 for at most 512 fp32 sums of 2^-24 and the staging, + 2^-11 where q was rounded to f16 after
     its normalisation or rotation), which moves every p by at most e_z relatively, and the denominator
-    too; the fp32 sums of p x and of p add 2^-14 (n <= 1024 additions of 2^-24)."""
+    too; the fp32 sums of p x and of p add 2^-14 (chains of at most 1024 additions of 2^-24: one for 16 rows
+    of a part, then the parts)."""
     n = x.shape[0]
     z = scale * (q @ x.T) if n else np.zeros((H, 0))
     top = z.max(1) if n else np.full(H, -np.inf)

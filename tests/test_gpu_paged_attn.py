@@ -671,3 +671,11 @@ def test_whole_run_tables_append_window_attention(oracle_mod):
             x = np.concatenate([decode(codes[r], scales[r]), F8[swa[b][rp[b] >= 0]]])
             ref.append(attention(x, q[b].double().numpy(), SCALE))
         close(out, lse, tuple(np.stack(z) for z in zip(*ref)))
+
+
+def test_more_entries_than_either_bound():
+    # shared and own entries together reach beyond 65,536, in pages of an odd size
+    b = Batch(43, [100_003, 65_537], 97, [(0, 2)], [65_500]).device()
+    out, lse, ws = b.prefix(own_max=34_600)
+    assert csa2.check(ws)[0] == 0
+    close(out, lse, b.reference())
