@@ -1548,6 +1548,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j, slot = m % kRing;
           const int r0 = resolve(k, r[0], true), r1 = resolve(k, r[1], true);
+          prefetch_row(k, r0);  // paged ragged 48 x 65536: 219 us without, 217 with
+          prefetch_row(k, r1);
           if (j + 1 < nc) find(j + 1);
           if (m >= kRing) good = wait(&S.r_free[slot], m / kRing - 1);
           if (!good) break;
