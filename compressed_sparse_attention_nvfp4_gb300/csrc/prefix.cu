@@ -5,7 +5,7 @@
 // O / l = sum 2^(z - m) x / l; parts join by log-sum-exp.  Each call is three launches:
 //   k_prefix_prep   the plan (which chunks of rows every CTA runs), the queries' f16 images, and the image:
 //                   the shared entries of groups of kImageQueries or more queries, widened to f16 once;
-//   k_paged_attn    one query to a CTA (G = 0), or
+//   k_paged_attn    one query to a CTA (without groups, or with small ones), or
 //   k_prefix_attn   two queries of a group to a pair of CTAs;
 //   k_paged_merge / k_prefix_merge   the join, the sink, the turn back, the output's type.
 // All chunks form one list that the CTAs share evenly, whatever the queries' lengths; a query cut between
@@ -40,7 +40,11 @@ constexpr int kPrepThreads = 512;
 constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of the 152 SMs
 constexpr int kChunk = 128;      // rows of a chunk
 constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
-constexpr int kImageQueries = 3;   // a group of at least this many queries has its shared entries widened once
+// A group of at least this many queries has its shared entries widened once, and groups smaller than this on
+// average run every query by itself.  64 queries on 8,192 entries, groups of four: 106 us with the image, 93
+// without; of eight: 86 and 90.  In pairs / by themselves: groups of one 160 / 98 us, two 93 / 98, three
+// 124 / 98, four 93 / 98, sixteen 76 / 98 (an odd group's last query takes a pair's time).
+constexpr int kImageQueries = 5;
 constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM,
 constexpr int kWidenFirst = 152;   // of which these come before the queries' staging
 constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
@@ -96,12 +100,14 @@ struct PrefixArgs {
   int32_t* gimage;    // [G] first image chunk of each group, or -1
   int2* gshared;      // [G] see shared_of (where shared memory is too small)
   int64_t image_cap;  // chunks the image has room for
-  int32_t parts;      // CTAs (G = 0: one query each) or pairs of CTAs that share the chunks
+  int32_t parts;      // CTAs (one query each) or pairs of CTAs that share the chunks
   void* ws;
 };
 
-// pairs of a batch, at most (G = 0: queries)
-__host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return G > 0 ? (B + G + 2) / 2 : B; }
+// whether a batch runs every query by itself
+__host__ __device__ __forceinline__ bool by_itself(int32_t B, int32_t G) { return B < (int64_t)kImageQueries * G || G == 0; }
+// pairs of a batch, at most (queries, where they run by themselves)
+__host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return by_itself(B, G) ? B : (B + G + 2) / 2; }
 
 // exclusive sum over the block of x (all threads call); total = the block's sum
 __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
@@ -188,7 +194,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   const int np = kAloneQueries ? a.B : base;
   // a group whose image would end beyond the room has none, and so do all behind it
   int images = 0;
-  for (int g0 = 0; g0 < G; g0 += kPrepThreads) {
+  for (int g0 = 0; !kAloneQueries && g0 < G; g0 += kPrepThreads) {
     const int g = g0 + tid, size = g < G ? a.group_start[g + 1] - a.group_start[g] : 0;
     const int n = size > 0 ? image_chunks(size, gshared[g].y) : 0;
     int total;
@@ -203,9 +209,21 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
     Pair x{};
     int n = 0;
     if (kAloneQueries && p < np) {  // a query by itself, in chunks of kOwnChunk rows
-      x.q0 = p;
+      x.q0 = x.first = p;
       x.q1 = x.image = -1;
-      x.own0 = min(visible(a, p), a.own_max);
+      if (G > 0 && p >= a.group_start[0] && p < a.group_start[G]) {
+        int lo = 0, hi = G;  // the group with group_start[g] <= p < group_start[g + 1]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (a.group_start[mid] <= p) lo = mid;
+          else hi = mid;
+        }
+        x.first = gshared[lo].x;
+        x.ns = gshared[lo].y;
+      }
+      const int c = visible(a, p), most = x.ns + a.own_max;
+      if (a.G > 0 && c > most) report_error(a.ws, CSA2_ERR_INDEX_RANGE, a.n_entries[p]);
+      x.own0 = min(c, most);  // the first ns through the row of `first`
       n = (x.own0 + a.n_swa + kOwnChunk - 1) / kOwnChunk;
     } else if (p < np) {
       int lo = 0, hi = R;  // the range with gpair[v] <= p < gpair[v + 1]
@@ -1169,8 +1187,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, Pref
   int b = (int)blockIdx.x - 1;
   if (b < 0) {
     int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
-    if (a.G > 0) plan_block<false>(a, ints, kPrepSmem / 4);
-    else plan_block<true>(a, ints, kPrepSmem / 4);
+    if (by_itself(a.B, a.G)) plan_block<true>(a, ints, kPrepSmem / 4);
+    else plan_block<false>(a, ints, kPrepSmem / 4);
     return;
   }
   if (b < widen1) return widen_chunks(a, k, image, b, widen);
@@ -1511,10 +1529,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     int p = part.p, end = part.end;
     uint32_t n = 0, items = 0;
     for (int t = t0; t < t1 && good;) {
-      const int q = px->q0, own = px->own0, c0 = t - px->chunk0, nc = min(end, t1) - t;
+      const Pair& x = *px;
+      const int q = x.q0, c0 = t - x.chunk0, nc = min(end, t1) - t;
       if (nc > 0) {
         t += nc;
-        body(q, own, p, c0, nc, n, items);
+        body(q, x, p, c0, nc, n, items);
         n += (uint32_t)nc;
         ++items;
       }
@@ -1537,11 +1556,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     where = 41;
   } else if (warp >= kAloneS) {
     if (warp == kAloneIndex) {
-      for_items([&](int q, int own, int, int c0, int nc, uint32_t n, uint32_t) {
+      ptx::prefetch_l1(&part.pair.ns);  // the record's second half
+      for_items([&](int q, const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
+        const int own = x.own0, ns = x.ns, first = x.first;
         RowRef r[2];
         auto find = [&](int j) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) r[i] = find_own(k, q, own, (c0 + j) * kRows + 32 * i + lane);
+          for (int i = 0; i < 2; ++i) {
+            const int e = (c0 + j) * kRows + 32 * i + lane;
+            r[i] = e < ns && e < own ? find_entry(k, first, e) : find_own(k, q, own, e);
+          }
         };
         find(0);
 #pragma unroll 1
@@ -1565,7 +1589,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       constexpr uint32_t idesc_s = ptx::idesc_f16(64, kRows, 0);
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.x[0][0][0], kRows * 16, 128);
-      for_items([&](int q, int, int, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](int q, const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
         // the item's query, once S of the item before has left q'; it lands before anyone leaves
         good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
         if (!good) return;
@@ -1600,7 +1624,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       constexpr uint32_t idesc_o = ptx::idesc_f16(128, kHAtt, 0) | (1u << 15);  // A M-major
       const uint64_t da = ptx::smem_desc_noswizzle(&S.x[0][0][0], 128, kRows * 16);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
-      for_items([&](int, int, int, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](int, const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j, slot = m & 1u;
@@ -1656,7 +1680,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.o_read);
     };
-    for_items([&](int q, int, int p, int, int nc, uint32_t n, uint32_t) {
+    for_items([&](int q, const Pair&, int p, int, int nc, uint32_t n, uint32_t) {
       const float c2 = k.c2[(int64_t)q * kHAtt + h];
       float m2 = -INFINITY, lsum = 0.0f;
 #pragma unroll 1
@@ -1919,8 +1943,9 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
     return p;
   };
   // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
-  const size_t parts = G > 0 ? kClusters : kAlone;
-  const size_t slots = ((size_t)max_pairs(B, G) + parts) * (G > 0 ? 2 : 1);
+  const bool alone = by_itself(B, G);
+  const size_t parts = alone ? kAlone : kClusters;
+  const size_t slots = ((size_t)max_pairs(B, G) + parts) * (alone ? 1 : 2);
   L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
   L.chunk0 = (int32_t*)take(((size_t)max_pairs(B, G) + 1) * 4);
@@ -1934,8 +1959,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.turn = (float2*)take((size_t)B * 32 * 8);
   L.part_o = (uint4*)take(slots * kHAtt * kDMain * 2);
   L.part_ml = (float2*)take(slots * kHAtt * 8);
-  const int64_t groups = B / kImageQueries < G ? B / kImageQueries : G;
-  L.image_cap = groups * cdiv(shared_max, kChunk);
+  L.image_cap = alone ? 0 : G * cdiv(shared_max, kChunk);
   if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
   L.image = (uint16_t*)take((size_t)L.image_cap * kChunk * kDMain * 2);
   L.bytes = off;
@@ -2012,12 +2036,13 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
   if (bad != CSA2_OK) return bad;
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+  const bool alone = by_itself(B, G);
   const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.gshared, L.image_cap, G > 0 ? kClusters : kAlone, ws};
+                     L.gimage, L.gshared, L.image_cap, alone ? kAlone : kClusters, ws};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
@@ -2033,9 +2058,9 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     return CSA2_ERR_CUDA;
   const size_t smem = sizeof(PrefixSmem);
   if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem) != cudaSuccess ||
-      (G > 0 ? cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-             : cudaFuncSetAttribute(k_paged_attn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sizeof(AloneSmem))) != cudaSuccess)
+      (alone ? cudaFuncSetAttribute(k_paged_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AloneSmem))
+             : cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+          cudaSuccess)
     return launch_status();
   {
     KernelTimer timer("k_prefix_prep", st);
@@ -2050,7 +2075,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     launch_clusters(kern, dim3(B, ctas), dim3(threads), 1, cluster, 0, st, (const int2*)L.qpart,
                     (const uint4*)L.part_o, (const float2*)L.part_ml, sink, turn, out, out_bf16, lse_out, fix);
   };
-  if (G == 0) {
+  if (alone) {
     {
       KernelTimer timer("k_paged_attn", st);
       launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);

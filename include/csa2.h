@@ -511,9 +511,10 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  *                n_entries[b] above pages->max_pages * kv->seq_stride counts as that
  * 1 <= G <= B.  Every other argument as in csa2_paged_attn_decode; the workspace is
  * csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa) bytes: besides what
- * csa2_paged_attn_decode takes, 1 KB for each shared entry of a group, counted as n_shared_max for
- * min(G, B / 3) groups and 1 GB at most (groups of three queries or more read them from there;
- * beyond 2^20 entries, and in smaller groups, they are widened where they are read). */
+ * csa2_paged_attn_decode takes, with B >= 5 G 1 KB for each shared entry of a group, counted as
+ * n_shared_max for each and 1 GB at most (groups of five queries or more read them from there; beyond
+ * 2^20 entries, and in smaller groups, they are widened where they are read).  With B < 5 G sharing
+ * would cost more than it saves, and every query reads the entries for itself. */
 csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                     const int32_t* n_entries, int32_t G, const int32_t* group_start,
                                     const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
