@@ -454,7 +454,7 @@ def prefix_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, G: int, 
                        lse_out=None, stream=None, q_nr: NormRope | None = None, q_pos=None, sink=None,
                        win: Window | None = None, out_type: int | None = None) -> None:
     """paged_attn_decode for queries that share prefixes: the queries [group_start[g], group_start[g + 1])
-    agree on their first n_shared[g] entries, which are read once for the group
+    agree on their first n_shared[g] entries, which are read once for the group where that pays
     (csa2_prefix_attn_decode)."""
     _ok(lib().csa2_prefix_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), B, _ptr(n_entries), G,
                                       _ptr(group_start), _ptr(n_shared), n_shared_max, n_own_max, _ptr(swa), n_swa,

@@ -4,7 +4,7 @@
 // window.  With z the logits in log2 units, a part of the rows leaves its reference m, l = sum 2^(z - m) and
 // O / l = sum 2^(z - m) x / l; parts join by log-sum-exp.  Each call is three launches:
 //   k_prefix_prep   the plan (which chunks of rows every CTA runs), the queries' f16 images, and the image:
-//                   the shared entries of groups of kImageQueries or more queries, widened to f16 once;
+//                   the shared entries of large groups, widened to f16 once;
 //   k_paged_attn    one query to a CTA (without groups, or with small ones), or
 //   k_prefix_attn   two queries of a group to a pair of CTAs;
 //   k_paged_merge / k_prefix_merge   the join, the sink, the turn back, the output's type.
@@ -28,8 +28,8 @@
 // Behind the shared entries come the two queries' own (their last entries and windows): chunks whose
 // first 64 rows are the first query's and whose last 64 the second's, each query masking the other's; behind
 // the shorter's last, 128 rows of the longer.
-// Measured: 64 queries on 65,000 shared entries 386 us, 1.42 PFLOP/s, 75 % of the rate of a library bf16
-// product; 2 queries on 512 17 us, three launches and their dependent loads.
+// Measured: 64 queries on 65,000 shared entries 383 us, 1.43 PFLOP/s, 76 % of the rate of a library bf16
+// product; 32 on 8,192, normalised and rotated, 49 us.
 #include "attn.cuh"
 #include "index_scan.cuh"
 
@@ -45,6 +45,10 @@ constexpr int kOwnChunk = 64;    // of which each query of a pair has this many 
 // without; of eight: 86 and 90.  In pairs / by themselves: groups of one 160 / 98 us, two 93 / 98, three
 // 124 / 98, four 93 / 98, sixteen 76 / 98 (an odd group's last query takes a pair's time).
 constexpr int kImageQueries = 5;
+// Queries times shared entries below which every query runs by itself all the same, its ramp being shorter.  In
+// pairs / by themselves, us: 8 queries on 8,192 entries 33.7 / 26.8, 32 on 2,000 31.5 / 29.7, 128 on 500
+// 40.5 / 38.7; 16 on 8,192 38.6 / 38.6, 128 on 1,000 46.2 / 46.9; 16 on 16,384 47.9 / 58.3.
+constexpr int64_t kPairWork = 1 << 17;
 constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM,
 constexpr int kWidenFirst = 152;   // of which these come before the queries' staging
 constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
@@ -105,9 +109,11 @@ struct PrefixArgs {
 };
 
 // whether a batch runs every query by itself
-__host__ __device__ __forceinline__ bool by_itself(int32_t B, int32_t G) { return B < (int64_t)kImageQueries * G || G == 0; }
-// pairs of a batch, at most (queries, where they run by themselves)
-__host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return by_itself(B, G) ? B : (B + G + 2) / 2; }
+__host__ __device__ __forceinline__ bool by_itself(int32_t B, int32_t G, int64_t shared_max) {
+  return G == 0 || B < (int64_t)kImageQueries * G || B * shared_max < kPairWork;
+}
+// pairs of a batch, at most
+__host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return (B + G + 2) / 2; }
 
 // exclusive sum over the block of x (all threads call); total = the block's sum
 __device__ __forceinline__ int block_scan(int x, int* s_warp, int* total) {
@@ -178,7 +184,8 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   const int G = s_bad ? 0 : a.G;
   const int R = G + 2;  // ranges; without groups the first is empty
   int32_t* const gpair = R + 1 <= smem_ints / 4 ? smem : a.gpair;
-  int32_t* const chunk0 = max_pairs(a.B, a.G) + 1 <= smem_ints / 2 ? smem + smem_ints / 2 : a.chunk0;
+  const int most_pairs = kAloneQueries ? a.B : max_pairs(a.B, a.G);
+  int32_t* const chunk0 = most_pairs + 1 <= smem_ints / 2 ? smem + smem_ints / 2 : a.chunk0;
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
   int base = 0;
@@ -1187,7 +1194,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, Pref
   int b = (int)blockIdx.x - 1;
   if (b < 0) {
     int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
-    if (by_itself(a.B, a.G)) plan_block<true>(a, ints, kPrepSmem / 4);
+    if (by_itself(a.B, a.G, a.shared_max)) plan_block<true>(a, ints, kPrepSmem / 4);
     else plan_block<false>(a, ints, kPrepSmem / 4);
     return;
   }
@@ -1385,7 +1392,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
 // Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs, 64 KB of rows and 8 KB of P
 // written, 296 KB = 2,300 cycles at 128 bytes a cycle; the MMAs alone (S at the half rate of M = 64) take
 // 1,800; measured, about 2,800, the wait of a slot for its softmax among them.  48 queries of up to 65,536 entries
-// take 219 us (0.79 PFLOP/s, 1.8 TB/s of entries), one of 4,096 entries 16 us.
+// take 217 us (0.80 PFLOP/s, 1.8 TB/s of entries), one of 4,096 entries 16 us, three launches.
 constexpr int kAlone = 152;
 constexpr int kRows = 64;  // rows of a chunk
 constexpr int kRing = 8;   // chunks whose rows are found ahead
@@ -1943,12 +1950,12 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
     return p;
   };
   // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
-  const bool alone = by_itself(B, G);
-  const size_t parts = alone ? kAlone : kClusters;
-  const size_t slots = ((size_t)max_pairs(B, G) + parts) * (alone ? 1 : 2);
-  L.pairs = (Pair*)take(((size_t)max_pairs(B, G) + 1) * sizeof(Pair));
+  const bool alone = by_itself(B, G, shared_max);
+  const size_t parts = alone ? kAlone : kClusters, pairs = alone ? B : max_pairs(B, G);
+  const size_t slots = (pairs + parts) * (alone ? 1 : 2);
+  L.pairs = (Pair*)take((pairs + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
-  L.chunk0 = (int32_t*)take(((size_t)max_pairs(B, G) + 1) * 4);
+  L.chunk0 = (int32_t*)take((pairs + 1) * 4);
   L.qpart = (int2*)take((size_t)B * 8);
   L.parts = (Part*)take(parts * sizeof(Part));
   L.gimage = (int32_t*)take((size_t)G * 4);
@@ -2036,7 +2043,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
   if (bad != CSA2_OK) return bad;
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
-  const bool alone = by_itself(B, G);
+  const bool alone = by_itself(B, G, n_shared_max);
   const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;

@@ -495,10 +495,10 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
 
 /* csa2_paged_attn_decode for a batch whose queries share prefixes (one system prompt, one document,
  * samples drawn in parallel): group g is the queries [group_start[g], group_start[g + 1]), whose
- * sequences agree on their first n_shared[g] entries.  Those are read once for the group, through the
- * table row of its first query that has them all (or of the longest, when none has); entries from
- * n_shared[g] on, and the window, are each query's own, through its own row.  The result is that of
- * csa2_paged_attn_decode.
+ * sequences agree on their first n_shared[g] entries.  Those are read once for the group where that
+ * pays (see below), through the table row of its first query that has them all (or of the longest, when
+ * none has); entries from n_shared[g] on, and the window, are each query's own, through its own row.
+ * The result is that of csa2_paged_attn_decode.
  *   group_start  [G + 1] int32 (device), ascending within [0, B]; queries outside every group share
  *                nothing.  A group that is not ascending, or leaves [0, B], counts as empty and is
  *                reported as CSA2_ERR_INDEX_RANGE
@@ -511,10 +511,11 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  *                n_entries[b] above pages->max_pages * kv->seq_stride counts as that
  * 1 <= G <= B.  Every other argument as in csa2_paged_attn_decode; the workspace is
  * csa2_prefix_attn_workspace_size(B, G, n_shared_max, n_own_max, n_swa) bytes: besides what
- * csa2_paged_attn_decode takes, with B >= 5 G 1 KB for each shared entry of a group, counted as
- * n_shared_max for each and 1 GB at most (groups of five queries or more read them from there; beyond
- * 2^20 entries, and in smaller groups, they are widened where they are read).  With B < 5 G sharing
- * would cost more than it saves, and every query reads the entries for itself. */
+ * csa2_paged_attn_decode takes, 1 KB for each shared entry of a group, counted as n_shared_max for
+ * each and 1 GB at most (groups of five queries or more read them from there; beyond 2^20 entries,
+ * and in smaller groups, they are widened where they are read).  With B < 5 G or B * n_shared_max <
+ * 2^17 sharing would cost more than it saves: every query reads the entries for itself, and the
+ * workspace is as csa2_paged_attn_decode's. */
 csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                     const int32_t* n_entries, int32_t G, const int32_t* group_start,
                                     const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,

@@ -41,6 +41,12 @@ class Batch:
         self.B, self.P, self.n, self.n_swa, self.groups, self.shared = len(n), P, list(n), n_swa, groups, list(shared)
         B = self.B
         self.max_pages = max(1, max(-(-x // P) for x in n))
+        # groups of five queries or more run in pairs where queries times n_shared_max reach 2^17: small
+        # cases take a large bound (and rows as long, which are not read)
+        self.shared_max = max([0, *shared])
+        if groups and B >= 5 * len(groups) and B * self.shared_max < 1 << 17:
+            self.shared_max = 65536
+            self.max_pages = max(self.max_pages, -(-65536 // P))
         first, whole, part = list(range(B)), [0] * B, [0] * B
         for g, (a, z) in enumerate(groups):
             long = next((b for b in range(a, z) if n[b] >= shared[g]), max(range(a, z), key=lambda b: n[b]))
@@ -135,7 +141,8 @@ class Batch:
         out, lse = self.outputs(dtype)
         start = [a for a, _ in self.groups] + [self.groups[-1][1]] if start is None else start
         shared = self.shared if shared is None else shared
-        shared_max = max(max(self.shared), 0) if shared_max is None else shared_max
+        if shared_max is None:
+            shared_max = max(self.shared_max, *shared)
         own_max = max(self.n) if own_max is None else own_max
         G = len(shared)
         ws = csa2.workspace(csa2.prefix_attn_workspace_size(self.B, G, shared_max, own_max, self.n_swa)) if ws is None else ws
@@ -289,7 +296,7 @@ def test_prefix_groups(n, groups, shared, P, times):
 def test_prefix_longer_than_the_first_query(n, groups, shared, own_max, times):
     n, groups, shared = repeated(n, groups, shared, times)
     b = Batch(40, n, 16, groups, shared, n_swa=5).device()
-    out, lse, ws = b.prefix(own_max=own_max, shared_max=min(280, 16 * b.max_pages))  # the tables' rows end there
+    out, lse, ws = b.prefix(own_max=own_max, shared_max=max(b.shared_max, 280) if times > 1 else min(280, 16 * b.max_pages))
     assert csa2.check(ws)[0] == 0
     close(out, lse, b.reference())
 
@@ -312,11 +319,11 @@ def test_one_head_of_a_query_not_finite(value, times):
 @pytest.mark.parametrize("B", [3, 20])
 def test_without_lse_the_same_output(B):
     b = Batch(42, [300 + i for i in range(B)], 16, [(0, B)], [290], n_swa=16, extras=True, sink=True).device()
-    ws = csa2.workspace(max(csa2.prefix_attn_workspace_size(B, 1, 290, 300, 16), csa2.paged_attn_workspace_size(B, 400, 16)))
+    ws = csa2.workspace(max(csa2.prefix_attn_workspace_size(B, 1, b.shared_max, 300, 16), csa2.paged_attn_workspace_size(B, 400, 16)))
     keep = to_dev(np.array([0, B], np.int32)), to_dev(np.array([290], np.int32))
     out = torch.empty((B, H, D), dtype=torch.bfloat16, device="cuda")
     one = b.prefix(torch.bfloat16)
-    csa2.prefix_attn_decode(b.planes, b.pages, B, b.dn, 1, *keep, 290, 300, b.dswa, 16, b.dq, SCALE, out, ws, **b.kw)
+    csa2.prefix_attn_decode(b.planes, b.pages, B, b.dn, 1, *keep, b.shared_max, 300, b.dswa, 16, b.dq, SCALE, out, ws, **b.kw)
     assert csa2.check(ws)[0] == 0 and torch.equal(out, one[0])
     one = b.paged(torch.bfloat16)
     csa2.paged_attn_decode(b.planes, b.pages, B, b.dn, 299 + B, b.dswa, 16, b.dq, SCALE, out, ws, **b.kw)
@@ -368,22 +375,26 @@ def test_prefix_many_small_groups_and_one_large(most):
     close(out, lse, b.reference())
 
 
-@pytest.mark.parametrize("times", [1, 2])
+@pytest.mark.parametrize("times", [1, 440])  # 1,320 queries: pairs also with the bound of 100
 def test_prefix_bounds_of_the_host(times):
-    b = Batch(14, [300, 310, 320] * times, 16, [(0, 3 * times)], [256]).device()
+    q = torch.randn((64, H, D), generator=torch.Generator().manual_seed(14)).to(torch.bfloat16)
+    B = 3 * times
+    b = Batch(14, [300, 310, 320] * times, 16, [(0, B)], [256], q=q.repeat(-(-B // 64), 1, 1)[:B]).device()
+    of = np.arange(B) if times == 1 else np.arange(0, B, 41)
+    at = torch.from_numpy(of).cuda()
     # n_shared above its bound: the rest is read as each query's own
     out, lse, ws = b.prefix(shared_max=100, own_max=220)
     assert csa2.check(ws)[0] == 0
-    close(out, lse, b.reference())
+    close(out[at], lse[at], b.reference(of=of))
     # own entries above theirs: left out and reported
     out, lse, ws = b.prefix(shared_max=256, own_max=50)
     st, det = csa2.check(ws)
     assert st == 6 and det in (310, 320)
-    close(out, lse, b.reference(n=[300, 306, 306] * times))
+    close(out[at], lse[at], b.reference(n=[300, 306, 306] * times, of=of))
     # a negative count of shared entries is none
-    out, lse, ws = b.prefix(shared=[-4], shared_max=0)
+    out, lse, ws = b.prefix(shared=[-4], shared_max=0 if times == 1 else 100)
     assert csa2.check(ws)[0] == 0
-    close(out, lse, b.reference())
+    close(out[at], lse[at], b.reference(of=of))
 
 
 @pytest.mark.parametrize("start,shared", [([0, -1, 3], [256, 256]), ([0, 9, 3], [256, 256]), ([2, 0, 3], [256, 256])])
@@ -621,7 +632,7 @@ def test_more_shared_entries_than_the_workspace_widens():
 
 def test_two_graphs_share_a_workspace():
     b = Batch(30, [300, 310, 320, 64, 0], 16, [(0, 3)], [256], n_swa=16, extras=True, sink=True).device()
-    size = max(csa2.prefix_attn_workspace_size(5, 1, 256, 70, 16), csa2.paged_attn_workspace_size(5, 320, 16))
+    size = max(csa2.prefix_attn_workspace_size(5, 1, b.shared_max, 70, 16), csa2.paged_attn_workspace_size(5, 320, 16))
     ws = csa2.workspace(size)
     b.prefix(own_max=70, ws=ws)
     b.paged(ws=ws)
@@ -726,3 +737,16 @@ def test_more_entries_than_either_bound(pairs):
     out, lse, ws = b.prefix(own_max=34_600)
     assert csa2.check(ws)[0] == 0
     close(out[:3], lse[:3], b.reference(of=range(min(3, len(n)))))
+
+
+@pytest.mark.parametrize("B,kernel", [(4, "k_paged_attn"), (5, "k_prefix_attn")])
+def test_which_form_runs(B, kernel):
+    # the tests of pairs run pairs
+    b = Batch(45, [300] * B, 16, [(0, B)], [290]).device()
+    csa2.timing_enable(True)
+    try:
+        b.prefix()
+        torch.cuda.synchronize()
+        assert {"k_paged_attn", "k_prefix_attn"} & set(csa2.kernel_times()) == {kernel}
+    finally:
+        csa2.timing_enable(False)
