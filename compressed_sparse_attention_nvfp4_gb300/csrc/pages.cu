@@ -274,8 +274,10 @@ __global__ void __launch_bounds__(kFillThreads) k_page_fill(PageArgs a, PlanView
   fill_rows(a, v, t, n);
 }
 
-// One CTA up to this many map rows and requests.
-constexpr int kOneCtaRows = 8192, kOneCtaRequests = 2048;
+// One CTA up to this many map rows and requests (whose plan its shared memory holds).  From a graph, one CTA /
+// plan and fill, us: 64 requests with 1,000 new entries 4.8 / 7.0, 256 with 1,000 5.8 / 7.0, 2,000 with 1,000
+// 8.7 / 11.5; 64 with 4,000 7.5 / 6.9, 256 with 4,000 8.0 / 7.6, 64 with 8,000 10.7 / 6.8.
+constexpr int kOneCtaRows = 2048, kOneCtaRequests = 2048;
 
 PlanView plan_view(void* ws, int32_t B, size_t* bytes) {
   size_t off = kWsHeader;

@@ -1228,10 +1228,11 @@ __device__ __forceinline__ void store_channels(void* out, int out_bf16, int64_t 
 //   out = sum 2^(m_i - m) l_i (O_i / l_i) / L,  L = sum 2^(m_i - m) l_i  (+ 2^(z - m) of the sink).
 // Latency bounds it: a thread reads up to kJoin partials at once (references and channels in one round trip),
 // and for few queries, which are cut into many partials, four slices of a CTA's threads take every fourth
-// and the first joins the four (one query of 4,096 entries, 66 partials: 27 us with one slice, 12 with four;
-// 128 queries of two or three partials: 12 us with one, 37 with four).
+// and the first joins the four.  A call with one slice / four, us: one query of 4,096 entries (66 partials) 31.2 /
+// 15.6, eight 24.4 / 21.1, 15 28.2 / 30.8, 32 37.0 / 47.3; 8 queries on 65,000 shared entries 77.0 / 78.1, 15 on
+// 20,000 52.7 / 58.0.
 constexpr int kJoin = 8;
-constexpr int kSliceQueries = 16;  // below this many queries: four slices
+constexpr int kSliceQueries = 12;  // below this many queries: four slices
 
 // the running join of one head's kC channels
 template <int kC>
