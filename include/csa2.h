@@ -500,8 +500,8 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  * none has); entries from n_shared[g] on, and the window, are each query's own, through its own row.
  * The result is that of csa2_paged_attn_decode.
  *   group_start  [G + 1] int32 (device), ascending within [0, B]; queries outside every group share
- *                nothing.  A group that is not ascending, or leaves [0, B], counts as empty and is
- *                reported as CSA2_ERR_INDEX_RANGE
+ *                nothing.  Otherwise CSA2_ERR_INDEX_RANGE (detail: such a group) is reported and no
+ *                query of the call shares anything: all its entries count as its own
  *   n_shared     [G] int32 (device): negative counts as 0, more than n_shared_max as n_shared_max
  *                (the rest is read as each query's own).  A query shorter than n_shared sees its
  *                first n_entries[b] entries only
