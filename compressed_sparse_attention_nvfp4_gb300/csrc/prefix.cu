@@ -1132,61 +1132,67 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
 // The image's chunks first, first + step, ..: a warp's lane l widens four blocks (of 32 channels), the rotated
 // one xor 4 i, of row l % 8 of its eight, and stores 16 bytes to each of the block's four planes, 128 contiguous
 // bytes for eight rows.  Bytes bound it: 288 read and 1,024 written an entry (65,000 entries: about 20 us, 12 of
-// them the bytes').
+// them the bytes').  The rows of a CTA's next chunk are asked for with this one's (64 on 65000 386.7 us without,
+// 384.1 with).
 __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
                                              int step) {
   __shared__ int s_warp[kPrepThreads / 32];
-  __shared__ int2 s_found;  // the row's query (-1: no such group) and the shared entries
-  __shared__ int s_at;
+  __shared__ int2 s_found;   // the row's query (-1: no such group) and the shared entries
+  __shared__ int2 s_chunks;  // the group's first chunk, and the next group's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = rotated(lane) & 7;
+  auto row_of = [&](int first, int e) {  // a page outside the planes is reported by the attention
+    const int pi = (int)((uint64_t)e * k.page_div >> 40);
+    return resolve(k, RowRef{k.table[first * k.max_pages + pi], e - pi * k.page_entries}, false);
+  };
+  int2 found = make_int2(-1, 0), chunks = make_int2(0, 0);
   for (int64_t t = first_chunk;; t += step) {
-    // the group whose image holds chunk t
-    if (threadIdx.x == 0) s_found.x = -1;
-    __syncthreads();
-    int base = 0;
-    for (int g0 = 0; g0 < a.G && base <= t; g0 += kPrepThreads) {
-      const int g = g0 + threadIdx.x;
-      int2 sh = make_int2(0, 0);
-      int n = 0;
-      if (g < a.G) {
-        const int lo = a.group_start[g], hi = a.group_start[g + 1];
-        if (lo >= 0 && hi <= a.B && hi - lo >= kImageQueries) {
-          sh = shared_of(a, g, lo, hi);
-          n = image_chunks(hi - lo, sh.y);
+    if (t >= chunks.y) {  // the group whose image holds chunk t
+      __syncthreads();
+      if (threadIdx.x == 0) s_found.x = -1;
+      __syncthreads();
+      int base = 0;
+      for (int g0 = 0; g0 < a.G && base <= t; g0 += kPrepThreads) {
+        const int g = g0 + threadIdx.x;
+        int2 sh = make_int2(0, 0);
+        int n = 0;
+        if (g < a.G) {
+          const int lo = a.group_start[g], hi = a.group_start[g + 1];
+          if (lo >= 0 && hi <= a.B && hi - lo >= kImageQueries) {
+            sh = shared_of(a, g, lo, hi);
+            n = image_chunks(hi - lo, sh.y);
+          }
         }
+        int total;
+        const int at = base + block_scan(n, s_warp, &total);
+        if (n > 0 && at + (int64_t)n <= a.image_cap && t >= at && t < at + n) {
+          s_found = sh;
+          s_chunks = make_int2(at, at + n);
+        }
+        base += total;
       }
-      int total;
-      const int at = base + block_scan(n, s_warp, &total);
-      if (n > 0 && at + (int64_t)n <= a.image_cap && t >= at && t < at + n) {
-        s_found = sh;
-        s_at = at;
-      }
-      base += total;
+      __syncthreads();
+      found = s_found;
+      if (found.x < 0) return;
+      chunks = s_chunks;
     }
-    __syncthreads();
-    const int first = s_found.x, ns = s_found.y;
-    if (first < 0) return;
-    const int row = 8 * warp + (lane & 7), e = (int)(t - s_at) * kChunk + row;
-    int r = kNoRow;
-    if (e < ns) {
-      const int pi = (int)((uint64_t)e * k.page_div >> 40);
-      r = resolve(k, RowRef{k.table[first * k.max_pages + pi], e - pi * k.page_entries}, false);  // the attention reports
-    }
+    const int row = 8 * warp + (lane & 7), e = (int)(t - chunks.x) * kChunk + row;
+    const int r = e < found.y ? row_of(found.x, e) : kNoRow;
     Fetch f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) fetch(f[i], k, r, b0 ^ (4 * i));
+    const int64_t next = e + (int64_t)step * kChunk;
+    if (lane < 8 && next < found.y) prefetch_row(k, row_of(found.x, (int)next));
     uint16_t* dst = image + t * kDMain * kChunk + row * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      put(f[i], r, dst + (b0 ^ (4 * i)) * 4 * kChunk * 8, kChunk * 8);
-    __syncthreads();  // s_found is written again
+    for (int i = 0; i < 4; ++i) put(f[i], r, dst + (b0 ^ (4 * i)) * 4 * kChunk * 8, kChunk * 8);
   }
 }
 
 // Everything the attention needs, by independent CTAs of one launch: the plan, the queries, the image, of which
 // half the CTAs come first (all behind the queries: 53.4 and 75.1 us for prefix 32 on 8192 and 101 on 4001
-// instead of 50.9 and 71.2).
-__global__ void __launch_bounds__(kPrepThreads) k_prefix_prep(PrefixArgs a, PrefixQuery q,
+// instead of 50.9 and 71.2).  Two CTAs on an SM: with the 72 registers it would take, one (ragged 101 on 4001
+// 68.5 us instead of 66.0).
+__global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, PrefixQuery q,
                                                               const __grid_constant__ PrefixKernel k, uint16_t* image) {
   extern __shared__ __align__(16) unsigned char prep_smem[];
   ptx::griddep_launch();
@@ -1448,7 +1454,8 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     if (m >= chunks) return;
     const uint32_t slot = (uint32_t)m & 1u;
     if (m >= 2)
-      good = good && ptx::mbar_wait_warp(&S.x_free[slot][half], (((uint32_t)m >> 1) - 1) & 1u, &S.abort_flag, kWaitBudget);
+      good = good && ptx::mbar_wait_warp(&S.x_free[slot][half], (((uint32_t)m >> 1) - 1) & 1u, &S.abort_flag,
+                                         kWaitBudget);
     if (!good) return;
     uint16_t* d = dst + slot * (kDMain * kRows);
     put(f[0], r, d, kRows * 8);
@@ -1851,7 +1858,8 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
     if (z != -INFINITY) L += ptx::ex2(z - ref);
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
-    if (lse && (kSlices == 1 || tile == 0) && lane == 0) lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
+    if (lse && (kSlices == 1 || tile == 0) && lane == 0)
+      lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
   }
   __syncthreads();
   float acc[8];
@@ -2074,8 +2082,8 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   {
     KernelTimer timer("k_prefix_prep", st);
     const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
-    launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads), (size_t)kPrepSmem, st, a, pq, k,
-               L.image);
+    launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
+               (size_t)kPrepSmem, st, a, pq, k, L.image);
   }
   const int slices = B < kSliceQueries ? 4 : 1;
   const float2* turn = ex.rope ? L.turn : nullptr;
