@@ -316,9 +316,9 @@ extern "C" csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const 
                                         int32_t* row_slot, int64_t* row_entry, int64_t* row_pos, int32_t* row_start,
                                         void* ws, size_t ws_bytes, csa2_stream stream) {
   using namespace csa2;
-  if (B <= 0 || B > 65535 || page_entries <= 0 || m <= 0 || max_pages <= 0 || n_pages <= 0 || n_rows < 0)
+  if (B <= 0 || B > 65535 || page_entries <= 0 || m <= 0 || max_pages < 0 || n_pages <= 0 || n_rows < 0)
     return CSA2_ERR_INVALID_ARG;
-  if (!n_have || !n_new || !page_table || !free_pages || !n_free || !n_free_out || !n_entries)
+  if (!n_have || !n_new || (max_pages > 0 && !page_table) || !free_pages || !n_free || !n_free_out || !n_entries)
     return CSA2_ERR_INVALID_ARG;
   const void* p4[] = {n_have, n_new, n_kept, page_table, free_pages, n_free, n_free_out, n_entries, row_query,
                       row_slot, row_start};

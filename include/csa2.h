@@ -453,7 +453,7 @@ size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  * outside [0, n_pages] (CSA2_ERR_INDEX_RANGE), or too few pages are free (CSA2_ERR_NO_PAGES,
  * detail = pages missing), the error word says so, no table or stack element changes, n_entries =
  * n_have, n_free_out = n_free, row_start = 0 and every row is -1.  A page listed twice is not
- * noticed.  1 <= B <= 65535, page_entries, m, max_pages, n_pages >= 1; arrays aligned to their
+ * noticed.  1 <= B <= 65535, page_entries, m, n_pages >= 1, max_pages >= 0; arrays aligned to their
  * elements; arrays other than the two named pairs must not overlap. */
 csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const int32_t* n_new, int32_t page_entries,
                              int32_t m, const int32_t* n_kept, int32_t* page_table, int32_t max_pages,

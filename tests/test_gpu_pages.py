@@ -202,3 +202,20 @@ def test_steps_in_place_from_a_graph_on_another_stream(B):
     st.synchronize()
     assert csa2.check(d.ws)[0] == 0
     check(d, s, rows, start, B, inplace=True)
+
+
+@pytest.mark.parametrize("table", [None, torch.empty((3, 0), dtype=torch.int32)])
+def test_no_request_has_or_gets_an_entry(table):
+    table = table if table is None else table.cuda()
+    e = lambda *n: torch.full(n, -77, dtype=torch.int32, device="cuda")
+    free, n_free, n_free_out, n_entries, start, query = i32([4, 2, 9]), i32([3]), e(1), e(3), e(4), e(5)
+    ws = csa2.workspace(csa2.page_tables_workspace_size(3))
+    call = lambda new: csa2.page_tables(3, i32([0, 0, 0]), i32(new), 16, table, 0, 10, free, n_free, n_free_out, n_entries,
+                                        ws, n_rows=5, query=query, row_start=start)
+    call([0, 0, 0])
+    assert csa2.check(ws)[0] == 0
+    assert n_entries.tolist() == [0, 0, 0] and n_free_out.tolist() == [3] and start.tolist() == [0] * 4
+    assert query.tolist() == [-1] * 5 and free.tolist() == [4, 2, 9]
+    call([0, 1, 0])
+    assert csa2.check(ws) == (6, 1)
+    assert n_entries.tolist() == [0, 0, 0] and n_free_out.tolist() == [3]

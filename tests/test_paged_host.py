@@ -18,7 +18,7 @@ def tables(B=4, have=16, new=16, page=64, m=1, kept=None, table=16, max_pages=8,
 
 
 @pytest.mark.parametrize("bad", [dict(B=0), dict(B=65536), dict(have=None), dict(new=None), dict(page=0),
-                                 dict(page=-1), dict(m=0), dict(table=None), dict(max_pages=0), dict(n_pages=0),
+                                 dict(page=-1), dict(m=0), dict(table=None), dict(max_pages=-1), dict(n_pages=0),
                                  dict(free=None), dict(n_free=None), dict(n_free_out=None), dict(n_entries=None),
                                  dict(n_rows=-1), dict(n_rows=5), dict(have=18), dict(kept=2), dict(table=6),
                                  dict(entry=12, n_rows=1), dict(pos=20, n_rows=1), dict(slot=3, n_rows=1),
