@@ -500,7 +500,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// p = 2^(s c2 - m) of 32 rows, packed in pairs as f16 from the fp32 values whose sum goes to `sum`;
+// Probabilities go to the tensor cores as f16 of p = 2^(z - m), a rounding of 2^-11 at most down to p = 2^-14, and
+// an absolute one of 2^-25 below.  A long context behind one strong row lies there: 65,536 rows, each 2^-25.5 of
+// the strongest, are a thousandth of the output together, and none of them would be left with m at the largest
+// logit.  So a new reference m is kTopExp below the largest logit, and moves when one exceeds it by more than
+// kMaxExp (f16 ends below 2^16): what a row loses is 2^-36 of the largest at most.  The 4 bits (2.8 nats) between
+// the two are what the running maximum may rise before O has to be scaled.
+constexpr float kTopExp = 11.0f, kMaxExp = 15.0f;
+
+// p of 32 rows (exponents s c2 - m), packed in pairs as f16 from the fp32 values whose sum goes to `sum`;
 // returns the largest exponent.  Rows that the mask has not are -inf.
 __device__ __forceinline__ float probs32(uint64_t (&s)[16], uint32_t mask, float c2, float m, uint32_t (&ph)[16],
                                          float& sum) {
@@ -934,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         mk1 &= __ballot_sync(0xffffffffu, S.rows[m & 3u][64 * half + 32 + lane] != kNoRow);
         if (good && lane == 0) ptx::mbar_arrive(&S.r_free[m & 3u]);
         // P with the reference so far (0 before the first row); it stands unless some head's logits
-        // exceed it by too much, then once more with that head's new reference
+        // exceed it by too much (kMaxExp), then once more with that head's new reference
         float alpha = 1.0f, sum, ref = m2 == -INFINITY ? 0.0f : m2;
         uint32_t nv;
 #pragma unroll 1
@@ -961,15 +969,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
             ptx::fence_proxy_async_smem();
           }
           if (round) break;
-          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kTau2;
+          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kMaxExp;
           nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
           if (nv == 0 || nv >= 8) break;
           S.red[half][h] = top;
           softmax_sync();
           const float cm = fmaxf(S.red[0][h], S.red[1][h]) + ref;  // over both threads' rows
-          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kTau2) {
-            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
-            m2 = cm;
+          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kMaxExp) {
+            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - (cm - kTopExp));
+            m2 = cm - kTopExp;
           }
           ref = m2 == -INFINITY ? 0.0f : m2;
         }
@@ -1271,6 +1279,12 @@ struct LseRest {
   const uint16_t* rest;  // null: q was not rounded, or no logsumexp is asked for
   const float* c2;
 };
+// ref + log2 L in natural units.  A sum is 2^11 (kTopExp) or more: its exponent joins the reference first, so that
+// the logarithm's rounding is that of a number below one.
+__device__ __forceinline__ float natural(float ref, float L) {
+  const int e = (int)(__float_as_uint(L) >> 23) - 127;
+  return (isfinite(L) ? ref + (float)e + log2f(L * exp2i_f32(-e)) : ref + log2f(L)) / kLog2e;
+}
 __device__ __forceinline__ float corrected(const LseRest& f, int b, int h, float l, float e) {
   // a query without rows may hold anything
   return l > -INFINITY && isfinite(e) ? fmaf(e, f.c2[(int64_t)b * kHAtt + h] / kLog2e, l) : l;
@@ -1379,7 +1393,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
         for (int i = 0; i < kPer / 32; ++i) e += s_dot[i][t];
     }
     if (t < kHeads) {
-      const float l = a.L == 0.0f ? -INFINITY : (a.ref + log2f(a.L)) / kLog2e;
+      const float l = a.L == 0.0f ? -INFINITY : natural(a.ref, a.L);
       lse[b * kHAtt + h] = fix.rest ? corrected(fix, b, h, l, e) : l;
     }
   }
@@ -1728,13 +1742,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             ptx::fence_proxy_async_smem();
           }
           if (round) break;
-          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kTau2;
+          const bool over = m2 == -INFINITY ? top > -INFINITY : top > kMaxExp;
           nv = softmax_vote(__any_sync(0xffffffffu, over), !good || *abort_flag != 0, lane);
           if (nv == 0 || nv >= 8) break;
           const float cm = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) + ref;
-          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kTau2) {
-            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - cm);
-            m2 = cm;
+          if (m2 == -INFINITY ? cm > -INFINITY : cm > m2 + kMaxExp) {
+            alpha = m2 == -INFINITY ? 0.0f : ptx::ex2(m2 - (cm - kTopExp));
+            m2 = cm - kTopExp;
           }
           ref = m2 == -INFINITY ? 0.0f : m2;
         }
@@ -1859,7 +1873,7 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
     if (lse && (kSlices == 1 || tile == 0) && lane == 0)
-      lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : (ref + log2f(L)) / kLog2e;
+      lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : natural(ref, L);
   }
   __syncthreads();
   float acc[8];
