@@ -9,7 +9,7 @@
 //   k_prefix_attn   two queries of a group to a pair of CTAs;
 //   k_paged_merge / k_prefix_merge   the join, the sink, the turn back, the output's type.
 // All chunks form one list that the CTAs share evenly, whatever the queries' lengths; a query cut between
-// CTAs leaves a partial in each.
+// CTAs leaves a partial in each, in fp32 for an fp32 output and in f16 for a bf16 one (Vec8).
 //
 // Pairs.  Two queries of a group make a pair, and their 2 x 64 heads the 128 rows of one MMA, so an entry of
 // the shared prefix serves two queries and the tensor cores run at their full rate (64 rows alone run at half
@@ -30,6 +30,8 @@
 // the shorter's last, 128 rows of the longer.
 // Measured: 64 queries on 65,000 shared entries 383 us, 1.43 PFLOP/s, 76 % of the rate of a library bf16
 // product; 32 on 8,192, normalised and rotated, 49 us.
+#include <type_traits>
+
 #include "attn.cuh"
 #include "index_scan.cuh"
 
@@ -357,7 +359,7 @@ struct PrefixKernel {
   const int64_t *win_pos, *win_lo;
   const Pair* pairs;
   const Part* parts;
-  uint4* part_o;    // [pairs + clusters][2][32][128]: eight f16 channels c8 of thread t of the epilogue, of O / l
+  uint4* part_o;    // [pairs + clusters][2][32 Vec8::kWords][128]: eight channels of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
 };
@@ -684,27 +686,71 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
   return good;
 }
 
-// Columns 32 c0 .. 32 c1 of O / l of thread t's accumulator row, in f16: at most the largest |x| (2,688), and a
-// rounding of 2^-11 at most, a quarter of that of a bf16 output; the partials are most of what a short call moves.
+// Eight values of a part's O / l, as the join reads them: fp32 for an fp32 output.  For a bf16 output f16, times 16:
+// |O / l| is at most the largest |x|, 2,688, so 2^-11 of a value or 2^-29 are the most that is rounded off, an
+// eighth of the output's own rounding; the smallest entry that is not zero is 2^-10.  The parts are most of what a
+// short call moves, in fp32 / f16, us: paged ragged 128 x 2000 52.3 / 44.5, prefix ragged 101 on 4001 67.1 / 61.1,
+// paged ragged 48 x 65536 223.7 / 217.6.
+template <bool kHalf>
+struct Vec8 {
+  static constexpr int kWords = kHalf ? 1 : 2;  // 16-byte words
+  static constexpr float kScale = kHalf ? 16.0f : 1.0f;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const uint4* p) {  // words 128 apart: a warp's stores are 512 contiguous bytes
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = p[i * 128];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (kHalf) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    } else {
+      const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+    }
+  }
+  // value(i) comes scaled by kScale
+  template <typename F>
+  static __device__ __forceinline__ void store(uint4* p, F value) {
+    if constexpr (kHalf) {
+      auto two = [&](int i) {
+        const __half2 v = __floats2half2_rn(value(i), value(i + 1));
+        return *reinterpret_cast<const uint32_t*>(&v);
+      };
+      p[0] = make_uint4(two(0), two(2), two(4), two(6));
+    } else {
+      auto one = [&](int i) { return __float_as_uint(value(i)); };
+      p[0] = make_uint4(one(0), one(1), one(2), one(3));
+      p[128] = make_uint4(one(4), one(5), one(6), one(7));
+    }
+  }
+};
+
+// Columns 32 c0 .. 32 c1 of O / l of thread t's accumulator row.
+template <bool kHalf>
 __device__ __forceinline__ void store_pair_o(const PrefixKernel& k, uint32_t tmem, int64_t slot, int t, float l, int c0,
                                              int c1) {
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  uint4* po = k.part_o + slot * 32 * 128 + t;
+  using Vec = Vec8<kHalf>;
+  const float inv = l > 0.0f ? Vec::kScale / l : 0.0f;
+  uint4* po = k.part_o + slot * (32 * Vec::kWords) * 128 + t;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     uint32_t a[32];
     ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(t & ~31) << 16) + 32u * (uint32_t)c, a);
     ptx::tmem_wait_ld();
-    auto pk = [&](int u) {
-      const __half2 v = __floats2half2_rn(__uint_as_float(a[2 * u]) * inv, __uint_as_float(a[2 * u + 1]) * inv);
-      return *reinterpret_cast<const uint32_t*>(&v);
-    };
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      po[(c * 4 + u) * 128] = make_uint4(pk(4 * u), pk(4 * u + 1), pk(4 * u + 2), pk(4 * u + 3));
+      Vec::store(po + (c * 4 + u) * Vec::kWords * 128, [&](int i) { return __uint_as_float(a[8 * u + i]) * inv; });
   }
 }
 
+template <bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k,
                                                                   const __grid_constant__ ImageMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -786,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     if (good && t1 > t0 && S.last_slot >= 0) {
       ptx::tc_fence_after();
       const int quarter = (warp - kRowWarp) / 4, t = 32 * (warp % 4) + lane;
-      store_pair_o(k, tmem, S.last_slot, t, S.red[0][t & 63] + S.red[1][t & 63], 2 * quarter, 2 * quarter + 2);
+      store_pair_o<kHalf>(k, tmem, S.last_slot, t, S.red[0][t & 63] + S.red[1][t & 63], 2 * quarter, 2 * quarter + 2);
       ptx::tc_fence_before();
     }
     where = 31;
@@ -913,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         softmax_sync();
       }
       if (open_slot >= 0) {
-        if (!ends) store_pair_o(k, tmem, open_slot, tid, l, 0, 8);
+        if (!ends) store_pair_o<kHalf>(k, tmem, open_slot, tid, l, 0, 8);
         if (half == 0) k.part_ml[(int64_t)open_slot * kHAtt + h] = make_float2(open_m, l);
       }
       ptx::tc_fence_before();
@@ -1220,9 +1266,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, P
 }
 
 // kC consecutive output channels at element `at`
-template <int kC>
-__device__ __forceinline__ void store_channels(void* out, int out_bf16, int64_t at, const float (&v)[kC]) {
-  if (out_bf16) {
+template <bool kBf16, int kC>
+__device__ __forceinline__ void store_channels(void* out, int64_t at, const float (&v)[kC]) {
+  if (kBf16) {
     uint32_t w[kC / 2];
 #pragma unroll
     for (int u = 0; u < kC / 2; ++u) {
@@ -1241,12 +1287,11 @@ __device__ __forceinline__ void store_channels(void* out, int out_bf16, int64_t 
 
 // The join of a query's partials.  Partial i has reference m_i (log2 units), sum l_i and O_i / l_i:
 //   out = sum 2^(m_i - m) l_i (O_i / l_i) / L,  L = sum 2^(m_i - m) l_i  (+ 2^(z - m) of the sink).
-// Latency bounds it: a thread reads up to kJoin partials at once (references and channels in one round trip),
-// and for few queries, which are cut into many partials, four slices of a CTA's threads take every fourth
+// Latency bounds it: a thread reads up to 16 words of partials at once (references and channels in one round
+// trip), and for few queries, which are cut into many partials, four slices of a CTA's threads take every fourth
 // and the first joins the four.  A call with one slice / four, us: one query of 4,096 entries (66 partials) 31.2 /
 // 15.6, eight 24.4 / 21.1, 15 28.2 / 30.8, 32 37.0 / 47.3; 8 queries on 65,000 shared entries 77.0 / 78.1, 15 on
 // 20,000 52.7 / 58.0.
-constexpr int kJoin = 8;
 constexpr int kSliceQueries = 12;  // below this many queries: four slices
 
 // the running join of one head's kC channels
@@ -1293,20 +1338,22 @@ __device__ __forceinline__ float corrected(const LseRest& f, int b, int h, float
 // A CTA joins 8 / kSlices heads: thread t of a slice has head t % (8 / kSlices) of them and kVec planes (of eight
 // channels): two, which share a weight, or one where slices make for more threads (one for all: 4 us more for
 // 101 queries).
-template <int kSlices>
+template <int kSlices, bool kHalf>
 struct PrefixMerge {
   static constexpr int kVec = kSlices > 1 ? 1 : 2, kHeads = 8 / kSlices, kPer = kHeads * (kDMain / 8) / kVec;
+  static constexpr int kAhead = kSlices > 1 || kHalf ? 8 : 4;  // partials read at once
   static constexpr int kThreads = kPer * kSlices;
 };
-template <int kSlices>
-__global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge(const int2* __restrict__ qpart,
+template <int kSlices, bool kHalf>
+__global__ void __launch_bounds__(PrefixMerge<kSlices, kHalf>::kThreads) k_prefix_merge(const int2* __restrict__ qpart,
                                                                 const uint4* __restrict__ part_o,
                                                                 const float2* __restrict__ part_ml,
                                                                 const float* __restrict__ sink,
                                                                 const float2* __restrict__ turn, void* __restrict__ out,
-                                                                int out_bf16, float* __restrict__ lse, LseRest fix) {
-  constexpr int kVec = PrefixMerge<kSlices>::kVec, kHeads = PrefixMerge<kSlices>::kHeads;
-  constexpr int kPer = PrefixMerge<kSlices>::kPer, kC = 8 * kVec;
+                                                                float* __restrict__ lse, LseRest fix) {
+  using Form = PrefixMerge<kSlices, kHalf>;
+  using Vec = Vec8<kHalf>;
+  constexpr int kVec = Form::kVec, kHeads = Form::kHeads, kPer = Form::kPer, kC = 8 * kVec, kAhead = Form::kAhead;
   __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][2 + kC][kSlices > 1 ? kPer : 1];
   __shared__ float s_dot[kPer / 32][kHeads];
   ptx::griddep_wait();
@@ -1316,39 +1363,36 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
   Join<kC> a;
   a.start(slice == 0 && sink ? sink[h] * kLog2e : -INFINITY);
   // the epilogue's thread h + 64 (plane / 32) wrote vector plane % 32
-  const uint4* po = part_o + (plane & 31) * 128 + 64 * (plane >> 5) + h;
-  for (int c0 = slice; c0 < part.y; c0 += kSlices * kJoin) {
-    float2 ml[kJoin];
-    uint4 v[kJoin][kVec];
+  const uint4* po = part_o + (plane & 31) * Vec::kWords * 128 + 64 * (plane >> 5) + h;
+  for (int c0 = slice; c0 < part.y; c0 += kSlices * kAhead) {
+    float2 ml[kAhead];
+    Vec v[kAhead][kVec];
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       ml[i] = make_float2(-INFINITY, 0.0f);
       if (c0 + i * kSlices < part.y) {
         const int64_t slot = part.x + 2 * (int64_t)(c0 + i * kSlices);
         ml[i] = part_ml[slot * kHAtt + h];
 #pragma unroll
-        for (int u = 0; u < kVec; ++u) v[i][u] = po[(slot * 32 + u) * 128];
+        for (int u = 0; u < kVec; ++u) v[i][u].load(po + (slot * 32 + u) * Vec::kWords * 128);
       }
     }
     float top = a.ref;
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i)
+    for (int i = 0; i < kAhead; ++i)
       if (ml[i].y != 0.0f) top = fmaxf(top, ml[i].x);
     a.raise(top);
 #pragma unroll
-    for (int i = 0; i < kJoin; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       if (ml[i].y == 0.0f) continue;
       const float f = ptx::ex2(ml[i].x - a.ref) * ml[i].y;
       a.L += f;
 #pragma unroll
       for (int u = 0; u < kVec; ++u) {
-        const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+        float x[8];
+        v[i][u].get(x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-          a.acc[8 * u + 2 * j] = fmaf(f, x.x, a.acc[8 * u + 2 * j]);
-          a.acc[8 * u + 2 * j + 1] = fmaf(f, x.y, a.acc[8 * u + 2 * j + 1]);
-        }
+        for (int j = 0; j < 8; ++j) a.acc[8 * u + j] = fmaf(f, x[j], a.acc[8 * u + j]);
       }
     }
   }
@@ -1372,7 +1416,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
       for (int u = 0; u < kC; ++u) a.acc[u] = fmaf(f, s_join[i][2 + u][t], a.acc[u]);
     }
   }
-  const float inv = a.L > 0.0f ? 1.0f / a.L : 0.0f;
+  const float inv = a.L > 0.0f ? 1.0f / (Vec::kScale * a.L) : 0.0f;
 #pragma unroll
   for (int u = 0; u < kC; ++u) a.acc[u] *= inv;
   if (lse) {
@@ -1402,7 +1446,7 @@ __global__ void __launch_bounds__(PrefixMerge<kSlices>::kThreads) k_prefix_merge
 #pragma unroll
     for (int u = 0; u < kC / 2; ++u) rope_pair(a.acc[2 * u], a.acc[2 * u + 1], cs[u].x, -cs[u].y);
   }
-  store_channels<kC>(out, out_bf16, ((int64_t)b * kHAtt + h) * kDMain + 8 * plane, a.acc);
+  store_channels<kHalf>(out, ((int64_t)b * kHAtt + h) * kDMain + 8 * plane, a.acc);
 }
 
 // ------------------------------------------------------------ queries alone
@@ -1423,7 +1467,7 @@ struct __align__(1024) AloneSmem {
   uint16_t x[2][kDMain / 8][kRows * 8];  // rows [c/8][row][c%8]
   uint16_t q[kDMain / 8][kQPlane];       // q' [c/8][head][c%8]
   uint16_t p[2][kRows / 8][kHAtt * 8];   // probabilities [row/8][head][row%8]
-  float alpha[kHAtt];                    // factor of O when a head's reference moved; at the end 1 / l
+  __align__(16) float alpha[kHAtt];      // factor of O when a head's reference moved; at the end 1 / l (read four at a time)
   int32_t last_slot;                     // the last item's partial
   uint64_t last_o;                       // its O complete, 1 / l in alpha (four softmax warps)
   int32_t rows[kRing][kRows];
@@ -1487,8 +1531,9 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
   return good;
 }
 
-// Tiles' columns 32 c0 .. 32 c1 of O^T / l in f16, thread t's channels; uint4 (c, u) of thread t holds heads
-// 32 (c % 2) + 8 u .. of channel 128 (c / 2) + t, so that every store is 512 contiguous bytes.
+// Tiles' columns 32 c0 .. 32 c1 of O^T / l, thread t's channels; vector (c, u) of thread t holds heads
+// 32 (c % 2) + 8 u .. of channel 128 (c / 2) + t.  1 / l comes scaled (Vec8).
+template <bool kHalf>
 __device__ __forceinline__ void store_alone_o(const AloneSmem& S, const PrefixKernel& k, uint32_t tmem, int64_t slot, int t,
                                               int c0, int c1) {
 #pragma unroll 1
@@ -1496,22 +1541,18 @@ __device__ __forceinline__ void store_alone_o(const AloneSmem& S, const PrefixKe
     uint32_t a[32];
     ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(t & ~31) << 16) + 32u * (uint32_t)c, a);
     ptx::tmem_wait_ld();
-    uint4* po = k.part_o + (slot * 32 + 4 * c) * 128 + t;
+    uint4* po = k.part_o + (slot * 32 + 4 * c) * Vec8<kHalf>::kWords * 128 + t;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      uint32_t w[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float2 i2 = *reinterpret_cast<const float2*>(&S.alpha[32 * (c & 1) + 8 * u + 2 * v]);
-        const __half2 hh = __floats2half2_rn(__uint_as_float(a[8 * u + 2 * v]) * i2.x,
-                                             __uint_as_float(a[8 * u + 2 * v + 1]) * i2.y);
-        w[v] = *reinterpret_cast<const uint32_t*>(&hh);
-      }
-      po[u * 128] = make_uint4(w[0], w[1], w[2], w[3]);
+      const float4* i8 = reinterpret_cast<const float4*>(&S.alpha[32 * (c & 1) + 8 * u]);
+      const float4 f0 = i8[0], f1 = i8[1];
+      const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+      Vec8<kHalf>::store(po + u * Vec8<kHalf>::kWords * 128, [&](int i) { return __uint_as_float(a[8 * u + i]) * f[i]; });
     }
   }
 }
 
+template <bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ PrefixKernel k) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   AloneSmem& S = *reinterpret_cast<AloneSmem*>(smem_raw);
@@ -1579,7 +1620,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       if (good) {
         ptx::tc_fence_after();
         const int quarter = (warp - 4) / 4;
-        store_alone_o(S, k, tmem, S.last_slot, 32 * (warp % 4) + lane, 2 * quarter, 2 * quarter + 2);
+        store_alone_o<kHalf>(S, k, tmem, S.last_slot, 32 * (warp % 4) + lane, 2 * quarter, 2 * quarter + 2);
         ptx::tc_fence_before();
       }
     }
@@ -1693,7 +1734,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       ptx::tc_fence_after();
       open_l += __shfl_xor_sync(0xffffffffu, open_l, 16);
       if (rh == 0) {
-        S.alpha[h] = open_l > 0.0f ? 1.0f / open_l : 0.0f;
+        S.alpha[h] = open_l > 0.0f ? Vec8<kHalf>::kScale / open_l : 0.0f;
         k.part_ml[(int64_t)open_slot * kHAtt + h] = make_float2(open_m, open_l);
       }
       if (ends) {
@@ -1704,7 +1745,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         return;
       }
       softmax_sync();
-      store_alone_o(S, k, tmem, open_slot, tid, 0, 8);
+      store_alone_o<kHalf>(S, k, tmem, open_slot, tid, 0, 8);
       softmax_sync();  // alpha is written again
       ptx::tc_fence_before();
       __syncwarp();
@@ -1818,17 +1859,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // The join over partials of the epilogue's order: a CTA has eight heads 8 g .. and all channels, thread t of it
 // channel t; with four slices the 128 channels of a tile, and four CTAs (a cluster where the logsumexp wants all
 // channels) make the heads.  The weights 2^(m_i - m) l_i / L are the same for all channels: the CTA forms them
-// once, while the first partials' channels are on their way.  Without slices a query has few partials: four at
+// once, while the first partials' channels are on their way.  Without slices a query has few partials: four (fp32: two) at
 // once, which leaves room for three CTAs on an SM (eight and two: paged ragged 128 x 2000 49.9 us, now 47.9).
 constexpr int kMergeThreads = 512;
-template <int kSlices>
+template <int kSlices, bool kHalf>
 __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_merge(const int2* __restrict__ qpart,
                                                                const uint4* __restrict__ part_o,
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
-                                                               int out_bf16, float* lse, LseRest fix) {
-  constexpr int kAhead = kSlices > 1 ? kJoin : 4;  // partials on their way
+                                                               float* lse, LseRest fix) {
+  constexpr int kAhead = kSlices > 1 ? 8 : kHalf ? 4 : 2;  // partials on their way
   constexpr int kTiles = 4 / kSlices, kPer = 128 * kTiles;
   static_assert(kSlices == 1 || kTiles == 1, "all channels, or a tile of them");
   __shared__ __align__(16) float s_w[kAlone][8];  // read four at a time
@@ -1846,11 +1887,12 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
     s_m[i / 8][i % 8] = ml.y == 0.0f ? -INFINITY : ml.x;
     s_w[i / 8][i % 8] = ml.y;
   }
-  uint4 v[kAhead];
+  Vec8<kHalf> v[kAhead];
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (k0 + j * kSlices < part.y) v[j] = part_o[((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * 128 + (t & 127)];
+      if (k0 + j * kSlices < part.y)
+        v[j].load(part_o + ((int64_t)(part.x + k0 + j * kSlices) * 32 + y) * Vec8<kHalf>::kWords * 128 + (t & 127));
   };
   fetch(slice);
   __syncthreads();
@@ -1870,7 +1912,7 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (z != -INFINITY) L += ptx::ex2(z - ref);
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L > 0.0f ? 1.0f / (Vec8<kHalf>::kScale * L) : 0.0f;
     for (int j = lane; j < part.y; j += 32) s_w[j][i] *= inv;
     if (lse && (kSlices == 1 || tile == 0) && lane == 0)
       lse[b * kHAtt + h0 + i] = L == 0.0f ? -INFINITY : natural(ref, L);
@@ -1887,13 +1929,10 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
       if (k >= part.y) break;
       const float4 w0 = *reinterpret_cast<const float4*>(&s_w[k][0]), w1 = *reinterpret_cast<const float4*>(&s_w[k][4]);
       const float f[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      float x[8];
+      v[j].get(x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        acc[2 * i] = fmaf(f[2 * i], x.x, acc[2 * i]);
-        acc[2 * i + 1] = fmaf(f[2 * i + 1], x.y, acc[2 * i + 1]);
-      }
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(f[i], x[i], acc[i]);
     }
   }
   if (kSlices > 1) {
@@ -1938,7 +1977,7 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
       o = fmaf(o, cs, partner * sn);
     }
     const int64_t at = ((int64_t)b * kHAtt + h0 + i) * kDMain + c;
-    if (out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
+    if (kHalf) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(o);
     else static_cast<float*>(out)[at] = o;
   }
   if (kSlices > 1 && fix.rest) {
@@ -1988,7 +2027,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.c2 = (float*)take(((size_t)B + 1) * kHAtt * 4);
   L.rest = (uint16_t*)take((size_t)B * kHAtt * kDMain * 2);
   L.turn = (float2*)take((size_t)B * 32 * 8);
-  L.part_o = (uint4*)take(slots * kHAtt * kDMain * 2);
+  L.part_o = (uint4*)take(slots * kHAtt * kDMain * 4);  // room for fp32: the output's type is not known here
   L.part_ml = (float2*)take(slots * kHAtt * 8);
   L.image_cap = alone ? 0 : G * cdiv(shared_max, kChunk);
   if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
@@ -2087,43 +2126,45 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (L.image_cap > 0 &&
       (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
     return CSA2_ERR_CUDA;
-  const size_t smem = sizeof(PrefixSmem);
-  if (cudaFuncSetAttribute(k_prefix_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem) != cudaSuccess ||
-      (alone ? cudaFuncSetAttribute(k_paged_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AloneSmem))
-             : cudaFuncSetAttribute(k_prefix_attn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
-    return launch_status();
-  {
-    KernelTimer timer("k_prefix_prep", st);
-    const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
-    launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
-               (size_t)kPrepSmem, st, a, pq, k, L.image);
-  }
   const int slices = B < kSliceQueries ? 4 : 1;
   const float2* turn = ex.rope ? L.turn : nullptr;
-  const int out_bf16 = out_type == CSA2_OUT_BF16 ? 1 : 0;
   auto merge = [&](auto kern, unsigned ctas, unsigned threads, unsigned cluster) {
     launch_clusters(kern, dim3(B, ctas), dim3(threads), 1, cluster, 0, st, (const int2*)L.qpart,
-                    (const uint4*)L.part_o, (const float2*)L.part_ml, sink, turn, out, out_bf16, lse_out, fix);
+                    (const uint4*)L.part_o, (const float2*)L.part_ml, sink, turn, out, lse_out, fix);
   };
-  if (alone) {
+  auto run = [&](auto half) {  // parts in f16 for a bf16 output (Vec8)
+    constexpr bool kHalf = decltype(half)::value;
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(k_prefix_prep, attr, kPrepSmem) != cudaSuccess ||
+        (alone ? cudaFuncSetAttribute(k_paged_attn<kHalf>, attr, (int)sizeof(AloneSmem))
+               : cudaFuncSetAttribute(k_prefix_attn<kHalf>, attr, (int)sizeof(PrefixSmem))) != cudaSuccess)
+      return launch_status();
     {
-      KernelTimer timer("k_paged_attn", st);
-      launch_pdl(k_paged_attn, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
+      KernelTimer timer("k_prefix_prep", st);
+      const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
+      launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
+                 (size_t)kPrepSmem, st, a, pq, k, L.image);
     }
-    KernelTimer timer("k_paged_merge", st);
-    if (slices > 1) merge(k_paged_merge<4>, 32, kMergeThreads, rest ? 4 : 1);
-    else merge(k_paged_merge<1>, 8, kMergeThreads, 1);
+    if (alone) {
+      {
+        KernelTimer timer("k_paged_attn", st);
+        launch_pdl(k_paged_attn<kHalf>, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
+      }
+      KernelTimer timer("k_paged_merge", st);
+      if (slices > 1) merge(k_paged_merge<4, kHalf>, 32, kMergeThreads, rest ? 4 : 1);
+      else merge(k_paged_merge<1, kHalf>, 8, kMergeThreads, 1);
+      return launch_status();
+    }
+    {
+      KernelTimer timer("k_prefix_attn", st);
+      launch_clusters(k_prefix_attn<kHalf>, dim3(2 * kClusters), dim3(kThreads), 2, 1, sizeof(PrefixSmem), st, k, maps);
+    }
+    KernelTimer timer("k_prefix_merge", st);
+    if (slices > 1) merge(k_prefix_merge<4, kHalf>, 32, PrefixMerge<4, kHalf>::kThreads, 1);
+    else merge(k_prefix_merge<1, kHalf>, 8, PrefixMerge<1, kHalf>::kThreads, 1);
     return launch_status();
-  }
-  {
-    KernelTimer timer("k_prefix_attn", st);
-    launch_clusters(k_prefix_attn, dim3(2 * kClusters), dim3(kThreads), 2, 1, smem, st, k, maps);
-  }
-  KernelTimer timer("k_prefix_merge", st);
-  if (slices > 1) merge(k_prefix_merge<4>, 32, PrefixMerge<4>::kThreads, 1);
-  else merge(k_prefix_merge<1>, 8, PrefixMerge<1>::kThreads, 1);
-  return launch_status();
+  };
+  return out_type == CSA2_OUT_BF16 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace

@@ -482,11 +482,11 @@ typedef enum { CSA2_OUT_F32 = 0, CSA2_OUT_BF16 = 1 } csa2_out_type;
  * entries that exist.  A page id outside [0, n_pages) is reported as CSA2_ERR_INDEX_RANGE and its
  * entries are skipped.  A NaN in an entry or a window row reaches the queries that see it, no others.
  * Rounded to f16 (by at most 2^-11): probabilities, for the tensor cores (and a row by at most 2^-36 of the
- * weight of the strongest), and the outputs of the parts of a query, which are joined in fp32; a normalised
- * or rotated q, whose effect on the logsumexp is corrected to the second order.  Sums and the logsumexp are
- * kept in fp32.  The same call gives the same bits again.  Every other argument as in csa2_dense_attn_decode;
- * the workspace is
- * csa2_paged_attn_workspace_size(B, n_max, n_swa) bytes (192 KB a query and 10 MB). */
+ * weight of the strongest); a normalised or rotated q, whose effect on the logsumexp is corrected to the
+ * second order; and, for a bf16 output, the outputs of the parts that a query is cut into (or by 2^-29),
+ * which are joined in fp32.  With an fp32 output those stay fp32; sums and the logsumexp always do.  The
+ * same call gives the same bits again.  Every other argument as in csa2_dense_attn_decode; the workspace is
+ * csa2_paged_attn_workspace_size(B, n_max, n_swa) bytes (256 KB a query and 20 MB). */
 csa2_status csa2_paged_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                    const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3, int32_t n_swa,
                                    const void* q_bf16, float softmax_scale, const csa2_norm_rope* q_nr,
