@@ -312,9 +312,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
 // ------------------------------------------------------------------ attention
 
 // warps 0-3: softmax, rescaling of O, epilogue; 4-11: rows of S's operand; 12-19: rows of O's; then one
-// warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), where rows come from
+// warp each: S MMAs, O MMAs (even CTA; in the odd one they pass arrivals on), where rows come from; the last one passes
+// P's arrivals on (odd CTA)
 constexpr int kRowWarp = 4, kSMma = 20, kOMma = 21, kIndexWarp = 22;
-constexpr int kThreads = 24 * 32;  // and one that fills the last warpgroup
+constexpr int kThreads = 24 * 32;
 // registers of a thread: 80 at launch, which the last warpgroup keeps; the softmax takes what the row
 // warpgroups give back
 constexpr int kSoftRegs = 104, kRowRegs = 72;
@@ -332,11 +333,12 @@ struct __align__(1024) PrefixSmem {
   float red[2][kHAtt];                      // of the two threads of a head; at the end their sums of p
   int32_t rows[4][kChunk];                  // where a chunk's rows come from, up to four chunks ahead
   int32_t image[4];                         // its chunk of the image, or -1
-  // what the MMA warps wait on counts the even CTA's own warps and one arrival that the odd CTA's warp
-  // of the same role passes on for all of that CTA's
-  uint64_t q_land, q_peer;                  // q' copied; the odd CTA's q'
+  // what the MMA warps wait on counts the even CTA's own warps and one arrival that a warp of the odd CTA
+  // passes on for all of that CTA's
+  uint64_t q_land, q_peer, q_free;          // q' copied; the odd CTA's q'; S of an item's chunks complete
   uint64_t i_full[4], r_full[4], r_free[4]; // image, rows written (one warp); read (16 row and 4 softmax warps)
   uint64_t x_full[2][kPieces], x_free[2][kPieces];  // [0] S's operand, [1] O's
+  uint64_t x_go[2][kPieces];                // the piece is free, where rows are written (see rows_role)
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_read;                          // epilogue done with O
   uint64_t drained;                         // every MMA issued complete (two warps)
@@ -546,6 +548,16 @@ __device__ __forceinline__ float probs32(uint64_t (&s)[16], uint32_t mask, float
   return top;
 }
 
+// Copies piece i of operand op from a chunk of the image to this CTA; its bytes count on the even CTA's barrier, whose
+// MMA warps read both CTAs'.
+constexpr int kPieceBytes = 16 * 1024;
+__device__ __forceinline__ void copy_piece(PrefixSmem& S, const ImageMaps& maps, int op, int rank, int i, int image) {
+  const int plane0 = image * (kDMain / 8);
+  uint64_t* const bar = &S.x_full[op][i];
+  if (op) ptx::tma_load_2d_pair(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, bar, 0);
+  else ptx::tma_load_2d_pair(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, bar, 0);
+}
+
 // The operands of all `chunks` chunks of this pair of CTAs, whatever items they belong to, by the 16 row
 // warps: per operand two groups of four, which write every other piece.  Operand 0 (S's, warps 0-7): this
 // CTA's 64 rows, handed over by 128 channels: in piece i a thread has one of the blocks (of 32 channels) 4 i .. of
@@ -553,11 +565,15 @@ __device__ __forceinline__ float probs32(uint64_t (&s)[16], uint32_t mask, float
 // has two of its eight blocks, four apart, of row 32 i + 8 (w % 4) + l % 8.  Either way a load reads 64
 // contiguous bytes of eight rows, and a store writes eight rows of a plane: no bank conflicts.  A step writes
 // one piece and fetches the codes of the next (half a chunk ahead); a chunk of the image is copied instead,
-// by the first warp of each group.  Both operands run the same code: the kernel's loops have to fit the
-// instruction cache (unrolled by piece and operand they waited more for instructions than for data).
+// by the first warp of each group, and its bytes count on the even CTA's barrier (x_full).  Only that warp waits for
+// x_free; the others go by its x_go, of which rows alone have phases: a warp that takes no part in a copy could miss
+// one of x_free.  The odd CTA's x_full too has phases of rows alone, which are passed on.  Both operands run the same code: the
+// kernel's loops have to fit the instruction cache (unrolled by piece and operand they waited more for instructions
+// than for data).
 __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int rank,
                                           int chunks, int w, int lane) {
   const int op = w >> 3, group = (w >> 2) & 1;
+  const bool lead = (w & 3) == 0;
   const int rl = 8 * (w & 3) + (lane & 7);
   const int row0 = op ? rl : kOwnChunk * rank + rl, row_step = op ? 32 : 0, row_u = op ? 0 : 32;
   const int b = rotated(lane) & (op ? 7 : 3);
@@ -570,6 +586,7 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   int r[2], image = -1;
   Fetch f[2];
   int issued = -1;  // last step copied from the image
+  uint32_t owns = 0;  // chunks not copied before this one
   bool good = true;
   auto load = [&](int st) {  // this thread's rows and codes of step st
     if (st >= steps) return;
@@ -599,33 +616,37 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
   for (int st = 0; st < steps && good; ++st) {
     const uint32_t m = (uint32_t)(st >> 1);
     const int i = 2 * (st & 1) + group;
-    if (m > 0) good = ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
-    if (!good) break;
+    if (lead && m > 0) good = ptx::mbar_wait_warp(&S.x_free[op][i], (m - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (image >= 0) {
-      // every warp arrives, also those that copy nothing: none may miss a phase of x_free
-      if ((w & 3) != 0) {
-        if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
-      } else if (lane == 0) {
-        const int plane0 = image * (kDMain / 8);
-        ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 16 * 1024);
-        if (op) ptx::tma_load_2d(&S.xo[i][0][0], &maps.o, 128 * i, plane0 + 32 * rank, &S.x_full[op][i]);
-        else ptx::tma_load_2d(&S.xs[16 * i][0], &maps.s, 256 * rank, plane0 + 16 * i, &S.x_full[op][i]);
+      if (!good) break;
+      if (lead) {
+        if (rank == 0 && lane < 4) ptx::mbar_arrive(&S.x_full[op][i]);  // for the others, and the odd CTA
+        if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&S.x_full[op][i], 2 * kPieceBytes);
+        if (lane == 0) copy_piece(S, maps, op, rank, i, image);
+        issued = st;
+        __syncwarp();
       }
-      issued = st;
-      __syncwarp();
     } else {
+      if (!lead) good = ptx::mbar_wait_warp(&S.x_go[op][i], owns & 1u, &S.abort_flag, kWaitBudget);
+      if (!good) break;
+      if (lead && lane == 0) ptx::mbar_arrive(&S.x_go[op][i]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) put(f[u], r[u], dst + i * dst_step + u * dst_u, plane, op ? kFinite : kAnyValue);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.x_full[op][i]);
+      if (st & 1) ++owns;
     }
     load(st + 1);
   }
-  if (!good && (w & 3) == 0) {  // copies in flight write shared memory: they land before anyone leaves
+  // copies in flight write shared memory: they land before anyone leaves (the odd CTA sees it by the MMAs behind
+  // them, or the limit)
+  if (!good && lead) {
     volatile int keep_waiting = 0;
-    for (int st = issued; st >= 0 && st > issued - 2; --st)
-      ptx::mbar_wait_warp(&S.x_full[op][2 * (st & 1) + group], (uint32_t)(st >> 1) & 1u, &keep_waiting, kWaitBudget);
+    for (int st = issued; st >= 0 && st > issued - 2; --st) {
+      uint64_t* const landed = (rank ? S.x_free : S.x_full)[op] + 2 * (st & 1) + group;
+      ptx::mbar_wait_warp(landed, (uint32_t)(st >> 1) & 1u, &keep_waiting, kWaitBudget);
+    }
   }
   return good;
 }
@@ -645,6 +666,13 @@ __device__ __forceinline__ void prefetch_row(const PrefixKernel& k, int r) {
   }
 }
 
+// Whether chunk c of a pair is copied from the image, which serves both operands: only where both queries see all of
+// the chunk's entries.
+__device__ __forceinline__ bool from_image(const Pair& x, int c) {
+  const int seen = x.q1 >= 0 ? min(x.vis0, x.vis1) : x.vis0;
+  return x.image >= 0 && c < x.nshared && min((c + 1) * kChunk, x.ns) <= seen;
+}
+
 // Where each chunk's rows come from (or its chunk of the image), by one warp (lane l rows l, 32 + l, ..) up to
 // four chunks ahead of the row and softmax warps.  Pages outside the planes are reported here.
 __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, int rank, int c0,
@@ -657,17 +685,13 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
     for (int i = 0; i < 4; ++i) r[i] = find_row(k, x, c0 + j, 32 * i + lane);
   };
   find(0);
-  // the image serves both operands: only where both queries see all of a chunk's entries
-  const int seen = x.q1 >= 0 ? min(x.vis0, x.vis1) : x.vis0;
 #pragma unroll 1
   for (int j = 0; j < nc && good; ++j) {
     const uint32_t m = n + (uint32_t)j, slot = m & 3u;
     if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) break;
     if (lane == 0) {
-      S.image[slot] = x.image >= 0 && c0 + j < x.nshared && min((c0 + j + 1) * kChunk, x.ns) <= seen
-                          ? x.image + c0 + j
-                          : -1;
+      S.image[slot] = from_image(x, c0 + j) ? x.image + c0 + j : -1;
       ptx::mbar_arrive(&S.i_full[slot]);
     }
     int row[4];
@@ -766,9 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       ptx::mbar_init(&S.q_peer, 1);
       for (int i = 0; i < 2 * kPieces; ++i) {
         ptx::mbar_init(&S.x_full[0][0] + i, 4 + peer);
+        ptx::mbar_init(&S.x_go[0][0] + i, 1);
         ptx::mbar_init(&S.x_free[0][0] + i, 1);
       }
       ptx::mbar_init(&S.q_land, 1);
+      ptx::mbar_init(&S.q_free, 1);
       for (int i = 0; i < 4; ++i) {
         ptx::mbar_init(&S.i_full[i], 1);
         ptx::mbar_init(&S.r_full[i], 1);
@@ -837,12 +863,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     }
     where = 31;
   } else if (warp >= kSMma) {
-    // the odd CTA's MMA warps pass their CTA's arrivals on, in the order the even CTA's wait for them
-    auto pass = [&](uint64_t* bar, uint32_t ph) {
-      if (good) good = wait(bar, ph);
+    // The odd CTA's MMA warps pass their CTA's arrivals on (and the last warp P's), released here and taken by the even
+    // CTA's at cluster scope: the MMAs that read this CTA's rows, P and tensor memory are issued there.
+    // Every release waits (ptx.cuh), hence two pieces of rows to one, and copies that count on the even CTA's
+    // barriers by themselves: 64 on 65000 takes 405 us, with a release for every piece and copy 733 (at CTA scope,
+    // which orders nothing between two CTAs, 370).
+    auto wait_pair = [&](uint64_t* bar, uint32_t n) {
+      return ptx::mbar_wait_warp<true>(bar, n & 1u, abort_flag, kWaitBudget);
+    };
+    auto pass = [&](uint64_t* bar, uint32_t ph, int n) {  // n neighbouring barriers
+      for (int i = 0; i < n; ++i) good = good && wait(bar + i, ph);
       ptx::tc_fence_after();  // the softmax's tensor-memory stores are among what is passed on
       ptx::tc_fence_before();
-      if (good && lane == 0) ptx::mbar_arrive_peer(bar, 0);
+      if (good && lane < n) ptx::mbar_arrive_peer(bar + lane, 0);
+      __syncwarp();
+    };
+    // the pair's chunk c, unless it was copied: by the chunks of rows before it
+    uint32_t owns = 0;
+    auto pass_rows = [&](int op, const Pair& x, int c) {
+      if (from_image(x, c)) return;
+      for (int i = 0; i < kPieces; i += 2) pass(&S.x_full[op][i], owns, 2);
+      ++owns;
     };
     if (warp == kIndexWarp) {
       for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
@@ -854,9 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       constexpr uint32_t idesc_s = ptx::idesc_f16(128, kChunk, 0);
       const uint64_t da = ptx::smem_desc_noswizzle(&S.q[0][0], kQPlane * 2, 128);
       const uint64_t db = ptx::smem_desc_noswizzle(&S.xs[0][0], kOwnChunk * 16, 128);
-      for_items([&](const Pair& x, int, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
         // the item's query, once S of the item before has left q'; the copy lands before anyone leaves
-        good = n == 0 || wait(&S.s_full[(n - 1) & 1u], (n - 1) >> 1);
+        good = items == 0 || wait(&S.q_free, items - 1);
         if (!good) return;
         if (lane == 0) {
           const int64_t q = rank == 0 ? x.q0 : x.q1 >= 0 ? x.q1 : k.B;
@@ -866,29 +907,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         __syncwarp();
         volatile int keep_waiting = 0;
         good = ptx::mbar_wait_warp(&S.q_land, items & 1u, &keep_waiting, kWaitBudget);
-        if (rank == 0) good = good && wait(&S.q_peer, items);
+        if (rank == 0) good = good && wait_pair(&S.q_peer, items);
         else if (good && lane == 0) ptx::mbar_arrive_peer(&S.q_peer, 0);
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j;
+          if (rank) {
+            pass_rows(0, x, c0 + j);
+            continue;
+          }
           // the softmax of both CTAs has left this S buffer
-          if (rank == 0 && m >= 2) good = wait(&S.p_full[m & 1], (m >> 1) - 1);
+          if (m >= 2) good = wait_pair(&S.p_full[m & 1], (m >> 1) - 1);
           const uint32_t dst = tmem + kColS + 64u * (m & 1u);
 #pragma unroll 1
           for (int i = 0; i < kPieces && good; ++i) {
-            if (rank) {
-              pass(&S.x_full[0][i], m);
-              continue;
-            }
-            good = wait(&S.x_full[0][i], m);
+            good = wait_pair(&S.x_full[0][i], m);
             if (!good) break;
             ptx::tc_fence_after();
             const uint64_t at = (uint64_t)(i * 1024);  // q'[16 i], xs[16 i]: 16 KB on; a K step 2 KB
             ptx::mma_f16_ss_pair_run_elect<8, 128, 128>(dst, da + at, db + at, idesc_s, i > 0 ? 1u : 0u);
             ptx::mma_commit_pair_elect(&S.x_free[0][i]);
           }
-          if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
+          if (good) ptx::mma_commit_pair_elect(&S.s_full[m & 1]);
         }
+        // a barrier of its own: the odd CTA's warp does not follow the chunks, whose phases it would miss
+        if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.q_free);
       });
       where = 33;
     } else if (warp == kOMma) {
@@ -896,25 +939,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       constexpr uint32_t idesc_o = ptx::idesc_f16(128, 256, 0) | ptx::kIdescBMajorMN;
       const uint64_t dp = ptx::smem_desc_noswizzle(&S.p[0][0][0], kHAtt * 16, 128);
       const uint64_t dx = ptx::smem_desc_noswizzle(&S.xo[0][0][0], 128, 512);
-      for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
+      for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t items) {
 #pragma unroll 1
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j;
           if (rank) {
-            pass(&S.p_full[m & 1], m >> 1);
-            if (j == 0 && items > 0) pass(&S.o_read, items - 1);
-          } else {
-            good = wait(&S.p_full[m & 1], m >> 1);
-            if (good && j == 0 && items > 0) good = wait(&S.o_read, items - 1);
+            pass_rows(1, x, c0 + j);
+            continue;
           }
+          good = wait_pair(&S.p_full[m & 1], m >> 1);
+          if (good && j == 0 && items > 0) good = wait_pair(&S.o_read, items - 1);
           const uint64_t dpo = dp + (uint64_t)((m & 1u) * (kChunk / 8 * kHAtt * 16 / 16));
 #pragma unroll 1
           for (int i = 0; i < kPieces && good; ++i) {
-            if (rank) {
-              pass(&S.x_full[1][i], m);
-              continue;
-            }
-            good = wait(&S.x_full[1][i], m);
+            good = wait_pair(&S.x_full[1][i], m);
             if (!good) break;
             ptx::tc_fence_after();
             // p[4 i ..]: 2 KB a K step; xo[i], rows 16 ks: 256 bytes a step
@@ -925,10 +963,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
                                                          (j | i) > 0 ? 1u : 0u);
             ptx::mma_commit_pair_elect(&S.x_free[1][i]);
           }
-          if (rank == 0 && good) ptx::mma_commit_pair_elect(&S.p_free[m & 1]);
+          if (good) ptx::mma_commit_pair_elect(&S.p_free[m & 1]);
         }
       });
       where = 34;
+    } else if (rank) {  // P, and O read
+      for_items([&](const Pair&, int, int, int nc, uint32_t n, uint32_t items) {
+#pragma unroll 1
+        for (int j = 0; j < nc && good; ++j) {
+          const uint32_t m = n + (uint32_t)j;
+          pass(&S.p_full[m & 1], m >> 1, 1);
+          if (j == 0 && items > 0) pass(&S.o_read, items - 1, 1);
+        }
+      });
+      where = 36;
     }
   } else {
     // ---- softmax: thread t head t % 64, chunk rows 64 (t / 64) ..

@@ -32,42 +32,54 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
+// kCluster: what threads of the cluster's other CTAs released at cluster scope is seen too.
+#define CSA2_TRY_WAIT(SCOPE)                                                                   \
+  asm volatile(                                                                                \
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire." SCOPE                          \
+      ".shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"                            \
+      : "=r"(ok)                                                                               \
+      : "r"(smem_u32(bar)), "r"(parity)                                                        \
+      : "memory")
+#define CSA2_TRY_WAIT_NS(SCOPE)                                                                \
+  asm volatile(                                                                                \
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire." SCOPE                          \
+      ".shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"                        \
+      : "=r"(ok)                                                                               \
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)                                               \
+      : "memory")
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kCluster) CSA2_TRY_WAIT("cluster");
+  else CSA2_TRY_WAIT("cta");
   return ok != 0;
 }
 
 // try_wait that lets the hardware suspend the thread for up to `ns` nanoseconds
 // (or until the phase completes) instead of returning at once, so waiting warps
 // do not spend issue slots polling.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
+  if constexpr (kCluster) CSA2_TRY_WAIT_NS("cluster");
+  else CSA2_TRY_WAIT_NS("cta");
   return ok != 0;
 }
+#undef CSA2_TRY_WAIT
+#undef CSA2_TRY_WAIT_NS
 
 // Waits for the phase of `parity` to complete.  Gives up (returns false) when
 // *abort becomes nonzero or after `budget` clock cycles.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           long long budget) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait<kCluster>(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
 #if CSA2_WAIT_SLEEP_NS > 0
-    if (mbar_try_wait_sleep(bar, parity, CSA2_WAIT_SLEEP_NS)) return true;
+    if (mbar_try_wait_sleep<kCluster>(bar, parity, CSA2_WAIT_SLEEP_NS)) return true;
 #else
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<kCluster>(bar, parity)) return true;
 #endif
     if (*abort) return false;
     if (clock64() - t0 > budget) return false;
@@ -76,9 +88,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // Warp-uniform form for warps that go on to issue .sync.aligned instructions:
 // every lane waits, and the warp gives up together if any lane gave up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                long long budget) {
-  const bool ok = mbar_wait(bar, parity, abort, budget);
+  const bool ok = mbar_wait<kCluster>(bar, parity, abort, budget);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -427,15 +440,23 @@ __device__ __forceinline__ void st_cluster_f32(const float* p, uint32_t rank, fl
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on the barrier at the same shared-memory offset of the cluster's CTA `rank`.  The arrival has CTA
-// scope: it tells the other CTA's MMA warp that operands in THIS CTA's shared and tensor memory are ready,
-// which that warp never reads itself -- the pair's MMA reads them here, after the proxy fence and the
-// CTA-scope release of their writers.  (With .release.cluster each arrival waited about 1,400 cycles for
-// the thread's memory operations everywhere.)
+// tma_load_2d into this CTA of a pair, whose bytes are counted by the barrier at the same offset of CTA `rank`.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst_smem, const void* map, int c0, int c1, uint64_t* bar,
+                                                 uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3}], [a];\n\t}" ::"r"(smem_u32(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "r"(rank)
+      : "memory");
+}
+// Arrives on the barrier at the same shared-memory offset of the cluster's CTA `rank`, whose waiter takes it with
+// mbar_wait_warp<true>: what this thread has seen or written before is seen after the wait.  The release waits some
+// 1,400 cycles, so a pair's barriers get few of these, from warps that have nothing else to do.
 __device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.release.cta.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
