@@ -272,7 +272,7 @@ def cache_append_workspace_size(G: int, d_model: int, m: int) -> int:
 def cache_append(H, G: int, d_model: int, Wkv, Wz, Wik, m: int, planes: Planes, n_slots: int, slot, entry,
                  ws, kv_nr: NormRope | None = None, pos=None, stream=None) -> None:
     """Decode-time append: G groups of m tokens (H bf16 [G][m][d_model]); entry g goes to slot
-    slot[g], index entry[g] (device int32 / int64 arrays), at position pos[g] with RoPE."""
+    slot[g], index entry[g] (device int32 / int64 arrays; -1 in both: skipped), at position pos[g] with RoPE."""
     _ok(lib().csa2_cache_append(_ptr(H), G, d_model, _ptr(Wkv), _ptr(Wz), _ptr(Wik), m,
                                 ctypes.byref(planes.c), n_slots, _ptr(slot), _ptr(entry),
                                 ctypes.byref(kv_nr) if kv_nr is not None else None, _ptr(pos), _ptr(ws),

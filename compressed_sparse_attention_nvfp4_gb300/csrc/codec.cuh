@@ -152,11 +152,13 @@ struct QDest {
 
 // Entry e of a quantize launch goes to plane row dest_row(d, e): contiguous rows
 // e0 + e, or (scattered) slot[e] * stride + entry[e], skipped and reported when
-// outside the planes.
+// outside the planes.  Slot -1 with entry -1, the padding of a slot map, is
+// skipped without a report: a step of fixed size would leave one every time.
 __device__ __forceinline__ int64_t dest_row(const QDest& d, int64_t e) {
   if (!d.slot) return d.e0 + e;
   const int32_t sl = d.slot[e];
   const int64_t en = d.entry[e];
+  if (sl == -1 && en == -1) return -1;
   if (sl < 0 || sl >= d.n_slots || en < 0 || en >= d.stride) {
     if (d.ws) report_error(d.ws, CSA2_ERR_INDEX_RANGE, sl < 0 || sl >= d.n_slots ? (long long)sl : en);
     return -1;

@@ -170,7 +170,8 @@ size_t csa2_cache_write_workspace_size(int64_t T, int32_t d_model, int32_t m);
  *   H [G][m][d_model] bf16, the group's tokens in order;
  *   entry g goes to slot slot[g] (< n_slots), entry index entry[g] (< seq_stride) --
  *   a destination outside the planes is skipped and reported as CSA2_ERR_INDEX_RANGE
- *   through the workspace error word;
+ *   through the workspace error word; slot -1 with entry -1 (the padding rows of
+ *   csa2_page_tables) is skipped without a report;
  *   kv_nr (or NULL) as in csa2_cache_write, entry g at position pos[g] (required with
  *   RoPE).  slot, entry, pos are device arrays. */
 csa2_status csa2_cache_append(const void* H_bf16, int32_t G, int32_t d_model, const void* Wkv_bf16,
