@@ -281,7 +281,8 @@ def cache_append(H, G: int, d_model: int, Wkv, Wz, Wik, m: int, planes: Planes, 
 
 def swa_append(x, R: int, pos, n_queries: int, ring, n_win: int, query=None, nr: NormRope | None = None,
                stream=None, ring_pos=None) -> None:
-    """Window ring write: row r of x (fp32 [R][512]) -> E4M3 into ring[query[r] or r][pos[r] % n_win];
+    """Window ring write: row r of x (fp32 [R][512]) -> E4M3 into ring[query[r] or r][pos[r] % n_win]; of more
+    than n_win rows of a query, at consecutive positions, the last n_win;
     ring_pos (int64 [n_queries][n_win], optional) records the rows' positions."""
     _ok(lib().csa2_swa_append(_ptr(x), R, _ptr(query), _ptr(pos), n_queries,
                               ctypes.byref(nr) if nr is not None else None, _ptr(ring), _ptr(ring_pos), n_win,

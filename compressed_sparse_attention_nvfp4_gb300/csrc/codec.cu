@@ -148,7 +148,9 @@ __global__ void k_quantize_query_mxfp4(const uint16_t* __restrict__ q, int64_t n
 // Window ring write: one warp per row; lane l holds channels 16l .. 16l + 15,
 // optional RMSNorm and RoPE (pairs in lanes 28-31), then E4M3 (nearest even,
 // saturating, no scale) into ring[query][pos mod n_win].  Rows with a negative
-// position or a query outside [0, n_queries) are skipped.
+// position or a query outside [0, n_queries) are skipped, and so is a row whose
+// place the row n_win behind it takes (the same query, n_win positions on): of more
+// rows than the ring has the last are kept, whatever order the warps run in.
 __global__ void k_swa_append(const float* __restrict__ x, int32_t R, const int32_t* __restrict__ query,
                              const int64_t* __restrict__ pos, int32_t n_queries, const float* __restrict__ w,
                              float eps, int rope, RopeTheta th, uint8_t* __restrict__ ring,
@@ -159,6 +161,7 @@ __global__ void k_swa_append(const float* __restrict__ x, int32_t R, const int32
   const int64_t p = pos[r];
   const int32_t b = query ? query[r] : (int32_t)r;
   if (p < 0 || b < 0 || b >= n_queries) return;  // the same for the whole warp
+  if (query && r + n_win < R && query[r + n_win] == b && pos[r + n_win] == p + n_win) return;
   float v[16];
   const float4* src = reinterpret_cast<const float4*>(x + r * kDMain + lane * 16);
 #pragma unroll

@@ -187,7 +187,10 @@ size_t csa2_cache_append_workspace_size(int32_t G, int32_t d_model, int32_t m);
  * query query[r] (query == NULL: query r), optionally normalised / rotated by nr at
  * pos[r], is encoded as E4M3 (nearest even, saturating at +-448, no scale) into
  * ring[query][pos mod n_win][512] (ring: [n_queries][n_win][512] bytes).  Rows with a
- * negative position or a query outside [0, n_queries) are skipped.  The ring is the
+ * negative position or a query outside [0, n_queries) are skipped.  A query's rows may
+ * be more than n_win where they stand one behind another at ascending positions without
+ * a gap (a prefill's): the last n_win are kept.  Two rows of a call that meet in one
+ * place of the ring in any other way leave either, or parts of both.  The ring is the
  * swa_e4m3 input of csa2_sparse_attn_decode (n_swa = the rows written so far, at most
  * n_win): the attention does not depend on the order of its rows.  ring_pos (or NULL),
  * [n_queries][n_win] int64, receives each written row's position: the row positions of

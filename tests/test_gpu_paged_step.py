@@ -46,3 +46,27 @@ def test_padded_rows_are_skipped_without_a_report(m):
     for s, e, detail in ((-1, 3, -1), (1, -1, -1), (-2, -1, -2), (3, 0, 3), (0, P, P)):
         slots[3], entries[3] = s, e
         assert append(slots, entries)[0] == (6, detail)
+
+
+@pytest.mark.parametrize("n_win", [8, 128])
+@pytest.mark.parametrize("nr", [False, True])
+def test_of_more_rows_than_the_ring_the_last_are_kept(n_win, nr):
+    # chunks of a prefill: several times the ring, once as many rows, fewer, and none; padding behind them
+    count, first = [5 * n_win + 3, n_win, 3, 0, n_win + 1], [1000, 17, n_win - 1, 0, 1 << 33]
+    query = np.concatenate([np.full(c, b) for b, c in enumerate(count)] + [[-1] * 2]).astype(np.int32)
+    pos = np.concatenate([f + np.arange(c) for f, c in zip(first, count)] + [[-1] * 2]).astype(np.int64)
+    R, B = len(pos), len(count)
+    x = to_dev(np.random.default_rng(n_win).standard_normal((R, 512)).astype(np.float32))
+    kw = dict(nr=csa2.norm_rope(None, 1e-6, True)) if nr else {}
+    last = np.concatenate([np.flatnonzero(query == b)[-n_win:] for b in range(B)])
+    rings = []
+    for rows in (np.arange(R), last):  # all rows, and the last ones alone
+        ring = torch.full((B, n_win, 512), 0xA5, dtype=torch.uint8, device="cuda")
+        at = torch.full((B, n_win), -1, dtype=torch.int64, device="cuda")
+        csa2.swa_append(x[torch.from_numpy(rows).cuda()], len(rows), to_dev(pos[rows]), B, ring, n_win,
+                        query=to_dev(query[rows]), ring_pos=at, **kw)
+        rings.append((ring, at))
+    assert torch.equal(rings[0][0], rings[1][0]) and torch.equal(rings[0][1], rings[1][1])
+    for b in range(B):
+        kept = set(range(first[b] + max(count[b] - n_win, 0), first[b] + count[b]))
+        assert set(rings[0][1][b].tolist()) - {-1} == kept
