@@ -411,8 +411,10 @@ def page_tables(B: int, n_have, n_new, page_entries: int, table, max_pages: int,
                 n_free_out, n_entries, ws, n_rows: int = 0, query=None, slot=None, entry=None, pos=None,
                 row_start=None, m: int = 1, n_kept=None, stream=None) -> None:
     """Extends (n_new >= 0) or shortens (n_new < 0) every request's pages and fills the map of the new
-    entries: query, slot (page), entry (index in the page) and pos per map row, as cache_append takes
-    them, -1 behind the last; n_free_out may be n_free and n_entries n_have (csa2_page_tables)."""
+    entries: query, slot (page), entry (index in the page) and pos per map row, as cache_append (and with
+    m = 1 swa_append) takes them, -1 behind the last; n_free_out may be n_free and n_entries n_have.
+    n_kept: leading full pages that are never given back; entries that grow into one after a drop are the
+    caller's to keep out, and so are a window's rows of dropped tokens (csa2_page_tables)."""
     _ok(lib().csa2_page_tables(B, _ptr(n_have), _ptr(n_new), page_entries, m, _ptr(n_kept), _ptr(table), max_pages,
                                n_pages, _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(n_entries), n_rows,
                                _ptr(query), _ptr(slot), _ptr(entry), _ptr(pos), _ptr(row_start), _ptr(ws),

@@ -444,13 +444,21 @@ size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  *              may be taken by another request in the same call.  Elements below n_free[0]
  *              stay as they are
  *   n_kept     [B] or NULL: leading pages of row b that belong to someone else as well (a
- *              shared prefix) and are never given back
+ *              shared prefix) and are never given back.  It does not keep entries out of them:
+ *              new entries go to n_have[b] and behind, whatever page that is in.  So only
+ *              pages that are full count, and a request that has dropped entries of a kept
+ *              page gets a page of its own in its place (a free id in that table element,
+ *              the entries below n_have[b] copied) and a lower n_kept before it grows
  *   n_free_out [1], n_entries [B]  the new values (n_have[b] + n_new[b]); each may be the input
  *              it follows, for a step replayed from a CUDA graph
  *   row_*      [n_rows], each optional: one row per new entry, in order of request and entry:
- *              request, page, index in the page, and position (entry index * m, the position of
- *              csa2_cache_append's and csa2_swa_append's pos for m tokens per entry).  Rows behind
- *              the last new entry are -1
+ *              request, page, index in the page, and position (entry index * m, as
+ *              csa2_cache_append's pos for m tokens per entry).  Rows behind the last new entry
+ *              are -1, which both appends skip.  With m = 1 query and position are those of
+ *              csa2_swa_append's rows as well; with m > 1 a window row is due for every token,
+ *              m for a row of this map.  A drop takes nothing out of a window: its rows at
+ *              positions of dropped tokens stay visible until ring_pos is set to -1 there (or
+ *              new tokens take their places), and rows that they had displaced are gone
  *   row_start  [B + 1] optional: first map row of each request, and their number
  * All or nothing: when a length is negative or beyond max_pages * page_entries (or 2^31 - 1), the
  * new entries exceed n_rows (with any row_* given), n_free or a page id that would move lies
