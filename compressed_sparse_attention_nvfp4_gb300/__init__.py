@@ -422,13 +422,24 @@ def page_tables(B: int, n_have, n_new, page_entries: int, table, max_pages: int,
 
 
 def _out_type(out, out_type: int | None) -> int:
-    """OUT_F32 / OUT_BF16 of a tensor (a raw pointer's type has to be given)."""
+    """OUT_F32 / OUT_BF16 of a tensor, fp32 where it has no dtype."""
     if out_type is not None:
         return out_type
     name = str(getattr(out, "dtype", "torch.float32"))
     if name not in ("torch.float32", "torch.bfloat16"):
         raise Csa2Error(1, f"attention output of type {name}")
     return OUT_BF16 if name == "torch.bfloat16" else OUT_F32
+
+
+def _given_out_type(out, out_type: int | None) -> int:
+    """The output's type of a call: a raw pointer's has to be given, a tensor's has to agree with the one
+    given (the call writes B * 64 * 512 values of it)."""
+    name = str(getattr(out, "dtype", None))
+    if out_type is None and name == "None":
+        raise Csa2Error(1, "attention output: the out_type of a raw pointer")
+    if (name, out_type) in (("torch.float32", OUT_BF16), ("torch.bfloat16", OUT_F32)):
+        raise Csa2Error(1, f"attention output of type {name}, out_type {out_type}")
+    return _out_type(out, out_type)
 
 
 def paged_attn_workspace_size(B: int, n_max: int, n_swa: int) -> int:
@@ -439,12 +450,12 @@ def paged_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, n_max: in
                       softmax_scale: float, out, ws, lse_out=None, stream=None, q_nr: NormRope | None = None,
                       q_pos=None, sink=None, win: Window | None = None, out_type: int | None = None) -> None:
     """Dense attention through a page table: entries [0, n_entries[b]) of row b's pages plus the window
-    rows; out fp32 or bf16 (csa2_paged_attn_decode)."""
+    rows; out fp32 or bf16, by its dtype, or by out_type for a raw pointer (csa2_paged_attn_decode)."""
     _ok(lib().csa2_paged_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), B, _ptr(n_entries), n_max,
                                      _ptr(swa), n_swa, _ptr(q), softmax_scale,
                                      ctypes.byref(q_nr) if q_nr is not None else None, _ptr(q_pos), _ptr(sink),
                                      ctypes.byref(win) if win is not None else None, _ptr(out),
-                                     _out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
+                                     _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
                                      _stream(stream)), "csa2_paged_attn_decode")
 
 
@@ -463,7 +474,7 @@ def prefix_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, G: int, 
                                       _ptr(group_start), _ptr(n_shared), n_shared_max, n_own_max, _ptr(swa), n_swa,
                                       _ptr(q), softmax_scale, ctypes.byref(q_nr) if q_nr is not None else None,
                                       _ptr(q_pos), _ptr(sink), ctypes.byref(win) if win is not None else None,
-                                      _ptr(out), _out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
+                                      _ptr(out), _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
                                       _stream(stream)), "csa2_prefix_attn_decode")
 
 
