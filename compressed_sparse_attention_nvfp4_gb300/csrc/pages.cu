@@ -342,7 +342,8 @@ extern "C" csa2_status csa2_page_tables(int32_t B, const int32_t* n_have, const 
   } else {
     {
       KernelTimer timer("k_page_plan", st);
-      launch_pdl(k_page_plan, dim3(1), dim3(kPlanThreads), 0, st, a, v);
+      if (launch_pdl(k_page_plan, dim3(1), dim3(kPlanThreads), 0, st, a, v) != cudaSuccess)
+        return launch_status();  // the fill would follow whatever plan the workspace held
     }
     const int64_t threads = n_rows > 4096 ? n_rows : 4096;
     const int blocks = (int)(cdiv(threads, kFillThreads) < 1216 ? cdiv(threads, kFillThreads) : 1216);

@@ -2190,13 +2190,16 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     {
       KernelTimer timer("k_prefix_prep", st);
       const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
-      launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
-                 (size_t)kPrepSmem, st, a, pq, k, L.image);
+      // without its plan the attention would run whatever one the workspace held, and the join its parts
+      if (launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
+                     (size_t)kPrepSmem, st, a, pq, k, L.image) != cudaSuccess)
+        return launch_status();
     }
     if (alone) {
       {
         KernelTimer timer("k_paged_attn", st);
-        launch_pdl(k_paged_attn<kHalf>, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k);
+        if (launch_pdl(k_paged_attn<kHalf>, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k) != cudaSuccess)
+          return launch_status();
       }
       KernelTimer timer("k_paged_merge", st);
       if (slices > 1) merge(k_paged_merge<4, kHalf>, 32, kMergeThreads, rest ? 4 : 1);
@@ -2205,7 +2208,9 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     }
     {
       KernelTimer timer("k_prefix_attn", st);
-      launch_clusters(k_prefix_attn<kHalf>, dim3(2 * kClusters), dim3(kThreads), 2, 1, sizeof(PrefixSmem), st, k, maps);
+      if (launch_clusters(k_prefix_attn<kHalf>, dim3(2 * kClusters), dim3(kThreads), 2, 1, sizeof(PrefixSmem), st, k,
+                          maps) != cudaSuccess)
+        return launch_status();
     }
     KernelTimer timer("k_prefix_merge", st);
     if (slices > 1) merge(k_prefix_merge<4, kHalf>, 32, PrefixMerge<4, kHalf>::kThreads, 1);
