@@ -178,3 +178,33 @@ def test_pairs_give_the_same_bits_again_and_again(sizes, shared, own):
             noise.add_(1)
         out, lse = attend(codes, scales, P, table, n, q, **more)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), i
+
+
+@pytest.mark.parametrize("shared_max,few", [(65_536, False), (4_000, True)])  # pairs, and every query by itself
+@pytest.mark.parametrize("case", ["first", "ninth", "late", "last", "none", "ties", "empty"])
+def test_whose_row_holds_the_shared_entries(case, shared_max, few):
+    """Groups that begin with queries too short for the prefix: it is read through the first row that has all of it,
+    else the longest (of equal ones the first).  Every other row ends with its own entries, in page ids that no pool
+    has: reading through one of them would be reported."""
+    P, sizes, want = 64, [300, 7, 1, 12] if not few else [30, 7, 1, 12], 1_000
+    B = sum(sizes)
+    start = np.concatenate([[0], np.cumsum(sizes)])
+    c = Counted(5, 200, P)
+    n, table = np.zeros(B, int), np.full((B, shared_max // P + 1), 0x7fffffff, np.int32)
+    for g, size in enumerate(sizes):
+        lead = c.rng.permutation(200)[:20]
+        m = c.rng.integers(0, 900, size)
+        at = {"first": 0, "ninth": min(8, size - 1), "late": size * 2 // 3, "last": size - 1}.get(case)
+        if at is not None:
+            m[at] = 1_100
+            m[at + 1:] = c.rng.integers(0, 1_100, size - at - 1)
+        if case == "ties":
+            m[size // 2:] = 905
+        if case == "empty":
+            m[:] = 0
+        n[start[g]:start[g + 1]] = m
+        for b in range(start[g], start[g + 1]):
+            table[b, :-(-n[b] // P)] = lead[:-(-n[b] // P)]
+    q = torch.zeros((B, H, D), dtype=torch.bfloat16, device="cuda")
+    got = attend(c.codes, c.scales, P, to_dev(table), n, q, groups=start, shared=[want] * 4, shared_max=shared_max, own_max=1_100)
+    c.check(table, n, *got)
