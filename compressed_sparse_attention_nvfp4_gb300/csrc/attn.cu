@@ -241,15 +241,16 @@ template <bool kPartial, bool kEx>
 __global__ void __launch_bounds__(512, 1) k_attn(
     const uint8_t* __restrict__ kv_codes, const uint8_t* __restrict__ kv_scales, int64_t seq_stride,
     const int32_t* __restrict__ topk, const int32_t* __restrict__ dense_n, int k, const uint8_t* __restrict__ swa,
-    int n_swa, const uint16_t* __restrict__ qg, float scale, AttnExtras ex, int nchunks, int cps,
+    int n_swa,
+    const uint16_t* __restrict__ qg, float scale, AttnExtras ex, int nchunks, int cps,
     float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
     float2* __restrict__ part_ml, void* ws) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   AttnSmem& S = *reinterpret_cast<AttnSmem*>(smem_raw);
   volatile int* abort_flag = &S.abort_flag;
   const int b = blockIdx.y, split = blockIdx.x;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int c0 = split * cps, nc = min(nchunks, c0 + cps) - c0;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (warp == kCtlWarp) {
     if (lane == 0) {
@@ -722,8 +723,7 @@ csa2_status attn_run(const csa2_kv_planes* kv, int32_t B, const int32_t* topk, c
   }
   if (partial) {
     KernelTimer timer("k_attn_merge", st);
-    launch_pdl(k_attn_merge, dim3(B * kHAtt), dim3(128), 0, st, L.part_o, L.part_ml, plan.nsplit, sink, out,
-               lse_out);
+    launch_pdl(k_attn_merge, dim3(B * kHAtt), dim3(128), 0, st, L.part_o, L.part_ml, plan.nsplit, sink, out, lse_out);
   }
   return launch_status();
 }
@@ -741,8 +741,8 @@ extern "C" csa2_status csa2_sparse_attn_decode(const csa2_kv_planes* kv, int32_t
   if (!planes_ok(kv) || B <= 0 || B > 65535 || k < 0 || k > CSA2_MAX_TOPK || n_swa < 0 || n_swa > CSA2_MAX_SWA)
     return CSA2_ERR_INVALID_ARG;
   if ((k > 0 && !topk) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, topk, nullptr, k, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win,
-                  out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, topk, nullptr, k, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos, sink, win, out,
+                  lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }
 
 extern "C" size_t csa2_dense_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa) {
@@ -762,6 +762,6 @@ extern "C" csa2_status csa2_dense_attn_decode(const csa2_kv_planes* kv, int32_t 
     return CSA2_ERR_INVALID_ARG;
   if ((n_max > 0 && !n_entries) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out) return CSA2_ERR_INVALID_ARG;
   if (n_entries && !aligned(n_entries, 4)) return CSA2_ERR_INVALID_ARG;
-  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr,
-                  q_pos, sink, win, out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
+  return attn_run(kv, B, nullptr, n_entries, (int32_t)n_max, swa_e4m3, n_swa, q_bf16, softmax_scale, q_nr, q_pos,
+                  sink, win, out, lse_out, ws, ws_bytes, (cudaStream_t)stream);
 }
