@@ -42,14 +42,18 @@ constexpr int kPrepThreads = 512;
 constexpr int kClusters = 76;    // CTA pairs of a launch: one for every two of the 152 SMs
 constexpr int kChunk = 128;      // rows of a chunk
 constexpr int kOwnChunk = 64;    // of which each query of a pair has this many in an own chunk
-// A group of at least this many queries has its shared entries widened once, and groups smaller than this on
-// average run every query by itself.  64 queries on 8,192 entries, groups of four: 106 us with the image, 93
-// without; of eight: 86 and 90.  In pairs / by themselves: groups of one 160 / 98 us, two 93 / 98, three
-// 124 / 98, four 93 / 98, sixteen 76 / 98 (an odd group's last query takes a pair's time).
+// A group of at least this many queries has its shared entries widened once: 64 queries on 8,192 entries, groups of
+// four: 114 us with the image, 94 without; of five 116 and 110, six 100 and 96, eight 92 and 94, sixteen 82 and 94.
+// Batches whose groups are smaller than this on average run every query by itself.  Two queries of a pair share every
+// row, but an odd group's last query takes a pair's time, and own rows cost a pair more.  In pairs / by themselves, us,
+// 64 on 8,192, groups of equal size: one 166 / 100, two 98 / 99, three 115 / 98, four 93 / 97, five 116 / 98, six
+// 100 / 100, eight 92 / 97, sixteen 82 / 97; groups and lengths drawn at random: 4 on average 94 / 77, 8 80 / 71,
+// 13 92 / 84 to 77 / 85, 20 (101 on 4,001) 68 / 75, 32 65 / 82.  The host knows the average alone: five is about where
+// equal groups break even, even ones below and odd ones above it; random ones do so at about thirteen.
 constexpr int kImageQueries = 5;
 // Queries times shared entries below which every query runs by itself all the same, its ramp being shorter.  In
-// pairs / by themselves, us: 8 queries on 8,192 entries 33.7 / 26.8, 32 on 2,000 31.5 / 29.7, 128 on 500
-// 40.5 / 38.7; 16 on 8,192 38.6 / 38.6, 128 on 1,000 46.2 / 46.9; 16 on 16,384 47.9 / 58.3.
+// pairs / by themselves, us: 8 queries on 8,192 entries 33 / 27, 32 on 2,000 31 / 27, 128 on 500 38 / 36; 16 on 8,192
+// 37 / 38, 128 on 1,000 45 / 45, 64 on 2,000 39 / 41; 16 on 16,384 48 / 57, 64 on 4,000 51 / 58.
 constexpr int64_t kPairWork = 1 << 17;
 constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM,
 constexpr int kWidenFirst = 152;   // of which these come before the queries' staging

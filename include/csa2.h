@@ -528,7 +528,8 @@ size_t csa2_paged_attn_workspace_size(int32_t B, int64_t n_max, int32_t n_swa);
  * each and 1 GB at most (groups of five queries or more read them from there; beyond 2^20 entries,
  * and in smaller groups, they are widened where they are read).  With B < 5 G or B * n_shared_max <
  * 2^17 sharing would cost more than it saves: every query reads the entries for itself, and the
- * workspace is as csa2_paged_attn_decode's. */
+ * workspace is as csa2_paged_attn_decode's.  This goes by the bounds, not by the lengths, which the host
+ * does not know: an n_shared_max far above the shared entries takes the wrong form, and workspace. */
 csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B,
                                     const int32_t* n_entries, int32_t G, const int32_t* group_start,
                                     const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
