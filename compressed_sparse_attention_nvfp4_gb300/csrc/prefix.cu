@@ -23,13 +23,13 @@
 // by every pair for itself 768 us a call on 64 queries of 65,000 shared entries, from the image 451); the rest
 // is widened by the row warps.  Shared memory bounds a chunk: 128 KB read by the S MMAs, 96 KB by the O MMAs,
 // 128 KB of rows and 16 KB of P written, 368 KB = 2,900 cycles at 128 bytes a cycle, against 2,048 cycles of
-// MMA; measured, 3,100 to 3,400.  With one buffer for each operand there is no room for a second chunk, so both
+// MMA; measured, 3,400 to 3,900, the waits of the odd CTA's arrivals among them.  With one buffer for each operand there is no room for a second chunk, so both
 // are handed over in four pieces (128 channels of S's rows, 32 rows of O's).
 // Behind the shared entries come the two queries' own (their last entries and windows): chunks whose
 // first 64 rows are the first query's and whose last 64 the second's, each query masking the other's; behind
 // the shorter's last, 128 rows of the longer.
-// Measured: 64 queries on 65,000 shared entries 383 us, 1.43 PFLOP/s, 76 % of the rate of a library bf16
-// product; 32 on 8,192, normalised and rotated, 49 us.
+// Measured: 64 queries on 65,000 shared entries 405 us, 1.35 PFLOP/s, 71 % of the rate of a library bf16
+// product; 32 on 8,192, normalised and rotated, 51 us.
 #include <type_traits>
 
 #include "attn.cuh"
