@@ -73,7 +73,10 @@ class Pages(ctypes.Structure):
 
 
 def pages(table, n_pages: int, max_pages: int | None = None) -> Pages:
-    """A csa2_pages over a device int32 array [B, max_pages]; keeps a reference to it."""
+    """A csa2_pages over a device int32 array [B, max_pages]; keeps a reference to it.  Rows lie one behind
+    another: a tensor of another type or a slice of wider rows is refused."""
+    if hasattr(table, "is_contiguous") and not (str(table.dtype) == "torch.int32" and table.is_contiguous()):
+        raise Csa2Error(1, f"page table of type {table.dtype}, strides {tuple(table.stride())}")
     p = Pages(_ptr(table), int(table.shape[-1] if max_pages is None else max_pages), int(n_pages))
     p._refs = (table,)
     return p

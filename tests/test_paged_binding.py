@@ -28,3 +28,13 @@ def test_the_output_type_has_to_be_known(call):
     assert status(call, out=f32, out_type=csa2.OUT_BF16) == 1
     assert status(call, out=bf16, out_type=csa2.OUT_F32) == 1
     assert status(call, out=torch.empty(16, dtype=torch.float16)) == 1
+
+
+def test_a_page_table_is_contiguous_int32():
+    t = torch.zeros((4, 16), dtype=torch.int32)
+    assert csa2.pages(t, 32).max_pages == 16 and csa2.pages(t[1:3], 32).max_pages == 16
+    assert csa2.pages(256, 32, max_pages=8).max_pages == 8
+    for bad in (t[:, :8], t.t(), t.long(), t.to(torch.int16)):
+        with pytest.raises(csa2.Csa2Error) as e:
+            csa2.pages(bad, 32)
+        assert e.value.status == 1
