@@ -26,6 +26,10 @@ STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED",
           3: "CSA2_ERR_WORKSPACE", 4: "CSA2_ERR_CUDA", 5: "CSA2_ERR_DEVICE_TIMEOUT",
           6: "CSA2_ERR_INDEX_RANGE", 7: "CSA2_ERR_NO_PAGES"}
 OUT_F32, OUT_BF16 = 0, 1
+F32, BF16 = 0, 1
+ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
+SCALE_NONE, SCALE_LINEAR, SCALE_YARN = 0, 1, 2
+MAX_TREE = 64
 
 
 class Csa2Error(RuntimeError):
@@ -82,6 +86,46 @@ def pages(table, n_pages: int, max_pages: int | None = None) -> Pages:
     return p
 
 
+class RopeScaling(ctypes.Structure):
+    """csa2_rope_scaling: how a rotation is slowed down for contexts longer than the trained ones."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_float), ("beta_fast", ctypes.c_float),
+                ("beta_slow", ctypes.c_float), ("original", ctypes.c_int64)]
+
+
+def rope_scaling(kind: int, factor: float, original: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0) -> RopeScaling:
+    """A csa2_rope_scaling: SCALE_LINEAR divides every angle by factor, SCALE_YARN those of pairs that turn rarely
+    within `original` tokens."""
+    return RopeScaling(int(kind), float(factor), float(beta_fast), float(beta_slow), int(original))
+
+
+class Rotary(ctypes.Structure):
+    """csa2_rotary: which channels turn, in which layout, how fast, times which magnitude."""
+    _fields_ = [("layout", ctypes.c_int32), ("first", ctypes.c_int32), ("n_rot", ctypes.c_int32),
+                ("base", ctypes.c_float), ("magnitude", ctypes.c_float), ("scaling", RopeScaling)]
+
+
+def rotary(n_rot: int, first: int = 0, layout: int = ROPE_INTERLEAVED, base: float = 10000.0,
+           magnitude: float = 1.0, scaling: RopeScaling | None = None) -> Rotary:
+    """A csa2_rotary of channels [first, first + n_rot)."""
+    return Rotary(int(layout), int(first), int(n_rot), float(base), float(magnitude),
+                  RopeScaling() if scaling is None else scaling)
+
+
+class Trees(ctypes.Structure):
+    """csa2_trees: the drafted tokens of a call (int32 device arrays) and their host bounds."""
+    _fields_ = [("start", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("R", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("entries", ctypes.c_int32)]
+
+
+def trees(start, parent, R: int, B: int, max_tokens: int, entries: bool = True) -> Trees:
+    """A csa2_trees over device int32 arrays start [R + 1] and parent [B] (indices within the request, -1: a child of
+    its last token); keeps references to both.  entries: a drafted token has an entry in the cache."""
+    t = Trees(_ptr(start), _ptr(parent), int(R), int(B), int(max_tokens), int(bool(entries)))
+    t._refs = (start, parent)
+    return t
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
@@ -103,6 +147,9 @@ def lib() -> ctypes.CDLL:
         nr = ctypes.POINTER(NormRope)
         wn = ctypes.POINTER(Window)
         pg = ctypes.POINTER(Pages)
+        sc = ctypes.POINTER(RopeScaling)
+        ro = ctypes.POINTER(Rotary)
+        tr = ctypes.POINTER(Trees)
         sig = {
             "csa2_quantize_entries": ([vp, vp, i64, pl, i64, vp], ctypes.c_int),
             "csa2_cache_write": ([vp, i64, i32, vp, vp, vp, i32, pl, i32, i64, nr, i64, vp, sz, vp],
@@ -138,6 +185,11 @@ def lib() -> ctypes.CDLL:
             "csa2_prefix_attn_decode": ([pl, pg, i32, vp, i32, vp, vp, i64, i64, vp, i32, vp, f32, nr, vp, vp, wn, vp,
                                          i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_prefix_attn_workspace_size": ([i32, i32, i64, i64, i32], sz),
+            "csa2_tree_commit": ([pl, pg, tr, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
+            "csa2_tree_commit_workspace_size": ([i32], sz),
+            "csa2_rope": ([vp, i64, i64, vp, i64, i64, i32, i64, i32, i32, vp, ro, i32, vp], ctypes.c_int),
+            "csa2_latent_append": ([vp, vp, i32, i32, pl, i32, vp, vp, nr, sc, vp, ro, vp, sz, vp], ctypes.c_int),
+            "csa2_latent_append_workspace_size": ([i32], sz),
             "csa2_compress_overlap": ([vp, i64, i32, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_compress_hca": ([vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_compress_workspace_size": ([i64, i32], sz),
@@ -280,6 +332,79 @@ def cache_append(H, G: int, d_model: int, Wkv, Wz, Wik, m: int, planes: Planes, 
                                 ctypes.byref(planes.c), n_slots, _ptr(slot), _ptr(entry),
                                 ctypes.byref(kv_nr) if kv_nr is not None else None, _ptr(pos), _ptr(ws),
                                 _nbytes(ws), _stream(stream)), "csa2_cache_append")
+
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+_types: dict = {}  # dtype -> F32 / BF16
+
+
+def _type_of(x) -> int | None:
+    """F32 / BF16 of a tensor, None of a raw pointer."""
+    dtype = getattr(x, "dtype", None)
+    if dtype is None:
+        return None
+    kind = _types.get(dtype)
+    if kind is None:
+        kind = {"torch.float32": F32, "torch.bfloat16": BF16}.get(str(dtype))
+        if kind is None:
+            raise Csa2Error(1, f"activations of type {dtype}")
+        _types[dtype] = kind
+    return kind
+
+
+def _common_type(a, b, type: int | None, what: str) -> int:
+    """The one type of a call's two activations (either may be None); of raw pointers it has to be given."""
+    of = [t for t in (_type_of(a), _type_of(b), type) if t is not None]
+    if not of or of.count(of[0]) != len(of):
+        raise Csa2Error(1, f"{what} of types {getattr(a, 'dtype', None)}, {getattr(b, 'dtype', None)}, type {type}")
+    return of[0]
+
+
+def _strides(x, heads: int, dim: int, strides, what: str) -> tuple[int, int]:
+    """Row and head strides in elements: those given, else a tensor's [n_rows, heads, dim] or [n_rows, dim], else
+    dense ones."""
+    if strides is not None:
+        return int(strides[0]), int(strides[1])
+    if not hasattr(x, "stride"):
+        return heads * dim, dim
+    shape, st = x.shape, x.stride()
+    if len(st) == 3 and shape[1] == heads and shape[2] == dim and (st[2] == 1 or dim == 1):
+        return st[0], st[1]
+    if len(st) == 2 and shape[1] == heads * dim and (st[1] == 1 or heads * dim == 1):
+        return st[0], dim
+    raise Csa2Error(1, f"{what} of shape {tuple(shape)}, strides {st} for {heads} vectors of {dim} channels")
+
+
+def rope(x, n_rows: int, heads: int, dim: int, pos, rot: Rotary, out, inverse: bool = False, type: int | None = None,
+         x_strides=None, out_strides=None, stream=None) -> None:
+    """Rotary positions: x [n_rows, heads, dim] (fp32 or bf16, rows and heads strided as the tensor says) -> out, which
+    may be x; pos int64 [n_rows].  inverse: by -pos, which is the gradient (csa2_rope)."""
+    kind = _common_type(x, out, type, "rope")
+    xs, ys = _strides(x, heads, dim, x_strides, "rope input"), _strides(out, heads, dim, out_strides, "rope output")
+    _ok(lib().csa2_rope(_ptr(x), *xs, _ptr(out), *ys, kind, n_rows, heads, dim, _ptr(pos), ctypes.byref(rot),
+                        int(bool(inverse)), _stream(stream)), "csa2_rope")
+
+
+def latent_append_workspace_size(R: int) -> int:
+    return lib().csa2_latent_append_workspace_size(R)
+
+
+def latent_append(x, R: int, planes: Planes, n_slots: int, slot, entry, ws, key=None, kv_nr: NormRope | None = None,
+                  scaling: RopeScaling | None = None, pos=None, key_rot: Rotary | None = None,
+                  type: int | None = None, stream=None) -> None:
+    """Ready latents x [R, 512] and indexer keys key [R, 128] (fp32 or bf16, either None) into slot[r], index
+    entry[r], as cache_append's map; kv_nr normalises and rotates the main copy, its rotation slowed down by scaling,
+    key_rot rotates the key (csa2_latent_append)."""
+    for t in (x, key):
+        if hasattr(t, "is_contiguous") and not t.is_contiguous():
+            raise Csa2Error(1, f"latents or keys of strides {tuple(t.stride())}")
+    kind = F32 if x is None and key is None else _common_type(x, key, type, "latents and keys")
+    _ok(lib().csa2_latent_append(_ptr(x), _ptr(key), kind, R, ctypes.byref(planes.c), n_slots, _ptr(slot), _ptr(entry),
+                                 _ref(kv_nr), _ref(scaling), _ptr(pos), _ref(key_rot), _ptr(ws), _nbytes(ws),
+                                 _stream(stream)), "csa2_latent_append")
 
 
 def swa_append(x, R: int, pos, n_queries: int, ring, n_win: int, query=None, nr: NormRope | None = None,
@@ -479,6 +604,21 @@ def prefix_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, G: int, 
                                       _ptr(q_pos), _ptr(sink), ctypes.byref(win) if win is not None else None,
                                       _ptr(out), _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
                                       _stream(stream)), "csa2_prefix_attn_decode")
+
+
+def tree_commit_workspace_size(R: int) -> int:
+    return lib().csa2_tree_commit_workspace_size(R)
+
+
+def tree_commit(planes: Planes | None, pages: Pages | None, trees: Trees, n_entries, n_accept, path, n_path: int,
+                n_new, ws, draft=None, pos=None, ring=None, ring_pos=None, n_win: int = 0, stream=None) -> None:
+    """Commit of accepted paths: token path[g, i] of request g becomes its entry n_entries[g] + i, its window row (of
+    draft) takes its place of the ring at position pos[g] + i; n_new (or None) is what page_tables takes to drop the
+    rest (csa2_tree_commit)."""
+    c = planes.c if planes is not None else None
+    _ok(lib().csa2_tree_commit(_ref(c), _ref(pages), ctypes.byref(trees), _ptr(n_entries), _ptr(n_accept), _ptr(path),
+                               n_path, _ptr(n_new), _ptr(draft), _ptr(pos), _ptr(ring), _ptr(ring_pos), n_win, _ptr(ws),
+                               _nbytes(ws), _stream(stream)), "csa2_tree_commit")
 
 
 def compress_workspace_size(T: int, d_model: int) -> int:

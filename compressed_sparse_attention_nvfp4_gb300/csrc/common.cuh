@@ -115,6 +115,27 @@ inline cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t
   return cudaLaunchKernelEx(&cfg, k, static_cast<KArgs>(args)...);
 }
 
+// launch_pdl in clusters of cx x cy CTAs
+template <typename... K>
+inline cudaError_t launch_clusters(void (*kern)(K...), dim3 grid, dim3 block, unsigned cx, unsigned cy, size_t smem,
+                            cudaStream_t st, const K&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cx;
+  attr[0].val.clusterDim.y = cy;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Status of the launches just issued.  With CSA2_DEBUG set in the environment the
 // CUDA error string goes to stderr as well.
 inline csa2_status launch_status() {

@@ -2133,27 +2133,6 @@ bool image_map(CUtensorMap* map, uint16_t* image, int64_t chunks, uint32_t rows,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// launch_pdl in clusters of cx x cy CTAs
-template <typename... K>
-cudaError_t launch_clusters(void (*kern)(K...), dim3 grid, dim3 block, unsigned cx, unsigned cy, size_t smem,
-                            cudaStream_t st, const K&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cx;
-  attr[0].val.clusterDim.y = cy;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 }  // namespace
 }  // namespace csa2
 

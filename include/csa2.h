@@ -135,6 +135,53 @@ typedef struct {
   float rope_base;
 } csa2_norm_rope;
 
+/* ------------------------------------------------------------ rotary positions */
+
+/* Longer contexts than a model was trained on (no counterpart on the design pages): which theta_i a
+ * rotation of n channels (n / 2 pairs, theta_i = base^(-2 i / n)) turns by.
+ *   LINEAR  theta_i / factor
+ *   YARN    theta_i (1 - r_i) + theta_i / factor r_i ("YaRN: Efficient Context Window Extension of Large
+ *           Language Models", NTK-by-parts; the ramp by pair index, as its published models have it):
+ *           r_i = (i - lo) / (hi - lo) within [0, 1], lo = floor(c(beta_fast)), hi = ceil(c(beta_slow)) within
+ *           [0, n - 1] (hi - lo at least 1/1000), c(b) = n ln(original / (2 pi b)) / (2 ln base): the pair that
+ *           turns b times over the original context.  Its softmax temperature is the caller's (softmax_scale, or
+ *           csa2_rotary's magnitude)
+ * factor > 0; YARN: original >= 1 tokens, beta_fast > beta_slow > 0.  A null pointer or NONE: theta_i. */
+typedef enum { CSA2_SCALE_NONE = 0, CSA2_SCALE_LINEAR = 1, CSA2_SCALE_YARN = 2 } csa2_rope_scale;
+typedef struct {
+  int32_t kind; /* csa2_rope_scale */
+  float factor, beta_fast, beta_slow;
+  int64_t original;
+} csa2_rope_scaling;
+
+/* Type of a call's activations. */
+typedef enum { CSA2_F32 = 0, CSA2_BF16 = 1 } csa2_type;
+
+/* A rotation of channels [first, first + n_rot) of a vector: pair i is the channels (first + 2 i, first + 2 i + 1)
+ * INTERLEAVED, or (first + i, first + n_rot / 2 + i) in HALVES; it turns counter-clockwise by pos * theta_i and is
+ * multiplied by magnitude.  n_rot even, 2 .. 512; 1 < base <= 1e30; magnitude finite. */
+typedef enum { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALVES = 1 } csa2_rope_layout;
+typedef struct {
+  int32_t layout; /* csa2_rope_layout */
+  int32_t first, n_rot;
+  float base, magnitude;
+  csa2_rope_scaling scaling;
+} csa2_rotary;
+
+/* Rotary positions of n_rows tokens of `heads` vectors of dim channels (indexer queries, which no other call
+ * rotates; queries, keys and outputs of other layouts than csa2_norm_rope's):
+ *   y[r][h] = x[r][h] with the channels of `rot` turned by pos[r]; inverse != 0: by -pos[r], multiplied by
+ *   magnitude all the same.  That is the transposed map, so the gradient of x is the inverse of y's.
+ *   x, y   of `type`, computed in fp32 and rounded once; element (r, h, c) of x at r * x_row + h * x_head + c, of y
+ *          at r * y_row + h * y_head + c (strides in elements, any alignment; 16-byte aligned ones run faster)
+ *   pos    [n_rows] int64 (device), any value: an angle is exact to |pos| 2^-53 turns
+ * y may be x, with the same strides: then only the rotated channels are written.  Otherwise they must not overlap, and
+ * the vectors of y must not overlap one another (CSA2_ERR_INVALID_ARG).  0 <= n_rows < 2^31, 1 <= heads <= 65535,
+ * first + n_rot <= dim <= 65536. */
+csa2_status csa2_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int64_t y_row, int64_t y_head, int32_t type,
+                      int64_t n_rows, int32_t heads, int32_t dim, const int64_t* pos, const csa2_rotary* rot,
+                      int32_t inverse, csa2_stream stream);
+
 /* -------------------------------------------------------------- cache write */
 
 /* Prefill cache write of one sequence slot (CED Eq. (1) and the CSA2 compressor):
@@ -180,6 +227,26 @@ csa2_status csa2_cache_append(const void* H_bf16, int32_t G, int32_t d_model, co
                               const int64_t* entry, const csa2_norm_rope* kv_nr, const int64_t* pos,
                               void* ws, size_t ws_bytes, csa2_stream stream);
 size_t csa2_cache_append_workspace_size(int32_t G, int32_t d_model, int32_t m);
+
+/* Append of ready latents to slots or pages, normalised and rotated on the way: the outputs of csa2_compress_overlap
+ * / csa2_compress_hca, or a caller's own, go where a slot map says ("DeepSeek-V4: ...", CSA, other details: RMSNorm and
+ * RoPE of the compressed entries; "DeepSeek-V4.1-Flash course, 02 Architecture", 2.4.4: quantized after RoPE).
+ *   x      [R][512] of `type`, or NULL: the main copy stays as it is; kv_nr (or NULL) normalises and rotates it, its
+ *          rotation slowed down by `scaling` (or NULL)
+ *   key    [R][128] of `type`, or NULL: the indexer key stays as it is; key_rot (or NULL) rotates it
+ *   slot, entry  [R] destinations as in csa2_cache_append: outside the planes a row is skipped and reported
+ *          (CSA2_ERR_INDEX_RANGE), slot -1 with entry -1 is skipped without a report.  Two rows of one destination
+ *          leave either, or parts of both
+ *   pos    [R] int64, required with a rotation
+ * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: |pos| 2^-53 turns)
+ * and rounded to fp32 once, then the codec of csa2_quantize_entries writes it; without norm and rotation the bytes
+ * are csa2_quantize_entries'.  x and key 16-byte aligned; 0 <= R <= 2^30;
+ * ws: csa2_latent_append_workspace_size(R) bytes (the error word). */
+csa2_status csa2_latent_append(const void* x, const void* key, int32_t type, int32_t R, const csa2_kv_planes* dst,
+                               int32_t n_slots, const int32_t* slot, const int64_t* entry, const csa2_norm_rope* kv_nr,
+                               const csa2_rope_scaling* scaling, const int64_t* pos, const csa2_rotary* key_rot,
+                               void* ws, size_t ws_bytes, csa2_stream stream);
+size_t csa2_latent_append_workspace_size(int32_t R);
 
 /* Sliding-window ring write ("DeepSeek-V4 ...", sliding-window branch: every query keeps
  * its last n_win uncompressed rows; "DeepSeek-V4.1-Flash course, 02 Architecture", 2.4.4:
@@ -538,6 +605,45 @@ csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const csa2_pages* 
                                     const csa2_window* win, void* out, int32_t out_type, float* lse_out, void* ws,
                                     size_t ws_bytes, csa2_stream stream);
 size_t csa2_prefix_attn_workspace_size(int32_t B, int32_t G, int64_t n_shared_max, int64_t n_own_max, int32_t n_swa);
+
+/* Drafted tokens that one call verifies (speculative decoding; no counterpart on the design pages): request g's are the
+ * queries [start[g], start[g + 1]), a tree in which parent[b] is the index of query b's parent within its request,
+ * below its own, or -1 where the parent is the request's last token.  Query b sees itself and its ancestors, of the
+ * drafted tokens.
+ *   entries  1: a drafted token has an entry in the cache (a layer with m = 1): token t of request g is the
+ *            request's entry n_entries[g] + t, appended before the call.  0: none of them has (m > 1: entries are
+ *            written once their tokens are accepted) */
+typedef struct {
+  const int32_t* start;  /* [R + 1] (device), ascending within [0, B] */
+  const int32_t* parent; /* [B] (device) */
+  int32_t R, B;          /* requests; queries */
+  int32_t max_tokens;    /* host bound of a tree's tokens, 1 .. CSA2_MAX_TREE */
+  int32_t entries;
+} csa2_trees;
+#define CSA2_MAX_TREE 64
+
+/* Commit of the accepted tokens of each tree, after csa2_tree_attn_decode and the sampler: token path[g][i], i <
+ * n_accept[g], is the i-th token that request g keeps.
+ *   trees      as in the attention; parent is not read and may be NULL
+ *   kv, pages, n_entries  with trees->entries: entry n_entries[g] + path[g][i] (all four planes) moves to
+ *              n_entries[g] + i; what lies behind the last kept entry is left as it may be.  Without, kv and pages
+ *              may be NULL
+ *   n_accept   [R] int32; path [R][n_path] int32, each within the tree (in any order: all entries are read before
+ *              one is written)
+ *   n_new      [R] int32 or NULL: n_accept[g] - tokens (0 without entries), with which csa2_page_tables drops the
+ *              rest from n_have = n_entries[g] + tokens
+ *   draft_e4m3 [B][512], pos [R] int64 (the position of the first draft), ring [R][n_win][512], ring_pos
+ *              [R][n_win]: the i-th kept token's window row goes to ring place (pos[g] + i) mod n_win, the last n_win of
+ *              them where there are more; n_win = 0: no window, the four may be NULL
+ * A request whose start is not in order, whose tree has more than max_tokens tokens, with n_accept outside [0, min(tokens,
+ * n_path)], a path index outside its tree, a negative n_entries or pos, an entry outside the table's row or a page outside
+ * the planes is reported as CSA2_ERR_INDEX_RANGE (detail: the request) and stays as it is, n_new 0.
+ * 1 <= R <= 65535; ws: csa2_tree_commit_workspace_size(R) bytes (the error word). */
+csa2_status csa2_tree_commit(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
+                             const int32_t* n_entries, const int32_t* n_accept, const int32_t* path, int32_t n_path,
+                             int32_t* n_new, const uint8_t* draft_e4m3, const int64_t* pos, uint8_t* ring,
+                             int64_t* ring_pos, int32_t n_win, void* ws, size_t ws_bytes, csa2_stream stream);
+size_t csa2_tree_commit_workspace_size(int32_t R);
 
 /* ---------------------------------------------------------------- schedule */
 
