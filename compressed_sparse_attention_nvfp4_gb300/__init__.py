@@ -185,6 +185,9 @@ def lib() -> ctypes.CDLL:
             "csa2_prefix_attn_decode": ([pl, pg, i32, vp, i32, vp, vp, i64, i64, vp, i32, vp, f32, nr, vp, vp, wn, vp,
                                          i32, vp, vp, sz, vp], ctypes.c_int),
             "csa2_prefix_attn_workspace_size": ([i32, i32, i64, i64, i32], sz),
+            "csa2_tree_attn_decode": ([pl, pg, tr, vp, i64, vp, vp, vp, i32, vp, vp, f32, nr, sc, vp, vp, i32, vp, vp, sz,
+                                       vp], ctypes.c_int),
+            "csa2_tree_attn_workspace_size": ([i32, i32, i32, i64, i32], sz),
             "csa2_tree_commit": ([pl, pg, tr, vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp], ctypes.c_int),
             "csa2_tree_commit_workspace_size": ([i32], sz),
             "csa2_rope": ([vp, i64, i64, vp, i64, i64, i32, i64, i32, i32, vp, ro, i32, vp], ctypes.c_int),
@@ -604,6 +607,23 @@ def prefix_attn_decode(planes: Planes, pages: Pages, B: int, n_entries, G: int, 
                                       _ptr(q_pos), _ptr(sink), ctypes.byref(win) if win is not None else None,
                                       _ptr(out), _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
                                       _stream(stream)), "csa2_prefix_attn_decode")
+
+
+def tree_attn_workspace_size(R: int, B: int, max_tokens: int, n_max: int, n_swa: int) -> int:
+    return lib().csa2_tree_attn_workspace_size(R, B, max_tokens, n_max, n_swa)
+
+
+def tree_attn_decode(planes: Planes, pages: Pages, trees: Trees, n_entries, n_max: int, swa, swa_pos, draft,
+                     n_swa: int, q, q_pos, softmax_scale: float, out, ws, lse_out=None, q_nr: NormRope | None = None,
+                     scaling: RopeScaling | None = None, sink=None, out_type: int | None = None, stream=None) -> None:
+    """paged_attn_decode for trees of drafted tokens: query b attends to its request's n_entries[g] entries, its own and
+    its ancestors' behind them, the ring rows swa at positions swa_pos and the drafted tokens' window rows draft
+    (csa2_tree_attn_decode); pages' rows are the requests'."""
+    _ok(lib().csa2_tree_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), ctypes.byref(trees), _ptr(n_entries),
+                                    n_max, _ptr(swa), _ptr(swa_pos), _ptr(draft), n_swa, _ptr(q), _ptr(q_pos),
+                                    softmax_scale, _ref(q_nr), _ref(scaling), _ptr(sink), _ptr(out),
+                                    _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)), "csa2_tree_attn_decode")
 
 
 def tree_commit_workspace_size(R: int) -> int:

@@ -1,4 +1,5 @@
-// Attention through page tables: for queries by themselves, and for a batch whose queries share prefixes.
+// Attention through page tables: for queries by themselves, for a batch whose queries share prefixes, and for trees of
+// drafted tokens.
 //
 // out = softmax(scale q X^T) X over the rows X that a query sees: the entries its table row names, then its
 // window.  With z the logits in log2 units, a part of the rows leaves its reference m, l = sum 2^(z - m) and
@@ -34,6 +35,7 @@
 
 #include "attn.cuh"
 #include "index_scan.cuh"
+#include "rotary.cuh"
 
 namespace csa2 {
 namespace {
@@ -55,12 +57,16 @@ constexpr int kImageQueries = 5;
 // pairs / by themselves, us: 8 queries on 8,192 entries 33 / 27, 32 on 2,000 31 / 27, 128 on 500 38 / 36; 16 on 8,192
 // 37 / 38, 128 on 1,000 45 / 45, 64 on 2,000 39 / 41; 16 on 16,384 48 / 57, 64 on 4,000 51 / 58.
 constexpr int64_t kPairWork = 1 << 17;
+constexpr int kTreesPerCta = kPrepThreads / 32;
 constexpr int kWidenCtas = 304;    // CTAs that widen, two for every SM,
 constexpr int kWidenFirst = 152;   // of which these come before the queries' staging
 constexpr int64_t kImageChunks = 8192;  // at most this many chunks (128 KB each) of the workspace
 
 // Two queries of a group (q1 = -1: one), and their rows: the group's shared entries [0, ns), seen
 // up to vis by each, then each query's own entries ns .. ns + own - 1 and its window.
+// Trees of drafted tokens (kTree): all of a request's rows are shared, its context, its drafts' entries, its ring and
+// its drafts' window rows, of which each query sees some (see Sight).  Then first is the request, ns its entries,
+// vis0 those of the context, vis1 the tree's tokens, own0 the first of them.
 struct Pair {
   int32_t q0, own0;
   int32_t chunk0;  // this pair's first chunk in the order of all pairs' chunks
@@ -112,7 +118,13 @@ struct PrefixArgs {
   int64_t image_cap;  // chunks the image has room for
   int32_t parts;      // CTAs (one query each) or pairs of CTAs that share the chunks
   void* ws;
+  // trees: group_start has their first tokens, n_entries [G] the contexts, shared_max the bound of those
+  const int32_t* parent;
+  int32_t max_tokens, entries;
+  uint64_t* kin;      // [B] itself and its ancestors, bit t token t of the request
+  int32_t* depth;     // [B] how many ancestors; + kBadParent where the parent is none
 };
+constexpr int32_t kBadParent = INT32_MIN;
 
 // whether a batch runs every query by itself
 __host__ __device__ __forceinline__ bool by_itself(int32_t B, int32_t G, int64_t shared_max) {
@@ -200,7 +212,25 @@ __device__ __forceinline__ int image_chunks(int n, int ns) {
   return n < kImageQueries ? 0 : (ns + kChunk - 1) / kChunk;
 }
 
-template <bool kAloneQueries>
+// trees: whether a request's first and last token are in order, its context, and chunks of that which are widened once
+// (whole ones: every query sees all of them)
+__device__ __forceinline__ bool tree_ok(const PrefixArgs& a, int lo, int hi) {
+  return lo >= 0 && hi >= lo && hi <= a.B && hi - lo <= a.max_tokens;
+}
+__device__ __forceinline__ int tree_context(const PrefixArgs& a, int g) { return min(max(a.n_entries[g], 0), a.shared_max); }
+__device__ __forceinline__ int tree_image_chunks(int tokens, int n) { return tokens < kImageQueries ? 0 : n / kChunk; }
+// the largest i in [0, n) with list[i] <= x, list[0] <= x
+__device__ __forceinline__ int last_at_most(const int32_t* list, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <bool kAloneQueries, bool kTree>
 __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, int smem_ints) {
   __shared__ int s_warp[kPrepThreads / 32];
   __shared__ int s_bad;
@@ -215,12 +245,14 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   for (int g0 = 0; g0 < a.G; g0 += kPrepThreads) {
     const int g = g0 + tid;
     const int lo = g < a.G ? a.group_start[g] : 0, hi = g < a.G ? a.group_start[g + 1] : 0;
-    const bool bad = lo < 0 || hi < lo || hi > a.B, any = !bad && lo < hi;
+    const bool bad = kTree ? !tree_ok(a, lo, hi) : lo < 0 || hi < lo || hi > a.B, any = !bad && lo < hi;
     if (bad) {
       s_bad = 1;
       report_error(a.ws, CSA2_ERR_INDEX_RANGE, g);
     }
-    const int2 sh = shared_of(a, any, g, lo, hi);
+    int2 sh = make_int2(0, 0);
+    if constexpr (!kTree) sh = shared_of(a, any, g, lo, hi);
+    else if (any) sh = make_int2(tree_context(a, g), hi - lo);
     if (any) gshared[g] = sh;
   }
   __syncthreads();
@@ -246,7 +278,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   int images = 0;
   for (int g0 = 0; !kAloneQueries && g0 < G; g0 += kPrepThreads) {
     const int g = g0 + tid, size = g < G ? a.group_start[g + 1] - a.group_start[g] : 0;
-    const int n = size > 0 ? image_chunks(size, gshared[g].y) : 0;
+    const int n = size <= 0 ? 0 : kTree ? tree_image_chunks(size, gshared[g].x) : image_chunks(size, gshared[g].y);
     int total;
     const int at = images + block_scan(n, s_warp, &total);
     if (g < G) a.gimage[g] = n > 0 && at + (int64_t)n <= a.image_cap ? at : -1;
@@ -258,7 +290,22 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
     const int p = p0 + tid;
     Pair x{};
     int n = 0;
-    if (kAloneQueries && p < np) {  // a query by itself, in chunks of kOwnChunk rows
+    auto tree_rows = [&](int g) {  // request g's, in chunks
+      x.first = g;
+      x.own0 = a.group_start[g];
+      x.vis0 = gshared[g].x;
+      x.vis1 = gshared[g].y;
+      x.ns = x.vis0 + (a.entries ? x.vis1 : 0);
+      constexpr int kPer = kAloneQueries ? kOwnChunk : kChunk;
+      n = x.nshared = (x.ns + (a.n_swa > 0 ? a.n_swa + x.vis1 : 0) + kPer - 1) / kPer;
+    };
+    if (kTree && kAloneQueries) {
+      if (p < np) {
+        x.q0 = p;
+        x.q1 = x.image = -1;
+        if (G > 0 && p >= a.group_start[0] && p < a.group_start[G]) tree_rows(last_at_most(a.group_start, G, p));
+      }
+    } else if (kAloneQueries && p < np) {  // a query by itself, in chunks of kOwnChunk rows
       x.q0 = x.first = p;
       x.q1 = x.image = -1;
       if (G > 0 && p >= a.group_start[0] && p < a.group_start[G]) {
@@ -288,12 +335,15 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
       x.first = first;
       x.image = -1;
       if (lo >= 1 && lo <= G) {
-        x.first = gshared[lo - 1].x;
-        x.ns = gshared[lo - 1].y;
+        if (kTree) tree_rows(lo - 1);
+        else {
+          x.first = gshared[lo - 1].x;
+          x.ns = gshared[lo - 1].y;
+        }
         x.image = a.gimage[lo - 1];
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < (kTree ? 0 : 2); ++i) {
         const int q = i ? x.q1 : x.q0;
         if (q < 0) continue;
         const int c = visible(a, q);
@@ -305,10 +355,12 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
         (i ? x.vis1 : x.vis0) = min(x.ns, c);
         (i ? x.own1 : x.own0) = own;
       }
-      x.nshared = (max(x.vis0, x.vis1) + kChunk - 1) / kChunk;
-      x.paired = x.q1 >= 0 ? (min(x.own0, x.own1) + a.n_swa + kOwnChunk - 1) / kOwnChunk : 0;
-      const int alone = max(x.own0, x.own1) + a.n_swa - x.paired * kOwnChunk;
-      n = x.nshared + x.paired + (max(alone, 0) + kChunk - 1) / kChunk;
+      if (!kTree) {
+        x.nshared = (max(x.vis0, x.vis1) + kChunk - 1) / kChunk;
+        x.paired = x.q1 >= 0 ? (min(x.own0, x.own1) + a.n_swa + kOwnChunk - 1) / kOwnChunk : 0;
+        const int alone = max(x.own0, x.own1) + a.n_swa - x.paired * kOwnChunk;
+        n = x.nshared + x.paired + (max(alone, 0) + kChunk - 1) / kChunk;
+      }
     }
     int total;
     x.chunk0 = chunks + block_scan(n, s_warp, &total);
@@ -402,6 +454,13 @@ struct PrefixKernel {
   const int64_t *win_pos, *win_lo;
   const Pair* pairs;
   const Part* parts;
+  // trees: kin and depth (PrefixArgs) and position of each query; swa and win_pos, n_ring rows, are the requests' rings,
+  // draft the tokens' window rows, which count behind those as window rows n_ring + query
+  const uint64_t* kin;
+  const int32_t* depth;
+  const int64_t* q_pos;
+  const uint8_t* draft;
+  int32_t n_ring;
   uint4* part_o;    // [pairs + clusters][2][32 Vec8::kWords][128]: eight channels of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
@@ -449,6 +508,60 @@ __device__ __forceinline__ RowRef find_row(const PrefixKernel& k, const Pair& x,
     idx = x.paired * kOwnChunk + (jo - x.paired) * kChunk + i;
   }
   return find_own(k, h ? x.q1 : x.q0, h ? x.own1 : x.own0, idx, x.ns);
+}
+// row idx of a request's (trees): entries, ring, drafts' window rows
+__device__ __forceinline__ RowRef find_tree(const PrefixKernel& k, const Pair& x, int idx) {
+  if (idx < x.ns) return find_entry(k, x.first, idx);
+  idx -= x.ns;
+  if (idx < k.n_swa) return RowRef{0, kNoRow - 1 - (x.first * k.n_swa + idx)};
+  idx -= k.n_swa;
+  if (k.n_swa == 0 || idx >= x.vis1) return RowRef{0, kNoRow};
+  return RowRef{0, kNoRow - 1 - (k.n_ring + x.own0 + idx)};
+}
+// What a query sees of its request's rows behind the context (trees).
+struct Sight {
+  uint64_t kin;
+  int32_t depth;
+  int64_t pos;
+};
+// of query q, by all lanes of a warp; a parent that is none is reported
+__device__ __forceinline__ Sight sight_of(const PrefixKernel& k, int q, int lane) {
+  if (q < 0) return Sight{0, 0, 0};
+  Sight v{__ldg(k.kin + q), __ldg(k.depth + q), k.q_pos ? __ldg(k.q_pos + q) : 0};
+  if (v.depth < 0) {
+    if (lane == 0) report_error(k.ws, CSA2_ERR_INDEX_RANGE, q);
+    v.depth -= kBadParent;
+  }
+  return v;
+}
+// whether it sees row idx, one behind the context
+__device__ __forceinline__ bool sees(const PrefixKernel& k, const Pair& x, const Sight& v, int idx) {
+  if (idx < x.ns) return (v.kin >> (idx - x.vis0)) & 1u;
+  idx -= x.ns;
+  if (idx < k.n_swa) {
+    const int64_t p = __ldg(k.win_pos + x.first * k.n_swa + idx);
+    return p >= max(v.pos - k.n_swa + 1, (int64_t)0) && p < v.pos - v.depth;
+  }
+  idx -= k.n_swa;
+  if (idx >= x.vis1 || !((v.kin >> idx) & 1u)) return false;
+  // a window of CSA2_MAX_TREE tokens holds any path
+  return k.n_swa >= CSA2_MAX_TREE || v.depth - (__ldg(k.depth + x.own0 + idx) & ~kBadParent) < k.n_swa;
+}
+// A row's bit 30 tells a CTA of a pair whether its query sees it (trees): as it is, the bit is bit 31's copy (entries
+// are fewer than 2^30, window rows than 2^24).
+__device__ __forceinline__ int flip_seen(int r) { return r ^ 1 << 30; }
+__device__ __forceinline__ bool seen(int r) { return (r ^ (int)((uint32_t)r << 1)) >= 0; }
+// whether a row of a chunk counts in the softmax
+template <bool kTree>
+__device__ __forceinline__ bool counts(int r) {
+  return r != kNoRow && (!kTree || seen(r));
+}
+// window row r (< kNoRow)
+template <bool kTree>
+__device__ __forceinline__ const uint8_t* window_row(const PrefixKernel& k, int r) {
+  const int w = kNoRow - 1 - r;
+  if (kTree && w >= k.n_ring) return k.draft + (int64_t)(w - k.n_ring) * kDMain;
+  return k.swa + (int64_t)w * kDMain;
 }
 // a page outside the planes is skipped, and reported by the warp that is told to
 __device__ __forceinline__ int resolve(const PrefixKernel& k, RowRef r, bool report) {
@@ -499,12 +612,13 @@ struct Fetch {
   uint32_t scales;
 };
 // Starts the loads of 32-channel block cb of row r.
+template <bool kTree>
 __device__ __forceinline__ void fetch(Fetch& f, const PrefixKernel& k, int r, int cb) {
   if (r >= 0) {
     f.codes = __ldg(reinterpret_cast<const uint4*>(k.kv_codes + (int64_t)r * 256) + cb);
     f.scales = __ldg(reinterpret_cast<const uint16_t*>(k.kv_scales + (int64_t)r * 32) + cb);
   } else if (r < kNoRow) {
-    const uint4* src = reinterpret_cast<const uint4*>(k.swa + (int64_t)(kNoRow - 1 - r) * kDMain) + 2 * cb;
+    const uint4* src = reinterpret_cast<const uint4*>(window_row<kTree>(k, r)) + 2 * cb;
     f.codes = __ldg(src);
     f.more = __ldg(src + 1);
   }
@@ -611,6 +725,7 @@ __device__ __forceinline__ void copy_piece(PrefixSmem& S, const ImageMaps& maps,
 // one of x_free.  The odd CTA's x_full too has phases of rows alone, which are passed on.  Both operands run the same code: the
 // kernel's loops have to fit the instruction cache (unrolled by piece and operand they waited more for instructions
 // than for data).
+template <bool kTree>
 __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, const ImageMaps& maps, int rank,
                                           int chunks, int w, int lane) {
   const int op = w >> 3, group = (w >> 2) & 1;
@@ -644,7 +759,8 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         r[u] = S.rows[slot][row0 + row_step * i + row_u * u];
-        fetch(f[u], k, r[u], blk0 + blk_step * i + blk_u * u);
+        if (kTree && !seen(r[u])) r[u] = flip_seen(r[u]);
+        fetch<kTree>(f[u], k, r[u], blk0 + blk_step * i + blk_u * u);
       }
     }
     if (st & 1) {
@@ -694,9 +810,10 @@ __device__ __forceinline__ bool rows_role(PrefixSmem& S, const PrefixKernel& k, 
 
 // A row's bytes into L2: the row warps fetch half a chunk ahead, which memory's latency exceeds (without this,
 // prefix ragged 101 on 4001 took 70.7 us instead of 66.2, 32 on 8192 51.0 instead of 49.4).
+template <bool kTree>
 __device__ __forceinline__ void prefetch_row(const PrefixKernel& k, int r) {
   if (r == kNoRow) return;
-  const uint8_t* at = r >= 0 ? k.kv_codes + (int64_t)r * 256 : k.swa + (int64_t)(kNoRow - 1 - r) * kDMain;
+  const uint8_t* at = r >= 0 ? k.kv_codes + (int64_t)r * 256 : window_row<kTree>(k, r);
   ptx::prefetch_l2(at);
   ptx::prefetch_l2(at + 128);
   if (r >= 0) {
@@ -709,21 +826,27 @@ __device__ __forceinline__ void prefetch_row(const PrefixKernel& k, int r) {
 
 // Whether chunk c of a pair is copied from the image, which serves both operands: only where both queries see all of
 // the chunk's entries.
+template <bool kTree>
 __device__ __forceinline__ bool from_image(const Pair& x, int c) {
+  if (kTree) return x.image >= 0 && (c + 1) * kChunk <= x.vis0;
   const int seen = x.q1 >= 0 ? min(x.vis0, x.vis1) : x.vis0;
   return x.image >= 0 && c < x.nshared && min((c + 1) * kChunk, x.ns) <= seen;
 }
 
 // Where each chunk's rows come from (or its chunk of the image), by one warp (lane l rows l, 32 + l, ..) up to
 // four chunks ahead of the row and softmax warps.  Pages outside the planes are reported here.
+template <bool kTree>
 __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k, const Pair& x, int rank, int c0,
                                            int nc, int lane, uint32_t n) {
   const bool report = rank == 0;
   bool good = true;
   RowRef r[4];
+  const int qme = rank ? x.q1 : x.q0;
+  const Sight sight = kTree ? sight_of(k, qme, lane) : Sight{};
   auto find = [&](int j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = find_row(k, x, c0 + j, 32 * i + lane);
+    for (int i = 0; i < 4; ++i)
+      r[i] = kTree ? find_tree(k, x, (c0 + j) * kChunk + 32 * i + lane) : find_row(k, x, c0 + j, 32 * i + lane);
   };
   find(0);
 #pragma unroll 1
@@ -732,15 +855,22 @@ __device__ __forceinline__ bool index_role(PrefixSmem& S, const PrefixKernel& k,
     if (m >= 4) good = ptx::mbar_wait_warp(&S.r_free[slot], ((m >> 2) - 1) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) break;
     if (lane == 0) {
-      S.image[slot] = from_image(x, c0 + j) ? x.image + c0 + j : -1;
+      S.image[slot] = from_image<kTree>(x, c0 + j) ? x.image + c0 + j : -1;
       ptx::mbar_arrive(&S.i_full[slot]);
     }
     int row[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) row[i] = resolve(k, r[i], report);
-    if (x.image < 0 || c0 + j >= x.nshared) {  // each CTA half of the rows
-      prefetch_row(k, rank ? row[1] : row[0]);
-      prefetch_row(k, rank ? row[3] : row[2]);
+    if (kTree ? !from_image<kTree>(x, c0 + j) : x.image < 0 || c0 + j >= x.nshared) {  // each CTA half of the rows
+      prefetch_row<kTree>(k, rank ? row[1] : row[0]);
+      prefetch_row<kTree>(k, rank ? row[3] : row[2]);
+    }
+    if (kTree) {  // both CTAs have the same rows, each its own query's view of them
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int idx = (c0 + j) * kChunk + 32 * i + lane;
+        if (row[i] != kNoRow && !(qme >= 0 && (idx < x.vis0 || sees(k, x, sight, idx)))) row[i] = flip_seen(row[i]);
+      }
     }
     if (j + 1 < nc) find(j + 1);
 #pragma unroll
@@ -815,7 +945,7 @@ __device__ __forceinline__ void store_pair_o(const PrefixKernel& k, uint32_t tme
   }
 }
 
-template <bool kHalf>
+template <bool kHalf, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_constant__ PrefixKernel k,
                                                                   const __grid_constant__ ImageMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -893,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 
   if (warp >= kRowWarp && warp < kSMma) {
     ptx::setmaxnreg_dec<kRowRegs>();
-    good = rows_role(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
+    good = rows_role<kTree>(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
     // the last item's partial is theirs, a quarter of the columns each four: nothing else is left to do
     if (good && t1 > t0) good = wait(&S.last_o, 0);
     if (good && t1 > t0 && S.last_slot >= 0) {
@@ -922,13 +1052,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
     // the pair's chunk c, unless it was copied: by the chunks of rows before it
     uint32_t owns = 0;
     auto pass_rows = [&](int op, const Pair& x, int c) {
-      if (from_image(x, c)) return;
+      if (from_image<kTree>(x, c)) return;
       for (int i = 0; i < kPieces; i += 2) pass(&S.x_full[op][i], owns, 2);
       ++owns;
     };
     if (warp == kIndexWarp) {
       for_items([&](const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
-        good = index_role(S, k, x, rank, c0, nc, lane, n);
+        good = index_role<kTree>(S, k, x, rank, c0, nc, lane, n);
       });
       where = 32;
     } else if (warp == kSMma) {
@@ -1066,15 +1196,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
         if (good && m >= 2) good = wait(&S.p_free[slot], (m >> 1) - 1);
         ptx::tc_fence_after();
         uint32_t mk0 = 0u, mk1 = 0u;
-        if (c0 + j < x.nshared) {  // entries below this query's own count
+        if (kTree) {
+          mk0 = mk1 = ~0u;
+        } else if (c0 + j < x.nshared) {  // entries below this query's own count
           const int left = vis - (c0 + j) * kChunk - 64 * half;
           mk0 = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
           mk1 = left >= 64 ? ~0u : left > 32 ? (1u << (left - 32)) - 1u : 0u;
         } else if (c0 + j - x.nshared < x.paired ? half == rank : (x.own1 > x.own0) == (rank == 1)) {
           mk0 = mk1 = ~0u;
         }
-        mk0 &= __ballot_sync(0xffffffffu, S.rows[m & 3u][64 * half + lane] != kNoRow);
-        mk1 &= __ballot_sync(0xffffffffu, S.rows[m & 3u][64 * half + 32 + lane] != kNoRow);
+        mk0 &= __ballot_sync(0xffffffffu, counts<kTree>(S.rows[m & 3u][64 * half + lane]));
+        mk1 &= __ballot_sync(0xffffffffu, counts<kTree>(S.rows[m & 3u][64 * half + 32 + lane]));
         if (good && lane == 0) ptx::mbar_arrive(&S.r_free[m & 3u]);
         // P with the reference so far (0 before the first row); it stands unless some head's logits
         // exceed it by too much (kMaxExp), then once more with that head's new reference
@@ -1277,6 +1409,7 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
 // bytes for eight rows.  Bytes bound it: 288 read and 1,024 written an entry (65,000 entries: about 20 us, 12 of
 // them the bytes').  The rows of a CTA's next chunk are asked for with this one's (64 on 65000 386.7 us without,
 // 384.1 with).
+template <bool kTree>
 __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKernel& k, uint16_t* image, int first_chunk,
                                              int step) {
   __shared__ int s_warp[kPrepThreads / 32];
@@ -1297,9 +1430,11 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
       for (int g0 = 0; g0 < a.G && base <= t; g0 += kPrepThreads) {
         const int g = g0 + threadIdx.x;
         const int lo = g < a.G ? a.group_start[g] : 0, hi = g < a.G ? a.group_start[g + 1] : 0;
-        const bool any = lo >= 0 && hi <= a.B && hi - lo >= kImageQueries;
-        const int2 sh = shared_of(a, any, g, lo, hi);
-        const int n = any ? image_chunks(hi - lo, sh.y) : 0;
+        const bool any = (kTree ? tree_ok(a, lo, hi) : lo >= 0 && hi <= a.B) && hi - lo >= kImageQueries;
+        int2 sh = make_int2(g, 0);
+        if constexpr (!kTree) sh = shared_of(a, any, g, lo, hi);
+        else if (any) sh.y = tree_context(a, g);
+        const int n = !any ? 0 : kTree ? tree_image_chunks(hi - lo, sh.y) : image_chunks(hi - lo, sh.y);
         int total;
         const int at = base + block_scan(n, s_warp, &total);
         if (n > 0 && at + (int64_t)n <= a.image_cap && t >= at && t < at + n) {
@@ -1317,12 +1452,64 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
     const int r = e < found.y ? row_of(found.x, e) : kNoRow;
     Fetch f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fetch(f[i], k, r, b0 ^ (4 * i));
+    for (int i = 0; i < 4; ++i) fetch<kTree>(f[i], k, r, b0 ^ (4 * i));
     const int64_t next = e + (int64_t)step * kChunk;
-    if (lane < 8 && next < found.y) prefetch_row(k, row_of(found.x, (int)next));
+    if (lane < 8 && next < found.y) prefetch_row<kTree>(k, row_of(found.x, (int)next));
     uint16_t* dst = image + t * kDMain * kChunk + row * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) put(f[i], r, dst + (b0 ^ (4 * i)) * 4 * kChunk * 8, kChunk * 8);
+  }
+}
+
+// Ancestors and depths of the tokens of request g (trees), by a warp: lane l has the tokens l and 32 + l, each at first
+// itself and its parent, and follows the parents in steps of twice the length: six for 64 tokens.
+__device__ __forceinline__ void tree_block(const PrefixArgs& a, int g) {
+  const int lane = threadIdx.x & 31, first = a.group_start[g], end = a.group_start[g + 1];
+  if (!tree_ok(a, first, end)) return;
+  uint32_t lo[2], hi[2];  // tokens 0 .. 31 and 32 .. 63
+  int up[2];
+  bool bad[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = 32 * i + lane;
+    up[i] = t < end - first ? a.parent[first + t] : -1;
+    bad[i] = up[i] < -1 || up[i] >= t;
+    if (bad[i]) up[i] = -1;
+    lo[i] = i == 0 ? 1u << lane : 0u;
+    hi[i] = i == 0 ? 0u : 1u << lane;
+  }
+#pragma unroll
+  for (int s = 0; s < 6; ++s) {
+    uint32_t l[2], h[2];
+    int u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int src = up[i] & 31;  // every lane shuffles
+      auto of = [&](auto(&v)[2]) {
+        const auto v0 = __shfl_sync(0xffffffffu, v[0], src), v1 = __shfl_sync(0xffffffffu, v[1], src);
+        return up[i] >= 32 ? v1 : v0;
+      };
+      l[i] = of(lo);
+      h[i] = of(hi);
+      u[i] = of(up);
+      if (up[i] < 0) {
+        l[i] = h[i] = 0u;
+        u[i] = -1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lo[i] |= l[i];
+      hi[i] |= h[i];
+      up[i] = u[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = 32 * i + lane;
+    if (t >= end - first) continue;
+    a.kin[first + t] = (uint64_t)hi[i] << 32 | lo[i];
+    a.depth[first + t] = __popc(lo[i]) + __popc(hi[i]) - 1 + (bad[i] ? kBadParent : 0);
   }
 }
 
@@ -1330,23 +1517,31 @@ __device__ __forceinline__ void widen_chunks(const PrefixArgs& a, const PrefixKe
 // half the CTAs come first (all behind the queries: 53.4 and 75.1 us for prefix 32 on 8192 and 101 on 4001
 // instead of 50.9 and 71.2).  Two CTAs on an SM: with the 72 registers it would take, one (ragged 101 on 4001
 // 68.5 us instead of 66.0).
+template <bool kTree>
 __global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, PrefixQuery q,
                                                               const __grid_constant__ PrefixKernel k, uint16_t* image) {
   extern __shared__ __align__(16) unsigned char prep_smem[];
   ptx::griddep_launch();
   ptx::griddep_wait();
-  const int stage = kStageCtas * (a.B + 1), widen = (int)gridDim.x - 1 - stage, widen1 = min(widen, kWidenFirst);
+  const int trees = kTree ? (a.G + kTreesPerCta - 1) / kTreesPerCta : 0, stage = kStageCtas * (a.B + 1);
+  const int widen = (int)gridDim.x - 1 - trees - stage, widen1 = min(widen, kWidenFirst);
   int b = (int)blockIdx.x - 1;
   if (b < 0) {
     int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
-    if (by_itself(a.B, a.G, a.shared_max)) plan_block<true>(a, ints, kPrepSmem / 4);
-    else plan_block<false>(a, ints, kPrepSmem / 4);
+    if (by_itself(a.B, a.G, a.shared_max)) plan_block<true, kTree>(a, ints, kPrepSmem / 4);
+    else plan_block<false, kTree>(a, ints, kPrepSmem / 4);
     return;
   }
-  if (b < widen1) return widen_chunks(a, k, image, b, widen);
+  if (b < trees) {
+    const int g = b * kTreesPerCta + (int)(threadIdx.x >> 5);
+    if (g < a.G) tree_block(a, g);
+    return;
+  }
+  b -= trees;
+  if (b < widen1) return widen_chunks<kTree>(a, k, image, b, widen);
   b -= widen1;
   if (b < stage) return stage_block(q, a.B, b / kStageCtas, b % kStageCtas, prep_smem);
-  widen_chunks(a, k, image, widen1 + b - stage, widen);
+  widen_chunks<kTree>(a, k, image, widen1 + b - stage, widen);
 }
 
 // kC consecutive output channels at element `at`
@@ -1571,6 +1766,7 @@ constexpr int kAloneS = 20, kAloneO = 21, kAloneIndex = 22;
 
 // The rows of all `chunks` chunks of this CTA, whatever queries they belong to: thread's row 8 (w % 8) + l % 8,
 // of the blocks (of 32 channels) 8 (w / 8) .. the rotated first and the one four on; codes fetched two chunks ahead.
+template <bool kTree>
 __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, int chunks, int w, int lane) {
   const int half = w >> 3, rl = 8 * (w & 7) + (lane & 7);
   const int b0 = 8 * half + (rotated(lane) & 7), b1 = b0 ^ 4;
@@ -1585,8 +1781,8 @@ __device__ __forceinline__ bool alone_rows(AloneSmem& S, const PrefixKernel& k, 
     good = good && ptx::mbar_wait_warp(&S.r_full[slot], ((uint32_t)m / kRing) & 1u, &S.abort_flag, kWaitBudget);
     if (!good) return;
     r = S.rows[slot][rl];
-    fetch(f[0], k, r, b0);
-    fetch(f[1], k, r, b1);
+    fetch<kTree>(f[0], k, r, b0);
+    fetch<kTree>(f[1], k, r, b1);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.r_free[slot]);
   };
@@ -1636,7 +1832,7 @@ __device__ __forceinline__ void store_alone_o(const AloneSmem& S, const PrefixKe
   }
 }
 
-template <bool kHalf>
+template <bool kHalf, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ PrefixKernel k) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   AloneSmem& S = *reinterpret_cast<AloneSmem*>(smem_raw);
@@ -1698,7 +1894,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   };
 
   if (warp >= 4 && warp < kAloneS) {
-    good = alone_rows(S, k, t1 - t0, warp - 4, lane);
+    good = alone_rows<kTree>(S, k, t1 - t0, warp - 4, lane);
     if (good && t1 > t0) {  // as in k_prefix_attn
       good = wait(&S.last_o, 0);
       if (good) {
@@ -1714,12 +1910,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       ptx::prefetch_l1(&part.pair.ns);  // the record's second half
       for_items([&](int q, const Pair& x, int, int c0, int nc, uint32_t n, uint32_t) {
         const int own = x.own0, ns = x.ns, first = x.first;
+        const Sight sight = kTree ? sight_of(k, q, lane) : Sight{};
         RowRef r[2];
         auto find = [&](int j) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int e = (c0 + j) * kRows + 32 * i + lane;
-            r[i] = e < ns && e < own ? find_entry(k, first, e) : find_own(k, q, own, e);
+            if (kTree) r[i] = e < x.vis0 || sees(k, x, sight, e) ? find_tree(k, x, e) : RowRef{0, kNoRow};
+            else r[i] = e < ns && e < own ? find_entry(k, first, e) : find_own(k, q, own, e);
           }
         };
         find(0);
@@ -1727,8 +1925,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         for (int j = 0; j < nc && good; ++j) {
           const uint32_t m = n + (uint32_t)j, slot = m % kRing;
           const int r0 = resolve(k, r[0], true), r1 = resolve(k, r[1], true);
-          prefetch_row(k, r0);  // paged ragged 48 x 65536: 219 us without, 217 with
-          prefetch_row(k, r1);
+          prefetch_row<kTree>(k, r0);  // paged ragged 48 x 65536: 219 us without, 217 with
+          prefetch_row<kTree>(k, r1);
           if (j + 1 < nc) find(j + 1);
           if (m >= kRing) good = wait(&S.r_free[slot], m / kRing - 1);
           if (!good) break;
@@ -2084,10 +2282,12 @@ struct PrefixWs {
   int64_t image_cap;
   uint4* part_o;
   float2* part_ml;
+  uint64_t* kin;
+  int32_t* depth;
   size_t bytes;
 };
 
-PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
+PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max, bool trees = false) {
   PrefixWs L{};
   size_t off = kWsHeader;
   char* base = (char*)ws;
@@ -2116,6 +2316,10 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max) {
   L.image_cap = alone ? 0 : G * cdiv(shared_max, kChunk);
   if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
   L.image = (uint16_t*)take((size_t)L.image_cap * kChunk * kDMain * 2);
+  if (trees) {
+    L.kin = (uint64_t*)take((size_t)B * 8);
+    L.depth = (int32_t*)take((size_t)B * 4);
+  }
   L.bytes = off;
   return L;
 }
@@ -2155,31 +2359,12 @@ bool pages_ok(const csa2_pages* p, const csa2_kv_planes* kv, int64_t n) {
   return n <= (int64_t)p->max_pages * kv->seq_stride;
 }
 
-// Attention of B queries through page tables, G groups of them sharing prefixes (G = 0: none).
-csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B, const int32_t* n_entries, int32_t G,
-                       const int32_t* group_start, const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
-                       const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
-                       const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
-                       void* out, int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
-  if (!n_entries || !aligned(n_entries, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out || !aligned(q_bf16, 16) ||
-      !aligned(out, 16) || (swa_e4m3 && !aligned(swa_e4m3, 16)) || (lse_out && !aligned(lse_out, 4)))
-    return CSA2_ERR_INVALID_ARG;
-  if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
-  AttnExtras ex;
-  const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
-  if (bad != CSA2_OK) return bad;
-  if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
-  const bool alone = by_itself(B, G, n_shared_max);
-  const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
-  if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
-  cudaStream_t st = (cudaStream_t)stream;
-  const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
-                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.gshared, L.image_cap, alone ? kAlone : kClusters, ws};
-  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
-                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
-                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
-                       L.pairs, L.parts, L.part_o, L.part_ml, ws};
+// The launches of a call: preparation, attention, join.
+template <bool kTree>
+csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs& L, const AttnExtras& ex, const void* q_bf16,
+                      float softmax_scale, const float* sink, void* out, int32_t out_type, float* lse_out, cudaStream_t st) {
+  const int32_t B = a.B;
+  const bool alone = by_itself(B, a.G, a.shared_max);
   // bf16 queries are exact in f16 unless they were normalised or rotated
   uint16_t* const rest = lse_out && (ex.qnorm_w || ex.rope) ? L.rest : nullptr;
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
@@ -2198,22 +2383,24 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   auto run = [&](auto half) {  // parts in f16 for a bf16 output (Vec8)
     constexpr bool kHalf = decltype(half)::value;
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (cudaFuncSetAttribute(k_prefix_prep, attr, kPrepSmem) != cudaSuccess ||
-        (alone ? cudaFuncSetAttribute(k_paged_attn<kHalf>, attr, (int)sizeof(AloneSmem))
-               : cudaFuncSetAttribute(k_prefix_attn<kHalf>, attr, (int)sizeof(PrefixSmem))) != cudaSuccess)
+    const auto prep = k_prefix_prep<kTree>;
+    if (cudaFuncSetAttribute(prep, attr, kPrepSmem) != cudaSuccess ||
+        (alone ? cudaFuncSetAttribute(k_paged_attn<kHalf, kTree>, attr, (int)sizeof(AloneSmem))
+               : cudaFuncSetAttribute(k_prefix_attn<kHalf, kTree>, attr, (int)sizeof(PrefixSmem))) != cudaSuccess)
       return launch_status();
     {
       KernelTimer timer("k_prefix_prep", st);
+      const int trees = kTree ? (a.G + kTreesPerCta - 1) / kTreesPerCta : 0;
       const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
       // without its plan the attention would run whatever one the workspace held, and the join its parts
-      if (launch_pdl(k_prefix_prep, dim3((unsigned)(1 + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
+      if (launch_pdl(prep, dim3((unsigned)(1 + trees + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
                      (size_t)kPrepSmem, st, a, pq, k, L.image) != cudaSuccess)
         return launch_status();
     }
     if (alone) {
       {
         KernelTimer timer("k_paged_attn", st);
-        if (launch_pdl(k_paged_attn<kHalf>, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k) != cudaSuccess)
+        if (launch_pdl(k_paged_attn<kHalf, kTree>, dim3(kAlone), dim3(kThreads), sizeof(AloneSmem), st, k) != cudaSuccess)
           return launch_status();
       }
       KernelTimer timer("k_paged_merge", st);
@@ -2223,7 +2410,7 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     }
     {
       KernelTimer timer("k_prefix_attn", st);
-      if (launch_clusters(k_prefix_attn<kHalf>, dim3(2 * kClusters), dim3(kThreads), 2, 1, sizeof(PrefixSmem), st, k,
+      if (launch_clusters(k_prefix_attn<kHalf, kTree>, dim3(2 * kClusters), dim3(kThreads), 2, 1, sizeof(PrefixSmem), st, k,
                           maps) != cudaSuccess)
         return launch_status();
     }
@@ -2233,6 +2420,33 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
     return launch_status();
   };
   return out_type == CSA2_OUT_BF16 ? run(std::true_type{}) : run(std::false_type{});
+}
+
+// Attention of B queries through page tables, G groups of them sharing prefixes (G = 0: none).
+csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_t B, const int32_t* n_entries, int32_t G,
+                       const int32_t* group_start, const int32_t* n_shared, int64_t n_shared_max, int64_t n_own_max,
+                       const uint8_t* swa_e4m3, int32_t n_swa, const void* q_bf16, float softmax_scale,
+                       const csa2_norm_rope* q_nr, const int64_t* q_pos, const float* sink, const csa2_window* win,
+                       void* out, int32_t out_type, float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream) {
+  if (!n_entries || !aligned(n_entries, 4) || (n_swa > 0 && !swa_e4m3) || !q_bf16 || !out || !aligned(q_bf16, 16) ||
+      !aligned(out, 16) || (swa_e4m3 && !aligned(swa_e4m3, 16)) || (lse_out && !aligned(lse_out, 4)))
+    return CSA2_ERR_INVALID_ARG;
+  if (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16) return CSA2_ERR_INVALID_ARG;
+  AttnExtras ex;
+  const csa2_status bad = attn_extras(q_nr, q_pos, sink, win, n_swa, softmax_scale, &ex);
+  if (bad != CSA2_OK) return bad;
+  if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+  const bool alone = by_itself(B, G, n_shared_max);
+  const PrefixWs L = prefix_ws(ws, B, G, n_shared_max);
+  if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
+  const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
+                     L.gimage, L.gshared, L.image_cap, alone ? kAlone : kClusters, ws, nullptr, 0, 0, nullptr, nullptr};
+  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
+                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
+                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
+                       L.pairs, L.parts, nullptr, nullptr, nullptr, nullptr, 0, L.part_o, L.part_ml, ws};
+  return attn_call<false>(a, k, L, ex, q_bf16, softmax_scale, sink, out, out_type, lse_out, (cudaStream_t)stream);
 }
 
 }  // namespace
@@ -2272,4 +2486,54 @@ extern "C" csa2_status csa2_prefix_attn_decode(const csa2_kv_planes* kv, const c
   if (!group_start || !n_shared || !aligned(group_start, 4) || !aligned(n_shared, 4)) return CSA2_ERR_INVALID_ARG;
   return prefix_run(kv, pages, B, n_entries, G, group_start, n_shared, n_shared_max, n_own_max, swa_e4m3, n_swa, q_bf16,
                     softmax_scale, q_nr, q_pos, sink, win, out, out_type, lse_out, ws, ws_bytes, stream);
+}
+
+extern "C" size_t csa2_tree_attn_workspace_size(int32_t R, int32_t B, int32_t max_tokens, int64_t n_max, int32_t n_swa) {
+  if (R <= 0 || R > 65535 || B <= 0 || B > 65535 || max_tokens < 1 || max_tokens > CSA2_MAX_TREE || n_max < 0 ||
+      n_max > CSA2_MAX_DENSE || n_swa < 0)
+    return 0;
+  return csa2::prefix_ws(nullptr, B, R, n_max, true).bytes;
+}
+
+extern "C" csa2_status csa2_tree_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
+                                             const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
+                                             const int64_t* swa_pos, const uint8_t* draft_e4m3, int32_t n_swa,
+                                             const void* q_bf16, const int64_t* q_pos, float softmax_scale,
+                                             const csa2_norm_rope* q_nr, const csa2_rope_scaling* scaling,
+                                             const float* sink, void* out, int32_t out_type, float* lse_out, void* ws,
+                                             size_t ws_bytes, csa2_stream stream) {
+  using namespace csa2;
+  if (!trees || !trees->start || !trees->parent || !aligned(trees->start, 4) || !aligned(trees->parent, 4) ||
+      trees->R <= 0 || trees->R > 65535 || trees->B <= 0 || trees->B > 65535 || trees->max_tokens < 1 ||
+      trees->max_tokens > CSA2_MAX_TREE)
+    return CSA2_ERR_INVALID_ARG;
+  const int32_t R = trees->R, B = trees->B;
+  if (!planes_ok(kv) || n_max < 0 || n_max > CSA2_MAX_DENSE || n_swa < 0 || n_swa > CSA2_MAX_SWA ||
+      !pages_ok(pages, kv, n_max + (trees->entries ? trees->max_tokens : 0)) ||
+      (int64_t)pages->n_pages * kv->seq_stride > 1 << 30)
+    return CSA2_ERR_INVALID_ARG;
+  if (!n_entries || !aligned(n_entries, 4) || !q_bf16 || !out || !aligned(q_bf16, 16) || !aligned(out, 16) ||
+      (lse_out && !aligned(lse_out, 4)) || (out_type != CSA2_OUT_F32 && out_type != CSA2_OUT_BF16))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_swa > 0 && (!swa_e4m3 || !swa_pos || !draft_e4m3 || !q_pos || !aligned(swa_e4m3, 16) || !aligned(swa_pos, 8) ||
+                    !aligned(draft_e4m3, 16)))
+    return CSA2_ERR_INVALID_ARG;
+  if (!scaling_ok(scaling)) return CSA2_ERR_INVALID_ARG;
+  AttnExtras ex;
+  const csa2_status bad = attn_extras(q_nr, q_pos, sink, nullptr, n_swa, softmax_scale, &ex);
+  if (bad != CSA2_OK) return bad;
+  if (ex.rope) make_thetas(ex.th.t, 64, q_nr->rope_base, scaling);
+  if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
+  const PrefixWs L = prefix_ws(ws, B, R, n_max, true);
+  if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
+  const PrefixArgs a{B, R, n_entries, trees->start, nullptr, (int32_t)n_max, 0, n_swa,
+                     (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
+                     L.gimage, L.gshared, L.image_cap, by_itself(B, R, n_max) ? kAlone : kClusters, ws,
+                     trees->parent, trees->max_tokens, trees->entries, L.kin, L.depth};
+  const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
+                       pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
+                       ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, swa_pos, nullptr,
+                       L.pairs, L.parts, L.kin, L.depth, n_swa > 0 ? q_pos : nullptr, draft_e4m3, R * n_swa,
+                       L.part_o, L.part_ml, ws};
+  return attn_call<true>(a, k, L, ex, q_bf16, softmax_scale, sink, out, out_type, lse_out, (cudaStream_t)stream);
 }

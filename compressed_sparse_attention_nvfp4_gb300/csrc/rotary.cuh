@@ -36,25 +36,33 @@ inline bool rotary_ok(const csa2_rotary* r, int64_t dim) {
   return isfinite(r->magnitude) && scaling_ok(&r->scaling);
 }
 
-// the pairs' theta / 2 pi of a rotation of n channels
-template <int kPairs>
-inline void make_turns(Turns<kPairs>* t, int n, double base, const csa2_rope_scaling* s) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
+// theta of the pairs of a rotation of n channels
+inline void make_thetas(double* t, int n, double base, const csa2_rope_scaling* s) {
   const int kind = s ? s->kind : CSA2_SCALE_NONE;
   double lo = 0.0, width = 1.0;
   if (kind == CSA2_SCALE_YARN) {
-    const auto at = [&](double turns) { return n * log((double)s->original / (turns * kTwoPi)) / (2.0 * log(base)); };
+    const auto at = [&](double turns) {
+      return n * log((double)s->original / (turns * 2.0 * 3.14159265358979323846)) / (2.0 * log(base));
+    };
     lo = fmax(floor(at(s->beta_fast)), 0.0);
     width = fmax(fmin(ceil(at(s->beta_slow)), n - 1.0) - lo, 1e-3);
   }
   for (int i = 0; i < n / 2; ++i) {
-    double theta = pow(base, -2.0 * i / n);
-    if (kind == CSA2_SCALE_LINEAR) theta /= (double)s->factor;
+    t[i] = pow(base, -2.0 * i / n);
+    if (kind == CSA2_SCALE_LINEAR) t[i] /= (double)s->factor;
     if (kind == CSA2_SCALE_YARN) {
       const double ramp = fmin(fmax((i - lo) / width, 0.0), 1.0);
-      theta = theta * (1.0 - ramp) + theta / (double)s->factor * ramp;
+      t[i] = t[i] * (1.0 - ramp) + t[i] / (double)s->factor * ramp;
     }
-    const double turns = theta / kTwoPi;
+  }
+}
+// theta / 2 pi of the pairs, as fractions of a turn
+template <int kPairs>
+inline void make_turns(Turns<kPairs>* t, int n, double base, const csa2_rope_scaling* s) {
+  double theta[kPairs];
+  make_thetas(theta, n, base, s);
+  for (int i = 0; i < n / 2; ++i) {
+    const double turns = theta[i] / 6.283185307179586476925286766559;
     t->f[i] = (uint64_t)((turns - floor(turns)) * 0x1p64);
   }
 }

@@ -622,6 +622,36 @@ typedef struct {
 } csa2_trees;
 #define CSA2_MAX_TREE 64
 
+/* csa2_paged_attn_decode for trees of drafted tokens: query b of request g attends to entries [0, n_entries[g]) of the
+ * request, to its own and its ancestors' entries behind them (trees->entries), and to its window: the last n_swa
+ * tokens on its path.  Rows of a request are read once for several of its queries.
+ *   pages      row g of the table is request g's: [R][max_pages]
+ *   n_entries  [R] int32 (device): entries of the context, without the drafts'; values above n_max count as n_max,
+ *              negative ones as 0.  0 <= n_max, n_max + max_tokens (where entries) <= max_pages * seq_stride;
+ *              n_max <= CSA2_MAX_DENSE
+ *   swa_e4m3   [R][n_swa][512], swa_pos [R][n_swa] int64: the requests' rings and their rows' positions
+ *              (csa2_swa_append); query b, at depth d (0 below the request's last token), sees rows at positions
+ *              [max(q_pos[b] - n_swa + 1, 0), q_pos[b] - d): rows of earlier drafts that stand there are not seen
+ *   draft_e4m3 [B][512]: window rows of the drafted tokens; query b sees its own and those of ancestors less than
+ *              n_swa tokens back.  Required with n_swa > 0, as swa_e4m3 and swa_pos; n_swa = 0: no window
+ *   q_pos      [B] int64, required with n_swa > 0 or a rotation: a token's position (its request's first draft's
+ *              plus its depth)
+ *   scaling    (or NULL) of q_nr's rotation
+ *   out        [B][64][512] of out_type; lse_out [B][64] or NULL
+ * Queries outside every tree see no rows.  A start that is not in order within [0, B], or a tree of more than max_tokens
+ * tokens, is reported as CSA2_ERR_INDEX_RANGE (detail: such a request), and no query of the call sees any row; a parent
+ * outside [-1, own index) is reported (detail: the query) and counts as -1.  Pages outside the planes, NaN, roundings, sink and repeated calls
+ * as in csa2_paged_attn_decode.  1 <= R <= 65535, 1 <= B <= 65535, n_pages * seq_stride <= 2^30; ws:
+ * csa2_tree_attn_workspace_size(R, B, max_tokens, n_max, n_swa) bytes.  As in csa2_prefix_attn_decode the host's bounds
+ * decide whether the queries of a request run in pairs, and whether its context is widened once for all of them. */
+csa2_status csa2_tree_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
+                                  const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
+                                  const int64_t* swa_pos, const uint8_t* draft_e4m3, int32_t n_swa, const void* q_bf16,
+                                  const int64_t* q_pos, float softmax_scale, const csa2_norm_rope* q_nr,
+                                  const csa2_rope_scaling* scaling, const float* sink, void* out, int32_t out_type,
+                                  float* lse_out, void* ws, size_t ws_bytes, csa2_stream stream);
+size_t csa2_tree_attn_workspace_size(int32_t R, int32_t B, int32_t max_tokens, int64_t n_max, int32_t n_swa);
+
 /* Commit of the accepted tokens of each tree, after csa2_tree_attn_decode and the sampler: token path[g][i], i <
  * n_accept[g], is the i-th token that request g keeps.
  *   trees      as in the attention; parent is not read and may be NULL

@@ -96,6 +96,48 @@ def test_tree_commit_workspace():
     assert commit(draft=None, pos=None, ring=None, ring_pos=None, n_win=0, ws=None) == 3
 
 
+TREES = csa2.Trees(16, 16, 4, 20, 8, 1)
+
+
+def attn(kv=FAKE, pages=csa2.Pages(16, 8, 32), trees=TREES, n=16, n_max=100, swa=256, swa_pos=16, draft=256, n_swa=128, q=256,
+         q_pos=16, scale=0.04, nr=None, scaling=None, sink=None, out=256, out_type=1, lse=None, ws=256, ws_bytes=1 << 40):
+    return csa2.lib().csa2_tree_attn_decode(ref(kv), ref(pages), ref(trees), n, n_max, swa, swa_pos, draft, n_swa, q, q_pos, scale,
+                                            ref(nr), ref(scaling), sink, out, out_type, lse, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad", [dict(kv=None), dict(kv=csa2.KVPlanes(None, 256, 256, 256, 64)),
+                                 dict(kv=csa2.KVPlanes(256, 256, 256, 256, 0)), dict(kv=csa2.KVPlanes(256, 256, 256, 256, 1 << 31)),
+                                 dict(pages=None), dict(pages=csa2.Pages(None, 8, 32)), dict(pages=csa2.Pages(18, 8, 32)),
+                                 dict(pages=csa2.Pages(16, -1, 32)), dict(pages=csa2.Pages(16, 8, -1)),
+                                 dict(pages=csa2.Pages(16, 1, 32)), dict(pages=csa2.Pages(16, 8, 1 << 25)),
+                                 dict(n_max=505), dict(n_max=512, trees=csa2.Trees(16, 16, 4, 20, 1, 1)), dict(trees=None),
+                                 dict(trees=csa2.Trees(None, 16, 4, 20, 8, 1)), dict(trees=csa2.Trees(16, None, 4, 20, 8, 1)),
+                                 dict(trees=csa2.Trees(18, 16, 4, 20, 8, 1)), dict(trees=csa2.Trees(16, 18, 4, 20, 8, 1)),
+                                 dict(trees=csa2.Trees(16, 16, 0, 20, 8, 1)), dict(trees=csa2.Trees(16, 16, 65536, 20, 8, 1)),
+                                 dict(trees=csa2.Trees(16, 16, 4, 0, 8, 1)), dict(trees=csa2.Trees(16, 16, 4, 65536, 8, 1)),
+                                 dict(trees=csa2.Trees(16, 16, 4, 20, 0, 1)), dict(trees=csa2.Trees(16, 16, 4, 20, 65, 1)),
+                                 dict(n=None), dict(n=18), dict(n_max=-1), dict(n_max=65537), dict(n_swa=-1), dict(n_swa=129),
+                                 dict(swa=None), dict(swa=264), dict(swa_pos=None), dict(swa_pos=20), dict(draft=None),
+                                 dict(draft=264), dict(q=None), dict(q=264), dict(q_pos=None), dict(q_pos=20), dict(scale=0.0),
+                                 dict(scale=NAN), dict(scale=INF), dict(nr=csa2.norm_rope(8, 1e-6)),
+                                 dict(nr=csa2.norm_rope(None, 1e-6, True), q_pos=None, n_swa=0), dict(sink=18), dict(out=None),
+                                 dict(out=264), dict(out_type=2), dict(lse=18)] + [dict(scaling=s) for s in BAD_SCALINGS])
+def test_tree_attn_refuses(bad):
+    assert attn(**bad) == 1
+
+
+def test_tree_attn_workspace():
+    need = csa2.tree_attn_workspace_size(4, 20, 8, 100, 128)
+    assert need > 0 and need % 256 == 0
+    assert attn(ws=None) == 3 and attn(ws=128) == 3 and attn(ws_bytes=need - 1) == 3
+    # right for a window that is not there, a table that just holds the bound, drafts without entries
+    assert attn(swa=None, swa_pos=None, draft=None, q_pos=None, n_swa=0, ws=None) == 3
+    assert attn(n_max=504, ws=None) == 3 and attn(n_max=512, trees=csa2.Trees(16, 16, 4, 20, 8, 0), ws=None) == 3
+    for bad in ((0, 20, 8, 100, 128), (4, 0, 8, 100, 128), (65536, 20, 8, 100, 128), (4, 65536, 8, 100, 128), (4, 20, 0, 100, 128),
+                (4, 20, 65, 100, 128), (4, 20, 8, -1, 128), (4, 20, 8, 65537, 128), (4, 20, 8, 100, -1)):
+        assert csa2.tree_attn_workspace_size(*bad) == 0
+
+
 def refused(call):
     with pytest.raises(csa2.Csa2Error) as e:
         call()
