@@ -2,8 +2,10 @@
 //
 // Row r's main copy: y = w x / sqrt(mean(x^2) + eps), the last 64 channels turned by pos, rounded to fp32 once, then
 // the cache's codec; its indexer key: turned by pos, then the codec.  The codec's borders make the bytes depend on the
-// last bits of y: with y formed in fp32, off by a few 2^-24, one code in five million falls to the other side, several
-// in a prefill chunk; formed in pairs of fp32 (rotary.cuh), off by 2^-36, the bytes are those of the definition.
+// last bits of y: from a y formed in fp32, off by up to 2^-19, a code in some thousand rows falls to the other side.  So
+// a row is formed in fp32 first, with every value's code taken at both ends of what it may be; where the ends agree,
+// the byte is certain.  Where one does not (one row in twenty after a norm), the row is formed again in pairs of fp32
+// (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
 //
 // A warp takes a row: lane l holds the channels 16 l .. (a quantization group), and for the rotation pair l of the
 // last 64, which lanes 28-31 get back through shared memory; of the key, channels 4 l ...  Bytes bound a long
@@ -125,8 +127,305 @@ __device__ __forceinline__ FF inverse_rms(float (&v)[16], float eps, float& scal
   return FF{r, 0.5f * r * d};
 }
 
+// ------------------------------------------------- in fp32, with both ends
+
+// packed fp32 arithmetic on two neighbouring registers
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// How far a value formed in fp32 may be off.  A norm: 16 fused steps and five sums of 2^-24 each, halved by the root,
+// the root's two units and two products: below 2^-20 of the value.  A rotation: 2^-21 of |a| + |b| of its pair (angle 2^-24
+// pi, sine and cosine 2^-22, three roundings).  A rotated channel of the main copy has its partner in its group, so
+// |a| + |b| <= 2 amax, and together 3 2^-20 amax; in units of the scale, of which amax is at most nine, below 2^-15.
+constexpr float kOffTop = 0x1p-18f, kOffCode = 0x1p-15f;
+constexpr float kTopMost = 2600.0f;  // beyond, the scale saturates and amax may be more than nine of it
+constexpr float kOffTurn = 0x1p-20f;  // of a key's channel, in units of the row's largest: |a| + |b| is two of it at most
+
+// The codes of eight values (E2M1, nearest even): value i of v at nibble i.
+__device__ __forceinline__ uint32_t codes8(const uint64_t (&t)[4]) {
+  uint32_t r;
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(t[i], f[2 * i], f[2 * i + 1]);
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n\t"
+      "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+
+// One lane's group: codes and scale, and whether they are certain for values that are off (else exact).
+__device__ __forceinline__ bool main_group(const uint64_t (&y)[8], bool off, uint2& codes, uint32_t& scale) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    unpack2(y[i], a, b);
+    amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+  }
+  const float d = off ? kOffTop : 0.0f;
+  scale = float_to_e4m3(__fdiv_rn(amax * (1.0f - d), 6.0f));
+  bool sure = !off || (amax < kTopMost && float_to_e4m3(__fdiv_rn(amax * (1.0f + d), 6.0f)) == scale);
+  const float s = e4m3_to_float(scale);
+  codes = make_uint2(0u, 0u);
+  if (s == 0.0f) return sure;
+  const float r = __frcp_rn(s);
+  // the ends; an exact value's are itself, a negative zero's too
+  const float e0 = off ? -kOffCode : -0.0f, e1 = off ? kOffCode : -0.0f;
+  const uint64_t s2 = pack2(-s, -s), r2 = pack2(r, r), m2 = pack2(e0, e0), e2 = pack2(e1, e1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint64_t lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // codec.cuh, div_by_e4m3
+      const uint64_t x = y[4 * h + i], q0 = mul2(x, r2), q = fma2(fma2(q0, s2, x), r2, q0);
+      lo[i] = add2(q, m2);
+      hi[i] = add2(q, e2);
+    }
+    const uint32_t c = codes8(lo);
+    sure = sure && c == codes8(hi);
+    (h ? codes.y : codes.x) = c;
+  }
+  return sure;
+}
+
+// The main copy of row r to plane row `row`; false, and nothing written, where it is not certain.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_latent_append(LatentArgs a, const __grid_constant__ LatentTurns turns) {
+__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
+                                            float* s_row, int lane) {
+  const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
+  float v[16];
+  load16(x + 16 * lane, v);
+  float2 p = make_float2(0.0f, 0.0f), g = make_float2(1.0f, 1.0f);
+  if (a.rope) p = load2(x + kRopeFirst + 2 * lane);
+  uint64_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = pack2(v[2 * i], v[2 * i + 1]);
+  float inv = 1.0f;
+  if (a.norm_w) {
+    uint64_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(a.norm_w + 16 * lane) + i);
+      w[2 * i] = pack2(f.x, f.y);
+      w[2 * i + 1] = pack2(f.z, f.w);
+    }
+    if (a.rope) g = load2(a.norm_w + kRopeFirst + 2 * lane);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fma2(y[i], y[i], sum);
+    float s0, s1;
+    unpack2(sum, s0, s1);
+    float ss = s0 + s1;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // sums whose terms are subnormal, or too large, are another's
+    if (!(ss > 0x1p-80f && ss < 0x1p100f)) return false;
+    inv = rsqrtf(fmaf(ss, 1.0f / kDMain, a.eps));
+    const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = mul2(mul2(y[i], inv2), w[i]);
+  }
+  if (a.rope) {
+    float c, s;
+    turn_cos_sin(turns.kv.f[lane], (int64_t)pos, c, s);
+    float m = p.x * inv * g.x, n = p.y * inv * g.y;
+    rope_pair(m, n, c, s);
+    *reinterpret_cast<float2*>(s_row + 2 * lane) = make_float2(m, n);
+    __syncwarp();
+    if (lane >= 28) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(s_row + 16 * (lane - 28) + 4 * i);
+        y[2 * i] = pack2(f.x, f.y);
+        y[2 * i + 1] = pack2(f.z, f.w);
+      }
+    }
+    __syncwarp();
+  }
+  uint2 codes;
+  uint32_t scale;
+  const bool sure = main_group(y, a.norm_w || (a.rope && lane >= 28), codes, scale);
+  if (!__all_sync(0xffffffffu, sure)) return false;
+  *reinterpret_cast<uint2*>(a.kv_codes + row * 256 + lane * 8) = codes;
+  a.kv_scales[row * 32 + lane] = (uint8_t)scale;
+  return true;
+}
+
+// A lane's four values of a key, quantized by the group's largest (codec.cuh, quantize_index_group_vals: eight lanes
+// have a group).
+__device__ __forceinline__ int key_exponent(float amax) {
+  if (!(amax > 0.0f)) return -127;
+  const int e = floor_log2_f32(amax) - 2;
+  return e < -127 ? -127 : (e > 127 ? 127 : e);
+}
+__device__ __forceinline__ uint32_t key_codes(const float (&v)[4], float f, float off) {
+  return float2_to_e2m1x2(fmaf(v[0], f, off), fmaf(v[1], f, off)) |
+         float2_to_e2m1x2(fmaf(v[2], f, off), fmaf(v[3], f, off)) << 8;
+}
+__device__ __forceinline__ float group_max(float m) {
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+__device__ __forceinline__ void put_key(const LatentArgs& a, int64_t row, int lane, uint32_t codes, int e) {
+  *reinterpret_cast<uint16_t*>(a.ix_codes + row * 64 + lane * 2) = (uint16_t)codes;
+  if (lane % 8 == 0) a.ix_scales[row * 4 + lane / 8] = (uint8_t)(e + 127);
+}
+
+// The key of row r, as append_main.
+template <typename T>
+__device__ __forceinline__ bool append_key(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
+                                           float* s_row, int lane) {
+  float v[4], off = 0.0f;
+  load4(static_cast<const T*>(a.key) + (int64_t)r * kDIdx + 4 * lane, v);
+  if (a.key_pairs) {
+    const float mine = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+    const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
+    if (4 * lane + 3 >= a.key_first && 4 * lane < a.key_first + 2 * a.key_pairs)
+      off = kOffTurn * most * fabsf(a.key_magnitude);
+    *reinterpret_cast<float4*>(s_row + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    __syncwarp();
+    for (int i = lane; i < a.key_pairs; i += 32) {
+      float c, s;
+      turn_cos_sin(turns.key.f[i], (int64_t)pos, c, s);
+      float* const at = s_row + a.key_first + i * a.key_step;
+      float m = at[0], n = at[a.key_other];
+      rope_pair(m, n, c * a.key_magnitude, s * a.key_magnitude);
+      at[0] = m;
+      at[a.key_other] = n;
+    }
+    __syncwarp();
+    const float4 f = *reinterpret_cast<const float4*>(s_row + 4 * lane);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  }
+  const float amax = group_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+  const float err = group_max(off);
+  const int e = key_exponent(amax);
+  const float f = exp2i_f32(-e);
+  uint32_t codes = 0;
+  bool sure = off < INFINITY;  // no NaN either
+  if (err != 0.0f) sure = sure && amax - err > 0.0f && key_exponent(amax - err) == e && key_exponent(amax + err) == e;
+  if (amax > 0.0f) {
+    codes = key_codes(v, f, -off * f);
+    if (off != 0.0f) sure = sure && codes == key_codes(v, f, off * f);
+  }
+  if (!__all_sync(0xffffffffu, sure)) return false;
+  put_key(a, row, lane, codes, e);
+  return true;
+}
+
+// --------------------------------------------------------- in pairs of fp32
+
+template <typename T>
+__device__ __noinline__ void exact_main(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
+                                        float* s_row, int lane) {
+  const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
+  float v[16];
+  load16(x + 16 * lane, v);
+  FF inv{1.0f, 0.0f};
+  float scale = 1.0f;
+  if (a.norm_w) {
+    inv = inverse_rms(v, a.eps, scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 w4 = __ldg(reinterpret_cast<const float4*>(a.norm_w + 16 * lane) + i);
+      const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = value(mul(mul(inv, v[4 * i + j]), w[j]));
+    }
+  }
+  if (a.rope) {
+    FF c, s;
+    turn_cos_sin(pos * turns.kv.f[lane], c, s);
+    const float2 p = load2(x + kRopeFirst + 2 * lane);
+    FF u{p.x * scale, 0.0f}, w{p.y * scale, 0.0f};
+    if (a.norm_w) {
+      const float2 g = load2(a.norm_w + kRopeFirst + 2 * lane);
+      u = mul(mul(inv, u.hi), g.x);
+      w = mul(mul(inv, w.hi), g.y);
+    }
+    turn_pair(u, w, c, s);
+    *reinterpret_cast<float2*>(s_row + 2 * lane) = make_float2(value(u), value(w));
+    __syncwarp();
+    if (lane >= 28) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(s_row + 16 * (lane - 28) + 4 * i);
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = f.z;
+        v[4 * i + 3] = f.w;
+      }
+    }
+    __syncwarp();
+  }
+  quantize_main_group_vals(v, a.kv_codes + row * 256 + lane * 8, a.kv_scales + row * 32 + lane);
+}
+
+template <typename T>
+__device__ __noinline__ void exact_key(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
+                                       float* s_row, int lane) {
+  float v[4];
+  load4(static_cast<const T*>(a.key) + (int64_t)r * kDIdx + 4 * lane, v);
+  if (a.key_pairs) {
+    *reinterpret_cast<float4*>(s_row + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    __syncwarp();
+    for (int i = lane; i < a.key_pairs; i += 32) {
+      FF c, s;
+      turn_cos_sin(pos * turns.key.f[i], c, s);
+      float* const at = s_row + a.key_first + i * a.key_step;
+      FF u{at[0], 0.0f}, w{at[a.key_other], 0.0f};
+      turn_pair(u, w, c, s);
+      at[0] = value(mul(u, a.key_magnitude));
+      at[a.key_other] = value(mul(w, a.key_magnitude));
+    }
+    __syncwarp();
+    const float4 f = *reinterpret_cast<const float4*>(s_row + 4 * lane);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  }
+  const float amax = group_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+  const int e = key_exponent(amax);
+  const float f = exp2i_f32(-e);
+  uint32_t codes = 0;
+  if (amax > 0.0f)
+    codes = float2_to_e2m1x2(__fmul_rn(v[0], f), __fmul_rn(v[1], f)) |
+            float2_to_e2m1x2(__fmul_rn(v[2], f), __fmul_rn(v[3], f)) << 8;
+  put_key(a, row, lane, codes, e);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_latent_append(const __grid_constant__ LatentArgs a,
+                                                            const __grid_constant__ LatentTurns turns) {
   __shared__ __align__(16) float s_row[kWarps][kDIdx];
   ptx::griddep_launch();
   ptx::griddep_wait();
@@ -147,87 +446,8 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(LatentArgs a, const 
   const int64_t row = place(a, r);
   if (row < 0) return;  // the same for the whole warp
   const uint64_t pos = a.pos ? (uint64_t)a.pos[r] : 0;
-  if (a.x) {
-    const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
-    float v[16];
-    load16(x + 16 * lane, v);
-    FF inv{1.0f, 0.0f};
-    float scale = 1.0f;
-    if (a.norm_w) {
-      inv = inverse_rms(v, a.eps, scale);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 w4 = __ldg(reinterpret_cast<const float4*>(a.norm_w + 16 * lane) + i);
-        const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * i + j] = value(mul(mul(inv, v[4 * i + j]), w[j]));
-      }
-    }
-    if (a.rope) {
-      FF c, s;
-      turn_cos_sin(pos * turns.kv.f[lane], c, s);
-      const float2 p = load2(x + kRopeFirst + 2 * lane);
-      FF u{p.x * scale, 0.0f}, w{p.y * scale, 0.0f};
-      if (a.norm_w) {
-        const float2 g = load2(a.norm_w + kRopeFirst + 2 * lane);
-        u = mul(mul(inv, u.hi), g.x);
-        w = mul(mul(inv, w.hi), g.y);
-      }
-      turn_pair(u, w, c, s);
-      *reinterpret_cast<float2*>(&s_row[warp][2 * lane]) = make_float2(value(u), value(w));
-      __syncwarp();
-      if (lane >= 28) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 f = *reinterpret_cast<const float4*>(&s_row[warp][16 * (lane - 28) + 4 * i]);
-          v[4 * i] = f.x;
-          v[4 * i + 1] = f.y;
-          v[4 * i + 2] = f.z;
-          v[4 * i + 3] = f.w;
-        }
-      }
-      __syncwarp();
-    }
-    quantize_main_group_vals(v, a.kv_codes + row * 256 + lane * 8, a.kv_scales + row * 32 + lane);
-  }
-  if (a.key) {
-    float v[4];
-    load4(static_cast<const T*>(a.key) + (int64_t)r * kDIdx + 4 * lane, v);
-    if (a.key_pairs) {
-      *reinterpret_cast<float4*>(&s_row[warp][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-      __syncwarp();
-      for (int i = lane; i < a.key_pairs; i += 32) {
-        FF c, s;
-        turn_cos_sin(pos * turns.key.f[i], c, s);
-        float* const at = &s_row[warp][a.key_first + i * a.key_step];
-        FF u{at[0], 0.0f}, w{at[a.key_other], 0.0f};
-        turn_pair(u, w, c, s);
-        at[0] = value(mul(u, a.key_magnitude));
-        at[a.key_other] = value(mul(w, a.key_magnitude));
-      }
-      __syncwarp();
-      const float4 f = *reinterpret_cast<const float4*>(&s_row[warp][4 * lane]);
-      v[0] = f.x;
-      v[1] = f.y;
-      v[2] = f.z;
-      v[3] = f.w;
-    }
-    // codec.cuh, quantize_index_group_vals: eight lanes have a group
-    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    int e = -127;
-    uint32_t codes = 0;
-    if (amax > 0.0f) {
-      e = floor_log2_f32(amax) - 2;
-      e = e < -127 ? -127 : (e > 127 ? 127 : e);
-      const float f = exp2i_f32(-e);
-      codes = float2_to_e2m1x2(__fmul_rn(v[0], f), __fmul_rn(v[1], f)) |
-              float2_to_e2m1x2(__fmul_rn(v[2], f), __fmul_rn(v[3], f)) << 8;
-    }
-    *reinterpret_cast<uint16_t*>(a.ix_codes + row * 64 + lane * 2) = (uint16_t)codes;
-    if (lane % 8 == 0) a.ix_scales[row * 4 + lane / 8] = (uint8_t)(e + 127);
-  }
+  if (a.x && !append_main<T>(a, turns, r, row, pos, s_row[warp], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp], lane);
+  if (a.key && !append_key<T>(a, turns, r, row, pos, s_row[warp], lane)) exact_key<T>(a, turns, r, row, pos, s_row[warp], lane);
 }
 
 }  // namespace
@@ -269,6 +489,7 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   KernelTimer timer("k_latent_append", st);
   const auto kern = type == CSA2_F32 ? k_latent_append<float> : k_latent_append<uint16_t>;
   const unsigned ctas = (unsigned)(align_up((size_t)(checkers + cdiv(R, kWarps)), (size_t)checkers));
-  launch_clusters(kern, dim3(ctas), dim3(kThreads), checkers, 1, 0, st, a, turns);
+  if (checkers > 1) launch_clusters(kern, dim3(ctas), dim3(kThreads), checkers, 1, 0, st, a, turns);
+  else launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, st, a, turns);
   return launch_status();
 }

@@ -3,8 +3,8 @@
 // Bytes bound it: x is read once and y written once, 3 flops a rotated channel.  A CTA takes a tile of rows and
 // heads and forms its cosines and sines once (a row's serve all its heads) in shared memory.  A vector's units are
 // its rotated ones, two vectors of kV channels whose kV pairs turn (HALVES: pair k is the k-th channel of the two;
-// INTERLEAVED: the neighbouring channels of each), and its copied ones, one vector each; a thread has one unit of every
-// so many vectors, so that a warp's loads are contiguous and its loop divides once a vector.
+// INTERLEAVED: the neighbouring channels of each), and its copied ones, one vector each.  Threads take units of one kind
+// at a time (both kinds in a warp: every warp would run both), four of each on their way before the first is used.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -15,10 +15,11 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 2048, kFewUnits = 512;  // of a tile, at most (about) and at least
-constexpr int kTiles = 608;                    // tiles a call is cut into where it has that many units: four on an SM
-constexpr int kTable = 4096;                   // cosines of a tile, at most
-constexpr int kBatch = 2;                      // units a thread has on their way
+constexpr int kBatch = 4;                    // units of a kind that a thread has on their way
+constexpr int kUnits = kBatch * kThreads;    // of the kind of which a tile has more, at most
+constexpr int kFewUnits = 256;               // and at least, where the call has them
+constexpr int kTiles = 456;                  // tiles that fill the GPU: three on an SM
+constexpr int kTable = 4096;                 // cosines of a tile, at most
 
 struct RopeArgs {
   const void* x;
@@ -29,9 +30,8 @@ struct RopeArgs {
   int32_t heads, first, pairs;
   int32_t rot, copies;        // units of a vector
   int32_t rows_of, heads_of;  // of a tile
-  int32_t lanes;              // vectors that a CTA's threads work on at once
   float magnitude, sign;
-  uint32_t by_heads, by_pairs;  // reciprocals (see over)
+  uint32_t by_heads, by_pairs, by_rot, by_copies;  // reciprocals (see over)
 };
 
 // i / d for i, d <= 2^16, by a product with r = ceil(2^32 / d); d = 1 has none
@@ -42,14 +42,58 @@ template <typename T, int kV>
 struct __align__(sizeof(T) * kV) Vec {
   T v[kV];
 };
-__device__ __forceinline__ float load(float x) { return x; }
-__device__ __forceinline__ float load(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void store(float& y, float x) { y = x; }
-__device__ __forceinline__ void store(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+// kV pairs of two vectors, turned; t: their cosines and sines
+template <bool kHalves, typename T, int kV>
+struct Turn {
+  static __device__ __forceinline__ void run(Vec<T, kV>& p, Vec<T, kV>& q, const float2* t) {
+    static_assert(sizeof(T) == 4 || kV == 1, "see the other form");
+    constexpr bool kApart = kHalves || kV == 1;
+    const Vec<T, kV> x = p, y = q;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const float2 cs = t[k];
+      const float m = (float)(kApart ? x.v[k] : 2 * k < kV ? x.v[2 * k] : y.v[2 * k - kV]);
+      const float n = (float)(kApart ? y.v[k] : 2 * k < kV ? x.v[2 * k + 1] : y.v[2 * k + 1 - kV]);
+      T& g = kApart ? p.v[k] : 2 * k < kV ? p.v[2 * k] : q.v[2 * k - kV];
+      T& h = kApart ? q.v[k] : 2 * k < kV ? p.v[2 * k + 1] : q.v[2 * k + 1 - kV];
+      g = (T)(m * cs.x - n * cs.y);
+      h = (T)(m * cs.y + n * cs.x);
+    }
+  }
+};
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <bool kHalves>
+struct Turn<kHalves, __nv_bfloat16, 8> {  // two channels to a word
+  static __device__ __forceinline__ void run(Vec<__nv_bfloat16, 8>& p, Vec<__nv_bfloat16, 8>& q, const float2* t) {
+    uint32_t* const a = reinterpret_cast<uint32_t*>(&p);
+    uint32_t* const b = reinterpret_cast<uint32_t*>(&q);
+    const float4* const t2 = reinterpret_cast<const float4*>(t);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 cs = t2[w];  // pairs 2 w, 2 w + 1
+      if (kHalves) {
+        const float m0 = low(a[w]), m1 = high(a[w]), n0 = low(b[w]), n1 = high(b[w]);
+        a[w] = pack(m0 * cs.x - n0 * cs.y, m1 * cs.z - n1 * cs.w);
+        b[w] = pack(m0 * cs.y + n0 * cs.x, m1 * cs.w + n1 * cs.z);
+      } else {
+        uint32_t* const c = w < 2 ? a + 2 * w : b + 2 * w - 4;
+        const float m0 = low(c[0]), n0 = high(c[0]), m1 = low(c[1]), n1 = high(c[1]);
+        c[0] = pack(m0 * cs.x - n0 * cs.y, m0 * cs.y + n0 * cs.x);
+        c[1] = pack(m1 * cs.z - n1 * cs.w, m1 * cs.w + n1 * cs.z);
+      }
+    }
+  }
+};
 
 template <typename T, int kV, bool kHalves, int kPairs>
-__global__ void __launch_bounds__(kThreads, 4) k_rope(RopeArgs a, const __grid_constant__ Turns<kPairs> turns) {
-  extern __shared__ float2 table[];  // [rows][pairs] cosine, sine
+__global__ void __launch_bounds__(kThreads, 3) k_rope(RopeArgs a, const __grid_constant__ Turns<kPairs> turns) {
+  extern __shared__ __align__(16) float2 table[];  // [rows][pairs] cosine, sine
+  using V = Vec<T, kV>;
   ptx::griddep_launch();
   ptx::griddep_wait();
   const int64_t row0 = (int64_t)blockIdx.x * a.rows_of;
@@ -57,59 +101,65 @@ __global__ void __launch_bounds__(kThreads, 4) k_rope(RopeArgs a, const __grid_c
   const int rows = (int)min((int64_t)a.rows_of, a.n_rows - row0), heads = min(a.heads_of, a.heads - head0);
   const T* const x = static_cast<const T*>(a.x) + row0 * a.x_row + head0 * a.x_head;
   T* const y = static_cast<T*>(a.y) + row0 * a.y_row + head0 * a.y_head;
-  for (int i = threadIdx.x; i < rows * a.pairs; i += blockDim.x) {
+  const int vectors = rows * a.heads_of, turned = vectors * a.rot, copied = vectors * a.copies;
+  const int second = kHalves ? a.pairs : kV;
+  // vector v = row v / heads, its head; -1: there is none
+  auto row_of = [&](int v, int& h) {
+    const int r = over(v, a.by_heads);
+    h = v - r * a.heads_of;
+    return v < vectors && h < heads ? r : -1;
+  };
+  V p[kBatch], q[kBatch];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads, v = over(i, a.by_rot), u = i - v * a.rot;
+      int h;
+      const int r = row_of(v, h);
+      if (r < 0) continue;
+      const T* const xs = x + r * a.x_row + h * a.x_head + a.first + (kHalves ? u * kV : 2 * u * kV);
+      p[j] = *reinterpret_cast<const V*>(xs);
+      q[j] = *reinterpret_cast<const V*>(xs + second);
+    }
+  };
+  if ((int)threadIdx.x < turned) fetch(threadIdx.x);
+  for (int i0 = threadIdx.x; i0 < copied; i0 += kUnits) {
+    V w[kBatch];
+    T* to[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads, v = over(i, a.by_copies);
+      int h, c = (i - v * a.copies) * kV;
+      const int r = row_of(v, h);
+      to[j] = nullptr;
+      if (r < 0) continue;
+      if (c >= a.first) c += 2 * a.pairs;
+      w[j] = *reinterpret_cast<const V*>(x + r * a.x_row + h * a.x_head + c);
+      to[j] = y + r * a.y_row + h * a.y_head + c;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (to[j]) *reinterpret_cast<V*>(to[j]) = w[j];
+  }
+  for (int i = threadIdx.x; i < rows * a.pairs; i += kThreads) {
     const int r = over(i, a.by_pairs);
     float c, s;
     turn_cos_sin(turns.f[i - r * a.pairs], a.pos[row0 + r], c, s);
     table[i] = make_float2(a.magnitude * c, a.sign * a.magnitude * s);
   }
   __syncthreads();
-  const int per = a.rot + a.copies, vectors = rows * a.heads_of;
-  const int lane = a.lanes > 1 ? threadIdx.x / per : 0;
-  if (lane >= a.lanes) return;
-  for (int u = threadIdx.x - lane * per; u < per; u += a.lanes > 1 ? per : blockDim.x) {
-    const bool turned = u < a.rot;
-    int c0 = a.first + (kHalves ? u * kV : 2 * u * kV), c1 = c0 + (kHalves ? a.pairs : kV);
-    if (!turned) {
-      c0 = (u - a.rot) * kV;
-      if (c0 >= a.first) c0 += 2 * a.pairs;
-    }
-    for (int v0 = lane; v0 < vectors; v0 += kBatch * a.lanes) {
-      Vec<T, kV> p[kBatch], q[kBatch];
-      int r[kBatch], h[kBatch];
+  for (int i0 = threadIdx.x; i0 < turned; i0 += kUnits) {
+    if (i0 >= kUnits) fetch(i0);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int v = v0 + j * a.lanes;
-        r[j] = over(v, a.by_heads);
-        h[j] = v - r[j] * a.heads_of;
-        if (v >= vectors) h[j] = heads;
-        if (h[j] >= heads) continue;
-        const T* const xs = x + r[j] * a.x_row + h[j] * a.x_head;
-        p[j] = *reinterpret_cast<const Vec<T, kV>*>(xs + c0);
-        if (turned) q[j] = *reinterpret_cast<const Vec<T, kV>*>(xs + c1);
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (h[j] >= heads) continue;
-        T* const ys = y + r[j] * a.y_row + h[j] * a.y_head;
-        if (turned) {
-          const float2* const t = table + r[j] * a.pairs + u * kV;
-          Vec<T, kV> o0, o1;
-#pragma unroll
-          for (int k = 0; k < kV; ++k) {
-            constexpr bool kApart = kHalves || kV == 1;
-            const float m = load(kApart ? p[j].v[k] : 2 * k < kV ? p[j].v[2 * k] : q[j].v[2 * k - kV]);
-            const float n = load(kApart ? q[j].v[k] : 2 * k < kV ? p[j].v[2 * k + 1] : q[j].v[2 * k + 1 - kV]);
-            const float2 cs = t[k];
-            store(kApart ? o0.v[k] : 2 * k < kV ? o0.v[2 * k] : o1.v[2 * k - kV], m * cs.x - n * cs.y);
-            store(kApart ? o1.v[k] : 2 * k < kV ? o0.v[2 * k + 1] : o1.v[2 * k + 1 - kV], m * cs.y + n * cs.x);
-          }
-          *reinterpret_cast<Vec<T, kV>*>(ys + c0) = o0;
-          *reinterpret_cast<Vec<T, kV>*>(ys + c1) = o1;
-        } else {
-          *reinterpret_cast<Vec<T, kV>*>(ys + c0) = p[j];
-        }
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads, v = over(i, a.by_rot), u = i - v * a.rot;
+      int h;
+      const int r = row_of(v, h);
+      if (r < 0) continue;
+      Turn<kHalves, T, kV>::run(p[j], q[j], table + r * a.pairs + u * kV);
+      T* const ys = y + r * a.y_row + h * a.y_head + a.first + (kHalves ? u * kV : 2 * u * kV);
+      *reinterpret_cast<V*>(ys) = p[j];
+      *reinterpret_cast<V*>(ys + second) = q[j];
     }
   }
 }
@@ -120,18 +170,19 @@ csa2_status run(RopeArgs a, const csa2_rotary* rot, int32_t dim, cudaStream_t st
   make_turns(&turns, rot->n_rot, rot->base, &rot->scaling);
   a.rot = a.pairs / kV;
   a.copies = a.x == a.y ? 0 : (dim - rot->n_rot) / kV;
-  const int per = a.rot + a.copies;
+  // units of the kind that is more; over() wants fewer than 2^16
+  const int per = std::max(a.rot, a.copies);
   const int64_t all = (int64_t)per * a.heads;
   const int64_t want = std::min<int64_t>(std::max<int64_t>(all * a.n_rows / kTiles, kFewUnits), kUnits);
   a.rows_of = (int)std::min<int64_t>({std::max<int64_t>(want / all, 1), kTable / a.pairs, a.n_rows});
   a.heads_of = (int)std::min<int64_t>(std::max<int64_t>(want / per, 1), a.heads);
-  a.lanes = std::max(kThreads / per, 1);
   a.by_heads = reciprocal(a.heads_of);
   a.by_pairs = reciprocal(a.pairs);
-  const int threads = per >= kThreads ? kThreads : (a.lanes * per + 31) / 32 * 32;
+  a.by_rot = reciprocal(a.rot);
+  a.by_copies = reciprocal(a.copies);
   KernelTimer timer("k_rope", st);
   launch_pdl(rot->layout == CSA2_ROPE_HALVES ? k_rope<T, kV, true, kPairs> : k_rope<T, kV, false, kPairs>,
-             dim3((unsigned)cdiv(a.n_rows, a.rows_of), (unsigned)cdiv(a.heads, a.heads_of)), dim3(threads),
+             dim3((unsigned)cdiv(a.n_rows, a.rows_of), (unsigned)cdiv(a.heads, a.heads_of)), dim3(kThreads),
              (size_t)a.rows_of * a.pairs * sizeof(float2), st, a, turns);
   return launch_status();
 }

@@ -181,6 +181,7 @@ extern "C" csa2_status csa2_tree_commit(const csa2_kv_planes* kv, const csa2_pag
   KernelTimer timer("k_tree_commit", st);
   a.checkers = (int64_t)trees->R * n_path > kManyPlaces ? kCheckers : 1;
   const unsigned ctas = (unsigned)align_up((size_t)(a.checkers + trees->R), (size_t)a.checkers);
-  launch_clusters(k_tree_commit, dim3(ctas), dim3(kThreads), a.checkers, 1, 0, st, a);
+  if (a.checkers > 1) launch_clusters(k_tree_commit, dim3(ctas), dim3(kThreads), a.checkers, 1, 0, st, a);
+  else launch_pdl(k_tree_commit, dim3(ctas), dim3(kThreads), 0, st, a);
   return launch_status();
 }

@@ -91,6 +91,12 @@ def test_bytes(oracle_mod, R, norm, rope, dtype):
     run(oracle_mod, R, seed=R, dtype=dtype, norm=norm, rope=rope)
 
 
+def test_bytes_of_many_rows(oracle_mod):
+    # about a thousand of them have a value whose fp32 form lies too near a border of the codec
+    run(oracle_mod, 20000, P=64, seed=21)
+    run(oracle_mod, 20000, P=64, seed=22, norm=False, dtype=torch.bfloat16)
+
+
 @pytest.mark.parametrize("key_rot", [None, (128, 0, False, 10000.0), (128, 0, True, 500000.0), (2, 126, False, 10000.0),
                                      (48, 5, True, 10000.0), (64, 0, False, 10000.0)])
 def test_keys(oracle_mod, key_rot):
