@@ -31,6 +31,7 @@
 // the shorter's last, 128 rows of the longer.
 // Measured: 64 queries on 65,000 shared entries 405 us, 1.35 PFLOP/s, 71 % of the rate of a library bf16
 // product; 32 on 8,192, normalised and rotated, 51 us.
+#include <algorithm>
 #include <type_traits>
 
 #include "attn.cuh"
@@ -121,6 +122,7 @@ struct PrefixArgs {
   // trees: group_start has their first tokens, n_entries [G] the contexts, shared_max the bound of those
   const int32_t* parent;
   int32_t max_tokens, entries;
+  int32_t* cost0;     // [pairs + 1] cost of the pairs before each (where shared memory is too small)
   uint64_t* kin;      // [B] itself and its ancestors, bit t token t of the request
   int32_t* depth;     // [B] how many ancestors; + kBadParent where the parent is none
 };
@@ -219,6 +221,14 @@ __device__ __forceinline__ bool tree_ok(const PrefixArgs& a, int lo, int hi) {
 }
 __device__ __forceinline__ int tree_context(const PrefixArgs& a, int g) { return min(max(a.n_entries[g], 0), a.shared_max); }
 __device__ __forceinline__ int tree_image_chunks(int tokens, int n) { return tokens < kImageQueries ? 0 : n / kChunk; }
+// Trees share the chunks among the pairs of CTAs by what they cost: a request of few tokens has no image, and of short
+// contexts the tails and the change from pair to pair are most.  In units of half an image chunk.
+constexpr int kCostImage = 2, kCostRows = 3, kCostPair = 4;
+__device__ __forceinline__ int image_chunks_of(const Pair& x) { return x.image >= 0 ? min(x.vis0 / kChunk, x.nshared) : 0; }
+__device__ __forceinline__ int cost_of(const Pair& x) {
+  const int im = image_chunks_of(x);
+  return x.nshared > 0 ? kCostPair + kCostImage * im + kCostRows * (x.nshared - im) : 0;
+}
 // the largest i in [0, n) with list[i] <= x, list[0] <= x
 __device__ __forceinline__ int last_at_most(const int32_t* list, int n, int x) {
   int lo = 0, hi = n;
@@ -260,7 +270,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   const int R = G + 2;  // ranges; without groups the first is empty
   int32_t* const gpair = R + 1 <= smem_ints / 4 ? smem : a.gpair;
   const int most_pairs = kAloneQueries ? a.B : max_pairs(a.B, a.G);
-  int32_t* const chunk0 = most_pairs + 1 <= smem_ints / 2 ? smem + smem_ints / 2 : a.chunk0;
+  constexpr bool kCosts = kTree && !kAloneQueries;
+  const int room = kCosts ? smem_ints / 4 : smem_ints / 2;
+  int32_t* const chunk0 = most_pairs + 1 <= room ? smem + smem_ints / 2 : a.chunk0;
+  int32_t* const cost0 = !kCosts ? nullptr : most_pairs + 1 <= room ? smem + 3 * (smem_ints / 4) : a.cost0;
   auto range_lo = [&](int v) { return v == 0 ? 0 : G == 0 ? 0 : a.group_start[v - 1]; };
   auto range_hi = [&](int v) { return v == R - 1 ? a.B : G == 0 ? 0 : a.group_start[v]; };
   int base = 0;
@@ -285,7 +298,7 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
     images += total;
   }
   __syncthreads();
-  int chunks = 0;
+  int chunks = 0, costs = 0;
   for (int p0 = 0; p0 < np; p0 += kPrepThreads) {
     const int p = p0 + tid;
     Pair x{};
@@ -369,9 +382,58 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
       chunk0[p] = x.chunk0;
     }
     chunks += total;
+    if (kCosts) {
+      const int at = costs + block_scan(p < np ? cost_of(x) : 0, s_warp, &total);
+      if (p < np) cost0[p] = at;
+      costs += total;
+    }
   }
-  if (tid == 0) a.pairs[np].chunk0 = chunk0[np] = chunks;
+  if (tid == 0) {
+    a.pairs[np].chunk0 = chunk0[np] = chunks;
+    if (kCosts) cost0[np] = costs;
+  }
   __syncthreads();
+  if constexpr (kCosts) {
+    // Chunk t, which begins at cost s, belongs to part s parts / costs.  Chunks begin kCostPair + kCostRows apart at
+    // most, so no part is empty if it is as long.
+    const long long parts = min((long long)a.parts, (long long)costs / (kCostPair + kCostRows));
+    for (int p = tid; p < np; p += kPrepThreads) {
+      const Pair& x = a.pairs[p];
+      int k0 = 0, k1 = 0;
+      if (x.nshared > 0) {
+        const int last = x.nshared > image_chunks_of(x) ? kCostRows : kCostImage;
+        k0 = (int)((cost0[p] + kCostPair) * parts / costs);
+        k1 = (int)((cost0[p] + cost_of(x) - last) * parts / costs) + 1;
+      }
+      a.qpart[x.q0] = make_int2(2 * (p + k0), k1 - k0);
+      if (x.q1 >= 0) a.qpart[x.q1] = make_int2(2 * (p + k0) + 1, k1 - k0);
+    }
+    for (int c = tid; c < a.parts; c += kPrepThreads) {
+      if (c >= parts) {
+        a.parts_of[c] = Part{};
+        continue;
+      }
+      // the first chunk that begins at cost (costs c / parts) or behind, and its pair
+      auto first_of = [&](int c, int& p) {
+        const int at = (int)((costs * (long long)c + parts - 1) / parts);
+        p = c < parts ? last_at_most(cost0, np, at) : np - 1;
+        const Pair& x = a.pairs[p];
+        const int im = image_chunks_of(x), off = at - cost0[p] - kCostPair;
+        const int j = off <= 0 ? 0 : off <= kCostImage * im ? (off + kCostImage - 1) / kCostImage
+                                   : im + (off - kCostImage * im + kCostRows - 1) / kCostRows;
+        if (c >= parts || j >= x.nshared) {
+          ++p;
+          return chunk0[p];
+        }
+        return chunk0[p] + j;
+      };
+      int p, next;
+      const int t0 = first_of(c, p), t1 = first_of(c + 1, next);
+      while (chunk0[p + 1] <= t0) ++p;  // pairs without chunks
+      a.parts_of[c] = Part{p, t0, t1, chunk0[p + 1], a.pairs[p]};
+    }
+    return;
+  }
   const int clusters = min(a.parts, chunks);
   for (int p = tid; p < np; p += kPrepThreads) {
     // chunk t belongs to part ceil((t + 1) parts / chunks) - 1; a pair's partial of part c is p + c
@@ -460,7 +522,7 @@ struct PrefixKernel {
   const int32_t* depth;
   const int64_t* q_pos;
   const uint8_t* draft;
-  int32_t n_ring;
+  int32_t n_ring, slices;  // slices: parts of each pair of CTAs
   uint4* part_o;    // [pairs + clusters][2][32 Vec8::kWords][128]: eight channels of thread t of the epilogue, of O / l
   float2* part_ml;  // [pairs + clusters][2][64]
   void* ws;
@@ -996,37 +1058,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
-  const Part& part = S.part;
-  const int t0 = part.t0, t1 = part.t1;
   auto wait = [&](uint64_t* bar, uint32_t n) { return ptx::mbar_wait_warp(bar, n & 1u, abort_flag, kWaitBudget); };
   bool good = true;
   int where = 0;
-  // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1;
-  // n counts the chunks before them, items the items.
+  // this pair of CTAs' parts: one, or (trees) every kClusters-th, so that all work on neighbouring pairs at a time
+  const int slices = kTree ? k.slices : 1;
+  auto part_of = [&](int i) { return i == 0 ? &S.part : k.parts + cluster + i * kClusters; };
+  int chunks = 0;
+  for (int i = 0; i < slices; ++i) chunks += part_of(i)->t1 - part_of(i)->t0;
+  // Every role runs the same list of items, in a loop of its own: pair x, its chunks c0 .. c0 + nc - 1, and the
+  // number of its partial; n counts the chunks before them, items the items.
   auto for_items = [&](auto body) {
-    const Pair* px = &part.pair;
-    int p = part.p, end = part.end;
     uint32_t n = 0, items = 0;
-    for (int t = t0; t < t1 && good;) {
-      const Pair x = *px;
-      const int c0 = t - x.chunk0, nc = min(end, t1) - t;
-      if (nc > 0) {  // else a pair without chunks
-        t += nc;
-        body(x, p, c0, nc, n, items);
-        n += (uint32_t)nc;
-        ++items;
+    for (int i = 0; i < slices && good; ++i) {
+      const Part& part = *part_of(i);
+      const Pair* px = &part.pair;
+      int p = part.p, end = part.end;
+      const int t1 = part.t1;
+      for (int t = part.t0; t < t1 && good;) {
+        const Pair x = *px;
+        const int c0 = t - x.chunk0, nc = min(end, t1) - t;
+        if (nc > 0) {  // else a pair without chunks
+          t += nc;
+          body(x, p + cluster + i * kClusters, c0, nc, n, items);
+          n += (uint32_t)nc;
+          ++items;
+        }
+        px = k.pairs + ++p;
+        if (t < t1) end = k.pairs[p + 1].chunk0;
       }
-      px = k.pairs + ++p;
-      if (t < t1) end = k.pairs[p + 1].chunk0;
     }
   };
 
   if (warp >= kRowWarp && warp < kSMma) {
     ptx::setmaxnreg_dec<kRowRegs>();
-    good = rows_role<kTree>(S, k, maps, rank, t1 - t0, warp - kRowWarp, lane);
+    good = rows_role<kTree>(S, k, maps, rank, chunks, warp - kRowWarp, lane);
     // the last item's partial is theirs, a quarter of the columns each four: nothing else is left to do
-    if (good && t1 > t0) good = wait(&S.last_o, 0);
-    if (good && t1 > t0 && S.last_slot >= 0) {
+    if (good && chunks > 0) good = wait(&S.last_o, 0);
+    if (good && chunks > 0 && S.last_slot >= 0) {
       ptx::tc_fence_after();
       const int quarter = (warp - kRowWarp) / 4, t = 32 * (warp % 4) + lane;
       store_pair_o<kHalf>(k, tmem, S.last_slot, t, S.red[0][t & 63] + S.red[1][t & 63], 2 * quarter, 2 * quarter + 2);
@@ -1185,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.o_read);
     };
-    for_items([&](const Pair& x, int p, int c0, int nc, uint32_t n, uint32_t) {
+    for_items([&](const Pair& x, int slot_of, int c0, int nc, uint32_t n, uint32_t) {
       const int qme = rank ? x.q1 : x.q0, vis = rank ? x.vis1 : x.vis0;
       float m2 = -INFINITY, lsum = 0.0f;
       const float c2 = k.c2[(int64_t)(qme >= 0 ? qme : k.B) * kHAtt + h];
@@ -1283,7 +1352,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
       good = softmax_vote(false, !good || *abort_flag != 0, lane) < 8;  // together, or none
       open = true;
       open_last = n + (uint32_t)nc - 1;
-      open_slot = (p + cluster) * 2 + rank;
+      open_slot = slot_of * 2 + rank;
       if (qme < 0) open_slot = -1 - open_slot;
       open_m = m2;
       open_l = lsum;
@@ -1617,20 +1686,21 @@ __device__ __forceinline__ float corrected(const LseRest& f, int b, int h, float
 // A CTA joins 8 / kSlices heads: thread t of a slice has head t % (8 / kSlices) of them and kVec planes (of eight
 // channels): two, which share a weight, or one where slices make for more threads (one for all: 4 us more for
 // 101 queries).
-template <int kSlices, bool kHalf>
+// Many queries of trees have two partials or so: two at once leave room for more CTAs on an SM.
+template <int kSlices, bool kHalf, bool kTree>
 struct PrefixMerge {
   static constexpr int kVec = kSlices > 1 ? 1 : 2, kHeads = 8 / kSlices, kPer = kHeads * (kDMain / 8) / kVec;
-  static constexpr int kAhead = kSlices > 1 || kHalf ? 8 : 4;  // partials read at once
-  static constexpr int kThreads = kPer * kSlices;
+  static constexpr int kAhead = kSlices > 1 ? 8 : kTree ? 2 : kHalf ? 8 : 4;  // partials read at once
+  static constexpr int kThreads = kPer * kSlices, kCtas = kTree && kSlices == 1 ? (kHalf ? 5 : 4) : 1;
 };
-template <int kSlices, bool kHalf>
-__global__ void __launch_bounds__(PrefixMerge<kSlices, kHalf>::kThreads) k_prefix_merge(const int2* __restrict__ qpart,
+template <int kSlices, bool kHalf, bool kTree>
+__global__ void __launch_bounds__(PrefixMerge<kSlices, kHalf, kTree>::kThreads, PrefixMerge<kSlices, kHalf, kTree>::kCtas) k_prefix_merge(const int2* __restrict__ qpart,
                                                                 const uint4* __restrict__ part_o,
                                                                 const float2* __restrict__ part_ml,
                                                                 const float* __restrict__ sink,
                                                                 const float2* __restrict__ turn, void* __restrict__ out,
                                                                 float* __restrict__ lse, LseRest fix) {
-  using Form = PrefixMerge<kSlices, kHalf>;
+  using Form = PrefixMerge<kSlices, kHalf, kTree>;
   using Vec = Vec8<kHalf>;
   constexpr int kVec = Form::kVec, kHeads = Form::kHeads, kPer = Form::kPer, kC = 8 * kVec, kAhead = Form::kAhead;
   __shared__ float s_join[kSlices > 1 ? kSlices - 1 : 1][2 + kC][kSlices > 1 ? kPer : 1];
@@ -2271,6 +2341,16 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_me
   }
 }
 
+// Parts of each pair of CTAs in a call for trees.  The pairs of CTAs work on neighbouring pairs of queries at a time, whose
+// image L2 then holds: one part for every 64 MB of image at most.  One / two / three / four / six / eight parts, us of the
+// attention: 4 trees of 64 on 65,000 (254 MB) 1,642 / 1,550 / 1,541 / 1,449 / 1,491 / 1,466, 48 of 32 on 4,001 (192 MB)
+// 684 / 667 / 656 / 634 / 639 / 637, 16 of 16 on 8,192 (128 MB) 232 / 219 / 217 / 216 / 223 / 232, 48 of 16 on 2,000
+// (96 MB) 200 / 192 / 193 / 198 / 199 / 210.  A part has sixteen chunks at least, by the bounds.
+int tree_slices(int32_t B, int32_t G, int64_t n_max) {
+  const int64_t image = (G * cdiv(n_max, kChunk) + 511) / 512, chunks = B * n_max / (2 * kChunk);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({8, image, chunks / (16 * kClusters)}));
+}
+
 struct PrefixWs {
   Pair* pairs;
   int32_t *gpair, *chunk0, *gimage;
@@ -2282,6 +2362,7 @@ struct PrefixWs {
   int64_t image_cap;
   uint4* part_o;
   float2* part_ml;
+  int32_t* cost0;
   uint64_t* kin;
   int32_t* depth;
   size_t bytes;
@@ -2298,7 +2379,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max, bool tree
   };
   // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
   const bool alone = by_itself(B, G, shared_max);
-  const size_t parts = alone ? kAlone : kClusters, pairs = alone ? B : max_pairs(B, G);
+  const size_t parts = alone ? kAlone : kClusters * (trees ? tree_slices(B, G, shared_max) : 1), pairs = alone ? B : max_pairs(B, G);
   const size_t slots = (pairs + parts) * (alone ? 1 : 2);
   L.pairs = (Pair*)take((pairs + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);
@@ -2317,6 +2398,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max, bool tree
   if (L.image_cap > kImageChunks) L.image_cap = kImageChunks;
   L.image = (uint16_t*)take((size_t)L.image_cap * kChunk * kDMain * 2);
   if (trees) {
+    L.cost0 = (int32_t*)take((pairs + 1) * 4);
     L.kin = (uint64_t*)take((size_t)B * 8);
     L.depth = (int32_t*)take((size_t)B * 4);
   }
@@ -2415,8 +2497,9 @@ csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs
         return launch_status();
     }
     KernelTimer timer("k_prefix_merge", st);
-    if (slices > 1) merge(k_prefix_merge<4, kHalf>, 32, PrefixMerge<4, kHalf>::kThreads, 1);
-    else merge(k_prefix_merge<1, kHalf>, 8, PrefixMerge<1, kHalf>::kThreads, 1);
+    // with slices the forms are the same
+    if (slices > 1) merge(k_prefix_merge<4, kHalf, false>, 32, PrefixMerge<4, kHalf, false>::kThreads, 1);
+    else merge(k_prefix_merge<1, kHalf, kTree>, 8, PrefixMerge<1, kHalf, kTree>::kThreads, 1);
     return launch_status();
   };
   return out_type == CSA2_OUT_BF16 ? run(std::true_type{}) : run(std::false_type{});
@@ -2441,11 +2524,12 @@ csa2_status prefix_run(const csa2_kv_planes* kv, const csa2_pages* pages, int32_
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
   const PrefixArgs a{B, G, n_entries, group_start, n_shared, (int32_t)n_shared_max, (int32_t)n_own_max, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.gshared, L.image_cap, alone ? kAlone : kClusters, ws, nullptr, 0, 0, nullptr, nullptr};
+                     L.gimage, L.gshared, L.image_cap, alone ? kAlone : kClusters, ws, nullptr, 0, 0, nullptr, nullptr,
+                     nullptr};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, ex.win_pos, ex.win_lo,
-                       L.pairs, L.parts, nullptr, nullptr, nullptr, nullptr, 0, L.part_o, L.part_ml, ws};
+                       L.pairs, L.parts, nullptr, nullptr, nullptr, nullptr, 0, 1, L.part_o, L.part_ml, ws};
   return attn_call<false>(a, k, L, ex, q_bf16, softmax_scale, sink, out, out_type, lse_out, (cudaStream_t)stream);
 }
 
@@ -2526,14 +2610,15 @@ extern "C" csa2_status csa2_tree_attn_decode(const csa2_kv_planes* kv, const csa
   if (!ws || !aligned(ws, 256)) return CSA2_ERR_WORKSPACE;
   const PrefixWs L = prefix_ws(ws, B, R, n_max, true);
   if (ws_bytes < L.bytes) return CSA2_ERR_WORKSPACE;
+  const int slices = tree_slices(B, R, n_max);
   const PrefixArgs a{B, R, n_entries, trees->start, nullptr, (int32_t)n_max, 0, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.gshared, L.image_cap, by_itself(B, R, n_max) ? kAlone : kClusters, ws,
-                     trees->parent, trees->max_tokens, trees->entries, L.kin, L.depth};
+                     L.gimage, L.gshared, L.image_cap, by_itself(B, R, n_max) ? kAlone : kClusters * slices, ws,
+                     trees->parent, trees->max_tokens, trees->entries, L.cost0, L.kin, L.depth};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,
                        ((1ull << 40) + kv->seq_stride - 1) / kv->seq_stride, swa_pos, nullptr,
-                       L.pairs, L.parts, L.kin, L.depth, n_swa > 0 ? q_pos : nullptr, draft_e4m3, R * n_swa,
+                       L.pairs, L.parts, L.kin, L.depth, n_swa > 0 ? q_pos : nullptr, draft_e4m3, R * n_swa, slices,
                        L.part_o, L.part_ml, ws};
   return attn_call<true>(a, k, L, ex, q_bf16, softmax_scale, sink, out, out_type, lse_out, (cudaStream_t)stream);
 }
