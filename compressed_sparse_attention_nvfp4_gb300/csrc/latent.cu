@@ -7,9 +7,9 @@
 // the byte is certain.  Where one does not (one row in twenty after a norm), the row is formed again in pairs of fp32
 // (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
 //
-// A warp takes a row: lane l holds the channels 16 l .. (a quantization group), and for the rotation pair l of the
-// last 64, which lanes 28-31 get back through shared memory; of the key, channels 4 l ...  Bytes bound a long
-// call: up to 2,560 read and 356 written a row.
+// A warp takes a row's main copy: lane l holds the channels 16 l .. (a quantization group), and for the rotation pair l
+// of the last 64, which lanes 28-31 get back through shared memory; another takes four rows' keys, eight lanes to each.
+// Bytes bound a long call: up to 2,560 read and 356 written a row.
 #include "codec.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -19,12 +19,13 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kKeys = 4;  // rows whose keys a warp takes
 // CTAs that look at the destinations: a cluster, so that none reports before the word is cleared; one for few rows
 constexpr int kCheckers = 8, kManyRows = 4096;
 
 struct LatentArgs {
   const void *x, *key;
-  int32_t R, n_slots, checkers;
+  int32_t R, n_slots, checkers, main_ctas;
   const int32_t* slot;
   const int64_t* entry;
   int64_t stride;
@@ -88,8 +89,8 @@ __device__ __forceinline__ float2 load2(const uint16_t* p) {
 
 // plane row of a destination, -1: padding, -2: outside the planes
 __device__ __forceinline__ int64_t place(const LatentArgs& a, int r) {
-  const int32_t s = a.slot[r];
-  const int64_t e = a.entry[r];
+  const int32_t s = __ldg(a.slot + r);
+  const int64_t e = __ldg(a.entry + r);
   if (s == -1 && e == -1) return -1;
   return s < 0 || s >= a.n_slots || e < 0 || e >= a.stride ? -2 : s * a.stride + e;
 }
@@ -158,7 +159,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // the root's two units and two products: below 2^-20 of the value.  A rotation: 2^-21 of |a| + |b| of its pair (angle 2^-24
 // pi, sine and cosine 2^-22, three roundings).  A rotated channel of the main copy has its partner in its group, so
 // |a| + |b| <= 2 amax, and together 3 2^-20 amax; in units of the scale, of which amax is at most nine, below 2^-15.
-constexpr float kOffTop = 0x1p-18f, kOffCode = 0x1p-15f;
+// A channel that is normalised alone is off by 2^-20 of itself: below 2^-17 of the scale up to eight of it, beyond which
+// its code is the largest anyway.
+struct Off {
+  float top, code;  // of the group's largest, relatively; of a value, in units of the scale
+};
+__device__ __forceinline__ Off off_by(bool norm, bool turned) {
+  return turned ? Off{0x1p-18f, 0x1p-15f} : norm ? Off{0x1p-19f, 0x1p-17f} : Off{0.0f, 0.0f};
+}
 constexpr float kTopMost = 2600.0f;  // beyond, the scale saturates and amax may be more than nine of it
 constexpr float kOffTurn = 0x1p-20f;  // of a key's channel, in units of the row's largest: |a| + |b| is two of it at most
 
@@ -178,7 +186,7 @@ __device__ __forceinline__ uint32_t codes8(const uint64_t (&t)[4]) {
 }
 
 // One lane's group: codes and scale, and whether they are certain for values that are off (else exact).
-__device__ __forceinline__ bool main_group(const uint64_t (&y)[8], bool off, uint2& codes, uint32_t& scale) {
+__device__ __forceinline__ bool main_group(const uint64_t (&y)[8], Off by, uint2& codes, uint32_t& scale) {
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -186,15 +194,18 @@ __device__ __forceinline__ bool main_group(const uint64_t (&y)[8], bool off, uin
     unpack2(y[i], a, b);
     amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
   }
-  const float d = off ? kOffTop : 0.0f;
-  scale = float_to_e4m3(__fdiv_rn(amax * (1.0f - d), 6.0f));
-  bool sure = !off || (amax < kTopMost && float_to_e4m3(__fdiv_rn(amax * (1.0f + d), 6.0f)) == scale);
+  const bool off = by.code > 0.0f;
+  const float t = __fdiv_rn(amax, 6.0f);
+  uint16_t ends;  // low byte: the lower one
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ends) : "f"(fmaf(t, by.top, t)), "f"(fmaf(t, -by.top, t)));
+  scale = ends & 0xFFu;
+  bool sure = !off || (amax < kTopMost && (ends >> 8) == scale);
   const float s = e4m3_to_float(scale);
   codes = make_uint2(0u, 0u);
   if (s == 0.0f) return sure;
   const float r = __frcp_rn(s);
   // the ends; an exact value's are itself, a negative zero's too
-  const float e0 = off ? -kOffCode : -0.0f, e1 = off ? kOffCode : -0.0f;
+  const float e0 = off ? -by.code : -0.0f, e1 = off ? by.code : -0.0f;
   const uint64_t s2 = pack2(-s, -s), r2 = pack2(r, r), m2 = pack2(e0, e0), e2 = pack2(e1, e1);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -212,15 +223,11 @@ __device__ __forceinline__ bool main_group(const uint64_t (&y)[8], bool off, uin
   return sure;
 }
 
-// The main copy of row r to plane row `row`; false, and nothing written, where it is not certain.
-template <typename T>
-__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
-                                            float* s_row, int lane) {
-  const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
-  float v[16];
-  load16(x + 16 * lane, v);
-  float2 p = make_float2(0.0f, 0.0f), g = make_float2(1.0f, 1.0f);
-  if (a.rope) p = load2(x + kRopeFirst + 2 * lane);
+// The main copy (v: this lane's values, p: its pair of the last 64) to plane row `row`; false, and nothing written,
+// where it is not certain.
+__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, const float (&v)[16], float2 p,
+                                            int64_t row, uint64_t pos, float* s_row, int lane) {
+  float2 g = make_float2(1.0f, 1.0f);
   uint64_t y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = pack2(v[2 * i], v[2 * i + 1]);
@@ -268,77 +275,102 @@ __device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTur
   }
   uint2 codes;
   uint32_t scale;
-  const bool sure = main_group(y, a.norm_w || (a.rope && lane >= 28), codes, scale);
+  const bool sure = main_group(y, off_by(a.norm_w, a.rope && lane >= 28), codes, scale);
   if (!__all_sync(0xffffffffu, sure)) return false;
   *reinterpret_cast<uint2*>(a.kv_codes + row * 256 + lane * 8) = codes;
   a.kv_scales[row * 32 + lane] = (uint8_t)scale;
   return true;
 }
 
-// A lane's four values of a key, quantized by the group's largest (codec.cuh, quantize_index_group_vals: eight lanes
-// have a group).
-__device__ __forceinline__ int key_exponent(float amax) {
-  if (!(amax > 0.0f)) return -127;
-  const int e = floor_log2_f32(amax) - 2;
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
-__device__ __forceinline__ uint32_t key_codes(const float (&v)[4], float f, float off) {
-  return float2_to_e2m1x2(fmaf(v[0], f, off), fmaf(v[1], f, off)) |
-         float2_to_e2m1x2(fmaf(v[2], f, off), fmaf(v[3], f, off)) << 8;
-}
-__device__ __forceinline__ float group_max(float m) {
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
-__device__ __forceinline__ void put_key(const LatentArgs& a, int64_t row, int lane, uint32_t codes, int e) {
-  *reinterpret_cast<uint16_t*>(a.ix_codes + row * 64 + lane * 2) = (uint16_t)codes;
-  if (lane % 8 == 0) a.ix_scales[row * 4 + lane / 8] = (uint8_t)(e + 127);
-}
+// Exponent of a key's group scale (codec.cuh, quantize_index_group_vals): floor(log2 amax) - 2, -127 at least; the
+// exponent field of a subnormal or zero gives that too.
+__device__ __forceinline__ int key_exponent(float amax) { return max((int)(__float_as_uint(amax) >> 23) - 129, -127); }
 
-// The key of row r, as append_main.
+// The keys of rows r .. r + kKeys - 1, eight lanes to each; returns the rows (bit i: row r + i) that are not certain,
+// of which nothing is written.
 template <typename T>
-__device__ __forceinline__ bool append_key(const LatentArgs& a, const LatentTurns& turns, int r, int64_t row, uint64_t pos,
-                                           float* s_row, int lane) {
-  float v[4], off = 0.0f;
-  load4(static_cast<const T*>(a.key) + (int64_t)r * kDIdx + 4 * lane, v);
+__device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const LatentTurns& turns, int r, float (*s_row)[kDIdx + 4],
+                                                int lane) {
+  const int i = lane / 8, j = lane % 8;  // the row, and of it channels 16 j ..
+  const bool any = r + i < a.R;
+  float v[16];
+#pragma unroll
+  for (int u = 0; u < 16; ++u) v[u] = 0.0f;
+  if (any) load16(static_cast<const T*>(a.key) + (int64_t)(r + i) * kDIdx + 16 * j, v);
+  const int64_t pos = any && a.pos ? __ldg(a.pos + r + i) : 0;
+  const int64_t row = any ? place(a, r + i) : -1;
+  auto largest = [&] {
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) m = fmaxf(m, fabsf(v[u]));
+    return m;
+  };
+  float off = 0.0f;
   if (a.key_pairs) {
-    const float mine = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-    const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
-    if (4 * lane + 3 >= a.key_first && 4 * lane < a.key_first + 2 * a.key_pairs)
+    float most = largest();
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (16 * j + 15 >= a.key_first && 16 * j < a.key_first + 2 * a.key_pairs)
       off = kOffTurn * most * fabsf(a.key_magnitude);
-    *reinterpret_cast<float4*>(s_row + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    float* const mine = s_row[i];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<float4*>(mine + 16 * j + 4 * u) = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
     __syncwarp();
-    for (int i = lane; i < a.key_pairs; i += 32) {
+    for (int t = j; t < a.key_pairs; t += 8) {
       float c, s;
-      turn_cos_sin(turns.key.f[i], (int64_t)pos, c, s);
-      float* const at = s_row + a.key_first + i * a.key_step;
+      turn_cos_sin(turns.key.f[t], pos, c, s);
+      float* const at = mine + a.key_first + t * a.key_step;
       float m = at[0], n = at[a.key_other];
       rope_pair(m, n, c * a.key_magnitude, s * a.key_magnitude);
       at[0] = m;
       at[a.key_other] = n;
     }
     __syncwarp();
-    const float4 f = *reinterpret_cast<const float4*>(s_row + 4 * lane);
-    v[0] = f.x;
-    v[1] = f.y;
-    v[2] = f.z;
-    v[3] = f.w;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4 f = *reinterpret_cast<const float4*>(mine + 16 * j + 4 * u);
+      v[4 * u] = f.x;
+      v[4 * u + 1] = f.y;
+      v[4 * u + 2] = f.z;
+      v[4 * u + 3] = f.w;
+    }
   }
-  const float amax = group_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-  const float err = group_max(off);
+  float amax = largest(), err = off;  // a group is two lanes'
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 1));
   const int e = key_exponent(amax);
   const float f = exp2i_f32(-e);
-  uint32_t codes = 0;
+  uint2 codes = make_uint2(0u, 0u);
   bool sure = off < INFINITY;  // no NaN either
   if (err != 0.0f) sure = sure && amax - err > 0.0f && key_exponent(amax - err) == e && key_exponent(amax + err) == e;
   if (amax > 0.0f) {
-    codes = key_codes(v, f, -off * f);
-    if (off != 0.0f) sure = sure && codes == key_codes(v, f, off * f);
+    // the ends; an exact value's are itself, a negative zero's too
+    const float by = off * f, lo = off != 0.0f ? -by : -0.0f, hi = off != 0.0f ? by : -0.0f;
+    const uint64_t f2 = pack2(f, f), lo2 = pack2(lo, lo), hi2 = pack2(hi, hi);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint64_t x[4], y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint64_t w = pack2(v[8 * h + 2 * u], v[8 * h + 2 * u + 1]);
+        x[u] = fma2(w, f2, lo2);
+        y[u] = fma2(w, f2, hi2);
+      }
+      const uint32_t c = codes8(x);
+      sure = sure && c == codes8(y);
+      (h ? codes.y : codes.x) = c;
+    }
   }
-  if (!__all_sync(0xffffffffu, sure)) return false;
-  put_key(a, row, lane, codes, e);
-  return true;
+  const uint32_t open = __ballot_sync(0xffffffffu, !sure && row >= 0);
+  if (row >= 0 && (open >> (8 * i) & 0xFFu) == 0u) {
+    *reinterpret_cast<uint2*>(a.ix_codes + row * 64 + j * 8) = codes;
+    if (j % 2 == 0) a.ix_scales[row * 4 + j / 2] = (uint8_t)(e + 127);
+  }
+  uint32_t rows = 0;
+#pragma unroll
+  for (int u = 0; u < kKeys; ++u) rows |= (open >> (8 * u) & 0xFFu) ? 1u << u : 0u;
+  return rows;
 }
 
 // --------------------------------------------------------- in pairs of fp32
@@ -413,20 +445,23 @@ __device__ __noinline__ void exact_key(const LatentArgs& a, const LatentTurns& t
     v[2] = f.z;
     v[3] = f.w;
   }
-  const float amax = group_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+  float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));  // eight lanes have a group
   const int e = key_exponent(amax);
   const float f = exp2i_f32(-e);
   uint32_t codes = 0;
   if (amax > 0.0f)
     codes = float2_to_e2m1x2(__fmul_rn(v[0], f), __fmul_rn(v[1], f)) |
             float2_to_e2m1x2(__fmul_rn(v[2], f), __fmul_rn(v[3], f)) << 8;
-  put_key(a, row, lane, codes, e);
+  *reinterpret_cast<uint16_t*>(a.ix_codes + row * 64 + lane * 2) = (uint16_t)codes;
+  if (lane % 8 == 0) a.ix_scales[row * 4 + lane / 8] = (uint8_t)(e + 127);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_latent_append(const __grid_constant__ LatentArgs a,
+__global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_constant__ LatentArgs a,
                                                             const __grid_constant__ LatentTurns turns) {
-  __shared__ __align__(16) float s_row[kWarps][kDIdx];
+  __shared__ __align__(16) float s_row[kWarps][kKeys][kDIdx + 4];
   ptx::griddep_launch();
   ptx::griddep_wait();
   if ((int)blockIdx.x < a.checkers) {  // these report destinations outside the planes: the error word is theirs alone
@@ -440,14 +475,27 @@ __global__ void __launch_bounds__(kThreads) k_latent_append(const __grid_constan
                      a.slot[r] < 0 || a.slot[r] >= a.n_slots ? (long long)a.slot[r] : a.entry[r]);
     return;
   }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int r = ((int)blockIdx.x - a.checkers) * kWarps + warp;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cta = (int)blockIdx.x - a.checkers;
+  if (cta >= a.main_ctas) {
+    const int r = ((cta - a.main_ctas) * kWarps + warp) * kKeys;
+    if (!a.key || r >= a.R) return;
+    for (uint32_t open = append_keys<T>(a, turns, r, s_row[warp], lane); open; open &= open - 1) {
+      const int i = r + __ffs(open) - 1;
+      exact_key<T>(a, turns, i, place(a, i), a.pos ? (uint64_t)a.pos[i] : 0, s_row[warp][0], lane);
+    }
+    return;
+  }
+  const int r = cta * kWarps + warp;
   if (r >= a.R) return;
+  // everything the row needs is asked for before the first of it is used
+  const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
+  float v[16];
+  load16(x + 16 * lane, v);
+  const float2 p = a.rope ? load2(x + kRopeFirst + 2 * lane) : make_float2(0.0f, 0.0f);
+  const uint64_t pos = a.pos ? (uint64_t)__ldg(a.pos + r) : 0;
   const int64_t row = place(a, r);
   if (row < 0) return;  // the same for the whole warp
-  const uint64_t pos = a.pos ? (uint64_t)a.pos[r] : 0;
-  if (a.x && !append_main<T>(a, turns, r, row, pos, s_row[warp], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp], lane);
-  if (a.key && !append_key<T>(a, turns, r, row, pos, s_row[warp], lane)) exact_key<T>(a, turns, r, row, pos, s_row[warp], lane);
+  if (!append_main(a, turns, v, p, row, pos, s_row[warp][0], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
 }
 
 }  // namespace
@@ -471,7 +519,7 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   if (R > 0 && (!slot || !entry || ((rope || key_rope) && !pos))) return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256) || ws_bytes < kWsHeader) return CSA2_ERR_WORKSPACE;
   const int checkers = R > kManyRows ? kCheckers : 1;
-  LatentArgs a{x, key, R, n_slots, checkers, slot, entry, dst->seq_stride, pos, x && kv_nr ? kv_nr->norm_weight : nullptr,
+  LatentArgs a{x, key, R, n_slots, checkers, x ? (int)cdiv(R, kWarps) : 0, slot, entry, dst->seq_stride, pos, x && kv_nr ? kv_nr->norm_weight : nullptr,
                kv_nr ? kv_nr->norm_eps : 0.0f, rope, 0, 0, 0, 0, 1.0f, dst->kv_codes, dst->kv_scales, dst->ix_codes,
                dst->ix_scales, ws};
   LatentTurns turns{};
@@ -488,7 +536,7 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   cudaStream_t st = (cudaStream_t)stream;
   KernelTimer timer("k_latent_append", st);
   const auto kern = type == CSA2_F32 ? k_latent_append<float> : k_latent_append<uint16_t>;
-  const unsigned ctas = (unsigned)(align_up((size_t)(checkers + cdiv(R, kWarps)), (size_t)checkers));
+  const unsigned ctas = (unsigned)align_up((size_t)(checkers + a.main_ctas + (key ? cdiv(R, kWarps * kKeys) : 0)), (size_t)checkers);
   if (checkers > 1) launch_clusters(kern, dim3(ctas), dim3(kThreads), checkers, 1, 0, st, a, turns);
   else launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, st, a, turns);
   return launch_status();

@@ -67,10 +67,18 @@ inline void make_turns(Turns<kPairs>* t, int n, double base, const csa2_rope_sca
   }
 }
 
-// cosine and sine of pos times f, fp32: the angle is rounded to 2^-24 of itself (below half a turn)
+// cosine and sine of pos times f, fp32: Taylor's series within an eighth of a turn, whose last terms are below 2^-28.
+// The angle is rounded to 2^-24 of itself (at most pi / 4), each series to about two units of 2^-24.
 __device__ __forceinline__ void turn_cos_sin(uint64_t f, int64_t pos, float& c, float& s) {
-  const uint64_t phase = (uint64_t)pos * f;
-  sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+  const uint32_t phase = (uint32_t)(((uint64_t)pos * f) >> 32);
+  const uint32_t quarter = (phase + (1u << 29)) >> 30;
+  const float x = (float)(int32_t)(phase - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), z = x * x;
+  const float sn = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), x);
+  const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f), -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
+  c = quarter & 1 ? sn : cs;
+  s = quarter & 1 ? cs : sn;
+  if ((quarter + 1) & 2) c = -c;
+  if (quarter & 2) s = -s;
 }
 
 // ------------------------------------------------------------- pairs of fp32
