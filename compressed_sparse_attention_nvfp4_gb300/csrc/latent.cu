@@ -7,9 +7,9 @@
 // the byte is certain.  Where one does not (one row in twenty after a norm), the row is formed again in pairs of fp32
 // (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
 //
-// A warp takes a row's main copy: lane l holds the channels 16 l .. (a quantization group), and for the rotation pair l
-// of the last 64, which lanes 28-31 get back through shared memory; another takes four rows' keys, eight lanes to each.
-// Bytes bound a long call: up to 2,560 read and 356 written a row.
+// A warp takes a row's main copy: lane l reads, normalises and rotates the channels 128 i + 4 l .. (whole lines) and
+// quantizes 16 l .. (a group); the row changes hands in shared memory.  Another takes four rows' keys, eight lanes to
+// each in the end.  Bytes bound a long call: up to 2,560 read and 356 written a row.
 #include "codec.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -168,7 +168,7 @@ __device__ __forceinline__ Off off_by(bool norm, bool turned) {
   return turned ? Off{0x1p-18f, 0x1p-15f} : norm ? Off{0x1p-19f, 0x1p-17f} : Off{0.0f, 0.0f};
 }
 constexpr float kTopMost = 2600.0f;  // beyond, the scale saturates and amax may be more than nine of it
-constexpr float kOffTurn = 0x1p-20f;  // of a key's channel, in units of the row's largest: |a| + |b| is two of it at most
+constexpr float kOffTurn = 0x1p-20f;  // of a key's channel, in units of the row's largest, turned: |a| + |b| is two of it at most
 
 // The codes of eight values (E2M1, nearest even): value i of v at nibble i.
 __device__ __forceinline__ uint32_t codes8(const uint64_t (&t)[4]) {
@@ -223,27 +223,40 @@ __device__ __forceinline__ bool main_group(const uint64_t (&y)[8], Off by, uint2
   return sure;
 }
 
-// The main copy (v: this lane's values, p: its pair of the last 64) to plane row `row`; false, and nothing written,
-// where it is not certain.
-__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, const float (&v)[16], float2 p,
-                                            int64_t row, uint64_t pos, float* s_row, int lane) {
-  float2 g = make_float2(1.0f, 1.0f);
-  uint64_t y[8];
+// Sixteen values of a row in shared memory, 64 bytes of it, by chunks of four: lane l's first chunk is l / 2 mod 4, so that
+// the eight lanes of an access are at different banks.
+__device__ __forceinline__ int first_chunk(int lane) { return lane >> 1 & 3; }
+__device__ __forceinline__ void take16(const float* at, int lane, uint64_t (&y)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = pack2(v[2 * i], v[2 * i + 1]);
-  float inv = 1.0f;
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = *reinterpret_cast<const float4*>(at + 4 * ((i + first_chunk(lane)) & 3));
+    y[2 * i] = pack2(f.x, f.y);
+    y[2 * i + 1] = pack2(f.z, f.w);
+  }
+}
+// their codes, 16 bits a chunk, put in order
+__device__ __forceinline__ uint2 in_order(uint2 c, int lane) {
+  const int s = first_chunk(lane);
+  if (s & 2) c = make_uint2(c.y, c.x);
+  if (s & 1) c = make_uint2(__funnelshift_l(c.y, c.x, 16), __funnelshift_l(c.x, c.y, 16));
+  return c;
+}
+
+// The main copy (v: this lane's values) to plane row `row`; false, and nothing written, where it is not certain.
+__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, float (&v)[4][4], int64_t row,
+                                            uint64_t pos, float* s_row, int lane) {
   if (a.norm_w) {
-    uint64_t w[8];
+    float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(a.norm_w + 16 * lane) + i);
-      w[2 * i] = pack2(f.x, f.y);
-      w[2 * i + 1] = pack2(f.z, f.w);
-    }
-    if (a.rope) g = load2(a.norm_w + kRopeFirst + 2 * lane);
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(a.norm_w) + 32 * i + lane);
     uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fma2(y[i], y[i], sum);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const uint64_t p = pack2(v[i][j], v[i][j + 1]);
+        sum = fma2(p, p, sum);
+      }
     float s0, s1;
     unpack2(sum, s0, s1);
     float ss = s0 + s1;
@@ -251,33 +264,34 @@ __device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTur
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     // sums whose terms are subnormal, or too large, are another's
     if (!(ss > 0x1p-80f && ss < 0x1p100f)) return false;
-    inv = rsqrtf(fmaf(ss, 1.0f / kDMain, a.eps));
-    const uint64_t inv2 = pack2(inv, inv);
+    const float inv = rsqrtf(fmaf(ss, 1.0f / kDMain, a.eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = mul2(mul2(y[i], inv2), w[i]);
-  }
-  if (a.rope) {
-    float c, s;
-    turn_cos_sin(turns.kv.f[lane], (int64_t)pos, c, s);
-    float m = p.x * inv * g.x, n = p.y * inv * g.y;
-    rope_pair(m, n, c, s);
-    *reinterpret_cast<float2*>(s_row + 2 * lane) = make_float2(m, n);
-    __syncwarp();
-    if (lane >= 28) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(s_row + 16 * (lane - 28) + 4 * i);
-        y[2 * i] = pack2(f.x, f.y);
-        y[2 * i + 1] = pack2(f.z, f.w);
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[i][0] = v[i][0] * inv * w[i].x;
+      v[i][1] = v[i][1] * inv * w[i].y;
+      v[i][2] = v[i][2] * inv * w[i].z;
+      v[i][3] = v[i][3] * inv * w[i].w;
     }
-    __syncwarp();
   }
+  if (a.rope && lane >= 16) {  // the last 64 channels
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float c, s;
+      turn_cos_sin(turns.kv.f[2 * (lane - 16) + j], (int64_t)pos, c, s);
+      rope_pair(v[3][2 * j], v[3][2 * j + 1], c, s);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(s_row + 128 * i + 4 * lane) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+  __syncwarp();
+  uint64_t y[8];
+  take16(s_row + 16 * lane, lane, y);
   uint2 codes;
   uint32_t scale;
   const bool sure = main_group(y, off_by(a.norm_w, a.rope && lane >= 28), codes, scale);
   if (!__all_sync(0xffffffffu, sure)) return false;
-  *reinterpret_cast<uint2*>(a.kv_codes + row * 256 + lane * 8) = codes;
+  *reinterpret_cast<uint2*>(a.kv_codes + row * 256 + lane * 8) = in_order(codes, lane);
   a.kv_scales[row * 32 + lane] = (uint8_t)scale;
   return true;
 }
@@ -292,53 +306,45 @@ template <typename T>
 __device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const LatentTurns& turns, int r, float (*s_row)[kDIdx + 4],
                                                 int lane) {
   const int i = lane / 8, j = lane % 8;  // the row, and of it channels 16 j ..
-  const bool any = r + i < a.R;
-  float v[16];
 #pragma unroll
-  for (int u = 0; u < 16; ++u) v[u] = 0.0f;
-  if (any) load16(static_cast<const T*>(a.key) + (int64_t)(r + i) * kDIdx + 16 * j, v);
+  for (int u = 0; u < kKeys; ++u) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r + u < a.R) load4(static_cast<const T*>(a.key) + (int64_t)(r + u) * kDIdx + 4 * lane, v);
+    *reinterpret_cast<float4*>(s_row[u] + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  const bool any = r + i < a.R;
   const int64_t pos = any && a.pos ? __ldg(a.pos + r + i) : 0;
   const int64_t row = any ? place(a, r + i) : -1;
-  auto largest = [&] {
-    float m = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 16; ++u) m = fmaxf(m, fabsf(v[u]));
-    return m;
-  };
-  float off = 0.0f;
-  if (a.key_pairs) {
-    float most = largest();
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (16 * j + 15 >= a.key_first && 16 * j < a.key_first + 2 * a.key_pairs)
-      off = kOffTurn * most * fabsf(a.key_magnitude);
-    float* const mine = s_row[i];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<float4*>(mine + 16 * j + 4 * u) = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-    __syncwarp();
-    for (int t = j; t < a.key_pairs; t += 8) {
-      float c, s;
-      turn_cos_sin(turns.key.f[t], pos, c, s);
-      float* const at = mine + a.key_first + t * a.key_step;
-      float m = at[0], n = at[a.key_other];
-      rope_pair(m, n, c * a.key_magnitude, s * a.key_magnitude);
-      at[0] = m;
-      at[a.key_other] = n;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 f = *reinterpret_cast<const float4*>(mine + 16 * j + 4 * u);
-      v[4 * u] = f.x;
-      v[4 * u + 1] = f.y;
-      v[4 * u + 2] = f.z;
-      v[4 * u + 3] = f.w;
-    }
+  __syncwarp();
+  for (int t = j; t < a.key_pairs; t += 8) {
+    float c, s;
+    turn_cos_sin(turns.key.f[t], pos, c, s);
+    float* const at = s_row[i] + a.key_first + t * a.key_step;
+    float m = at[0], n = at[a.key_other];
+    rope_pair(m, n, c * a.key_magnitude, s * a.key_magnitude);
+    at[0] = m;
+    at[a.key_other] = n;
   }
-  float amax = largest(), err = off;  // a group is two lanes'
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 1));
+  __syncwarp();
+  uint64_t v[8];
+  take16(s_row[i] + 16 * j, j, v);
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float x, y;
+    unpack2(v[u], x, y);
+    amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // a group is two lanes'
+  float off = 0.0f, err = 0.0f;
+  if (a.key_pairs) {
+    float most = amax;
+#pragma unroll
+    for (int o = 4; o >= 2; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // an infinity in the row, or a NaN that hides behind other values, is another's
+    if (16 * j + 15 >= a.key_first && 16 * j < a.key_first + 2 * a.key_pairs) off = kOffTurn * most;
+    err = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, 1));
+  }
   const int e = key_exponent(amax);
   const float f = exp2i_f32(-e);
   uint2 codes = make_uint2(0u, 0u);
@@ -353,9 +359,8 @@ __device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const Laten
       uint64_t x[4], y[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint64_t w = pack2(v[8 * h + 2 * u], v[8 * h + 2 * u + 1]);
-        x[u] = fma2(w, f2, lo2);
-        y[u] = fma2(w, f2, hi2);
+        x[u] = fma2(v[4 * h + u], f2, lo2);
+        y[u] = fma2(v[4 * h + u], f2, hi2);
       }
       const uint32_t c = codes8(x);
       sure = sure && c == codes8(y);
@@ -364,7 +369,7 @@ __device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const Laten
   }
   const uint32_t open = __ballot_sync(0xffffffffu, !sure && row >= 0);
   if (row >= 0 && (open >> (8 * i) & 0xFFu) == 0u) {
-    *reinterpret_cast<uint2*>(a.ix_codes + row * 64 + j * 8) = codes;
+    *reinterpret_cast<uint2*>(a.ix_codes + row * 64 + j * 8) = in_order(codes, j);
     if (j % 2 == 0) a.ix_scales[row * 4 + j / 2] = (uint8_t)(e + 127);
   }
   uint32_t rows = 0;
@@ -461,7 +466,8 @@ __device__ __noinline__ void exact_key(const LatentArgs& a, const LatentTurns& t
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_constant__ LatentArgs a,
                                                             const __grid_constant__ LatentTurns turns) {
-  __shared__ __align__(16) float s_row[kWarps][kKeys][kDIdx + 4];
+  __shared__ __align__(16) float s_row[kWarps][kKeys][kDIdx + 4];  // a row, or four keys
+  static_assert(kKeys * (kDIdx + 4) >= kDMain, "a row");
   ptx::griddep_launch();
   ptx::griddep_wait();
   if ((int)blockIdx.x < a.checkers) {  // these report destinations outside the planes: the error word is theirs alone
@@ -488,14 +494,13 @@ __global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_cons
   const int r = cta * kWarps + warp;
   if (r >= a.R) return;
   // everything the row needs is asked for before the first of it is used
-  const T* const x = static_cast<const T*>(a.x) + (int64_t)r * kDMain;
-  float v[16];
-  load16(x + 16 * lane, v);
-  const float2 p = a.rope ? load2(x + kRopeFirst + 2 * lane) : make_float2(0.0f, 0.0f);
+  float v[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load4(static_cast<const T*>(a.x) + (int64_t)r * kDMain + 128 * i + 4 * lane, v[i]);
   const uint64_t pos = a.pos ? (uint64_t)__ldg(a.pos + r) : 0;
   const int64_t row = place(a, r);
   if (row < 0) return;  // the same for the whole warp
-  if (!append_main(a, turns, v, p, row, pos, s_row[warp][0], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
+  if (!append_main(a, turns, v, row, pos, s_row[warp][0], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
 }
 
 }  // namespace
