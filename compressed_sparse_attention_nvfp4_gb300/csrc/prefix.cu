@@ -1386,10 +1386,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix_attn(const __grid_consta
 // for all 64 heads the call on 32 normalised and rotated queries took 63.9 us, with four 58.9.
 constexpr int kStageCtas = 4, kStageHeads = kHAtt / kStageCtas;  // of a query; heads of each
 static_assert(kStageHeads == kPrepThreads / 32, "a head for each warp");
+// CTAs that stage in a call for trees, at most.  A part for each CTA / 304 CTAs for all, us of the preparation: 1,536 queries
+// 110 / 93, 664 42 / 36, 256 (with norm, rotation and 128 MB of image) 60 / 57.
+constexpr int kStageMost = 304;
 constexpr int kQPad = kStageHeads * 16 + 16;  // bytes of a plane
 constexpr int kPrepSmem = 64 * 1024;          // this, or the plan's lists
 static_assert(kDMain / 8 * kQPad <= kPrepSmem, "shared memory of the staging");
-__device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, int part, unsigned char* smem) {
+// This thread's channels of a query's part.
+struct StageWords {
+  uint4 w0, w1;
+};
+__device__ __forceinline__ StageWords stage_words(const PrefixQuery& a, int b, int part) {
+  const int h = kStageHeads * part + (threadIdx.x >> 5);
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + h) * kDMain) + 2 * (threadIdx.x & 31);
+  return StageWords{src[0], src[1]};
+}
+// words: read already, or null
+__device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, int part, unsigned char* smem,
+                                            const StageWords* words = nullptr) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = kStageHeads * part + warp;
   uint4* const img = reinterpret_cast<uint4*>(a.image + (int64_t)b * kHAtt * kDMain) + kStageHeads * part;
   auto image_at = [&](int i) -> uint4& { return img[i / kStageHeads * kHAtt + i % kStageHeads]; };
@@ -1398,8 +1412,8 @@ __device__ __forceinline__ void stage_block(const PrefixQuery& a, int B, int b, 
     if (lane == 0) a.c2[(int64_t)b * kHAtt + h] = 1.0f;
     return;
   }
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * kHAtt + h) * kDMain) + 2 * lane;
-  const uint4 q0 = src[0], q1 = src[1];
+  const StageWords x = words ? *words : stage_words(a, b, part);
+  const uint4 q0 = x.w0, q1 = x.w1;
   float4 g[4];
   if (a.norm_w)
 #pragma unroll
@@ -1592,7 +1606,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, P
   extern __shared__ __align__(16) unsigned char prep_smem[];
   ptx::griddep_launch();
   ptx::griddep_wait();
-  const int trees = kTree ? (a.G + kTreesPerCta - 1) / kTreesPerCta : 0, stage = kStageCtas * (a.B + 1);
+  const int trees = kTree ? (a.G + kTreesPerCta - 1) / kTreesPerCta : 0;
+  const int parts = kStageCtas * (a.B + 1), stage = kTree ? min(parts, kStageMost) : parts;
   const int widen = (int)gridDim.x - 1 - trees - stage, widen1 = min(widen, kWidenFirst);
   int b = (int)blockIdx.x - 1;
   if (b < 0) {
@@ -1609,7 +1624,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, P
   b -= trees;
   if (b < widen1) return widen_chunks<kTree>(a, k, image, b, widen);
   b -= widen1;
-  if (b < stage) return stage_block(q, a.B, b / kStageCtas, b % kStageCtas, prep_smem);
+  if (b < stage && stage == parts) return stage_block(q, a.B, b / kStageCtas, b % kStageCtas, prep_smem);
+  if (kTree && b < stage) {  // parts b, b + stage, ..: the next one's words are on their way while one is worked on
+    StageWords w{}, next{};
+    if (b < parts - kStageCtas) w = stage_words(q, b / kStageCtas, b % kStageCtas);  // the last query is none
+    for (int i = b; i < parts; i += stage) {
+      const int n = i + stage;
+      if (n < parts - kStageCtas) next = stage_words(q, n / kStageCtas, n % kStageCtas);
+      if (i != b) __syncthreads();  // shared memory is written again
+      stage_block(q, a.B, i / kStageCtas, i % kStageCtas, prep_smem, &w);
+      w = next;
+    }
+    return;
+  }
   widen_chunks<kTree>(a, k, image, widen1 + b - stage, widen);
 }
 
@@ -2475,7 +2502,8 @@ csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs
       const int trees = kTree ? (a.G + kTreesPerCta - 1) / kTreesPerCta : 0;
       const int widen = (int)(L.image_cap < kWidenCtas ? L.image_cap : kWidenCtas);
       // without its plan the attention would run whatever one the workspace held, and the join its parts
-      if (launch_pdl(prep, dim3((unsigned)(1 + trees + kStageCtas * (B + 1) + widen)), dim3(kPrepThreads),
+      const int stage = kTree ? std::min(kStageCtas * (B + 1), kStageMost) : kStageCtas * (B + 1);
+      if (launch_pdl(prep, dim3((unsigned)(1 + trees + stage + widen)), dim3(kPrepThreads),
                      (size_t)kPrepSmem, st, a, pq, k, L.image) != cudaSuccess)
         return launch_status();
     }
