@@ -132,6 +132,18 @@ constexpr int32_t kBadParent = INT32_MIN;
 __host__ __device__ __forceinline__ bool by_itself(int32_t B, int32_t G, int64_t shared_max) {
   return G == 0 || B < (int64_t)kImageQueries * G || B * shared_max < kPairWork;
 }
+// The same for trees, which share all their rows: the more tokens a tree has, the more a row of the image serves.  In pairs /
+// by themselves, us: trees of five on 2,000 (160,000 queries times entries) 54 / 50, on 4,000 80 / 72; of eight on 5,000
+// (160,000) 44.7 / 43.5; of nine on 20,000 (180,000) 47 / 45, on 40,000 68 / 73; of 16 on 5,000 (80,000) 32.6 / 32.5, on
+// 9,000 38.5 / 40.4; of 32 on 700 (90,000) 39 / 44; of 64 on 700 (45,000) 31.7 / 33.2.
+constexpr int64_t kTreeWork = 1 << 21;
+__host__ __device__ __forceinline__ bool trees_by_themselves(int32_t B, int32_t R, int64_t n_max) {
+  return B < (int64_t)kImageQueries * R || (int64_t)B * B * n_max < kTreeWork * R;
+}
+template <bool kTree>
+__host__ __device__ __forceinline__ bool alone_of(int32_t B, int32_t G, int64_t shared_max) {
+  return kTree ? trees_by_themselves(B, G, shared_max) : by_itself(B, G, shared_max);
+}
 // pairs of a batch, at most
 __host__ __device__ __forceinline__ int max_pairs(int32_t B, int32_t G) { return (B + G + 2) / 2; }
 
@@ -222,8 +234,10 @@ __device__ __forceinline__ bool tree_ok(const PrefixArgs& a, int lo, int hi) {
 __device__ __forceinline__ int tree_context(const PrefixArgs& a, int g) { return min(max(a.n_entries[g], 0), a.shared_max); }
 __device__ __forceinline__ int tree_image_chunks(int tokens, int n) { return tokens < kImageQueries ? 0 : n / kChunk; }
 // Trees share the chunks among the pairs of CTAs by what they cost: a request of few tokens has no image, and of short
-// contexts the tails and the change from pair to pair are most.  In units of half an image chunk.
-constexpr int kCostImage = 2, kCostRows = 3, kCostPair = 4;
+// contexts the tails and the change from pair to pair are most.  In units of half an image chunk; a change of 2 / 4 / 8, us:
+// ragged 48 of up to 32 on up to 4,001 134 / 135 / 141 (by the number of chunks 184), 64 of up to 48 on up to 900 118 / 123 /
+// 129; rows of 3 / 4 with a change of 4 135 / 140 and 123 / 127.
+constexpr int kCostImage = 2, kCostRows = 3, kCostPair = 2;
 __device__ __forceinline__ int image_chunks_of(const Pair& x) { return x.image >= 0 ? min(x.vis0 / kChunk, x.nshared) : 0; }
 __device__ __forceinline__ int cost_of(const Pair& x) {
   const int im = image_chunks_of(x);
@@ -1612,7 +1626,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_prefix_prep(PrefixArgs a, P
   int b = (int)blockIdx.x - 1;
   if (b < 0) {
     int32_t* ints = reinterpret_cast<int32_t*>(prep_smem);
-    if (by_itself(a.B, a.G, a.shared_max)) plan_block<true, kTree>(a, ints, kPrepSmem / 4);
+    if (alone_of<kTree>(a.B, a.G, a.shared_max)) plan_block<true, kTree>(a, ints, kPrepSmem / 4);
     else plan_block<false, kTree>(a, ints, kPrepSmem / 4);
     return;
   }
@@ -2241,14 +2255,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // once, while the first partials' channels are on their way.  Without slices a query has few partials: four (fp32: two) at
 // once, which leaves room for three CTAs on an SM (eight and two: paged ragged 128 x 2000 49.9 us, now 47.9).
 constexpr int kMergeThreads = 512;
-template <int kSlices, bool kHalf>
-__global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? 1 : 3) k_paged_merge(const int2* __restrict__ qpart,
+constexpr int kOneWave = 4;  // queries whose 32 CTAs each fit the GPU one to an SM
+// Queries of trees, each by itself, below which slices join them, with two CTAs on an SM from five on.  A call without /
+// with slices, us: 12 on 4,096 28.9 / 27.0, 16 30.6 / 30.0, 20 33.1 / 34.2, 32 on 3,000 35.2 / 39.4; with slices one CTA
+// to an SM / two: eight on 4,096 23.8 / 22.3, normalised and rotated 29.1 / 25.2.
+constexpr int kTreeSliceQueries = 17;
+// kTwo: with slices, two CTAs on an SM, for which half as many partials are on their way.
+template <int kSlices, bool kHalf, bool kTwo = false>
+__global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? (kTwo ? 2 : 1) : 3) k_paged_merge(const int2* __restrict__ qpart,
                                                                const uint4* __restrict__ part_o,
                                                                const float2* __restrict__ part_ml,
                                                                const float* __restrict__ sink,
                                                                const float2* __restrict__ turn, void* __restrict__ out,
                                                                float* lse, LseRest fix) {
-  constexpr int kAhead = kSlices > 1 ? 8 : kHalf ? 4 : 2;  // partials on their way
+  constexpr int kAhead = kSlices > 1 ? (kTwo ? 4 : 8) : kHalf ? 4 : 2;  // partials on their way
   constexpr int kTiles = 4 / kSlices, kPer = 128 * kTiles;
   static_assert(kSlices == 1 || kTiles == 1, "all channels, or a tile of them");
   __shared__ __align__(16) float s_w[kAlone][8];  // read four at a time
@@ -2405,7 +2425,7 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max, bool tree
     return p;
   };
   // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
-  const bool alone = by_itself(B, G, shared_max);
+  const bool alone = trees ? trees_by_themselves(B, G, shared_max) : by_itself(B, G, shared_max);
   const size_t parts = alone ? kAlone : kClusters * (trees ? tree_slices(B, G, shared_max) : 1), pairs = alone ? B : max_pairs(B, G);
   const size_t slots = (pairs + parts) * (alone ? 1 : 2);
   L.pairs = (Pair*)take((pairs + 1) * sizeof(Pair));
@@ -2473,7 +2493,7 @@ template <bool kTree>
 csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs& L, const AttnExtras& ex, const void* q_bf16,
                       float softmax_scale, const float* sink, void* out, int32_t out_type, float* lse_out, cudaStream_t st) {
   const int32_t B = a.B;
-  const bool alone = by_itself(B, a.G, a.shared_max);
+  const bool alone = alone_of<kTree>(B, a.G, a.shared_max);
   // bf16 queries are exact in f16 unless they were normalised or rotated
   uint16_t* const rest = lse_out && (ex.qnorm_w || ex.rope) ? L.rest : nullptr;
   const PrefixQuery pq{(const uint16_t*)q_bf16, ex.qnorm_w, ex.eps, softmax_scale, ex.rope, ex.qpos, ex.th,
@@ -2483,7 +2503,7 @@ csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs
   if (L.image_cap > 0 &&
       (!image_map(&maps.s, L.image, L.image_cap, 64, 16) || !image_map(&maps.o, L.image, L.image_cap, 32, 32)))
     return CSA2_ERR_CUDA;
-  const int slices = B < kSliceQueries ? 4 : 1;
+  const int slices = B < (kTree && alone ? kTreeSliceQueries : kSliceQueries) ? 4 : 1;
   const float2* turn = ex.rope ? L.turn : nullptr;
   auto merge = [&](auto kern, unsigned ctas, unsigned threads, unsigned cluster) {
     launch_clusters(kern, dim3(B, ctas), dim3(threads), 1, cluster, 0, st, (const int2*)L.qpart,
@@ -2514,7 +2534,8 @@ csa2_status attn_call(const PrefixArgs& a, const PrefixKernel& k, const PrefixWs
           return launch_status();
       }
       KernelTimer timer("k_paged_merge", st);
-      if (slices > 1) merge(k_paged_merge<4, kHalf>, 32, kMergeThreads, rest ? 4 : 1);
+      if (kTree && slices > 1 && B > kOneWave) merge(k_paged_merge<4, kHalf, true>, 32, kMergeThreads, rest ? 4 : 1);
+      else if (slices > 1) merge(k_paged_merge<4, kHalf>, 32, kMergeThreads, rest ? 4 : 1);
       else merge(k_paged_merge<1, kHalf>, 8, kMergeThreads, 1);
       return launch_status();
     }
@@ -2641,7 +2662,7 @@ extern "C" csa2_status csa2_tree_attn_decode(const csa2_kv_planes* kv, const csa
   const int slices = tree_slices(B, R, n_max);
   const PrefixArgs a{B, R, n_entries, trees->start, nullptr, (int32_t)n_max, 0, n_swa,
                      (int64_t)pages->max_pages * kv->seq_stride, L.pairs, L.gpair, L.chunk0, L.qpart, L.parts,
-                     L.gimage, L.gshared, L.image_cap, by_itself(B, R, n_max) ? kAlone : kClusters * slices, ws,
+                     L.gimage, L.gshared, L.image_cap, trees_by_themselves(B, R, n_max) ? kAlone : kClusters * slices, ws,
                      trees->parent, trees->max_tokens, trees->entries, L.cost0, L.kin, L.depth};
   const PrefixKernel k{kv->kv_codes, kv->kv_scales, swa_e4m3, L.qimage, L.c2, pages->table,
                        pages->max_pages, pages->n_pages, (int32_t)kv->seq_stride, n_swa, B,

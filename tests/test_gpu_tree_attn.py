@@ -56,8 +56,8 @@ class Forest:
         total = [h + t * entries for h, t in zip(n, T)]
         self.n_max = max(n)
         if pairs:  # queries run in pairs where there are five to a request and n_max makes for enough work
-            assert self.B >= 5 * R
-            self.n_max = max(self.n_max, -(-(1 << 17) // self.B))
+            self.n_max = max(self.n_max, -(-(R << 21) // self.B ** 2))
+            assert self.B >= 5 * R and self.n_max <= 65536
         self.most = max(1, max(T))
         self.max_pages = -(-(self.n_max + csa2.MAX_TREE) // P)
         count = sum(-(-t // P) for t in total) + spare
@@ -228,8 +228,8 @@ def test_random_forests(seed):
 
 def test_long_contexts():
     rng = np.random.default_rng(3)
-    f = Forest(3, [9000, 4000], [random_tree(rng, 16), random_tree(rng, 12)], 64, 128)
-    assert f.B * f.n_max >= 1 << 17
+    f = Forest(3, [12000, 4000], [random_tree(rng, 16), random_tree(rng, 12)], 64, 128)
+    assert f.B ** 2 * f.n_max >= f.R << 21
     f.device().check(of=[0, 1, 7, 15, 16, 20, 27])
 
 
