@@ -219,6 +219,11 @@ def _ptr(x) -> int | None:
     return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
+def _ptrs(*xs) -> list:
+    """_ptr of each: short calls spend much of their time on the host."""
+    return [x if x is None or x.__class__ is int else x.data_ptr() for x in xs]
+
+
 def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
@@ -386,9 +391,11 @@ def rope(x, n_rows: int, heads: int, dim: int, pos, rot: Rotary, out, inverse: b
     """Rotary positions: x [n_rows, heads, dim] (fp32 or bf16, rows and heads strided as the tensor says) -> out, which
     may be x; pos int64 [n_rows].  inverse: by -pos, which is the gradient (csa2_rope)."""
     kind = _common_type(x, out, type, "rope")
-    xs, ys = _strides(x, heads, dim, x_strides, "rope input"), _strides(out, heads, dim, out_strides, "rope output")
-    _ok(lib().csa2_rope(_ptr(x), *xs, _ptr(out), *ys, kind, n_rows, heads, dim, _ptr(pos), ctypes.byref(rot),
-                        int(bool(inverse)), _stream(stream)), "csa2_rope")
+    (x_row, x_head), (y_row, y_head) = (_strides(x, heads, dim, x_strides, "rope input"),
+                                        _strides(out, heads, dim, out_strides, "rope output"))
+    px, py, pp = _ptrs(x, out, pos)
+    _ok(lib().csa2_rope(px, x_row, x_head, py, y_row, y_head, kind, n_rows, heads, dim, pp, ctypes.byref(rot),
+                        1 if inverse else 0, _stream(stream)), "csa2_rope")
 
 
 def latent_append_workspace_size(R: int) -> int:
@@ -405,9 +412,9 @@ def latent_append(x, R: int, planes: Planes, n_slots: int, slot, entry, ws, key=
         if hasattr(t, "is_contiguous") and not t.is_contiguous():
             raise Csa2Error(1, f"latents or keys of strides {tuple(t.stride())}")
     kind = F32 if x is None and key is None else _common_type(x, key, type, "latents and keys")
-    _ok(lib().csa2_latent_append(_ptr(x), _ptr(key), kind, R, ctypes.byref(planes.c), n_slots, _ptr(slot), _ptr(entry),
-                                 _ref(kv_nr), _ref(scaling), _ptr(pos), _ref(key_rot), _ptr(ws), _nbytes(ws),
-                                 _stream(stream)), "csa2_latent_append")
+    px, pk, ps, pe, pp, pw = _ptrs(x, key, slot, entry, pos, ws)
+    _ok(lib().csa2_latent_append(px, pk, kind, R, ctypes.byref(planes.c), n_slots, ps, pe, _ref(kv_nr), _ref(scaling), pp,
+                                 _ref(key_rot), pw, _nbytes(ws), _stream(stream)), "csa2_latent_append")
 
 
 def swa_append(x, R: int, pos, n_queries: int, ring, n_win: int, query=None, nr: NormRope | None = None,
@@ -635,10 +642,10 @@ def tree_commit(planes: Planes | None, pages: Pages | None, trees: Trees, n_entr
     """Commit of accepted paths: token path[g, i] of request g becomes its entry n_entries[g] + i, its window row (of
     draft) takes its place of the ring at position pos[g] + i; n_new (or None) is what page_tables takes to drop the
     rest (csa2_tree_commit)."""
-    c = planes.c if planes is not None else None
-    _ok(lib().csa2_tree_commit(_ref(c), _ref(pages), ctypes.byref(trees), _ptr(n_entries), _ptr(n_accept), _ptr(path),
-                               n_path, _ptr(n_new), _ptr(draft), _ptr(pos), _ptr(ring), _ptr(ring_pos), n_win, _ptr(ws),
-                               _nbytes(ws), _stream(stream)), "csa2_tree_commit")
+    pn, pa, pp, pw, pd, ppos, pr, prp, pws = _ptrs(n_entries, n_accept, path, n_new, draft, pos, ring, ring_pos, ws)
+    _ok(lib().csa2_tree_commit(None if planes is None else ctypes.byref(planes.c), _ref(pages), ctypes.byref(trees), pn, pa,
+                               pp, n_path, pw, pd, ppos, pr, prp, n_win, pws, _nbytes(ws), _stream(stream)),
+        "csa2_tree_commit")
 
 
 def compress_workspace_size(T: int, d_model: int) -> int:

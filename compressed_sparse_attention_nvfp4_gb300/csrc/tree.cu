@@ -82,11 +82,10 @@ __global__ void __launch_bounds__(kThreads) k_tree_commit(CommitArgs a) {
     if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<ErrWord*>(a.ws) = ErrWord{0, 0, 0};
     if (a.checkers > 1) ptx::cluster_sync();
     else __syncthreads();
-    const int per = max(a.n_path, 1);  // a thread for each place of each path
-    const int64_t all = (int64_t)a.trees.R * per;
+    const int per = max(min(a.n_path, CSA2_MAX_TREE), 1), all = a.trees.R * per;  // a thread for each place of each path
 #pragma unroll 4
-    for (int64_t i = blockIdx.x * kThreads + tid; i < all; i += a.checkers * kThreads) {
-      const int g = (int)(i / per), k = (int)(i - (int64_t)g * per);
+    for (int i = blockIdx.x * kThreads + tid; i < all; i += a.checkers * kThreads) {
+      const int g = i / per, k = i - g * per;
       Commit c;
       int t;
       int64_t from, to;
