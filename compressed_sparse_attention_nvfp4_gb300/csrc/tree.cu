@@ -45,7 +45,8 @@ __device__ __forceinline__ bool commit_of(const CommitArgs& a, int g, Commit& c)
   c.have = a.trees.entries ? a.n_entries[g] : 0;
   c.pos = a.n_win > 0 ? a.pos[g] : 0;
   if (lo < 0 || hi < lo || hi > a.trees.B || c.tokens > a.trees.max_tokens) return false;
-  if (c.keep < 0 || c.keep > min(c.tokens, a.n_path) || c.have < 0 || c.pos < 0) return false;
+  if (c.keep < 0 || c.keep > min(c.tokens, a.n_path) || c.have < 0) return false;
+  if (c.pos < 0 || c.pos > INT64_MAX - CSA2_MAX_TREE) return false;  // the last token's position is one too
   return !a.trees.entries || (int64_t)c.have + c.tokens <= (int64_t)a.max_pages * a.kv.seq_stride;
 }
 // plane row of entry e of request g, or -1

@@ -666,8 +666,8 @@ size_t csa2_tree_attn_workspace_size(int32_t R, int32_t B, int32_t max_tokens, i
  *              [R][n_win]: the i-th kept token's window row goes to ring place (pos[g] + i) mod n_win, the last n_win of
  *              them where there are more; n_win = 0: no window, the four may be NULL
  * A request whose start is not in order, whose tree has more than max_tokens tokens, with n_accept outside [0, min(tokens,
- * n_path)], a path index outside its tree, a negative n_entries or pos, an entry outside the table's row or a page outside
- * the planes is reported as CSA2_ERR_INDEX_RANGE (detail: the request) and stays as it is, n_new 0.
+ * n_path)], a path index outside its tree, a negative n_entries, a pos outside [0, 2^63 - 65], an entry outside the table's
+ * row or a page outside the planes is reported as CSA2_ERR_INDEX_RANGE (detail: the request) and stays as it is, n_new 0.
  * 1 <= R <= 65535; ws: csa2_tree_commit_workspace_size(R) bytes (the error word). */
 csa2_status csa2_tree_commit(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
                              const int32_t* n_entries, const int32_t* n_accept, const int32_t* path, int32_t n_path,

@@ -382,3 +382,15 @@ def test_graph_replayed_on_other_trees(pairs):
     graph.replay()
     assert csa2.check(ws) == (0, 0)
     close(out, lse, g.reference(), None, torch.float32)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_more_requests_than_the_plans_lists_hold(pairs):
+    # lists of 2,048 requests and more lie in global memory, and those of 4,096 pairs and more
+    R = 2100 if pairs else 5000
+    rng = np.random.default_rng(16)
+    trees = [binary(int(T)) for T in (rng.integers(4, 9, R) if pairs else rng.integers(0, 3, R))]
+    trees[0], trees[-1] = binary(9), binary(9)
+    f = Forest(16, rng.integers(0, 30, R).tolist(), trees, 16, 3, pairs=pairs)
+    assert not pairs or (f.B > 8400 and f.B ** 2 * f.n_max >= R << 21)
+    f.device().check(torch.bfloat16, of=[0, 5, 8, 9, f.B // 3, f.B // 2, f.B - 9, f.B - 1])

@@ -118,7 +118,8 @@ def test_far_positions():
 @pytest.mark.parametrize("put,skip", [
     (dict(accept=[2, 5]), 1), (dict(accept=[-1, 1]), 0), (dict(accept=[4, 1]), 0), (dict(path=[[0, 3, 0], [1, 0, 0]]), 0),
     (dict(path=[[0, -1, 0], [1, 0, 0]]), 0), (dict(start=[0, 3, 99]), 1), (dict(start=[4, 3, 7]), 0), (dict(start=[-1, 3, 7]), 0),
-    (dict(have=[4, -1]), 1), (dict(have=[4, 1 << 30]), 1), (dict(pos=[-1, 5]), 0)])
+    (dict(have=[4, -1]), 1), (dict(have=[4, 1 << 30]), 1), (dict(pos=[-1, 5]), 0),
+    (dict(pos=[3, (1 << 63) - 2]), 1)])
 def test_what_is_out_of_range_stays_as_it_is(put, skip):
     c = Case(3, [4, 5], [3, 4], [[0, 2], [1]], 8, n_path=3)
     put = {k: np.array(v, np.int64 if k == "pos" else np.int32) for k, v in put.items()}
