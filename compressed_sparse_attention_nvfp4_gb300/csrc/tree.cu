@@ -55,10 +55,13 @@ __device__ __forceinline__ int64_t row_of(const CommitArgs& a, int g, int64_t e)
   const int page = a.table[(int64_t)g * a.max_pages + pi];
   return page < 0 || page >= a.n_pages ? -1 : page * a.kv.seq_stride + (e - pi * a.kv.seq_stride);
 }
-// token i of the path and its entry's rows, by one thread; false where they are none
-__device__ __forceinline__ bool kept_token(const CommitArgs& a, int g, const Commit& c, int i, int& t, int64_t& from,
+// place i of request g's path, whether it counts or not: asked for with the lengths that say so
+__device__ __forceinline__ int path_at(const CommitArgs& a, int g, int i) {
+  return i < a.n_path ? a.path[(int64_t)g * a.n_path + i] : -1;
+}
+// the rows of token t's entry, place i of the path, by one thread; false where they are none
+__device__ __forceinline__ bool kept_token(const CommitArgs& a, int g, const Commit& c, int i, int t, int64_t& from,
                                            int64_t& to) {
-  t = a.path[(int64_t)g * a.n_path + i];
   from = to = 0;
   if (t < 0 || t >= c.tokens) return false;
   if (!a.trees.entries) return true;
@@ -88,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) k_tree_commit(CommitArgs a) {
     for (int i = blockIdx.x * kThreads + tid; i < all; i += a.checkers * kThreads) {
       const int g = i / per, k = i - g * per;
       Commit c;
-      int t;
       int64_t from, to;
+      const int t = path_at(a, g, k);
       if (!commit_of(a, g, c) || (k < c.keep && !kept_token(a, g, c, k, t, from, to)))
         report_error(a.ws, CSA2_ERR_INDEX_RANGE, g);
     }
@@ -98,8 +101,12 @@ __global__ void __launch_bounds__(kThreads) k_tree_commit(CommitArgs a) {
   const int g = (int)blockIdx.x - a.checkers;
   if (g >= a.trees.R) return;
   Commit c;
+  const int t = tid < CSA2_MAX_TREE ? path_at(a, g, tid) : -1;
   bool ok = commit_of(a, g, c);
-  if (ok && tid < c.keep) ok = kept_token(a, g, c, tid, s_token[tid], s_from[tid], s_to[tid]);
+  if (ok && tid < c.keep) {
+    s_token[tid] = t;
+    ok = kept_token(a, g, c, tid, t, s_from[tid], s_to[tid]);
+  }
   ok = __syncthreads_and(ok);
   if (a.n_new && tid == 0) a.n_new[g] = ok && a.trees.entries ? c.keep - c.tokens : 0;
   if (!ok) return;
