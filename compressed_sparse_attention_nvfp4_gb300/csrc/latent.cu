@@ -4,12 +4,15 @@
 // the cache's codec; its indexer key: turned by pos, then the codec.  The codec's borders make the bytes depend on the
 // last bits of y: from a y formed in fp32, off by up to 2^-19, a code in some thousand rows falls to the other side.  So
 // a row is formed in fp32 first, with every value's code taken at both ends of what it may be; where the ends agree,
-// the byte is certain.  Where one does not (one row in twenty after a norm), the row is formed again in pairs of fp32
+// the byte is certain.  Where one does not (one row in fifty after a norm), the row is formed again in pairs of fp32
 // (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
 //
 // A warp takes a row's main copy: lane l reads, normalises and rotates the channels 128 i + 4 l .. (whole lines) and
 // quantizes 16 l .. (a group); the row changes hands in shared memory.  Another takes four rows' keys, eight lanes to
-// each in the end.  Bytes bound a long call: up to 2,560 read and 356 written a row.
+// each in the end.  Bytes would bound a long call, up to 2,560 read and 356 written a row; measured, instructions and
+// the chain from a row's loads to its bytes do: 32,768 fp32 rows with keys, normalised and rotated, 28 us (3.4 TB/s; the
+// main copies alone without norm and rotation 15), four rows to a warp with the next one's loads ahead 26 but 128 rows
+// 3.6 instead of 3.2.
 #include "codec.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -21,11 +24,11 @@ namespace {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kKeys = 4;  // rows whose keys a warp takes
 // CTAs that look at the destinations: a cluster, so that none reports before the word is cleared; one for few rows
-constexpr int kCheckers = 8, kManyRows = 4096;
+constexpr int kReporters = 8, kManyRows = 4096;
 
 struct LatentArgs {
   const void *x, *key;
-  int32_t R, n_slots, checkers, main_ctas;
+  int32_t R, n_slots, reporters, main_ctas;
   const int32_t* slot;
   const int64_t* entry;
   int64_t stride;
@@ -156,8 +159,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // How far a value formed in fp32 may be off.  A norm: 16 fused steps and five sums of 2^-24 each, halved by the root,
-// the root's two units and two products: below 2^-20 of the value.  A rotation: 2^-21 of |a| + |b| of its pair (angle 2^-24
-// pi, sine and cosine 2^-22, three roundings).  A rotated channel of the main copy has its partner in its group, so
+// the root's two units and two products: below 2^-20 of the value.  A rotation: 2^-21 of |a| + |b| of its pair (angle
+// 2^-24 pi, sine and cosine 2^-22, three roundings).  A rotated channel of the main copy has its partner in its group, so
 // |a| + |b| <= 2 amax, and together 3 2^-20 amax; in units of the scale, of which amax is at most nine, below 2^-15.
 // A channel that is normalised alone is off by 2^-20 of itself: below 2^-17 of the scale up to eight of it, beyond which
 // its code is the largest anyway.
@@ -168,7 +171,8 @@ __device__ __forceinline__ Off off_by(bool norm, bool turned) {
   return turned ? Off{0x1p-18f, 0x1p-15f} : norm ? Off{0x1p-19f, 0x1p-17f} : Off{0.0f, 0.0f};
 }
 constexpr float kTopMost = 2600.0f;  // beyond, the scale saturates and amax may be more than nine of it
-constexpr float kOffTurn = 0x1p-20f;  // of a key's channel, in units of the row's largest, turned: |a| + |b| is two of it at most
+// of a key's channel, in units of the row's largest, turned: |a| + |b| is two of it at most
+constexpr float kOffTurn = 0x1p-20f;
 
 // The codes of eight values (E2M1, nearest even): value i of v at nibble i.
 __device__ __forceinline__ uint32_t codes8(const uint64_t (&t)[4]) {
@@ -223,8 +227,8 @@ __device__ __forceinline__ bool main_group(const uint64_t (&y)[8], Off by, uint2
   return sure;
 }
 
-// Sixteen values of a row in shared memory, 64 bytes of it, by chunks of four: lane l's first chunk is l / 2 mod 4, so that
-// the eight lanes of an access are at different banks.
+// Sixteen values of a row in shared memory, 64 bytes of it, by chunks of four: lane l's first chunk is l / 2 mod 4, so
+// that the eight lanes of an access are at different banks.
 __device__ __forceinline__ int first_chunk(int lane) { return lane >> 1 & 3; }
 __device__ __forceinline__ void take16(const float* at, int lane, uint64_t (&y)[8]) {
 #pragma unroll
@@ -303,8 +307,8 @@ __device__ __forceinline__ int key_exponent(float amax) { return max((int)(__flo
 // The keys of rows r .. r + kKeys - 1, eight lanes to each; returns the rows (bit i: row r + i) that are not certain,
 // of which nothing is written.
 template <typename T>
-__device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const LatentTurns& turns, int r, float (*s_row)[kDIdx + 4],
-                                                int lane) {
+__device__ __forceinline__ uint32_t append_keys(const LatentArgs& a, const LatentTurns& turns, int r,
+                                                float (*s_row)[kDIdx + 4], int lane) {
   const int i = lane / 8, j = lane % 8;  // the row, and of it channels 16 j ..
 #pragma unroll
   for (int u = 0; u < kKeys; ++u) {
@@ -452,7 +456,8 @@ __device__ __noinline__ void exact_key(const LatentArgs& a, const LatentTurns& t
   }
   float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));  // eight lanes have a group
+  for (int o = 4; o >= 1; o >>= 1)  // eight lanes have a group
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const int e = key_exponent(amax);
   const float f = exp2i_f32(-e);
   uint32_t codes = 0;
@@ -470,18 +475,18 @@ __global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_cons
   static_assert(kKeys * (kDIdx + 4) >= kDMain, "a row");
   ptx::griddep_launch();
   ptx::griddep_wait();
-  if ((int)blockIdx.x < a.checkers) {  // these report destinations outside the planes: the error word is theirs alone
+  if ((int)blockIdx.x < a.reporters) {  // these report destinations outside the planes: the error word is theirs alone
     if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<ErrWord*>(a.ws) = ErrWord{0, 0, 0};
-    if (a.checkers > 1) ptx::cluster_sync();
+    if (a.reporters > 1) ptx::cluster_sync();
     else __syncthreads();
 #pragma unroll 8
-    for (int r = blockIdx.x * kThreads + threadIdx.x; r < a.R; r += a.checkers * kThreads)
+    for (int r = blockIdx.x * kThreads + threadIdx.x; r < a.R; r += a.reporters * kThreads)
       if (place(a, r) == -2)
         report_error(a.ws, CSA2_ERR_INDEX_RANGE,
                      a.slot[r] < 0 || a.slot[r] >= a.n_slots ? (long long)a.slot[r] : a.entry[r]);
     return;
   }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cta = (int)blockIdx.x - a.checkers;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, cta = (int)blockIdx.x - a.reporters;
   if (cta >= a.main_ctas) {
     const int r = ((cta - a.main_ctas) * kWarps + warp) * kKeys;
     if (!a.key || r >= a.R) return;
@@ -500,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_cons
   const uint64_t pos = a.pos ? (uint64_t)__ldg(a.pos + r) : 0;
   const int64_t row = place(a, r);
   if (row < 0) return;  // the same for the whole warp
-  if (!append_main(a, turns, v, row, pos, s_row[warp][0], lane)) exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
+  if (!append_main(a, turns, v, row, pos, s_row[warp][0], lane))
+    exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
 }
 
 }  // namespace
@@ -523,10 +529,11 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   const bool rope = x && kv_nr && kv_nr->rope, key_rope = key && key_rot;
   if (R > 0 && (!slot || !entry || ((rope || key_rope) && !pos))) return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256) || ws_bytes < kWsHeader) return CSA2_ERR_WORKSPACE;
-  const int checkers = R > kManyRows ? kCheckers : 1;
-  LatentArgs a{x, key, R, n_slots, checkers, x ? (int)cdiv(R, kWarps) : 0, slot, entry, dst->seq_stride, pos, x && kv_nr ? kv_nr->norm_weight : nullptr,
-               kv_nr ? kv_nr->norm_eps : 0.0f, rope, 0, 0, 0, 0, 1.0f, dst->kv_codes, dst->kv_scales, dst->ix_codes,
-               dst->ix_scales, ws};
+  const int reporters = R > kManyRows ? kReporters : 1;
+  const int main_ctas = x ? (int)cdiv(R, kWarps) : 0, key_ctas = key ? (int)cdiv(R, kWarps * kKeys) : 0;
+  LatentArgs a{x, key, R, n_slots, reporters, main_ctas, slot, entry, dst->seq_stride, pos,
+               x && kv_nr ? kv_nr->norm_weight : nullptr, kv_nr ? kv_nr->norm_eps : 0.0f, rope, 0, 0, 0, 0, 1.0f,
+               dst->kv_codes, dst->kv_scales, dst->ix_codes, dst->ix_scales, ws};
   LatentTurns turns{};
   if (rope) make_turns(&turns.kv, 64, kv_nr->rope_base, scaling);
   if (key_rope) {
@@ -541,8 +548,8 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   cudaStream_t st = (cudaStream_t)stream;
   KernelTimer timer("k_latent_append", st);
   const auto kern = type == CSA2_F32 ? k_latent_append<float> : k_latent_append<uint16_t>;
-  const unsigned ctas = (unsigned)align_up((size_t)(checkers + a.main_ctas + (key ? cdiv(R, kWarps * kKeys) : 0)), (size_t)checkers);
-  if (checkers > 1) launch_clusters(kern, dim3(ctas), dim3(kThreads), checkers, 1, 0, st, a, turns);
+  const unsigned ctas = (unsigned)align_up((size_t)reporters + main_ctas + key_ctas, (size_t)reporters);
+  if (reporters > 1) launch_clusters(kern, dim3(ctas), dim3(kThreads), reporters, 1, 0, st, a, turns);
   else launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, st, a, turns);
   return launch_status();
 }

@@ -29,6 +29,11 @@
 // Behind the shared entries come the two queries' own (their last entries and windows): chunks whose
 // first 64 rows are the first query's and whose last 64 the second's, each query masking the other's; behind
 // the shorter's last, 128 rows of the longer.
+// Trees of drafted tokens (kTree): a request's queries share all its rows, its context and behind it the drafts' entries,
+// its ring and the drafts' window rows, of which each query sees its own path's.  The preparation follows the parents
+// (tree_block); whole chunks of context come from the image, the others' rows carry in a bit whether the CTA's query sees
+// them (flip_seen), and probabilities of rows that it does not are 0.  Measured: 16 trees of 16 tokens on 8,192 entries,
+// normalised and rotated, 281 us (0.99 PFLOP/s), 4 of 64 on 65,000 1,580 us (1.38 PFLOP/s), one of 8 on 4,096 22 us.
 // Measured: 64 queries on 65,000 shared entries 405 us, 1.35 PFLOP/s, 71 % of the rate of a library bf16
 // product; 32 on 8,192, normalised and rotated, 51 us.
 #include <algorithm>
@@ -1727,7 +1732,8 @@ __device__ __forceinline__ float corrected(const LseRest& f, int b, int h, float
 // A CTA joins 8 / kSlices heads: thread t of a slice has head t % (8 / kSlices) of them and kVec planes (of eight
 // channels): two, which share a weight, or one where slices make for more threads (one for all: 4 us more for
 // 101 queries).
-// Many queries of trees have two partials or so: two at once leave room for more CTAs on an SM.
+// Many queries of trees have two partials or so: two at once leave room for more CTAs on an SM (the join of 256 queries
+// 28 us with eight, 19 with two, of 664 39 and 25).
 template <int kSlices, bool kHalf, bool kTree>
 struct PrefixMerge {
   static constexpr int kVec = kSlices > 1 ? 1 : 2, kHeads = 8 / kSlices, kPer = kHeads * (kDMain / 8) / kVec;
@@ -1735,12 +1741,11 @@ struct PrefixMerge {
   static constexpr int kThreads = kPer * kSlices, kCtas = kTree && kSlices == 1 ? (kHalf ? 5 : 4) : 1;
 };
 template <int kSlices, bool kHalf, bool kTree>
-__global__ void __launch_bounds__(PrefixMerge<kSlices, kHalf, kTree>::kThreads, PrefixMerge<kSlices, kHalf, kTree>::kCtas) k_prefix_merge(const int2* __restrict__ qpart,
-                                                                const uint4* __restrict__ part_o,
-                                                                const float2* __restrict__ part_ml,
-                                                                const float* __restrict__ sink,
-                                                                const float2* __restrict__ turn, void* __restrict__ out,
-                                                                float* __restrict__ lse, LseRest fix) {
+__global__ void __launch_bounds__(PrefixMerge<kSlices, kHalf, kTree>::kThreads,
+                                  PrefixMerge<kSlices, kHalf, kTree>::kCtas)
+    k_prefix_merge(const int2* __restrict__ qpart, const uint4* __restrict__ part_o, const float2* __restrict__ part_ml,
+                   const float* __restrict__ sink, const float2* __restrict__ turn, void* __restrict__ out,
+                   float* __restrict__ lse, LseRest fix) {
   using Form = PrefixMerge<kSlices, kHalf, kTree>;
   using Vec = Vec8<kHalf>;
   constexpr int kVec = Form::kVec, kHeads = Form::kHeads, kPer = Form::kPer, kC = 8 * kVec, kAhead = Form::kAhead;
@@ -2426,7 +2431,8 @@ PrefixWs prefix_ws(void* ws, int32_t B, int32_t G, int64_t shared_max, bool tree
   };
   // partials: of pairs cut by kClusters pairs of CTAs (two queries each), or of queries cut by kAlone CTAs
   const bool alone = trees ? trees_by_themselves(B, G, shared_max) : by_itself(B, G, shared_max);
-  const size_t parts = alone ? kAlone : kClusters * (trees ? tree_slices(B, G, shared_max) : 1), pairs = alone ? B : max_pairs(B, G);
+  const size_t parts = alone ? kAlone : kClusters * (trees ? tree_slices(B, G, shared_max) : 1);
+  const size_t pairs = alone ? B : max_pairs(B, G);
   const size_t slots = (pairs + parts) * (alone ? 1 : 2);
   L.pairs = (Pair*)take((pairs + 1) * sizeof(Pair));
   L.gpair = (int32_t*)take(((size_t)G + 3) * 4);

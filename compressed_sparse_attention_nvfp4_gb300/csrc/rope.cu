@@ -17,9 +17,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatch = 2;              // units of a kind that a thread has on their way
-// Units of a tile, of the kind of which it has more: at most, and at least where the call has them.  512 / 1,024 / 1,536 /
-// 2,048 at most, us: 32,768 x 32 queries of 128 103 / 82 / 83 / 84, 16,385 rows of 512 fp32 17.1 / 14.4 / 15.8 / 15.8 (four
-// on their way in three CTAs an SM instead of two in four: 82 and 14.5 at 2,048, 85 and 15.4 at 1,024).
+// Units of a tile, of the kind of which it has more: at most, and at least where the call has them.  512 / 1,024 /
+// 1,536 / 2,048 at most, us: 32,768 x 32 queries of 128 channels 87 / 82 / 83 / 84, 16,385 rows of 512 in fp32 17.1 /
+// 14.4 / 15.8 / 15.8 (four on their way in three CTAs an SM instead of two in four: 82 and 14.5 at 2,048).
 constexpr int kUnits = 4 * kThreads, kFewUnits = 256;
 constexpr int kTiles = 608;            // tiles that fill the GPU: four on an SM
 constexpr int kTable = 4096;           // cosines of a tile, at most
@@ -38,7 +38,9 @@ struct RopeArgs {
 };
 
 // i / d for i, d <= 2^16, by a product with r = ceil(2^32 / d); d = 1 has none
-__host__ __device__ __forceinline__ uint32_t reciprocal(uint32_t d) { return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0; }
+__host__ __device__ __forceinline__ uint32_t reciprocal(uint32_t d) {
+  return d > 1 ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0;
+}
 __device__ __forceinline__ int over(int i, uint32_t r) { return r ? (int)__umulhi((uint32_t)i, r) : i; }
 
 template <typename T, int kV>
@@ -217,8 +219,10 @@ extern "C" csa2_status csa2_rope(const void* x, int64_t x_row, int64_t x_head, v
   if (x_row > kMost >> 12 || x_row < -(kMost >> 12) || x_head > kMost || x_head < -kMost || y_row > kMost >> 12 ||
       y_head > kMost)
     return CSA2_ERR_INVALID_ARG;
-  const bool by_row = (heads == 1 || y_head >= dim) && (n_rows == 1 || y_row >= (heads - 1) * (heads > 1 ? y_head : 0) + dim);
-  const bool by_head = (n_rows == 1 || y_row >= dim) && (heads == 1 || y_head >= (n_rows - 1) * (n_rows > 1 ? y_row : 0) + dim);
+  const int64_t row_of = (heads > 1 ? (heads - 1) * y_head : 0) + dim;
+  const int64_t head_of = (n_rows > 1 ? (n_rows - 1) * y_row : 0) + dim;
+  const bool by_row = (heads == 1 || y_head >= dim) && (n_rows == 1 || y_row >= row_of);
+  const bool by_head = (n_rows == 1 || y_row >= dim) && (heads == 1 || y_head >= head_of);
   if (!by_row && !by_head) return CSA2_ERR_INVALID_ARG;
   const int64_t v = 16 / (int64_t)size;
   const bool wide = aligned(x, 16) && aligned(y, 16) && rot->first % v == 0 && rot->n_rot / 2 % v == 0 && dim % v == 0 &&

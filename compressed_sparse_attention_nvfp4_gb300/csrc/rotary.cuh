@@ -73,8 +73,9 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t f, int64_t pos, float& c, 
   const uint32_t phase = (uint32_t)(((uint64_t)pos * f) >> 32);
   const uint32_t quarter = (phase + (1u << 29)) >> 30;
   const float x = (float)(int32_t)(phase - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), z = x * x;
-  const float sn = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), x);
-  const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f), -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
+  float sn = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f), cs = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  sn = fmaf(x * z, fmaf(z, fmaf(z, sn, 1.0f / 120.0f), -1.0f / 6.0f), x);
+  cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, cs, -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
   c = quarter & 1 ? sn : cs;
   s = quarter & 1 ? cs : sn;
   if ((quarter + 1) & 2) c = -c;

@@ -640,10 +640,11 @@ typedef struct {
  *   out        [B][64][512] of out_type; lse_out [B][64] or NULL
  * Queries outside every tree see no rows.  A start that is not in order within [0, B], or a tree of more than max_tokens
  * tokens, is reported as CSA2_ERR_INDEX_RANGE (detail: such a request), and no query of the call sees any row; a parent
- * outside [-1, own index) is reported (detail: the query) and counts as -1.  Pages outside the planes, NaN, roundings, sink and repeated calls
- * as in csa2_paged_attn_decode.  1 <= R <= 65535, 1 <= B <= 65535, n_pages * seq_stride <= 2^30; ws:
- * csa2_tree_attn_workspace_size(R, B, max_tokens, n_max, n_swa) bytes.  As in csa2_prefix_attn_decode the host's bounds
- * decide whether the queries of a request run in pairs, and whether its context is widened once for all of them. */
+ * outside [-1, own index) is reported (detail: the query) and counts as -1.  Pages outside the planes, NaN, roundings,
+ * sink and repeated calls as in csa2_paged_attn_decode.  1 <= R <= 65535, 1 <= B <= 65535, n_pages * seq_stride <= 2^30;
+ * ws: csa2_tree_attn_workspace_size(R, B, max_tokens, n_max, n_swa) bytes.  As in csa2_prefix_attn_decode the host's
+ * bounds decide whether the queries of a request run in pairs, and whether its context is widened once for all of them:
+ * 1 KB of workspace for each entry then, R * n_max of them and 1 GB at most. */
 csa2_status csa2_tree_attn_decode(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
                                   const int32_t* n_entries, int64_t n_max, const uint8_t* swa_e4m3,
                                   const int64_t* swa_pos, const uint8_t* draft_e4m3, int32_t n_swa, const void* q_bf16,
@@ -665,9 +666,10 @@ size_t csa2_tree_attn_workspace_size(int32_t R, int32_t B, int32_t max_tokens, i
  *   draft_e4m3 [B][512], pos [R] int64 (the position of the first draft), ring [R][n_win][512], ring_pos
  *              [R][n_win]: the i-th kept token's window row goes to ring place (pos[g] + i) mod n_win, the last n_win of
  *              them where there are more; n_win = 0: no window, the four may be NULL
- * A request whose start is not in order, whose tree has more than max_tokens tokens, with n_accept outside [0, min(tokens,
- * n_path)], a path index outside its tree, a negative n_entries, a pos outside [0, 2^63 - 65], an entry outside the table's
- * row or a page outside the planes is reported as CSA2_ERR_INDEX_RANGE (detail: the request) and stays as it is, n_new 0.
+ * A request whose start is not in order, whose tree has more than max_tokens tokens, with n_accept outside [0,
+ * min(tokens, n_path)], a path index outside its tree, a negative n_entries, a pos outside [0, 2^63 - 65], an entry
+ * outside the table's row or a page outside the planes is reported as CSA2_ERR_INDEX_RANGE (detail: the request) and
+ * stays as it is, n_new 0.
  * 1 <= R <= 65535; ws: csa2_tree_commit_workspace_size(R) bytes (the error word). */
 csa2_status csa2_tree_commit(const csa2_kv_planes* kv, const csa2_pages* pages, const csa2_trees* trees,
                              const int32_t* n_entries, const int32_t* n_accept, const int32_t* path, int32_t n_path,
