@@ -248,6 +248,7 @@ __device__ __forceinline__ int cost_of(const Pair& x) {
   const int im = image_chunks_of(x);
   return x.nshared > 0 ? kCostPair + kCostImage * im + kCostRows * (x.nshared - im) : 0;
 }
+constexpr int kSliceChunks = 512;  // chunks of image (64 MB) to each part of the list that all CTAs work on (tree_slices)
 // the largest i in [0, n) with list[i] <= x, list[0] <= x
 __device__ __forceinline__ int last_at_most(const int32_t* list, int n, int x) {
   int lo = 0, hi = n;
@@ -415,7 +416,10 @@ __device__ __forceinline__ void plan_block(const PrefixArgs& a, int32_t* smem, i
   if constexpr (kCosts) {
     // Chunk t, which begins at cost s, belongs to part s parts / costs.  Chunks begin kCostPair + kCostRows apart at
     // most, so no part is empty if it is as long.
-    const long long parts = min((long long)a.parts, (long long)costs / (kCostPair + kCostRows));
+    // no more parts than the image needs: tree_slices goes by the bounds
+    const long long image = min((long long)images, (long long)a.image_cap);
+    const long long most = max((image + kSliceChunks - 1) / kSliceChunks, 1LL) * kClusters;
+    const long long parts = min(min((long long)a.parts, most), (long long)costs / (kCostPair + kCostRows));
     for (int p = tid; p < np; p += kPrepThreads) {
       const Pair& x = a.pairs[p];
       int k0 = 0, k1 = 0;
@@ -2399,7 +2403,7 @@ __global__ void __launch_bounds__(kMergeThreads, kSlices > 1 ? (kTwo ? 2 : 1) : 
 // 684 / 667 / 656 / 634 / 639 / 637, 16 of 16 on 8,192 (128 MB) 232 / 219 / 217 / 216 / 223 / 232, 48 of 16 on 2,000
 // (96 MB) 200 / 192 / 193 / 198 / 199 / 210.  A part has sixteen chunks at least, by the bounds.
 int tree_slices(int32_t B, int32_t G, int64_t n_max) {
-  const int64_t image = (G * cdiv(n_max, kChunk) + 511) / 512, chunks = B * n_max / (2 * kChunk);
+  const int64_t image = cdiv(G * cdiv(n_max, kChunk), kSliceChunks), chunks = B * n_max / (2 * kChunk);
   return (int)std::max<int64_t>(1, std::min<int64_t>({8, image, chunks / (16 * kClusters)}));
 }
 

@@ -394,3 +394,19 @@ def test_more_requests_than_the_plans_lists_hold(pairs):
     f = Forest(16, rng.integers(0, 30, R).tolist(), trees, 16, 3, pairs=pairs)
     assert not pairs or (f.B > 8400 and f.B ** 2 * f.n_max >= R << 21)
     f.device().check(torch.bfloat16, of=[0, 5, 8, 9, f.B // 3, f.B // 2, f.B - 9, f.B - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("extras,sink", [(True, True), (True, False), (False, True), (False, False)])
+def test_more_pairs_than_parts(extras, sink, dtype):
+    # most pairs are one CTA pair's as a whole
+    R = 90
+    rng = np.random.default_rng(17 + extras)
+    trees = [random_tree(rng, int(T)) for T in rng.integers(3, 12, R)]
+    trees[3], trees[40], trees[-1] = [], chain(11), star(1)
+    f = Forest(17, rng.integers(0, 60, R).tolist(), trees, 16, 128, extras=extras, sink=sink, pairs=True, pad=2)
+    f.device()
+    out, lse = f.check(dtype, of=sorted(rng.choice(f.B, 60, replace=False).tolist()) + [f.B - 3, f.B - 1])
+    # without the logsumexp the same outputs
+    again, _, ws = f.run(dtype, lse=None)
+    assert csa2.check(ws) == (0, 0) and torch.equal(out, again)
