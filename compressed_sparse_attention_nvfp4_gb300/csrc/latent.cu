@@ -7,12 +7,12 @@
 // the byte is certain.  Where one does not (one row in fifty after a norm), the row is formed again in pairs of fp32
 // (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
 //
-// A warp takes a row's main copy: lane l reads, normalises and rotates the channels 128 i + 4 l .. (whole lines) and
-// quantizes 16 l .. (a group); the row changes hands in shared memory.  Another takes four rows' keys, eight lanes to
-// each in the end.  Bytes would bound a long call, up to 2,560 read and 356 written a row; measured, instructions and
-// the chain from a row's loads to its bytes do: 32,768 fp32 rows with keys, normalised and rotated, 28 us (3.4 TB/s; the
-// main copies alone without norm and rotation 15), four rows to a warp with the next one's loads ahead 26 but 128 rows
-// 3.6 instead of 3.2.
+// A warp takes the main copies of one row or two: lane l reads, normalises and rotates the channels 128 i + 4 l .. (whole
+// lines) and quantizes 16 l .. (a group); a row changes hands in shared memory.  Another takes four rows' keys, eight
+// lanes to each in the end.  Bytes would bound a long call, up to 2,560 read and 356 written a row; measured, the chain
+// from a row's loads to its bytes does, some 390 instructions of which a warp issues one in eleven cycles: 32,768 fp32
+// rows with keys, normalised and rotated, 24.6 us (3.9 TB/s; the main copies alone without norm and rotation 17).  Two
+// rows are two chains side by side.
 #include "codec.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -24,7 +24,12 @@ namespace {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kKeys = 4;  // rows whose keys a warp takes
 // CTAs that look at the destinations: a cluster, so that none reports before the word is cleared; one for few rows
-constexpr int kReporters = 8, kManyRows = 4096;
+// (4,096 rows with one / eight 8.8 / 6.6 us, 2,048 without norm, rotation and keys 4.6 / 2.8).
+constexpr int kReporters = 8, kManyRows = 512;
+// Rows from which a warp takes two.  One / two, us, normalised and rotated with keys: 8,192 9.4 / 9.5, 12,000 11.9 / 11.7,
+// 16,384 14.8 / 14.1, 32,768 25.8 / 23.6, 100,000 73 / 64; bf16 32,768 26.8 / 23.0; 32,768 without any 15.1 / 16.6 in fp32,
+// 13.8 / 12.4 in bf16.
+constexpr int kTwoRows = 12000;
 
 struct LatentArgs {
   const void *x, *key;
@@ -246,58 +251,86 @@ __device__ __forceinline__ uint2 in_order(uint2 c, int lane) {
   return c;
 }
 
-// The main copy (v: this lane's values) to plane row `row`; false, and nothing written, where it is not certain.
-__device__ __forceinline__ bool append_main(const LatentArgs& a, const LatentTurns& turns, float (&v)[4][4], int64_t row,
-                                            uint64_t pos, float* s_row, int lane) {
+// The main copies of kRows rows (v: this lane's values) to plane rows `row` (< 0: nowhere); returns the rows (bit n: row n)
+// that are not certain, of which nothing is written.
+template <int kRows>
+__device__ __forceinline__ uint32_t append_main(const LatentArgs& a, const LatentTurns& turns, float (&v)[kRows][4][4],
+                                                const int64_t (&row)[kRows], const uint64_t (&pos)[kRows], float* s_row,
+                                                int lane) {
+  uint32_t open = 0;
+  float2 turn[kRows];
+  if (a.rope) {
+    const uint64_t f = turns.kv.f[lane];
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) turn_cos_sin(f, (int64_t)pos[n], turn[n].x, turn[n].y);
+  }
   if (a.norm_w) {
     float4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(a.norm_w) + 32 * i + lane);
-    uint64_t sum = 0;
+    float ss[kRows];
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      uint64_t sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          const uint64_t p = pack2(v[n][i][j], v[n][i][j + 1]);
+          sum = fma2(p, p, sum);
+        }
+      float s0, s1;
+      unpack2(sum, s0, s1);
+      ss[n] = s0 + s1;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < kRows; ++n) ss[n] += __shfl_xor_sync(0xffffffffu, ss[n], o);
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) {
+      // sums whose terms are subnormal, or too large, are another's
+      if (!(ss[n] > 0x1p-80f && ss[n] < 0x1p100f)) open |= 1u << n;
+      const float inv = rsqrtf(fmaf(ss[n], 1.0f / kDMain, a.eps));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[n][i][0] = v[n][i][0] * inv * w[i].x;
+        v[n][i][1] = v[n][i][1] * inv * w[i].y;
+        v[n][i][2] = v[n][i][2] * inv * w[i].z;
+        v[n][i][3] = v[n][i][3] * inv * w[i].w;
+      }
+    }
+  }
+  if (a.rope) {  // the last 64 channels, lanes 16 .. two pairs each; lane l has formed pair l's angle
+#pragma unroll
+    for (int n = 0; n < kRows; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float c = __shfl_sync(0xffffffffu, turn[n].x, 2 * lane + j);
+        const float s = __shfl_sync(0xffffffffu, turn[n].y, 2 * lane + j);
+        if (lane >= 16) rope_pair(v[n][3][2 * j], v[n][3][2 * j + 1], c, s);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < kRows; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const uint64_t p = pack2(v[i][j], v[i][j + 1]);
-        sum = fma2(p, p, sum);
-      }
-    float s0, s1;
-    unpack2(sum, s0, s1);
-    float ss = s0 + s1;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    // sums whose terms are subnormal, or too large, are another's
-    if (!(ss > 0x1p-80f && ss < 0x1p100f)) return false;
-    const float inv = rsqrtf(fmaf(ss, 1.0f / kDMain, a.eps));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i][0] = v[i][0] * inv * w[i].x;
-      v[i][1] = v[i][1] * inv * w[i].y;
-      v[i][2] = v[i][2] * inv * w[i].z;
-      v[i][3] = v[i][3] * inv * w[i].w;
-    }
-  }
-  if (a.rope && lane >= 16) {  // the last 64 channels
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float c, s;
-      turn_cos_sin(turns.kv.f[2 * (lane - 16) + j], (int64_t)pos, c, s);
-      rope_pair(v[3][2 * j], v[3][2 * j + 1], c, s);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(s_row + 128 * i + 4 * lane) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      *reinterpret_cast<float4*>(s_row + kDMain * n + 128 * i + 4 * lane) =
+          make_float4(v[n][i][0], v[n][i][1], v[n][i][2], v[n][i][3]);
   __syncwarp();
-  uint64_t y[8];
-  take16(s_row + 16 * lane, lane, y);
-  uint2 codes;
-  uint32_t scale;
-  const bool sure = main_group(y, off_by(a.norm_w, a.rope && lane >= 28), codes, scale);
-  if (!__all_sync(0xffffffffu, sure)) return false;
-  *reinterpret_cast<uint2*>(a.kv_codes + row * 256 + lane * 8) = in_order(codes, lane);
-  a.kv_scales[row * 32 + lane] = (uint8_t)scale;
-  return true;
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    uint64_t y[8];
+    take16(s_row + kDMain * n + 16 * lane, lane, y);
+    uint2 codes;
+    uint32_t scale;
+    const bool sure = main_group(y, off_by(a.norm_w, a.rope && lane >= 28), codes, scale);
+    if (!__all_sync(0xffffffffu, sure)) open |= 1u << n;
+    if (row[n] < 0 || (open >> n & 1u)) continue;
+    *reinterpret_cast<uint2*>(a.kv_codes + row[n] * 256 + lane * 8) = in_order(codes, lane);
+    a.kv_scales[row[n] * 32 + lane] = (uint8_t)scale;
+  }
+  return open;
 }
 
 // Exponent of a key's group scale (codec.cuh, quantize_index_group_vals): floor(log2 amax) - 2, -127 at least; the
@@ -468,11 +501,12 @@ __device__ __noinline__ void exact_key(const LatentArgs& a, const LatentTurns& t
   if (lane % 8 == 0) a.ix_scales[row * 4 + lane / 8] = (uint8_t)(e + 127);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_constant__ LatentArgs a,
-                                                            const __grid_constant__ LatentTurns turns) {
-  __shared__ __align__(16) float s_row[kWarps][kKeys][kDIdx + 4];  // a row, or four keys
-  static_assert(kKeys * (kDIdx + 4) >= kDMain, "a row");
+template <typename T, int kRows>
+__global__ void __launch_bounds__(kThreads, kRows > 1 ? 8 : 9)
+    k_latent_append(const __grid_constant__ LatentArgs a, const __grid_constant__ LatentTurns turns) {
+  constexpr int kRoom = kRows > 1 ? kRows * kDMain : kKeys * (kDIdx + 4);
+  static_assert(kRoom % 4 == 0 && kRoom >= kDMain && kRoom >= kKeys * (kDIdx + 4), "rows, or four keys");
+  __shared__ __align__(16) float s_room[kWarps][kRoom];
   ptx::griddep_launch();
   ptx::griddep_wait();
   if ((int)blockIdx.x < a.reporters) {  // these report destinations outside the planes: the error word is theirs alone
@@ -490,23 +524,35 @@ __global__ void __launch_bounds__(kThreads, 9) k_latent_append(const __grid_cons
   if (cta >= a.main_ctas) {
     const int r = ((cta - a.main_ctas) * kWarps + warp) * kKeys;
     if (!a.key || r >= a.R) return;
-    for (uint32_t open = append_keys<T>(a, turns, r, s_row[warp], lane); open; open &= open - 1) {
+    auto* const s_keys = reinterpret_cast<float(*)[kDIdx + 4]>(s_room[warp]);
+    for (uint32_t open = append_keys<T>(a, turns, r, s_keys, lane); open; open &= open - 1) {
       const int i = r + __ffs(open) - 1;
-      exact_key<T>(a, turns, i, place(a, i), a.pos ? (uint64_t)a.pos[i] : 0, s_row[warp][0], lane);
+      exact_key<T>(a, turns, i, place(a, i), a.pos ? (uint64_t)a.pos[i] : 0, s_room[warp], lane);
     }
     return;
   }
-  const int r = cta * kWarps + warp;
+  const int r = (cta * kWarps + warp) * kRows;
   if (r >= a.R) return;
-  // everything the row needs is asked for before the first of it is used
-  float v[4][4];
+  // everything the rows need is asked for before the first of it is used
+  float v[kRows][4][4];
+  uint64_t pos[kRows];
+  int64_t row[kRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load4(static_cast<const T*>(a.x) + (int64_t)r * kDMain + 128 * i + 4 * lane, v[i]);
-  const uint64_t pos = a.pos ? (uint64_t)__ldg(a.pos + r) : 0;
-  const int64_t row = place(a, r);
-  if (row < 0) return;  // the same for the whole warp
-  if (!append_main(a, turns, v, row, pos, s_row[warp][0], lane))
-    exact_main<T>(a, turns, r, row, pos, s_row[warp][0], lane);
+  for (int n = 0; n < kRows; ++n) {
+    const int at = min(r + n, a.R - 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load4(static_cast<const T*>(a.x) + (int64_t)at * kDMain + 128 * i + 4 * lane, v[n][i]);
+    pos[n] = a.pos ? (uint64_t)__ldg(a.pos + at) : 0;
+    row[n] = r + n < a.R ? place(a, at) : -1;
+  }
+  uint32_t open = append_main(a, turns, v, row, pos, s_room[warp], lane);
+#pragma unroll
+  for (int n = 0; n < kRows; ++n)
+    if (row[n] < 0) open &= ~(1u << n);
+  for (; open; open &= open - 1) {
+    const int at = r + __ffs(open) - 1;
+    exact_main<T>(a, turns, at, place(a, at), a.pos ? (uint64_t)a.pos[at] : 0, s_room[warp], lane);
+  }
 }
 
 }  // namespace
@@ -530,7 +576,8 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   if (R > 0 && (!slot || !entry || ((rope || key_rope) && !pos))) return CSA2_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256) || ws_bytes < kWsHeader) return CSA2_ERR_WORKSPACE;
   const int reporters = R > kManyRows ? kReporters : 1;
-  const int main_ctas = x ? (int)cdiv(R, kWarps) : 0, key_ctas = key ? (int)cdiv(R, kWarps * kKeys) : 0;
+  const int rows = R >= kTwoRows ? 2 : 1;
+  const int main_ctas = x ? (int)cdiv(R, kWarps * rows) : 0, key_ctas = key ? (int)cdiv(R, kWarps * kKeys) : 0;
   LatentArgs a{x, key, R, n_slots, reporters, main_ctas, slot, entry, dst->seq_stride, pos,
                x && kv_nr ? kv_nr->norm_weight : nullptr, kv_nr ? kv_nr->norm_eps : 0.0f, rope, 0, 0, 0, 0, 1.0f,
                dst->kv_codes, dst->kv_scales, dst->ix_codes, dst->ix_scales, ws};
@@ -547,7 +594,8 @@ extern "C" csa2_status csa2_latent_append(const void* x, const void* key, int32_
   }
   cudaStream_t st = (cudaStream_t)stream;
   KernelTimer timer("k_latent_append", st);
-  const auto kern = type == CSA2_F32 ? k_latent_append<float> : k_latent_append<uint16_t>;
+  const auto kern = type == CSA2_F32 ? (rows > 1 ? k_latent_append<float, 2> : k_latent_append<float, 1>)
+                                     : (rows > 1 ? k_latent_append<uint16_t, 2> : k_latent_append<uint16_t, 1>);
   const unsigned ctas = (unsigned)align_up((size_t)reporters + main_ctas + key_ctas, (size_t)reporters);
   if (reporters > 1) launch_clusters(kern, dim3(ctas), dim3(kThreads), reporters, 1, 0, st, a, turns);
   else launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, st, a, turns);

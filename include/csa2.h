@@ -238,9 +238,10 @@ size_t csa2_cache_append_workspace_size(int32_t G, int32_t d_model, int32_t m);
  *          (CSA2_ERR_INDEX_RANGE), slot -1 with entry -1 is skipped without a report.  Two rows of one destination
  *          leave either, or parts of both
  *   pos    [R] int64, required with a rotation
- * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: |pos| 2^-53 turns)
- * and rounded to fp32 once, then the codec of csa2_quantize_entries writes it; without norm and rotation the bytes
- * are csa2_quantize_entries'.  x and key 16-byte aligned; 0 <= R <= 2^30;
+ * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: |pos| 2^-53 turns;
+ * near fp32's smallest values 2^-148 more) and rounded to fp32 once, then the codec of csa2_quantize_entries
+ * writes it; without norm and rotation the bytes are csa2_quantize_entries'.  x and key 16-byte aligned;
+ * 0 <= R <= 2^30;
  * ws: csa2_latent_append_workspace_size(R) bytes (the error word). */
 csa2_status csa2_latent_append(const void* x, const void* key, int32_t type, int32_t R, const csa2_kv_planes* dst,
                                int32_t n_slots, const int32_t* slot, const int64_t* entry, const csa2_norm_rope* kv_nr,

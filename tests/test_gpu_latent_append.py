@@ -97,6 +97,48 @@ def test_bytes_of_many_rows(oracle_mod):
     run(oracle_mod, 20000, P=64, seed=22, norm=False, dtype=torch.bfloat16)
 
 
+@pytest.mark.parametrize("R", [511, 513, 11999, 12000, 12001])
+def test_bytes_where_the_form_changes(oracle_mod, R):
+    run(oracle_mod, R, P=64, seed=R)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("norm,rope", [(True, True), (False, True), (True, False), (False, False)])
+def test_bytes_of_two_rows_a_warp(oracle_mod, norm, rope, dtype):
+    run(oracle_mod, 12003, P=64, seed=30, dtype=dtype, norm=norm, rope=rope, parts="x")
+
+
+@pytest.mark.parametrize("scale,eps", [(1e-18, 1e-6), (1e-15, 0.0), (1e30, 1e-6)])
+def test_many_rows_far_from_one(oracle_mod, scale, eps):
+    run(oracle_mod, 12001, P=64, seed=31, scale=scale, eps=eps, parts="x")
+
+
+def test_many_rows_of_which_some_are_not_written(oracle_mod):
+    # padding, destinations outside and a NaN beside rows that share a warp with them
+    R, P = 12005, 64
+    rng = np.random.default_rng(32)
+    x = rng.standard_normal((R, 512)).astype(np.float32)
+    pages = -(-R // P)
+    at = rng.permutation(R)
+    slot, entry = (at // P).astype(np.int32), (at % P).astype(np.int64)
+    pad, out, nan = [0, 5, 77, R - 1], [2, 101, 5001], [9, 200, 6000, 6001]
+    slot[pad], entry[pad] = -1, -1
+    slot[out] = pages
+    x[nan, 100] = np.nan
+    weight = (1 + 0.3 * rng.standard_normal(512)).astype(np.float32)
+    pos = rng.integers(0, 1 << 20, R)
+    pool, ws = Pool(pages, P), csa2.workspace(256)
+    csa2.latent_append(to_dev(x), R, pool.planes, pages, to_dev(slot), to_dev(entry), ws,
+                       kv_nr=csa2.norm_rope(to_dev(weight), 1e-6, True), pos=to_dev(pos))
+    assert csa2.check(ws) == (6, pages)
+    clean = np.where(np.isfinite(x), x, 0).astype(np.float64)
+    want = reference(oracle_mod, clean, None, weight, 1e-6, pos, True, None, None)
+    good = np.setdiff1d(np.arange(R), pad + out + nan)
+    for got, w in zip(pool.bytes(), want[:2]):
+        assert np.array_equal(got[at[good]], w[good])
+        assert (got[at[pad + out]] == 0xA5).all()
+
+
 @pytest.mark.parametrize("key_rot", [None, (128, 0, False, 10000.0), (128, 0, True, 500000.0), (2, 126, False, 10000.0),
                                      (48, 5, True, 10000.0), (64, 0, False, 10000.0)])
 def test_keys(oracle_mod, key_rot):
