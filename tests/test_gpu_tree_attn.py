@@ -233,6 +233,26 @@ def test_long_contexts():
     f.device().check(of=[0, 1, 7, 15, 16, 20, 27])
 
 
+@pytest.mark.parametrize("short", [False, True])
+@pytest.mark.parametrize("n_swa,entries,extras,dtype", [(128, True, True, torch.bfloat16), (0, False, False, torch.float32)])
+def test_bounds_that_cut_the_list(short, n_swa, entries, extras, dtype):
+    # bounds of 20 requests of 6,000 entries make for a list in parts; the lengths fill all of them, or less than one
+    rng = np.random.default_rng(23)
+    R, bound = 20, 6000
+    trees = [random_tree(rng, int(T)) for T in rng.integers(0, 40, R)]
+    trees[0] = random_tree(rng, 40)
+    n = rng.integers(0, 200 if short else bound, R)
+    n[1], n[2] = 0, 200 if short else bound
+    f = Forest(24, n.tolist(), trees, 64, n_swa, entries, extras, extras)
+    f.n_max, narrow = bound, f.table
+    f.max_pages = -(-(bound + csa2.MAX_TREE) // 64)
+    f.table = np.full((R, f.max_pages), 0x7fffffff, np.int32)
+    f.table[:, :narrow.shape[1]] = narrow
+    assert R * -(-bound // 128) > 512 and f.B * bound // 256 >= 2 * 16 * 76
+    of = sorted({0, f.B - 1, *rng.choice(f.B, 24, replace=False).tolist()})
+    f.device().check(dtype, of=of)
+
+
 def test_one_token_is_the_paged_attention():
     # a tree of one token: the same rows as csa2_paged_attn_decode over its context, itself and its window
     f = Forest(5, [333, 70], [chain(1), chain(1)], 16, 128).device()
