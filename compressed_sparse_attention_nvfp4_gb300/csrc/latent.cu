@@ -205,8 +205,10 @@ __device__ __forceinline__ bool main_group(const uint64_t (&y)[8], Off by, uint2
   }
   const bool off = by.code > 0.0f;
   const float t = __fdiv_rn(amax, 6.0f);
+  // an exact value's ends are itself, an infinity's too
+  const float t0 = off ? fmaf(t, -by.top, t) : t, t1 = off ? fmaf(t, by.top, t) : t;
   uint16_t ends;  // low byte: the lower one
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ends) : "f"(fmaf(t, by.top, t)), "f"(fmaf(t, -by.top, t)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(ends) : "f"(t1), "f"(t0));
   scale = ends & 0xFFu;
   bool sure = !off || (amax < kTopMost && (ends >> 8) == scale);
   const float s = e4m3_to_float(scale);

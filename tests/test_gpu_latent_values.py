@@ -1,0 +1,63 @@
+"""csa2_latent_append on values at the ends of fp32.  The bytes are the codec's (csa2_quantize_entries) on the values of the
+definition."""
+import numpy as np
+import pytest
+
+from gpu_common import csa2, require_gpu, to_dev, torch
+from test_gpu_latent_append import Pool
+
+pytestmark = pytest.mark.gpu
+INF, NAN = np.inf, np.nan
+ODD = [INF, -INF, NAN]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def append(x, key, R, **kw):
+    """The four planes' rows, row r at entry r."""
+    pool, ws = Pool(1, R), csa2.workspace(256)
+    csa2.latent_append(x, R, pool.planes, 1, torch.zeros(R, dtype=torch.int32, device="cuda"), torch.arange(R, device="cuda"), ws,
+                       key=key, **kw)
+    assert csa2.check(ws) == (0, 0)
+    return pool.bytes()
+
+
+def codec(x, key, R):
+    pool = Pool(1, R)
+    csa2.quantize_entries(pool.planes, x.float(), key.float(), R, 0)
+    return pool.bytes()
+
+
+def with_odd_values(R, dtype):
+    """Rows of which all but every fifth have infinities and NaN: one, two of both signs, next to a NaN, in both ends."""
+    rng = np.random.default_rng(R)
+    x, key = rng.standard_normal((R, 512)).astype(np.float32), rng.standard_normal((R, 128)).astype(np.float32)
+    for v in (x, key):
+        n = v.shape[1]
+        for r in range(R):
+            for _ in range(r % 5):
+                v[r, rng.integers(0, n)] = ODD[rng.integers(0, 3)]
+        v[1, 3], v[2, n - 1], v[3, [0, 5]] = INF, -INF, (NAN, INF)
+    return to_dev(x).to(dtype), to_dev(key).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [7, 12003])
+def test_what_is_not_finite_has_the_codecs_bytes(R, dtype):
+    x, key = with_odd_values(R, dtype)
+    for a, b in zip(append(x, key, R), codec(x, key, R)):
+        assert np.array_equal(a, b), np.argwhere(a != b)[:5]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [7, 12003])
+def test_groups_beside_a_rotation_keep_theirs(R, dtype):
+    # the last 64 channels of the main copy turn, and of the key: the others' groups are the codec's
+    x, key = with_odd_values(R, dtype)
+    got = append(x, key, R, kv_nr=csa2.norm_rope(None, 1e-6, True), key_rot=csa2.rotary(64, 64),
+                 pos=torch.arange(R, device="cuda") + 3)
+    for a, b, n in zip(got, codec(x, key, R), (224, 28, 32, 2)):
+        assert np.array_equal(a[:, :n], b[:, :n]), np.argwhere(a[:, :n] != b[:, :n])[:5]
