@@ -112,8 +112,9 @@ __device__ __forceinline__ FF inverse_rms(float (&v)[16], float eps, float& scal
   const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));  // of values >= 0 as their bits
   const int e = (int)(top >> 23) - 127;
   scale = 1.0f;
-  if (e > 40 || e < -40) {  // squares and their remainders within fp32's range
-    const int k = min(max(e, -60), 100);
+  if (e > 40 || e < -40) {  // squares and their remainders within fp32's range, and eps's: 2^61 at most
+    const int least = max(((int)(__float_as_uint(eps) >> 23) - 127 - 60) / 2, -60);
+    const int k = min(max(e, least), 100);
     scale = exp2i_f32(-k);
     eps = ldexpf(eps, -2 * k);
 #pragma unroll

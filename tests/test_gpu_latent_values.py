@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from gpu_common import csa2, require_gpu, to_dev, torch
-from test_gpu_latent_append import Pool
+from test_gpu_latent_append import Pool, reference
 
 pytestmark = pytest.mark.gpu
 INF, NAN = np.inf, np.nan
@@ -61,3 +61,17 @@ def test_groups_beside_a_rotation_keep_theirs(R, dtype):
                  pos=torch.arange(R, device="cuda") + 3)
     for a, b, n in zip(got, codec(x, key, R), (224, 28, 32, 2)):
         assert np.array_equal(a[:, :n], b[:, :n]), np.argwhere(a[:, :n] != b[:, :n])[:5]
+
+
+@pytest.mark.parametrize("R", [5, 12001])
+@pytest.mark.parametrize("scale,eps,gain", [(1e-20, 1e4, 1e22), (1e-25, 1e12, 1e31), (1e-30, 0.5, 1e30), (1e-13, 2e3, 1e15)])
+def test_small_rows_that_eps_outweighs(oracle_mod, R, scale, eps, gain):
+    rng = np.random.default_rng(R)
+    x = (scale * rng.standard_normal((R, 512))).astype(np.float32)
+    weight = (gain * (1 + 0.3 * rng.standard_normal(512))).astype(np.float32)
+    pos = rng.integers(0, 1 << 20, R)
+    got = append(to_dev(x), None, R, kv_nr=csa2.norm_rope(to_dev(weight), eps, True), pos=to_dev(pos))
+    want = reference(oracle_mod, x.astype(np.float64), None, weight, eps, pos, True, None, None)
+    assert (want[0] != 0).mean() > 0.5
+    for a, b in zip(got[:2], want[:2]):
+        assert np.array_equal(a, b), np.argwhere(a != b)[:5]
