@@ -143,10 +143,10 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t phase, FF& c, FF& s) {
   if (quarter == 1 || quarter == 2) c = neg(c);
   if (quarter >= 2) s = neg(s);
 }
-// (x, y) turned counter-clockwise; infinities, whose remainders are none, in fp32
+// (x, y) turned counter-clockwise; infinities, given or where the sum passes the largest fp32, have no remainders: in fp32
 __device__ __forceinline__ void turn_pair(FF& x, FF& y, FF c, FF s) {
   FF nx = add(mul(x, c), neg(mul(y, s))), ny = add(mul(x, s), mul(y, c));
-  if (!isfinite(x.hi) || !isfinite(y.hi)) {
+  if (!isfinite(x.hi) || !isfinite(y.hi) || !isfinite(nx.hi) || !isfinite(ny.hi)) {
     nx = FF{x.hi * c.hi - y.hi * s.hi, 0.0f};
     ny = FF{x.hi * s.hi + y.hi * c.hi, 0.0f};
   }

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from gpu_common import csa2, require_gpu, to_dev, torch
+from rotary_common import rotate
 from test_gpu_latent_append import Pool, reference
 
 pytestmark = pytest.mark.gpu
@@ -74,4 +75,24 @@ def test_small_rows_that_eps_outweighs(oracle_mod, R, scale, eps, gain):
     want = reference(oracle_mod, x.astype(np.float64), None, weight, eps, pos, True, None, None)
     assert (want[0] != 0).mean() > 0.5
     for a, b in zip(got[:2], want[:2]):
+        assert np.array_equal(a, b), np.argwhere(a != b)[:5]
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_pairs_that_turn_past_the_largest_value(halves):
+    # (a, a) turned by an eighth of a turn is 1.41 a: an infinity as fp32, its partner nearly nothing
+    R = 64
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((R, 512)).astype(np.float32)
+    key = rng.standard_normal((R, 128)).astype(np.float32)
+    x[:, 448:] = 3e38 * rng.choice([-1, 1], (R, 64))
+    key[:, 64:] = 3e38 * rng.choice([-1, 1], (R, 64))
+    pos = rng.integers(0, 1 << 20, R)
+    got = append(to_dev(x), to_dev(key), R, kv_nr=csa2.norm_rope(None, 1e-6, True), key_rot=csa2.rotary(64, 64, int(halves)),
+                 pos=to_dev(pos))
+    with np.errstate(over="ignore"):
+        turned = [rotate(x.astype(np.float64), pos, 64, 448, False, 10000.0).astype(np.float32),
+                  rotate(key.astype(np.float64), pos, 64, 64, halves, 10000.0).astype(np.float32)]
+    assert all(np.isinf(t).any(1).mean() > 0.9 for t in turned)
+    for a, b in zip(got, codec(to_dev(turned[0]), to_dev(turned[1]), R)):
         assert np.array_equal(a, b), np.argwhere(a != b)[:5]
