@@ -3,8 +3,8 @@
 //
 // A pair's theta / 2 pi goes to the kernels as a 64-bit binary fraction f; pos * f modulo 2^64 is the angle in
 // turns, already reduced, by two integer products: no product in fp64, of which an SM does one warp
-// instruction in 16 cycles.  f is theta's double rounded once more by 2^-65, so an angle is off by
-// |pos| theta 2^-53 at most, what a double of it would be.
+// instruction in 16 cycles.  f is off by theta / 2 pi times 3 2^-53 (the roundings of power, quotient and 2 pi) and by
+// its own last half step, 2^-65; an angle by |pos| times that, below |pos| max(theta, 1) 2^-53 turns.
 #pragma once
 
 #include <math.h>
@@ -63,7 +63,7 @@ inline void make_turns(Turns<kPairs>* t, int n, double base, const csa2_rope_sca
   make_thetas(theta, n, base, s);
   for (int i = 0; i < n / 2; ++i) {
     const double turns = theta[i] / 6.283185307179586476925286766559;
-    t->f[i] = (uint64_t)((turns - floor(turns)) * 0x1p64);
+    t->f[i] = (uint64_t)rint((turns - floor(turns)) * 0x1p64);  // doubles of 2^53 and more are whole already
   }
 }
 

@@ -172,9 +172,10 @@ typedef struct {
  * rotates; queries, keys and outputs of other layouts than csa2_norm_rope's):
  *   y[r][h] = x[r][h] with the channels of `rot` turned by pos[r]; inverse != 0: by -pos[r], multiplied by
  *   magnitude all the same.  That is the transposed map, so the gradient of x is the inverse of y's.
- *   x, y   of `type`, computed in fp32 and rounded once; element (r, h, c) of x at r * x_row + h * x_head + c, of y
- *          at r * y_row + h * y_head + c (strides in elements, any alignment; 16-byte aligned ones run faster)
- *   pos    [n_rows] int64 (device), any value: an angle is exact to |pos| 2^-53 turns
+ *   x, y   of `type`, computed in fp32 (a turned channel is off by 2^-21 of |a| + |b| of its pair, times magnitude:
+ *          angle, sine and cosine are fp32's) and rounded once; element (r, h, c) of x at r * x_row + h * x_head + c,
+ *          of y at r * y_row + h * y_head + c (strides in elements, any alignment; 16-byte aligned ones run faster)
+ *   pos    [n_rows] int64 (device), any value: far ones add |pos| max(theta_i, 1) 2^-53 turns to the angle's error
  * y may be x, with the same strides: then only the rotated channels are written.  Otherwise they must not overlap, and
  * the vectors of y must not overlap one another (CSA2_ERR_INVALID_ARG).  0 <= n_rows < 2^31, 1 <= heads <= 65535,
  * first + n_rot <= dim <= 65536. */
@@ -238,7 +239,7 @@ size_t csa2_cache_append_workspace_size(int32_t G, int32_t d_model, int32_t m);
  *          (CSA2_ERR_INDEX_RANGE), slot -1 with entry -1 is skipped without a report.  Two rows of one destination
  *          leave either, or parts of both
  *   pos    [R] int64, required with a rotation
- * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: |pos| 2^-53 turns;
+ * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: as in csa2_rope;
  * near fp32's smallest values 2^-148 more) and rounded to fp32 once, then the codec of csa2_quantize_entries
  * writes it; without norm and rotation the bytes are csa2_quantize_entries'.  x and key 16-byte aligned;
  * 0 <= R <= 2^30;

@@ -5,6 +5,8 @@ The bound.  The angle of a position is off by |pos| 2^-53 turns twice (the refer
 |pos| 2^-50 with the factor 2 pi; it is rounded to fp32 as a part of half a turn (pi 2^-25), cut at 2^-32 turns, and the
 sine and cosine are off by 2 units of 2^-24 and multiplied by magnitude (2^-24); the two products and their sum add 2^-24
 each: 2^-21 of |a| + |b| in all.  Then the output's own rounding."""
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 
@@ -194,3 +196,24 @@ def test_streams_graph_and_no_rows():
     graph.replay()
     csa2.rope(x, 300, 8, 128, d, rot, want)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_angles_of_slow_pairs_at_far_positions(halves):
+    # an angle is off by |pos| (3 theta / 2 pi 2^-53 + 2^-65) turns (the power's, the quotient's and 2 pi's rounding of
+    # theta, and the fraction's own): beside the angle in 50 digits, which numpy's doubles do not have
+    getcontext().prec = 50
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582")
+    pos, n, base = np.array([1 << 50, -(1 << 50) - 12345, (1 << 51) + 7, 3 << 48], np.int64), 64, 1e9
+    turns = [(Decimal(base).ln() * Decimal(-2 * i) / n).exp() / two_pi for i in range(n // 2)]
+    angle = np.array([[float((int(p) * t) % 1 * two_pi) for t in turns] for p in pos])
+    x = np.zeros((len(pos), 1, n), np.float32)
+    a, b = (np.arange(n // 2), np.arange(n // 2, n)) if halves else (np.arange(0, n, 2), np.arange(1, n, 2))
+    x[:, :, a] = 1.0
+    out = torch.empty(x.shape, device="cuda")
+    csa2.rope(to_dev(x), len(pos), 1, n, to_dev(pos), csa2.rotary(n, 0, int(halves), base=base), out)
+    got = out.cpu().double().numpy()[:, 0]
+    off = np.abs(pos).astype(np.float64)[:, None] * (3 * np.array([float(t) for t in turns]) * 2.0 ** -53 + 2.0 ** -65)
+    bound = 2 * np.pi * off + 2.0 ** -21 + 2.0 ** -24
+    for have, want in ((got[:, a], np.cos(angle)), (got[:, b], np.sin(angle))):
+        assert (np.abs(have - want) <= bound).all(), (np.abs(have - want) / bound).max()
