@@ -121,7 +121,7 @@ class Trees(ctypes.Structure):
 def trees(start, parent, R: int, B: int, max_tokens: int, entries: bool = True) -> Trees:
     """A csa2_trees over device int32 arrays start [R + 1] and parent [B] (indices within the request, -1: a child of
     its last token); keeps references to both.  entries: a drafted token has an entry in the cache."""
-    t = Trees(_ptr(start), _ptr(parent), int(R), int(B), int(max_tokens), int(bool(entries)))
+    t = Trees(*_ints("start, parent", 4, start, parent), int(R), int(B), int(max_tokens), int(bool(entries)))
     t._refs = (start, parent)
     return t
 
@@ -222,6 +222,24 @@ def _ptr(x) -> int | None:
 def _ptrs(*xs) -> list:
     """_ptr of each: short calls spend much of their time on the host."""
     return [x if x is None or x.__class__ is int else x.data_ptr() for x in xs]
+
+
+_int_sizes: dict = {}  # dtype -> 4 of int32, 8 of int64, 0 of any other
+
+
+def _ints(what: str, size: int, *xs) -> list:
+    """_ptr of each array of integers of `size` bytes: a tensor of another type, or with gaps, is refused."""
+    out = []
+    for x in xs:
+        if x is not None and x.__class__ is not int:
+            kind = _int_sizes.get(x.dtype)
+            if kind is None:
+                kind = _int_sizes[x.dtype] = {"torch.int32": 4, "torch.int64": 8}.get(str(x.dtype), 0)
+            if kind != size or not x.is_contiguous():
+                raise Csa2Error(1, f"{what}: int{8 * size} wanted, is {x.dtype}, strides {tuple(x.stride())}")
+            x = x.data_ptr()
+        out.append(x)
+    return out
 
 
 def _nbytes(x) -> int:
@@ -393,7 +411,8 @@ def rope(x, n_rows: int, heads: int, dim: int, pos, rot: Rotary, out, inverse: b
     kind = _common_type(x, out, type, "rope")
     (x_row, x_head), (y_row, y_head) = (_strides(x, heads, dim, x_strides, "rope input"),
                                         _strides(out, heads, dim, out_strides, "rope output"))
-    px, py, pp = _ptrs(x, out, pos)
+    px, py = _ptrs(x, out)
+    (pp,) = _ints("rope positions", 8, pos)
     _ok(lib().csa2_rope(px, x_row, x_head, py, y_row, y_head, kind, n_rows, heads, dim, pp, ctypes.byref(rot),
                         1 if inverse else 0, _stream(stream)), "csa2_rope")
 
@@ -412,7 +431,9 @@ def latent_append(x, R: int, planes: Planes, n_slots: int, slot, entry, ws, key=
         if hasattr(t, "is_contiguous") and not t.is_contiguous():
             raise Csa2Error(1, f"latents or keys of strides {tuple(t.stride())}")
     kind = F32 if x is None and key is None else _common_type(x, key, type, "latents and keys")
-    px, pk, ps, pe, pp, pw = _ptrs(x, key, slot, entry, pos, ws)
+    px, pk, pw = _ptrs(x, key, ws)
+    (ps,) = _ints("slots", 4, slot)
+    pe, pp = _ints("entries, positions", 8, entry, pos)
     _ok(lib().csa2_latent_append(px, pk, kind, R, ctypes.byref(planes.c), n_slots, ps, pe, _ref(kv_nr), _ref(scaling), pp,
                                  _ref(key_rot), pw, _nbytes(ws), _stream(stream)), "csa2_latent_append")
 
@@ -626,8 +647,10 @@ def tree_attn_decode(planes: Planes, pages: Pages, trees: Trees, n_entries, n_ma
     """paged_attn_decode for trees of drafted tokens: query b attends to its request's n_entries[g] entries, its own and
     its ancestors' behind them, the ring rows swa at positions swa_pos and the drafted tokens' window rows draft
     (csa2_tree_attn_decode); pages' rows are the requests'."""
-    _ok(lib().csa2_tree_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), ctypes.byref(trees), _ptr(n_entries),
-                                    n_max, _ptr(swa), _ptr(swa_pos), _ptr(draft), n_swa, _ptr(q), _ptr(q_pos),
+    (pn,) = _ints("tree attention lengths", 4, n_entries)
+    psp, pqp = _ints("tree attention positions", 8, swa_pos, q_pos)
+    _ok(lib().csa2_tree_attn_decode(ctypes.byref(planes.c), ctypes.byref(pages), ctypes.byref(trees), pn,
+                                    n_max, _ptr(swa), psp, _ptr(draft), n_swa, _ptr(q), pqp,
                                     softmax_scale, _ref(q_nr), _ref(scaling), _ptr(sink), _ptr(out),
                                     _given_out_type(out, out_type), _ptr(lse_out), _ptr(ws), _nbytes(ws),
                                     _stream(stream)), "csa2_tree_attn_decode")
@@ -642,7 +665,9 @@ def tree_commit(planes: Planes | None, pages: Pages | None, trees: Trees, n_entr
     """Commit of accepted paths: token path[g, i] of request g becomes its entry n_entries[g] + i, its window row (of
     draft) takes its place of the ring at position pos[g] + i; n_new (or None) is what page_tables takes to drop the
     rest (csa2_tree_commit)."""
-    pn, pa, pp, pw, pd, ppos, pr, prp, pws = _ptrs(n_entries, n_accept, path, n_new, draft, pos, ring, ring_pos, ws)
+    pn, pa, pp, pw = _ints("tree commit lengths and paths", 4, n_entries, n_accept, path, n_new)
+    ppos, prp = _ints("tree commit positions", 8, pos, ring_pos)
+    pd, pr, pws = _ptrs(draft, ring, ws)
     _ok(lib().csa2_tree_commit(None if planes is None else ctypes.byref(planes.c), _ref(pages), ctypes.byref(trees), pn, pa,
                                pp, n_path, pw, pd, ppos, pr, prp, n_win, pws, _nbytes(ws), _stream(stream)),
         "csa2_tree_commit")
