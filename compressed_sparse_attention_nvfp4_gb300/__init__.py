@@ -389,14 +389,16 @@ def _common_type(a, b, type: int | None, what: str) -> int:
     return of[0]
 
 
-def _strides(x, heads: int, dim: int, strides, what: str) -> tuple[int, int]:
-    """Row and head strides in elements: those given, else a tensor's [n_rows, heads, dim] or [n_rows, dim], else
-    dense ones."""
+def _strides(x, n_rows: int, heads: int, dim: int, strides, what: str) -> tuple[int, int]:
+    """Row and head strides in elements: those given, else a tensor's [n_rows, heads, dim] or [n_rows, heads * dim] (it
+    may have more rows), else dense ones."""
     if strides is not None:
         return int(strides[0]), int(strides[1])
     if not hasattr(x, "stride"):
         return heads * dim, dim
     shape, st = x.shape, x.stride()
+    if st and shape[0] < n_rows:
+        raise Csa2Error(1, f"{what} of shape {tuple(shape)} for {n_rows} rows")
     if len(st) == 3 and shape[1] == heads and shape[2] == dim and (st[2] == 1 or dim == 1):
         return st[0], st[1]
     if len(st) == 2 and shape[1] == heads * dim and (st[1] == 1 or heads * dim == 1):
@@ -409,8 +411,8 @@ def rope(x, n_rows: int, heads: int, dim: int, pos, rot: Rotary, out, inverse: b
     """Rotary positions: x [n_rows, heads, dim] (fp32 or bf16, rows and heads strided as the tensor says) -> out, which
     may be x; pos int64 [n_rows].  inverse: by -pos, which is the gradient (csa2_rope)."""
     kind = _common_type(x, out, type, "rope")
-    (x_row, x_head), (y_row, y_head) = (_strides(x, heads, dim, x_strides, "rope input"),
-                                        _strides(out, heads, dim, out_strides, "rope output"))
+    (x_row, x_head), (y_row, y_head) = (_strides(x, n_rows, heads, dim, x_strides, "rope input"),
+                                        _strides(out, n_rows, heads, dim, out_strides, "rope output"))
     px, py = _ptrs(x, out)
     (pp,) = _ints("rope positions", 8, pos)
     _ok(lib().csa2_rope(px, x_row, x_head, py, y_row, y_head, kind, n_rows, heads, dim, pp, ctypes.byref(rot),

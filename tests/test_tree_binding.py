@@ -62,3 +62,11 @@ def test_rope_positions_are_int64():
     csa2.rope(x, 0, 8, 128, torch.zeros(4, dtype=I64), rot, x)
     for bad in (torch.zeros(4, dtype=I32), torch.zeros(4), torch.zeros(8, dtype=I64)[::2]):
         assert status(lambda: csa2.rope(x, 0, 8, 128, bad, rot, x)) == 1
+
+
+def test_rope_tensors_have_the_rows_that_are_asked_for():
+    x, few, pos, rot = torch.empty(4, 8, 128), torch.empty(3, 8, 128), torch.zeros(4, dtype=I64), csa2.rotary(64)
+    rope = lambda a, b, n: csa2.rope(a, n, 8, 128, pos, rot, b)  # noqa: E731
+    rope(x, x, 0)  # more rows than are turned
+    for a, b in ((few, x), (x, few), (few.view(3, 1024), x), (torch.empty(0, 8, 128), x)):
+        assert status(lambda: rope(a, b, 4)) == 1
