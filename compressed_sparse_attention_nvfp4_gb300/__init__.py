@@ -429,9 +429,11 @@ def latent_append(x, R: int, planes: Planes, n_slots: int, slot, entry, ws, key=
     """Ready latents x [R, 512] and indexer keys key [R, 128] (fp32 or bf16, either None) into slot[r], index
     entry[r], as cache_append's map; kv_nr normalises and rotates the main copy, its rotation slowed down by scaling,
     key_rot rotates the key (csa2_latent_append)."""
-    for t in (x, key):
-        if hasattr(t, "is_contiguous") and not t.is_contiguous():
-            raise Csa2Error(1, f"latents or keys of strides {tuple(t.stride())}")
+    for t, width in ((x, 512), (key, 128)):
+        if t is not None and t.__class__ is not int:
+            shape = t.shape  # rows of `width`, R at least; or a flat array of as many
+            if not t.is_contiguous() or t.numel() < R * width or (len(shape) > 1 and shape[-1] != width):
+                raise Csa2Error(1, f"latents or keys of shape {tuple(shape)}, strides {tuple(t.stride())} for {R} rows of {width}")
     kind = F32 if x is None and key is None else _common_type(x, key, type, "latents and keys")
     px, pk, pw = _ptrs(x, key, ws)
     (ps,) = _ints("slots", 4, slot)

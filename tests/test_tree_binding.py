@@ -70,3 +70,13 @@ def test_rope_tensors_have_the_rows_that_are_asked_for():
     rope(x, x, 0)  # more rows than are turned
     for a, b in ((few, x), (x, few), (few.view(3, 1024), x), (torch.empty(0, 8, 128), x)):
         assert status(lambda: rope(a, b, 4)) == 1
+
+
+def test_append_takes_rows_of_latents_and_keys():
+    E = torch.empty
+    f = lambda x, key: status(lambda: csa2.latent_append(x, 4, PLANES, 8, 16, 16, WS, key=key))  # noqa: E731
+    for x, key in ((E(4, 512), E(4, 128)), (E(9, 512), E(2, 2, 128)), (E(2048), E(513)), (None, E(4, 128)), (E(4, 512), None)):
+        assert f(x, key) == 3  # right but for the workspace
+    for x, key in ((E(3, 512), None), (E(4, 256), None), (E(4, 1024), None), (E(2047), None), (E(0, 512), None),
+                   (None, E(3, 128)), (None, E(4, 512)), (None, E(4, 64)), (E(4, 512), E(4, 127))):
+        assert f(x, key) == 1
