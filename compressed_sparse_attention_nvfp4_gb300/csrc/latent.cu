@@ -6,13 +6,15 @@
 // a row is formed in fp32 first, with every value's code taken at both ends of what it may be; where the ends agree,
 // the byte is certain.  Where one does not (one row in fifty after a norm), the row is formed again in pairs of fp32
 // (rotary.cuh), to 2^-36, and quantized from that.  In pairs alone: 1,283 warp instructions a row and 47 us for 32,768.
+// That goes by dense data: a zero's ends have different codes (8 and 0), so a row with a zero in a group that is normalised or
+// rotated is formed twice.  32,768 rows with a channel that is always zero take 50.7 us (bf16 50.3), with zero key pairs 38.0.
 //
 // A warp takes the main copies of one row or two: lane l reads, normalises and rotates the channels 128 i + 4 l .. (whole
 // lines) and quantizes 16 l .. (a group); a row changes hands in shared memory.  Another takes four rows' keys, eight
 // lanes to each in the end.  Bytes would bound a long call, up to 2,560 read and 356 written a row; measured, the chain
-// from a row's loads to its bytes does, some 390 instructions of which a warp issues one in eleven cycles: 32,768 fp32
-// rows with keys, normalised and rotated, 24.6 us (3.9 TB/s; the main copies alone without norm and rotation 17).  Two
-// rows are two chains side by side.
+// from a row's loads to its bytes does, 355 warp instructions for a main copy and 118 for a key, of which a warp issues one in
+// eleven cycles: 32,768 rows with keys, normalised and rotated, 24.6 us in fp32 (3.9 TB/s), 23.6 in bf16 (2.3 TB/s); the
+// main copies alone 20.4, without norm and rotation 16.1.  Two rows are two chains side by side.
 #include "codec.cuh"
 #include "ptx.cuh"
 #include "rotary.cuh"
@@ -27,8 +29,8 @@ constexpr int kKeys = 4;  // rows whose keys a warp takes
 // (4,096 rows with one / eight 8.8 / 6.6 us, 2,048 without norm, rotation and keys 4.6 / 2.8).
 constexpr int kReporters = 8, kManyRows = 512;
 // Rows from which a warp takes two.  One / two, us, normalised and rotated with keys: 8,192 9.4 / 9.5, 12,000 11.9 / 11.7,
-// 16,384 14.8 / 14.1, 32,768 25.8 / 23.6, 100,000 73 / 64; bf16 32,768 26.8 / 23.0; 32,768 without any 15.1 / 16.6 in fp32,
-// 13.8 / 12.4 in bf16.
+// 16,384 14.8 / 14.1, 32,768 25.8 / 23.6, 100,000 73 / 64; bf16 32,768 26.8 / 23.0; 32,768 without any 15.1 / 16.6 in fp32
+// (the form that loses by it), 13.8 / 12.4 in bf16.
 constexpr int kTwoRows = 12000;
 
 struct LatentArgs {

@@ -5,7 +5,9 @@
 // its rotated ones, two vectors of kV channels whose kV pairs turn (HALVES: pair k is the k-th channel of the two;
 // INTERLEAVED: the neighbouring channels of each), and its copied ones, one vector each.  Threads take units of one kind
 // at a time: with both kinds in a warp every warp runs both (32,768 x 32 queries 120 us).  Measured: 32,768 x 32 bf16
-// queries of 128 channels, half of them rotated, 82 us, 6.6 TB/s; 128 x 32 2.3 us from a graph.
+// queries of 128 channels, half of them rotated, 82 us, 6.6 TB/s, in fp32 153, 7.0 TB/s; 128 x 32 2.3 us from a graph.
+// Where an address, a stride or a number of pairs is no multiple of 16 bytes all units are of one channel: with gaps of 7
+// or 4 channels between the rows 271 us (fp32, 7: 273), with 20 pairs 354 (fp32, 18: 362).
 #include <algorithm>
 
 #include "ptx.cuh"

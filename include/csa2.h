@@ -174,11 +174,12 @@ typedef struct {
  *   magnitude all the same.  That is the transposed map, so the gradient of x is the inverse of y's.
  *   x, y   of `type`, computed in fp32 (a turned channel is off by 2^-21 of |a| + |b| of its pair, times magnitude:
  *          angle, sine and cosine are fp32's) and rounded once; element (r, h, c) of x at r * x_row + h * x_head + c,
- *          of y at r * y_row + h * y_head + c (strides in elements, any alignment; 16-byte aligned ones run faster)
+ *          of y at r * y_row + h * y_head + c (strides in elements, any alignment; where x, y, their strides, first,
+ *          n_rot / 2 and dim are all multiples of 16 bytes it runs up to four times as fast)
  *   pos    [n_rows] int64 (device), any value: far ones add |pos| max(theta_i, 1) 2^-53 turns to the angle's error
- * y may be x, with the same strides: then only the rotated channels are written.  Otherwise they must not overlap, and
- * the vectors of y must not overlap one another (CSA2_ERR_INVALID_ARG).  0 <= n_rows < 2^31, 1 <= heads <= 65535,
- * first + n_rot <= dim <= 65536. */
+ * y may be x, with the same strides: then only the rotated channels are written.  Otherwise no vector of y may overlap
+ * one of x (which is not looked at); vectors of y that overlap one another are CSA2_ERR_INVALID_ARG.
+ * 0 <= n_rows < 2^31, 1 <= heads <= 65535, first + n_rot <= dim <= 65536. */
 csa2_status csa2_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int64_t y_row, int64_t y_head, int32_t type,
                       int64_t n_rows, int32_t heads, int32_t dim, const int64_t* pos, const csa2_rotary* rot,
                       int32_t inverse, csa2_stream stream);
@@ -241,9 +242,9 @@ size_t csa2_cache_append_workspace_size(int32_t G, int32_t d_model, int32_t m);
  *   pos    [R] int64, required with a rotation
  * Each value is formed with an error of about 2^-36 of its vector's (a far position's angle: as in csa2_rope;
  * near fp32's smallest values 2^-148 more) and rounded to fp32 once, then the codec of csa2_quantize_entries
- * writes it; without norm and rotation the bytes are csa2_quantize_entries'.  x and key 16-byte aligned;
- * 0 <= R <= 2^30;
- * ws: csa2_latent_append_workspace_size(R) bytes (the error word). */
+ * writes it; without norm and rotation the bytes are csa2_quantize_entries', of infinities and NaN too.  Rows with
+ * zeros among their normalised or rotated values take about twice the time.  x and key 16-byte aligned;
+ * 0 <= R <= 2^30; ws: csa2_latent_append_workspace_size(R) bytes (the error word). */
 csa2_status csa2_latent_append(const void* x, const void* key, int32_t type, int32_t R, const csa2_kv_planes* dst,
                                int32_t n_slots, const int32_t* slot, const int64_t* entry, const csa2_norm_rope* kv_nr,
                                const csa2_rope_scaling* scaling, const int64_t* pos, const csa2_rotary* key_rot,
@@ -638,7 +639,8 @@ typedef struct {
  *              n_swa tokens back.  Required with n_swa > 0, as swa_e4m3 and swa_pos; n_swa = 0: no window
  *   q_pos      [B] int64, required with n_swa > 0 or a rotation: a token's position (its request's first draft's
  *              plus its depth)
- *   scaling    (or NULL) of q_nr's rotation
+ *   scaling    (or NULL) of q_nr's rotation.  Entries and window rows have to carry the same: csa2_latent_append writes
+ *              such entries, csa2_swa_append rotates unscaled (rows without a norm can be turned by csa2_rope before)
  *   out        [B][64][512] of out_type; lse_out [B][64] or NULL
  * Queries outside every tree see no rows.  A start that is not in order within [0, B], or a tree of more than max_tokens
  * tokens, is reported as CSA2_ERR_INDEX_RANGE (detail: such a request), and no query of the call sees any row; a parent
